@@ -1,7 +1,7 @@
 """GB300 block-quantized matrix-vector product: thin Python binding.
 
 The work happens in the CUDA library libqgemv.so (the C ABI of
-include/qgemv.h); this module only marshals arguments: it checks dtypes,
+include/qgemv.h; attention.py binds include/qattn.h); this module only marshals arguments: it checks dtypes,
 devices and sizes of torch tensors, allocates outputs with torch when the
 caller passes none, and calls the C entry points with raw device pointers and
 the current CUDA stream. There is no fallback: if the library is missing,
@@ -22,6 +22,8 @@ __all__ = [
     "qgemv_batched_workspace_bytes", "BatchPlan", "device_error", "kernel_info", "EXPORTED_SYMBOLS",
     "MAX_BATCH", "tune", "qgemm_workspace_bytes", "qgemm", "qgemm_f16", "selftest_bounded_wait",
     "gemm_kernel_info",
+    "KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes", "prompt_attend",
+    "rope_table", "ATTENTION_SYMBOLS",
 ]
 
 F32, F16, Q4_0, Q4_1, Q5_0, Q8_0, Q8_1 = 0, 1, 2, 3, 6, 8, 9
@@ -395,3 +397,20 @@ def device_error() -> int:
     v = ctypes.c_int32(0)
     _check(lib().qg_device_error(ctypes.byref(v)), "qg_device_error")
     return v.value
+
+
+# ------------------------------------------------------------ attention
+# The names of attention.py (include/qattn.h) are looked up on first use: they
+# need torch, which the C library's own binding above imports only when a
+# tensor is passed.
+_ATTENTION = frozenset(("KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes",
+                        "prompt_attend", "rope_table", "ATTENTION_SYMBOLS"))
+
+
+def __getattr__(name):
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -26,8 +26,8 @@ def _sources():
 
 
 def _deps():
-    return (sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
-            + [os.path.join(ROOT, "include", "qgemv.h"), os.path.abspath(__file__)])
+    return (sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.h")))
+            + sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)])
 
 
 def _stale(target, inputs):

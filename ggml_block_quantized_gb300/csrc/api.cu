@@ -7,6 +7,7 @@
 
 #include <atomic>
 
+#include "api_common.h"
 #include "gemm_tc.cuh"
 #include "gemv_launch.cuh"
 #include "gemv_tc.cuh"
@@ -49,11 +50,15 @@ namespace {
 
 thread_local char g_last_cuda_error[256] = "";
 
-int cuda_fail(cudaError_t e, const char *where = "") {
+}  // namespace
+
+int cuda_fail(cudaError_t e, const char *where) {
     std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "%s: %s (%s)", cudaGetErrorName(e),
                   cudaGetErrorString(e), where);
     return QG_ERR_CUDA;
 }
+
+namespace {
 
 bool block_info(int type, int *elems, int *bytes) {
     switch (type) {
@@ -74,14 +79,7 @@ bool block_info(int type, int *elems, int *bytes) {
     }
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct DeviceInfo {
-    int device;
-    int sms;
-    int smem_optin;  // opt-in dynamic shared memory per CTA (bytes)
-    int32_t *err;    // device address of g_device_error on this device
-};
+}  // namespace
 
 int current_device(DeviceInfo *info) {
     static int sm_count[64] = {0};
@@ -115,6 +113,8 @@ int current_device(DeviceInfo *info) {
     info->err = err;
     return QG_OK;
 }
+
+namespace {
 
 int env_int(const char *name, int dflt, int lo, int hi) {
     const char *s = std::getenv(name);

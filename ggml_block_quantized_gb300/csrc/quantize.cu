@@ -28,19 +28,9 @@
 // without fast-math, so '/' is correctly rounded), roundf and the f16
 // conversion, so the bytes equal the scalar definition's.
 #include "qg_common.cuh"
+#include "quant_codes.cuh"
 
 namespace qg {
-
-// Float to int as the lesson's Java code casts it: truncation toward zero,
-// 0 for NaN, the int range's end beyond it (a NaN element, or a scale so
-// small that 1/d overflows, reaches those cases). Written out rather than
-// left to the conversion instruction's own NaN and overflow rules.
-__device__ __forceinline__ int java_f2i(float t) {
-    if (t != t) return 0;
-    if (t >= 2147483648.0f) return 2147483647;
-    if (t <= -2147483648.0f) return -2147483647 - 1;
-    return static_cast<int>(t);
-}
 
 // Two 4-bit codes into one byte: the low 4 bits of each (a code below 0
 // comes only from -inf and keeps its low bits, 0).

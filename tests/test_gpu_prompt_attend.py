@@ -1,0 +1,172 @@
+"""qattn_prompt against the formula in 64 bits (attn_ref.attend). The inputs are
+f16, exact in the products; the softmax weights are rounded to f16, half an
+ulp, 2^-11 of a weight: attn_ref.bound with 10 bits for it (weights and their
+sum) is the tolerance."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import attn_ref  # noqa: E402
+import ggml_block_quantized_gb300 as qg  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    yield
+    assert qg.device_error() == 0
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def inputs(rng, n, heads, hk, d, fused=True, q_size=1.5, v_size=1.0):
+    x = rng.standard_normal((n, heads + 2 * hk, d)).astype(np.float32)
+    x[:, :heads] *= q_size
+    x[:, heads + hk:] = (x[:, heads + hk:] + 0.3) * v_size
+    x = torch.from_numpy(x).cuda().half()
+    q, k, v = x[:, :heads], x[:, heads:heads + hk], x[:, heads + hk:]
+    return (q, k, v) if fused else (q.contiguous(), k.contiguous(), v.contiguous())
+
+
+def check(got, q, k, v, lens, scale, f16=True, rows=None, heads=None):
+    got, q, k, v = (t.detach().cpu().numpy().astype(np.float64) for t in (got, q, k, v))
+    d, group, at = q.shape[2], q.shape[1] // k.shape[1], 0
+    for n in lens:
+        mine = np.arange(n) if rows is None else np.array(sorted({r for r in rows if 0 <= r < n}))
+        for h in range(q.shape[1]) if heads is None else heads:
+            if not len(mine):
+                continue
+            out, pv, mag, big = attn_ref.attend(q[at + mine, h], k[at:at + n, h // group], v[at:at + n, h // group],
+                                                mine + 1, scale)
+            tol = attn_ref.bound(out, pv, mag, big, d, n, 24, 10, f16)
+            err = np.abs(got[at + mine, h] - out)
+            assert np.isfinite(got[at + mine, h]).all(), (n, h)
+            assert (err <= tol).all(), (n, h, float((err / tol).max()))
+        at += n
+
+
+CASES = [  # D, kv heads, group, lengths, fused
+    (128, 2, 4, [1], True), (64, 1, 1, [2], False), (128, 8, 4, [61], True), (64, 3, 1, [127, 128, 129], True),
+    (128, 1, 8, [0, 1, 0, 2, 3, 15, 16, 17, 31, 33, 0], True), (128, 2, 2, [255, 1, 257], True),
+    (64, 2, 8, [300, 5, 700], True), (128, 1, 3, [190, 64], True), (64, 1, 7, [100, 333], False),
+    (128, 1, 16, [130, 40], True), (128, 4, 1, [513], True), (64, 1, 5, [385, 1, 1, 1], True),
+    (128, 1, 128, [3, 2], True), (64, 1, 200, [5], True), (128, 1, 6, [260], False),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)).replace(" ", "")[:60])
+def test_prompt(case):
+    d, hk, group, lens, fused = case
+    rng = np.random.default_rng(sum(map(ord, str(case))))
+    q, k, v = inputs(rng, sum(lens), hk * group, hk, d, fused)
+    off = i32(np.cumsum([0] + lens))
+    got = qg.prompt_attend(q, k, v, off)
+    assert got.dtype == torch.float16
+    check(got, q, k, v, lens, d ** -0.5)
+    assert torch.equal(got, qg.prompt_attend(q, k, v, off))
+    wide = torch.full(got.shape, np.nan, device="cuda")
+    assert qg.prompt_attend(q, k, v, off, out=wide) is wide
+    check(wide, q, k, v, lens, d ** -0.5, f16=False)
+
+
+def test_long_prompt():
+    """Many key tiles; sampled rows, among them the tiles' borders."""
+    rng = np.random.default_rng(30)
+    lens = [2500, 3, 1797]
+    q, k, v = inputs(rng, sum(lens), 6, 2, 128)
+    got = qg.prompt_attend(q, k, v, i32(np.cumsum([0] + lens)))
+    rows = [0, 1, 2, 63, 64, 127, 128, 129, 255, 256, 1000, 1023, 1024, 1796, 2047, 2048, 2303, 2304, 2498, 2499]
+    check(got, q, k, v, lens, 128 ** -0.5, rows=rows)
+
+
+@pytest.mark.parametrize("q_size,v_size,scale", [(1, 1, -0.3), (1, 1, 0.0), (20, 1, 1.0), (1, 5000.0, 0.09),
+                                                 (1, 1e-4, 0.09), (3000, 1, 0.01)])
+def test_sizes_of_values(q_size, v_size, scale):
+    rng = np.random.default_rng(31)
+    lens = [200, 70]
+    q, k, v = inputs(rng, sum(lens), 4, 2, 128, q_size=q_size, v_size=v_size)
+    check(qg.prompt_attend(q, k, v, i32([0, 200, 270]), scale=scale), q, k, v, lens, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_unseen_nan_and_infinity(d, bad):
+    """Row 150 of the first prompt and row 5 of the second hold what is not
+    finite: no row before them, and no row of another prompt, sees it."""
+    rng = np.random.default_rng(32)
+    lens = [300, 40, 90]
+    q, k, v = (t.clone() for t in inputs(rng, sum(lens), 4, 2, d, fused=False))
+    k[150], v[150], k[305], v[305] = bad, bad, bad, bad
+    got = qg.prompt_attend(q, k, v, i32(np.cumsum([0] + lens)))
+    check(got[:150], q[:150], k[:150], v[:150], [150], d ** -0.5)
+    check(got[300:305], q[300:305], k[300:305], v[300:305], [5], d ** -0.5)
+    check(got[340:], q[340:], k[340:], v[340:], [90], d ** -0.5)
+    assert not torch.isfinite(got[150:300]).all(-1).all() and not torch.isfinite(got[305:340]).all(-1).all()
+
+
+def test_infinite_value_that_is_seen():
+    """An infinite value with a weight above zero gives that infinity."""
+    rng = np.random.default_rng(33)
+    q, k, v = (t.clone() for t in inputs(rng, 140, 2, 1, 128, fused=False))
+    v[3, 0, 7] = float("inf")
+    v[130, 0, 9] = -float("inf")
+    got = qg.prompt_attend(q, k, v, i32([0, 140]))
+    assert bool((got[3:, :, 7] == float("inf")).all()) and bool((got[130:, :, 9] == -float("inf")).all())
+    clean = torch.isfinite(got)
+    clean[3:, :, 7] = True
+    clean[130:, :, 9] = True
+    assert bool(clean.all())
+
+
+def test_strides_rows_in_no_sequence_and_stream():
+    rng = np.random.default_rng(34)
+    q, k, v = inputs(rng, 100, 4, 2, 64)
+    out = torch.full((100, 4, 64), 9.0, device="cuda", dtype=torch.float16)
+    off = i32([10, 40, 40, 90])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    qg.prompt_attend(q, k, v, off, out=out, stream=side)
+    side.synchronize()
+    assert bool((out[:10] == 9).all()) and bool((out[90:] == 9).all())
+    check(out[10:90], q[10:90], k[10:90], v[10:90], [30, 50], 64 ** -0.5)
+
+
+def test_offsets_out_of_range():
+    rng = np.random.default_rng(35)
+    q, k, v = inputs(rng, 50, 2, 1, 64)
+    out = torch.full((50, 2, 64), 9.0, device="cuda", dtype=torch.float16)
+    qg.prompt_attend(q, k, v, i32([0, 20, 10, 60]), out=out)  # the second falls, the third ends past the rows
+    assert qg.device_error() == 4
+    check(out[:20], q[:20], k[:20], v[:20], [20], 64 ** -0.5)
+    assert bool((out[20:] == 9).all())
+    qg.prompt_attend(q, k, v, i32([-3, 20, 50]), out=out)
+    assert qg.device_error() == 4
+    check(out[20:], q[20:], k[20:], v[20:], [30], 64 ** -0.5)
+
+
+def test_refusals():
+    q, k = torch.zeros(5, 4, 128, device="cuda", dtype=torch.float16), torch.zeros(5, 2, 128, device="cuda", dtype=torch.float16)
+    off = i32([0, 5])
+    bad = [(TypeError, lambda: qg.prompt_attend(q.float(), k, k, off)),
+           (TypeError, lambda: qg.prompt_attend(q, k, k, off.long())),
+           (ValueError, lambda: qg.prompt_attend(q, k[:4], k[:4], off)),
+           (ValueError, lambda: qg.prompt_attend(q[:, :3], k, k, off)),
+           (qg.QGError, lambda: qg.prompt_attend(q[..., :96].contiguous(), k[..., :96].contiguous(), k[..., :96].contiguous(), off)),
+           (ValueError, lambda: qg.prompt_attend(q, k, k, off, out=q[:2])),
+           (TypeError, lambda: qg.prompt_attend(q, k, k, off, out=q.double())),
+           (qg.QGError, lambda: qg.prompt_attend(q, k, k, off, scale=float("inf"))),
+           (qg.QGError, lambda: qg.prompt_attend(q[:1].expand(5, 4, 128), k, k, off))]
+    for error, call in bad:
+        with pytest.raises(error):
+            call()
+    assert qg.prompt_attend(q[:0], k[:0], k[:0], i32([0])).shape == (0, 4, 128)
+    assert qg.device_error() == 0
