@@ -1,116 +1,795 @@
 // kv_attend.cu - attention of new tokens over the 4-bit paged cache
-// (include/qattn.h, qkv_attend).
+// (include/qattn.h, qkv_attend), split over the cache's length.
 //
-// One warp for one query row (a token's head): 32 cache tokens at a time, a
-// lane each for the scores, then the running maximum and sum of the softmax,
-// then four (or two) channels a lane for the weighted values.
+// Work. A segment is one (sequence, key/value head, row tile): up to 8 NT query
+// rows (token-major over the sequence's queries and the head's group) against
+// the sequence's tokens, cut into tiles of 32 tokens (two cache groups). All
+// segments' tiles, in order, form one list that the resident thread blocks
+// share out in equal contiguous parts (at least one tile a warp), whatever the
+// lengths are: they are read on the device. A part that ends inside a segment
+// leaves its running maximum, sum and values in the workspace, and a second
+// kernel joins the parts of each such segment in order (deterministic).
+//
+// A block has four consumer warps and one producer warp. The producer walks
+// the list, looks the pages up 32 at a time and sends each tile's two groups
+// (18 D bytes each, contiguous) into a shared-memory ring with bulk copies;
+// consumer w takes tiles w, w + 4, ... of the block's part and keeps its own
+// softmax statistics; the four join through shared memory at a segment's end.
+//
+// Arithmetic, on mma.sync.m16n8k16 (f16 operands, f32 sums), tokens or
+// channels as the 16 rows and query rows as the 8 columns, so that a decode
+// step's few rows waste little:
+//  * scores: A = the key codes themselves. A 4-byte code word masked with
+//    0x000F000F holds two codes as f16 subnormals c 2^-24 (with 0x00F000F0,
+//    16 c 2^-24): one logic operation for two elements and no conversion; the
+//    queries of low-nibble elements carry the missing 16. The offset 8 of
+//    (code - 8) is the accumulator's start value, -8 sum of the block's q. Per
+//    block the f32 sum is multiplied by the token's key scale. Queries are
+//    scaled by a power of two to a largest magnitude of 2^10 .. 2^11 (exact).
+//  * values: B = weight x value scale per token and block (the scale varies
+//    along the summed axis), transposed among lanes with movmatrix; A = code -
+//    8 in f16 (exact). The softmax's running reference is not the largest
+//    score but the largest score plus the exponent of its token's largest value
+//    scale, less 29: every product is then below 2^15 and a row's largest near
+//    it, whatever the values' size. Weights, their sum and the accumulators
+//    share that reference, so it cancels.
+// So codes enter exactly and only q and the weights are rounded: f16 queries
+// are exact and the weights take one f16 (2^-11 relative); for f32 both are
+// split in two f16 parts and each product is formed twice.
+#include <atomic>
+
 #include "kv_cache.cuh"
+#include "tc_common.cuh"
 
 namespace qg {
 
-template <int D, class T>
-__global__ void __launch_bounds__(128) kv_attend_kernel(const KvAttendParams p) {
-    pdl_allow_dependents();
-    pdl_wait_prior_grids();
+namespace {
+
+constexpr int kWarps = 4;                  // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kTile = 32;                  // tokens of a tile
+constexpr int kMaxCtas = 640;              // thread blocks of a launch (workspace is sized for them)
+
+template <int D, int NT, int TERMS> struct Shape {
     using G = KvGroup<D>;
-    constexpr int kPer = D / 32;
-    __shared__ float qs[4][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x, h = blockIdx.y * 4 + warp;
-    if (h >= p.n_heads) return;
-    int q0 = s, q1 = s + 1;
-    if (p.q_offsets != nullptr) q0 = p.q_offsets[s], q1 = p.q_offsets[s + 1];
-    if (q0 < 0 || q1 < q0 || q1 > p.n_tok || q1 - q0 > p.max_q_len) {
-        if (lane == 0) record_error(p.err, kErrBadIndex);
-        return;
-    }
-    int len = p.lengths[s];
-    const int64_t room = p.table_stride * p.c.page_size;
-    if (len < 0 || len > room) {
-        if (lane == 0) record_error(p.err, kErrBadIndex);
-        len = len < 0 ? 0 : static_cast<int>(room);
-    }
-    const int hk = h / p.group;
-    for (int tok = q0; tok < q1; ++tok) {
-        const T *q = static_cast<const T *>(p.q) + tok * p.q_stride + h * D;
-        __syncwarp();
-        for (int i = lane; i < D; i += 32) qs[warp][i] = static_cast<float>(q[i]) * p.scale;
-        __syncwarp();
-        const int seen = len - (q1 - tok) + 1;
-        float m = -INFINITY, l = 0.0f, o[kPer] = {};
-        for (int t0 = 0; t0 < seen; t0 += 32) {
-            const int t = t0 + lane;
-            float sc = -INFINITY;
-            const uint8_t *g = nullptr;
-            if (t < seen) {
-                const int page = p.table[s * p.table_stride + t / p.c.page_size];
-                if (page < 0 || page >= p.c.n_pages) {
-                    record_error(p.err, kErrBadIndex);
-                } else {
-                    g = p.c.data + ((static_cast<int64_t>(page) * p.c.n_heads + hk) * p.c.page_groups +
-                                    ((t % p.c.page_size) >> 4)) * G::kBytes;
-                    const int i = t & 15;
-                    float sum = 0.0f;
-                    for (int b = 0; b < G::kNB; ++b) {
-                        float part = 0.0f;
-                        for (int w4 = 0; w4 < 4; ++w4) {
-                            const uint32_t w =
-                                *reinterpret_cast<const uint32_t *>(g + i * G::kRow + (w4 * G::kNB + b) * 4);
-                            for (int e = 0; e < 4; ++e) {
-                                part += qs[warp][32 * b + 4 * w4 + e] * (static_cast<int>((w >> (8 * e)) & 15u) - 8);
-                                part += qs[warp][32 * b + 16 + 4 * w4 + e] *
-                                        (static_cast<int>((w >> (8 * e + 4)) & 15u) - 8);
-                            }
-                        }
-                        sum += part * f16_bits_to_f32(
-                                          reinterpret_cast<const unsigned short *>(g + G::kKS + i * G::kScaleRow)[b]);
-                    }
-                    sc = sum;
-                }
-            }
-            float mt = sc;
-            for (int k = 16; k; k >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, k));
-            const float mn = fmaxf(m, mt);
-            if (mn == -INFINITY) continue;
-            const float keep = expf(m - mn);
-            const float w = g != nullptr ? expf(sc - mn) : 0.0f;
-            m = mn;
-            l = l * keep + w;
-            for (int k = 0; k < kPer; ++k) o[k] *= keep;
-            for (int j = 0; j < 32; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, w, j);
-                const uint8_t *gj = reinterpret_cast<const uint8_t *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(g), j));
-                if (gj == nullptr) continue;
-                const int i = (t0 + j) & 15, r = kv_value_row(i);
-                for (int k = 0; k < kPer; ++k) {
-                    const int e = lane;  // element of block k
-                    const int byte = e & 15, u = kv_value_unit(r, byte >> 1);
-                    const int c = (gj[G::kV + r * G::kRow + (u * G::kNB + k) * 2 + (byte & 1)] >> (e & 16 ? 4 : 0)) & 15;
-                    o[k] += wj * ((c - 8) *
-                                  f16_bits_to_f32(
-                                      reinterpret_cast<const unsigned short *>(gj + G::kVS + i * G::kScaleRow)[k]));
-                }
-            }
+    static constexpr int kTileBytes = 2 * G::kBytes;
+    static constexpr int kSlots = D == 128 ? 8 : 16;
+    static constexpr int kChunkBlocks = NT == 1 && G::kNB > 1 ? 2 : 1;  // blocks of 32 channels joined at a time
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kOffRing = 1024;
+    static constexpr int kOffQ = kOffRing + kSlots * kTileBytes;               // [term][nt][block][lane] 16 bytes
+    static constexpr int kOffInit = kOffQ + TERMS * NT * G::kNB * 512;         // [nt][block][8] f32
+    static constexpr int kOffRow = kOffInit + NT * G::kNB * 32;                // factor f32, limit int [rows]
+    static constexpr int kOffStat = kOffRow + kRows * 8;                       // [warp][rows] m, l
+    static constexpr int kOffJoin = kOffStat + kWarps * kRows * 8;             // [warp][rows][32 kChunkBlocks + 2]
+    static constexpr int kJoinPitch = 32 * kChunkBlocks + 2;
+    static constexpr int kSmem = kOffJoin + kWarps * kRows * kJoinPitch * 4;
+    static constexpr int kCtas = NT == 1 ? 3 : (NT == 2 ? 2 : 1);              // resident blocks a multiprocessor
+};
+
+// A partial result: rows x D values, then the rows' maxima and sums.
+__host__ __device__ constexpr int64_t part_floats(int d, int rows) { return static_cast<int64_t>(rows) * (d + 2); }
+
+struct Seq {
+    int len, m, q0;  // tokens in the cache, queries, first query row
+};
+
+// Sequence s, checked: no queries (m = 0) where its offsets are out of range.
+__device__ __forceinline__ Seq load_seq(const KvAttendParams &p, int s) {
+    Seq q;
+    q.q0 = s;
+    q.m = 1;
+    if (p.q_offsets != nullptr) {
+        q.q0 = __ldg(p.q_offsets + s);
+        const int q1 = __ldg(p.q_offsets + s + 1);
+        q.m = q1 - q.q0;
+        if (q.q0 < 0 || q1 < q.q0 || q1 > p.n_tok || q.m > p.max_q_len) {
+            record_error(p.err, kErrBadIndex);
+            q.m = 0;
         }
-        for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-        T *out = static_cast<T *>(p.out) + (static_cast<int64_t>(tok) * p.n_heads + h) * D;
-        for (int k = 0; k < kPer; ++k) out[32 * k + lane] = static_cast<T>(l > 0.0f || l != l ? o[k] / l : 0.0f);
+    }
+    q.len = __ldg(p.lengths + s);
+    const int64_t room = p.table_stride * p.c.page_size;
+    if (q.len < 0 || q.len > room) {
+        record_error(p.err, kErrBadIndex);
+        q.len = q.len < 0 ? 0 : static_cast<int>(room);
+    }
+    return q;
+}
+
+__device__ __forceinline__ int row_tiles(const KvAttendParams &p, const Seq &q, int rows) {
+    return (q.m * p.group + rows - 1) / rows;
+}
+__device__ __forceinline__ int tok_tiles(const Seq &q) { return q.len > kTile ? (q.len + kTile - 1) / kTile : 1; }
+__device__ __forceinline__ int64_t seq_units(const KvAttendParams &p, int s, int rows) {
+    const Seq q = load_seq(p, s);
+    return q.m == 0 ? 0 : static_cast<int64_t>(p.c.n_heads) * row_tiles(p, q, rows) * tok_tiles(q);
+}
+
+// Where a block's part begins: the sequence and the unit within it.
+struct Place {
+    int seq;
+    int64_t at;     // units of this sequence before the part
+    int64_t units;  // of all sequences
+    int64_t share;  // units of a block's part
+};
+
+// Finds the part of block `cta` of `ctas` (by the whole block: every thread
+// gets the result). seq = n_seq where the part is empty.
+template <int THREADS> __device__ Place locate(const KvAttendParams &p, int rows, int64_t cta, int ctas) {
+    __shared__ int64_t warp_sum[THREADS / 32];
+    __shared__ int found_seq;
+    __shared__ int64_t found_at;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t first = tid < p.n_seq ? seq_units(p, tid, rows) : 0;
+    int64_t v = first;
+    for (int s = tid + THREADS; s < p.n_seq; s += THREADS) v += seq_units(p, s, rows);
+#pragma unroll
+    for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if (lane == 0) warp_sum[warp] = v;
+    if (tid == 0) found_seq = p.n_seq, found_at = 0;
+    __syncthreads();
+    Place r;
+    r.units = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) r.units += warp_sum[w];
+    r.share = (r.units + ctas - 1) / ctas;
+    if (r.share < kWarps) r.share = kWarps;
+    const int64_t u = cta * r.share;
+    if (u < r.units) {
+        int64_t base = 0;
+        for (int s0 = 0; s0 < p.n_seq; s0 += THREADS) {
+            const int s = s0 + tid;
+            const int64_t mine = s0 == 0 ? first : (s < p.n_seq ? seq_units(p, s, rows) : 0);
+            int64_t incl = mine;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, incl, m);
+                if (lane >= m) incl += o;
+            }
+            __syncthreads();
+            if (lane == 31) warp_sum[warp] = incl;
+            __syncthreads();
+            int64_t before = base;
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w < warp) before += warp_sum[w];
+                base += warp_sum[w];
+            }
+            if (u >= before + incl - mine && u < before + incl) {
+                found_seq = s;
+                found_at = u - (before + incl - mine);
+            }
+            if (u < base) break;  // the same for every thread
+        }
+    }
+    __syncthreads();
+    r.seq = found_seq;
+    r.at = found_at;
+    return r;
+}
+
+// Walks the segments of a part.
+struct Walk {
+    Seq q;
+    int seq, head, rt, tile, tiles, rts;
+    int64_t left;  // units of the part from here on
+
+    __device__ __forceinline__ void start(const KvAttendParams &p, const Place &pl, int rows, int64_t units) {
+        left = units;
+        seq = pl.seq;
+        if (left <= 0) return;
+        q = load_seq(p, seq);
+        tiles = tok_tiles(q);
+        rts = row_tiles(p, q, rows);
+        tile = static_cast<int>(pl.at % tiles);
+        const int hr = static_cast<int>(pl.at / tiles);
+        head = hr / rts;
+        rt = hr - head * rts;
+    }
+    // Tiles of the part in this segment.
+    __device__ __forceinline__ int count() const {
+        return left < tiles - tile ? static_cast<int>(left) : tiles - tile;
+    }
+    __device__ __forceinline__ void next(const KvAttendParams &p, int rows) {
+        left -= count();
+        tile = 0;
+        if (left <= 0) return;
+        if (++rt < rts) return;
+        rt = 0;
+        if (++head < p.c.n_heads) return;
+        head = 0;
+        do {
+            ++seq;
+            q = load_seq(p, seq);
+        } while (q.m == 0);  // units are left, so there is one
+        tiles = tok_tiles(q);
+        rts = row_tiles(p, q, rows);
+    }
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+// code - 8 in f16 of the low (high) nibbles of bytes 0 and 2.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u); }
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+    return hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 c) / 16 - 72
+}
+template <int NB> __device__ __forceinline__ void ld_words(uint32_t a, uint32_t (&w)[NB]) {
+    if (NB == 4) {
+        const uint4 v = ld_s128(a);
+        w[0] = v.x, w[1] = v.y, w[NB - 2] = v.z, w[NB - 1] = v.w;
+    } else {
+        const uint2 v = ld_s64(a);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+// NB f16 (one row's scales, or one value unit of every block) as NB/2 words.
+template <int NB> __device__ __forceinline__ void ld_halves(uint32_t a, uint32_t (&w)[NB / 2]) {
+    if (NB == 4) {
+        const uint2 v = ld_s64(a);
+        w[0] = v.x, w[NB / 2 - 1] = v.y;
+    } else {
+        w[0] = ld_s32(a);
     }
 }
 
-size_t kv_attend_workspace(int, int) { return 16; }
+// Eight query elements of a row, 32 b + 4 t + (0..3) and + 16: in f32.
+template <class T> __device__ __forceinline__ void load_q8(const T *p, float (&x)[8]);
+template <> __device__ __forceinline__ void load_q8<float>(const float *p, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 16);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+template <> __device__ __forceinline__ void load_q8<__half>(const __half *p, float (&x)[8]) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p), b = *reinterpret_cast<const uint2 *>(p + 16);
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = unpack_half2(w[i]).x, x[2 * i + 1] = unpack_half2(w[i]).y;
+}
 
-cudaError_t launch_kv_attend(const KvAttendParams &p, int head_dim, int type, int, int, cudaStream_t s) {
-    const dim3 grid(p.n_seq, (p.n_heads + 3) / 4);
-    if (head_dim == 64) {
-        if (type == QG_F32) kv_attend_kernel<64, float><<<grid, 128, 0, s>>>(p);
-        else kv_attend_kernel<64, __half><<<grid, 128, 0, s>>>(p);
-    } else {
-        if (type == QG_F32) kv_attend_kernel<128, float><<<grid, 128, 0, s>>>(p);
-        else kv_attend_kernel<128, __half><<<grid, 128, 0, s>>>(p);
+__device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__half *p, float a, float b) { *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b); }
+
+template <int D, class T, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1)>::kCtas)
+    kv_attend_kernel(const KvAttendParams p) {
+    using G = KvGroup<D>;
+    constexpr int NB = G::kNB, TERMS = sizeof(T) == 4 ? 2 : 1, ROWS = 8 * NT;
+    using Sh = Shape<D, NT, TERMS>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    const uint32_t full0 = base, empty0 = base + 8 * Sh::kSlots;
+    volatile int *slot_info = reinterpret_cast<volatile int *>(smem + 16 * Sh::kSlots);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Sh::kSlots; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    return cudaGetLastError();
+    pdl_wait_prior_grids();
+    pdl_allow_dependents();
+    const Place place = locate<kThreads>(p, ROWS, blockIdx.x, gridDim.x);  // (synchronizes the block)
+    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * place.share;
+    int64_t units = place.units - u0;
+    if (units > place.share) units = place.share;
+    if (units <= 0) return;
+    Walk walk;
+    walk.start(p, place, ROWS, units);
+
+    if (warp == kWarps) {
+        // ---------------- producer
+        int slot = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        while (walk.left > 0 && ok) {
+            const int n = walk.count();
+            const int groups = (walk.q.len + 15) >> 4;  // of the sequence
+            const int32_t *table = p.table + walk.seq * p.table_stride;
+            int have = 0;      // first group whose address the lanes hold
+            int64_t src = -1;  // byte offset of group have + lane, -1: none
+            for (int i = 0; i < n && ok; ++i) {
+                const int g0 = 2 * (walk.tile + i);
+                if (i == 0 || g0 >= have + 32) {
+                    have = g0;
+                    const int g = have + lane;
+                    src = -1;
+                    if (g < groups && g < 2 * (walk.tile + n)) {
+                        const int page = __ldg(table + g / p.c.page_groups);
+                        if (page >= 0 && page < p.c.n_pages)
+                            src = ((static_cast<int64_t>(page) * p.c.n_heads + walk.head) * p.c.page_groups +
+                                   g % p.c.page_groups) * G::kBytes;
+                        else
+                            record_error(p.err, kErrBadIndex);
+                    }
+                }
+                const int64_t mine = __shfl_sync(0xffffffffu, src, (g0 - have + (lane & 1)) & 31);
+                const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0) & 3u;
+                if (issued >= Sh::kSlots) ok = __all_sync(0xffffffffu, tc_wait(empty0 + 8 * slot, phase ^ 1u, abort_flag));
+                if (!ok) break;
+                if (lane == 0) {
+                    slot_info[slot] = static_cast<int>(valid);
+                    mbar_arrive_expect_tx(full0 + 8 * slot, static_cast<uint32_t>(__popc(valid)) * G::kBytes);
+                }
+                __syncwarp();
+                if (lane < 2 && mine >= 0)
+                    bulk_copy_g2s_plain(base + Sh::kOffRing + slot * Sh::kTileBytes + lane * G::kBytes, p.c.data + mine,
+                                        G::kBytes, full0 + 8 * slot);
+                ++issued;
+                if (++slot == Sh::kSlots) slot = 0, phase ^= 1u;
+            }
+            if (ok) walk.next(p, ROWS);
+        }
+        if (!ok) {
+            if (lane == 0) record_error(p.err, kErrProducerWait);
+            *abort_flag = 1;
+            // leave no copy in flight into this block's shared memory
+            for (int64_t k = issued > Sh::kSlots ? issued - Sh::kSlots : 0; k < issued; ++k)
+                if (!mbar_wait_bounded(full0 + 8 * static_cast<int>(k % Sh::kSlots),
+                                       static_cast<uint32_t>((k / Sh::kSlots) & 1)))
+                    record_error(p.err, kErrDrainWait);
+        }
+        return;
+    }
+
+    // ---------------- consumers
+    const int g = lane >> 2, t = lane & 3;
+    float *row_factor = reinterpret_cast<float *>(smem + Sh::kOffRow);
+    int *row_limit = reinterpret_cast<int *>(smem + Sh::kOffRow) + ROWS;
+    float *stat = reinterpret_cast<float *>(smem + Sh::kOffStat);
+    float *join = reinterpret_cast<float *>(smem + Sh::kOffJoin);
+    int64_t k = warp;        // this warp's next tile of the part
+    int64_t seg_k = 0;       // the part's tiles before this segment
+    int slot = warp;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (; walk.left > 0; walk.next(p, ROWS)) {
+        const int n = walk.count();
+        // ---- the segment's queries, as the mma's B fragments
+        {
+            constexpr int kItems = ROWS * NB * 4;
+            for (int it = threadIdx.x; it < kItems; it += kWarps * 32) {
+                const int r = it / (NB * 4), b = it / 4 % NB, ti = it & 3;
+                const int row = walk.rt * ROWS + r;
+                const bool live = row < walk.q.m * p.group;
+                float x[8] = {};
+                if (live) {
+                    const int tok = row / p.group;
+                    load_q8(static_cast<const T *>(p.q) + (walk.q.q0 + tok) * p.q_stride +
+                                (walk.head * p.group + row - tok * p.group) * D + 32 * b + 4 * ti,
+                            x);
+                }
+                float big = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[i]));
+#pragma unroll
+                for (int m = 1; m < NB * 4; m <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
+                int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;  // exponent of the largest
+                if (e < -116 || e == 128) e = 0;                              // zeros, infinities
+                if (e > 100) e = 100;
+                const float up = __uint_as_float(static_cast<uint32_t>(10 - e + 127) << 23) * (p.scale < 0.0f ? -1.0f : 1.0f);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] *= up;
+                    if (TERMS == 1) sum += x[i];  // exact in f16
+                }
+                uint32_t w[TERMS][4];
+                // elements of the fragment's words: 0 2 | 1 3 (low nibbles) | 16 18 | 17 19 (high)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e0 = (i & 2) * 2 + (i & 1);
+                    const float f = i < 2 ? 16.0f : 1.0f;
+                    w[0][i] = pack_half2(x[e0] * f, x[e0 + 2] * f);
+                    if (TERMS == 2) {
+                        const float2 hi = unpack_half2(w[0][i]);
+                        w[TERMS - 1][i] = pack_half2(x[e0] * f - hi.x, x[e0 + 2] * f - hi.y);
+                        const float2 lo = unpack_half2(w[TERMS - 1][i]);
+                        sum += (hi.x + lo.x + (hi.y + lo.y)) / f;
+                    }
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int nt = r >> 3, rr = r & 7;
+#pragma unroll
+                for (int q = 0; q < TERMS; ++q)
+                    *reinterpret_cast<uint4 *>(smem + Sh::kOffQ + ((q * NT + nt) * NB + b) * 512 + (rr * 4 + ti) * 16) =
+                        make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                if (ti == 0) {
+                    reinterpret_cast<float *>(smem + Sh::kOffInit)[(nt * NB + b) * 8 + rr] = sum * -0x1p-17f;  // -8 * 16 * 2^-24
+                    if (b == 0) {
+                        // 2^24 / 16 2^(e - 10); never 0, which times an unseen token's -inf would be NaN
+                        row_factor[r] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * 0x1p10f *
+                                                  __uint_as_float(static_cast<uint32_t>(e + 127) << 23),
+                                              1e-37f);
+                        row_limit[r] = live ? walk.q.len - walk.q.m + row / p.group + 1 : 0;
+                    }
+                }
+            }
+        }
+        named_barrier(1, kWarps * 32);
+        float factor[NT][2];
+        int limit[NT][2];
+        // the first row sees least (rows past the last have no say: their result is not stored)
+        const int least = row_limit[0];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                factor[nt][c] = row_factor[8 * nt + 2 * t + c];
+                limit[nt][c] = row_limit[8 * nt + 2 * t + c];
+            }
+        float m[NT][2], l[NT][2], o[NT][NB][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[nt][b][h][i] = 0.0f;
+        }
+
+        for (; k < seg_k + n; k += kWarps) {
+            if (ok && !__all_sync(0xffffffffu, tc_wait(full0 + 8 * slot, phase, abort_flag))) {
+                if (lane == 0) record_error(p.err, kErrConsumerWait);
+                *abort_flag = 1;
+                ok = false;
+            }
+            if (ok) {
+                const uint32_t tile_a = base + Sh::kOffRing + slot * Sh::kTileBytes;
+                const int tok0 = (walk.tile + static_cast<int>(k - seg_k)) * kTile;
+                const int info = slot_info[slot];
+                // ---- scores of 2 x 16 tokens: s[group][nt][0, 1: token g; 2, 3: token g + 8]
+                float s[2][NT][4];
+                uint32_t dv[2][2][NB / 2];  // value scales of tokens g and g + 8
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {
+                    const uint32_t ga = tile_a + gr * G::kBytes;
+                    uint32_t w0[NB], w1[NB], d0[NB / 2], d1[NB / 2];
+                    ld_words<NB>(ga + g * G::kRow + t * (4 * NB), w0);
+                    ld_words<NB>(ga + (g + 8) * G::kRow + t * (4 * NB), w1);
+                    ld_halves<NB>(ga + G::kKS + g * G::kScaleRow, d0);
+                    ld_halves<NB>(ga + G::kKS + (g + 8) * G::kScaleRow, d1);
+                    ld_halves<NB>(ga + G::kVS + g * G::kScaleRow, dv[gr][0]);
+                    ld_halves<NB>(ga + G::kVS + (g + 8) * G::kScaleRow, dv[gr][1]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) s[gr][nt][0] = s[gr][nt][1] = s[gr][nt][2] = s[gr][nt][3] = 0.0f;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t x0 = w0[b], x1 = w1[b], y0 = x0 >> 8, y1 = x1 >> 8;
+                        const float2 k0 = unpack_half2(d0[b / 2]), k1 = unpack_half2(d1[b / 2]);
+                        const float ka = b & 1 ? k0.y : k0.x, kb = b & 1 ? k1.y : k1.x;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 ini = ld_s64(base + Sh::kOffInit + (nt * NB + b) * 32 + t * 8);
+                            float acc[4] = {__uint_as_float(ini.x), __uint_as_float(ini.y), __uint_as_float(ini.x),
+                                            __uint_as_float(ini.y)};
+#pragma unroll
+                            for (int q = 0; q < TERMS; ++q) {
+                                const uint4 bq = ld_s128(base + Sh::kOffQ + ((q * NT + nt) * NB + b) * 512 + lane * 16);
+                                mma_f16(acc, x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu, bq.x, bq.y);
+                                mma_f16(acc, x0 & 0x00F000F0u, x1 & 0x00F000F0u, y0 & 0x00F000F0u, y1 & 0x00F000F0u, bq.z, bq.w);
+                            }
+                            s[gr][nt][0] = fmaf(ka, acc[0], s[gr][nt][0]);
+                            s[gr][nt][1] = fmaf(ka, acc[1], s[gr][nt][1]);
+                            s[gr][nt][2] = fmaf(kb, acc[2], s[gr][nt][2]);
+                            s[gr][nt][3] = fmaf(kb, acc[3], s[gr][nt][3]);
+                        }
+                    }
+                }
+                bool odd = false;  // a value scale that is not finite, of a token that some rows do not see
+                if (tok0 + kTile > least || info != 3) {
+                    // tokens that a row does not see, or that lie in no page: whatever
+                    // the ring holds there (it may be NaN) is replaced
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int tok = tok0 + 16 * gr + 8 * h + g;
+                            const bool in_page = (info >> gr) & 1;
+#pragma unroll
+                            for (int i = 0; i < NB / 2; ++i) {
+                                if (!in_page || tok >= walk.q.len) dv[gr][h][i] = 0;
+                                odd = odd || (dv[gr][h][i] & 0x7C00u) == 0x7C00u || (dv[gr][h][i] & 0x7C000000u) == 0x7C000000u;
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (!in_page || tok >= limit[nt][c]) s[gr][nt][2 * h + c] = -INFINITY;
+                        }
+                    odd = __any_sync(0xffffffffu, odd);
+                }
+                // ---- exponents of the tokens' largest value scales (f16 exponent fields, 0 .. 30)
+                float ex[2][2];
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t vmax = dv[gr][h][0] & 0x7FFF7FFFu;
+                        if (NB == 4) vmax = __vmaxu2(vmax, dv[gr][h][NB / 2 - 1] & 0x7FFF7FFFu);
+                        ex[gr][h] = static_cast<float>(min(max(vmax & 0xFFFFu, vmax >> 16) >> 10, 30u));
+                    }
+                // ---- running reference, weights
+                float keep[NT][2];
+                bool same = true;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float f = factor[nt][c];
+                        float mx = fmaxf(fmaxf(fmaf(s[0][nt][c], f, ex[0][0]), fmaf(s[0][nt][2 + c], f, ex[0][1])),
+                                         fmaxf(fmaf(s[1][nt][c], f, ex[1][0]), fmaf(s[1][nt][2 + c], f, ex[1][1])));
+#pragma unroll
+                        for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+                        mx = fmaxf(m[nt][c], mx - 29.0f);
+                        const float ref = mx == -INFINITY ? 0.0f : mx;
+                        keep[nt][c] = exp2_approx(m[nt][c] - ref);
+                        same = same && mx == m[nt][c];
+                        m[nt][c] = mx;
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float w = exp2_approx(fmaf(s[gr][nt][2 * h + c], f, -ref));
+                                s[gr][nt][2 * h + c] = w;
+                                sum += w;
+                            }
+                        l[nt][c] = fmaf(l[nt][c], keep[nt][c], sum);
+                    }
+                if (!__all_sync(0xffffffffu, same)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[nt][b][h][i] *= keep[nt][i & 1];
+                }
+                // ---- values
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {
+                    const uint32_t va = tile_a + gr * G::kBytes + G::kV;
+                    uint32_t v[4][NB / 2];  // unit g of every block, tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        ld_halves<NB>(va + (4 * i + t) * G::kRow + (g ^ ((t & 2) << 1)) * (2 * NB), v[i]);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t wa = __byte_perm(v[0][b / 2], v[1][b / 2], sel);
+                        const uint32_t wb = __byte_perm(v[2][b / 2], v[3][b / 2], sel);
+                        const uint32_t a0 = low_codes(wa), a1 = low_codes(wa >> 8), a2 = low_codes(wb), a3 = low_codes(wb >> 8);
+                        const uint32_t h0 = high_codes(wa), h1 = high_codes(wa >> 8), h2 = high_codes(wb), h3 = high_codes(wb >> 8);
+                        const float2 f0 = unpack_half2(dv[gr][0][b / 2]), f1 = unpack_half2(dv[gr][1][b / 2]);
+                        const float fa = b & 1 ? f0.y : f0.x, fb = b & 1 ? f1.y : f1.x;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float p0 = s[gr][nt][0] * fa, p1 = s[gr][nt][1] * fa;
+                            float p2 = s[gr][nt][2] * fb, p3 = s[gr][nt][3] * fb;
+                            if (odd) {  // no weight, no share, whatever the scale
+                                p0 = s[gr][nt][0] == 0.0f ? 0.0f : p0, p1 = s[gr][nt][1] == 0.0f ? 0.0f : p1;
+                                p2 = s[gr][nt][2] == 0.0f ? 0.0f : p2, p3 = s[gr][nt][3] == 0.0f ? 0.0f : p3;
+                            }
+                            uint32_t x = pack_half2(p0, p1), y = pack_half2(p2, p3);
+#pragma unroll
+                            for (int q = 0; q < TERMS; ++q) {
+                                const uint32_t b0 = transpose8(x), b1 = transpose8(y);
+                                mma_f16(o[nt][b][0], a0, a1, a2, a3, b0, b1);
+                                mma_f16(o[nt][b][1], h0, h1, h2, h3, b0, b1);
+                                if (q + 1 < TERMS) {
+                                    const float2 xh = unpack_half2(x), yh = unpack_half2(y);
+                                    x = pack_half2(p0 - xh.x, p1 - xh.y);
+                                    y = pack_half2(p2 - yh.x, p3 - yh.y);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * slot);
+            slot += kWarps;
+            if (slot >= Sh::kSlots) slot -= Sh::kSlots, phase ^= 1u;
+        }
+        seg_k += n;
+
+        // ---- the warps' results become one
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int q = 4; q < 32; q <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], q);
+                if (g == 0) {
+                    stat[(warp * ROWS + 8 * nt + 2 * t + c) * 2] = m[nt][c];
+                    stat[(warp * ROWS + 8 * nt + 2 * t + c) * 2 + 1] = l[nt][c];
+                }
+            }
+        named_barrier(1, kWarps * 32);
+        const bool whole = walk.tile == 0 && n == walk.tiles;
+        // a part's result: slot 0 if it enters the segment from outside, slot 1 if the segment starts in it
+        float *part = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile == 0 ? 1 : 0)) * part_floats(D, ROWS);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = 8 * nt + 2 * t + c;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[(w * ROWS + r) * 2]);
+                const float f = top == -INFINITY ? 0.0f : exp2_approx(m[nt][c] - top);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) o[nt][b][h][c] *= f, o[nt][b][h][2 + c] *= f;
+            }
+#pragma unroll
+        for (int b0 = 0; b0 < NB; b0 += Sh::kChunkBlocks) {
+            if (b0 != 0) named_barrier(1, kWarps * 32);  // the chunk before has been read
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int b = b0; b < b0 + Sh::kChunkBlocks; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            *reinterpret_cast<float2 *>(join + (warp * ROWS + 8 * nt + 2 * t + c) * Sh::kJoinPitch +
+                                                        32 * (b - b0) + 16 * h + 2 * g) =
+                                make_float2(o[nt][b][h][c], o[nt][b][h][2 + c]);
+            named_barrier(1, kWarps * 32);
+            constexpr int kPairs = 16 * Sh::kChunkBlocks;  // channel pairs of a row in this chunk
+            for (int it = threadIdx.x; it < ROWS * kPairs; it += kWarps * 32) {
+                const int r = it / kPairs, c2 = 2 * (it % kPairs);
+                float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 v = *reinterpret_cast<const float2 *>(join + (w * ROWS + r) * Sh::kJoinPitch + c2);
+                    sum.x += v.x, sum.y += v.y;
+                }
+                const int row = walk.rt * ROWS + r;
+                if (row >= walk.q.m * p.group) continue;
+                float top = -INFINITY, den = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[(w * ROWS + r) * 2]);
+                if (top != -INFINITY)
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w)
+                        den = fmaf(stat[(w * ROWS + r) * 2 + 1], exp2_approx(stat[(w * ROWS + r) * 2] - top), den);
+                const int d = 32 * b0 + c2;
+                if (whole) {
+                    const int tok = row / p.group;
+                    const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
+                    store2(static_cast<T *>(p.out) +
+                               (static_cast<int64_t>(walk.q.q0 + tok) * p.n_heads + walk.head * p.group + row - tok * p.group) * D + d,
+                           sum.x * inv, sum.y * inv);
+                } else {
+                    store2(part + static_cast<int64_t>(r) * D + d, sum.x, sum.y);
+                    if (d == 0) store2(part + static_cast<int64_t>(ROWS) * D + 2 * r, top, den);
+                }
+            }
+        }
+        named_barrier(1, kWarps * 32);  // statistics and sums have been read
+    }
+}
+
+// Joins the parts of the segments that thread blocks of kv_attend_kernel cut.
+// Block c - 1 looks at the cut before part c: if it is the first one inside
+// its segment, the parts c - 1, c, ... up to the segment's end are summed.
+template <int D, class T, int NT>
+__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttendParams p, int ctas) {
+    constexpr int ROWS = 8 * NT;
+    // every block of the kernel before has passed its own wait, so the lengths are there
+    const int64_t c = blockIdx.x + 1;
+    const Place place = locate<128>(p, ROWS, c, ctas);
+    pdl_allow_dependents();
+    const int64_t u = c * place.share;
+    Walk walk;
+    walk.start(p, place, ROWS, u < place.units ? 1 : 0);
+    pdl_wait_prior_grids();  // in every block: what comes next on the stream then waits for the kernel before, too
+    if (u >= place.units || walk.tile == 0 || walk.tile > place.share) return;  // no cut, or not its segment's first
+    const int64_t end = u - walk.tile + walk.tiles;                             // the segment's end
+    const int parts = 1 + static_cast<int>((end - u + place.share - 1) / place.share);
+    // part 0 is the second slot of block c - 1, the others the first of c, c + 1, ...
+    const float *part0 = p.partial + (2 * (c - 1) + 1) * part_floats(D, ROWS);
+    const float *part1 = p.partial + 2 * c * part_floats(D, ROWS);
+    const int64_t pitch = 2 * part_floats(D, ROWS);
+    int rows = walk.q.m * p.group - walk.rt * ROWS;
+    if (rows > ROWS) rows = ROWS;
+    for (int it = threadIdx.x; it < rows * (D / 2); it += blockDim.x) {
+        const int r = it / (D / 2), d = 2 * (it % (D / 2));
+        const int64_t st = static_cast<int64_t>(ROWS) * D + 2 * r, at = static_cast<int64_t>(r) * D + d;
+        float top = __ldcg(part0 + st), den = 0.0f;
+        for (int i = 0; i + 1 < parts; ++i) top = fmaxf(top, __ldcg(part1 + i * pitch + st));
+        float2 sum = make_float2(0.0f, 0.0f);
+        if (top != -INFINITY) {
+            for (int i = 0; i < parts; ++i) {
+                const float *q = i == 0 ? part0 : part1 + (i - 1) * pitch;
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q + st));
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(q + at));
+                const float f = exp2_approx(ml.x - top);
+                den = fmaf(ml.y, f, den);
+                sum.x = fmaf(v.x, f, sum.x);
+                sum.y = fmaf(v.y, f, sum.y);
+            }
+        }
+        const int row = walk.rt * ROWS + r, tok = row / p.group;
+        const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+        store2(static_cast<T *>(p.out) +
+                   (static_cast<int64_t>(walk.q.q0 + tok) * p.n_heads + walk.head * p.group + row - tok * p.group) * D + d,
+               sum.x * inv, sum.y * inv);
+    }
+}
+
+// Query rows a segment takes: 8 a fragment column set, as few as hold all rows
+// of a head, at most 32 (more rows run as further segments over the same tokens).
+int row_sets(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+template <int D, class T, int NT> cudaError_t launch(const KvAttendParams &p, int sms, int device, cudaStream_t s) {
+    using Sh = Shape<D, NT, (sizeof(T) == 4 ? 2 : 1)>;
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (device & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    int ctas = sms * Sh::kCtas;
+    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    cudaError_t e = launch_pdl(kv_attend_kernel<D, T, NT>, ctas, kThreads, Sh::kSmem, s, p);
+    if (e != cudaSuccess || ctas == 1) return e;
+    return launch_pdl(kv_join_kernel<D, T, NT>, ctas - 1, 128, 0, s, p, ctas);
+}
+
+template <int D, class T> cudaError_t launch_rows(const KvAttendParams &p, int sms, int device, cudaStream_t s) {
+    switch (row_sets(static_cast<int64_t>(p.max_q_len) * p.group)) {
+    case 1: return launch<D, T, 1>(p, sms, device, s);
+    case 2: return launch<D, T, 2>(p, sms, device, s);
+    default: return launch<D, T, 4>(p, sms, device, s);
+    }
+}
+
+}  // namespace
+
+size_t kv_attend_workspace(int head_dim, int rows) {
+    return static_cast<size_t>(2 * kMaxCtas * part_floats(head_dim, 8 * row_sets(rows))) * sizeof(float);
+}
+
+cudaError_t launch_kv_attend(const KvAttendParams &p, int head_dim, int type, int sms, int device, cudaStream_t s) {
+    if (head_dim == 64)
+        return type == QG_F32 ? launch_rows<64, float>(p, sms, device, s) : launch_rows<64, __half>(p, sms, device, s);
+    return type == QG_F32 ? launch_rows<128, float>(p, sms, device, s) : launch_rows<128, __half>(p, sms, device, s);
 }
 
 }  // namespace qg
