@@ -48,19 +48,22 @@ namespace {
 constexpr int kWarps = 4;                  // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = 32;                  // tokens of a tile
+constexpr int kStart = 3;                  // units of the list that a segment's start counts for
 constexpr int kMaxCtas = 640;              // thread blocks of a launch (workspace is sized for them)
 
 template <int D, int NT, int TERMS> struct Shape {
     using G = KvGroup<D>;
     static constexpr int kTileBytes = 2 * G::kBytes;
     static constexpr int kSlots = D == 128 ? 8 : 16;
-    static constexpr int kChunkBlocks = NT == 1 && G::kNB > 1 ? 2 : 1;  // blocks of 32 channels joined at a time
     static constexpr int kRows = 8 * NT;
+    static constexpr int kChunkBlocks = NT == 1 ? G::kNB : (NT == 2 ? 2 : 1);  // blocks of 32 channels joined at a time
+    static constexpr int kRawRow = D * (TERMS == 2 ? 4 : 2);                   // bytes of a query row
     static constexpr int kOffRing = 1024;
-    static constexpr int kOffQ = kOffRing + kSlots * kTileBytes;               // [term][nt][block][lane] 16 bytes
+    static constexpr int kOffRaw = kOffRing + kSlots * kTileBytes;             // two segments' query rows
+    static constexpr int kOffQ = kOffRaw + 2 * kRows * kRawRow;                // [term][nt][block][lane] 16 bytes
     static constexpr int kOffInit = kOffQ + TERMS * NT * G::kNB * 512;         // [nt][block][8] f32
     static constexpr int kOffRow = kOffInit + NT * G::kNB * 32;                // factor f32, limit int [rows]
-    static constexpr int kOffStat = kOffRow + kRows * 8;                       // [warp][rows] m, l
+    static constexpr int kOffStat = kOffRow + kRows * 8;                       // [warp][rows] reference, sum
     static constexpr int kOffJoin = kOffStat + kWarps * kRows * 8;             // [warp][rows][32 kChunkBlocks + 2]
     static constexpr int kJoinPitch = 32 * kChunkBlocks + 2;
     static constexpr int kSmem = kOffJoin + kWarps * kRows * kJoinPitch * 4;
@@ -100,7 +103,8 @@ __device__ __forceinline__ Seq load_seq(const KvAttendParams &p, int s) {
 __device__ __forceinline__ int row_tiles(const KvAttendParams &p, const Seq &q, int rows) {
     return (q.m * p.group + rows - 1) / rows;
 }
-__device__ __forceinline__ int tok_tiles(const Seq &q) { return q.len > kTile ? (q.len + kTile - 1) / kTile : 1; }
+// Units of a segment: its tiles, and kStart for its queries and its join.
+__device__ __forceinline__ int tok_tiles(const Seq &q) { return kStart + (q.len + kTile - 1) / kTile; }
 __device__ __forceinline__ int64_t seq_units(const KvAttendParams &p, int s, int rows) {
     const Seq q = load_seq(p, s);
     return q.m == 0 ? 0 : static_cast<int64_t>(p.c.n_heads) * row_tiles(p, q, rows) * tok_tiles(q);
@@ -134,7 +138,7 @@ template <int THREADS> __device__ Place locate(const KvAttendParams &p, int rows
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) r.units += warp_sum[w];
     r.share = (r.units + ctas - 1) / ctas;
-    if (r.share < kWarps) r.share = kWarps;
+    if (r.share < kStart + kWarps) r.share = kStart + kWarps;
     const int64_t u = cta * r.share;
     if (u < r.units) {
         int64_t base = 0;
@@ -171,8 +175,10 @@ template <int THREADS> __device__ Place locate(const KvAttendParams &p, int rows
 // Walks the segments of a part.
 struct Walk {
     Seq q;
-    int seq, head, rt, tile, tiles, rts;
-    int64_t left;  // units of the part from here on
+    int seq, head, rt;
+    int tile, tiles;  // first unit in the segment (kStart is its first tile), the segment's units
+    int rts;
+    int64_t left;     // units of the part from here on
 
     __device__ __forceinline__ void start(const KvAttendParams &p, const Place &pl, int rows, int64_t units) {
         left = units;
@@ -186,9 +192,14 @@ struct Walk {
         head = hr / rts;
         rt = hr - head * rts;
     }
-    // Tiles of the part in this segment.
+    // Units of the part in this segment; of them tiles; the first such tile.
     __device__ __forceinline__ int count() const {
         return left < tiles - tile ? static_cast<int>(left) : tiles - tile;
+    }
+    __device__ __forceinline__ int first_tile() const { return tile > kStart ? tile - kStart : 0; }
+    __device__ __forceinline__ int n_tiles() const {
+        const int n = tile + count() - kStart - first_tile();
+        return n > 0 ? n : 0;
     }
     __device__ __forceinline__ void next(const KvAttendParams &p, int rows) {
         left -= count();
@@ -207,6 +218,14 @@ struct Walk {
     }
 };
 
+// d = a b + c
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, float c0, float c1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -255,15 +274,28 @@ template <int NB> __device__ __forceinline__ void ld_halves(uint32_t a, uint32_t
     }
 }
 
-// Eight query elements of a row, 32 b + 4 t + (0..3) and + 16: in f32.
-template <class T> __device__ __forceinline__ void load_q8(const T *p, float (&x)[8]);
-template <> __device__ __forceinline__ void load_q8<float>(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 16);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// The largest magnitudes among a row's scales (halves apart; NaN has no say),
+// and the f16 exponent field of the larger one, 0 .. 30, as a float.
+template <int NB> __device__ __forceinline__ __half2 max_scales(const uint32_t (&w)[NB / 2]) {
+    __half2 m = __habs2(*reinterpret_cast<const __half2 *>(&w[0]));
+    if (NB == 4) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2 *>(&w[NB / 2 - 1])));
+    return m;
 }
-template <> __device__ __forceinline__ void load_q8<__half>(const __half *p, float (&x)[8]) {
-    const uint2 a = *reinterpret_cast<const uint2 *>(p), b = *reinterpret_cast<const uint2 *>(p + 16);
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+__device__ __forceinline__ float exponent_field(__half2 m) {
+    const uint32_t f = static_cast<uint32_t>(__half_as_ushort(__hmax(__low2half(m), __high2half(m)))) >> 10;
+    return __uint_as_float(0x4B000000u | min(f, 30u)) - 8388608.0f;
+}
+
+// Eight query elements of a row (elements 0..3 and 16..19 from shared address a on) in f32.
+template <class T> __device__ __forceinline__ void load_q8(uint32_t a, float (&x)[8]);
+template <> __device__ __forceinline__ void load_q8<float>(uint32_t a, float (&x)[8]) {
+    const uint4 u = ld_s128(a), v = ld_s128(a + 64);
+    x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    x[4] = __uint_as_float(v.x), x[5] = __uint_as_float(v.y), x[6] = __uint_as_float(v.z), x[7] = __uint_as_float(v.w);
+}
+template <> __device__ __forceinline__ void load_q8<__half>(uint32_t a, float (&x)[8]) {
+    const uint2 u = ld_s64(a), v = ld_s64(a + 32);
+    const uint32_t w[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = unpack_half2(w[i]).x, x[2 * i + 1] = unpack_half2(w[i]).y;
 }
@@ -282,11 +314,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     const uint32_t full0 = base, empty0 = base + 8 * Sh::kSlots;
     volatile int *slot_info = reinterpret_cast<volatile int *>(smem + 16 * Sh::kSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots);
+    const uint32_t qfull0 = base + 20 * Sh::kSlots + 16, qempty0 = qfull0 + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Sh::kSlots; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull0 + 8 * i, 1);
+            mbar_init(qempty0 + 8 * i, kWarps);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -303,23 +340,41 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 
     if (warp == kWarps) {
         // ---------------- producer
-        int slot = 0;
+        int slot = 0, seg = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        while (walk.left > 0 && ok) {
-            const int n = walk.count();
+        for (; walk.left > 0 && ok; ++seg) {
+            const int n = walk.n_tiles(), tile0 = walk.first_tile();
             const int groups = (walk.q.len + 15) >> 4;  // of the sequence
             const int32_t *table = p.table + walk.seq * p.table_stride;
+            // the segment's query rows: of each token they cover, the heads are contiguous
+            {
+                const uint32_t raw = base + Sh::kOffRaw + (seg & 1) * ROWS * Sh::kRawRow, bar = qfull0 + 8 * (seg & 1);
+                if (seg >= 2) ok = __all_sync(0xffffffffu, tc_wait(qempty0 + 8 * (seg & 1), ((seg >> 1) - 1) & 1, abort_flag));
+                if (!ok) break;
+                const int row0 = walk.rt * ROWS;
+                int row1 = walk.q.m * p.group;
+                if (row1 > row0 + ROWS) row1 = row0 + ROWS;
+                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>((row1 - row0) * Sh::kRawRow));
+                __syncwarp();
+                const int tok = row0 / p.group + lane;
+                const int a = max(row0, tok * p.group), z = min(row1, (tok + 1) * p.group);
+                if (a < z)
+                    bulk_copy_g2s_plain(raw + (a - row0) * Sh::kRawRow,
+                                        static_cast<const T *>(p.q) + (walk.q.q0 + tok) * p.q_stride +
+                                            (static_cast<int64_t>(walk.head) * p.group + a - tok * p.group) * D,
+                                        static_cast<uint32_t>((z - a) * Sh::kRawRow), bar);
+            }
             int have = 0;      // first group whose address the lanes hold
             int64_t src = -1;  // byte offset of group have + lane, -1: none
             for (int i = 0; i < n && ok; ++i) {
-                const int g0 = 2 * (walk.tile + i);
+                const int g0 = 2 * (tile0 + i);
                 if (i == 0 || g0 >= have + 32) {
                     have = g0;
                     const int g = have + lane;
                     src = -1;
-                    if (g < groups && g < 2 * (walk.tile + n)) {
+                    if (g < groups && g < 2 * (tile0 + n)) {
                         const int page = __ldg(table + g / p.c.page_groups);
                         if (page >= 0 && page < p.c.n_pages)
                             src = ((static_cast<int64_t>(page) * p.c.n_heads + walk.head) * p.c.page_groups +
@@ -353,6 +408,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 if (!mbar_wait_bounded(full0 + 8 * static_cast<int>(k % Sh::kSlots),
                                        static_cast<uint32_t>((k / Sh::kSlots) & 1)))
                     record_error(p.err, kErrDrainWait);
+            for (int k = seg > 2 ? seg - 2 : 0; k < seg; ++k)
+                if (!mbar_wait_bounded(qfull0 + 8 * (k & 1), (k >> 1) & 1)) record_error(p.err, kErrDrainWait);
         }
         return;
     }
@@ -368,22 +425,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     int slot = warp;
     uint32_t phase = 0;
     bool ok = true;
-    for (; walk.left > 0; walk.next(p, ROWS)) {
-        const int n = walk.count();
+    for (int seg = 0; walk.left > 0; walk.next(p, ROWS), ++seg) {
+        const int n = walk.n_tiles(), tile0 = walk.first_tile();
         // ---- the segment's queries, as the mma's B fragments
+        if (ok && !__all_sync(0xffffffffu, tc_wait(qfull0 + 8 * (seg & 1), (seg >> 1) & 1, abort_flag))) {
+            if (lane == 0) record_error(p.err, kErrConsumerWait);
+            *abort_flag = 1;
+            ok = false;
+        }
         {
+            const uint32_t raw = base + Sh::kOffRaw + (seg & 1) * ROWS * Sh::kRawRow;
             constexpr int kItems = ROWS * NB * 4;
             for (int it = threadIdx.x; it < kItems; it += kWarps * 32) {
                 const int r = it / (NB * 4), b = it / 4 % NB, ti = it & 3;
                 const int row = walk.rt * ROWS + r;
                 const bool live = row < walk.q.m * p.group;
                 float x[8] = {};
-                if (live) {
-                    const int tok = row / p.group;
-                    load_q8(static_cast<const T *>(p.q) + (walk.q.q0 + tok) * p.q_stride +
-                                (walk.head * p.group + row - tok * p.group) * D + 32 * b + 4 * ti,
-                            x);
-                }
+                if (live) load_q8<T>(raw + r * Sh::kRawRow + (32 * b + 4 * ti) * static_cast<int>(sizeof(T)), x);
                 float big = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[i]));
@@ -432,6 +490,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty0 + 8 * (seg & 1));
         named_barrier(1, kWarps * 32);
         float factor[NT][2];
         int limit[NT][2];
@@ -465,48 +525,65 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             }
             if (ok) {
                 const uint32_t tile_a = base + Sh::kOffRing + slot * Sh::kTileBytes;
-                const int tok0 = (walk.tile + static_cast<int>(k - seg_k)) * kTile;
+                const int tok0 = (tile0 + static_cast<int>(k - seg_k)) * kTile;
                 const int info = slot_info[slot];
                 // ---- scores of 2 x 16 tokens: s[group][nt][0, 1: token g; 2, 3: token g + 8]
                 float s[2][NT][4];
                 uint32_t dv[2][2][NB / 2];  // value scales of tokens g and g + 8
+                {
+                    uint32_t w[2][2][NB], dk[2][2][NB / 2];
 #pragma unroll
-                for (int gr = 0; gr < 2; ++gr) {
-                    const uint32_t ga = tile_a + gr * G::kBytes;
-                    uint32_t w0[NB], w1[NB], d0[NB / 2], d1[NB / 2];
-                    ld_words<NB>(ga + g * G::kRow + t * (4 * NB), w0);
-                    ld_words<NB>(ga + (g + 8) * G::kRow + t * (4 * NB), w1);
-                    ld_halves<NB>(ga + G::kKS + g * G::kScaleRow, d0);
-                    ld_halves<NB>(ga + G::kKS + (g + 8) * G::kScaleRow, d1);
-                    ld_halves<NB>(ga + G::kVS + g * G::kScaleRow, dv[gr][0]);
-                    ld_halves<NB>(ga + G::kVS + (g + 8) * G::kScaleRow, dv[gr][1]);
+                    for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) s[gr][nt][0] = s[gr][nt][1] = s[gr][nt][2] = s[gr][nt][3] = 0.0f;
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t ga = tile_a + gr * G::kBytes;
+                            ld_words<NB>(ga + (g + 8 * h) * G::kRow + t * (4 * NB), w[gr][h]);
+                            ld_halves<NB>(ga + G::kKS + (g + 8 * h) * G::kScaleRow, dk[gr][h]);
+                            ld_halves<NB>(ga + G::kVS + (g + 8 * h) * G::kScaleRow, dv[gr][h]);
+                        }
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        const uint32_t x0 = w0[b], x1 = w1[b], y0 = x0 >> 8, y1 = x1 >> 8;
-                        const float2 k0 = unpack_half2(d0[b / 2]), k1 = unpack_half2(d1[b / 2]);
-                        const float ka = b & 1 ? k0.y : k0.x, kb = b & 1 ? k1.y : k1.x;
+                        uint32_t lo[2][4], hi[2][4];
+                        float ks[2][2];
+#pragma unroll
+                        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t x = w[gr][h][b], y = x >> 8;
+                                lo[gr][h] = x & 0x000F000Fu, lo[gr][2 + h] = y & 0x000F000Fu;
+                                hi[gr][h] = x & 0x00F000F0u, hi[gr][2 + h] = y & 0x00F000F0u;
+                                const float2 k2 = unpack_half2(dk[gr][h][b / 2]);
+                                ks[gr][h] = b & 1 ? k2.y : k2.x;
+                            }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint2 ini = ld_s64(base + Sh::kOffInit + (nt * NB + b) * 32 + t * 8);
-                            float acc[4] = {__uint_as_float(ini.x), __uint_as_float(ini.y), __uint_as_float(ini.x),
-                                            __uint_as_float(ini.y)};
+                            float acc[2][4];
 #pragma unroll
                             for (int q = 0; q < TERMS; ++q) {
                                 const uint4 bq = ld_s128(base + Sh::kOffQ + ((q * NT + nt) * NB + b) * 512 + lane * 16);
-                                mma_f16(acc, x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu, bq.x, bq.y);
-                                mma_f16(acc, x0 & 0x00F000F0u, x1 & 0x00F000F0u, y0 & 0x00F000F0u, y1 & 0x00F000F0u, bq.z, bq.w);
+#pragma unroll
+                                for (int gr = 0; gr < 2; ++gr) {
+                                    if (q == 0)
+                                        mma_f16(acc[gr], lo[gr][0], lo[gr][1], lo[gr][2], lo[gr][3], bq.x, bq.y,
+                                                __uint_as_float(ini.x), __uint_as_float(ini.y));
+                                    else
+                                        mma_f16(acc[gr], lo[gr][0], lo[gr][1], lo[gr][2], lo[gr][3], bq.x, bq.y);
+                                    mma_f16(acc[gr], hi[gr][0], hi[gr][1], hi[gr][2], hi[gr][3], bq.z, bq.w);
+                                }
                             }
-                            s[gr][nt][0] = fmaf(ka, acc[0], s[gr][nt][0]);
-                            s[gr][nt][1] = fmaf(ka, acc[1], s[gr][nt][1]);
-                            s[gr][nt][2] = fmaf(kb, acc[2], s[gr][nt][2]);
-                            s[gr][nt][3] = fmaf(kb, acc[3], s[gr][nt][3]);
+#pragma unroll
+                            for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    s[gr][nt][i] = b == 0 ? ks[gr][i >> 1] * acc[gr][i]
+                                                          : fmaf(ks[gr][i >> 1], acc[gr][i], s[gr][nt][i]);
                         }
                     }
                 }
                 bool odd = false;  // a value scale that is not finite, of a token that some rows do not see
-                if (tok0 + kTile > least || info != 3) {
+                const bool masked = tok0 + kTile > least || info != 3;
+                if (masked) {
                     // tokens that a row does not see, or that lie in no page: whatever
                     // the ring holds there (it may be NaN) is replaced
 #pragma unroll
@@ -528,16 +605,34 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         }
                     odd = __any_sync(0xffffffffu, odd);
                 }
-                // ---- exponents of the tokens' largest value scales (f16 exponent fields, 0 .. 30)
-                float ex[2][2];
+                // ---- the lane's largest score plus exponent, by column
+                float top[NT][2];
+                if (!masked) {
+                    __half2 vm[2];
 #pragma unroll
-                for (int gr = 0; gr < 2; ++gr)
+                    for (int gr = 0; gr < 2; ++gr) vm[gr] = __hmax2(max_scales<NB>(dv[gr][0]), max_scales<NB>(dv[gr][1]));
+                    const float ex = exponent_field(__hmax2(vm[0], vm[1]));
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t vmax = dv[gr][h][0] & 0x7FFF7FFFu;
-                        if (NB == 4) vmax = __vmaxu2(vmax, dv[gr][h][NB / 2 - 1] & 0x7FFF7FFFu);
-                        ex[gr][h] = static_cast<float>(min(max(vmax & 0xFFFFu, vmax >> 16) >> 10, 30u));
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            top[nt][c] = fmaf(fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])),
+                                              factor[nt][c], ex);
+                } else {  // token by token: one that a row does not see has no say in its reference
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float ex = exponent_field(max_scales<NB>(dv[gr][h]));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    top[nt][c] = fmaxf(top[nt][c], fmaf(s[gr][nt][2 * h + c], factor[nt][c], ex));
+                        }
+                }
                 // ---- running reference, weights
                 float keep[NT][2];
                 bool same = true;
@@ -546,8 +641,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float f = factor[nt][c];
-                        float mx = fmaxf(fmaxf(fmaf(s[0][nt][c], f, ex[0][0]), fmaf(s[0][nt][2 + c], f, ex[0][1])),
-                                         fmaxf(fmaf(s[1][nt][c], f, ex[1][0]), fmaf(s[1][nt][2 + c], f, ex[1][1])));
+                        float mx = top[nt][c];
 #pragma unroll
                         for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
                         mx = fmaxf(m[nt][c], mx - 29.0f);
@@ -631,29 +725,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], q);
-                if (g == 0) {
-                    stat[(warp * ROWS + 8 * nt + 2 * t + c) * 2] = m[nt][c];
-                    stat[(warp * ROWS + 8 * nt + 2 * t + c) * 2 + 1] = l[nt][c];
-                }
+                if (g == 0)
+                    *reinterpret_cast<float2 *>(stat + (warp * ROWS + 8 * nt + 2 * t + c) * 2) = make_float2(m[nt][c], l[nt][c]);
             }
-        named_barrier(1, kWarps * 32);
-        const bool whole = walk.tile == 0 && n == walk.tiles;
+        const bool whole = walk.tile == 0 && walk.count() == walk.tiles;
         // a part's result: slot 0 if it enters the segment from outside, slot 1 if the segment starts in it
         float *part = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile == 0 ? 1 : 0)) * part_floats(D, ROWS);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int r = 8 * nt + 2 * t + c;
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[(w * ROWS + r) * 2]);
-                const float f = top == -INFINITY ? 0.0f : exp2_approx(m[nt][c] - top);
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) o[nt][b][h][c] *= f, o[nt][b][h][2 + c] *= f;
-            }
 #pragma unroll
         for (int b0 = 0; b0 < NB; b0 += Sh::kChunkBlocks) {
             if (b0 != 0) named_barrier(1, kWarps * 32);  // the chunk before has been read
@@ -671,22 +748,24 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             named_barrier(1, kWarps * 32);
             constexpr int kPairs = 16 * Sh::kChunkBlocks;  // channel pairs of a row in this chunk
             for (int it = threadIdx.x; it < ROWS * kPairs; it += kWarps * 32) {
-                const int r = it / kPairs, c2 = 2 * (it % kPairs);
+                const int r = it / kPairs, c2 = 2 * (it % kPairs), row = walk.rt * ROWS + r;
+                if (row >= walk.q.m * p.group) continue;
+                float2 ml[kWarps];
+                float top = -INFINITY, den = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    ml[w] = *reinterpret_cast<const float2 *>(stat + (w * ROWS + r) * 2);
+                    top = fmaxf(top, ml[w].x);
+                }
+                const float ref = top == -INFINITY ? 0.0f : top;
                 float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 v = *reinterpret_cast<const float2 *>(join + (w * ROWS + r) * Sh::kJoinPitch + c2);
-                    sum.x += v.x, sum.y += v.y;
+                    const float f = exp2_approx(ml[w].x - ref);
+                    den = fmaf(ml[w].y, f, den);
+                    sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y);
                 }
-                const int row = walk.rt * ROWS + r;
-                if (row >= walk.q.m * p.group) continue;
-                float top = -INFINITY, den = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[(w * ROWS + r) * 2]);
-                if (top != -INFINITY)
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w)
-                        den = fmaf(stat[(w * ROWS + r) * 2 + 1], exp2_approx(stat[(w * ROWS + r) * 2] - top), den);
                 const int d = 32 * b0 + c2;
                 if (whole) {
                     const int tok = row / p.group;
@@ -700,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 }
             }
         }
-        named_barrier(1, kWarps * 32);  // statistics and sums have been read
+        // the next segment's first barrier comes after these reads; the join's areas are written after it
     }
 }
 
