@@ -19,20 +19,25 @@
 // Arithmetic, on mma.sync.m16n8k16 (f16 operands, f32 sums), tokens or
 // channels as the 16 rows and query rows as the 8 columns, so that a decode
 // step's few rows waste little:
-//  * scores: A = the key codes themselves. A 4-byte code word masked with
-//    0x000F000F holds two codes as f16 subnormals c 2^-24 (with 0x00F000F0,
-//    16 c 2^-24): one logic operation for two elements and no conversion; the
-//    queries of low-nibble elements carry the missing 16. The offset 8 of
-//    (code - 8) is the accumulator's start value, -8 sum of the block's q. Per
-//    block the f32 sum is multiplied by the token's key scale. Queries are
-//    scaled by a power of two to a largest magnitude of 2^10 .. 2^11 (exact).
+//  * codes as A: for f16 queries the key codes themselves. A 4-byte code word
+//    masked with 0x000F000F holds two codes as f16 subnormals c 2^-24 (with
+//    0x00F000F0, 16 c 2^-24): one logic operation for two elements and no
+//    conversion; the queries of low-nibble elements carry the missing 16, and
+//    the offset 8 of (code - 8) is the accumulator's start value, -8 sum of the
+//    block's q. The tensor cores align subnormals unnormalised, which costs
+//    about 7 of the sum's 24 bits: enough for f16 queries, not for f32 ones and
+//    not for values (a sum that nearly cancels), so those take code - 8 in f16,
+//    exact, for one more packed operation.
+//  * scores: per block the f32 sum is multiplied by the token's key scale.
+//    Queries are scaled by a power of two to a largest magnitude of 2^10 ..
+//    2^11 (exact).
 //  * values: B = weight x value scale per token and block (the scale varies
-//    along the summed axis), transposed among lanes with movmatrix; A = code -
-//    8 in f16 (exact). The softmax's running reference is not the largest
-//    score but the largest score plus the exponent of its token's largest value
-//    scale, less 29: every product is then below 2^15 and a row's largest near
-//    it, whatever the values' size. Weights, their sum and the accumulators
-//    share that reference, so it cancels.
+//    along the summed axis), transposed among lanes with movmatrix. The
+//    softmax's running reference is not the largest score but the largest score
+//    plus the exponent of its token's largest value scale, less 29: every
+//    product is then below 2^15 and a row's largest near it, whatever the
+//    values' size. Weights, their sum and the accumulators share that
+//    reference, so it cancels.
 // So codes enter exactly and only q and the weights are rounded: f16 queries
 // are exact and the weights take one f16 (2^-11 relative); for f32 both are
 // split in two f16 parts and each product is formed twice.
@@ -54,15 +59,15 @@ constexpr int kMaxCtas = 640;              // thread blocks of a launch (workspa
 template <int D, int NT, int TERMS> struct Shape {
     using G = KvGroup<D>;
     static constexpr int kTileBytes = 2 * G::kBytes;
-    static constexpr int kSlots = D == 128 ? 8 : 16;
+    static constexpr int kSlots = D == 128 ? 12 : 24;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kChunkBlocks = NT == 1 ? G::kNB : (NT == 2 ? 2 : 1);  // blocks of 32 channels joined at a time
+    static constexpr int kChunkBlocks = NT == 4 ? 1 : 2;  // blocks of 32 channels joined at a time
     static constexpr int kRawRow = D * (TERMS == 2 ? 4 : 2);                   // bytes of a query row
     static constexpr int kOffRing = 1024;
-    static constexpr int kOffRaw = kOffRing + kSlots * kTileBytes;             // two segments' query rows
-    static constexpr int kOffQ = kOffRaw + 2 * kRows * kRawRow;                // [term][nt][block][lane] 16 bytes
-    static constexpr int kOffInit = kOffQ + TERMS * NT * G::kNB * 512;         // [nt][block][8] f32
-    static constexpr int kOffRow = kOffInit + NT * G::kNB * 32;                // factor f32, limit int [rows]
+    static constexpr int kOffRaw = kOffRing + kSlots * kTileBytes;             // a segment's query rows
+    static constexpr int kOffQ = kOffRaw + kRows * kRawRow;                    // [term][nt][block][lane] 16 bytes
+    static constexpr int kOffInit = kOffQ + TERMS * NT * G::kNB * 512;         // [nt][block][4 pairs of columns, twice] f32
+    static constexpr int kOffRow = kOffInit + NT * G::kNB * 64;                // factor f32, limit int [rows]
     static constexpr int kOffStat = kOffRow + kRows * 8;                       // [warp][rows] reference, sum
     static constexpr int kOffJoin = kOffStat + kWarps * kRows * 8;             // [warp][rows][32 kChunkBlocks + 2]
     static constexpr int kJoinPitch = 32 * kChunkBlocks + 2;
@@ -72,6 +77,17 @@ template <int D, int NT, int TERMS> struct Shape {
 
 // A partial result: rows x D values, then the rows' maxima and sums.
 __host__ __device__ constexpr int64_t part_floats(int d, int rows) { return static_cast<int64_t>(rows) * (d + 2); }
+
+// What a thread block leaves for the join: the segment that starts in its part
+// and goes on in the next ones. At the workspace's start, one a block.
+struct Cut {
+    int parts;      // this block's and the following ones'; 0: no such segment
+    int rows, row0; // rows of the segment, its first row among the sequence's
+    int q0, head;   // first query row of the sequence, key/value head
+    int pad[3];
+};
+static_assert(sizeof(Cut) == 32, "two 16-byte loads");
+constexpr int64_t kCutFloats = kMaxCtas * static_cast<int64_t>(sizeof(Cut)) / 4;
 
 struct Seq {
     int len, m, q0;  // tokens in the cache, queries, first query row
@@ -118,7 +134,7 @@ struct Place {
     int64_t share;  // units of a block's part
 };
 
-// Finds the part of block `cta` of `ctas` (by the whole block: every thread
+// Finds the part of block `cta` of `ctas` (with the whole block: every thread
 // gets the result). seq = n_seq where the part is empty.
 template <int THREADS> __device__ Place locate(const KvAttendParams &p, int rows, int64_t cta, int ctas) {
     __shared__ int64_t warp_sum[THREADS / 32];
@@ -218,13 +234,26 @@ struct Walk {
     }
 };
 
+// Bounded wait (about 1 s) that suspends the thread between polls and gives up
+// once another thread of the block has set the abort flag.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1; i < kWaitLimitPolls; ++i) {
+        if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
+        if ((i & 15u) == 0 && (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    }
+    return false;
+}
+
 // d = a b + c
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1, float c0, float c1) {
+                                        uint32_t b1, const uint4 &c) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(__uint_as_float(c.x)), "f"(__uint_as_float(c.y)),
+          "f"(__uint_as_float(c.z)), "f"(__uint_as_float(c.w)));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -250,10 +279,12 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_half2(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
-// code - 8 in f16 of the low (high) nibbles of bytes 0 and 2.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) { return hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u); }
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
-    return hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 c) / 16 - 72
+// code - 8 in f16 of the low (high) nibbles of bytes 0 and 2; magic = 0x64006400.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t magic) {
+    return hsub2((w & 0x000F000Fu) | magic, 0x64086408u);  // 1024 + c - 1032
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t magic) {
+    return hfma2((w & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 c) / 16 - 72
 }
 template <int NB> __device__ __forceinline__ void ld_words(uint32_t a, uint32_t (&w)[NB]) {
     if (NB == 4) {
@@ -273,6 +304,8 @@ template <int NB> __device__ __forceinline__ void ld_halves(uint32_t a, uint32_t
         w[0] = ld_s32(a);
     }
 }
+
+__device__ __forceinline__ bool not_finite(uint32_t half_bits) { return (half_bits & 0x7C00u) == 0x7C00u; }
 
 // The largest magnitudes among a row's scales (halves apart; NaN has no say),
 // and the f16 exponent field of the larger one, 0 .. 30, as a float.
@@ -314,17 +347,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     const uint32_t full0 = base, empty0 = base + 8 * Sh::kSlots;
     volatile int *slot_info = reinterpret_cast<volatile int *>(smem + 16 * Sh::kSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots);
-    const uint32_t qfull0 = base + 20 * Sh::kSlots + 16, qempty0 = qfull0 + 16;
+    const uint32_t qfull = base + 20 * Sh::kSlots + 16, qempty = qfull + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Sh::kSlots; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(qfull0 + 8 * i, 1);
-            mbar_init(qempty0 + 8 * i, kWarps);
-        }
+        mbar_init(qfull, 1);
+        mbar_init(qempty, kWarps);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -334,6 +365,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     const int64_t u0 = static_cast<int64_t>(blockIdx.x) * place.share;
     int64_t units = place.units - u0;
     if (units > place.share) units = place.share;
+    Cut *const cut = reinterpret_cast<Cut *>(p.partial) + blockIdx.x;
+    float *const parts = p.partial + kCutFloats;
+    if (threadIdx.x == 0) cut->parts = 0;
     if (units <= 0) return;
     Walk walk;
     walk.start(p, place, ROWS, units);
@@ -350,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             const int32_t *table = p.table + walk.seq * p.table_stride;
             // the segment's query rows: of each token they cover, the heads are contiguous
             {
-                const uint32_t raw = base + Sh::kOffRaw + (seg & 1) * ROWS * Sh::kRawRow, bar = qfull0 + 8 * (seg & 1);
-                if (seg >= 2) ok = __all_sync(0xffffffffu, tc_wait(qempty0 + 8 * (seg & 1), ((seg >> 1) - 1) & 1, abort_flag));
+                const uint32_t raw = base + Sh::kOffRaw, bar = qfull;
+                if (seg >= 1) ok = __all_sync(0xffffffffu, wait_bounded(qempty, (seg - 1) & 1, abort_flag));
                 if (!ok) break;
                 const int row0 = walk.rt * ROWS;
                 int row1 = walk.q.m * p.group;
@@ -368,8 +402,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             }
             int have = 0;      // first group whose address the lanes hold
             int64_t src = -1;  // byte offset of group have + lane, -1: none
-            for (int i = 0; i < n && ok; ++i) {
-                const int g0 = 2 * (tile0 + i);
+            // up to four tiles at a time, two lanes each (one for each group)
+            for (int i = 0; i < n; i += 4) {
+                const int g0 = 2 * (tile0 + i), batch = min(4, n - i);
                 if (i == 0 || g0 >= have + 32) {
                     have = g0;
                     const int g = have + lane;
@@ -383,20 +418,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                             record_error(p.err, kErrBadIndex);
                     }
                 }
-                const int64_t mine = __shfl_sync(0xffffffffu, src, (g0 - have + (lane & 1)) & 31);
-                const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0) & 3u;
-                if (issued >= Sh::kSlots) ok = __all_sync(0xffffffffu, tc_wait(empty0 + 8 * slot, phase ^ 1u, abort_flag));
+                const int64_t mine = __shfl_sync(0xffffffffu, src, (g0 - have + (lane & 7)) & 31);
+                const uint32_t valid = (__ballot_sync(0xffffffffu, mine >= 0) >> (lane & 6)) & 3u;  // of the lane's tile
+                int my_slot = slot + (lane >> 1);
+                uint32_t my_phase = phase;
+                if (my_slot >= Sh::kSlots) my_slot -= Sh::kSlots, my_phase ^= 1u;
+                const bool active = lane < 2 * batch;
+                if (active && issued + (lane >> 1) >= Sh::kSlots) ok = wait_bounded(empty0 + 8 * my_slot, my_phase ^ 1u, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (lane == 0) {
-                    slot_info[slot] = static_cast<int>(valid);
-                    mbar_arrive_expect_tx(full0 + 8 * slot, static_cast<uint32_t>(__popc(valid)) * G::kBytes);
+                if (active && (lane & 1) == 0) {
+                    slot_info[my_slot] = static_cast<int>(valid);
+                    mbar_arrive_expect_tx(full0 + 8 * my_slot, static_cast<uint32_t>(__popc(valid)) * G::kBytes);
                 }
                 __syncwarp();
-                if (lane < 2 && mine >= 0)
-                    bulk_copy_g2s_plain(base + Sh::kOffRing + slot * Sh::kTileBytes + lane * G::kBytes, p.c.data + mine,
-                                        G::kBytes, full0 + 8 * slot);
-                ++issued;
-                if (++slot == Sh::kSlots) slot = 0, phase ^= 1u;
+                if (active && mine >= 0)
+                    bulk_copy_g2s_plain(base + Sh::kOffRing + my_slot * Sh::kTileBytes + (lane & 1) * G::kBytes,
+                                        p.c.data + mine, G::kBytes, full0 + 8 * my_slot);
+                issued += batch;
+                slot += batch;
+                if (slot >= Sh::kSlots) slot -= Sh::kSlots, phase ^= 1u;
             }
             if (ok) walk.next(p, ROWS);
         }
@@ -408,14 +449,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 if (!mbar_wait_bounded(full0 + 8 * static_cast<int>(k % Sh::kSlots),
                                        static_cast<uint32_t>((k / Sh::kSlots) & 1)))
                     record_error(p.err, kErrDrainWait);
-            for (int k = seg > 2 ? seg - 2 : 0; k < seg; ++k)
-                if (!mbar_wait_bounded(qfull0 + 8 * (k & 1), (k >> 1) & 1)) record_error(p.err, kErrDrainWait);
+            if (seg > 0 && !mbar_wait_bounded(qfull, (seg - 1) & 1)) record_error(p.err, kErrDrainWait);
         }
         return;
     }
 
     // ---------------- consumers
     const int g = lane >> 2, t = lane & 3;
+    // 0x64006400, by way of a value the compiler does not know: (word & mask) | magic is then one
+    // logic operation (it takes one immediate) and not two
+    const uint32_t magic = 0x64006400u | (static_cast<uint32_t>(p.n_tok) >> 31);
     float *row_factor = reinterpret_cast<float *>(smem + Sh::kOffRow);
     int *row_limit = reinterpret_cast<int *>(smem + Sh::kOffRow) + ROWS;
     float *stat = reinterpret_cast<float *>(smem + Sh::kOffStat);
@@ -428,13 +471,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     for (int seg = 0; walk.left > 0; walk.next(p, ROWS), ++seg) {
         const int n = walk.n_tiles(), tile0 = walk.first_tile();
         // ---- the segment's queries, as the mma's B fragments
-        if (ok && !__all_sync(0xffffffffu, tc_wait(qfull0 + 8 * (seg & 1), (seg >> 1) & 1, abort_flag))) {
+        if (ok && !__all_sync(0xffffffffu, wait_bounded(qfull, seg & 1, abort_flag))) {
             if (lane == 0) record_error(p.err, kErrConsumerWait);
             *abort_flag = 1;
             ok = false;
         }
         {
-            const uint32_t raw = base + Sh::kOffRaw + (seg & 1) * ROWS * Sh::kRawRow;
+            const uint32_t raw = base + Sh::kOffRaw;
             constexpr int kItems = ROWS * NB * 4;
             for (int it = threadIdx.x; it < kItems; it += kWarps * 32) {
                 const int r = it / (NB * 4), b = it / 4 % NB, ti = it & 3;
@@ -462,27 +505,29 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e0 = (i & 2) * 2 + (i & 1);
-                    const float f = i < 2 ? 16.0f : 1.0f;
+                    const float f = i < 2 && TERMS == 1 ? 16.0f : 1.0f;  // (subnormal codes: the high nibbles are 16 c)
                     w[0][i] = pack_half2(x[e0] * f, x[e0 + 2] * f);
                     if (TERMS == 2) {
                         const float2 hi = unpack_half2(w[0][i]);
                         w[TERMS - 1][i] = pack_half2(x[e0] * f - hi.x, x[e0 + 2] * f - hi.y);
-                        const float2 lo = unpack_half2(w[TERMS - 1][i]);
-                        sum += (hi.x + lo.x + (hi.y + lo.y)) / f;
                     }
                 }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (TERMS == 1) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                }
                 const int nt = r >> 3, rr = r & 7;
 #pragma unroll
                 for (int q = 0; q < TERMS; ++q)
                     *reinterpret_cast<uint4 *>(smem + Sh::kOffQ + ((q * NT + nt) * NB + b) * 512 + (rr * 4 + ti) * 16) =
                         make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
                 if (ti == 0) {
-                    reinterpret_cast<float *>(smem + Sh::kOffInit)[(nt * NB + b) * 8 + rr] = sum * -0x1p-17f;  // -8 * 16 * 2^-24
+                    float *ini = reinterpret_cast<float *>(smem + Sh::kOffInit) + (nt * NB + b) * 16 + (rr >> 1) * 4 + (rr & 1);
+                    ini[0] = ini[2] = sum * -0x1p-17f;  // -8 * 16 * 2^-24, 0 for code - 8
                     if (b == 0) {
-                        // 2^24 / 16 2^(e - 10); never 0, which times an unseen token's -inf would be NaN
-                        row_factor[r] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * 0x1p10f *
+                        // 2^(e - 10), for subnormal codes times 2^24 / 16; never 0, which times an unseen
+                        // token's -inf would be NaN
+                        row_factor[r] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * (TERMS == 1 ? 0x1p10f : 0x1p-10f) *
                                                   __uint_as_float(static_cast<uint32_t>(e + 127) << 23),
                                               1e-37f);
                         row_limit[r] = live ? walk.q.len - walk.q.m + row / p.group + 1 : 0;
@@ -491,10 +536,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(qempty0 + 8 * (seg & 1));
+        if (lane == 0) mbar_arrive(qempty);
         named_barrier(1, kWarps * 32);
         float factor[NT][2];
-        int limit[NT][2];
         // the first row sees least (rows past the last have no say: their result is not stored)
         const int least = row_limit[0];
 #pragma unroll
@@ -502,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 factor[nt][c] = row_factor[8 * nt + 2 * t + c];
-                limit[nt][c] = row_limit[8 * nt + 2 * t + c];
             }
         float m[NT][2], l[NT][2], o[NT][NB][2][4];
 #pragma unroll
@@ -518,12 +561,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
         }
 
         for (; k < seg_k + n; k += kWarps) {
-            if (ok && !__all_sync(0xffffffffu, tc_wait(full0 + 8 * slot, phase, abort_flag))) {
+            if (!ok) continue;
+            ok = __all_sync(0xffffffffu, wait_bounded(full0 + 8 * slot, phase, abort_flag));
+            if (!ok) {
                 if (lane == 0) record_error(p.err, kErrConsumerWait);
                 *abort_flag = 1;
-                ok = false;
+                continue;
             }
-            if (ok) {
+            {
                 const uint32_t tile_a = base + Sh::kOffRing + slot * Sh::kTileBytes;
                 const int tok0 = (tile0 + static_cast<int>(k - seg_k)) * kTile;
                 const int info = slot_info[slot];
@@ -550,14 +595,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const uint32_t x = w[gr][h][b], y = x >> 8;
-                                lo[gr][h] = x & 0x000F000Fu, lo[gr][2 + h] = y & 0x000F000Fu;
-                                hi[gr][h] = x & 0x00F000F0u, hi[gr][2 + h] = y & 0x00F000F0u;
+                                if (TERMS == 1) {
+                                    lo[gr][h] = x & 0x000F000Fu, lo[gr][2 + h] = y & 0x000F000Fu;
+                                    hi[gr][h] = x & 0x00F000F0u, hi[gr][2 + h] = y & 0x00F000F0u;
+                                } else {
+                                    lo[gr][h] = low_codes(x, magic), lo[gr][2 + h] = low_codes(y, magic);
+                                    hi[gr][h] = high_codes(x, magic), hi[gr][2 + h] = high_codes(y, magic);
+                                }
                                 const float2 k2 = unpack_half2(dk[gr][h][b / 2]);
                                 ks[gr][h] = b & 1 ? k2.y : k2.x;
                             }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const uint2 ini = ld_s64(base + Sh::kOffInit + (nt * NB + b) * 32 + t * 8);
+                            const uint4 ini = TERMS == 1 ? ld_s128(base + Sh::kOffInit + (nt * NB + b) * 64 + t * 16)
+                                                         : make_uint4(0u, 0u, 0u, 0u);
                             float acc[2][4];
 #pragma unroll
                             for (int q = 0; q < TERMS; ++q) {
@@ -565,8 +616,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                                 for (int gr = 0; gr < 2; ++gr) {
                                     if (q == 0)
-                                        mma_f16(acc[gr], lo[gr][0], lo[gr][1], lo[gr][2], lo[gr][3], bq.x, bq.y,
-                                                __uint_as_float(ini.x), __uint_as_float(ini.y));
+                                        mma_f16(acc[gr], lo[gr][0], lo[gr][1], lo[gr][2], lo[gr][3], bq.x, bq.y, ini);
                                     else
                                         mma_f16(acc[gr], lo[gr][0], lo[gr][1], lo[gr][2], lo[gr][3], bq.x, bq.y);
                                     mma_f16(acc[gr], hi[gr][0], hi[gr][1], hi[gr][2], hi[gr][3], bq.z, bq.w);
@@ -595,13 +645,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                             for (int i = 0; i < NB / 2; ++i) {
                                 if (!in_page || tok >= walk.q.len) dv[gr][h][i] = 0;
-                                odd = odd || (dv[gr][h][i] & 0x7C00u) == 0x7C00u || (dv[gr][h][i] & 0x7C000000u) == 0x7C000000u;
+                                odd = odd || not_finite(dv[gr][h][i]) || not_finite(dv[gr][h][i] >> 16);
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int c = 0; c < 2; ++c)
-                                    if (!in_page || tok >= limit[nt][c]) s[gr][nt][2 * h + c] = -INFINITY;
+                                    if (!in_page || tok >= row_limit[8 * nt + 2 * t + c]) s[gr][nt][2 * h + c] = -INFINITY;
                         }
                     odd = __any_sync(0xffffffffu, odd);
                 }
@@ -670,6 +720,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) o[nt][b][h][i] *= keep[nt][i & 1];
                 }
+                if (odd) {
+                    // a value scale that is not finite: the block's channels become NaN for the rows
+                    // that give its token a weight, and no other row's product meets it
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                const bool bad = not_finite(dv[gr][h][b / 2] >> (16 * (b & 1)));
+                                if (bad) dv[gr][h][b / 2] &= b & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c) {
+                                        int hit = bad && s[gr][nt][2 * h + c] != 0.0f;
+#pragma unroll
+                                        for (int q = 4; q < 32; q <<= 1) hit |= __shfl_xor_sync(0xffffffffu, hit, q);
+                                        if (hit) o[nt][b][0][c] = o[nt][b][0][2 + c] = o[nt][b][1][c] = o[nt][b][1][2 + c] = NAN;
+                                    }
+                            }
+                }
                 // ---- values
 #pragma unroll
                 for (int gr = 0; gr < 2; ++gr) {
@@ -683,19 +755,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
                         const uint32_t wa = __byte_perm(v[0][b / 2], v[1][b / 2], sel);
                         const uint32_t wb = __byte_perm(v[2][b / 2], v[3][b / 2], sel);
-                        const uint32_t a0 = low_codes(wa), a1 = low_codes(wa >> 8), a2 = low_codes(wb), a3 = low_codes(wb >> 8);
-                        const uint32_t h0 = high_codes(wa), h1 = high_codes(wa >> 8), h2 = high_codes(wb), h3 = high_codes(wb >> 8);
+                        const uint32_t a0 = low_codes(wa, magic), a1 = low_codes(wa >> 8, magic);
+                        const uint32_t a2 = low_codes(wb, magic), a3 = low_codes(wb >> 8, magic);
+                        const uint32_t h0 = high_codes(wa, magic), h1 = high_codes(wa >> 8, magic);
+                        const uint32_t h2 = high_codes(wb, magic), h3 = high_codes(wb >> 8, magic);
                         const float2 f0 = unpack_half2(dv[gr][0][b / 2]), f1 = unpack_half2(dv[gr][1][b / 2]);
                         const float fa = b & 1 ? f0.y : f0.x, fb = b & 1 ? f1.y : f1.x;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float p0 = s[gr][nt][0] * fa, p1 = s[gr][nt][1] * fa;
-                            float p2 = s[gr][nt][2] * fb, p3 = s[gr][nt][3] * fb;
-                            if (odd) {  // no weight, no share, whatever the scale
-                                p0 = s[gr][nt][0] == 0.0f ? 0.0f : p0, p1 = s[gr][nt][1] == 0.0f ? 0.0f : p1;
-                                p2 = s[gr][nt][2] == 0.0f ? 0.0f : p2, p3 = s[gr][nt][3] == 0.0f ? 0.0f : p3;
-                            }
-                            uint32_t x = pack_half2(p0, p1), y = pack_half2(p2, p3);
+                            const float2 pa = make_float2(s[gr][nt][0] * fa, s[gr][nt][1] * fa);
+                            const float2 pb = make_float2(s[gr][nt][2] * fb, s[gr][nt][3] * fb);
+                            uint32_t x = pack_half2(pa.x, pa.y), y = pack_half2(pb.x, pb.y);
 #pragma unroll
                             for (int q = 0; q < TERMS; ++q) {
                                 const uint32_t b0 = transpose8(x), b1 = transpose8(y);
@@ -703,8 +773,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                                 mma_f16(o[nt][b][1], h0, h1, h2, h3, b0, b1);
                                 if (q + 1 < TERMS) {
                                     const float2 xh = unpack_half2(x), yh = unpack_half2(y);
-                                    x = pack_half2(p0 - xh.x, p1 - xh.y);
-                                    y = pack_half2(p2 - yh.x, p3 - yh.y);
+                                    const float2 ra = fadd2(pa, make_float2(-xh.x, -xh.y)), rb = fadd2(pb, make_float2(-yh.x, -yh.y));
+                                    x = pack_half2(ra.x, ra.y), y = pack_half2(rb.x, rb.y);
                                 }
                             }
                         }
@@ -730,7 +800,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             }
         const bool whole = walk.tile == 0 && walk.count() == walk.tiles;
         // a part's result: slot 0 if it enters the segment from outside, slot 1 if the segment starts in it
-        float *part = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile == 0 ? 1 : 0)) * part_floats(D, ROWS);
+        float *part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile == 0 ? 1 : 0)) * part_floats(D, ROWS);
+        if (!whole && walk.tile == 0 && threadIdx.x == 0) {  // (thread 0 wrote the 0 above)
+            const int row0 = walk.rt * ROWS;
+            *cut = Cut{1 + static_cast<int>((walk.tiles - walk.count() + place.share - 1) / place.share),
+                       min(ROWS, walk.q.m * p.group - row0), row0, walk.q.q0, walk.head, {0, 0, 0}};
+        }
 #pragma unroll
         for (int b0 = 0; b0 < NB; b0 += Sh::kChunkBlocks) {
             if (b0 != 0) named_barrier(1, kWarps * 32);  // the chunk before has been read
@@ -783,57 +858,100 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     }
 }
 
-// Joins the parts of the segments that thread blocks of kv_attend_kernel cut.
-// Block c - 1 looks at the cut before part c: if it is the first one inside
-// its segment, the parts c - 1, c, ... up to the segment's end are summed.
+// Joins the parts of the segments that thread blocks of kv_attend_kernel cut:
+// block (c, r) row r of the segment that starts in block c and goes on in the
+// next ones, part 0 the second slot of block c, the others the first slots of
+// c + 1, c + 2, ... Eight warps take the parts in turn, each lane D/32 channels;
+// their sums meet in shared memory in a fixed order.
 template <int D, class T, int NT>
-__global__ void __launch_bounds__(128) kv_join_kernel(const KvAttendParams p, int ctas) {
-    constexpr int ROWS = 8 * NT;
-    // every block of the kernel before has passed its own wait, so the lengths are there
-    const int64_t c = blockIdx.x + 1;
-    const Place place = locate<128>(p, ROWS, c, ctas);
+__global__ void __launch_bounds__(256) kv_join_kernel(const KvAttendParams p) {
+    constexpr int ROWS = 8 * NT, kPer = D / 32, kJoinWarps = 8;
+    __shared__ float sums[kJoinWarps][D];
+    __shared__ float2 stats[kJoinWarps];
     pdl_allow_dependents();
-    const int64_t u = c * place.share;
-    Walk walk;
-    walk.start(p, place, ROWS, u < place.units ? 1 : 0);
     pdl_wait_prior_grids();  // in every block: what comes next on the stream then waits for the kernel before, too
-    if (u >= place.units || walk.tile == 0 || walk.tile > place.share) return;  // no cut, or not its segment's first
-    const int64_t end = u - walk.tile + walk.tiles;                             // the segment's end
-    const int parts = 1 + static_cast<int>((end - u + place.share - 1) / place.share);
-    // part 0 is the second slot of block c - 1, the others the first of c, c + 1, ...
-    const float *part0 = p.partial + (2 * (c - 1) + 1) * part_floats(D, ROWS);
-    const float *part1 = p.partial + 2 * c * part_floats(D, ROWS);
+    const Cut cut = reinterpret_cast<const Cut *>(p.partial)[blockIdx.x];
+    const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (cut.parts == 0 || r >= cut.rows) return;
     const int64_t pitch = 2 * part_floats(D, ROWS);
-    int rows = walk.q.m * p.group - walk.rt * ROWS;
-    if (rows > ROWS) rows = ROWS;
-    for (int it = threadIdx.x; it < rows * (D / 2); it += blockDim.x) {
-        const int r = it / (D / 2), d = 2 * (it % (D / 2));
-        const int64_t st = static_cast<int64_t>(ROWS) * D + 2 * r, at = static_cast<int64_t>(r) * D + d;
-        float top = __ldcg(part0 + st), den = 0.0f;
-        for (int i = 0; i + 1 < parts; ++i) top = fmaxf(top, __ldcg(part1 + i * pitch + st));
-        float2 sum = make_float2(0.0f, 0.0f);
-        if (top != -INFINITY) {
-            for (int i = 0; i < parts; ++i) {
-                const float *q = i == 0 ? part0 : part1 + (i - 1) * pitch;
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q + st));
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(q + at));
-                const float f = exp2_approx(ml.x - top);
-                den = fmaf(ml.y, f, den);
-                sum.x = fmaf(v.x, f, sum.x);
-                sum.y = fmaf(v.y, f, sum.y);
+    const float *first = p.partial + kCutFloats + blockIdx.x * pitch;  // the parts: first + part_floats, first + i pitch
+    const int64_t at = static_cast<int64_t>(r) * D + lane * kPer, st = static_cast<int64_t>(ROWS) * D + 2 * r;
+    float top = -INFINITY, den = 0.0f, acc[kPer] = {};
+    for (int i0 = warp; i0 < cut.parts; i0 += 4 * kJoinWarps) {
+        float2 ml[4];
+        float v[4][kPer];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kJoinWarps;
+            ml[j] = make_float2(-INFINITY, 0.0f);
+            if (i < cut.parts) {
+                const float *q = i == 0 ? first + part_floats(D, ROWS) : first + i * pitch;
+                ml[j] = __ldcg(reinterpret_cast<const float2 *>(q + st));
+#pragma unroll
+                for (int k = 0; k < kPer; k += 2) {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(q + at + k));
+                    v[j][k] = x.x, v[j][k + 1] = x.y;
+                }
             }
         }
-        const int row = walk.rt * ROWS + r, tok = row / p.group;
-        const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-        store2(static_cast<T *>(p.out) +
-                   (static_cast<int64_t>(walk.q.q0 + tok) * p.n_heads + walk.head * p.group + row - tok * p.group) * D + d,
-               sum.x * inv, sum.y * inv);
+        float nt = top;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) nt = fmaxf(nt, ml[j].x);
+        if (nt == -INFINITY) continue;
+        const float keep = exp2_approx(top - nt);
+        top = nt;
+        den *= keep;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] *= keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i0 + j * kJoinWarps >= cut.parts) break;
+            const float f = exp2_approx(ml[j].x - top);
+            den = fmaf(ml[j].y, f, den);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] = fmaf(v[j][k], f, acc[k]);
+        }
     }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) sums[warp][lane * kPer + k] = acc[k];
+    if (lane == 0) stats[warp] = make_float2(top, den);
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    const int d = 2 * threadIdx.x;
+    top = -INFINITY, den = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w].x);
+    float2 sum = make_float2(0.0f, 0.0f);
+    if (top != -INFINITY)
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = exp2_approx(stats[w].x - top);
+            den = fmaf(stats[w].y, f, den);
+            sum.x = fmaf(sums[w][d], f, sum.x), sum.y = fmaf(sums[w][d + 1], f, sum.y);
+        }
+    const int row = cut.row0 + r, tok = row / p.group;
+    const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+    store2(static_cast<T *>(p.out) +
+               (static_cast<int64_t>(cut.q0 + tok) * p.n_heads + cut.head * p.group + row - tok * p.group) * D + d,
+           sum.x * inv, sum.y * inv);
 }
 
 // Query rows a segment takes: 8 a fragment column set, as few as hold all rows
 // of a head, at most 32 (more rows run as further segments over the same tokens).
 int row_sets(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+cudaError_t launch_join(void (*kernel)(KvAttendParams), dim3 grid, cudaStream_t s, const KvAttendParams &p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 template <int D, class T, int NT> cudaError_t launch(const KvAttendParams &p, int sms, int device, cudaStream_t s) {
     using Sh = Shape<D, NT, (sizeof(T) == 4 ? 2 : 1)>;
@@ -848,7 +966,8 @@ template <int D, class T, int NT> cudaError_t launch(const KvAttendParams &p, in
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     cudaError_t e = launch_pdl(kv_attend_kernel<D, T, NT>, ctas, kThreads, Sh::kSmem, s, p);
     if (e != cudaSuccess || ctas == 1) return e;
-    return launch_pdl(kv_join_kernel<D, T, NT>, ctas - 1, 128, 0, s, p, ctas);
+    const int64_t rows = static_cast<int64_t>(p.max_q_len) * p.group;
+    return launch_join(kv_join_kernel<D, T, NT>, dim3(ctas - 1, static_cast<unsigned>(rows < 8 * NT ? rows : 8 * NT)), s, p);
 }
 
 template <int D, class T> cudaError_t launch_rows(const KvAttendParams &p, int sms, int device, cudaStream_t s) {
@@ -862,7 +981,7 @@ template <int D, class T> cudaError_t launch_rows(const KvAttendParams &p, int s
 }  // namespace
 
 size_t kv_attend_workspace(int head_dim, int rows) {
-    return static_cast<size_t>(2 * kMaxCtas * part_floats(head_dim, 8 * row_sets(rows))) * sizeof(float);
+    return static_cast<size_t>(kCutFloats + 2 * kMaxCtas * part_floats(head_dim, 8 * row_sets(rows))) * sizeof(float);
 }
 
 cudaError_t launch_kv_attend(const KvAttendParams &p, int head_dim, int type, int sms, int device, cudaStream_t s) {

@@ -125,7 +125,9 @@ size_t qkv_attend_workspace_bytes(int head_dim, int n_kv_heads, int n_heads, int
  * sequence's number of queries; a sequence with more, or with q_offsets
  * outside 0 .. n_tok or falling, is left out (code 4). A length outside
  * 0 .. table_stride * page_size is taken as the nearer end, a page outside the
- * cache as tokens that are not seen (both code 4). The result does not depend
+ * cache as tokens that are not seen (both code 4). A value block whose scale
+ * is not finite gives NaN in its 32 channels to the rows that see its token.
+ * The result does not depend
  * on what other sequences a call has beyond rounding: a long sequence is split
  * where the thread blocks' shares end. Same inputs, same bits. */
 int qkv_attend(const qkv_cache *cache, int type, const void *q, int64_t q_stride, void *out, const int32_t *table,
