@@ -4,19 +4,25 @@
 // A work item is 256 query rows of one key/value head's group: tokens of one
 // sequence times `pack` heads (the largest power of two that divides the
 // group, at most 128), so that a short prompt's rows fill a tile. Two 128-row
-// tiles A and B share every key/value tile of 128 tokens. Per thread block:
-//  * warp 0, lane 0: TMA producer. The two query tiles, then key and value
-//    tiles in turn into a ring (128-byte swizzle, 64 channels a box).
+// tiles A and B share every key/value tile of 128 tokens. One thread block a
+// multiprocessor takes items in turn (of falling length, in snake order, so
+// that the blocks' sums are alike), and every role runs on into the next item
+// as soon as its own operands allow:
+//  * warp 0: finds the items and publishes them; lane 0 is the TMA producer:
+//    query tiles, then key and value tiles in turn into a ring (128-byte
+//    swizzle, 64 channels a box).
 //  * warp 1, lane 0: issues tcgen05.mma. S = Q K^T into 128 tensor-memory
 //    columns a tile, O += P V with P read from tensor memory (f16, over S's
 //    columns) and V as it lies in memory (N-major operand). The order
 //    PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) keeps the tensor cores on one tile while
 //    the other one's softmax runs.
-//  * warps 2..5 and 6..9: softmax of tile A and B, a row a thread: S from
+//  * warps 4..7 and 8..11: softmax of tile A and B, a row a thread: S from
 //    tensor memory, running maximum, exp2, P back in f16. O is rescaled in
 //    place only when a row's maximum has grown by more than 2^8 over the one
-//    its weights refer to (weights then stay below 2^8, far from f16's limit);
-//    the same threads divide by the sum and store.
+//    its weights refer to (weights then stay below 2^8, far from f16's limit).
+//  * warps 12..15: divide O by the rows' sums and store, while the others are
+//    in the next item.
+// The softmax warps take the registers that the other two warpgroups give up.
 // Only tiles on the diagonal are masked. The product P V takes 0 times every
 // unseen value, which is NaN for a value that is not finite: a row whose
 // result is not finite is computed again, over its own rows alone, by one warp.
@@ -31,7 +37,8 @@ namespace qg {
 
 namespace {
 
-constexpr int kThreads = 10 * 32;
+constexpr int kThreads = 16 * 32;
+constexpr int kItems = 4;  // items known ahead
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr uint32_t kTmemCols = 512;  // S_A, S_B, O_A, O_B at 0, 128, 256, 384
 constexpr float kGrow = 8.0f;        // log2 of how far a row's weights may exceed 1
@@ -39,21 +46,34 @@ constexpr float kGrow = 8.0f;        // log2 of how far a row's weights may exce
 template <int D> struct Shape {
     static constexpr int kTile = 128 * D * 2;  // bytes of a query, key or value tile
     static constexpr int kStages = D == 128 ? 5 : 10;
-    static constexpr int kSmem = 1024 + 1024 + (2 + kStages) * kTile;  // alignment, barriers, tiles
+    static constexpr int kTiles = (2 + kStages) * kTile;
+    static constexpr int kSmem = kTiles + 2560;  // tiles, then barriers, items and sums
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
-// Two-operand forms of tcgen05.mma, kind::f16, f32 accumulators.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// tcgen05.mma, kind::f16, f32 accumulators, and its commit, issued where
+// `issue` is not 0 (one lane). The whole warp runs the code around them: its
+// addresses and descriptors then stay in uniform registers, which the
+// instructions take their operands from; inside a branch of one lane each
+// operand was moved there anew, and issuing took longer than the products.
+__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc),
+        "r"(issue)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc),
+        "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t issue, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(issue)
         : "memory");
 }
 // Shared-memory descriptor of a 128-byte-swizzled N-major operand (64-element
@@ -98,6 +118,18 @@ __device__ __forceinline__ void tm_wait_ld(uint32_t (&v)[32]) {
                  : "memory");
 }
 
+// tc_wait for waits that are usually long: suspended between polls, so that it
+// takes no issue slots from the softmax warps.
+__device__ __forceinline__ bool idle_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1; i < kWaitLimitPolls; ++i) {
+        if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
+        if ((i & 15u) == 0 && (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    }
+    return false;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -114,6 +146,7 @@ struct Item {
     int tok0;         // first token of tile A within the sequence
     int head0;        // first query head
     int tiles[2];     // key/value tiles that A and B see (0: no rows)
+    int last;         // 1: no item, the end
 };
 
 // Sequence s as rows [start, end); empty where its offsets are out of range.
@@ -177,14 +210,30 @@ __device__ __forceinline__ bool find_item(const PromptParams &p, int pack, int i
     return true;
 }
 
-__device__ __forceinline__ void store8(__half *p, const float (&x)[8]) {
-    *reinterpret_cast<uint4 *>(p) =
-        make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+// Sixteen values in one (f16) or two (f32) 32-byte stores.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store16(__half *p, const float (&x)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_half2(x[2 * i], x[2 * i + 1]);
+    store32(p, w);
 }
+__device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * h + i]);
+        store32(p + 8 * h, w);
+    }
+}
+
+template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // One query row over the rows it sees, by one warp, in f32.
 template <int D, class TO>
@@ -227,30 +276,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap map_v, const PromptParams p, const int pack) {
     using Sh = Shape<D>;
     constexpr int kHalves = D / 64;  // boxes of 64 channels
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_a = smem_addr(smem_raw), base_a = (raw_a + 1023u) & ~1023u;
-    uint8_t *base = smem_raw + (base_a - raw_a);
-    // full[stages] | empty[stages] | q | s_full[2] | p_ready[2] | o_full[2] | final | tensor-memory address | abort | item
-    const uint32_t full0 = base_a, empty0 = base_a + 8 * Sh::kStages, bar_q = base_a + 16 * Sh::kStages;
-    const uint32_t s_full = bar_q + 8, p_ready = bar_q + 24, o_full = bar_q + 40, mfinal = bar_q + 56;
-    uint8_t *misc = base + 16 * Sh::kStages + 64;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 4);
-    volatile int *found = reinterpret_cast<volatile int *>(misc + 8);
-    Item *shared_item = reinterpret_cast<Item *>(misc + 16);
-    const uint32_t q_a = base_a + 1024, ring_a = q_a + 2 * Sh::kTile;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];  // (the swizzle's atoms are 1024 bytes)
+    const uint32_t q_a = smem_addr(smem_raw), ring_a = q_a + 2 * Sh::kTile, base_a = q_a + Sh::kTiles;
+    uint8_t *base = smem_raw + Sh::kTiles;
+    // barriers, 8 bytes each (those of the two tiles side by side)
+    const uint32_t full0 = base_a, empty0 = full0 + 8 * Sh::kStages, q_full = empty0 + 8 * Sh::kStages, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, p_ready = s_full + 16, o_full = p_ready + 16, o_empty = o_full + 16;
+    const uint32_t l_full = o_empty + 16, item_full = l_full + 16, item_empty = item_full + 8 * kItems, mfinal = item_empty + 8 * kItems;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + 384);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(base + 388);
+    volatile Item *items = reinterpret_cast<volatile Item *>(base + 392);
+    volatile float *sums = reinterpret_cast<volatile float *>(base + 512);  // [item parity][tile][row]
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Sh::kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
-        mbar_init(bar_q, 1);
         for (int x = 0; x < 2; ++x) {
+            mbar_init(q_full + 8 * x, 1);
+            mbar_init(q_empty + 8 * x, 1);
             mbar_init(s_full + 8 * x, 1);
             mbar_init(p_ready + 8 * x, 4);
             mbar_init(o_full + 8 * x, 1);
+            mbar_init(o_empty + 8 * x, 4);
+            mbar_init(l_full + 8 * x, 4);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(item_full + 8 * i, 1);
+            mbar_init(item_empty + 8 * i, 13);  // the mma issuer and twelve warps
         }
         mbar_init(mfinal, 1);
         *abort_flag = 0;
@@ -260,215 +315,340 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_alloc(smem_addr(tmem_slot), kTmemCols);
         tc_relinquish();
     }
-    pdl_wait_prior_grids();
-    pdl_allow_dependents();
-    if (warp == 0) {
-        Item it;
-        const bool ok = find_item(p, pack, blockIdx.x, it);
-        if (lane == 0) {
-            *found = ok;
-            if (ok) *shared_item = it;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (!*found) {
-        if (warp == 1) tc_dealloc(tmem, kTmemCols);
-        return;
-    }
-    const Item item = *shared_item;
-    const int n_tiles = max(item.tiles[0], item.tiles[1]);
     const int tile_toks = kTileRows / pack;
+    pdl_wait_prior_grids();
+    pdl_allow_dependents();
+    // item k of the block as a consumer: all lanes of the warp (or one thread) call it
+    auto wait_item = [&](int k) { return idle_wait(item_full + 8 * (k % kItems), (k / kItems) & 1, abort_flag); };
+    auto read_item = [&](int k) {
+        const volatile Item &s = items[k % kItems];
+        Item it;
+        it.start = s.start, it.end = s.end, it.tok0 = s.tok0, it.head0 = s.head0;
+        it.tiles[0] = s.tiles[0], it.tiles[1] = s.tiles[1], it.last = s.last;
+        return it;
+    };
 
-    if (warp == 0) {
-        // ---------------- producer
-        if (lane == 0) {
-            const int kv_head = item.head0 / p.group;
-            mbar_arrive_expect_tx(bar_q, 2 * Sh::kTile);
-            for (int x = 0; x < 2; ++x)
-                for (int h = 0; h < kHalves; ++h)
-                    tma_load_3d(q_a + x * Sh::kTile + h * (128 * 128), &map_q, 64 * h, item.head0,
-                                item.start + item.tok0 + x * tile_toks, bar_q);
-            int s = 0, issued = 0;
+    if (warp < 4) {
+        fewer_registers<64>();
+        if (warp == 0) {
+            // ---------------- items and copies
+            int stage = 0;
             uint32_t ph = 0;
-            for (int i = 0; i < 2 * n_tiles; ++i) {
-                if (issued >= Sh::kStages && !tc_wait(empty0 + 8 * s, ph ^ 1u, abort_flag)) {
-                    record_error(p.err, kErrProducerWait);
-                    *abort_flag = 1;
-                    break;
+            int64_t issued = 0;
+            int used[2] = {0, 0};  // query tiles loaded
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                Item it;
+                const int64_t index = static_cast<int64_t>(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                it.last = index > INT32_MAX || !find_item(p, pack, static_cast<int>(index), it);
+                if (k >= kItems) ok = __all_sync(0xffffffffu, idle_wait(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
+                if (!ok) break;
+                if (lane == 0) {
+                    volatile Item &dst = items[k % kItems];
+                    dst.start = it.start, dst.end = it.end, dst.tok0 = it.tok0, dst.head0 = it.head0;
+                    dst.tiles[0] = it.tiles[0], dst.tiles[1] = it.tiles[1], dst.last = it.last;
+                    mbar_arrive(item_full + 8 * (k % kItems));
                 }
-                mbar_arrive_expect_tx(full0 + 8 * s, Sh::kTile);
-                for (int h = 0; h < kHalves; ++h)
-                    tma_load_3d(ring_a + s * Sh::kTile + h * (128 * 128), i & 1 ? &map_v : &map_k, 64 * h, kv_head,
-                                item.start + (i >> 1) * kTileKeys, full0 + 8 * s);
-                ++issued;
-                if (++s == Sh::kStages) s = 0, ph ^= 1u;
+                if (it.last) break;
+                if (lane == 0) {
+                    const int kv_head = it.head0 / p.group, n = 2 * max(it.tiles[0], it.tiles[1]);
+                    for (int i = -2; ok && i < n; ++i) {
+                        if (i < 0) {  // query tile
+                            const int x = i + 2;
+                            if (it.tiles[x] == 0) continue;
+                            if (used[x] > 0) ok = idle_wait(q_empty + 8 * x, (used[x] - 1) & 1, abort_flag);
+                            if (!ok) break;
+                            ++used[x];
+                            mbar_arrive_expect_tx(q_full + 8 * x, Sh::kTile);
+                            for (int h = 0; h < kHalves; ++h)
+                                tma_load_3d(q_a + x * Sh::kTile + h * (128 * 128), &map_q, 64 * h, it.head0,
+                                            it.start + it.tok0 + x * tile_toks, q_full + 8 * x);
+                            continue;
+                        }
+                        if (issued >= Sh::kStages) ok = idle_wait(empty0 + 8 * stage, ph ^ 1u, abort_flag);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(full0 + 8 * stage, Sh::kTile);
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_3d(ring_a + stage * Sh::kTile + h * (128 * 128), i & 1 ? &map_v : &map_k, 64 * h, kv_head,
+                                        it.start + (i >> 1) * kTileKeys, full0 + 8 * stage);
+                        ++issued;
+                        if (++stage == Sh::kStages) stage = 0, ph ^= 1u;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            // leave no copy in flight into this block's shared memory
-            for (int k = issued > Sh::kStages ? issued - Sh::kStages : 0; k < issued; ++k)
-                if (!mbar_wait_bounded(full0 + 8 * (k % Sh::kStages), (k / Sh::kStages) & 1)) {
-                    record_error(p.err, kErrDrainWait);
-                    break;
-                }
-            if (!mbar_wait_bounded(bar_q, 0u)) record_error(p.err, kErrDrainWait);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- mma issuer
-        if (lane == 0) {
+            if (!ok && lane == 0) {
+                record_error(p.err, kErrProducerWait);
+                *abort_flag = 1;
+            }
+            if (lane == 0) {
+                // leave no copy in flight into this block's shared memory
+                bool landed = true;
+                for (int64_t i = issued > Sh::kStages ? issued - Sh::kStages : 0; i < issued; ++i)
+                    landed = landed && mbar_wait_bounded(full0 + 8 * static_cast<int>(i % Sh::kStages), (i / Sh::kStages) & 1);
+                for (int x = 0; x < 2; ++x)
+                    if (used[x] > 0) landed = landed && mbar_wait_bounded(q_full + 8 * x, (used[x] - 1) & 1);
+                if (!landed) record_error(p.err, kErrDrainWait);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------- mma issuer (the whole warp, one lane issues)
+            const uint32_t issue = lane == 0;
             const uint32_t id_s = tc_idesc_f16(128, kTileKeys), id_o = tc_idesc_f16(128, D) | kIdescNMajorB;
-            bool ok = tc_wait(bar_q, 0u, abort_flag);
-            auto wait_stage = [&](int i) {  // key tile j is ring entry 2 j, value tile j 2 j + 1
-                return tc_wait(full0 + 8 * (i % Sh::kStages), (i / Sh::kStages) & 1, abort_flag);
+            int entry = 0;             // the item's first ring entry: key tile j is entry + 2 j, value tile j the next
+            int n_p[2] = {0, 0};       // weight tiles consumed so far
+            int n_items[2] = {0, 0};   // items whose O has been started, by tile
+            int n_q[2] = {0, 0};       // query tiles used so far
+            auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, tc_wait(bar, parity & 1, abort_flag)) != 0; };
+            auto there = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1)) != 0; };
+            auto stage = [&](int e) { return ring_a + (e % Sh::kStages) * Sh::kTile; };
+            auto full = [&](int e) { return full0 + 8 * (e % Sh::kStages); };
+            // item k, published: its fields as values that are the same in every lane for the compiler, too
+            auto take_item = [&](int k) {
+                Item it = read_item(k);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(item_empty + 8 * (k % kItems));
+                it.tiles[0] = __shfl_sync(0xffffffffu, it.tiles[0], 0);
+                it.tiles[1] = __shfl_sync(0xffffffffu, it.tiles[1], 0);
+                it.last = __shfl_sync(0xffffffffu, it.last, 0);
+                return it;
             };
-            auto stage = [&](int i) { return ring_a + (i % Sh::kStages) * Sh::kTile; };
-            auto product_s = [&](int x, int j) {
-                const uint64_t a = tc_smem_desc(q_a + x * Sh::kTile, 1024), b = tc_smem_desc(stage(2 * j), 1024);
+            auto product_s = [&](int x, int e, bool final) {
+                const uint64_t a = tc_smem_desc(q_a + x * Sh::kTile, 1024), b = tc_smem_desc(stage(e), 1024);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = static_cast<uint64_t>((k >> 2) * (128 * 128 / 16) + (k & 3) * 2);
-                    mma_ss(tmem + 128 * x, a + off, b + off, id_s, k != 0);
+                    mma_ss(issue, tmem + 128 * x, a + off, b + off, id_s, k != 0);
                 }
-                tc_commit(s_full + 8 * x);
+                commit(issue, s_full + 8 * x);
+                if (final) commit(issue, q_empty + 8 * x);
             };
-            if (ok) ok = wait_stage(0);
-            tc_fence_after();
-            if (ok)
-                for (int x = 0; x < 2; ++x)
-                    if (item.tiles[x] > 0) product_s(x, 0);
-            if (ok) tc_commit(empty0);
-            for (int j = 0; ok && j < n_tiles; ++j) {
-                ok = wait_stage(2 * j + 1);
-                if (ok && j + 1 < n_tiles) ok = wait_stage(2 * j + 2);
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if (j >= item.tiles[x]) continue;
-                    ok = tc_wait(p_ready + 8 * x, j & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t v = desc_n_major(stage(2 * j + 1), 128 * 128);
+            bool ok = wait(item_full, 0);
+            Item item = {};
+            if (ok) item = take_item(0);
+            bool started = false;  // S of the item's first key tile issued early for tile A
+            for (int k = 0; ok && !item.last; ++k) {
+                const int n = max(item.tiles[0], item.tiles[1]);
 #pragma unroll
-                    for (int k = 0; k < kTileKeys / 16; ++k)
-                        mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, v + static_cast<uint64_t>(k * (2048 / 16)), id_o,
-                               (j | k) != 0);
-                    if (j + 1 < item.tiles[x]) product_s(x, j + 1);
-                    else tc_commit(o_full + 8 * x);
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || item.tiles[x] == 0 || (x == 0 && started)) continue;
+                    ok = wait(q_full + 8 * x, n_q[x]) && wait(full(entry), entry / Sh::kStages);
+                    ++n_q[x];
+                    tc_fence_after();
+                    if (ok) product_s(x, entry, item.tiles[x] == 1);
                 }
                 if (!ok) break;
-                tc_commit(empty0 + 8 * ((2 * j + 1) % Sh::kStages));
-                if (j + 1 < n_tiles) tc_commit(empty0 + 8 * ((2 * j + 2) % Sh::kStages));
+                commit(issue, empty0 + 8 * (entry % Sh::kStages));
+                Item next = {};
+                bool known = false;
+                started = false;
+                for (int j = 0; ok && j < n; ++j) {
+                    const int ev = entry + 2 * j + 1, ek = ev + 1;
+                    ok = wait(full(ev), ev / Sh::kStages) && (j + 1 >= n || wait(full(ek), ek / Sh::kStages));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (!ok) continue;
+                        if (j < item.tiles[x]) {
+                            ok = wait(p_ready + 8 * x, n_p[x]);
+                            ++n_p[x];
+                            if (ok && j == 0) {
+                                if (n_items[x] > 0) ok = wait(o_empty + 8 * x, n_items[x] - 1);
+                                ++n_items[x];
+                            }
+                            if (!ok) continue;
+                            tc_fence_after();
+                            const uint64_t v = desc_n_major(stage(ev), 128 * 128);
+#pragma unroll
+                            for (int i = 0; i < kTileKeys / 16; ++i)
+                                mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 8 * i, v + static_cast<uint64_t>(i * (2048 / 16)),
+                                       id_o, i != 0 || j != 0);
+                            if (j + 1 < item.tiles[x]) product_s(x, ek, j + 2 == item.tiles[x]);
+                            else commit(issue, o_full + 8 * x);
+                        }
+                        if (x == 0 && j + 1 == n) {
+                            // tile A is done: its next item's first S, if the operands are there, before B's last product
+                            const int en = entry + 2 * n;
+                            if (there(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems)) {
+                                next = take_item(k + 1);
+                                known = true;
+                            }
+                            if (known && !next.last && next.tiles[0] > 0 && there(q_full, n_q[0]) && there(full(en), en / Sh::kStages)) {
+                                tc_fence_after();
+                                ++n_q[0];
+                                product_s(0, en, next.tiles[0] == 1);
+                                started = true;
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    commit(issue, empty0 + 8 * (ev % Sh::kStages));
+                    if (j + 1 < n) commit(issue, empty0 + 8 * (ek % Sh::kStages));
+                }
+                if (!ok) break;
+                entry += 2 * n;
+                if (!known) {
+                    ok = wait(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems);
+                    if (!ok) break;
+                    next = take_item(k + 1);
+                }
+                item = next;
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 record_error(p.err, kErrConsumerWait);
                 *abort_flag = 1;
             }
-            tc_commit(mfinal);  // every mma complete before tensor memory is freed
-            if (!mbar_wait_bounded(mfinal, 0u)) record_error(p.err, kErrDrainWait);
+            commit(issue, mfinal);  // every mma complete before tensor memory is freed
+            if (!mbar_wait_bounded(mfinal, 0u) && lane == 0) record_error(p.err, kErrDrainWait);
+            __syncwarp();
         }
-        __syncwarp();
-    } else {
+    } else if (warp < 12) {
         // ---------------- softmax of one tile: thread = row = tensor-memory lane 32 (warp % 4) + lane
-        const int x = (warp - 2) >> 2, row = 32 * (warp & 3) + lane;
+        more_registers<192>();
+        const int x = (warp - 4) >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t s_t = tmem + lanes + 128 * x, o_t = tmem + lanes + 256 + 128 * x;
-        const int tok = item.tok0 + x * tile_toks + row / pack;  // within the sequence
-        const int first_tok = item.tok0 + x * tile_toks;
         const float c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-37f);  // not 0, which times -inf would be NaN
         const bool negate = p.scale < 0.0f;
-        float ref = -INFINITY;
-        float2 sum = make_float2(0.0f, 0.0f);
+        int n_s = 0, n_items = 0;  // tiles, items of this tile so far
         bool ok = true;
-        for (int j = 0; j < item.tiles[x]; ++j) {
-            ok = __all_sync(0xffffffffu, tc_wait(s_full + 8 * x, j & 1, abort_flag));
+        for (int k = 0; ok; ++k) {
+            ok = __all_sync(0xffffffffu, wait_item(k));
             if (!ok) break;
-            tc_fence_after();
-            uint32_t v[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tm_ld32(s_t + 32 * i, v[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tm_wait_ld(v[i]);
-            if (negate)
-#pragma unroll
-                for (int i = 0; i < 128; ++i) v[i >> 5][i & 31] ^= 0x80000000u;
-            const int key0 = j * kTileKeys;
-            if (key0 + kTileKeys - 1 > first_tok) {  // some row does not see every key
-                const int see = tok - key0;          // columns 0 .. see
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i > see) v[i >> 5][i & 31] = 0xFF800000u;
-            }
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mx[i] = __uint_as_float(v[i][0]);
-#pragma unroll
-                for (int k = 1; k < 31; k += 2) mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(v[i][k])), __uint_as_float(v[i][k + 1]));
-                mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            if (j == 0) {
-                ref = top;
-            } else if (__any_sync(0xffffffffu, top > ref + kGrow)) {
-                // S of this tile is complete, so P V of the tiles before is, too
-                const float next = fmaxf(ref, top), keep = exp2_approx(ref - next);
-                ref = next;
-                sum.x *= keep, sum.y *= keep;
-#pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                    uint32_t o[32];
-                    tm_ld32(o_t + i, o);
-                    tm_wait_ld(o);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-                    tc_st32(o_t + i, o);
-                }
-            }
-            const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
-            float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                uint32_t w[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    float2 e = ffma2(make_float2(__uint_as_float(v[i + (k >> 4)][2 * (k & 15)]),
-                                                 __uint_as_float(v[i + (k >> 4)][2 * (k & 15) + 1])), c2, r2);
-                    e.x = exp2_approx(e.x), e.y = exp2_approx(e.y);
-                    part[k & 1] = fadd2(part[k & 1], e);
-                    w[k] = pack_half2(e.x, e.y);
-                }
-                tc_st32(s_t + 16 * i, w);
-            }
-            sum = fadd2(sum, fadd2(part[0], part[1]));
-            tc_wait_st();
-            tc_fence_before();
+            const Item item = read_item(k);
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_ready + 8 * x);
-        }
-        // ---- the rows' results
-        if (ok && item.tiles[x] > 0) {
-            ok = __all_sync(0xffffffffu, tc_wait(o_full + 8 * x, 0u, abort_flag));
-            if (ok) {
+            if (lane == 0) mbar_arrive(item_empty + 8 * (k % kItems));
+            if (item.last) break;
+            const int first_tok = item.tok0 + x * tile_toks, tok = first_tok + row / pack;  // within the sequence
+            const int n = x == 0 ? item.tiles[0] : item.tiles[1];
+            if (n == 0) continue;
+            float ref = -INFINITY;
+            float2 sum = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < n; ++j, ++n_s) {
+                ok = __all_sync(0xffffffffu, tc_wait(s_full + 8 * x, n_s & 1, abort_flag));
+                if (!ok) break;
                 tc_fence_after();
-                const float inv = 1.0f / (sum.x + sum.y);
+                uint32_t v[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tm_ld32(s_t + 32 * i, v[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tm_wait_ld(v[i]);
+                if (negate)
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) v[i >> 5][i & 31] ^= 0x80000000u;
+                const int key0 = j * kTileKeys;
+                if (key0 + kTileKeys - 1 > first_tok) {  // some row does not see every key
+                    const int see = tok - key0;          // columns 0 .. see
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i > see) v[i >> 5][i & 31] = 0xFF800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mx[i] = __uint_as_float(v[i][0]);
+#pragma unroll
+                    for (int q = 1; q < 31; q += 2) mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(v[i][q])), __uint_as_float(v[i][q + 1]));
+                    mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                if (j == 0) {
+                    ref = top;
+                } else if (__any_sync(0xffffffffu, top > ref + kGrow)) {
+                    // S of this tile is complete, so P V of the tiles before is, too
+                    const float next = fmaxf(ref, top), keep = exp2_approx(ref - next);
+                    ref = next;
+                    sum.x *= keep, sum.y *= keep;
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 32) {
+                        uint32_t o[32];
+                        tm_ld32(o_t + i, o);
+                        tm_wait_ld(o);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * keep);
+                        tc_st32(o_t + i, o);
+                    }
+                }
+                const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        float2 e = ffma2(make_float2(__uint_as_float(v[i + (q >> 4)][2 * (q & 15)]),
+                                                     __uint_as_float(v[i + (q >> 4)][2 * (q & 15) + 1])), c2, r2);
+                        e.x = exp2_approx(e.x), e.y = exp2_approx(e.y);
+                        part[q & 1] = fadd2(part[q & 1], e);
+                        w[q] = pack_half2(e.x, e.y);
+                    }
+                    tc_st32(s_t + 16 * i, w);
+                }
+                sum = fadd2(sum, fadd2(part[0], part[1]));
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * x);
+            }
+            if (!ok) break;
+            // read by the storing warps before this tile's item after next comes here
+            sums[((n_items & 1) * 2 + x) * 128 + row] = sum.x + sum.y;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(l_full + 8 * x);
+            ++n_items;
+        }
+        if (!ok) {
+            if (lane == 0) record_error(p.err, kErrConsumerWait);
+            *abort_flag = 1;
+        }
+    } else {
+        // ---------------- results: O over the rows' sums
+        fewer_registers<64>();
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        int n_items[2] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            ok = __all_sync(0xffffffffu, wait_item(k));
+            if (!ok) break;
+            const Item item = read_item(k);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_empty + 8 * (k % kItems));
+            if (item.last) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!ok || item.tiles[x] == 0) continue;
+                const int parity = n_items[x]++ & 1;
+                ok = __all_sync(0xffffffffu, idle_wait(l_full + 8 * x, parity, abort_flag) && idle_wait(o_full + 8 * x, parity, abort_flag));
+                if (!ok) continue;
+                tc_fence_after();
+                const float inv = 1.0f / sums[(parity * 2 + x) * 128 + row];
+                const int tok = item.tok0 + x * tile_toks + row / pack, head = item.head0 + row % pack;
                 const bool live = item.start + tok < item.end;
-                const int head = item.head0 + row % pack;
                 TO *out = static_cast<TO *>(p.out) + (static_cast<int64_t>(item.start + tok) * p.n_heads + head) * D;
                 float check = 0.0f;  // 0 times every value: NaN if one is not finite
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
-                    tm_ld32(o_t + i, o);
+                    tm_ld32(tmem + lanes + 256 + 128 * x + i, o);
                     tm_wait_ld(o);
+                    if (i + 32 == D) {  // all of O has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_empty + 8 * x);
+                    }
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        float y[8];
+                    for (int q = 0; q < 32; q += 16) {
+                        float y[16];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            y[q] = __uint_as_float(o[k + q]) * inv;
-                            check = fmaf(y[q], 0.0f, check);
+                        for (int e = 0; e < 16; ++e) {
+                            y[e] = __uint_as_float(o[q + e]) * inv;
+                            check = fmaf(y[e], 0.0f, check);
                         }
-                        if (live) store8(out + i + k, y);
+                        if (live) store16(out + i + q, y);
                     }
                 }
                 uint32_t bad = __ballot_sync(0xffffffffu, live && check != 0.0f);
@@ -517,7 +697,7 @@ bool encode_rows(CUtensorMap *tm, const void *base, int64_t n_tok, int heads, in
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, class TO> cudaError_t launch(const PromptParams &p, int device, cudaStream_t s) {
+template <int D, class TO> cudaError_t launch(const PromptParams &p, int sms, int device, cudaStream_t s) {
     // heads that share a tile: the largest power of two that divides the group
     int pack = p.group & -p.group;
     if (pack > kTileRows) pack = kTileRows;
@@ -540,14 +720,14 @@ template <int D, class TO> cudaError_t launch(const PromptParams &p, int device,
     const int toks = 2 * kTileRows / pack;
     const int64_t items = (static_cast<int64_t>(p.n_tok) / toks + p.n_seq) * (p.n_heads / pack);
     if (items > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(prompt_attend_kernel<D, TO>, static_cast<int>(items), kThreads, Shape<D>::kSmem, s, mq, mk, mv, p, pack);
+    return launch_pdl(prompt_attend_kernel<D, TO>, static_cast<int>(items < sms ? items : sms), kThreads, Shape<D>::kSmem, s, mq, mk, mv, p, pack);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attend(const PromptParams &p, int head_dim, int out_type, int, int device, cudaStream_t s) {
-    if (head_dim == 64) return out_type == QG_F32 ? launch<64, float>(p, device, s) : launch<64, __half>(p, device, s);
-    return out_type == QG_F32 ? launch<128, float>(p, device, s) : launch<128, __half>(p, device, s);
+cudaError_t launch_prompt_attend(const PromptParams &p, int head_dim, int out_type, int sms, int device, cudaStream_t s) {
+    if (head_dim == 64) return out_type == QG_F32 ? launch<64, float>(p, sms, device, s) : launch<64, __half>(p, sms, device, s);
+    return out_type == QG_F32 ? launch<128, float>(p, sms, device, s) : launch<128, __half>(p, sms, device, s);
 }
 
 }  // namespace qg
