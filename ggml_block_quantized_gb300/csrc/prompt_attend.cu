@@ -8,14 +8,14 @@
 // multiprocessor takes items in turn (of falling length, in snake order, so
 // that the blocks' sums are alike), and every role runs on into the next item
 // as soon as its own operands allow:
-//  * warp 0: finds the items and publishes them; lane 0 is the TMA producer:
-//    query tiles, then key and value tiles in turn into a ring (128-byte
-//    swizzle, 64 channels a box).
+//  * warp 2: finds the items and publishes them, up to four ahead.
+//  * warp 0, lane 0: TMA producer: query tiles, and key and value tiles in turn
+//    into a ring (128-byte swizzle, 64 channels a box).
 //  * warp 1, lane 0: issues tcgen05.mma. S = Q K^T into 128 tensor-memory
 //    columns a tile, O += P V with P read from tensor memory (f16, over S's
 //    columns) and V as it lies in memory (N-major operand). The order
 //    PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) keeps the tensor cores on one tile while
-//    the other one's softmax runs.
+//    the other one's softmax runs; P V starts on the first half of P.
 //  * warps 4..7 and 8..11: softmax of tile A and B, a row a thread: S from
 //    tensor memory, running maximum, exp2, P back in f16. O is rescaled in
 //    place only when a row's maximum has grown by more than 2^8 over the one
@@ -23,9 +23,14 @@
 //  * warps 12..15: divide O by the rows' sums and store, while the others are
 //    in the next item.
 // The softmax warps take the registers that the other two warpgroups give up.
-// Only tiles on the diagonal are masked. The product P V takes 0 times every
-// unseen value, which is NaN for a value that is not finite: a row whose
-// result is not finite is computed again, over its own rows alone, by one warp.
+//  * warp 3: looks through the value tiles on the diagonal, on warp 1's demand
+//    and while the softmax of the tile runs. The product P V
+//    takes 0 times every value that a row does not see, which is NaN for a
+//    value that is not finite; such values are set to 0 in shared memory
+//    before the product, and the storing warps add them to the rows that do
+//    see them (a weight above 0 times an infinity or NaN is that value).
+// Only tiles on the diagonal are masked; they also hold whatever follows the
+// sequence's end.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -47,7 +52,7 @@ template <int D> struct Shape {
     static constexpr int kTile = 128 * D * 2;  // bytes of a query, key or value tile
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kTiles = (2 + kStages) * kTile;
-    static constexpr int kSmem = kTiles + 2560;  // tiles, then barriers, items and sums
+    static constexpr int kSmem = kTiles + 2752;  // tiles, then barriers, items and sums
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
@@ -76,6 +81,25 @@ __device__ __forceinline__ void commit(uint32_t issue, uint32_t bar) {
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(issue)
         : "memory");
 }
+__device__ __forceinline__ void arrive_if(uint32_t issue, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(issue)
+                 : "memory");
+}
+__device__ __forceinline__ void store_if(uint32_t issue, uint32_t a, int x, int y) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q st.shared.v2.b32 [%0], {%1, %2};\n\t}" ::"r"(a), "r"(x),
+                 "r"(y), "r"(issue)
+                 : "memory");
+}
+// tc_wait of a whole warp that goes on in either case: a wait that gives up
+// sets the abort flag, with which all others of the block give up soon.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *err) {
+    if (!__all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag))) {
+        record_error(err, kErrConsumerWait);
+        *abort_flag = 1;
+    }
+}
+
 // Shared-memory descriptor of a 128-byte-swizzled N-major operand (64-element
 // rows of N, one row a k): the stride between 64-element parts of N, and
 // between groups of 8 k (one atom, 1024 bytes).
@@ -116,18 +140,6 @@ __device__ __forceinline__ void tm_wait_ld(uint32_t (&v)[32]) {
                    "+r"(v[30]), "+r"(v[31])
                  :
                  : "memory");
-}
-
-// tc_wait for waits that are usually long: suspended between polls, so that it
-// takes no issue slots from the softmax warps.
-__device__ __forceinline__ bool idle_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1; i < kWaitLimitPolls; ++i) {
-        if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
-        if ((i & 15u) == 0 && (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs)) return false;
-    }
-    return false;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -235,40 +247,9 @@ __device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// One query row over the rows it sees, by one warp, in f32.
-template <int D, class TO>
-__device__ __noinline__ void attend_row(const PromptParams &p, int start, int row, int head) {
-    constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31, hk = head / p.group;
-    const __half *q = static_cast<const __half *>(p.q) + row * p.q_stride + head * D;
-    const __half *kb = static_cast<const __half *>(p.k) + hk * D, *vb = static_cast<const __half *>(p.v) + hk * D;
-    float m = -INFINITY, l = 0.0f, o[kPer] = {};
-    for (int t0 = start; t0 <= row; t0 += 32) {
-        const int t = t0 + lane;
-        float sc = -INFINITY;
-        if (t <= row) {
-            sc = 0.0f;
-            for (int i = 0; i < D; ++i) sc += __half2float(q[i]) * __half2float(kb[t * p.k_stride + i]);
-            sc *= p.scale;
-        }
-        float mt = sc;
-        for (int k = 16; k; k >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, k));
-        const float mn = fmaxf(m, mt);
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        const float keep = expf(m - base);
-        const float w = t <= row ? expf(sc - base) : 0.0f;
-        m = mn;
-        l = l * keep + w;
-        for (int k = 0; k < kPer; ++k) o[k] *= keep;
-        for (int j = 0; j < 32 && t0 + j <= row; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            for (int k = 0; k < kPer; ++k) o[k] += wj * __half2float(vb[(t0 + j) * p.v_stride + 32 * k + lane]);
-        }
-    }
-    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-    TO *out = static_cast<TO *>(p.out) + (static_cast<int64_t>(row) * p.n_heads + head) * D;
-    for (int k = 0; k < kPer; ++k) out[32 * k + lane] = static_cast<TO>(o[k] / l);
-}
+// Not 0 where one of a word's two f16 is not finite (an exponent field of
+// ones, to which one more carries into the sign's place).
+__device__ __forceinline__ uint32_t odd_half2(uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
 
 template <int D, class TO>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -283,10 +264,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t full0 = base_a, empty0 = full0 + 8 * Sh::kStages, q_full = empty0 + 8 * Sh::kStages, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, p_ready = s_full + 16, o_full = p_ready + 16, o_empty = o_full + 16;
     const uint32_t l_full = o_empty + 16, item_full = l_full + 16, item_empty = item_full + 8 * kItems, mfinal = item_empty + 8 * kItems;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + 384);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(base + 388);
-    volatile Item *items = reinterpret_cast<volatile Item *>(base + 392);
-    volatile float *sums = reinterpret_cast<volatile float *>(base + 512);  // [item parity][tile][row]
+    const uint32_t p_half = mfinal + 8, v_ask = p_half + 16, v_clean = v_ask + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + 448);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(base + 452);
+    volatile Item *items = reinterpret_cast<volatile Item *>(base + 456);
+    volatile int *asked = reinterpret_cast<volatile int *>(base + 576);     // v_ask's stage (-1: the end) and item
+    volatile int *odd = reinterpret_cast<volatile int *>(base + 584);       // [item % 8][2]: diagonal values that are not finite
+    volatile float *sums = reinterpret_cast<volatile float *>(base + 704);  // [item parity][tile][row]
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -298,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(q_full + 8 * x, 1);
             mbar_init(q_empty + 8 * x, 1);
             mbar_init(s_full + 8 * x, 1);
+            mbar_init(p_half + 8 * x, 4);
             mbar_init(p_ready + 8 * x, 4);
             mbar_init(o_full + 8 * x, 1);
             mbar_init(o_empty + 8 * x, 4);
@@ -305,9 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full + 8 * i, 1);
-            mbar_init(item_empty + 8 * i, 13);  // the mma issuer and twelve warps
+            mbar_init(item_empty + 8 * i, 14);  // the copies, the mma issuer and twelve warps
         }
         mbar_init(mfinal, 1);
+        mbar_init(v_ask, 1);
+        mbar_init(v_clean, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -323,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait_prior_grids();
     pdl_allow_dependents();
     // item k of the block as a consumer: all lanes of the warp (or one thread) call it
-    auto wait_item = [&](int k) { return idle_wait(item_full + 8 * (k % kItems), (k / kItems) & 1, abort_flag); };
+    auto wait_item = [&](int k) { return tc_wait(item_full + 8 * (k % kItems), (k / kItems) & 1, abort_flag); };
     auto read_item = [&](int k) {
         const volatile Item &s = items[k % kItems];
         Item it;
@@ -331,45 +318,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.tiles[0] = s.tiles[0], it.tiles[1] = s.tiles[1], it.last = s.last;
         return it;
     };
+    // first key tile that some row of the item does not see in full
+    auto first_masked = [&](const Item &it) { return (it.tok0 + 1) / kTileKeys; };
 
     if (warp < 4) {
         fewer_registers<64>();
         if (warp == 0) {
-            // ---------------- items and copies
+            // ---------------- copies
             int stage = 0;
             uint32_t ph = 0;
             int64_t issued = 0;
             int used[2] = {0, 0};  // query tiles loaded
             bool ok = true;
             for (int k = 0; ok; ++k) {
-                Item it;
-                const int64_t index = static_cast<int64_t>(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                it.last = index > INT32_MAX || !find_item(p, pack, static_cast<int>(index), it);
-                if (k >= kItems) ok = __all_sync(0xffffffffu, idle_wait(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_item(k));
                 if (!ok) break;
-                if (lane == 0) {
-                    volatile Item &dst = items[k % kItems];
-                    dst.start = it.start, dst.end = it.end, dst.tok0 = it.tok0, dst.head0 = it.head0;
-                    dst.tiles[0] = it.tiles[0], dst.tiles[1] = it.tiles[1], dst.last = it.last;
-                    mbar_arrive(item_full + 8 * (k % kItems));
-                }
+                const Item it = read_item(k);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(item_empty + 8 * (k % kItems));
                 if (it.last) break;
                 if (lane == 0) {
                     const int kv_head = it.head0 / p.group, n = 2 * max(it.tiles[0], it.tiles[1]);
-                    for (int i = -2; ok && i < n; ++i) {
-                        if (i < 0) {  // query tile
-                            const int x = i + 2;
-                            if (it.tiles[x] == 0) continue;
-                            if (used[x] > 0) ok = idle_wait(q_empty + 8 * x, (used[x] - 1) & 1, abort_flag);
-                            if (!ok) break;
-                            ++used[x];
-                            mbar_arrive_expect_tx(q_full + 8 * x, Sh::kTile);
-                            for (int h = 0; h < kHalves; ++h)
-                                tma_load_3d(q_a + x * Sh::kTile + h * (128 * 128), &map_q, 64 * h, it.head0,
-                                            it.start + it.tok0 + x * tile_toks, q_full + 8 * x);
-                            continue;
-                        }
-                        if (issued >= Sh::kStages) ok = idle_wait(empty0 + 8 * stage, ph ^ 1u, abort_flag);
+                    for (int i = 0; ok && i < n; ++i) {
+                        if (issued >= Sh::kStages) ok = tc_wait(empty0 + 8 * stage, ph ^ 1u, abort_flag);
                         if (!ok) break;
                         mbar_arrive_expect_tx(full0 + 8 * stage, Sh::kTile);
                         for (int h = 0; h < kHalves; ++h)
@@ -377,6 +348,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         it.start + (i >> 1) * kTileKeys, full0 + 8 * stage);
                         ++issued;
                         if (++stage == Sh::kStages) stage = 0, ph ^= 1u;
+                        if (i > 0) continue;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {  // the queries, once the last item's are used up
+                            if (!ok || it.tiles[x] == 0) continue;
+                            if (used[x] > 0) ok = tc_wait(q_empty + 8 * x, (used[x] - 1) & 1, abort_flag);
+                            if (!ok) continue;
+                            ++used[x];
+                            mbar_arrive_expect_tx(q_full + 8 * x, Sh::kTile);
+                            for (int h = 0; h < kHalves; ++h)
+                                tma_load_3d(q_a + x * Sh::kTile + h * (128 * 128), &map_q, 64 * h, it.head0,
+                                            it.start + it.tok0 + x * tile_toks, q_full + 8 * x);
+                        }
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -395,114 +378,182 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!landed) record_error(p.err, kErrDrainWait);
             }
             __syncwarp();
+        } else if (warp == 2) {
+            // ---------------- items
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                Item it;
+                const int64_t index = static_cast<int64_t>(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                it.last = index > INT32_MAX || !find_item(p, pack, static_cast<int>(index), it);
+                if (k >= kItems) ok = __all_sync(0xffffffffu, tc_wait(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
+                if (!ok) break;
+                if (lane == 0) {
+                    volatile Item &dst = items[k % kItems];
+                    dst.start = it.start, dst.end = it.end, dst.tok0 = it.tok0, dst.head0 = it.head0;
+                    dst.tiles[0] = it.tiles[0], dst.tiles[1] = it.tiles[1], dst.last = it.last;
+                    mbar_arrive(item_full + 8 * (k % kItems));
+                }
+                __syncwarp();
+                if (it.last) break;
+            }
+        } else if (warp == 3) {
+            // ---------------- value tiles on the diagonal
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                ok = __all_sync(0xffffffffu, tc_wait(v_ask, i & 1, abort_flag));
+                const int st = asked[0], k = asked[1];
+                __syncwarp();
+                if (!ok || st < 0) break;
+                uint4 *tile = reinterpret_cast<uint4 *>(smem_raw + 2 * Sh::kTile + st * Sh::kTile);
+                uint32_t found = 0;
+#pragma unroll 8
+                for (int q = lane; q < Sh::kTile / 16; q += 32) {
+                    const uint4 w = tile[q];
+                    found |= odd_half2(w.x) | odd_half2(w.y) | odd_half2(w.z) | odd_half2(w.w);
+                }
+                if (__any_sync(0xffffffffu, found != 0)) {
+                    __half *h = reinterpret_cast<__half *>(tile);
+                    for (int q = lane; q < Sh::kTile / 2; q += 32)
+                        if ((__half_as_ushort(h[q]) & 0x7C00u) == 0x7C00u) h[q] = __ushort_as_half(0);
+                    fence_proxy_async_smem();
+                    if (lane == 0) odd[2 * (k % 8)] = 1;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_clean);
+            }
+            __syncwarp();
         } else if (warp == 1) {
-            // ---------------- mma issuer (the whole warp, one lane issues)
+            // ---------------- mma issuer (the whole warp, one lane issues). The steps are straight-line code
+            // but for branches that are alike in all lanes; what a failed wait leaves is not used.
             const uint32_t issue = lane == 0;
-            const uint32_t id_s = tc_idesc_f16(128, kTileKeys), id_o = tc_idesc_f16(128, D) | kIdescNMajorB;
-            int entry = 0;             // the item's first ring entry: key tile j is entry + 2 j, value tile j the next
-            int n_p[2] = {0, 0};       // weight tiles consumed so far
-            int n_items[2] = {0, 0};   // items whose O has been started, by tile
-            int n_q[2] = {0, 0};       // query tiles used so far
-            auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, tc_wait(bar, parity & 1, abort_flag)) != 0; };
-            auto there = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1)) != 0; };
-            auto stage = [&](int e) { return ring_a + (e % Sh::kStages) * Sh::kTile; };
-            auto full = [&](int e) { return full0 + 8 * (e % Sh::kStages); };
+            constexpr uint32_t kIdS = tc_idesc_f16(128, kTileKeys), kIdO = tc_idesc_f16(128, D) | kIdescNMajorB;
+            const uint64_t q_desc = tc_smem_desc(q_a, 1024), k_desc = tc_smem_desc(ring_a, 1024), v_desc = desc_n_major(ring_a, 128 * 128);
+            constexpr uint64_t kStep = Sh::kTile / 16;  // from tile to tile in a descriptor
+            struct Ring {  // place of a key or value tile
+                uint32_t s, ph;
+                __device__ __forceinline__ Ring next() const {
+                    const uint32_t t = s + 1 == Sh::kStages ? 0u : s + 1;
+                    return Ring{t, t == 0u ? ph ^ 1u : ph};
+                }
+            };
+            uint32_t n_p[2] = {0, 0};      // weight tiles consumed so far
+            uint32_t n_o[2] = {0, 0};      // items whose O has been started, by tile
+            uint32_t n_q[2] = {0, 0};      // query tiles used so far
+            uint32_t n_clean = 0;          // value tiles looked through
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u))) wait_slow(bar, parity & 1u, abort_flag, p.err);
+            };
+            auto there = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)) != 0; };
             // item k, published: its fields as values that are the same in every lane for the compiler, too
             auto take_item = [&](int k) {
                 Item it = read_item(k);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(item_empty + 8 * (k % kItems));
+                arrive_if(issue, item_empty + 8 * (k % kItems));
                 it.tiles[0] = __shfl_sync(0xffffffffu, it.tiles[0], 0);
                 it.tiles[1] = __shfl_sync(0xffffffffu, it.tiles[1], 0);
-                it.last = __shfl_sync(0xffffffffu, it.last, 0);
+                it.last = __shfl_sync(0xffffffffu, it.last | *abort_flag, 0);
+                it.tok0 = __shfl_sync(0xffffffffu, it.tok0, 0);
                 return it;
             };
-            auto product_s = [&](int x, int e, bool final) {
-                const uint64_t a = tc_smem_desc(q_a + x * Sh::kTile, 1024), b = tc_smem_desc(stage(e), 1024);
+            auto product_s = [&](int x, const Ring &r, bool final) {
+                const uint64_t a = q_desc + x * kStep, b = k_desc + r.s * kStep;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = static_cast<uint64_t>((k >> 2) * (128 * 128 / 16) + (k & 3) * 2);
-                    mma_ss(issue, tmem + 128 * x, a + off, b + off, id_s, k != 0);
+                    mma_ss(issue, tmem + 128 * x, a + off, b + off, kIdS, k != 0);
                 }
                 commit(issue, s_full + 8 * x);
                 if (final) commit(issue, q_empty + 8 * x);
             };
-            bool ok = wait(item_full, 0);
-            Item item = {};
-            if (ok) item = take_item(0);
+            auto ask = [&](const Ring &r, int k) {
+                store_if(issue, smem_addr(const_cast<int *>(asked)), static_cast<int>(r.s), k);
+                arrive_if(issue, v_ask);
+            };
+            Ring r = {0, 0};  // the item's first key tile, then the last one used
+            wait(item_full, 0);
+            Item item = take_item(0);
             bool started = false;  // S of the item's first key tile issued early for tile A
-            for (int k = 0; ok && !item.last; ++k) {
-                const int n = max(item.tiles[0], item.tiles[1]);
+            for (int k = 0; !item.last; ++k) {
+                const int n = max(item.tiles[0], item.tiles[1]), masked = first_masked(item);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (!ok || item.tiles[x] == 0 || (x == 0 && started)) continue;
-                    ok = wait(q_full + 8 * x, n_q[x]) && wait(full(entry), entry / Sh::kStages);
-                    ++n_q[x];
+                    if (item.tiles[x] == 0 || (x == 0 && started)) continue;
+                    wait(q_full + 8 * x, n_q[x]++);
+                    wait(full0 + 8 * r.s, r.ph);
                     tc_fence_after();
-                    if (ok) product_s(x, entry, item.tiles[x] == 1);
+                    product_s(x, r, item.tiles[x] == 1);
                 }
-                if (!ok) break;
-                commit(issue, empty0 + 8 * (entry % Sh::kStages));
+                commit(issue, empty0 + 8 * r.s);
+                store_if(issue, smem_addr(const_cast<int *>(odd + 2 * (k % 8))), 0, 0);  // (the storing warps are less than eight items behind)
                 Item next = {};
                 bool known = false;
                 started = false;
-                for (int j = 0; ok && j < n; ++j) {
-                    const int ev = entry + 2 * j + 1, ek = ev + 1;
-                    ok = wait(full(ev), ev / Sh::kStages) && (j + 1 >= n || wait(full(ek), ek / Sh::kStages));
+                bool asked_next = false;  // the next value tile, where masked
+                for (int j = 0; j < n; ++j) {
+                    const Ring rv = r.next(), rk = rv.next();
+                    const bool more = j + 1 < n;
+                    wait(full0 + 8 * rv.s, rv.ph);
+                    if (more) wait(full0 + 8 * rk.s, rk.ph);
+                    if (j >= masked) {
+                        if (!asked_next) ask(rv, k);
+                        wait(v_clean, n_clean++);
+                        asked_next = false;
+                    }
+                    if (more && j + 1 >= masked) {
+                        const Ring rn = rk.next();
+                        if (there(full0 + 8 * rn.s, rn.ph)) {
+                            ask(rn, k);
+                            asked_next = true;
+                        }
+                    }
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (!ok) continue;
                         if (j < item.tiles[x]) {
-                            ok = wait(p_ready + 8 * x, n_p[x]);
-                            ++n_p[x];
-                            if (ok && j == 0) {
-                                if (n_items[x] > 0) ok = wait(o_empty + 8 * x, n_items[x] - 1);
-                                ++n_items[x];
+                            if (j == 0) {
+                                if (n_o[x] > 0) wait(o_empty + 8 * x, n_o[x] - 1);
+                                ++n_o[x];
                             }
-                            if (!ok) continue;
-                            tc_fence_after();
-                            const uint64_t v = desc_n_major(stage(ev), 128 * 128);
+                            const uint64_t v = v_desc + rv.s * kStep;
 #pragma unroll
-                            for (int i = 0; i < kTileKeys / 16; ++i)
-                                mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 8 * i, v + static_cast<uint64_t>(i * (2048 / 16)),
-                                       id_o, i != 0 || j != 0);
-                            if (j + 1 < item.tiles[x]) product_s(x, ek, j + 2 == item.tiles[x]);
+                            for (int h = 0; h < 2; ++h) {
+                                wait((h == 0 ? p_half : p_ready) + 8 * x, n_p[x]);
+                                tc_fence_after();
+#pragma unroll
+                                for (int i = 4 * h; i < 4 * h + 4; ++i)
+                                    mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 8 * i, v + static_cast<uint64_t>(i * (2048 / 16)),
+                                           kIdO, i != 0 ? 1u : static_cast<uint32_t>(j));
+                            }
+                            ++n_p[x];
+                            if (j + 1 < item.tiles[x]) product_s(x, rk, j + 2 == item.tiles[x]);
                             else commit(issue, o_full + 8 * x);
                         }
-                        if (x == 0 && j + 1 == n) {
+                        if (x == 0 && !more) {
                             // tile A is done: its next item's first S, if the operands are there, before B's last product
-                            const int en = entry + 2 * n;
                             if (there(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems)) {
                                 next = take_item(k + 1);
                                 known = true;
-                            }
-                            if (known && !next.last && next.tiles[0] > 0 && there(q_full, n_q[0]) && there(full(en), en / Sh::kStages)) {
-                                tc_fence_after();
-                                ++n_q[0];
-                                product_s(0, en, next.tiles[0] == 1);
-                                started = true;
+                                if (!next.last && next.tiles[0] > 0 && there(q_full, n_q[0]) && there(full0 + 8 * rk.s, rk.ph)) {
+                                    tc_fence_after();
+                                    ++n_q[0];
+                                    product_s(0, rk, next.tiles[0] == 1);
+                                    started = true;
+                                }
                             }
                         }
                     }
-                    if (!ok) break;
-                    commit(issue, empty0 + 8 * (ev % Sh::kStages));
-                    if (j + 1 < n) commit(issue, empty0 + 8 * (ek % Sh::kStages));
+                    commit(issue, empty0 + 8 * rv.s);
+                    if (more) commit(issue, empty0 + 8 * rk.s);
+                    r = rk;
                 }
-                if (!ok) break;
-                entry += 2 * n;
                 if (!known) {
-                    ok = wait(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems);
-                    if (!ok) break;
+                    wait(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems);
                     next = take_item(k + 1);
                 }
                 item = next;
             }
-            if (!ok && lane == 0) {
-                record_error(p.err, kErrConsumerWait);
-                *abort_flag = 1;
-            }
+            ask(Ring{0xFFFFFFFFu, 0}, 0);
             commit(issue, mfinal);  // every mma complete before tensor memory is freed
-            if (!mbar_wait_bounded(mfinal, 0u) && lane == 0) record_error(p.err, kErrDrainWait);
+            wait(mfinal, 0);
             __syncwarp();
         }
     } else if (warp < 12) {
@@ -586,12 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         w[q] = pack_half2(e.x, e.y);
                     }
                     tc_st32(s_t + 16 * i, w);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive((i == 0 ? p_half : p_ready) + 8 * x);
                 }
                 sum = fadd2(sum, fadd2(part[0], part[1]));
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * x);
             }
             if (!ok) break;
             // read by the storing warps before this tile's item after next comes here
@@ -622,14 +673,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
                 if (!ok || item.tiles[x] == 0) continue;
                 const int parity = n_items[x]++ & 1;
-                ok = __all_sync(0xffffffffu, idle_wait(l_full + 8 * x, parity, abort_flag) && idle_wait(o_full + 8 * x, parity, abort_flag));
+                ok = __all_sync(0xffffffffu, tc_wait(l_full + 8 * x, parity, abort_flag) && tc_wait(o_full + 8 * x, parity, abort_flag));
                 if (!ok) continue;
                 tc_fence_after();
                 const float inv = 1.0f / sums[(parity * 2 + x) * 128 + row];
                 const int tok = item.tok0 + x * tile_toks + row / pack, head = item.head0 + row % pack;
                 const bool live = item.start + tok < item.end;
                 TO *out = static_cast<TO *>(p.out) + (static_cast<int64_t>(item.start + tok) * p.n_heads + head) * D;
-                float check = 0.0f;  // 0 times every value: NaN if one is not finite
+                const bool patch = odd[2 * (k % 8)] != 0;
+                const __half *values = static_cast<const __half *>(p.v) + item.head0 / p.group * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
@@ -642,20 +694,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int q = 0; q < 32; q += 16) {
+                        if (!live) continue;
                         float y[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            y[e] = __uint_as_float(o[q + e]) * inv;
-                            check = fmaf(y[e], 0.0f, check);
-                        }
-                        if (live) store16(out + i + q, y);
+                        for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(o[q + e]) * inv;
+                        if (patch)  // what warp 3 took out of the tiles on the diagonal, as far as this row sees it
+                            for (int key = first_masked(item) * kTileKeys; key <= tok; ++key) {
+                                const __half *row_v = values + (item.start + key) * p.v_stride + i + q;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if ((__half_as_ushort(row_v[e]) & 0x7C00u) == 0x7C00u) y[e] += __half2float(row_v[e]);
+                            }
+                        store16(out + i + q, y);
                     }
-                }
-                uint32_t bad = __ballot_sync(0xffffffffu, live && check != 0.0f);
-                for (; bad; bad &= bad - 1) {
-                    const int src = __ffs(bad) - 1;
-                    attend_row<D, TO>(p, item.start, item.start + __shfl_sync(0xffffffffu, tok, src),
-                                      __shfl_sync(0xffffffffu, head, src));
+                    __syncwarp();
                 }
             }
         }
