@@ -4,18 +4,27 @@
 // A work item is 256 query rows of one key/value head's group: tokens of one
 // sequence times `pack` heads (the largest power of two that divides the
 // group, at most 128), so that a short prompt's rows fill a tile. Two 128-row
-// tiles A and B share every key/value tile of 128 tokens. One thread block a
-// multiprocessor takes items in turn (of falling length, in snake order, so
-// that the blocks' sums are alike), and every role runs on into the next item
-// as soon as its own operands allow:
-//  * warp 2: finds the items and publishes them, up to four ahead.
-//  * warp 0, lane 0: TMA producer: query tiles, and key and value tiles in turn
-//    into a ring (128-byte swizzle, 64 channels a box).
-//  * warp 1, lane 0: issues tcgen05.mma. S = Q K^T into 128 tensor-memory
-//    columns a tile, O += P V with P read from tensor memory (f16, over S's
-//    columns) and V as it lies in memory (N-major operand). The order
-//    PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) keeps the tensor cores on one tile while
-//    the other one's softmax runs; P V starts on the first half of P.
+// tiles A and B share every key/value tile of 128 tokens. The launch has a
+// thread block an item, the longest first; the block that a multiprocessor runs
+// takes over the next one not yet started (cluster launch control) whenever it
+// needs work, and every role runs on into the next item as soon as its own
+// operands allow:
+//  * warp 0, lane 0: TMA producer: query tiles, key tiles and value tiles, the
+//    latter two into a ring each (128-byte swizzle, 64 channels a box).
+//  * warp 1: issues the tcgen05.mma. S = Q K^T into 128 tensor-memory columns a
+//    tile, O += P V with P read from tensor memory (f16, over S's columns) and
+//    V as it lies in memory (N-major operand). The order PV_A(j) S_A(j+1)
+//    PV_B(j) S_B(j+1) keeps the two tiles in turn: the tensor cores have one's
+//    products while the other's softmax runs (two issuers of their own fell
+//    into step, softmax with softmax: 524 us at 8192 tokens instead of 371).
+//    P V starts on the first half of P.
+//  * warp 2: takes items over, finds their rows and publishes them, up to four
+//    ahead.
+//  * warp 3: looks through the value tiles on the diagonal. The product P V
+//    takes 0 times every value that a row does not see, which is NaN for a
+//    value that is not finite; such values are set to 0 in shared memory
+//    before the product, and the storing warps add them to the rows that do
+//    see them (a weight above 0 times an infinity or NaN is that value).
 //  * warps 4..7 and 8..11: softmax of tile A and B, a row a thread: S from
 //    tensor memory, running maximum, exp2, P back in f16. O is rescaled in
 //    place only when a row's maximum has grown by more than 2^8 over the one
@@ -23,14 +32,9 @@
 //  * warps 12..15: divide O by the rows' sums and store, while the others are
 //    in the next item.
 // The softmax warps take the registers that the other two warpgroups give up.
-//  * warp 3: looks through the value tiles on the diagonal, on warp 1's demand
-//    and while the softmax of the tile runs. The product P V
-//    takes 0 times every value that a row does not see, which is NaN for a
-//    value that is not finite; such values are set to 0 in shared memory
-//    before the product, and the storing warps add them to the rows that do
-//    see them (a weight above 0 times an infinity or NaN is that value).
 // Only tiles on the diagonal are masked; they also hold whatever follows the
-// sequence's end.
+// sequence's end. The products leave out the keys that no row of the tile sees
+// (in steps of 16).
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -50,29 +54,95 @@ constexpr float kGrow = 8.0f;        // log2 of how far a row's weights may exce
 
 template <int D> struct Shape {
     static constexpr int kTile = 128 * D * 2;  // bytes of a query, key or value tile
-    static constexpr int kStages = D == 128 ? 5 : 10;
-    static constexpr int kTiles = (2 + kStages) * kTile;
-    static constexpr int kSmem = kTiles + 2752;  // tiles, then barriers, items and sums
+    static constexpr int kK = D == 128 ? 2 : 5, kV = D == 128 ? 3 : 5;  // key, value tiles in shared memory
+    static constexpr int kTiles = (2 + kK + kV) * kTile;
+    static constexpr int kSmem = kTiles + 640 + 1024;  // tiles, then barriers, items and sums
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
 // tcgen05.mma, kind::f16, f32 accumulators, and its commit, issued where
 // `issue` is not 0 (one lane). The whole warp runs the code around them: its
 // addresses and descriptors then stay in uniform registers, which the
-// instructions take their operands from; inside a branch of one lane each
-// operand was moved there anew, and issuing took longer than the products.
-__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// instructions take their operands from. The issuing warp is bound by its
+// instructions' latency, not by their number on the multiprocessor, so the
+// products come as blocks with one predicate and a constant high descriptor
+// word: with descriptors added up in 64 bits and a predicate each, 32 products
+// took about 3800 cycles to issue, 60% more than the tensor cores need.
+// S = Q K^T: 16 channels a product, the 64-channel halves 16 KB apart.
+template <int D> __device__ __forceinline__ void mma_s(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t hi) {
+    if (D == 64)
+        asm volatile(
+            "{\n\t.reg .pred p0, p1, q;\n\t.reg .b64 da, db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %4, 0;\n\tsetp.ne.u32 p0, 0, 0;\n\tsetp.eq.u32 p1, 0, 0;\n\t"
+            "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p0;\n\t"
+            "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(issue), "r"(hi)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p0, p1, q;\n\t.reg .b64 da, db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %4, 0;\n\tsetp.ne.u32 p0, 0, 0;\n\tsetp.eq.u32 p1, 0, 0;\n\t"
+            "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p0;\n\t"
+            "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 1024;\n\tadd.u32 b, %2, 1024;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 1026;\n\tadd.u32 b, %2, 1026;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 1028;\n\tadd.u32 b, %2, 1028;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "add.u32 a, %1, 1030;\n\tadd.u32 b, %2, 1030;\n\t"
+            "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p1;\n\t"
+            "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(issue), "r"(hi)
+            : "memory");
+}
+// O (+)= P V over 64 keys: 16 keys a product, 8 columns of P and 2 KB of V.
+__device__ __forceinline__ void mma_pv(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t hi) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc),
-        "r"(issue)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "setp.ne.u32 p, 1, 0;\n\t"
+        "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(issue), "r"(hi)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The same over 16 keys.
+__device__ __forceinline__ void mma_pv16(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t hi) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc),
-        "r"(issue)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.b64 db, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+        "r"(issue), "r"(hi)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t issue, uint32_t bar) {
@@ -86,11 +156,20 @@ __device__ __forceinline__ void arrive_if(uint32_t issue, uint32_t bar) {
                  "r"(issue)
                  : "memory");
 }
-__device__ __forceinline__ void store_if(uint32_t issue, uint32_t a, int x, int y) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q st.shared.v2.b32 [%0], {%1, %2};\n\t}" ::"r"(a), "r"(x),
-                 "r"(y), "r"(issue)
-                 : "memory");
+// Bounded wait (about 1 s) that sleeps about NS nanoseconds between polls and
+// gives up once another thread of the block has set the abort flag. Polling
+// without a pause takes shared-memory cycles from the tensor cores' operands.
+template <int NS> __device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1; i < kWaitLimitPolls; ++i) {
+        __nanosleep(NS);
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0 && (*abort_flag || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    }
+    return false;
 }
+
 // tc_wait of a whole warp that goes on in either case: a wait that gives up
 // sets the abort flag, with which all others of the block give up soon.
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *err) {
@@ -100,14 +179,13 @@ __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile i
     }
 }
 
-// Shared-memory descriptor of a 128-byte-swizzled N-major operand (64-element
-// rows of N, one row a k): the stride between 64-element parts of N, and
-// between groups of 8 k (one atom, 1024 bytes).
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t start, uint32_t n_stride) {
-    return static_cast<uint64_t>((start >> 4) & 0x3FFFu) | (static_cast<uint64_t>((n_stride >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>((1024u >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
+// Shared-memory descriptors, 128-byte swizzle: low word the address and the
+// leading stride, high word the stride between groups of 8 rows (K-major) or of
+// 8 k (N-major), one atom of 1024 bytes, version 1, swizzle mode 2. K-major has
+// no leading stride (1); N-major operands lie as 64-element rows of N, one row
+// a k, and their leading stride is the one between 64-element parts of N.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t start, uint32_t leading) { return ((start >> 4) & 0x3FFFu) | leading << 16; }
 constexpr uint32_t kIdescNMajorB = 1u << 16;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, int c0, int c1, int c2, uint32_t bar) {
@@ -244,12 +322,113 @@ __device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
     }
 }
 
+// Asks for the next thread block of the launch that has not started; the
+// answer, 16 bytes, arrives on `bar`.
+__device__ __forceinline__ void ask_block(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+                 "r"(bar)
+                 : "memory");
+}
+// Its index, -1 where none was left.
+__device__ __forceinline__ int asked_block(uint32_t answer) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tmov.s32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+        : "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return x;
+}
+
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// Place in a ring of N tiles: the tile and its barriers' phase.
+template <int N> struct Ring {
+    uint32_t s, ph;
+    __device__ __forceinline__ Ring next() const {
+        const uint32_t t = s + 1 == N ? 0u : s + 1;
+        return Ring{t, t == 0u ? ph ^ 1u : ph};
+    }
+};
 
 // Not 0 where one of a word's two f16 is not finite (an exponent field of
 // ones, to which one more carries into the sign's place).
 __device__ __forceinline__ uint32_t odd_half2(uint32_t w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
+
+// The softmax of one tile of S, a row a thread: S at s_t becomes P in place,
+// `ref` and `sum` go on, O at o_t is rescaled where a maximum grew too far.
+// Columns past `see` count as -inf; the warp's rows all see those up to
+// see_all.
+template <int D>
+__device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, uint32_t bar_half, uint32_t bar_all, float c, bool negate,
+                                             bool first, int see, int see_all, float &ref, float2 &sum) {
+    uint32_t v[4][32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tm_ld32(s_t + 32 * i, v[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tm_wait_ld(v[i]);
+    if (negate)
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i >> 5][i & 31] ^= 0x80000000u;
+    if (see_all < kTileKeys - 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (see_all < 32 * i + 31) {
+#pragma unroll
+                for (int q = 0; q < 32; ++q)
+                    if (32 * i + q > see) v[i][q] = 0xFF800000u;
+            }
+    }
+    float mx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        mx[i] = __uint_as_float(v[i][0]);
+#pragma unroll
+        for (int q = 1; q < 31; q += 2) mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(v[i][q])), __uint_as_float(v[i][q + 1]));
+        mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
+    }
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+    if (first) {
+        ref = top;
+    } else if (__any_sync(0xffffffffu, top > ref + kGrow)) {
+        // S of this tile is complete, so P V of the tiles before is, too
+        const float next = fmaxf(ref, top), keep = exp2_approx(ref - next);
+        ref = next;
+        sum.x *= keep, sum.y *= keep;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tm_ld32(o_t + i, o);
+            tm_wait_ld(o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * keep);
+            tc_st32(o_t + i, o);
+        }
+    }
+    const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+    float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+            float2 e = ffma2(make_float2(__uint_as_float(v[2 * h + (q >> 4)][2 * (q & 15)]),
+                                         __uint_as_float(v[2 * h + (q >> 4)][2 * (q & 15) + 1])), c2, r2);
+            e.x = exp2_approx(e.x), e.y = exp2_approx(e.y);
+            part[q & 1] = fadd2(part[q & 1], e);
+            w[q] = pack_half2(e.x, e.y);
+        }
+        tc_st32(s_t + 32 * h, w);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(h == 0 ? bar_half : bar_all);
+    }
+    sum = fadd2(sum, fadd2(part[0], part[1]));
+}
 
 template <int D, class TO>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -258,25 +437,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     using Sh = Shape<D>;
     constexpr int kHalves = D / 64;  // boxes of 64 channels
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // (the swizzle's atoms are 1024 bytes)
-    const uint32_t q_a = smem_addr(smem_raw), ring_a = q_a + 2 * Sh::kTile, base_a = q_a + Sh::kTiles;
+    const uint32_t q_a = smem_addr(smem_raw), k_a = q_a + 2 * Sh::kTile, v_a = k_a + Sh::kK * Sh::kTile, base_a = q_a + Sh::kTiles;
     uint8_t *base = smem_raw + Sh::kTiles;
     // barriers, 8 bytes each (those of the two tiles side by side)
-    const uint32_t full0 = base_a, empty0 = full0 + 8 * Sh::kStages, q_full = empty0 + 8 * Sh::kStages, q_empty = q_full + 16;
-    const uint32_t s_full = q_empty + 16, p_ready = s_full + 16, o_full = p_ready + 16, o_empty = o_full + 16;
-    const uint32_t l_full = o_empty + 16, item_full = l_full + 16, item_empty = item_full + 8 * kItems, mfinal = item_empty + 8 * kItems;
-    const uint32_t p_half = mfinal + 8, v_ask = p_half + 16, v_clean = v_ask + 8;
+    const uint32_t k_full = base_a, k_empty = k_full + 8 * Sh::kK, v_full = k_empty + 8 * Sh::kK, v_empty = v_full + 8 * Sh::kV;
+    const uint32_t v_ready = v_empty + 8 * Sh::kV, q_full = v_ready + 8 * Sh::kV, q_empty = q_full + 16, s_full = q_empty + 16;
+    const uint32_t p_half = s_full + 16, p_ready = p_half + 16, o_full = p_ready + 16, o_empty = o_full + 16, l_full = o_empty + 16;
+    const uint32_t item_full = l_full + 16, item_empty = item_full + 8 * kItems, mfinal = item_empty + 8 * kItems, block_bar = mfinal + 16;
+    const uint32_t block_answer = base_a + 416;  // 16 bytes
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + 448);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(base + 452);
     volatile Item *items = reinterpret_cast<volatile Item *>(base + 456);
-    volatile int *asked = reinterpret_cast<volatile int *>(base + 576);     // v_ask's stage (-1: the end) and item
-    volatile int *odd = reinterpret_cast<volatile int *>(base + 584);       // [item % 8][2]: diagonal values that are not finite
-    volatile float *sums = reinterpret_cast<volatile float *>(base + 704);  // [item parity][tile][row]
+    volatile int *odd = reinterpret_cast<volatile int *>(base + 576);       // [item % 8]: diagonal values that are not finite
+    volatile float *sums = reinterpret_cast<volatile float *>(base + 640);  // [tile][row]
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Sh::kStages; ++s) {
-            mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, 1);
+        for (int i = 0; i < Sh::kK; ++i) {
+            mbar_init(k_full + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < Sh::kV; ++i) {
+            mbar_init(v_full + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, 1);
+            mbar_init(v_ready + 8 * i, 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(q_full + 8 * x, 1);
@@ -290,17 +474,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full + 8 * i, 1);
-            mbar_init(item_empty + 8 * i, 14);  // the copies, the mma issuer and twelve warps
+            mbar_init(item_empty + 8 * i, 15);  // every warp but 2
         }
+        mbar_init(block_bar, 1);
         mbar_init(mfinal, 1);
-        mbar_init(v_ask, 1);
-        mbar_init(v_clean, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
         tc_alloc(smem_addr(tmem_slot), kTmemCols);
         tc_relinquish();
+    }
+    if (warp == 2 && lane < 3) {
+        const CUtensorMap *m = lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -310,13 +497,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait_prior_grids();
     pdl_allow_dependents();
     // item k of the block as a consumer: all lanes of the warp (or one thread) call it
-    auto wait_item = [&](int k) { return tc_wait(item_full + 8 * (k % kItems), (k / kItems) & 1, abort_flag); };
+    auto wait_item = [&](int k) { return sleep_wait<100>(item_full + 8 * (k % kItems), (k / kItems) & 1, abort_flag); };
     auto read_item = [&](int k) {
         const volatile Item &s = items[k % kItems];
         Item it;
         it.start = s.start, it.end = s.end, it.tok0 = s.tok0, it.head0 = s.head0;
         it.tiles[0] = s.tiles[0], it.tiles[1] = s.tiles[1], it.last = s.last;
         return it;
+    };
+    // keys of key tile j that some row of tile x of the item sees
+    auto live_keys = [&](const Item &it, int x, int j) {
+        const int past = min(it.end - it.start, it.tok0 + (x + 1) * tile_toks) - j * kTileKeys;
+        return past < kTileKeys ? past : kTileKeys;
     };
     // first key tile that some row of the item does not see in full
     auto first_masked = [&](const Item &it) { return (it.tok0 + 1) / kTileKeys; };
@@ -325,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         fewer_registers<64>();
         if (warp == 0) {
             // ---------------- copies
-            int stage = 0;
-            uint32_t ph = 0;
-            int64_t issued = 0;
+            Ring<Sh::kK> rk = {0, 0};
+            Ring<Sh::kV> rv = {0, 0};
+            int n_k = 0;           // key tiles so far, at most the ring's
             int used[2] = {0, 0};  // query tiles loaded
             bool ok = true;
             for (int k = 0; ok; ++k) {
@@ -338,28 +530,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(item_empty + 8 * (k % kItems));
                 if (it.last) break;
                 if (lane == 0) {
-                    const int kv_head = it.head0 / p.group, n = 2 * max(it.tiles[0], it.tiles[1]);
-                    for (int i = 0; ok && i < n; ++i) {
-                        if (issued >= Sh::kStages) ok = tc_wait(empty0 + 8 * stage, ph ^ 1u, abort_flag);
+                    const int kv_head = it.head0 / p.group, n = max(it.tiles[0], it.tiles[1]);
+                    auto load = [&](uint32_t dst, const CUtensorMap *map, int head, int row, uint32_t bar) {
+                        mbar_arrive_expect_tx(bar, Sh::kTile);
+                        for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * (128 * 128), map, 64 * h, head, row, bar);
+                    };
+                    for (int j = 0; ok && j < n; ++j) {
+                        // (the rings are the same depth or the keys' shallower: a first round of keys is one of values, too)
+                        if (n_k >= Sh::kK) ok = sleep_wait<40>(k_empty + 8 * rk.s, rk.ph ^ 1u, abort_flag);
                         if (!ok) break;
-                        mbar_arrive_expect_tx(full0 + 8 * stage, Sh::kTile);
-                        for (int h = 0; h < kHalves; ++h)
-                            tma_load_3d(ring_a + stage * Sh::kTile + h * (128 * 128), i & 1 ? &map_v : &map_k, 64 * h, kv_head,
-                                        it.start + (i >> 1) * kTileKeys, full0 + 8 * stage);
-                        ++issued;
-                        if (++stage == Sh::kStages) stage = 0, ph ^= 1u;
-                        if (i > 0) continue;
+                        load(k_a + rk.s * Sh::kTile, &map_k, kv_head, it.start + j * kTileKeys, k_full + 8 * rk.s);
+                        rk = rk.next();
+                        if (j == 0)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {  // the queries, once the last item's are used up
-                            if (!ok || it.tiles[x] == 0) continue;
-                            if (used[x] > 0) ok = tc_wait(q_empty + 8 * x, (used[x] - 1) & 1, abort_flag);
-                            if (!ok) continue;
-                            ++used[x];
-                            mbar_arrive_expect_tx(q_full + 8 * x, Sh::kTile);
-                            for (int h = 0; h < kHalves; ++h)
-                                tma_load_3d(q_a + x * Sh::kTile + h * (128 * 128), &map_q, 64 * h, it.head0,
-                                            it.start + it.tok0 + x * tile_toks, q_full + 8 * x);
-                        }
+                            for (int x = 0; x < 2; ++x) {  // the queries, once the last item's are used up
+                                if (!ok || it.tiles[x] == 0) continue;
+                                if (used[x] > 0) ok = sleep_wait<40>(q_empty + 8 * x, (used[x] - 1) & 1, abort_flag);
+                                if (!ok) continue;
+                                ++used[x];
+                                load(q_a + x * Sh::kTile, &map_q, it.head0, it.start + it.tok0 + x * tile_toks, q_full + 8 * x);
+                            }
+                        if (ok && n_k >= Sh::kV) ok = sleep_wait<40>(v_empty + 8 * rv.s, rv.ph ^ 1u, abort_flag);
+                        if (!ok) break;
+                        load(v_a + rv.s * Sh::kTile, &map_v, kv_head, it.start + j * kTileKeys, v_full + 8 * rv.s);
+                        rv = rv.next();
+                        if (n_k < 16) ++n_k;
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -368,26 +563,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 record_error(p.err, kErrProducerWait);
                 *abort_flag = 1;
             }
-            if (lane == 0) {
-                // leave no copy in flight into this block's shared memory
+            // Leave no copy in flight into this block's shared memory. Without an error every tile has been
+            // waited for by those who used it; else each wait here is for a tile's own barrier to turn.
+            if (!ok && lane == 0) {
                 bool landed = true;
-                for (int64_t i = issued > Sh::kStages ? issued - Sh::kStages : 0; i < issued; ++i)
-                    landed = landed && mbar_wait_bounded(full0 + 8 * static_cast<int>(i % Sh::kStages), (i / Sh::kStages) & 1);
+                for (int i = 0; i < Sh::kK && i < n_k + 1; ++i, rk = rk.next()) landed = mbar_wait_bounded(k_full + 8 * rk.s, rk.ph ^ 1u) && landed;
+                for (int i = 0; i < Sh::kV && i < n_k; ++i, rv = rv.next()) landed = mbar_wait_bounded(v_full + 8 * rv.s, rv.ph ^ 1u) && landed;
                 for (int x = 0; x < 2; ++x)
-                    if (used[x] > 0) landed = landed && mbar_wait_bounded(q_full + 8 * x, (used[x] - 1) & 1);
+                    if (used[x] > 0) landed = mbar_wait_bounded(q_full + 8 * x, (used[x] - 1) & 1) && landed;
                 if (!landed) record_error(p.err, kErrDrainWait);
             }
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- items
             bool ok = true;
+            int index = blockIdx.x;
             for (int k = 0; ok; ++k) {
                 Item it;
-                const int64_t index = static_cast<int64_t>(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                it.last = index > INT32_MAX || !find_item(p, pack, static_cast<int>(index), it);
-                if (k >= kItems) ok = __all_sync(0xffffffffu, tc_wait(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
-                if (!ok) break;
-                if (lane == 0) {
+                // (an index that is no item ends the block as the launch's end does: none after it is one)
+                it.last = index < 0 || !find_item(p, pack, index, it);
+                if (!it.last && lane == 0) {
+                    fence_proxy_async_smem();  // the last answer has been read
+                    mbar_arrive_expect_tx(block_bar, 16);
+                    ask_block(block_answer, block_bar);
+                }
+                if (k >= kItems) ok = __all_sync(0xffffffffu, sleep_wait<200>(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
+                if (ok && lane == 0) {
                     volatile Item &dst = items[k % kItems];
                     dst.start = it.start, dst.end = it.end, dst.tok0 = it.tok0, dst.head0 = it.head0;
                     dst.tiles[0] = it.tiles[0], dst.tiles[1] = it.tiles[1], dst.last = it.last;
@@ -395,163 +596,180 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (it.last) break;
+                // (waited for in every case: the answer must not arrive after the block's end)
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(block_bar, k & 1))) {
+                    if (lane == 0) record_error(p.err, kErrProducerWait);
+                    *abort_flag = 1;
+                    break;
+                }
+                index = asked_block(block_answer);
+                __syncwarp();
             }
-        } else if (warp == 3) {
-            // ---------------- value tiles on the diagonal
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                ok = __all_sync(0xffffffffu, tc_wait(v_ask, i & 1, abort_flag));
-                const int st = asked[0], k = asked[1];
-                __syncwarp();
-                if (!ok || st < 0) break;
-                uint4 *tile = reinterpret_cast<uint4 *>(smem_raw + 2 * Sh::kTile + st * Sh::kTile);
-                uint32_t found = 0;
-#pragma unroll 8
-                for (int q = lane; q < Sh::kTile / 16; q += 32) {
-                    const uint4 w = tile[q];
-                    found |= odd_half2(w.x) | odd_half2(w.y) | odd_half2(w.z) | odd_half2(w.w);
-                }
-                if (__any_sync(0xffffffffu, found != 0)) {
-                    __half *h = reinterpret_cast<__half *>(tile);
-                    for (int q = lane; q < Sh::kTile / 2; q += 32)
-                        if ((__half_as_ushort(h[q]) & 0x7C00u) == 0x7C00u) h[q] = __ushort_as_half(0);
-                    fence_proxy_async_smem();
-                    if (lane == 0) odd[2 * (k % 8)] = 1;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v_clean);
+            if (!ok) {
+                if (lane == 0) record_error(p.err, kErrProducerWait);
+                *abort_flag = 1;
             }
             __syncwarp();
-        } else if (warp == 1) {
+        } else if (warp == 3) {
+            // ---------------- value tiles on the diagonal
+            Ring<Sh::kV> rv = {0, 0};
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                ok = __all_sync(0xffffffffu, wait_item(k));
+                if (!ok) break;
+                const Item it = read_item(k);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(item_empty + 8 * (k % kItems));
+                    odd[k % 8] = 0;  // (the storing warps are less than eight items behind)
+                }
+                if (it.last) break;
+                const int n = max(it.tiles[0], it.tiles[1]), masked = first_masked(it);
+                for (int j = 0; j < n; ++j) {
+                    ok = __all_sync(0xffffffffu, sleep_wait<40>(v_full + 8 * rv.s, rv.ph, abort_flag));
+                    if (!ok) break;
+                    if (j >= masked) {
+                        uint4 *mem = reinterpret_cast<uint4 *>(smem_raw + (2 + Sh::kK + rv.s) * Sh::kTile);
+                        uint32_t bad = 0;
+#pragma unroll 8
+                        for (int q = lane; q < Sh::kTile / 16; q += 32) {
+                            const uint4 w = mem[q];
+                            bad |= odd_half2(w.x) | odd_half2(w.y) | odd_half2(w.z) | odd_half2(w.w);
+                        }
+                        if (__any_sync(0xffffffffu, bad != 0)) {
+                            __half *h = reinterpret_cast<__half *>(mem);
+                            for (int q = lane; q < Sh::kTile / 2; q += 32)
+                                if ((__half_as_ushort(h[q]) & 0x7C00u) == 0x7C00u) h[q] = __ushort_as_half(0);
+                            fence_proxy_async_smem();
+                            if (lane == 0) odd[k % 8] = 1;
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(v_ready + 8 * rv.s);
+                    rv = rv.next();
+                }
+            }
+            if (!ok) {
+                if (lane == 0) record_error(p.err, kErrConsumerWait);
+                *abort_flag = 1;
+            }
+            __syncwarp();
+        } else {
             // ---------------- mma issuer (the whole warp, one lane issues). The steps are straight-line code
             // but for branches that are alike in all lanes; what a failed wait leaves is not used.
             const uint32_t issue = lane == 0;
             constexpr uint32_t kIdS = tc_idesc_f16(128, kTileKeys), kIdO = tc_idesc_f16(128, D) | kIdescNMajorB;
-            const uint64_t q_desc = tc_smem_desc(q_a, 1024), k_desc = tc_smem_desc(ring_a, 1024), v_desc = desc_n_major(ring_a, 128 * 128);
-            constexpr uint64_t kStep = Sh::kTile / 16;  // from tile to tile in a descriptor
-            struct Ring {  // place of a key or value tile
-                uint32_t s, ph;
-                __device__ __forceinline__ Ring next() const {
-                    const uint32_t t = s + 1 == Sh::kStages ? 0u : s + 1;
-                    return Ring{t, t == 0u ? ph ^ 1u : ph};
-                }
-            };
-            uint32_t n_p[2] = {0, 0};      // weight tiles consumed so far
-            uint32_t n_o[2] = {0, 0};      // items whose O has been started, by tile
-            uint32_t n_q[2] = {0, 0};      // query tiles used so far
-            uint32_t n_clean = 0;          // value tiles looked through
+            const uint32_t q_desc = desc_lo(q_a, 1), k_desc = desc_lo(k_a, 1), v_desc = desc_lo(v_a, 128 * 128 / 16);
+            constexpr uint32_t kStep = Sh::kTile / 16;  // from tile to tile in a descriptor
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u))) wait_slow(bar, parity & 1u, abort_flag, p.err);
             };
             auto there = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)) != 0; };
-            // item k, published: its fields as values that are the same in every lane for the compiler, too
+            struct Work {
+                int t[2], n;     // key tiles of A and B, of the item
+                int steps[2];    // of the last one's keys, in steps of 16
+                int last;
+            };
+            // item k, published (through shuffles: the same in every lane for the compiler, too)
             auto take_item = [&](int k) {
-                Item it = read_item(k);
+                const Item it = read_item(k);
                 __syncwarp();
                 arrive_if(issue, item_empty + 8 * (k % kItems));
-                it.tiles[0] = __shfl_sync(0xffffffffu, it.tiles[0], 0);
-                it.tiles[1] = __shfl_sync(0xffffffffu, it.tiles[1], 0);
-                it.last = __shfl_sync(0xffffffffu, it.last | *abort_flag, 0);
-                it.tok0 = __shfl_sync(0xffffffffu, it.tok0, 0);
-                return it;
-            };
-            auto product_s = [&](int x, const Ring &r, bool final) {
-                const uint64_t a = q_desc + x * kStep, b = k_desc + r.s * kStep;
+                Work w;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = static_cast<uint64_t>((k >> 2) * (128 * 128 / 16) + (k & 3) * 2);
-                    mma_ss(issue, tmem + 128 * x, a + off, b + off, kIdS, k != 0);
+                for (int x = 0; x < 2; ++x) {
+                    w.t[x] = __shfl_sync(0xffffffffu, it.tiles[x], 0);
+                    w.steps[x] = __shfl_sync(0xffffffffu, (live_keys(it, x, it.tiles[x] - 1) + 15) / 16, 0);
                 }
+                w.n = max(w.t[0], w.t[1]);
+                w.last = __shfl_sync(0xffffffffu, it.last | *abort_flag, 0);
+                return w;
+            };
+            // S of tile x with key tile j of its item, at r
+            auto product_s = [&](const Work &w, int x, int j, const Ring<Sh::kK> &r) {
+                const uint32_t a = q_desc + x * kStep, b = k_desc + r.s * kStep;
+                const bool final = j + 1 == w.t[x];
+                const uint32_t id = final ? (kIdS & ~(0x3Fu << 17)) | static_cast<uint32_t>(w.steps[x] * 2) << 17 : kIdS;
+                mma_s<D>(issue, tmem + 128 * x, a, b, id, kDescHi);
                 commit(issue, s_full + 8 * x);
                 if (final) commit(issue, q_empty + 8 * x);
             };
-            auto ask = [&](const Ring &r, int k) {
-                store_if(issue, smem_addr(const_cast<int *>(asked)), static_cast<int>(r.s), k);
-                arrive_if(issue, v_ask);
-            };
-            Ring r = {0, 0};  // the item's first key tile, then the last one used
+            Ring<Sh::kK> rk = {0, 0};
+            Ring<Sh::kV> rv = {0, 0};
+            uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0}, n_o[2] = {0, 0};  // weight tiles, query tiles, results so far
             wait(item_full, 0);
-            Item item = take_item(0);
+            Work w = take_item(0);
             bool started = false;  // S of the item's first key tile issued early for tile A
-            for (int k = 0; !item.last; ++k) {
-                const int n = max(item.tiles[0], item.tiles[1]), masked = first_masked(item);
+            for (int k = 0; !w.last; ++k) {
+                wait(k_full + 8 * rk.s, rk.ph);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (item.tiles[x] == 0 || (x == 0 && started)) continue;
+                    if (w.t[x] == 0 || (x == 0 && started)) continue;
                     wait(q_full + 8 * x, n_q[x]++);
-                    wait(full0 + 8 * r.s, r.ph);
                     tc_fence_after();
-                    product_s(x, r, item.tiles[x] == 1);
+                    product_s(w, x, 0, rk);
                 }
-                commit(issue, empty0 + 8 * r.s);
-                store_if(issue, smem_addr(const_cast<int *>(odd + 2 * (k % 8))), 0, 0);  // (the storing warps are less than eight items behind)
-                Item next = {};
+                commit(issue, k_empty + 8 * rk.s);
+                rk = rk.next();
+                Work next;
                 bool known = false;
                 started = false;
-                bool asked_next = false;  // the next value tile, where masked
-                for (int j = 0; j < n; ++j) {
-                    const Ring rv = r.next(), rk = rv.next();
-                    const bool more = j + 1 < n;
-                    wait(full0 + 8 * rv.s, rv.ph);
-                    if (more) wait(full0 + 8 * rk.s, rk.ph);
-                    if (j >= masked) {
-                        if (!asked_next) ask(rv, k);
-                        wait(v_clean, n_clean++);
-                        asked_next = false;
-                    }
-                    if (more && j + 1 >= masked) {
-                        const Ring rn = rk.next();
-                        if (there(full0 + 8 * rn.s, rn.ph)) {
-                            ask(rn, k);
-                            asked_next = true;
-                        }
-                    }
+                for (int j = 0; j < w.n; ++j) {
+                    const bool more = j + 1 < w.n;
+                    wait(v_ready + 8 * rv.s, rv.ph);
+                    if (more) wait(k_full + 8 * rk.s, rk.ph);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (j < item.tiles[x]) {
+                        if (j < w.t[x]) {
+                            const bool final = j + 1 == w.t[x];
                             if (j == 0) {
                                 if (n_o[x] > 0) wait(o_empty + 8 * x, n_o[x] - 1);
                                 ++n_o[x];
                             }
-                            const uint64_t v = v_desc + rv.s * kStep;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                wait((h == 0 ? p_half : p_ready) + 8 * x, n_p[x]);
+                            const uint32_t v = v_desc + rv.s * kStep;
+                            const uint32_t o_t = tmem + 256 + 128 * x, p_t = tmem + 128 * x;
+                            wait(p_half + 8 * x, n_p[x]);
+                            tc_fence_after();
+                            if (!final) {
+                                mma_pv(issue, o_t, p_t, v, kIdO, j, kDescHi);
+                                wait(p_ready + 8 * x, n_p[x]);
                                 tc_fence_after();
-#pragma unroll
-                                for (int i = 4 * h; i < 4 * h + 4; ++i)
-                                    mma_ts(issue, tmem + 256 + 128 * x, tmem + 128 * x + 8 * i, v + static_cast<uint64_t>(i * (2048 / 16)),
-                                           kIdO, i != 0 ? 1u : static_cast<uint32_t>(j));
+                                mma_pv(issue, o_t, p_t + 32, v + 4 * (2048 / 16), kIdO, 1, kDescHi);
+                                product_s(w, x, j + 1, rk);
+                            } else {  // the keys that some row sees
+                                wait(p_ready + 8 * x, n_p[x]);
+                                tc_fence_after();
+                                for (int i = 0; i < w.steps[x]; ++i)
+                                    mma_pv16(issue, o_t, p_t + 8 * i, v + i * (2048 / 16), kIdO, i | j, kDescHi);
+                                commit(issue, o_full + 8 * x);
                             }
                             ++n_p[x];
-                            if (j + 1 < item.tiles[x]) product_s(x, rk, j + 2 == item.tiles[x]);
-                            else commit(issue, o_full + 8 * x);
                         }
-                        if (x == 0 && !more) {
+                        if (x == 0 && !more && there(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems)) {
                             // tile A is done: its next item's first S, if the operands are there, before B's last product
-                            if (there(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems)) {
-                                next = take_item(k + 1);
-                                known = true;
-                                if (!next.last && next.tiles[0] > 0 && there(q_full, n_q[0]) && there(full0 + 8 * rk.s, rk.ph)) {
-                                    tc_fence_after();
-                                    ++n_q[0];
-                                    product_s(0, rk, next.tiles[0] == 1);
-                                    started = true;
-                                }
+                            next = take_item(k + 1);
+                            known = true;
+                            if (!next.last && next.t[0] > 0 && there(q_full, n_q[0]) && there(k_full + 8 * rk.s, rk.ph)) {
+                                tc_fence_after();
+                                ++n_q[0];
+                                product_s(next, 0, 0, rk);
+                                started = true;
                             }
                         }
                     }
-                    commit(issue, empty0 + 8 * rv.s);
-                    if (more) commit(issue, empty0 + 8 * rk.s);
-                    r = rk;
+                    commit(issue, v_empty + 8 * rv.s);
+                    rv = rv.next();
+                    if (more) {
+                        commit(issue, k_empty + 8 * rk.s);
+                        rk = rk.next();
+                    }
                 }
                 if (!known) {
                     wait(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems);
                     next = take_item(k + 1);
                 }
-                item = next;
+                w = next;
             }
-            ask(Ring{0xFFFFFFFFu, 0}, 0);
             commit(issue, mfinal);  // every mma complete before tensor memory is freed
             wait(mfinal, 0);
             __syncwarp();
@@ -579,74 +797,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             float ref = -INFINITY;
             float2 sum = make_float2(0.0f, 0.0f);
             for (int j = 0; j < n; ++j, ++n_s) {
-                ok = __all_sync(0xffffffffu, tc_wait(s_full + 8 * x, n_s & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, sleep_wait<20>(s_full + 8 * x, n_s & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t v[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tm_ld32(s_t + 32 * i, v[i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tm_wait_ld(v[i]);
-                if (negate)
-#pragma unroll
-                    for (int i = 0; i < 128; ++i) v[i >> 5][i & 31] ^= 0x80000000u;
-                const int key0 = j * kTileKeys;
-                if (key0 + kTileKeys - 1 > first_tok) {  // some row does not see every key
-                    const int see = tok - key0;          // columns 0 .. see
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i > see) v[i >> 5][i & 31] = 0xFF800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mx[i] = __uint_as_float(v[i][0]);
-#pragma unroll
-                    for (int q = 1; q < 31; q += 2) mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(v[i][q])), __uint_as_float(v[i][q + 1]));
-                    mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                if (j == 0) {
-                    ref = top;
-                } else if (__any_sync(0xffffffffu, top > ref + kGrow)) {
-                    // S of this tile is complete, so P V of the tiles before is, too
-                    const float next = fmaxf(ref, top), keep = exp2_approx(ref - next);
-                    ref = next;
-                    sum.x *= keep, sum.y *= keep;
-#pragma unroll 1
-                    for (int i = 0; i < D; i += 32) {
-                        uint32_t o[32];
-                        tm_ld32(o_t + i, o);
-                        tm_wait_ld(o);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * keep);
-                        tc_st32(o_t + i, o);
-                    }
-                }
-                const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
-                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        float2 e = ffma2(make_float2(__uint_as_float(v[i + (q >> 4)][2 * (q & 15)]),
-                                                     __uint_as_float(v[i + (q >> 4)][2 * (q & 15) + 1])), c2, r2);
-                        e.x = exp2_approx(e.x), e.y = exp2_approx(e.y);
-                        part[q & 1] = fadd2(part[q & 1], e);
-                        w[q] = pack_half2(e.x, e.y);
-                    }
-                    tc_st32(s_t + 16 * i, w);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive((i == 0 ? p_half : p_ready) + 8 * x);
-                }
-                sum = fadd2(sum, fadd2(part[0], part[1]));
+                // the last column that the warp's first row sees
+                const int see_all = first_tok + (row & ~31) / pack - j * kTileKeys;
+                softmax_tile<D>(s_t, o_t, p_half + 8 * x, p_ready + 8 * x, c, negate, j == 0, tok - j * kTileKeys, see_all, ref, sum);
             }
             if (!ok) break;
-            // read by the storing warps before this tile's item after next comes here
-            sums[((n_items & 1) * 2 + x) * 128 + row] = sum.x + sum.y;
+            // the storing warps must have taken the item before (one of a single tile can be through here
+            // while they are still busy with the other tile), or they would miss a phase of l_full
+            if (n_items > 0) ok = __all_sync(0xffffffffu, sleep_wait<20>(o_empty + 8 * x, (n_items - 1) & 1, abort_flag));
+            if (!ok) break;
+            sums[x * 128 + row] = sum.x + sum.y;
             __syncwarp();
             if (lane == 0) mbar_arrive(l_full + 8 * x);
             ++n_items;
@@ -673,14 +836,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
                 if (!ok || item.tiles[x] == 0) continue;
                 const int parity = n_items[x]++ & 1;
-                ok = __all_sync(0xffffffffu, tc_wait(l_full + 8 * x, parity, abort_flag) && tc_wait(o_full + 8 * x, parity, abort_flag));
+                ok = __all_sync(0xffffffffu, sleep_wait<100>(l_full + 8 * x, parity, abort_flag) && sleep_wait<40>(o_full + 8 * x, parity, abort_flag));
                 if (!ok) continue;
                 tc_fence_after();
-                const float inv = 1.0f / sums[(parity * 2 + x) * 128 + row];
+                const float inv = 1.0f / sums[x * 128 + row];
                 const int tok = item.tok0 + x * tile_toks + row / pack, head = item.head0 + row % pack;
                 const bool live = item.start + tok < item.end;
                 TO *out = static_cast<TO *>(p.out) + (static_cast<int64_t>(item.start + tok) * p.n_heads + head) * D;
-                const bool patch = odd[2 * (k % 8)] != 0;
+                const bool patch = odd[k % 8] != 0;
                 const __half *values = static_cast<const __half *>(p.v) + item.head0 / p.group * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
@@ -749,7 +912,7 @@ bool encode_rows(CUtensorMap *tm, const void *base, int64_t n_tok, int heads, in
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, class TO> cudaError_t launch(const PromptParams &p, int sms, int device, cudaStream_t s) {
+template <int D, class TO> cudaError_t launch(const PromptParams &p, int device, cudaStream_t s) {
     // heads that share a tile: the largest power of two that divides the group
     int pack = p.group & -p.group;
     if (pack > kTileRows) pack = kTileRows;
@@ -772,14 +935,14 @@ template <int D, class TO> cudaError_t launch(const PromptParams &p, int sms, in
     const int toks = 2 * kTileRows / pack;
     const int64_t items = (static_cast<int64_t>(p.n_tok) / toks + p.n_seq) * (p.n_heads / pack);
     if (items > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(prompt_attend_kernel<D, TO>, static_cast<int>(items < sms ? items : sms), kThreads, Shape<D>::kSmem, s, mq, mk, mv, p, pack);
+    return launch_pdl(prompt_attend_kernel<D, TO>, static_cast<int>(items), kThreads, Shape<D>::kSmem, s, mq, mk, mv, p, pack);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attend(const PromptParams &p, int head_dim, int out_type, int sms, int device, cudaStream_t s) {
-    if (head_dim == 64) return out_type == QG_F32 ? launch<64, float>(p, sms, device, s) : launch<64, __half>(p, sms, device, s);
-    return out_type == QG_F32 ? launch<128, float>(p, sms, device, s) : launch<128, __half>(p, sms, device, s);
+cudaError_t launch_prompt_attend(const PromptParams &p, int head_dim, int out_type, int, int device, cudaStream_t s) {
+    if (head_dim == 64) return out_type == QG_F32 ? launch<64, float>(p, device, s) : launch<64, __half>(p, device, s);
+    return out_type == QG_F32 ? launch<128, float>(p, device, s) : launch<128, __half>(p, device, s);
 }
 
 }  // namespace qg

@@ -88,6 +88,19 @@ def test_long_prompt():
     check(got, q, k, v, lens, 128 ** -0.5, rows=rows)
 
 
+@pytest.mark.parametrize("d,heads,hk,n_seq,most", [(128, 8, 2, 700, 3), (64, 4, 4, 900, 2), (128, 16, 1, 300, 40)])
+def test_many_short_prompts(d, heads, hk, n_seq, most):
+    """More work items than multiprocessors, most of a single tile or less."""
+    rng = np.random.default_rng(36)
+    lens = rng.integers(0, most + 1, n_seq).tolist()
+    q, k, v = inputs(rng, sum(lens), heads, hk, d)
+    off = i32(np.cumsum([0] + lens))
+    got = qg.prompt_attend(q, k, v, off)
+    for _ in range(20):
+        assert torch.equal(got, qg.prompt_attend(q, k, v, off))
+    check(got, q, k, v, lens, d ** -0.5, heads=[0, heads - 1])
+
+
 @pytest.mark.parametrize("q_size,v_size,scale", [(1, 1, -0.3), (1, 1, 0.0), (20, 1, 1.0), (1, 5000.0, 0.09),
                                                  (1, 1e-4, 0.09), (3000, 1, 0.01)])
 def test_sizes_of_values(q_size, v_size, scale):
