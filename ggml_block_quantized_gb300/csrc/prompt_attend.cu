@@ -9,15 +9,16 @@
 // takes over the next one not yet started (cluster launch control) whenever it
 // needs work, and every role runs on into the next item as soon as its own
 // operands allow:
-//  * warp 0, lane 0: TMA producer: query tiles, key tiles and value tiles, the
-//    latter two into a ring each (128-byte swizzle, 64 channels a box).
+//  * warp 0, lane 0: TMA producer: query tiles, and steps: value tile j with key
+//    tile j + 1 (128-byte swizzle, 64 channels a box), in a ring of tiles.
 //  * warp 1: issues the tcgen05.mma. S = Q K^T into 128 tensor-memory columns a
 //    tile, O += P V with P read from tensor memory (f16, over S's columns) and
 //    V as it lies in memory (N-major operand). The order PV_A(j) S_A(j+1)
 //    PV_B(j) S_B(j+1) keeps the two tiles in turn: the tensor cores have one's
 //    products while the other's softmax runs (two issuers of their own fell
-//    into step, softmax with softmax: 524 us at 8192 tokens instead of 371).
-//    P V starts on the first half of P.
+//    into step, softmax with softmax: 524 us at 8192 tokens). A product leaves
+//    the warp only when the one before it is nearly done, so what the warp does
+//    between them is lost to the tensor cores: one wait a step and one a tile.
 //  * warp 2: takes items over, finds their rows and publishes them, up to four
 //    ahead.
 //  * warp 3: looks through the value tiles on the diagonal. The product P V
@@ -48,16 +49,18 @@ namespace {
 
 constexpr int kThreads = 16 * 32;
 constexpr int kItems = 4;  // items known ahead
+constexpr int kSteps = 16;  // barriers of steps: more than the ring can hold (a step has a slot at least)
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr uint32_t kTmemCols = 512;  // S_A, S_B, O_A, O_B at 0, 128, 256, 384
 constexpr float kGrow = 8.0f;        // log2 of how far a row's weights may exceed 1
 
 template <int D> struct Shape {
     static constexpr int kTile = 128 * D * 2;  // bytes of a query, key or value tile
-    static constexpr int kK = D == 128 ? 2 : 5, kV = D == 128 ? 3 : 5;  // key, value tiles in shared memory
-    static constexpr int kTiles = (2 + kK + kV) * kTile;
-    static constexpr int kSmem = kTiles + 640 + 1024;  // tiles, then barriers, items and sums
+    static constexpr int kSlots = D == 128 ? 5 : 10;  // key and value tiles in shared memory
+    static constexpr int kTiles = (2 + kSlots) * kTile;
+    static constexpr int kSmem = kTiles + 768 + 1024;  // tiles, then barriers, items and sums
     static_assert(kSmem <= kSmemLimit, "shared memory");
+    static_assert(kSlots < kSteps, "a barrier for every step in flight");
 };
 
 // tcgen05.mma, kind::f16, f32 accumulators, and its commit, issued where
@@ -345,12 +348,17 @@ __device__ __forceinline__ int asked_block(uint32_t answer) {
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// Place in a ring of N tiles: the tile and its barriers' phase.
-template <int N> struct Ring {
-    uint32_t s, ph;
-    __device__ __forceinline__ Ring next() const {
-        const uint32_t t = s + 1 == N ? 0u : s + 1;
-        return Ring{t, t == 0u ? ph ^ 1u : ph};
+// The steps of a block, in order over its items: step 0 of an item has key tile
+// 0, step j + 1 value tile j and, but for the last, key tile j + 1; a tile takes
+// the next slot of the ring.
+template <int SLOTS> struct Step {
+    uint32_t n = 0, slot = 0;  // steps, slots so far (slot modulo SLOTS)
+    __device__ __forceinline__ uint32_t bar(uint32_t first) const { return first + 8 * (n % kSteps); }
+    __device__ __forceinline__ uint32_t parity() const { return n / kSteps & 1u; }
+    __device__ __forceinline__ uint32_t take() {  // a slot
+        const uint32_t s = slot;
+        slot = s + 1 == SLOTS ? 0u : s + 1;
+        return s;
     }
 };
 
@@ -363,7 +371,7 @@ __device__ __forceinline__ uint32_t odd_half2(uint32_t w) { return ((w & 0x7C007
 // Columns past `see` count as -inf; the warp's rows all see those up to
 // see_all.
 template <int D>
-__device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, uint32_t bar_half, uint32_t bar_all, float c, bool negate,
+__device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, uint32_t bar, float c, bool negate,
                                              bool first, int see, int see_all, float &ref, float2 &sum) {
     uint32_t v[4][32];
 #pragma unroll
@@ -422,11 +430,11 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, uint32_
             w[q] = pack_half2(e.x, e.y);
         }
         tc_st32(s_t + 32 * h, w);
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(h == 0 ? bar_half : bar_all);
     }
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
     sum = fadd2(sum, fadd2(part[0], part[1]));
 }
 
@@ -437,36 +445,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     using Sh = Shape<D>;
     constexpr int kHalves = D / 64;  // boxes of 64 channels
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // (the swizzle's atoms are 1024 bytes)
-    const uint32_t q_a = smem_addr(smem_raw), k_a = q_a + 2 * Sh::kTile, v_a = k_a + Sh::kK * Sh::kTile, base_a = q_a + Sh::kTiles;
+    const uint32_t q_a = smem_addr(smem_raw), ring_a = q_a + 2 * Sh::kTile, base_a = q_a + Sh::kTiles;
     uint8_t *base = smem_raw + Sh::kTiles;
     // barriers, 8 bytes each (those of the two tiles side by side)
-    const uint32_t k_full = base_a, k_empty = k_full + 8 * Sh::kK, v_full = k_empty + 8 * Sh::kK, v_empty = v_full + 8 * Sh::kV;
-    const uint32_t v_ready = v_empty + 8 * Sh::kV, q_full = v_ready + 8 * Sh::kV, q_empty = q_full + 16, s_full = q_empty + 16;
-    const uint32_t p_half = s_full + 16, p_ready = p_half + 16, o_full = p_ready + 16, o_empty = o_full + 16, l_full = o_empty + 16;
-    const uint32_t item_full = l_full + 16, item_empty = item_full + 8 * kItems, mfinal = item_empty + 8 * kItems, block_bar = mfinal + 16;
-    const uint32_t block_answer = base_a + 416;  // 16 bytes
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + 448);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(base + 452);
-    volatile Item *items = reinterpret_cast<volatile Item *>(base + 456);
-    volatile int *odd = reinterpret_cast<volatile int *>(base + 576);       // [item % 8]: diagonal values that are not finite
-    volatile float *sums = reinterpret_cast<volatile float *>(base + 640);  // [tile][row]
+    const uint32_t full = base_a, ready = full + 8 * kSteps, empty = ready + 8 * kSteps, q_full = empty + 8 * kSteps, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, p_ready = s_full + 16, o_full = p_ready + 16, o_empty = o_full + 16, l_full = o_empty + 16;
+    const uint32_t item_full = l_full + 16, item_empty = item_full + 8 * kItems, mfinal = item_empty + 8 * kItems, block_bar = mfinal + 8;
+    const uint32_t block_answer = base_a + 592;  // 16 bytes
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + 608);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(base + 612);
+    volatile Item *items = reinterpret_cast<volatile Item *>(base + 616);
+    volatile int *odd = reinterpret_cast<volatile int *>(base + 728);       // [item % 8]: diagonal values that are not finite
+    volatile float *sums = reinterpret_cast<volatile float *>(base + 768);  // [tile][row]
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < Sh::kK; ++i) {
-            mbar_init(k_full + 8 * i, 1);
-            mbar_init(k_empty + 8 * i, 1);
-        }
-        for (int i = 0; i < Sh::kV; ++i) {
-            mbar_init(v_full + 8 * i, 1);
-            mbar_init(v_empty + 8 * i, 1);
-            mbar_init(v_ready + 8 * i, 1);
+        for (int i = 0; i < kSteps; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(ready + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(q_full + 8 * x, 1);
             mbar_init(q_empty + 8 * x, 1);
             mbar_init(s_full + 8 * x, 1);
-            mbar_init(p_half + 8 * x, 4);
             mbar_init(p_ready + 8 * x, 4);
             mbar_init(o_full + 8 * x, 1);
             mbar_init(o_empty + 8 * x, 4);
@@ -517,10 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fewer_registers<64>();
         if (warp == 0) {
             // ---------------- copies
-            Ring<Sh::kK> rk = {0, 0};
-            Ring<Sh::kV> rv = {0, 0};
-            int n_k = 0;           // key tiles so far, at most the ring's
-            int used[2] = {0, 0};  // query tiles loaded
+            Step<Sh::kSlots> step;
+            uint32_t n_free = 0;       // steps known to be used up
+            int room = Sh::kSlots;     // free slots
+            uint64_t single = 0;       // of the last steps (bit n % 64): only one tile
+            int used[2] = {0, 0};      // query tiles loaded
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 ok = __all_sync(0xffffffffu, wait_item(k));
@@ -532,29 +535,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     const int kv_head = it.head0 / p.group, n = max(it.tiles[0], it.tiles[1]);
                     auto load = [&](uint32_t dst, const CUtensorMap *map, int head, int row, uint32_t bar) {
-                        mbar_arrive_expect_tx(bar, Sh::kTile);
                         for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * (128 * 128), map, 64 * h, head, row, bar);
                     };
-                    for (int j = 0; ok && j < n; ++j) {
-                        // (the rings are the same depth or the keys' shallower: a first round of keys is one of values, too)
-                        if (n_k >= Sh::kK) ok = sleep_wait<40>(k_empty + 8 * rk.s, rk.ph ^ 1u, abort_flag);
+                    for (int j = 0; ok && j <= n; ++j) {
+                        const int tiles = (j > 0) + (j < n);
+                        while (ok && room < tiles) {
+                            ok = sleep_wait<20>(empty + 8 * (n_free % kSteps), n_free / kSteps & 1u, abort_flag);
+                            room += (single >> (n_free % 64)) & 1 ? 1 : 2;
+                            ++n_free;
+                        }
                         if (!ok) break;
-                        load(k_a + rk.s * Sh::kTile, &map_k, kv_head, it.start + j * kTileKeys, k_full + 8 * rk.s);
-                        rk = rk.next();
+                        room -= tiles;
+                        single = (single & ~(1ull << (step.n % 64))) | static_cast<uint64_t>(tiles == 1) << (step.n % 64);
+                        const uint32_t bar = step.bar(full);
+                        mbar_arrive_expect_tx(bar, tiles * Sh::kTile);
+                        if (j > 0) load(ring_a + step.take() * Sh::kTile, &map_v, kv_head, it.start + (j - 1) * kTileKeys, bar);
+                        if (j < n) load(ring_a + step.take() * Sh::kTile, &map_k, kv_head, it.start + j * kTileKeys, bar);
+                        ++step.n;
                         if (j == 0)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {  // the queries, once the last item's are used up
                                 if (!ok || it.tiles[x] == 0) continue;
-                                if (used[x] > 0) ok = sleep_wait<40>(q_empty + 8 * x, (used[x] - 1) & 1, abort_flag);
+                                if (used[x] > 0) ok = sleep_wait<20>(q_empty + 8 * x, (used[x] - 1) & 1, abort_flag);
                                 if (!ok) continue;
                                 ++used[x];
+                                mbar_arrive_expect_tx(q_full + 8 * x, Sh::kTile);
                                 load(q_a + x * Sh::kTile, &map_q, it.head0, it.start + it.tok0 + x * tile_toks, q_full + 8 * x);
                             }
-                        if (ok && n_k >= Sh::kV) ok = sleep_wait<40>(v_empty + 8 * rv.s, rv.ph ^ 1u, abort_flag);
-                        if (!ok) break;
-                        load(v_a + rv.s * Sh::kTile, &map_v, kv_head, it.start + j * kTileKeys, v_full + 8 * rv.s);
-                        rv = rv.next();
-                        if (n_k < 16) ++n_k;
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -562,13 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok && lane == 0) {
                 record_error(p.err, kErrProducerWait);
                 *abort_flag = 1;
-            }
-            // Leave no copy in flight into this block's shared memory. Without an error every tile has been
-            // waited for by those who used it; else each wait here is for a tile's own barrier to turn.
-            if (!ok && lane == 0) {
+                // Leave no copy in flight into this block's shared memory (without an error every copy has been
+                // waited for by those who used it).
                 bool landed = true;
-                for (int i = 0; i < Sh::kK && i < n_k + 1; ++i, rk = rk.next()) landed = mbar_wait_bounded(k_full + 8 * rk.s, rk.ph ^ 1u) && landed;
-                for (int i = 0; i < Sh::kV && i < n_k; ++i, rv = rv.next()) landed = mbar_wait_bounded(v_full + 8 * rv.s, rv.ph ^ 1u) && landed;
+                for (; n_free < step.n; ++n_free) landed = mbar_wait_bounded(full + 8 * (n_free % kSteps), n_free / kSteps & 1u) && landed;
                 for (int x = 0; x < 2; ++x)
                     if (used[x] > 0) landed = mbar_wait_bounded(q_full + 8 * x, (used[x] - 1) & 1) && landed;
                 if (!landed) record_error(p.err, kErrDrainWait);
@@ -611,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         } else if (warp == 3) {
-            // ---------------- value tiles on the diagonal
-            Ring<Sh::kV> rv = {0, 0};
+            // ---------------- steps' arrival, and value tiles on the diagonal
+            Step<Sh::kSlots> step;
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 ok = __all_sync(0xffffffffu, wait_item(k));
@@ -625,28 +629,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (it.last) break;
                 const int n = max(it.tiles[0], it.tiles[1]), masked = first_masked(it);
-                for (int j = 0; j < n; ++j) {
-                    ok = __all_sync(0xffffffffu, sleep_wait<40>(v_full + 8 * rv.s, rv.ph, abort_flag));
+                for (int j = 0; j <= n; ++j) {
+                    ok = __all_sync(0xffffffffu, sleep_wait<20>(step.bar(full), step.parity(), abort_flag));
                     if (!ok) break;
-                    if (j >= masked) {
-                        uint4 *mem = reinterpret_cast<uint4 *>(smem_raw + (2 + Sh::kK + rv.s) * Sh::kTile);
-                        uint32_t bad = 0;
+                    if (j > 0) {
+                        uint4 *mem = reinterpret_cast<uint4 *>(smem_raw + (2 + step.take()) * Sh::kTile);
+                        if (j - 1 >= masked) {
+                            uint32_t bad = 0;
 #pragma unroll 8
-                        for (int q = lane; q < Sh::kTile / 16; q += 32) {
-                            const uint4 w = mem[q];
-                            bad |= odd_half2(w.x) | odd_half2(w.y) | odd_half2(w.z) | odd_half2(w.w);
+                            for (int q = lane; q < Sh::kTile / 16; q += 32) {
+                                const uint4 w = mem[q];
+                                bad |= odd_half2(w.x) | odd_half2(w.y) | odd_half2(w.z) | odd_half2(w.w);
+                            }
+                            if (__any_sync(0xffffffffu, bad != 0)) {
+                                __half *h = reinterpret_cast<__half *>(mem);
+                                for (int q = lane; q < Sh::kTile / 2; q += 32)
+                                    if ((__half_as_ushort(h[q]) & 0x7C00u) == 0x7C00u) h[q] = __ushort_as_half(0);
+                                fence_proxy_async_smem();
+                                if (lane == 0) odd[k % 8] = 1;
+                            }
+                            __syncwarp();
                         }
-                        if (__any_sync(0xffffffffu, bad != 0)) {
-                            __half *h = reinterpret_cast<__half *>(mem);
-                            for (int q = lane; q < Sh::kTile / 2; q += 32)
-                                if ((__half_as_ushort(h[q]) & 0x7C00u) == 0x7C00u) h[q] = __ushort_as_half(0);
-                            fence_proxy_async_smem();
-                            if (lane == 0) odd[k % 8] = 1;
-                        }
-                        __syncwarp();
                     }
-                    if (lane == 0) mbar_arrive(v_ready + 8 * rv.s);
-                    rv = rv.next();
+                    if (j < n) step.take();
+                    if (lane == 0) mbar_arrive(step.bar(ready));
+                    ++step.n;
                 }
             }
             if (!ok) {
@@ -659,12 +666,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // but for branches that are alike in all lanes; what a failed wait leaves is not used.
             const uint32_t issue = lane == 0;
             constexpr uint32_t kIdS = tc_idesc_f16(128, kTileKeys), kIdO = tc_idesc_f16(128, D) | kIdescNMajorB;
-            const uint32_t q_desc = desc_lo(q_a, 1), k_desc = desc_lo(k_a, 1), v_desc = desc_lo(v_a, 128 * 128 / 16);
+            const uint32_t q_desc = desc_lo(q_a, 1), k_desc = desc_lo(ring_a, 1), v_desc = desc_lo(ring_a, 128 * 128 / 16);
             constexpr uint32_t kStep = Sh::kTile / 16;  // from tile to tile in a descriptor
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u))) wait_slow(bar, parity & 1u, abort_flag, p.err);
             };
-            auto there = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)) != 0; };
             struct Work {
                 int t[2], n;     // key tiles of A and B, of the item
                 int steps[2];    // of the last one's keys, in steps of 16
@@ -685,90 +691,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w.last = __shfl_sync(0xffffffffu, it.last | *abort_flag, 0);
                 return w;
             };
-            // S of tile x with key tile j of its item, at r
-            auto product_s = [&](const Work &w, int x, int j, const Ring<Sh::kK> &r) {
-                const uint32_t a = q_desc + x * kStep, b = k_desc + r.s * kStep;
-                const bool final = j + 1 == w.t[x];
-                const uint32_t id = final ? (kIdS & ~(0x3Fu << 17)) | static_cast<uint32_t>(w.steps[x] * 2) << 17 : kIdS;
-                mma_s<D>(issue, tmem + 128 * x, a, b, id, kDescHi);
+            // S of tile x with key tile j of its item, in slot `s`
+            auto product_s = [&](const Work &w, int x, int j, uint32_t s) {
+                const int t = x == 0 ? w.t[0] : w.t[1];
+                const bool final = j + 1 == t;
+                const uint32_t id = final ? (kIdS & ~(0x3Fu << 17)) | static_cast<uint32_t>((x == 0 ? w.steps[0] : w.steps[1]) * 2) << 17 : kIdS;
+                mma_s<D>(issue, tmem + 128 * x, q_desc + x * kStep, k_desc + s * kStep, id, kDescHi);
                 commit(issue, s_full + 8 * x);
                 if (final) commit(issue, q_empty + 8 * x);
             };
-            Ring<Sh::kK> rk = {0, 0};
-            Ring<Sh::kV> rv = {0, 0};
-            uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0}, n_o[2] = {0, 0};  // weight tiles, query tiles, results so far
-            wait(item_full, 0);
-            Work w = take_item(0);
-            bool started = false;  // S of the item's first key tile issued early for tile A
-            for (int k = 0; !w.last; ++k) {
-                wait(k_full + 8 * rk.s, rk.ph);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (w.t[x] == 0 || (x == 0 && started)) continue;
-                    wait(q_full + 8 * x, n_q[x]++);
-                    tc_fence_after();
-                    product_s(w, x, 0, rk);
-                }
-                commit(issue, k_empty + 8 * rk.s);
-                rk = rk.next();
-                Work next;
-                bool known = false;
-                started = false;
-                for (int j = 0; j < w.n; ++j) {
-                    const bool more = j + 1 < w.n;
-                    wait(v_ready + 8 * rv.s, rv.ph);
-                    if (more) wait(k_full + 8 * rk.s, rk.ph);
-#pragma unroll
+            Step<Sh::kSlots> step;
+            uint32_t par_p = 0, par_q = 0, par_o = 3;  // parities of p_ready, q_full and o_empty, by tile
+            uint32_t results = 0;                      // tiles that have had a result
+            for (int k = 0;; ++k) {
+                wait(item_full + 8 * (k % kItems), k / kItems);
+                const Work w = take_item(k);
+                if (w.last) break;
+                wait(step.bar(ready), step.parity());
+                {
+                    const uint32_t s = step.take();
+#pragma unroll 1
                     for (int x = 0; x < 2; ++x) {
-                        if (j < w.t[x]) {
-                            const bool final = j + 1 == w.t[x];
-                            if (j == 0) {
-                                if (n_o[x] > 0) wait(o_empty + 8 * x, n_o[x] - 1);
-                                ++n_o[x];
-                            }
-                            const uint32_t v = v_desc + rv.s * kStep;
-                            const uint32_t o_t = tmem + 256 + 128 * x, p_t = tmem + 128 * x;
-                            wait(p_half + 8 * x, n_p[x]);
-                            tc_fence_after();
-                            if (!final) {
-                                mma_pv(issue, o_t, p_t, v, kIdO, j, kDescHi);
-                                wait(p_ready + 8 * x, n_p[x]);
-                                tc_fence_after();
-                                mma_pv(issue, o_t, p_t + 32, v + 4 * (2048 / 16), kIdO, 1, kDescHi);
-                                product_s(w, x, j + 1, rk);
-                            } else {  // the keys that some row sees
-                                wait(p_ready + 8 * x, n_p[x]);
-                                tc_fence_after();
-                                for (int i = 0; i < w.steps[x]; ++i)
-                                    mma_pv16(issue, o_t, p_t + 8 * i, v + i * (2048 / 16), kIdO, i | j, kDescHi);
-                                commit(issue, o_full + 8 * x);
-                            }
-                            ++n_p[x];
+                        if ((x == 0 ? w.t[0] : w.t[1]) == 0) continue;
+                        wait(q_full + 8 * x, par_q >> x);
+                        par_q ^= 1u << x;
+                        tc_fence_after();
+                        product_s(w, x, 0, s);
+                    }
+                    commit(issue, step.bar(empty));
+                    ++step.n;
+                }
+                for (int j = 0; j < w.n; ++j) {
+                    wait(step.bar(ready), step.parity());
+                    const uint32_t sv = step.take(), sk = j + 1 < w.n ? step.take() : 0;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        const int t = x == 0 ? w.t[0] : w.t[1];
+                        if (j >= t) continue;
+                        const uint32_t v = v_desc + sv * kStep, o_t = tmem + 256 + 128 * x, p_t = tmem + 128 * x;
+                        if (j == 0) {
+                            if (results >> x & 1u) wait(o_empty + 8 * x, par_o >> x);
+                            par_o ^= 1u << x;
+                            results |= 1u << x;
                         }
-                        if (x == 0 && !more && there(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems)) {
-                            // tile A is done: its next item's first S, if the operands are there, before B's last product
-                            next = take_item(k + 1);
-                            known = true;
-                            if (!next.last && next.t[0] > 0 && there(q_full, n_q[0]) && there(k_full + 8 * rk.s, rk.ph)) {
-                                tc_fence_after();
-                                ++n_q[0];
-                                product_s(next, 0, 0, rk);
-                                started = true;
-                            }
+                        wait(p_ready + 8 * x, par_p >> x);
+                        par_p ^= 1u << x;
+                        tc_fence_after();
+                        if (j + 1 < t) {
+                            mma_pv(issue, o_t, p_t, v, kIdO, j, kDescHi);
+                            mma_pv(issue, o_t, p_t + 32, v + 4 * (2048 / 16), kIdO, 1, kDescHi);
+                            product_s(w, x, j + 1, sk);
+                        } else {  // the keys that some row sees
+                            const int steps = x == 0 ? w.steps[0] : w.steps[1];
+                            for (int i = 0; i < steps; ++i)
+                                mma_pv16(issue, o_t, p_t + 8 * i, v + i * (2048 / 16), kIdO, i | j, kDescHi);
+                            commit(issue, o_full + 8 * x);
                         }
                     }
-                    commit(issue, v_empty + 8 * rv.s);
-                    rv = rv.next();
-                    if (more) {
-                        commit(issue, k_empty + 8 * rk.s);
-                        rk = rk.next();
-                    }
+                    commit(issue, step.bar(empty));
+                    ++step.n;
                 }
-                if (!known) {
-                    wait(item_full + 8 * ((k + 1) % kItems), (k + 1) / kItems);
-                    next = take_item(k + 1);
-                }
-                w = next;
             }
             commit(issue, mfinal);  // every mma complete before tensor memory is freed
             wait(mfinal, 0);
@@ -802,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // the last column that the warp's first row sees
                 const int see_all = first_tok + (row & ~31) / pack - j * kTileKeys;
-                softmax_tile<D>(s_t, o_t, p_half + 8 * x, p_ready + 8 * x, c, negate, j == 0, tok - j * kTileKeys, see_all, ref, sum);
+                softmax_tile<D>(s_t, o_t, p_ready + 8 * x, c, negate, j == 0, tok - j * kTileKeys, see_all, ref, sum);
             }
             if (!ok) break;
             // the storing warps must have taken the item before (one of a single tile can be through here
