@@ -249,22 +249,20 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, cons
 // d = a b + c
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1, const uint4 &c) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(__uint_as_float(c.x)), "f"(__uint_as_float(c.y)),
           "f"(__uint_as_float(c.z)), "f"(__uint_as_float(c.w)));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -286,25 +284,26 @@ __device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t magic) {
 __device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t magic) {
     return hfma2((w & 0x00F000F0u) | magic, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 c) / 16 - 72
 }
-template <int NB> __device__ __forceinline__ void ld_words(uint32_t a, uint32_t (&w)[NB]) {
+// Loads from the tile (plain ones, which the compiler may move among the
+// products but not over the waits).
+template <int NB> __device__ __forceinline__ void ld_words(const uint8_t *p, uint32_t (&w)[NB]) {
     if (NB == 4) {
-        const uint4 v = ld_s128(a);
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
         w[0] = v.x, w[1] = v.y, w[NB - 2] = v.z, w[NB - 1] = v.w;
     } else {
-        const uint2 v = ld_s64(a);
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
         w[0] = v.x, w[1] = v.y;
     }
 }
 // NB f16 (one row's scales, or one value unit of every block) as NB/2 words.
-template <int NB> __device__ __forceinline__ void ld_halves(uint32_t a, uint32_t (&w)[NB / 2]) {
+template <int NB> __device__ __forceinline__ void ld_halves(const uint8_t *p, uint32_t (&w)[NB / 2]) {
     if (NB == 4) {
-        const uint2 v = ld_s64(a);
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
         w[0] = v.x, w[NB / 2 - 1] = v.y;
     } else {
-        w[0] = ld_s32(a);
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
     }
 }
-
 __device__ __forceinline__ bool not_finite(uint32_t half_bits) { return (half_bits & 0x7C00u) == 0x7C00u; }
 
 // The largest magnitudes among a row's scales (halves apart; NaN has no say),
@@ -336,6 +335,23 @@ template <> __device__ __forceinline__ void load_q8<__half>(uint32_t a, float (&
 __device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
 __device__ __forceinline__ void store2(__half *p, float a, float b) { *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b); }
 
+// Whether a row that sees the tokens up to `limit` sees, among those from
+// `least` on within the part's tokens first .. past - 1, one whose value scale
+// of block b is not finite. Such a token is left out of the products where
+// some rows do not see it (0 times its scale would be NaN); the rows that do
+// get NaN in the block's channels here.
+template <int D> __device__ __noinline__ bool odd_tokens(const KvAttendParams &p, const Walk &seg, int least, int limit, int first, int past, int b) {
+    using G = KvGroup<D>;
+    if (past > limit) past = limit;
+    for (int tok = max(first, least); tok < past; ++tok) {
+        const int page = p.table[seg.seq * p.table_stride + tok / p.c.page_size], r = tok % p.c.page_size;
+        if (page < 0 || page >= p.c.n_pages) continue;
+        const uint8_t *g = p.c.data + ((static_cast<int64_t>(page) * p.c.n_heads + seg.head) * p.c.page_groups + (r >> 4)) * G::kBytes;
+        if (not_finite(reinterpret_cast<const unsigned short *>(g + G::kVS + (r & 15) * G::kScaleRow)[b])) return true;
+    }
+    return false;
+}
+
 template <int D, class T, int NT>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1)>::kCtas)
     kv_attend_kernel(const KvAttendParams p) {
@@ -348,6 +364,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     volatile int *slot_info = reinterpret_cast<volatile int *>(smem + 16 * Sh::kSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots);
     const uint32_t qfull = base + 20 * Sh::kSlots + 16, qempty = qfull + 8;
+    __shared__ Walk walks[kWarps];
+    volatile int *const odd_flag = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Sh::kSlots; ++s) {
@@ -463,26 +481,32 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     int *row_limit = reinterpret_cast<int *>(smem + Sh::kOffRow) + ROWS;
     float *stat = reinterpret_cast<float *>(smem + Sh::kOffStat);
     float *join = reinterpret_cast<float *>(smem + Sh::kOffJoin);
-    int64_t k = warp;        // this warp's next tile of the part
-    int64_t seg_k = 0;       // the part's tiles before this segment
+    // The walk lies in shared memory, a copy a warp: in registers it cost the loop over the tiles a dozen, which
+    // were spilled there.
+    Walk &seg = walks[warp];
+    if (lane == 0) seg = walk;
+    __syncwarp();
+    int k = warp;      // this warp's next tile, counted from the segment's first one in the part
     int slot = warp;
-    uint32_t phase = 0;
+    uint32_t phase = 0, phase_q = 0;
     bool ok = true;
-    for (int seg = 0; walk.left > 0; walk.next(p, ROWS), ++seg) {
-        const int n = walk.n_tiles(), tile0 = walk.first_tile();
+    while (seg.left > 0) {
+        const int n = seg.n_tiles(), tile0 = seg.first_tile();
         // ---- the segment's queries, as the mma's B fragments
-        if (ok && !__all_sync(0xffffffffu, wait_bounded(qfull, seg & 1, abort_flag))) {
+        if (ok && !__all_sync(0xffffffffu, wait_bounded(qfull, phase_q, abort_flag))) {
             if (lane == 0) record_error(p.err, kErrConsumerWait);
             *abort_flag = 1;
             ok = false;
         }
+        phase_q ^= 1u;
         {
             const uint32_t raw = base + Sh::kOffRaw;
+            const int rows = seg.q.m * p.group, row0 = seg.rt * ROWS, before = seg.q.len - seg.q.m + 1;
             constexpr int kItems = ROWS * NB * 4;
             for (int it = threadIdx.x; it < kItems; it += kWarps * 32) {
                 const int r = it / (NB * 4), b = it / 4 % NB, ti = it & 3;
-                const int row = walk.rt * ROWS + r;
-                const bool live = row < walk.q.m * p.group;
+                const int row = row0 + r;
+                const bool live = row < rows;
                 float x[8] = {};
                 if (live) load_q8<T>(raw + r * Sh::kRawRow + (32 * b + 4 * ti) * static_cast<int>(sizeof(T)), x);
                 float big = 0.0f;
@@ -530,13 +554,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         row_factor[r] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * (TERMS == 1 ? 0x1p10f : 0x1p-10f) *
                                                   __uint_as_float(static_cast<uint32_t>(e + 127) << 23),
                                               1e-37f);
-                        row_limit[r] = live ? walk.q.len - walk.q.m + row / p.group + 1 : 0;
+                        row_limit[r] = live ? before + row / p.group : 0;
                     }
                 }
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(qempty);
+        if (threadIdx.x == 0) *odd_flag = 0;
         named_barrier(1, kWarps * 32);
         float factor[NT][2];
         // the first row sees least (rows past the last have no say: their result is not stored)
@@ -560,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                     for (int i = 0; i < 4; ++i) o[nt][b][h][i] = 0.0f;
         }
 
-        for (; k < seg_k + n; k += kWarps) {
+        for (; k < n; k += kWarps) {
             if (!ok) continue;
             ok = __all_sync(0xffffffffu, wait_bounded(full0 + 8 * slot, phase, abort_flag));
             if (!ok) {
@@ -569,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 continue;
             }
             {
-                const uint32_t tile_a = base + Sh::kOffRing + slot * Sh::kTileBytes;
-                const int tok0 = (tile0 + static_cast<int>(k - seg_k)) * kTile;
+                const uint8_t *const tile_p = smem + Sh::kOffRing + slot * Sh::kTileBytes;
+                const int tok0 = (tile0 + k) * kTile;
                 const int info = slot_info[slot];
                 // ---- scores of 2 x 16 tokens: s[group][nt][0, 1: token g; 2, 3: token g + 8]
                 float s[2][NT][4];
@@ -581,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                     for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t ga = tile_a + gr * G::kBytes;
+                            const uint8_t *const ga = tile_p + gr * G::kBytes;
                             ld_words<NB>(ga + (g + 8 * h) * G::kRow + t * (4 * NB), w[gr][h]);
                             ld_halves<NB>(ga + G::kKS + (g + 8 * h) * G::kScaleRow, dk[gr][h]);
                             ld_halves<NB>(ga + G::kVS + (g + 8 * h) * G::kScaleRow, dv[gr][h]);
@@ -607,12 +632,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                             }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const uint4 ini = TERMS == 1 ? ld_s128(base + Sh::kOffInit + (nt * NB + b) * 64 + t * 16)
+                            const uint4 ini = TERMS == 1 ? *reinterpret_cast<const uint4 *>(smem + Sh::kOffInit + (nt * NB + b) * 64 + t * 16)
                                                          : make_uint4(0u, 0u, 0u, 0u);
                             float acc[2][4];
 #pragma unroll
                             for (int q = 0; q < TERMS; ++q) {
-                                const uint4 bq = ld_s128(base + Sh::kOffQ + ((q * NT + nt) * NB + b) * 512 + lane * 16);
+                                const uint4 bq = *reinterpret_cast<const uint4 *>(smem + Sh::kOffQ + ((q * NT + nt) * NB + b) * 512 + lane * 16);
 #pragma unroll
                                 for (int gr = 0; gr < 2; ++gr) {
                                     if (q == 0)
@@ -631,11 +656,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         }
                     }
                 }
-                bool odd = false;  // a value scale that is not finite, of a token that some rows do not see
                 const bool masked = tok0 + kTile > least || info != 3;
                 if (masked) {
                     // tokens that a row does not see, or that lie in no page: whatever
                     // the ring holds there (it may be NaN) is replaced
+                    const int len = seg.q.len;
+                    bool odd = false;
 #pragma unroll
                     for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
@@ -644,8 +670,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                             const bool in_page = (info >> gr) & 1;
 #pragma unroll
                             for (int i = 0; i < NB / 2; ++i) {
-                                if (!in_page || tok >= walk.q.len) dv[gr][h][i] = 0;
-                                odd = odd || not_finite(dv[gr][h][i]) || not_finite(dv[gr][h][i] >> 16);
+                                if (!in_page || tok >= len) dv[gr][h][i] = 0;
+                                // a scale that is not finite, of a token that only some rows see: see `odd_tokens`
+                                if (tok >= least && not_finite(dv[gr][h][i])) odd = true, dv[gr][h][i] &= 0xFFFF0000u;
+                                if (tok >= least && not_finite(dv[gr][h][i] >> 16)) odd = true, dv[gr][h][i] &= 0x0000FFFFu;
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
@@ -653,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                                 for (int c = 0; c < 2; ++c)
                                     if (!in_page || tok >= row_limit[8 * nt + 2 * t + c]) s[gr][nt][2 * h + c] = -INFINITY;
                         }
-                    odd = __any_sync(0xffffffffu, odd);
+                    if (odd) *odd_flag = 1;
                 }
                 // ---- the lane's largest score plus exponent, by column
                 float top[NT][2];
@@ -720,32 +748,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) o[nt][b][h][i] *= keep[nt][i & 1];
                 }
-                if (odd) {
-                    // a value scale that is not finite: the block's channels become NaN for the rows
-                    // that give its token a weight, and no other row's product meets it
-#pragma unroll
-                    for (int gr = 0; gr < 2; ++gr)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                const bool bad = not_finite(dv[gr][h][b / 2] >> (16 * (b & 1)));
-                                if (bad) dv[gr][h][b / 2] &= b & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c) {
-                                        int hit = bad && s[gr][nt][2 * h + c] != 0.0f;
-#pragma unroll
-                                        for (int q = 4; q < 32; q <<= 1) hit |= __shfl_xor_sync(0xffffffffu, hit, q);
-                                        if (hit) o[nt][b][0][c] = o[nt][b][0][2 + c] = o[nt][b][1][c] = o[nt][b][1][2 + c] = NAN;
-                                    }
-                            }
-                }
                 // ---- values
 #pragma unroll
                 for (int gr = 0; gr < 2; ++gr) {
-                    const uint32_t va = tile_a + gr * G::kBytes + G::kV;
+                    const uint8_t *const va = tile_p + gr * G::kBytes + G::kV;
                     uint32_t v[4][NB / 2];  // unit g of every block, tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -786,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             slot += kWarps;
             if (slot >= Sh::kSlots) slot -= Sh::kSlots, phase ^= 1u;
         }
-        seg_k += n;
+        k -= n;
 
         // ---- the warps' results become one
 #pragma unroll
@@ -798,13 +804,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 if (g == 0)
                     *reinterpret_cast<float2 *>(stat + (warp * ROWS + 8 * nt + 2 * t + c) * 2) = make_float2(m[nt][c], l[nt][c]);
             }
-        const bool whole = walk.tile == 0 && walk.count() == walk.tiles;
+        const bool whole = seg.tile == 0 && seg.count() == seg.tiles;
         // a part's result: slot 0 if it enters the segment from outside, slot 1 if the segment starts in it
-        float *part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (walk.tile == 0 ? 1 : 0)) * part_floats(D, ROWS);
-        if (!whole && walk.tile == 0 && threadIdx.x == 0) {  // (thread 0 wrote the 0 above)
-            const int row0 = walk.rt * ROWS;
-            *cut = Cut{1 + static_cast<int>((walk.tiles - walk.count() + place.share - 1) / place.share),
-                       min(ROWS, walk.q.m * p.group - row0), row0, walk.q.q0, walk.head, {0, 0, 0}};
+        float *part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (seg.tile == 0 ? 1 : 0)) * part_floats(D, ROWS);
+        if (!whole && seg.tile == 0 && threadIdx.x == 0) {  // (thread 0 wrote the 0 above)
+            const int row0 = seg.rt * ROWS;
+            *cut = Cut{1 + static_cast<int>((seg.tiles - seg.count() + place.share - 1) / place.share),
+                       min(ROWS, seg.q.m * p.group - row0), row0, seg.q.q0, seg.head, {0, 0, 0}};
         }
 #pragma unroll
         for (int b0 = 0; b0 < NB; b0 += Sh::kChunkBlocks) {
@@ -823,8 +829,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             named_barrier(1, kWarps * 32);
             constexpr int kPairs = 16 * Sh::kChunkBlocks;  // channel pairs of a row in this chunk
             for (int it = threadIdx.x; it < ROWS * kPairs; it += kWarps * 32) {
-                const int r = it / kPairs, c2 = 2 * (it % kPairs), row = walk.rt * ROWS + r;
-                if (row >= walk.q.m * p.group) continue;
+                const int r = it / kPairs, c2 = 2 * (it % kPairs), row = seg.rt * ROWS + r;
+                if (row >= seg.q.m * p.group) continue;
                 float2 ml[kWarps];
                 float top = -INFINITY, den = 0.0f;
 #pragma unroll
@@ -842,11 +848,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                     sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y);
                 }
                 const int d = 32 * b0 + c2;
+                if (*odd_flag && odd_tokens<D>(p, seg, row_limit[0], row_limit[r], tile0 * kTile, (tile0 + n) * kTile, d >> 5))
+                    sum.x = sum.y = NAN;
                 if (whole) {
                     const int tok = row / p.group;
                     const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
                     store2(static_cast<T *>(p.out) +
-                               (static_cast<int64_t>(walk.q.q0 + tok) * p.n_heads + walk.head * p.group + row - tok * p.group) * D + d,
+                               (static_cast<int64_t>(seg.q.q0 + tok) * p.n_heads + seg.head * p.group + row - tok * p.group) * D + d,
                            sum.x * inv, sum.y * inv);
                 } else {
                     store2(part + static_cast<int64_t>(r) * D + d, sum.x, sum.y);
@@ -855,6 +863,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             }
         }
         // the next segment's first barrier comes after these reads; the join's areas are written after it
+        __syncwarp();
+        if (lane == 0) seg.next(p, ROWS);
+        __syncwarp();
     }
 }
 
