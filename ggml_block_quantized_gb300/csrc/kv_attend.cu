@@ -59,18 +59,17 @@ constexpr int kMaxCtas = 640;              // thread blocks of a launch (workspa
 template <int D, int NT, int TERMS> struct Shape {
     using G = KvGroup<D>;
     static constexpr int kTileBytes = 2 * G::kBytes;
-    static constexpr int kSlots = D == 128 ? 12 : 24;
+    static constexpr int kSlots = D == 128 ? 8 : 16;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kChunkBlocks = NT == 4 ? 1 : 2;  // blocks of 32 channels joined at a time
     static constexpr int kRawRow = D * (TERMS == 2 ? 4 : 2);                   // bytes of a query row
     static constexpr int kOffRing = 1024;
     static constexpr int kOffRaw = kOffRing + kSlots * kTileBytes;             // a segment's query rows
     static constexpr int kOffQ = kOffRaw + kRows * kRawRow;                    // [term][nt][block][lane] 16 bytes
     static constexpr int kOffInit = kOffQ + TERMS * NT * G::kNB * 512;         // [nt][block][4 pairs of columns, twice] f32
-    static constexpr int kOffRow = kOffInit + NT * G::kNB * 64;                // factor f32, limit int [rows]
-    static constexpr int kOffStat = kOffRow + kRows * 8;                       // [warp][rows] reference, sum
-    static constexpr int kOffJoin = kOffStat + kWarps * kRows * 8;             // [warp][rows][32 kChunkBlocks + 2]
-    static constexpr int kJoinPitch = 32 * kChunkBlocks + 2;
+    static constexpr int kOffRow = kOffInit + NT * G::kNB * 64;                // factor f32, limit and place in out int [rows]
+    static constexpr int kOffStat = kOffRow + kRows * 16;                      // [row][warp] reference, sum
+    static constexpr int kJoinPitch = D + 4;
+    static constexpr int kOffJoin = kOffStat + kWarps * kRows * 8;             // [warp][rows][kJoinPitch]
     static constexpr int kSmem = kOffJoin + kWarps * kRows * kJoinPitch * 4;
     static constexpr int kCtas = NT == 1 ? 3 : (NT == 2 ? 2 : 1);              // resident blocks a multiprocessor
 };
@@ -479,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     const uint32_t magic = 0x64006400u | (static_cast<uint32_t>(p.n_tok) >> 31);
     float *row_factor = reinterpret_cast<float *>(smem + Sh::kOffRow);
     int *row_limit = reinterpret_cast<int *>(smem + Sh::kOffRow) + ROWS;
+    int *row_out = row_limit + ROWS;  // the row's place in out, in heads; -1: none
     float *stat = reinterpret_cast<float *>(smem + Sh::kOffStat);
     float *join = reinterpret_cast<float *>(smem + Sh::kOffJoin);
     // The walk lies in shared memory, a copy a warp: in registers it cost the loop over the tiles a dozen, which
@@ -554,7 +554,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         row_factor[r] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * (TERMS == 1 ? 0x1p10f : 0x1p-10f) *
                                                   __uint_as_float(static_cast<uint32_t>(e + 127) << 23),
                                               1e-37f);
-                        row_limit[r] = live ? before + row / p.group : 0;
+                        const int tok = row / p.group;
+                        row_limit[r] = live ? before + tok : 0;
+                        row_out[r] = live ? (seg.q.q0 + tok) * p.n_heads + seg.head * p.group + row - tok * p.group : -1;
                     }
                 }
             }
@@ -792,77 +794,80 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             slot += kWarps;
             if (slot >= Sh::kSlots) slot -= Sh::kSlots, phase ^= 1u;
         }
-        k -= n;
-
         // ---- the warps' results become one
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                const int r = 8 * nt + 2 * t + c;
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], q);
-                if (g == 0)
-                    *reinterpret_cast<float2 *>(stat + (warp * ROWS + 8 * nt + 2 * t + c) * 2) = make_float2(m[nt][c], l[nt][c]);
-            }
-        const bool whole = seg.tile == 0 && seg.count() == seg.tiles;
-        // a part's result: slot 0 if it enters the segment from outside, slot 1 if the segment starts in it
-        float *part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (seg.tile == 0 ? 1 : 0)) * part_floats(D, ROWS);
-        if (!whole && seg.tile == 0 && threadIdx.x == 0) {  // (thread 0 wrote the 0 above)
-            const int row0 = seg.rt * ROWS;
-            *cut = Cut{1 + static_cast<int>((seg.tiles - seg.count() + place.share - 1) / place.share),
-                       min(ROWS, seg.q.m * p.group - row0), row0, seg.q.q0, seg.head, {0, 0, 0}};
-        }
+                if (g == 0) *reinterpret_cast<float2 *>(stat + (r * kWarps + warp) * 2) = make_float2(m[nt][c], l[nt][c]);
+                float *dst = join + (warp * ROWS + r) * Sh::kJoinPitch + 2 * g;
 #pragma unroll
-        for (int b0 = 0; b0 < NB; b0 += Sh::kChunkBlocks) {
-            if (b0 != 0) named_barrier(1, kWarps * 32);  // the chunk before has been read
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int b = b0; b < b0 + Sh::kChunkBlocks; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            *reinterpret_cast<float2 *>(join + (warp * ROWS + 8 * nt + 2 * t + c) * Sh::kJoinPitch +
-                                                        32 * (b - b0) + 16 * h + 2 * g) =
-                                make_float2(o[nt][b][h][c], o[nt][b][h][2 + c]);
-            named_barrier(1, kWarps * 32);
-            constexpr int kPairs = 16 * Sh::kChunkBlocks;  // channel pairs of a row in this chunk
-            for (int it = threadIdx.x; it < ROWS * kPairs; it += kWarps * 32) {
-                const int r = it / kPairs, c2 = 2 * (it % kPairs), row = seg.rt * ROWS + r;
-                if (row >= seg.q.m * p.group) continue;
+                        *reinterpret_cast<float2 *>(dst + 32 * b + 16 * h) = make_float2(o[nt][b][h][c], o[nt][b][h][2 + c]);
+            }
+        const int units = seg.count();
+        const bool from = seg.tile == 0, whole = from && units == seg.tiles;
+        named_barrier(1, kWarps * 32);
+        {
+            // a row's channels by 16 / NT threads, four at a time
+            constexpr int kPer = 16 / NT;
+            const int r = threadIdx.x / kPer, out_row = row_out[r];
+            if (out_row >= 0) {
                 float2 ml[kWarps];
                 float top = -INFINITY, den = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    ml[w] = *reinterpret_cast<const float2 *>(stat + (w * ROWS + r) * 2);
-                    top = fmaxf(top, ml[w].x);
+                for (int w = 0; w < kWarps; w += 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(stat + (r * kWarps + w) * 2);
+                    ml[w] = make_float2(v.x, v.y), ml[w + 1] = make_float2(v.z, v.w);
                 }
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w].x);
                 const float ref = top == -INFINITY ? 0.0f : top;
-                float2 sum = make_float2(0.0f, 0.0f);
+                float f[kWarps];
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float2 v = *reinterpret_cast<const float2 *>(join + (w * ROWS + r) * Sh::kJoinPitch + c2);
-                    const float f = exp2_approx(ml[w].x - ref);
-                    den = fmaf(ml[w].y, f, den);
-                    sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y);
+                    f[w] = exp2_approx(ml[w].x - ref);
+                    den = fmaf(ml[w].y, f[w], den);
                 }
-                const int d = 32 * b0 + c2;
-                if (*odd_flag && odd_tokens<D>(p, seg, row_limit[0], row_limit[r], tile0 * kTile, (tile0 + n) * kTile, d >> 5))
-                    sum.x = sum.y = NAN;
-                if (whole) {
-                    const int tok = row / p.group;
-                    const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
-                    store2(static_cast<T *>(p.out) +
-                               (static_cast<int64_t>(seg.q.q0 + tok) * p.n_heads + seg.head * p.group + row - tok * p.group) * D + d,
-                           sum.x * inv, sum.y * inv);
-                } else {
-                    store2(part + static_cast<int64_t>(r) * D + d, sum.x, sum.y);
-                    if (d == 0) store2(part + static_cast<int64_t>(ROWS) * D + 2 * r, top, den);
+                // a part's result: slot 0 if it enters the segment from outside, slot 1 if the segment starts in it
+                float *part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (from ? 1 : 0)) * part_floats(D, ROWS);
+                const float inv = !whole ? 1.0f : den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
+                T *out = static_cast<T *>(p.out) + static_cast<int64_t>(out_row) * D;
+                const bool odd = *odd_flag != 0;
+#pragma unroll
+                for (int d0 = 0; d0 < D; d0 += 4 * kPer) {
+                    const int d = d0 + 4 * (threadIdx.x % kPer);
+                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float4 v = *reinterpret_cast<const float4 *>(join + (w * ROWS + r) * Sh::kJoinPitch + d);
+                        sum.x = fmaf(v.x, f[w], sum.x), sum.y = fmaf(v.y, f[w], sum.y);
+                        sum.z = fmaf(v.z, f[w], sum.z), sum.w = fmaf(v.w, f[w], sum.w);
+                    }
+                    if (odd && odd_tokens<D>(p, seg, row_limit[0], row_limit[r], tile0 * kTile, (tile0 + n) * kTile, d >> 5))
+                        sum.x = sum.y = sum.z = sum.w = NAN;
+                    if (whole) {
+                        store2(out + d, sum.x * inv, sum.y * inv);
+                        store2(out + d + 2, sum.z * inv, sum.w * inv);
+                    } else {
+                        *reinterpret_cast<float4 *>(part + r * D + d) = sum;
+                    }
                 }
+                if (!whole && threadIdx.x % kPer == 0) store2(part + ROWS * D + 2 * r, top, den);
+            }
+            if (!whole && from && threadIdx.x == 0) {  // (thread 0 wrote the 0 above)
+                const int row0 = seg.rt * ROWS;
+                *cut = Cut{1 + static_cast<int>((seg.tiles - units + place.share - 1) / place.share),
+                           min(ROWS, seg.q.m * p.group - row0), row0, seg.q.q0, seg.head, {0, 0, 0}};
             }
         }
         // the next segment's first barrier comes after these reads; the join's areas are written after it
+        k -= n;
         __syncwarp();
         if (lane == 0) seg.next(p, ROWS);
         __syncwarp();
