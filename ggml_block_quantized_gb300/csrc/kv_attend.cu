@@ -34,10 +34,12 @@
 //  * values: B = weight x value scale per token and block (the scale varies
 //    along the summed axis), transposed among lanes with movmatrix. The
 //    softmax's running reference is not the largest score but the largest score
-//    plus the exponent of its token's largest value scale, less 29: every
-//    product is then below 2^15 and a row's largest near it, whatever the
-//    values' size. Weights, their sum and the accumulators share that
-//    reference, so it cancels.
+//    plus the exponent field of its token's largest value scale, less 21, and is
+//    raised only when that sum passes it by 29: every product is then below 2^15
+//    and a row's largest above 2^6, whatever the values' size. Weights, their
+//    sum and the accumulators share that reference, so it cancels. (Raised for
+//    every larger score, with a maximum over the lanes each tile, 131071 tokens
+//    took 50.1 us instead of 48.0.)
 // So codes enter exactly and only q and the weights are rounded: f16 queries
 // are exact and the weights take one f16 (2^-11 relative); for f32 both are
 // split in two f16 parts and each product is formed twice.
@@ -54,6 +56,7 @@ constexpr int kWarps = 4;                  // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = 32;                  // tokens of a tile
 constexpr int kStart = 3;                  // units of the list that a segment's start counts for
+constexpr float kLow = 21.0f, kHigh = 29.0f;  // of the softmax's running reference, above
 constexpr int kMaxCtas = 640;              // thread blocks of a launch (workspace is sized for them)
 
 template <int D, int NT, int TERMS> struct Shape {
@@ -713,43 +716,42 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                                     top[nt][c] = fmaxf(top[nt][c], fmaf(s[gr][nt][2 * h + c], factor[nt][c], ex));
                         }
                 }
-                // ---- running reference, weights
-                float keep[NT][2];
-                bool same = true;
+                // ---- running reference (raised when a product could pass 2^15), weights
+                bool grow = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) grow = grow || top[nt][0] - kHigh > m[nt][0] || top[nt][1] - kHigh > m[nt][1];
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float mx = top[nt][c];
+#pragma unroll
+                            for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+                            mx = fmaxf(m[nt][c], mx - kLow);
+                            const float keep = exp2_approx(m[nt][c] - (mx == -INFINITY ? 0.0f : mx));
+                            m[nt][c] = mx;
+                            l[nt][c] *= keep;
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) o[nt][b][h][c] *= keep, o[nt][b][h][2 + c] *= keep;
+                        }
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float f = factor[nt][c];
-                        float mx = top[nt][c];
-#pragma unroll
-                        for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
-                        mx = fmaxf(m[nt][c], mx - 29.0f);
-                        const float ref = mx == -INFINITY ? 0.0f : mx;
-                        keep[nt][c] = exp2_approx(m[nt][c] - ref);
-                        same = same && mx == m[nt][c];
-                        m[nt][c] = mx;
-                        float sum = 0.0f;
+                        const float ref = m[nt][c] == -INFINITY ? 0.0f : m[nt][c];
 #pragma unroll
                         for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const float w = exp2_approx(fmaf(s[gr][nt][2 * h + c], f, -ref));
+                                const float w = exp2_approx(fmaf(s[gr][nt][2 * h + c], factor[nt][c], -ref));
                                 s[gr][nt][2 * h + c] = w;
-                                sum += w;
+                                l[nt][c] += w;
                             }
-                        l[nt][c] = fmaf(l[nt][c], keep[nt][c], sum);
                     }
-                if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int b = 0; b < NB; ++b)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) o[nt][b][h][i] *= keep[nt][i & 1];
-                }
                 // ---- values
 #pragma unroll
                 for (int gr = 0; gr < 2; ++gr) {
