@@ -99,7 +99,7 @@ int qkv_read(const qkv_cache *cache, const int32_t *slots, int64_t n, float *k_o
     KvCacheView c;
     int st = check_cache(cache, &c);
     if (st != QG_OK) return st;
-    if (n < 0 || n > (1 << 30)) return QG_ERR_SHAPE;
+    if (n < 0 || n > (1 << 30) || n * c.n_heads > (1 << 30)) return QG_ERR_SHAPE;
     if (n == 0 || (!k_out && !v_out)) return QG_OK;
     if (!slots || (!cache->data && cache->n_pages > 0)) return QG_ERR_NULL;
     if (!aligned16(cache->data) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(slots)) return QG_ERR_ALIGN;

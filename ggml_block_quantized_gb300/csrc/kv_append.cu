@@ -9,34 +9,49 @@
 // butterfly steps among its eight lanes, and the four lanes with elements 0..15
 // of a block take the codes of 16..31 by one shuffle and own one 4-byte code
 // word each.
+#include <algorithm>
+
 #include "kv_cache.cuh"
 #include "quant_codes.cuh"
 
 namespace qg {
 
-template <class T> __device__ __forceinline__ void load4(const T *p, float (&x)[4]);
-template <> __device__ __forceinline__ void load4<float>(const float *p, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+// Four elements of a row as they lie in memory.
+template <class T> struct Four;
+template <> struct Four<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p, bool there) {
+        v = there ? *reinterpret_cast<const float4 *>(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = make_float2(v.x, v.y), x[1] = make_float2(v.z, v.w); }
+    __device__ __forceinline__ Four from(int lane) const {
+        return {make_float4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
+                            __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane))};
+    }
+};
+template <> struct Four<__half> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __half *p, bool there) {
+        v = there ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0u, 0u);
+    }
+    __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = unpack_half2(v.x), x[1] = unpack_half2(v.y); }
+    __device__ __forceinline__ Four from(int lane) const {
+        return {make_uint2(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane))};
+    }
+};
+__device__ __forceinline__ void store4(float *p, const float2 (&x)[2]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
 }
-template <> __device__ __forceinline__ void load4<__half>(const __half *p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    x[0] = f16_bits_to_f32(v.x), x[1] = f16_bits_to_f32(v.x >> 16);
-    x[2] = f16_bits_to_f32(v.y), x[3] = f16_bits_to_f32(v.y >> 16);
-}
-__device__ __forceinline__ void store4(float *p, const float (&x)[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void store4(__half *p, const float (&x)[4]) {
-    const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+__device__ __forceinline__ void store4(__half *p, const float2 (&x)[2]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_half2(x[0].x, x[0].y), pack_half2(x[1].x, x[1].y));
 }
 
 // The signed maximum of a block (eight neighbouring lanes, four elements
 // each): the first element of strictly largest magnitude, NaN never (the
-// quantizer's rule), +0 for a block of zeros.
-__device__ __forceinline__ float block_signed_max(const float (&x)[4], int sub) {
+// quantizer's rule), 0 for a block of zeros. From the block's largest and its
+// smallest element; only where both have the same size does the order decide.
+__device__ __noinline__ float first_of_largest(const float2 (&x2)[2], int sub) {
+    const float x[4] = {x2[0].x, x2[0].y, x2[1].x, x2[1].y};
     float best = -1.0f, val = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -49,170 +64,235 @@ __device__ __forceinline__ float block_signed_max(const float (&x)[4], int sub) 
     }
     return best > 0.0f ? val : 0.0f;
 }
+__device__ __forceinline__ float signed_max(const float2 (&x)[2], int sub) {
+    float hi = fmaxf(fmaxf(fmaxf(0.0f, x[0].x), x[0].y), fmaxf(x[1].x, x[1].y));
+    float lo = fminf(fminf(fminf(0.0f, x[0].x), x[0].y), fminf(x[1].x, x[1].y));
+#pragma unroll
+    for (int m = 1; m <= 4; m <<= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+    }
+    if (__any_sync(0xffffffffu, hi == -lo && hi > 0.0f)) return first_of_largest(x, sub);
+    return hi > -lo ? hi : hi < -lo ? lo : 0.0f;
+}
 
-template <int D, class TI, class TO>
+// Two products, each rounded by itself. (Packed products followed by a packed
+// sum come out of the compiler as one fused operation, even with .rn on both.)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
+}
+
+// A warp takes ROWS x (32 / kLanes) rows of one token and one kind (q, k or v)
+// at a time: their loads are in flight together, and what the token needs (its
+// slot, its position's cosines and sines) is loaded and worked out once.
+template <int D, class TI, class TO, int ROWS>
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) {
     pdl_allow_dependents();
     pdl_wait_prior_grids();
     using G = KvGroup<D>;
-    constexpr int kLanes = D / 4, kRows = 32 / kLanes;
-    const int lane = threadIdx.x & 31, sub = lane % kLanes;
-    const int per_tok = p.n_heads + 2 * p.c.n_heads;
-    const int total = p.n_tok * per_tok;
+    constexpr int kLanes = D / 4, kAside = 32 / kLanes, kBatch = ROWS * kAside;
+    const int lane = threadIdx.x & 31, sub = lane % kLanes, aside = lane / kLanes;
+    const uint32_t q_batches = (p.n_heads + kBatch - 1) / kBatch, kv_batches = (p.c.n_heads + kBatch - 1) / kBatch;
+    const uint32_t batches = q_batches + 2 * kv_batches, total = static_cast<uint32_t>(p.n_tok) * batches;
     const int half = p.rot_dim >> 3;  // lanes of the first halves of the rotated channels
-    const int step = static_cast<int>(gridDim.x * (blockDim.x >> 5)) * kRows;
-    // the bound is the warp's (its first row), so that every lane takes part in the shuffles
-    for (int first = static_cast<int>(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kRows; first < total;
-         first += step) {
-        const int row = first + lane / kLanes;
-        const bool live = row < total;
-        const int tok = live ? row / per_tok : 0;
-        const int h = live ? row - tok * per_tok : 0;
-        const bool is_q = h < p.n_heads, is_k = !is_q && h < p.n_heads + p.c.n_heads;
-        const int hk = is_q ? 0 : (is_k ? h - p.n_heads : h - p.n_heads - p.c.n_heads);
-        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        bool ok = live;
-        if (live) {
-            const TI *src = is_q ? static_cast<const TI *>(p.q) + tok * p.q_stride + h * D
-                            : is_k ? static_cast<const TI *>(p.k) + tok * p.k_stride + hk * D
-                                   : static_cast<const TI *>(p.v) + tok * p.v_stride + hk * D;
-            load4(src + 4 * sub, x);
-        }
-        if (p.rope != nullptr) {
-            int pos = live ? p.positions[tok] : 0;
+    const bool low = sub < half, turned = sub < 2 * half;
+    const uint32_t step = gridDim.x * (blockDim.x >> 5);
+    // the bounds are the warp's, so that every lane takes part in the shuffles
+    for (uint32_t unit = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); unit < total; unit += step) {
+        const int tok = static_cast<int>(unit / batches);
+        const uint32_t batch = unit - tok * batches;
+        const bool is_q = batch < q_batches, is_k = !is_q && batch < q_batches + kv_batches;
+        const int first = static_cast<int>(is_q ? batch : (batch - q_batches) - (is_k ? 0 : kv_batches)) * kBatch + aside;
+        const int rows = is_q ? p.n_heads : p.c.n_heads;
+        const TI *const src = static_cast<const TI *>(is_q ? p.q : is_k ? p.k : p.v) +
+                              tok * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) + first * D + 4 * sub;
+        const bool roped = p.rope != nullptr;
+        const int slot = is_q ? -1 : p.slots[tok];
+        int pos = roped ? p.positions[tok] : 0;
+        Four<TI> raw[ROWS];
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) raw[j].load(src + j * kAside * D, first + j * kAside < rows);
+        bool ok = true;
+        float2 c[2], s[2];  // s: less than zero what the first element of a rotated pair takes of the second
+        int partner = lane;
+        if (roped) {
             if (pos < 0 || pos >= p.n_pos) {
-                if (sub == 0) record_error(p.err, kErrBadIndex);
+                if (lane == 0) record_error(p.err, kErrBadIndex);
                 ok = false;
                 pos = 0;
             }
-            const float *row_t = p.rope + static_cast<int64_t>(pos) * p.rot_dim;
-            const bool turned = (is_q || is_k) && sub < 2 * half;
-            if (p.pairs) {
-                if (turned) {
-                    const float4 cs = __ldg(reinterpret_cast<const float4 *>(row_t + 4 * sub));
-                    const float a0 = x[0], b0 = x[1], a1 = x[2], b1 = x[3];
-                    x[0] = __fsub_rn(__fmul_rn(a0, cs.x), __fmul_rn(b0, cs.y));
-                    x[1] = __fadd_rn(__fmul_rn(a0, cs.y), __fmul_rn(b0, cs.x));
-                    x[2] = __fsub_rn(__fmul_rn(a1, cs.z), __fmul_rn(b1, cs.w));
-                    x[3] = __fadd_rn(__fmul_rn(a1, cs.w), __fmul_rn(b1, cs.z));
-                }
-            } else {
-                const bool low = sub < half;
-                const int at = low ? sub : sub - half;
-                const int partner = (lane - sub) + (turned ? (low ? sub + half : at) : sub);
-                float o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], partner);
-                if (turned) {
-                    const float4 c0 = __ldg(reinterpret_cast<const float4 *>(row_t + 8 * at));
-                    const float4 c1 = __ldg(reinterpret_cast<const float4 *>(row_t + 8 * at) + 1);
-                    const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = low ? __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o[i], s[i]))
-                                   : __fadd_rn(__fmul_rn(o[i], s[i]), __fmul_rn(x[i], c[i]));
+            if (turned && p.n_pos > 0) {
+                const float *row_t = p.rope + static_cast<int64_t>(pos) * p.rot_dim;
+                if (p.pairs) {
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(row_t + 4 * sub));
+                    c[0] = make_float2(v.x, v.x), c[1] = make_float2(v.z, v.z);
+                    s[0] = make_float2(-v.y, v.y), s[1] = make_float2(-v.w, v.w);
+                } else {
+                    partner = low ? lane + half : lane - half;
+                    const float4 *at = reinterpret_cast<const float4 *>(row_t) + 2 * (low ? sub : sub - half);
+                    const float4 v0 = __ldg(at), v1 = __ldg(at + 1);
+                    c[0] = make_float2(v0.x, v0.z), c[1] = make_float2(v1.x, v1.z);
+                    s[0] = make_float2(low ? -v0.y : v0.y, low ? -v0.w : v0.w);
+                    s[1] = make_float2(low ? -v1.y : v1.y, low ? -v1.w : v1.w);
                 }
             }
         }
-        // f32 rows out
-        if (ok) {
-            const int64_t at = is_q ? (static_cast<int64_t>(tok) * p.n_heads + h) * D
-                                    : (static_cast<int64_t>(tok) * p.c.n_heads + hk) * D;
-            TO *out = static_cast<TO *>(is_q ? p.q_out : is_k ? p.k_out : p.v_out);
-            if (out != nullptr) store4(out + at + 4 * sub, x);
-        }
-        if (__all_sync(0xffffffffu, is_q)) continue;
-        // Q4_0 (each step rounded in f32, as quantize_rows has it)
-        const float d = block_signed_max(x, sub) / -8.0f;
-        const float id = d != 0.0f ? 1.0f / d : 0.0f;
-        uint32_t codes = 0;
+        TO *out = static_cast<TO *>(is_q ? p.q_out : is_k ? p.k_out : p.v_out);
+        const bool writes = ok && out != nullptr;
+        out += (static_cast<int64_t>(tok) * rows + first) * D + 4 * sub;
+        auto rotate = [&](const Four<TI> &row, float2 (&x)[2]) {
+            row.get(x);
+            if (!roped) return;
+            float2 o[2];
+            if (p.pairs) {
+                o[0] = make_float2(x[0].y, x[0].x), o[1] = make_float2(x[1].y, x[1].x);
+            } else {
+                row.from(partner).get(o);
+            }
+            if (turned) {
+                x[0] = fadd2(mul2(x[0], c[0]), mul2(o[0], s[0]));
+                x[1] = fadd2(mul2(x[1], c[1]), mul2(o[1], s[1]));
+            }
+        };
+        if (is_q) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = java_f2i(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
-            codes |= (static_cast<uint32_t>(c < 15 ? c : 15) & 0xFu) << (8 * i);
-        }
-        const uint32_t upper = __shfl_down_sync(0xffffffffu, codes, 4);
-        const int slot = live && !is_q ? p.slots[tok] : -1;
-        if (!ok || is_q || slot < 0) continue;
-        if (slot >= p.c.n_slots) {
-            if (sub == 0) record_error(p.err, kErrBadIndex);
+            for (int j = 0; j < ROWS; ++j) {
+                float2 x[2];
+                rotate(raw[j], x);
+                if (writes && first + j * kAside < rows) store4(out + j * kAside * D, x);
+            }
             continue;
         }
-        uint8_t *g = p.c.group<D>(slot, hk);
-        const int i = (slot % p.c.page_size) & 15, b = sub >> 3, t = sub & 7;
-        if (t < 4) {
-            const uint32_t w = codes | (upper << 4);
-            if (is_k) {
-                *reinterpret_cast<uint32_t *>(g + i * G::kRow + (t * G::kNB + b) * 4) = w;
-            } else {
-                const int r = kv_value_row(i);
-                unsigned short *vr = reinterpret_cast<unsigned short *>(g + G::kV + r * G::kRow);
-                vr[kv_value_unit(r, 2 * t) * G::kNB + b] = static_cast<unsigned short>(w & 0xFFFFu);
-                vr[kv_value_unit(r, 2 * t + 1) * G::kNB + b] = static_cast<unsigned short>(w >> 16);
+        if (ok && slot >= p.c.n_slots && lane == 0) record_error(p.err, kErrBadIndex);
+        const bool kept = ok && slot >= 0 && slot < p.c.n_slots;
+        // the group of the first row, and where in it this lane's codes and scale go: a value row's units hold two
+        // bytes of every block, so two blocks' lanes trade halves and each writes four bytes, the lane of the even
+        // block unit 2t, the other unit 2t + 1
+        const int b = sub >> 3, t = sub & 7;
+        uint8_t *group = nullptr;
+        uint32_t code_at = 0, scale_at = 0;
+        if (kept) {
+            group = p.c.group<D>(slot, 0) + static_cast<int64_t>(first) * p.c.page_groups * G::kBytes;
+            const int i = (slot % p.c.page_size) & 15, r = kv_value_row(i);
+            code_at = is_k ? i * G::kRow + (t * G::kNB + b) * 4
+                           : G::kV + r * G::kRow + (kv_value_unit(r, 2 * t + (b & 1)) * G::kNB + (b & ~1)) * 2;
+            scale_at = (is_k ? G::kKS : G::kVS) + i * G::kScaleRow + 2 * b;
+        }
+        const int64_t group_step = static_cast<int64_t>(kAside) * p.c.page_groups * G::kBytes;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j, group += group_step) {
+            if (first - aside + j * kAside >= rows) break;
+            float2 x[2];
+            if (is_k)
+                rotate(raw[j], x);
+            else
+                raw[j].get(x);
+            const bool live = first + j * kAside < rows;
+            if (writes && live) store4(out + j * kAside * D, x);
+            // Q4_0 (each step rounded in f32, as quantize_rows has it)
+            const float d = signed_max(x, sub) * -0.125f;
+            const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
+            const float2 id2 = make_float2(id, id), mid = make_float2(8.5f, 8.5f);
+            const float2 y0 = fadd2(mul2(x[0], id2), mid), y1 = fadd2(mul2(x[1], id2), mid);
+            const uint32_t e0 = q4_0_code(y0.x), e1 = q4_0_code(y0.y), e2 = q4_0_code(y1.x), e3 = q4_0_code(y1.y);
+            const uint32_t codes = __byte_perm(__byte_perm(e0, e1, 0x0040), __byte_perm(e2, e3, 0x0040), 0x5410);
+            uint32_t w = codes | (__shfl_down_sync(0xffffffffu, codes, 4) << 4);
+            if (!is_k) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 8);
+                w = b & 1 ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
             }
-            if (t == 0)
-                reinterpret_cast<unsigned short *>(g + (is_k ? G::kKS : G::kVS) + i * G::kScaleRow)[b] =
-                    __half_as_ushort(__float2half_rn(d));
+            if (kept && live && t < 4) {
+                *reinterpret_cast<uint32_t *>(group + code_at) = w;
+                if (t == 0) *reinterpret_cast<unsigned short *>(group + scale_at) = __half_as_ushort(__float2half_rn(d));
+            }
         }
     }
 }
 
-// The values of a cache row, four elements to a lane as above: the k rows of a
-// token, then its v rows.
-template <int D>
+// The values of cache rows: a token's k rows, then its v rows, ROWS at a time
+// as above. A lane takes one 4-byte word (elements 4t .. 4t + 3 and 16 more of a
+// block), D/8 lanes a row.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheView c, const int32_t *__restrict__ slots, int n,
                                                       float *__restrict__ k_out, float *__restrict__ v_out,
                                                       int32_t *err) {
     pdl_allow_dependents();
     pdl_wait_prior_grids();
     using G = KvGroup<D>;
-    constexpr int kLanes = D / 4;
-    const int kinds = (k_out != nullptr) + (v_out != nullptr);
-    const int per_tok = kinds * c.n_heads;
-    const int64_t lanes = static_cast<int64_t>(n) * per_tok * kLanes;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; at < lanes;
-         at += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = at / kLanes;
-        const int sub = static_cast<int>(at % kLanes);
-        const int64_t tok = row / per_tok;
-        int h = static_cast<int>(row - tok * per_tok);
-        const bool is_k = k_out != nullptr && h < c.n_heads;
-        if (!is_k && k_out != nullptr) h -= c.n_heads;
+    constexpr int kLanes = D / 8, kAside = 32 / kLanes;
+    const int lane = threadIdx.x & 31, b = (lane % kLanes) >> 2, t = lane & 3;
+    const int n_k = k_out != nullptr ? c.n_heads : 0, per_tok = n_k + (v_out != nullptr ? c.n_heads : 0);
+    const uint32_t batches = (per_tok + ROWS * kAside - 1) / (ROWS * kAside);
+    const uint32_t total = static_cast<uint32_t>(n) * batches, step = gridDim.x * (blockDim.x >> 5);
+    for (uint32_t unit = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); unit < total; unit += step) {
+        const int tok = static_cast<int>(unit / batches);
+        const int first = static_cast<int>(unit - tok * batches) * (ROWS * kAside) + lane / kLanes;
         const int slot = slots[tok];
-        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (slot >= c.n_slots) {
-            if (sub == 0) record_error(err, kErrBadIndex);
-        } else if (slot >= 0) {
-            const uint8_t *g = c.group<D>(slot, h);
-            const int i = (slot % c.page_size) & 15, b = sub >> 3, t = sub & 3;
-            uint32_t w;
-            if (is_k) {
-                w = *reinterpret_cast<const uint32_t *>(g + i * G::kRow + (t * G::kNB + b) * 4);
-            } else {
-                const int r = kv_value_row(i);
-                const unsigned short *vr = reinterpret_cast<const unsigned short *>(g + G::kV + r * G::kRow);
-                w = vr[kv_value_unit(r, 2 * t) * G::kNB + b] |
-                    static_cast<uint32_t>(vr[kv_value_unit(r, 2 * t + 1) * G::kNB + b]) << 16;
-            }
-            if (sub & 4) w >>= 4;
-            const float d = f16_bits_to_f32(
-                reinterpret_cast<const unsigned short *>(g + (is_k ? G::kKS : G::kVS) + i * G::kScaleRow)[b]);
+        if (slot >= c.n_slots && lane == 0) record_error(err, kErrBadIndex);
+        const bool there = slot >= 0 && slot < c.n_slots;
+        const int i = there ? (slot % c.page_size) & 15 : 0, r = kv_value_row(i);
+        const uint8_t *const g0 = there ? c.group<D>(slot, 0) : nullptr;
+        uint32_t w[ROWS];
+        unsigned short d[ROWS];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[e] = static_cast<float>(static_cast<int>((w >> (8 * e)) & 0xFu) - 8) * d;  // exact
+        for (int j = 0; j < ROWS; ++j) {
+            const int h = first + j * kAside;
+            w[j] = 0, d[j] = 0;
+            if (!there || h >= per_tok) continue;
+            const bool is_k = h < n_k;
+            const uint8_t *g = g0 + static_cast<int64_t>(is_k ? h : h - n_k) * c.page_groups * G::kBytes;
+            if (is_k) {
+                w[j] = *reinterpret_cast<const uint32_t *>(g + i * G::kRow + (t * G::kNB + b) * 4);
+            } else {
+                const unsigned short *vr = reinterpret_cast<const unsigned short *>(g + G::kV + r * G::kRow);
+                w[j] = vr[kv_value_unit(r, 2 * t) * G::kNB + b] |
+                       static_cast<uint32_t>(vr[kv_value_unit(r, 2 * t + 1) * G::kNB + b]) << 16;
+            }
+            d[j] = reinterpret_cast<const unsigned short *>(g + (is_k ? G::kKS : G::kVS) + i * G::kScaleRow)[b];
         }
-        store4((is_k ? k_out : v_out) + (tok * c.n_heads + h) * D + 4 * sub, x);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            const int h = first + j * kAside;
+            if (h >= per_tok) break;
+            const float ds = f16_bits_to_f32(d[j]);
+            // a code in the low byte of 2^23, less 2^23 + 8: exact, and so is the product
+            const float2 d2 = make_float2(ds, ds), off = make_float2(-8388616.0f, -8388616.0f);
+            float2 x[2][2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t n = (w[j] >> (4 * q)) & 0x0F0F0F0Fu;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    x[q][e] = there ? mul2(fadd2(make_float2(__uint_as_float(__byte_perm(n, 0x4B000000u, 0x7650 + 2 * e)),
+                                                            __uint_as_float(__byte_perm(n, 0x4B000000u, 0x7651 + 2 * e))),
+                                                off),
+                                           d2)
+                                    : make_float2(0.0f, 0.0f);
+            }
+            const bool is_k = h < n_k;
+            float *out = (is_k ? k_out : v_out) + (static_cast<int64_t>(tok) * c.n_heads + (is_k ? h : h - n_k)) * D + 32 * b + 4 * t;
+            store4(out, x[0]);
+            store4(out + 16, x[1]);
+        }
     }
 }
 
 namespace {
 
-template <int D, class TI, class TO>
-cudaError_t launch_append(const KvAppendParams &p, int sms, cudaStream_t s) {
-    const int64_t warps = (static_cast<int64_t>(p.n_tok) * (p.n_heads + 2 * p.c.n_heads) * (D / 4) + 31) / 32;
-    int64_t grid = (warps + 7) / 8;
-    if (grid > static_cast<int64_t>(sms) * 8) grid = static_cast<int64_t>(sms) * 8;
-    return launch_pdl(kv_append_kernel<D, TI, TO>, static_cast<int>(grid), 256, 0, s, p);
+// Rows a warp has in flight: four where every warp of the machine still finds
+// work, else one, for the most warps (64 tokens of 32 + 2 x 32 heads: ONE us
+// with one, FOUR with four; 8191 of 32 + 2 x 8: ONEB and FOURB).
+constexpr int kAtOnce = 4;
+bool many(int64_t warps, int sms) { return warps >= static_cast<int64_t>(sms) * 64 * kAtOnce; }
+
+template <int D, class TI, class TO> cudaError_t launch_append(const KvAppendParams &p, int sms, cudaStream_t s) {
+    const int aside = 128 / D, per_tok = p.n_heads + 2 * p.c.n_heads;
+    const bool at_once = many(static_cast<int64_t>(p.n_tok) * per_tok / aside, sms);
+    const int rows = (at_once ? kAtOnce : 1) * aside;
+    const int64_t warps = static_cast<int64_t>(p.n_tok) * ((per_tok + rows - 1) / rows);
+    const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(sms) * 8));
+    return at_once ? launch_pdl(kv_append_kernel<D, TI, TO, kAtOnce>, grid, 256, 0, s, p)
+                   : launch_pdl(kv_append_kernel<D, TI, TO, 1>, grid, 256, 0, s, p);
 }
 
 template <int D>
@@ -220,6 +300,18 @@ cudaError_t launch_append_types(const KvAppendParams &p, int in_type, int out_ty
     if (in_type == QG_F32)
         return out_type == QG_F32 ? launch_append<D, float, float>(p, sms, s) : launch_append<D, float, __half>(p, sms, s);
     return out_type == QG_F32 ? launch_append<D, __half, float>(p, sms, s) : launch_append<D, __half, __half>(p, sms, s);
+}
+
+template <int D>
+cudaError_t launch_read(const KvCacheView &c, const int32_t *slots, int n, float *k_out, float *v_out, int32_t *err,
+                        int sms, cudaStream_t s) {
+    const int aside = 256 / D, per_tok = ((k_out != nullptr) + (v_out != nullptr)) * c.n_heads;
+    const bool at_once = many(static_cast<int64_t>(n) * per_tok / aside, sms);
+    const int rows = (at_once ? kAtOnce : 1) * aside;
+    const int64_t warps = static_cast<int64_t>(n) * ((per_tok + rows - 1) / rows);
+    const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(sms) * 8));
+    return at_once ? launch_pdl(kv_read_kernel<D, kAtOnce>, grid, 256, 0, s, c, slots, n, k_out, v_out, err)
+                   : launch_pdl(kv_read_kernel<D, 1>, grid, 256, 0, s, c, slots, n, k_out, v_out, err);
 }
 
 }  // namespace
@@ -231,13 +323,8 @@ cudaError_t launch_kv_append(const KvAppendParams &p, int head_dim, int in_type,
 
 cudaError_t launch_kv_read(const KvCacheView &c, int head_dim, const int32_t *slots, int64_t n, float *k_out,
                            float *v_out, int32_t *err, int sms, cudaStream_t s) {
-    const int kinds = (k_out != nullptr) + (v_out != nullptr);
-    int64_t grid = (n * kinds * c.n_heads * (head_dim / 4) + 255) / 256;
-    if (grid > static_cast<int64_t>(sms) * 16) grid = static_cast<int64_t>(sms) * 16;
-    return head_dim == 64 ? launch_pdl(kv_read_kernel<64>, static_cast<int>(grid), 256, 0, s, c, slots,
-                                       static_cast<int>(n), k_out, v_out, err)
-                          : launch_pdl(kv_read_kernel<128>, static_cast<int>(grid), 256, 0, s, c, slots,
-                                       static_cast<int>(n), k_out, v_out, err);
+    return head_dim == 64 ? launch_read<64>(c, slots, static_cast<int>(n), k_out, v_out, err, sms, s)
+                          : launch_read<128>(c, slots, static_cast<int>(n), k_out, v_out, err, sms, s);
 }
 
 }  // namespace qg

@@ -275,13 +275,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t v) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-}
 // code - 8 in f16 of the low (high) nibbles of bytes 0 and 2; magic = 0x64006400.
 __device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t magic) {
     return hsub2((w & 0x000F000Fu) | magic, 0x64086408u);  // 1024 + c - 1032

@@ -25,6 +25,15 @@ __host__ __device__ constexpr int kv_value_row(int i) { return (i & 8) | ((i & 1
 // into different shared-memory banks.
 __host__ __device__ constexpr int kv_value_unit(int row, int u) { return u ^ ((row & 2) << 1); }
 
+// Two f16 as one word, the first in the low half.
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+
 // A cache as its kernels take it.
 struct KvCacheView {
     uint8_t *data;

@@ -16,4 +16,13 @@ __device__ __forceinline__ int java_f2i(float t) {
     return static_cast<int>(t);
 }
 
+// min(java_f2i(t), 15) & 15 for t = x (1/d) + 8.5 of a Q4_0 block, in three
+// operations. There t is in 0.4 .. 16.6 or, where 1/d overflows or x is not
+// finite, an infinity or NaN: clamped (NaN becomes 0, as the cast has it), then
+// truncated by an addition of 2^23 that rounds toward zero. The code is the
+// result's low byte; its high bytes are those of 2^23.
+__device__ __forceinline__ uint32_t q4_0_code(float t) {
+    return __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.0f), 15.5f), 8388608.0f));
+}
+
 }  // namespace qg
