@@ -2,13 +2,18 @@
 // values back (include/qattn.h: qkv_append, qkv_read).
 //
 // A row is one head of one token (q, k or v), D elements, four to a lane: D/4
-// lanes hold a row, eight lanes a Q4_0 block. A warp holds 128 elements, that
-// is one row of D = 128 or two of D = 64; the rows of q, k and v of a token
-// follow one another. The rotation's partner channel is in another lane of the
-// row (one shuffle an element), the block's signed maximum takes three
-// butterfly steps among its eight lanes, and the four lanes with elements 0..15
-// of a block take the codes of 16..31 by one shuffle and own one 4-byte code
-// word each.
+// lanes hold a row, eight lanes a Q4_0 block. A warp's load is 128 elements, one
+// row of D = 128 or two of D = 64. The rotation's partner channel is in another
+// lane of the row (shuffled as it was loaded: two shuffles for four f16), the
+// block's signed maximum takes three butterfly steps among its eight lanes, and
+// the four lanes with elements 0..15 of a block take the codes of 16..31 by one
+// shuffle and own one 4-byte code word each.
+//
+// Bound: memory for many rows, latency for few. A prompt of 8191 tokens (32 + 2 x 8
+// heads of 128, f16) moves 214 MB and takes 43 us (5.0 TB/s), 13 more with its
+// values read back; one token takes 2 us beside the launch. The rest is
+// instructions: about 85 a row, of which the bounds, the addresses and the
+// rotation's loads are shared by a warp's rows.
 #include <algorithm>
 
 #include "kv_cache.cuh"
@@ -23,7 +28,7 @@ template <> struct Four<float> {
     __device__ __forceinline__ void load(const float *p, bool there) {
         v = there ? *reinterpret_cast<const float4 *>(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = make_float2(v.x, v.y), x[1] = make_float2(v.z, v.w); }
+    __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
     __device__ __forceinline__ Four from(int lane) const {
         return {make_float4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
                             __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane))};
@@ -34,24 +39,26 @@ template <> struct Four<__half> {
     __device__ __forceinline__ void load(const __half *p, bool there) {
         v = there ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0u, 0u);
     }
-    __device__ __forceinline__ void get(float2 (&x)[2]) const { x[0] = unpack_half2(v.x), x[1] = unpack_half2(v.y); }
+    __device__ __forceinline__ void get(float (&x)[4]) const {
+        const float2 a = unpack_half2(v.x), b = unpack_half2(v.y);
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    }
     __device__ __forceinline__ Four from(int lane) const {
         return {make_uint2(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane))};
     }
 };
-__device__ __forceinline__ void store4(float *p, const float2 (&x)[2]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+__device__ __forceinline__ void store4(float *p, const float (&x)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
-__device__ __forceinline__ void store4(__half *p, const float2 (&x)[2]) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_half2(x[0].x, x[0].y), pack_half2(x[1].x, x[1].y));
+__device__ __forceinline__ void store4(__half *p, const float (&x)[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
 }
 
 // The signed maximum of a block (eight neighbouring lanes, four elements
 // each): the first element of strictly largest magnitude, NaN never (the
 // quantizer's rule), 0 for a block of zeros. From the block's largest and its
 // smallest element; only where both have the same size does the order decide.
-__device__ __noinline__ float first_of_largest(const float2 (&x2)[2], int sub) {
-    const float x[4] = {x2[0].x, x2[0].y, x2[1].x, x2[1].y};
+__device__ __noinline__ float first_of_largest(const float (&x)[4], int sub) {
     float best = -1.0f, val = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -64,9 +71,9 @@ __device__ __noinline__ float first_of_largest(const float2 (&x2)[2], int sub) {
     }
     return best > 0.0f ? val : 0.0f;
 }
-__device__ __forceinline__ float signed_max(const float2 (&x)[2], int sub) {
-    float hi = fmaxf(fmaxf(fmaxf(0.0f, x[0].x), x[0].y), fmaxf(x[1].x, x[1].y));
-    float lo = fminf(fminf(fminf(0.0f, x[0].x), x[0].y), fminf(x[1].x, x[1].y));
+__device__ __forceinline__ float signed_max(const float (&x)[4], int sub) {
+    float hi = fmaxf(fmaxf(fmaxf(0.0f, x[0]), x[1]), fmaxf(x[2], x[3]));
+    float lo = fminf(fminf(fminf(0.0f, x[0]), x[1]), fminf(x[2], x[3]));
 #pragma unroll
     for (int m = 1; m <= 4; m <<= 1) {
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
@@ -76,16 +83,11 @@ __device__ __forceinline__ float signed_max(const float2 (&x)[2], int sub) {
     return hi > -lo ? hi : hi < -lo ? lo : 0.0f;
 }
 
-// Two products, each rounded by itself. (Packed products followed by a packed
-// sum come out of the compiler as one fused operation, even with .rn on both.)
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
-}
-
 // A warp takes ROWS x (32 / kLanes) rows of one token and one kind (q, k or v)
 // at a time: their loads are in flight together, and what the token needs (its
-// slot, its position's cosines and sines) is loaded and worked out once.
-template <int D, class TI, class TO, int ROWS>
+// slot, its position's cosines and sines) is loaded and worked out once. TURN:
+// 0 no rotation, 1 of halves, 2 of neighbours.
+template <int D, class TI, class TO, int ROWS, int TURN>
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) {
     pdl_allow_dependents();
     pdl_wait_prior_grids();
@@ -106,16 +108,15 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) 
         const int rows = is_q ? p.n_heads : p.c.n_heads;
         const TI *const src = static_cast<const TI *>(is_q ? p.q : is_k ? p.k : p.v) +
                               tok * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) + first * D + 4 * sub;
-        const bool roped = p.rope != nullptr;
         const int slot = is_q ? -1 : p.slots[tok];
-        int pos = roped ? p.positions[tok] : 0;
+        int pos = TURN != 0 ? p.positions[tok] : 0;
         Four<TI> raw[ROWS];
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) raw[j].load(src + j * kAside * D, first + j * kAside < rows);
+        for (int j = 0; j < ROWS; ++j) raw[j].load(src + j * kAside * D, j * kAside < rows - first);
         bool ok = true;
-        float2 c[2], s[2];  // s: less than zero what the first element of a rotated pair takes of the second
+        float c[4], s[4];  // s: less than zero what the first element of a rotated pair takes of the second
         int partner = lane;
-        if (roped) {
+        if (TURN != 0) {
             if (pos < 0 || pos >= p.n_pos) {
                 if (lane == 0) record_error(p.err, kErrBadIndex);
                 ok = false;
@@ -123,43 +124,54 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) 
             }
             if (turned && p.n_pos > 0) {
                 const float *row_t = p.rope + static_cast<int64_t>(pos) * p.rot_dim;
-                if (p.pairs) {
+                if (TURN == 2) {
                     const float4 v = __ldg(reinterpret_cast<const float4 *>(row_t + 4 * sub));
-                    c[0] = make_float2(v.x, v.x), c[1] = make_float2(v.z, v.z);
-                    s[0] = make_float2(-v.y, v.y), s[1] = make_float2(-v.w, v.w);
+                    c[0] = c[1] = v.x, c[2] = c[3] = v.z;
+                    s[0] = -v.y, s[1] = v.y, s[2] = -v.w, s[3] = v.w;
                 } else {
                     partner = low ? lane + half : lane - half;
                     const float4 *at = reinterpret_cast<const float4 *>(row_t) + 2 * (low ? sub : sub - half);
                     const float4 v0 = __ldg(at), v1 = __ldg(at + 1);
-                    c[0] = make_float2(v0.x, v0.z), c[1] = make_float2(v1.x, v1.z);
-                    s[0] = make_float2(low ? -v0.y : v0.y, low ? -v0.w : v0.w);
-                    s[1] = make_float2(low ? -v1.y : v1.y, low ? -v1.w : v1.w);
+                    c[0] = v0.x, c[1] = v0.z, c[2] = v1.x, c[3] = v1.z;
+                    s[0] = low ? -v0.y : v0.y, s[1] = low ? -v0.w : v0.w;
+                    s[2] = low ? -v1.y : v1.y, s[3] = low ? -v1.w : v1.w;
                 }
             }
         }
+        const int left = rows - first;  // row j is there if j kAside < left
         TO *out = static_cast<TO *>(is_q ? p.q_out : is_k ? p.k_out : p.v_out);
-        const bool writes = ok && out != nullptr;
+        const int writes = ok && out != nullptr ? left : 0;
         out += (static_cast<int64_t>(tok) * rows + first) * D + 4 * sub;
-        auto rotate = [&](const Four<TI> &row, float2 (&x)[2]) {
+        // (each product and the sum rounded by itself)
+        auto rotate = [&](const Four<TI> &row, float (&x)[4]) {
             row.get(x);
-            if (!roped) return;
-            float2 o[2];
-            if (p.pairs) {
-                o[0] = make_float2(x[0].y, x[0].x), o[1] = make_float2(x[1].y, x[1].x);
+            if (TURN == 0) return;
+            float o[4];
+            if (TURN == 2) {
+                o[0] = x[1], o[1] = x[0], o[2] = x[3], o[3] = x[2];
             } else {
                 row.from(partner).get(o);
             }
-            if (turned) {
-                x[0] = fadd2(mul2(x[0], c[0]), mul2(o[0], s[0]));
-                x[1] = fadd2(mul2(x[1], c[1]), mul2(o[1], s[1]));
-            }
-        };
-        if (is_q) {
+            if (turned)
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                float2 x[2];
-                rotate(raw[j], x);
-                if (writes && first + j * kAside < rows) store4(out + j * kAside * D, x);
+                for (int e = 0; e < 4; ++e) x[e] = __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(o[e], s[e]));
+        };
+        const bool full = left - aside >= kBatch;
+        if (is_q) {
+            if (full && ok) {
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j) {
+                    float x[4];
+                    rotate(raw[j], x);
+                    store4(out + j * kAside * D, x);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j) {
+                    float x[4];
+                    rotate(raw[j], x);
+                    if (j * kAside < writes) store4(out + j * kAside * D, x);
+                }
             }
             continue;
         }
@@ -178,30 +190,30 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) 
                            : G::kV + r * G::kRow + (kv_value_unit(r, 2 * t + (b & 1)) * G::kNB + (b & ~1)) * 2;
             scale_at = (is_k ? G::kKS : G::kVS) + i * G::kScaleRow + 2 * b;
         }
+        const int keeps = kept ? left : 0;
         const int64_t group_step = static_cast<int64_t>(kAside) * p.c.page_groups * G::kBytes;
 #pragma unroll
         for (int j = 0; j < ROWS; ++j, group += group_step) {
-            if (first - aside + j * kAside >= rows) break;
-            float2 x[2];
+            if (j * kAside >= left + aside) break;
+            float x[4];
             if (is_k)
                 rotate(raw[j], x);
             else
                 raw[j].get(x);
-            const bool live = first + j * kAside < rows;
-            if (writes && live) store4(out + j * kAside * D, x);
+            if (j * kAside < writes) store4(out + j * kAside * D, x);
             // Q4_0 (each step rounded in f32, as quantize_rows has it)
             const float d = signed_max(x, sub) * -0.125f;
             const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
-            const float2 id2 = make_float2(id, id), mid = make_float2(8.5f, 8.5f);
-            const float2 y0 = fadd2(mul2(x[0], id2), mid), y1 = fadd2(mul2(x[1], id2), mid);
-            const uint32_t e0 = q4_0_code(y0.x), e1 = q4_0_code(y0.y), e2 = q4_0_code(y1.x), e3 = q4_0_code(y1.y);
-            const uint32_t codes = __byte_perm(__byte_perm(e0, e1, 0x0040), __byte_perm(e2, e3, 0x0040), 0x5410);
+            uint32_t e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = q4_0_code(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
+            const uint32_t codes = __byte_perm(__byte_perm(e[0], e[1], 0x0040), __byte_perm(e[2], e[3], 0x0040), 0x5410);
             uint32_t w = codes | (__shfl_down_sync(0xffffffffu, codes, 4) << 4);
             if (!is_k) {
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 8);
                 w = b & 1 ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
             }
-            if (kept && live && t < 4) {
+            if (t < 4 && j * kAside < keeps) {
                 *reinterpret_cast<uint32_t *>(group + code_at) = w;
                 if (t == 0) *reinterpret_cast<unsigned short *>(group + scale_at) = __half_as_ushort(__float2half_rn(d));
             }
@@ -255,19 +267,13 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheView c, const
             const int h = first + j * kAside;
             if (h >= per_tok) break;
             const float ds = f16_bits_to_f32(d[j]);
-            // a code in the low byte of 2^23, less 2^23 + 8: exact, and so is the product
-            const float2 d2 = make_float2(ds, ds), off = make_float2(-8388616.0f, -8388616.0f);
-            float2 x[2][2];
+            float x[2][4];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const uint32_t n = (w[j] >> (4 * q)) & 0x0F0F0F0Fu;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    x[q][e] = there ? mul2(fadd2(make_float2(__uint_as_float(__byte_perm(n, 0x4B000000u, 0x7650 + 2 * e)),
-                                                            __uint_as_float(__byte_perm(n, 0x4B000000u, 0x7651 + 2 * e))),
-                                                off),
-                                           d2)
-                                    : make_float2(0.0f, 0.0f);
+                for (int e = 0; e < 4; ++e)  // a code in the low byte of 2^23, less 2^23 + 8: exact, and so is the product
+                    x[q][e] = there ? (__uint_as_float(__byte_perm(n, 0x4B000000u, 0x7650 + e)) - 8388616.0f) * ds : 0.0f;
             }
             const bool is_k = h < n_k;
             float *out = (is_k ? k_out : v_out) + (static_cast<int64_t>(tok) * c.n_heads + (is_k ? h : h - n_k)) * D + 32 * b + 4 * t;
@@ -279,20 +285,31 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvCacheView c, const
 
 namespace {
 
-// Rows a warp has in flight: four where every warp of the machine still finds
-// work, else one, for the most warps (64 tokens of 32 + 2 x 32 heads: ONE us
-// with one, FOUR with four; 8191 of 32 + 2 x 8: ONEB and FOURB).
-constexpr int kAtOnce = 4;
-bool many(int64_t warps, int sms) { return warps >= static_cast<int64_t>(sms) * 64 * kAtOnce; }
+// Rows a warp has in flight: eight where that still leaves a few rounds for
+// every warp of the machine, two from one row a warp on, else one (8191 tokens
+// of 32 + 2 x 8 heads of 128, written and read: 58.8 us with eight, 62.3 with four,
+// 79.9 with two; 64 of 32 + 2 x 32: 6.9 with one, 6.6 with two, 7.6 with four; 1
+// of 32 + 2 x 8: 3.7, 4.3, 5.4). Reading is best at two (56.1 us of those 58.8).
+int rows_at_once(int64_t warps, int sms) {
+    return warps >= static_cast<int64_t>(sms) * 512 ? 8 : warps >= static_cast<int64_t>(sms) * 32 ? 2 : 1;
+}
+
+template <int D, class TI, class TO, int ROWS> cudaError_t launch_append_rows(const KvAppendParams &p, int sms, cudaStream_t s) {
+    const int rows = ROWS * (128 / D);
+    const int64_t warps = static_cast<int64_t>(p.n_tok) * ((p.n_heads + rows - 1) / rows + 2 * ((p.c.n_heads + rows - 1) / rows));
+    const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(sms) * 8));
+    return p.rope == nullptr ? launch_pdl(kv_append_kernel<D, TI, TO, ROWS, 0>, grid, 256, 0, s, p)
+           : p.pairs         ? launch_pdl(kv_append_kernel<D, TI, TO, ROWS, 2>, grid, 256, 0, s, p)
+                             : launch_pdl(kv_append_kernel<D, TI, TO, ROWS, 1>, grid, 256, 0, s, p);
+}
 
 template <int D, class TI, class TO> cudaError_t launch_append(const KvAppendParams &p, int sms, cudaStream_t s) {
-    const int aside = 128 / D, per_tok = p.n_heads + 2 * p.c.n_heads;
-    const bool at_once = many(static_cast<int64_t>(p.n_tok) * per_tok / aside, sms);
-    const int rows = (at_once ? kAtOnce : 1) * aside;
-    const int64_t warps = static_cast<int64_t>(p.n_tok) * ((per_tok + rows - 1) / rows);
-    const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(sms) * 8));
-    return at_once ? launch_pdl(kv_append_kernel<D, TI, TO, kAtOnce>, grid, 256, 0, s, p)
-                   : launch_pdl(kv_append_kernel<D, TI, TO, 1>, grid, 256, 0, s, p);
+    const int per_tok = p.n_heads + 2 * p.c.n_heads;
+    switch (rows_at_once(static_cast<int64_t>(p.n_tok) * per_tok / (128 / D), sms)) {
+    case 8: return launch_append_rows<D, TI, TO, 8>(p, sms, s);
+    case 2: return launch_append_rows<D, TI, TO, 2>(p, sms, s);
+    default: return launch_append_rows<D, TI, TO, 1>(p, sms, s);
+    }
 }
 
 template <int D>
@@ -306,12 +323,12 @@ template <int D>
 cudaError_t launch_read(const KvCacheView &c, const int32_t *slots, int n, float *k_out, float *v_out, int32_t *err,
                         int sms, cudaStream_t s) {
     const int aside = 256 / D, per_tok = ((k_out != nullptr) + (v_out != nullptr)) * c.n_heads;
-    const bool at_once = many(static_cast<int64_t>(n) * per_tok / aside, sms);
-    const int rows = (at_once ? kAtOnce : 1) * aside;
+    const bool two = rows_at_once(static_cast<int64_t>(n) * per_tok / aside, sms) > 1;
+    const int rows = (two ? 2 : 1) * aside;
     const int64_t warps = static_cast<int64_t>(n) * ((per_tok + rows - 1) / rows);
     const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, static_cast<int64_t>(sms) * 8));
-    return at_once ? launch_pdl(kv_read_kernel<D, kAtOnce>, grid, 256, 0, s, c, slots, n, k_out, v_out, err)
-                   : launch_pdl(kv_read_kernel<D, 1>, grid, 256, 0, s, c, slots, n, k_out, v_out, err);
+    return two ? launch_pdl(kv_read_kernel<D, 2>, grid, 256, 0, s, c, slots, n, k_out, v_out, err)
+               : launch_pdl(kv_read_kernel<D, 1>, grid, 256, 0, s, c, slots, n, k_out, v_out, err);
 }
 
 }  // namespace

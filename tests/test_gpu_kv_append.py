@@ -46,6 +46,9 @@ CASES = [  # n_tok, heads, kv_heads, D, rot, pairs, in, out, page, fused (q, k a
     (50, 4, 2, 128, 8, True, "f32", "f16", 64, True), (19, 7, 7, 64, 56, False, "f16", "f16", 16, False),
     (130, 16, 2, 128, 128, True, "f32", "f32", 128, True), (257, 3, 1, 64, 40, False, "f32", "f32", 16, True),
     (64, 32, 8, 128, 128, False, "f16", "f16", 64, True), (5, 2, 1, 128, 0, False, "f32", "f32", 16, False),
+    # rows enough for two a warp, and for eight; heads that do not divide by them
+    (301, 14, 7, 128, 96, False, "f16", "f32", 32, True), (1201, 6, 3, 64, 64, True, "f32", "f32", 16, False),
+    (1201, 54, 9, 128, 128, False, "f16", "f16", 64, True), (3101, 48, 2, 64, 0, False, "f32", "f16", 16, False),
 ]
 
 
