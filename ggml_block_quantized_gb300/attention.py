@@ -75,46 +75,58 @@ def _check(st, where):
         raise QGError(st, where)
 
 
-def _on(t, device, name, dtype):
-    """t as a contiguous CUDA tensor of `dtype` on `device`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows(t, device, name, head_dim, dtype=None):
-    """(pointer, stride from token to token) of [n_tok, heads, head_dim] with
-    contiguous heads; the tokens may lie apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _TYPE or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be {dtype or 'float32 or float16'}, got {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
-    if t.dim() != 3 or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be [tokens, heads, {head_dim}], got {list(t.shape)}")
-    stride = t.stride()
-    if (stride[2] != 1 or (stride[1] != head_dim and t.shape[1] > 1)) and t.numel():
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), stride[0] if t.shape[0] > 1 else t.shape[1] * head_dim
-
-
-def _out(t, shape, dtypes, device, name):
+def _refuse(t, device, name, dtypes):
+    """Raises for what every tensor argument must be; returns where t is that."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+
+
+# The checks below ask once for what nearly every call passes, and look for the
+# reason of a refusal only then: a step of few tokens is as long as its host code.
+# (A CPU tensor's get_device() is -1; what is no tensor has none.)
+def _on(t, device, name, dtype):
+    """The address of t, a contiguous tensor of `dtype` on `device`."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, device, name, (dtype,))
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, device, name, head_dim, dtypes):
+    """(address, stride from token to token, tokens, heads) of [tokens, heads,
+    head_dim] with contiguous heads; the tokens may lie apart."""
+    try:
+        n, heads, d = t.shape
+        if d == head_dim and t.dtype in dtypes and t.get_device() == device:
+            if t.is_contiguous():
+                return t.data_ptr(), heads * d, n, heads
+            stride = t.stride()
+            if stride[2] == 1 and (stride[1] == d or heads == 1):
+                return t.data_ptr(), stride[0] if n > 1 else heads * d, n, heads
+    except (AttributeError, ValueError):
+        pass
+    _refuse(t, device, name, dtypes)
+    if t.dim() != 3 or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [tokens, heads, {head_dim}], got {list(t.shape)}")
+    raise ValueError(f"{name}: the heads of a token must be contiguous")
+
+
+def _out(t, shape, dtypes, device, name):
+    """The address of t, contiguous, of `shape` and one of `dtypes`."""
+    try:
+        if t.shape == shape and t.dtype in dtypes and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, device, name, dtypes)
+    raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
 
 
 def _place(t, name):
@@ -137,8 +149,9 @@ def _new(shape, dtype, device, stream):
     return t
 
 
-def _stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _stream(stream, device):
+    """The stream's handle; the current stream's without building its object (2.8 us on the host)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 # ------------------------------------------------------------ the cache
@@ -157,12 +170,13 @@ class KVCache:
             raise TypeError("data must be a uint8 CUDA tensor")
         if not data.is_contiguous():
             raise ValueError("data must be contiguous")
-        page = kv_cache_bytes(1, n_kv_heads, head_dim, page_size)
-        if page < 0:
+        page = n_kv_heads * (page_size // 16) * 18 * head_dim  # (as kv_cache_bytes has it)
+        n_pages = data.numel() // page if page > 0 else 0
+        total = kv_cache_bytes(n_pages, n_kv_heads, head_dim, page_size)
+        if total < 0 and kv_cache_bytes(1, n_kv_heads, head_dim, page_size) < 0:
             raise ValueError(f"no cache of {n_kv_heads} heads of {head_dim} in pages of {page_size}: heads of 64 or "
                              "128, pages of a multiple of 16 tokens")
-        n_pages, rest = divmod(data.numel(), page)
-        if rest or kv_cache_bytes(n_pages, n_kv_heads, head_dim, page_size) < 0:
+        if total != data.numel():
             raise ValueError(f"data holds {data.numel()} bytes, not a number of pages of {page}")
         self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
         self.data = data
@@ -198,10 +212,9 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope=None, rope_pairs
     device = _place(k, "k")
     _on(cache.data, device, "the cache", torch.uint8)
     d, t = cache.head_dim, k.dtype
-    k_ptr, k_stride = _rows(k, device, "k", d)
-    v_ptr, v_stride = _rows(v, device, "v", d, t)
-    n = k.shape[0]
-    if k.shape[1] != cache.n_kv_heads or v.shape != k.shape:
+    k_ptr, k_stride, n, n_kv = _rows(k, device, "k", d, _TYPE)
+    v_ptr, v_stride, n_v, n_kv_v = _rows(v, device, "v", d, (t,))
+    if n_kv != cache.n_kv_heads or n_kv_v != n_kv or n_v != n:
         raise ValueError(f"k and v must be [tokens, {cache.n_kv_heads}, {d}]")
     if slots.shape != (n,):
         raise ValueError(f"slots must be [{n}]")
@@ -209,9 +222,8 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope=None, rope_pairs
     q_ptr = q_stride = heads = n_pos = rot = 0
     rope_ptr = pos_ptr = None
     if q is not None:
-        q_ptr, q_stride = _rows(q, device, "q", d, t)
-        heads = q.shape[1]
-        if q.shape[0] != n or heads < 1 or heads % cache.n_kv_heads:
+        q_ptr, q_stride, n_q, heads = _rows(q, device, "q", d, (t,))
+        if n_q != n or heads < 1 or heads % n_kv:
             raise ValueError(f"q must be [{n}, a multiple of {cache.n_kv_heads}, {d}]")
         if q_out is None:
             q_out = _new(q.shape, (k_out if k_out is not None else q).dtype, q.device, stream)
@@ -221,20 +233,23 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope=None, rope_pairs
         if positions is None:
             raise ValueError("rope needs positions")
         rope_ptr = _on(rope, device, "rope", torch.float32)
-        if rope.dim() != 3 or rope.shape[2] != 2 or rope.shape[1] % 4 or not 4 <= rope.shape[1] <= d // 2:
+        shape = rope.shape
+        if len(shape) != 3 or shape[2] != 2 or shape[1] % 4 or not 4 <= shape[1] <= d // 2:
             raise ValueError(f"rope must be [positions, pairs, 2], pairs a multiple of 4 up to {d // 2}")
-        n_pos, rot = rope.shape[0], 2 * rope.shape[1]
+        n_pos, rot = shape[0], 2 * shape[1]
         if positions.shape != (n,):
             raise ValueError(f"positions must be [{n}]")
         pos_ptr = _on(positions, device, "positions", torch.int32)
-    out_t, outs = None, [None, None, None]
-    for i, (o, like, name) in enumerate(((q_out, q, "q_out"), (k_out, k, "k_out"), (v_out, v, "v_out"))):
-        if o is not None:
-            outs[i] = _out(o, like.shape, _TYPE if out_t is None else (out_t,), device, name)
-            out_t = o.dtype
-    args = _AppendArgs(q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride, slots_ptr, pos_ptr, rope_ptr, outs[0],
-                       outs[1], outs[2], n, heads, _TYPE[t], _TYPE[out_t or t], n_pos, rot, 1 if rope_pairs else 0)
-    st = _lib().qkv_append(cache.ref, ctypes.byref(args), _stream(stream))
+    out_t = q_out_ptr = k_out_ptr = v_out_ptr = None
+    if q_out is not None:
+        q_out_ptr, out_t = _out(q_out, (n, heads, d), _TYPE, device, "q_out"), q_out.dtype
+    if k_out is not None:
+        k_out_ptr, out_t = _out(k_out, (n, n_kv, d), _TYPE if out_t is None else (out_t,), device, "k_out"), k_out.dtype
+    if v_out is not None:
+        v_out_ptr, out_t = _out(v_out, (n, n_kv, d), _TYPE if out_t is None else (out_t,), device, "v_out"), v_out.dtype
+    args = _AppendArgs(q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride, slots_ptr, pos_ptr, rope_ptr, q_out_ptr,
+                       k_out_ptr, v_out_ptr, n, heads, _TYPE[t], _TYPE[out_t or t], n_pos, rot, 1 if rope_pairs else 0)
+    st = _lib().qkv_append(cache.ref, ctypes.byref(args), _stream(stream, device))
     if st:
         _check(st, "kv_append")
     return q_out
@@ -255,7 +270,7 @@ def kv_read(cache: KVCache, slots, k_out=None, v_out=None, stream=None):
     f32 = (torch.float32,)
     st = _lib().qkv_read(cache.ref, slots_ptr, shape[0],
                          _out(k_out, shape, f32, device, "k_out") if k_out is not None else None,
-                         _out(v_out, shape, f32, device, "v_out") if v_out is not None else None, _stream(stream))
+                         _out(v_out, shape, f32, device, "v_out") if v_out is not None else None, _stream(stream, device))
     if st:
         _check(st, "kv_read")
     return k_out, v_out
@@ -278,15 +293,15 @@ def kv_attend(cache: KVCache, q, table, lengths, q_offsets=None, max_q_len: int 
     device = _place(q, "q")
     _on(cache.data, device, "the cache", torch.uint8)
     d = cache.head_dim
-    q_ptr, q_stride = _rows(q, device, "q", d)
-    n_tok, heads, _ = q.shape
+    q_ptr, q_stride, n_tok, heads = _rows(q, device, "q", d, _TYPE)
     if heads < 1 or heads % cache.n_kv_heads:
         raise ValueError(f"q must have a multiple of {cache.n_kv_heads} heads")
     table_ptr = _on(table, device, "table", torch.int32)
     len_ptr = _on(lengths, device, "lengths", torch.int32)
-    if lengths.dim() != 1 or table.dim() != 2 or table.shape[0] != lengths.shape[0]:
+    shape, off_ptr = table.shape, None
+    if len(shape) != 2 or lengths.shape != shape[:1]:
         raise ValueError("table must be [sequences, pages] and lengths [sequences]")
-    n_seq, off_ptr = lengths.shape[0], None
+    n_seq, pages = shape
     if q_offsets is not None:
         off_ptr = _on(q_offsets, device, "q_offsets", torch.int32)
         if q_offsets.shape != (n_seq + 1,):
@@ -295,15 +310,15 @@ def kv_attend(cache: KVCache, q, table, lengths, q_offsets=None, max_q_len: int 
         raise ValueError(f"q holds {n_tok} tokens for {n_seq} sequences: q_offsets is needed")
     if out is None:
         out = _new(q.shape, q.dtype, q.device, stream)
-    out_ptr = _out(out, q.shape, (q.dtype,), device, "out")
+    out_ptr = _out(out, (n_tok, heads, d), (q.dtype,), device, "out")
     L = _lib()
     if workspace is None:
         need = L.qkv_attend_workspace_bytes(d, cache.n_kv_heads, heads, max_q_len)
         workspace = _new((max(need, 16),), torch.uint8, q.device, stream)
     ws_ptr = _on(workspace, device, "workspace", torch.uint8)
-    st = L.qkv_attend(cache.ref, _TYPE[q.dtype], q_ptr, q_stride, out_ptr, table_ptr, table.shape[1], len_ptr, off_ptr,
+    st = L.qkv_attend(cache.ref, _TYPE[q.dtype], q_ptr, q_stride, out_ptr, table_ptr, pages, len_ptr, off_ptr,
                       n_seq, n_tok, heads, max_q_len, d ** -0.5 if scale is None else scale, ws_ptr,
-                      workspace.numel(), _stream(stream))
+                      workspace.numel(), _stream(stream, device))
     if st:
         _check(st, "kv_attend")
     return out
@@ -317,22 +332,22 @@ def prompt_attend(q, k, v, offsets, scale=None, out=None, stream=None):
     float16 (or float32 if such an `out` is passed); rows in no sequence are
     not written."""
     device = _place(q, "q")
-    d = q.shape[-1]
-    q_ptr, q_stride = _rows(q, device, "q", d, torch.float16)
-    k_ptr, k_stride = _rows(k, device, "k", d, torch.float16)
-    v_ptr, v_stride = _rows(v, device, "v", d, torch.float16)
-    n_tok, heads, _ = q.shape
-    if k.shape != v.shape or k.shape[0] != n_tok or k.shape[1] < 1 or heads < 1 or heads % k.shape[1]:
+    d, f16 = q.shape[-1] if q.dim() else 0, (torch.float16,)
+    q_ptr, q_stride, n_tok, heads = _rows(q, device, "q", d, f16)
+    k_ptr, k_stride, n_k, n_kv = _rows(k, device, "k", d, f16)
+    v_ptr, v_stride, n_v, n_kv_v = _rows(v, device, "v", d, f16)
+    if n_k != n_tok or n_v != n_k or n_kv_v != n_kv or n_kv < 1 or heads < 1 or heads % n_kv:
         raise ValueError("k and v must be [tokens, kv heads, D], q [tokens, a multiple of the kv heads, D]")
     off_ptr = _on(offsets, device, "offsets", torch.int32)
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
+    ends = offsets.shape
+    if len(ends) != 1 or ends[0] < 1:
         raise ValueError("offsets must be [sequences + 1]")
     if out is None:
         out = _new(q.shape, torch.float16, q.device, stream)
-    out_ptr = _out(out, q.shape, _TYPE, device, "out")
+    out_ptr = _out(out, (n_tok, heads, d), _TYPE, device, "out")
     st = _lib().qattn_prompt(q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride, _TYPE[out.dtype], out_ptr, off_ptr,
-                             offsets.shape[0] - 1, n_tok, heads, k.shape[1], d, d ** -0.5 if scale is None else scale,
-                             _stream(stream))
+                             ends[0] - 1, n_tok, heads, n_kv, d, d ** -0.5 if scale is None else scale,
+                             _stream(stream, device))
     if st:
         _check(st, "prompt_attend")
     return out
