@@ -1,0 +1,73 @@
+"""The example's layer: products, append, prompt attention and attention over
+the cache, one after the other on one stream, as a user runs them."""
+import os
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import attn_ref  # noqa: E402
+import ggml_block_quantized_gb300 as qg  # noqa: E402
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+import attention_layer as ex  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+LENGTHS, STEPS, PAGE = [37, 1, 130], 3, 32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    yield
+    assert qg.device_error() == 0
+
+
+@pytest.mark.parametrize("heads,kv_heads,head_dim", [(6, 2, 64), (4, 4, 128)])
+def test_layer(heads, kv_heads, head_dim):
+    """Each sequence's prompt rows against 64-bit attention over f16 rows, each step's against 64-bit attention over
+    the 4-bit values of all its rows. The bounds are the operators' own (f16 rows and weights for a prompt; f32 rows
+    and split weights for a step)."""
+    n_in = 256
+    layer = ex.random_layer(heads, kv_heads, head_dim, n_in, n_pos=256)
+    g = torch.Generator(device="cuda").manual_seed(head_dim)
+    x = [torch.randn(n + STEPS, n_in, generator=g, device="cuda") for n in LENGTHS]
+    got, _, _ = ex.run(layer, x, LENGTHS, STEPS, PAGE)
+    assert [tuple(r.shape) for r in got] == [(sum(LENGTHS), heads, head_dim)] + [(len(LENGTHS), heads, head_dim)] * STEPS
+    assert layer.output(got[1]).shape == (len(LENGTHS), n_in)
+    packed = torch.cat([r[:n] for r, n in zip(x, LENGTHS)])
+    pq, pk, pv = (t.cpu().numpy() for t in layer.project(packed))  # as the prompts' one product gives them
+    scale, group, at = head_dim ** -0.5, heads // kv_heads, 0
+    for s, n in enumerate(LENGTHS):
+        table = layer.rope.cpu().numpy()[:n + STEPS]
+        q, k, v = pq[at:at + n], pk[at:at + n], pv[at:at + n]
+        q, k = (attn_ref.rotate(t, table[:n], False, np.float32) for t in (q, k))
+        mine = got[0][at:at + n].cpu().numpy()
+        for h in range(heads):
+            a, b, c = (t.astype(np.float16).astype(np.float64) for t in (q[:, h], k[:, h // group], v[:, h // group]))
+            out, p_v, mag, big = attn_ref.attend(a, b, c, np.arange(1, n + 1), scale)
+            assert np.all(np.abs(mine[:, h] - out) <= attn_ref.bound(out, p_v, mag, big, head_dim, n, 24, 10, False))
+        for i in range(STEPS):  # a step's three rows are one product; the next row of k and v joins the sequence's
+            new = torch.stack([r[m + i] for r, m in zip(x, LENGTHS)])
+            nq, nk, nv = (t.cpu().numpy()[s:s + 1] for t in layer.project(new))
+            nq, nk = (attn_ref.rotate(t, table[n + i:n + i + 1], False, np.float32) for t in (nq, nk))
+            k, v = np.concatenate([k, nk]), np.concatenate([v, nv])
+            mine_s = got[1 + i][s].cpu().numpy()
+            for h in range(heads):
+                b, c = (attn_ref.q4_0_values(*attn_ref.q4_0(t[:, h // group])) for t in (k, v))
+                out, p_v, mag, big = attn_ref.attend(nq[:, h].astype(np.float64), b, c, [len(k)], scale)
+                assert np.all(np.abs(mine_s[h:h + 1] - out) <=
+                              attn_ref.bound(out, p_v, mag, big, head_dim, len(k), 20, 20, False))
+        at += n
+
+
+def test_example_command(capsys):
+    ex.main()
+    text = capsys.readouterr().out
+    assert "prompt rows" in text and "apart" in text
