@@ -771,17 +771,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         for (int nt = 0; nt < NT; ++nt) {
                             const float2 pa = make_float2(s[gr][nt][0] * fa, s[gr][nt][1] * fa);
                             const float2 pb = make_float2(s[gr][nt][2] * fb, s[gr][nt][3] * fb);
-                            uint32_t x = pack_half2(pa.x, pa.y), y = pack_half2(pb.x, pb.y);
-#pragma unroll
-                            for (int q = 0; q < TERMS; ++q) {
+                            const uint32_t x = pack_half2(pa.x, pa.y), y = pack_half2(pb.x, pb.y);
+                            if (TERMS == 1) {
                                 const uint32_t b0 = transpose8(x), b1 = transpose8(y);
                                 mma_f16(o[nt][b][0], a0, a1, a2, a3, b0, b1);
                                 mma_f16(o[nt][b][1], h0, h1, h2, h3, b0, b1);
-                                if (q + 1 < TERMS) {
-                                    const float2 xh = unpack_half2(x), yh = unpack_half2(y);
-                                    const float2 ra = fadd2(pa, make_float2(-xh.x, -xh.y)), rb = fadd2(pb, make_float2(-yh.x, -yh.y));
-                                    x = pack_half2(ra.x, ra.y), y = pack_half2(rb.x, rb.y);
-                                }
+                            } else {
+                                // sums of 16 tokens, added to the long ones by themselves: the tensor cores cut what
+                                // they add off where an ordinary sum rounds, always toward zero, and over 131071
+                                // tokens that came to 1.4e-6 of the result
+                                const float2 xh = unpack_half2(x), yh = unpack_half2(y);
+                                const float2 ra = fadd2(pa, make_float2(-xh.x, -xh.y)), rb = fadd2(pb, make_float2(-yh.x, -yh.y));
+                                const uint32_t b0 = transpose8(x), b1 = transpose8(y);
+                                const uint32_t b2 = transpose8(pack_half2(ra.x, ra.y)), b3 = transpose8(pack_half2(rb.x, rb.y));
+                                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                                float lo[4], hi[4];
+                                mma_f16(lo, a0, a1, a2, a3, b0, b1, zero);
+                                mma_f16(hi, h0, h1, h2, h3, b0, b1, zero);
+                                mma_f16(lo, a0, a1, a2, a3, b2, b3);
+                                mma_f16(hi, h0, h1, h2, h3, b2, b3);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[nt][b][0][i] += lo[i], o[nt][b][1][i] += hi[i];
                             }
                         }
                     }
