@@ -75,7 +75,7 @@ template <int D, int NT, int TERMS> struct Shape {
     static constexpr int kJoinPitch = D + 4;
     static constexpr int kOffJoin = kOffStat + kWarps * kRows * 8;             // [warp][rows][kJoinPitch]
     static constexpr int kSmem = kOffJoin + kWarps * kRows * kJoinPitch * 4;
-    static constexpr int kCtas = NT == 1 ? 3 : (NT == 2 ? 2 : 1);              // resident blocks a multiprocessor
+    static constexpr int kCtas = NT == 1 ? 3 : 2;                              // resident blocks a multiprocessor
 };
 
 // A partial result: rows x D values, then the rows' maxima and sums.
@@ -791,7 +791,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                                 mma_f16(lo, a0, a1, a2, a3, b2, b3);
                                 mma_f16(hi, h0, h1, h2, h3, b2, b3);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) o[nt][b][0][i] += lo[i], o[nt][b][1][i] += hi[i];
+                                for (int i = 0; i < 4; i += 2) {
+                                    const float2 u = fadd2(make_float2(o[nt][b][0][i], o[nt][b][0][i + 1]), make_float2(lo[i], lo[i + 1]));
+                                    const float2 w2 = fadd2(make_float2(o[nt][b][1][i], o[nt][b][1][i + 1]), make_float2(hi[i], hi[i + 1]));
+                                    o[nt][b][0][i] = u.x, o[nt][b][0][i + 1] = u.y;
+                                    o[nt][b][1][i] = w2.x, o[nt][b][1][i + 1] = w2.y;
+                                }
                             }
                         }
                     }
@@ -960,9 +965,15 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttendParams p) {
            sum.x * inv, sum.y * inv);
 }
 
-// Query rows a segment takes: 8 a fragment column set, as few as hold all rows
-// of a head, at most 32 (more rows run as further segments over the same tokens).
-int row_sets(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// Query rows a segment takes, in sets of 8: two sets share a tile's loads and
+// code conversions, unless the rows make few sets and an odd number of them, whose
+// last pair would be half empty. 8 sequences of 3000 .. 6000 tokens, heads of 128,
+// f32: 16 rows 34.3 us with two and 34.8 with one, 24 rows 54.2 and 45.9; one of
+// 60000, 32 rows: 74.7 and 79.6. (Four sets spill: 67.2 us at 24 rows, 91.8 at 32.)
+int row_sets(int64_t rows) {
+    const int64_t sets = (rows + 7) / 8;
+    return sets % 2 == 1 && sets < 8 ? 1 : 2;
+}
 
 cudaError_t launch_join(void (*kernel)(KvAttendParams), dim3 grid, cudaStream_t s, const KvAttendParams &p) {
     cudaLaunchConfig_t cfg = {};
@@ -997,8 +1008,7 @@ template <int D, class T, int NT> cudaError_t launch(const KvAttendParams &p, in
 template <int D, class T> cudaError_t launch_rows(const KvAttendParams &p, int sms, int device, cudaStream_t s) {
     switch (row_sets(static_cast<int64_t>(p.max_q_len) * p.group)) {
     case 1: return launch<D, T, 1>(p, sms, device, s);
-    case 2: return launch<D, T, 2>(p, sms, device, s);
-    default: return launch<D, T, 4>(p, sms, device, s);
+    default: return launch<D, T, 2>(p, sms, device, s);
     }
 }
 
