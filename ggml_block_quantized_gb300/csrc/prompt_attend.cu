@@ -48,7 +48,7 @@ namespace qg {
 namespace {
 
 constexpr int kThreads = 16 * 32;
-constexpr int kItems = 4;  // items known ahead
+constexpr int kItems = 1;  // items known ahead
 constexpr int kSteps = 16;  // barriers of steps: more than the ring can hold (a step has a slot at least)
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr uint32_t kTmemCols = 512;  // S_A, S_B, O_A, O_B at 0, 128, 256, 384
