@@ -120,7 +120,7 @@ template <int D> __device__ __forceinline__ void mma_s(uint32_t issue, uint32_t 
             "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(issue), "r"(hi)
             : "memory");
 }
-// O (+)= P V over 64 keys: 16 keys a product, 8 columns of P and 2 KB of V.
+// O (+)= P V: 16 keys a product, 8 columns of P and 2 KB of V.
 __device__ __forceinline__ void mma_pv(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t hi) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
@@ -137,15 +137,19 @@ __device__ __forceinline__ void mma_pv(uint32_t issue, uint32_t d, uint32_t a, u
         "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\t"
         "mov.b64 db, {b, %6};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "add.u32 a, %1, 32;\n\tadd.u32 b, %2, 512;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "add.u32 a, %1, 40;\n\tadd.u32 b, %2, 640;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "add.u32 a, %1, 48;\n\tadd.u32 b, %2, 768;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+        "add.u32 a, %1, 56;\n\tadd.u32 b, %2, 896;\n\t"
+        "mov.b64 db, {b, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
         "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(issue), "r"(hi)
-        : "memory");
-}
-// The same over 16 keys.
-__device__ __forceinline__ void mma_pv16(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t hi) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.b64 db, {%2, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
-        "r"(issue), "r"(hi)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t issue, uint32_t bar) {
@@ -703,50 +707,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             Step<Sh::kSlots> step;
             uint32_t par_p = 0, par_q = 0, par_o = 3;  // parities of p_ready, q_full and o_empty, by tile
             uint32_t results = 0;                      // tiles that have had a result
+            // One piece of code for an item's first step (keys only), the others and the last (values only): what
+            // runs once an item would come from instruction memory each time, and nothing hides that here.
             for (int k = 0;; ++k) {
                 wait(item_full + 8 * (k % kItems), k / kItems);
                 const Work w = take_item(k);
                 if (w.last) break;
-                wait(step.bar(ready), step.parity());
-                {
-                    const uint32_t s = step.take();
-#pragma unroll 1
-                    for (int x = 0; x < 2; ++x) {
-                        if ((x == 0 ? w.t[0] : w.t[1]) == 0) continue;
-                        wait(q_full + 8 * x, par_q >> x);
-                        par_q ^= 1u << x;
-                        tc_fence_after();
-                        product_s(w, x, 0, s);
-                    }
-                    commit(issue, step.bar(empty));
-                    ++step.n;
-                }
-                for (int j = 0; j < w.n; ++j) {
+                for (int j = -1; j < w.n; ++j) {
                     wait(step.bar(ready), step.parity());
-                    const uint32_t sv = step.take(), sk = j + 1 < w.n ? step.take() : 0;
+                    const uint32_t sv = j < 0 ? 0 : step.take(), sk = j + 1 < w.n ? step.take() : 0;
 #pragma unroll 1
                     for (int x = 0; x < 2; ++x) {
                         const int t = x == 0 ? w.t[0] : w.t[1];
                         if (j >= t) continue;
-                        const uint32_t v = v_desc + sv * kStep, o_t = tmem + 256 + 128 * x, p_t = tmem + 128 * x;
+                        uint32_t bar = q_full + 8 * x, parity = par_q;
+                        if (j >= 0) {
+                            bar = p_ready + 8 * x, parity = par_p;
+                            par_p ^= 1u << x;
+                        } else {
+                            if (t == 0) continue;
+                            par_q ^= 1u << x;
+                        }
+                        wait(bar, parity >> x);
                         if (j == 0) {
                             if (results >> x & 1u) wait(o_empty + 8 * x, par_o >> x);
                             par_o ^= 1u << x;
                             results |= 1u << x;
                         }
-                        wait(p_ready + 8 * x, par_p >> x);
-                        par_p ^= 1u << x;
                         tc_fence_after();
-                        if (j + 1 < t) {
-                            mma_pv(issue, o_t, p_t, v, kIdO, j, kDescHi);
-                            mma_pv(issue, o_t, p_t + 32, v + 4 * (2048 / 16), kIdO, 1, kDescHi);
+                        if (j >= 0) mma_pv(issue, tmem + 256 + 128 * x, tmem + 128 * x, v_desc + sv * kStep, kIdO, j, kDescHi);
+                        if (j + 1 < t)
                             product_s(w, x, j + 1, sk);
-                        } else {  // the keys that some row sees
-                            const int steps = x == 0 ? w.steps[0] : w.steps[1];
-                            for (int i = 0; i < steps; ++i)
-                                mma_pv16(issue, o_t, p_t + 8 * i, v + i * (2048 / 16), kIdO, i | j, kDescHi);
+                        else
                             commit(issue, o_full + 8 * x);
-                        }
                     }
                     commit(issue, step.bar(empty));
                     ++step.n;
