@@ -57,7 +57,8 @@ def check(got, q, k, v, lens, scale, f16=True, rows=None, heads=None):
 CASES = [  # D, kv heads, group, lengths, fused
     (128, 2, 4, [1], True), (64, 1, 1, [2], False), (128, 8, 4, [61], True), (64, 3, 1, [127, 128, 129], True),
     (128, 1, 8, [0, 1, 0, 2, 3, 15, 16, 17, 31, 33, 0], True), (128, 2, 2, [255, 1, 257], True),
-    (64, 2, 8, [300, 5, 700], True), (128, 1, 3, [190, 64], True), (64, 1, 7, [100, 333], False),
+    (64, 2, 8, [300, 5, 700], True), (128, 2, 5, [37, 1, 260], True), (64, 1, 12, [9, 130], False), (128, 1, 6, [300, 43], True),
+    (64, 1, 48, [70, 3], True), (128, 1, 19, [14], False), (128, 1, 3, [190, 64], True), (64, 1, 7, [100, 333], False),
     (128, 1, 16, [130, 40], True), (128, 4, 1, [513], True), (64, 1, 5, [385, 1, 1, 1], True),
     (128, 1, 128, [3, 2], True), (64, 1, 200, [5], True), (128, 1, 6, [260], False),
 ]
