@@ -233,10 +233,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 
 // A work item: 2 x 128 rows.
 struct Item {
@@ -257,20 +253,30 @@ __device__ __forceinline__ int2 seq_rows(const PromptParams &p, int s) {
     return make_int2(a, b);
 }
 
+// A sequence's rows and its number of items a head pack (0 past the last sequence).
+struct SeqItems {
+    int2 rows;
+    int n;
+};
+__device__ __forceinline__ SeqItems seq_items(const PromptParams &p, int toks, int s) {
+    SeqItems q;
+    q.rows = s < p.n_seq ? seq_rows(p, s) : make_int2(0, 0);
+    q.n = (q.rows.y - q.rows.x + toks - 1) / toks;
+    return q;
+}
+
 // Item `index` in the order of falling length: items are (token tile l of its
 // sequence, sequence, head pack), all tiles of the largest l first, so that the
 // longest run first whatever the lengths are. One warp; false past the last.
-__device__ __forceinline__ bool find_item(const PromptParams &p, int pack, int index, Item &item) {
+// mine: of sequence `lane`, so that up to 32 sequences are read once a block
+// (read again for each question, 16 packed prompts took 48.5 us instead of 45.2).
+__device__ __forceinline__ bool find_item(const PromptParams &p, int pack, int index, const SeqItems &mine, Item &item) {
     const int lane = threadIdx.x & 31, packs = p.n_heads / pack, toks = 2 * (kTileRows / pack);
     const int rank = index / packs;
     // tiles with number >= l
     auto tiles_from = [&](int l) {
-        int n = 0;
-        for (int s = lane; s < p.n_seq; s += 32) {
-            const int2 r = seq_rows(p, s);
-            const int t = (r.y - r.x + toks - 1) / toks;
-            n += t > l ? t - l : 0;
-        }
+        int n = max(mine.n - l, 0);
+        for (int s = lane + 32; s < p.n_seq; s += 32) n += max(seq_items(p, toks, s).n - l, 0);
         return __reduce_add_sync(0xffffffffu, n);
     };
     if (rank >= tiles_from(0)) return false;
@@ -283,10 +289,8 @@ __device__ __forceinline__ bool find_item(const PromptParams &p, int pack, int i
     }
     int skip = rank - tiles_from(lo + 1);  // sequences with a tile lo before the item's
     for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-        const int s = s0 + lane;
-        int2 r = make_int2(0, 0);
-        if (s < p.n_seq) r = seq_rows(p, s);
-        uint32_t has = __ballot_sync(0xffffffffu, (r.y - r.x + toks - 1) / toks > lo);
+        const SeqItems q = s0 == 0 ? mine : seq_items(p, toks, s0 + lane);
+        uint32_t has = __ballot_sync(0xffffffffu, q.n > lo);
         const int n = __popc(has);
         if (skip >= n) {
             skip -= n;
@@ -294,8 +298,8 @@ __device__ __forceinline__ bool find_item(const PromptParams &p, int pack, int i
         }
         for (; skip > 0; --skip) has &= has - 1;
         const int at = __ffs(has) - 1;
-        item.start = __shfl_sync(0xffffffffu, r.x, at);
-        item.end = __shfl_sync(0xffffffffu, r.y, at);
+        item.start = __shfl_sync(0xffffffffu, q.rows.x, at);
+        item.end = __shfl_sync(0xffffffffu, q.rows.y, at);
         break;
     }
     item.tok0 = lo * toks;
@@ -587,10 +591,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- items
             bool ok = true;
             int index = blockIdx.x;
+            const SeqItems mine = seq_items(p, 2 * tile_toks, lane);
             for (int k = 0; ok; ++k) {
                 Item it;
                 // (an index that is no item ends the block as the launch's end does: none after it is one)
-                it.last = index < 0 || !find_item(p, pack, index, it);
+                it.last = index < 0 || !find_item(p, pack, index, mine, it);
                 if (!it.last && lane == 0) {
                     fence_proxy_async_smem();  // the last answer has been read
                     mbar_arrive_expect_tx(block_bar, 16);
