@@ -135,7 +135,7 @@ def _place(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     device = t.get_device()
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is not on the current CUDA device")
     return device
 
@@ -163,7 +163,7 @@ class KVCache:
     """A paged cache of keys and values held in 4 bits (the layout of
     qkv_cache in include/qattn.h) over `data`, a uint8 CUDA tensor whose size
     says how many pages it has. Allocates and keeps nothing else."""
-    __slots__ = ("n_kv_heads", "head_dim", "page_size", "n_pages", "data", "c", "ref")
+    __slots__ = ("n_kv_heads", "head_dim", "page_size", "n_pages", "data", "device", "c", "ref")
 
     def __init__(self, n_kv_heads: int, head_dim: int, page_size: int, data):
         if not isinstance(data, torch.Tensor) or not data.is_cuda or data.dtype != torch.uint8:
@@ -179,7 +179,7 @@ class KVCache:
         if total != data.numel():
             raise ValueError(f"data holds {data.numel()} bytes, not a number of pages of {page}")
         self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
-        self.data = data
+        self.data, self.device = data, data.get_device()
         self.c = _Cache(data.data_ptr(), n_pages, n_kv_heads, head_dim, page_size)
         self.ref = ctypes.byref(self.c)
 
@@ -210,7 +210,8 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope=None, rope_pairs
     k_out's type or else q's), and the rotated k and v to k_out and v_out where
     given. Inputs float32 or float16, of one type; outputs likewise. Returns q_out."""
     device = _place(k, "k")
-    _on(cache.data, device, "the cache", torch.uint8)
+    if cache.device != device:
+        raise ValueError(f"the cache is on cuda:{cache.device}, not on cuda:{device}")
     d, t = cache.head_dim, k.dtype
     k_ptr, k_stride, n, n_kv = _rows(k, device, "k", d, _TYPE)
     v_ptr, v_stride, n_v, n_kv_v = _rows(v, device, "v", d, (t,))
@@ -260,7 +261,8 @@ def kv_read(cache: KVCache, slots, k_out=None, v_out=None, stream=None):
     zeros for a slot < 0. Both are allocated if neither is given; one given
     alone is read alone."""
     device = _place(slots, "slots")
-    _on(cache.data, device, "the cache", torch.uint8)
+    if cache.device != device:
+        raise ValueError(f"the cache is on cuda:{cache.device}, not on cuda:{device}")
     slots_ptr = _on(slots, device, "slots", torch.int32)
     if slots.dim() != 1:
         raise ValueError("slots must be [n]")
@@ -291,7 +293,8 @@ def kv_attend(cache: KVCache, q, table, lengths, q_offsets=None, max_q_len: int 
     each sees the tokens up to its own. scale: 1 / sqrt(D) by default. Returns
     out [n_tok, heads, D] in q's type; zeros for a row that sees nothing."""
     device = _place(q, "q")
-    _on(cache.data, device, "the cache", torch.uint8)
+    if cache.device != device:
+        raise ValueError(f"the cache is on cuda:{cache.device}, not on cuda:{device}")
     d = cache.head_dim
     q_ptr, q_stride, n_tok, heads = _rows(q, device, "q", d, _TYPE)
     if heads < 1 or heads % cache.n_kv_heads:

@@ -95,8 +95,8 @@ typedef struct {
 int qkv_append(const qkv_cache *cache, const qkv_append_args *args, qg_stream_t stream);
 
 /* The values of the rows `slots` of the cache, (code - 8) d, exact in f32:
- * k_out and v_out f32 [n][n_kv_heads][D], either may be NULL. A slot < 0 or
- * past the cache gives zeros (past it, code 4 as well). */
+ * k_out and v_out f32 [n][n_kv_heads][D], either may be NULL; at most 2^30
+ * rows. A slot < 0 or past the cache gives zeros (past it, code 4 as well). */
 int qkv_read(const qkv_cache *cache, const int32_t *slots, int64_t n, float *k_out, float *v_out, qg_stream_t stream);
 
 /* ---- Attention over the cache ---------------------------------------------- */
