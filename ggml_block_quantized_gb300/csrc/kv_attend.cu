@@ -941,8 +941,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvAttend
             float nt = top;
 #pragma unroll
             for (int j = 0; j < 4; ++j) nt = fmaxf(nt, ml[j].x);
-            if (nt == -INFINITY) continue;
-            const float keep = exp2_approx(top - nt);
+            const float ref = nt == -INFINITY ? 0.0f : nt;  // (nothing seen: zeros; scores that are NaN: NaN)
+            const float keep = exp2_approx(top - ref);
             top = nt;
             den *= keep;
 #pragma unroll
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvAttend
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (i0 + j * kJoinWarps >= cut.parts) break;
-                const float f = exp2_approx(ml[j].x - top);
+                const float f = exp2_approx(ml[j].x - ref);
                 den = fmaf(ml[j].y, f, den);
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) acc[k] = fmaf(v[j][k], f, acc[k]);
@@ -965,14 +965,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvAttend
             top = -INFINITY, den = 0.0f;
 #pragma unroll
             for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w].x);
+            const float ref = top == -INFINITY ? 0.0f : top;
             float2 sum = make_float2(0.0f, 0.0f);
-            if (top != -INFINITY)
 #pragma unroll
-                for (int w = 0; w < kJoinWarps; ++w) {
-                    const float f = exp2_approx(stats[w].x - top);
-                    den = fmaf(stats[w].y, f, den);
-                    sum.x = fmaf(sums[w][d], f, sum.x), sum.y = fmaf(sums[w][d + 1], f, sum.y);
-                }
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float f = exp2_approx(stats[w].x - ref);
+                den = fmaf(stats[w].y, f, den);
+                sum.x = fmaf(sums[w][d], f, sum.x), sum.y = fmaf(sums[w][d + 1], f, sum.y);
+            }
             const int row = cut.row0 + r, tok = row / p.group;
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
             store2(static_cast<T *>(p.out) +

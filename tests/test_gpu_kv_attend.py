@@ -171,6 +171,24 @@ def test_infinite_and_nan_tokens_reach_only_those_who_see_them():
     check(got[:3], q[:3], [ks[0][:97]], [vs[0][:97]], [97], [3], 4, d ** -0.5, False)
 
 
+@pytest.mark.parametrize("t", [torch.float32, torch.float16], ids=["f32", "f16"])
+@pytest.mark.parametrize("lens", [[5, 40], [777, 3, 40000]], ids=["short", "split"])
+def test_nan_queries_give_nan(t, lens):
+    """A query that is not a number makes its own row NaN, split over thread blocks or not, and no other one."""
+    rng = np.random.default_rng(31)
+    cache, table, ks, vs = filled(rng, lens, 2, 128, 32)
+    q = torch.from_numpy(rng.standard_normal((len(lens), 8, 128)).astype(np.float32)).cuda().to(t)
+    clean = qg.kv_attend(cache, q, i32(table), i32(lens))
+    check(clean, q, ks, vs, lens, [1] * len(lens), 4, 128 ** -0.5, t == torch.float16)
+    q[0, 1, 77] = float("nan")
+    q[-1, 6] = float("nan")
+    got = qg.kv_attend(cache, q, i32(table), i32(lens))
+    assert torch.isnan(got[0, 1]).all() and torch.isnan(got[-1, 6]).all()
+    rest = torch.ones(len(lens), 8, dtype=torch.bool, device="cuda")
+    rest[0, 1] = rest[-1, 6] = False
+    assert torch.equal(got[rest], clean[rest])
+
+
 def test_indexes_out_of_range():
     """A bad page counts as unseen, a length past the table as the table's end, a bad sequence is left out."""
     rng = np.random.default_rng(21)
