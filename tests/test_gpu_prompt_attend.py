@@ -141,6 +141,26 @@ def test_infinite_value_that_is_seen():
     assert bool(clean.all())
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 3), (128, 4)])
+def test_a_query_that_is_not_finite(d, group, bad):
+    """It gives NaN in its own row and head and changes no other one (a query with an infinity has scores of both
+    signs of it, or NaN)."""
+    rng = np.random.default_rng(35)
+    lens = [290, 33]
+    q, k, v = (t.clone() for t in inputs(rng, sum(lens), 2 * group, 2, d, fused=False))
+    clean = qg.prompt_attend(q, k, v, i32([0, 290, 323]))
+    rows, heads = [7, 200, 289, 291, 322], [0, 2 * group - 1, group, group - 1, 1]
+    for r, h in zip(rows, heads):
+        q[r, h, ::9] = bad
+    got = qg.prompt_attend(q, k, v, i32([0, 290, 323]))
+    rest = torch.ones(323, 2 * group, dtype=torch.bool, device="cuda")
+    for r, h in zip(rows, heads):
+        assert torch.isnan(got[r, h]).all()
+        rest[r, h] = False
+    assert torch.equal(got[rest], clean[rest])
+
+
 def test_strides_rows_in_no_sequence_and_stream():
     rng = np.random.default_rng(34)
     q, k, v = inputs(rng, 100, 4, 2, 64)
