@@ -189,6 +189,21 @@ def test_nan_queries_give_nan(t, lens):
     assert torch.equal(got[rest], clean[rest])
 
 
+@pytest.mark.parametrize("t", [torch.float32, torch.float16], ids=["f32", "f16"])
+def test_infinite_queries_give_nan(t):
+    """Infinities in a query have scores of both signs of it, or NaN: its row is NaN, and no other one."""
+    rng, lens = np.random.default_rng(36), [300, 9000]
+    cache, table, ks, vs = filled(rng, lens, 2, 64, 16)
+    q = torch.from_numpy(rng.standard_normal((2, 6, 64)).astype(np.float32)).cuda().to(t)
+    clean = qg.kv_attend(cache, q, i32(table), i32(lens))
+    q[0, 4, ::9], q[1, 0, ::5] = float("inf"), -float("inf")
+    got = qg.kv_attend(cache, q, i32(table), i32(lens))
+    assert torch.isnan(got[0, 4]).all() and torch.isnan(got[1, 0]).all()
+    rest = torch.ones(2, 6, dtype=torch.bool, device="cuda")
+    rest[0, 4] = rest[1, 0] = False
+    assert torch.equal(got[rest], clean[rest])
+
+
 def test_indexes_out_of_range():
     """A bad page counts as unseen, a length past the table as the table's end, a bad sequence is left out."""
     rng = np.random.default_rng(21)
