@@ -48,9 +48,10 @@
 // it goes into the consumers' instructions, about 700 and 900 a tile, at 55 and
 // 57% of the issue slots with the 12 warps a multiprocessor that 128 registers
 // allow (14 in two larger blocks were no faster). 24 sequences of 200 .. 4096
-// tokens, 32 heads of 128, f16: 58.9 us, 4.0 TB/s; one of 131071, 64 query and 8
-// key heads, f32: 50.4 us, 3.0 TB/s; 777 tokens, 32 and 8 heads, f32: 8.6 us, of
-// which the two launches, the start and the join are most.
+// tokens, 32 heads of 128, f16: 58.7 us, 4.0 TB/s; one of 131071, 64 query and 8
+// key heads, f32: 50.0 us, 3.0 TB/s; 777 tokens, 32 and 8 heads, f32: 7.9 us, of
+// which a tile's work is 1.1: the rest is the place in the list (1.0), the queries
+// (1.3), the join (0.5 and 1.1) and the launches.
 #include <atomic>
 
 #include "kv_cache.cuh"
@@ -148,8 +149,36 @@ struct Place {
     int64_t share;  // units of a block's part
 };
 
-// Finds the part of block `cta` of `ctas` (with the whole block: every thread
-// gets the result). seq = n_seq where the part is empty.
+// The parts' size.
+__device__ __forceinline__ int64_t part_share(int64_t units, int ctas) {
+    const int64_t share = (units + ctas - 1) / ctas;
+    return share < kLeast ? kLeast : share;
+}
+
+// Finds the part of block `cta` of `ctas`: up to 32 sequences, every warp by
+// itself. seq = n_seq where the part is empty.
+__device__ __forceinline__ Place locate_few(const KvAttendParams &p, int rows, int64_t cta, int ctas) {
+    const int lane = threadIdx.x & 31;
+    const int64_t mine = lane < p.n_seq ? seq_units(p, lane, rows) : 0;
+    int64_t past = mine;  // units of the sequences up to this one
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, past, m);
+        if (lane >= m) past += o;
+    }
+    Place r;
+    r.units = __shfl_sync(0xffffffffu, past, 31);
+    r.share = part_share(r.units, ctas);
+    const int64_t u = cta * r.share;
+    const uint32_t after = __ballot_sync(0xffffffffu, past > u);
+    r.seq = after == 0 ? p.n_seq : __ffs(after) - 1;
+    r.at = u - __shfl_sync(0xffffffffu, past - mine, r.seq & 31);
+    return r;
+}
+
+// The same for any number of sequences, with the whole block (every thread gets
+// the result). 32 sequences of 100 tokens take 10.7 us in all with it and 10.3 with
+// the one above; 777 tokens of one 8.0 and 7.9.
 template <int THREADS> __device__ Place locate(const KvAttendParams &p, int rows, int64_t cta, int ctas) {
     __shared__ int64_t warp_sum[THREADS / 32];
     __shared__ int found_seq;
@@ -167,8 +196,7 @@ template <int THREADS> __device__ Place locate(const KvAttendParams &p, int rows
     r.units = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) r.units += warp_sum[w];
-    r.share = (r.units + ctas - 1) / ctas;
-    if (r.share < kLeast) r.share = kLeast;
+    r.share = part_share(r.units, ctas);
     const int64_t u = cta * r.share;
     if (u < r.units) {
         int64_t base = 0;
@@ -386,7 +414,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     }
     pdl_wait_prior_grids();
     pdl_allow_dependents();
-    const Place place = locate<kThreads>(p, ROWS, blockIdx.x, gridDim.x);  // (synchronizes the block)
+    __syncthreads();
+    const Place place = p.n_seq <= 32 ? locate_few(p, ROWS, blockIdx.x, gridDim.x) : locate<kThreads>(p, ROWS, blockIdx.x, gridDim.x);
     const int64_t u0 = static_cast<int64_t>(blockIdx.x) * place.share;
     int64_t units = place.units - u0;
     if (units > place.share) units = place.share;
