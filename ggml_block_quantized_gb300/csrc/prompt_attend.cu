@@ -319,25 +319,34 @@ __device__ __forceinline__ bool find_item(const PromptParams &p, int pack, int i
     return true;
 }
 
-// Sixteen values in one (f16) or two (f32) 32-byte stores.
-__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+// 32 bytes in one store, or in two where `out` (and with it every row, a multiple
+// of 32 bytes) lies only on the 16-byte boundary that the interface asks for: a
+// 32-byte store there would fault.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool wide) {
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else {
+        uint4 *q = static_cast<uint4 *>(p);
+        q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
-__device__ __forceinline__ void store16(__half *p, const float (&x)[16]) {
+// Sixteen values.
+__device__ __forceinline__ void store16(__half *p, const float (&x)[16], bool wide) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack_half2(x[2 * i], x[2 * i + 1]);
-    store32(p, w);
+    store32(p, w, wide);
 }
-__device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
+__device__ __forceinline__ void store16(float *p, const float (&x)[16], bool wide) {
     uint32_t w[8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * h + i]);
-        store32(p + 8 * h, w);
+        store32(p + 8 * h, w, wide);
     }
 }
 
@@ -811,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fewer_registers<64>();
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         int n_items[2] = {0, 0};
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -856,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int e = 0; e < 16; ++e)
                                     if ((__half_as_ushort(row_v[e]) & 0x7C00u) == 0x7C00u) y[e] += __half2float(row_v[e]);
                             }
-                        store16(out + i + q, y);
+                        store16(out + i + q, y, wide);
                     }
                     __syncwarp();
                 }

@@ -174,6 +174,25 @@ def test_strides_rows_in_no_sequence_and_stream():
     check(out[10:90], q[10:90], k[10:90], v[10:90], [30, 50], 64 ** -0.5)
 
 
+@pytest.mark.parametrize("t", [torch.float16, torch.float32], ids=["f16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_an_output_on_a_16_byte_boundary(d, t):
+    """`out` begins 16 bytes into a buffer: the same bits, and nothing beside it."""
+    rng = np.random.default_rng(37)
+    lens = [140, 3]
+    q, k, v = inputs(rng, sum(lens), 6, 2, d)
+    off = i32([0, 140, 143])
+    want = qg.prompt_attend(q, k, v, off, out=torch.empty(143, 6, d, dtype=t, device="cuda"))
+    check(want, q, k, v, lens, d ** -0.5, f16=t == torch.float16)
+    pad = 16 // want.element_size()
+    buffer = torch.full((pad + want.numel() + pad,), 9.0, dtype=t, device="cuda")
+    out = buffer[pad:-pad].view(143, 6, d)
+    assert out.data_ptr() % 32 == 16
+    qg.prompt_attend(q, k, v, off, out=out)
+    assert torch.equal(out, want)
+    assert bool((buffer[:pad] == 9).all()) and bool((buffer[-pad:] == 9).all())
+
+
 def test_offsets_out_of_range():
     rng = np.random.default_rng(35)
     q, k, v = inputs(rng, 50, 2, 1, 64)
