@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots);
     const uint32_t qfull = base + 20 * Sh::kSlots + 16, qempty = qfull + 8;
     __shared__ Walk walks[kWarps];
-    volatile int *const odd_flag = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots + 8);
+    // one for each of two segments in turn: see the join
+    volatile int *const odd_flags = reinterpret_cast<volatile int *>(smem + 20 * Sh::kSlots + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Sh::kSlots; ++s) {
@@ -529,13 +530,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     bool ok = true;
     while (seg.left > 0) {
         const int n = seg.n_tiles(), tile0 = seg.first_tile();
+        volatile int *const odd_flag = odd_flags + phase_q;
         // ---- the segment's queries, as the mma's B fragments
         if (ok && !__all_sync(0xffffffffu, wait_bounded(qfull, phase_q, abort_flag))) {
             if (lane == 0) record_error(p.err, kErrConsumerWait);
             *abort_flag = 1;
             ok = false;
         }
-        phase_q ^= 1u;
         {
             const uint32_t raw = base + Sh::kOffRaw;
             const int rows = seg.q.m * p.group, row0 = seg.rt * ROWS, before = seg.q.len - seg.q.m + 1;
@@ -863,11 +864,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
             }
         const int units = seg.count();
         const bool from = seg.tile == 0, whole = from && units == seg.tiles;
+        // A row's channels by 16 / NT threads, four at a time. What the rows' preparation wrote is read before the
+        // barrier: a warp that is through with the join prepares the next segment's rows while others still join,
+        // and the warp that prepares a row need not be the one that joins it.
+        constexpr int kPer = 16 / NT;
+        const int r = threadIdx.x / kPer, out_row = row_out[r], limit = row_limit[r];
         named_barrier(1, kWarps * 32);
         {
-            // a row's channels by 16 / NT threads, four at a time
-            constexpr int kPer = 16 / NT;
-            const int r = threadIdx.x / kPer, out_row = row_out[r];
             if (out_row >= 0) {
                 float2 ml[kWarps];
                 float top = -INFINITY, den = 0.0f;
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         sum.x = fmaf(v.x, f[w], sum.x), sum.y = fmaf(v.y, f[w], sum.y);
                         sum.z = fmaf(v.z, f[w], sum.z), sum.w = fmaf(v.w, f[w], sum.w);
                     }
-                    if (odd && odd_tokens<D>(p, seg, row_limit[0], row_limit[r], tile0 * kTile, (tile0 + n) * kTile, d >> 5))
+                    if (odd && odd_tokens<D>(p, seg, least, limit, tile0 * kTile, (tile0 + n) * kTile, d >> 5))
                         sum.x = sum.y = sum.z = sum.w = NAN;
                     if (whole) {
                         store2(out + d, sum.x * inv, sum.y * inv);
@@ -917,7 +920,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                            min(ROWS, seg.q.m * p.group - row0), row0, seg.q.q0, seg.head, {0, 0, 0}};
             }
         }
-        // the next segment's first barrier comes after these reads; the join's areas are written after it
+        // The join's areas are written again after the next segment's first barrier, which comes after these reads; its
+        // flag is cleared for the next segment but one, after the next one's last barrier.
+        phase_q ^= 1u;
         k -= n;
         __syncwarp();
         if (lane == 0) seg.next(p, ROWS);

@@ -171,6 +171,44 @@ def test_infinite_and_nan_tokens_reach_only_those_who_see_them():
     check(got[:3], q[:3], [ks[0][:97]], [vs[0][:97]], [97], [3], 4, d ** -0.5, False)
 
 
+@pytest.mark.parametrize("t", ["f32", "f16"])
+@pytest.mark.parametrize("d,group,per", [(64, 2, 4), (128, 3, 4), (128, 1, 8), (64, 3, 5)], ids=lambda x: str(x))
+def test_segments_one_after_another_in_a_thread_block(d, group, per, t):
+    """More segments than thread blocks, each of a few tiles, so that a block goes from one to the next; in every other
+    sequence the values of a token that only the later queries see are not finite. Each row has its own result in its
+    own place, NaN in the affected block's channels where it sees the token, and the same bits each time."""
+    rng = np.random.default_rng(41)
+    n_seq, hk = 150, 8
+    lens = rng.integers(per, 120, n_seq).tolist()
+    cache, table, ks, vs = filled(rng, lens, hk, d, 16)
+    marked = list(range(0, n_seq, 2))
+    for s in marked:  # the third token from the end: its second value block's scale becomes NaN
+        tok = lens[s] - 3
+        slot = int(table[s, tok // 16]) * 16 + tok % 16
+        for h in range(hk):
+            at = attn_ref.slot_bytes(16, hk, d, slot, h)[3][1]
+            cache.data[torch.from_numpy(at).cuda()] = torch.tensor([0, 0x7E], dtype=torch.uint8, device="cuda")
+    q = torch.from_numpy(rng.standard_normal((n_seq * per, hk * group, d)).astype(np.float32)).cuda().to(TYPES[t])
+    off = i32(np.arange(n_seq + 1) * per)
+    got = qg.kv_attend(cache, q, i32(table), i32(lens), q_offsets=off, max_q_len=per)
+    for _ in range(10):
+        again = qg.kv_attend(cache, q, i32(table), i32(lens), q_offsets=off, max_q_len=per)
+        assert torch.equal(got.nan_to_num(7.0), again.nan_to_num(7.0))
+    sees = torch.zeros(n_seq, per, dtype=torch.bool, device="cuda")
+    sees[::2, per - 3:] = True
+    nan = torch.isnan(got)
+    want = sees.view(-1, 1, 1) & ((torch.arange(d, device="cuda") // 32) == 1)
+    assert torch.equal(nan, want.expand_as(nan))
+    filled_in = torch.where(nan, torch.zeros_like(got), got)
+    some = [s for s in range(n_seq) if s % 2 or s % 10 == 0]
+    for s in some:
+        rows = slice(s * per, (s + 1) * per)
+        keep = torch.ones(per, dtype=torch.bool) if s % 2 else ~sees[s].cpu()
+        m = int(keep.sum())
+        check(filled_in[rows][:m], q[rows][:m], [ks[s][:lens[s] - per + m]], [vs[s][:lens[s] - per + m]],
+              [lens[s] - per + m], [m], group, d ** -0.5, t == "f16")
+
+
 @pytest.mark.parametrize("t", [torch.float32, torch.float16], ids=["f32", "f16"])
 @pytest.mark.parametrize("lens", [[5, 40], [777, 3, 40000]], ids=["short", "split"])
 def test_nan_queries_give_nan(t, lens):
