@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(o[e], s[e]));
         };
-        const bool full = left - aside >= kBatch;
+        const bool full = left + aside >= kBatch;  // (all rows of the batch are there: alike in every lane)
         if (is_q) {
             if (full && ok) {
 #pragma unroll

@@ -111,6 +111,23 @@ def test_append_bytes(case):
     assert torch.equal(alone, k_rows)
 
 
+@pytest.mark.parametrize("n,heads,hk", [(3, 2, 1), (40, 8, 2), (1500, 4, 4), (1500, 6, 2), (9000, 16, 1), (9000, 18, 3)])
+def test_batches_that_end_with_the_heads(n, heads, hk):
+    """Heads of 64, two side by side in a warp, one, two and eight pairs at a time: query heads that fill a token's
+    last batch, and ones that end a head or a pair before its end, each rotated by halves."""
+    d, page = 64, 16
+    rng = np.random.default_rng(n + heads)
+    x = rng.standard_normal((n, heads + 2 * hk, d)).astype(np.float32)
+    table, pos = rng.standard_normal((31, d // 2, 2)).astype(np.float32), rng.integers(0, 31, n).astype(np.int32)
+    cache = qg.KVCache.empty(-(-n // page), hk, d, page)
+    xd = dev(x)
+    q, k, v = xd[:, :heads], xd[:, heads:heads + hk], xd[:, heads + hk:]
+    k_out = torch.empty(n, hk, d, device="cuda")
+    got = qg.kv_append(cache, k, v, dev(np.arange(n, dtype=np.int32)), positions=dev(pos), rope=dev(table), q=q, k_out=k_out)
+    assert same_bits(got.cpu().numpy(), attn_ref.rotate(x[:, :heads], table[pos], False, np.float32))
+    assert same_bits(k_out.cpu().numpy(), attn_ref.rotate(x[:, heads:heads + hk], table[pos], False, np.float32))
+
+
 def test_special_values_keep_the_quantizer_rule():
     """NaN, infinite and subnormal rows get the bytes that Q4_0's rule gives them."""
     d, page = 128, 16
