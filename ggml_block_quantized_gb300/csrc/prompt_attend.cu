@@ -272,52 +272,126 @@ __device__ __forceinline__ SeqItems seq_items(const PromptParams &p, int toks, i
     return q;
 }
 
-// Item `index` in the order of falling length: items are (token tile l of its
-// sequence, sequence, head pack), all tiles of the largest l first, so that the
-// longest run first whatever the lengths are. One warp; false past the last.
-// mine: of sequence `lane`, so that up to 32 sequences are read once a block
-// (read again for each question, 16 packed prompts took 48.5 us instead of 45.2).
-__device__ __forceinline__ bool find_item(const PromptParams &p, int pack, int index, const SeqItems &mine, Item &item) {
-    const int lane = threadIdx.x & 31, packs = p.n_heads / pack, toks = 2 * (kTileRows / pack);
-    const int rank = index / packs;
-    // tiles with number >= l
-    auto tiles_from = [&](int l) {
-        int n = max(mine.n - l, 0);
-        for (int s = lane + 32; s < p.n_seq; s += 32) n += max(seq_items(p, toks, s).n - l, 0);
-        return __reduce_add_sync(0xffffffffu, n);
-    };
-    if (rank >= tiles_from(0)) return false;
-    // the level l with tiles_from(l + 1) <= rank < tiles_from(l)
-    int lo = 0, hi = (p.n_tok + toks - 1) / toks;  // tiles_from(lo) > rank >= tiles_from(hi)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (tiles_from(mid) > rank) lo = mid;
-        else hi = mid;
+// Finds items by their index, one warp together. Items come in groups of `packs`
+// (one for each head pack); the groups of a launch of up to 32 sequences are
+// (token tile l of its sequence, sequence), all tiles of the largest l first, so
+// that the longest run first whatever the lengths are. With more sequences that
+// order would take several looks at all of them for each item: there the groups
+// are (class, sequence, l from its last tile on), class the power of two of the
+// sequence's tiles, the largest first. The classes' sizes are counted once a
+// block, and since indexes mostly rise from call to call, the search goes on at
+// the 32 sequences where the last one ended: a block looks at each sequence about
+// once a class, and an item never costs more than one look at all of them. (With
+// the first order's search for each item 33 prompts of 5 .. 60 tokens, 32 and 8
+// heads of 128, took 26.9 us instead of 23.4, 256 151 instead of 74, 4096 27 ms
+// instead of 1.07, and hundreds of thousands seconds, past the waits' limit in the
+// end; 64 of 700, where the order counts for most, 340 instead of 344.)
+struct ItemFinder {
+    SeqItems q;            // of sequence s0 + lane
+    int packs, toks, s0;
+    int64_t before, count; // lane c: groups of the classes above c, and of c
+    int cls, base;         // where the last search ended: its class, the class's groups in the sequences before s0
+
+    __device__ __forceinline__ int class_of() const { return 31 - __clz(q.n); }  // (-1 without tiles)
+    __device__ __forceinline__ void look(const PromptParams &p, int s) {
+        s0 = s;
+        q = seq_items(p, toks, s + (threadIdx.x & 31));
     }
-    int skip = rank - tiles_from(lo + 1);  // sequences with a tile lo before the item's
-    for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-        const SeqItems q = s0 == 0 ? mine : seq_items(p, toks, s0 + lane);
-        uint32_t has = __ballot_sync(0xffffffffu, q.n > lo);
-        const int n = __popc(has);
-        if (skip >= n) {
-            skip -= n;
-            continue;
+
+    __device__ __forceinline__ void start(const PromptParams &p, int pack) {
+        packs = p.n_heads / pack, toks = 2 * (kTileRows / pack);
+        const int lane = threadIdx.x & 31;
+        before = count = 0;
+        cls = -1, base = 0;
+        if (p.n_seq > 32) {
+            SeqItems next = seq_items(p, toks, lane);
+            for (int s = 0; s < p.n_seq; s += 32) {
+                q = next;
+                if (s + 32 < p.n_seq) next = seq_items(p, toks, s + 32 + lane);
+                uint32_t left = __ballot_sync(0xffffffffu, q.n > 0);
+                while (left) {
+                    const int c = __shfl_sync(0xffffffffu, class_of(), __ffs(left) - 1);
+                    const bool in = class_of() == c;
+                    const int n = __reduce_add_sync(0xffffffffu, in ? q.n : 0);
+                    if (lane == c) count += n;
+                    left &= ~__ballot_sync(0xffffffffu, in);
+                }
+            }
+            int64_t from = count;  // groups of the classes from the lane's on
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t o = __shfl_down_sync(0xffffffffu, from, m);
+                if (lane + m < 32) from += o;
+            }
+            before = from - count;
         }
-        for (; skip > 0; --skip) has &= has - 1;
-        const int at = __ffs(has) - 1;
+        look(p, 0);
+    }
+
+    // The sequence (its lane among q) and token tile of group `rank`; false past the last.
+    __device__ __forceinline__ bool find_by_tile(const PromptParams &p, int rank, int &at, int &tile) const {
+        auto tiles_from = [&](int l) { return __reduce_add_sync(0xffffffffu, max(q.n - l, 0)); };
+        if (rank >= tiles_from(0)) return false;
+        // the level l with tiles_from(l + 1) <= rank < tiles_from(l)
+        int lo = 0, hi = (p.n_tok + toks - 1) / toks;  // tiles_from(lo) > rank >= tiles_from(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (tiles_from(mid) > rank) lo = mid;
+            else hi = mid;
+        }
+        uint32_t has = __ballot_sync(0xffffffffu, q.n > lo);
+        for (int skip = rank - tiles_from(lo + 1); skip > 0; --skip) has &= has - 1;  // sequences with a tile lo before it
+        at = __ffs(has) - 1;
+        tile = lo;
+        return true;
+    }
+    __device__ __forceinline__ bool find_by_class(const PromptParams &p, int rank, int &at, int &tile) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t is = __ballot_sync(0xffffffffu, rank >= before && rank < before + count);
+        if (is == 0) return false;
+        const int c = __ffs(is) - 1;
+        const int r = rank - static_cast<int>(__shfl_sync(0xffffffffu, before, c));
+        if (c != cls || r < base) {
+            cls = c, base = 0;
+            if (s0 != 0) look(p, 0);
+        }
+        for (;;) {
+            const int mine = class_of() == c ? q.n : 0;
+            int past = mine;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, past, m);
+                if (lane >= m) past += o;
+            }
+            const uint32_t after = __ballot_sync(0xffffffffu, past > r - base);
+            if (after != 0) {
+                at = __ffs(after) - 1;
+                tile = __shfl_sync(0xffffffffu, past, at) - 1 - (r - base);
+                return true;
+            }
+            base += __shfl_sync(0xffffffffu, past, 31);
+            if (s0 + 32 >= p.n_seq) return false;  // (the count above has it among them)
+            look(p, s0 + 32);
+        }
+    }
+
+    // Item `index`; false past the last.
+    __device__ __forceinline__ bool find(const PromptParams &p, int pack, int index, Item &item) {
+        const int rank = index / packs;
+        int at, tile;
+        if (!(p.n_seq <= 32 ? find_by_tile(p, rank, at, tile) : find_by_class(p, rank, at, tile))) return false;
         item.start = __shfl_sync(0xffffffffu, q.rows.x, at);
         item.end = __shfl_sync(0xffffffffu, q.rows.y, at);
-        break;
+        item.tok0 = tile * toks;
+        item.head0 = (index - rank * packs) * pack;
+        const int len = item.end - item.start;
+        for (int x = 0; x < 2; ++x) {
+            const int first = item.tok0 + x * (toks / 2), past = min(len, first + toks / 2);
+            item.tiles[x] = first < len ? (past + kTileKeys - 1) / kTileKeys : 0;
+        }
+        return true;
     }
-    item.tok0 = lo * toks;
-    item.head0 = (index % packs) * pack;
-    const int len = item.end - item.start;
-    for (int x = 0; x < 2; ++x) {
-        const int first = item.tok0 + x * (toks / 2), past = min(len, first + toks / 2);
-        item.tiles[x] = first < len ? (past + kTileKeys - 1) / kTileKeys : 0;
-    }
-    return true;
-}
+};
 
 // 32 bytes in one store, or in two where `out` (and with it every row, a multiple
 // of 32 bytes) lies only on the 16-byte boundary that the interface asks for: a
@@ -607,17 +681,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- items
             bool ok = true;
             int index = blockIdx.x;
-            const SeqItems mine = seq_items(p, 2 * tile_toks, lane);
-            for (int k = 0; ok; ++k) {
-                Item it;
-                // (an index that is no item ends the block as the launch's end does: none after it is one)
-                it.last = index < 0 || !find_item(p, pack, index, mine, it);
-                if (!it.last && lane == 0) {
+            uint32_t asked = 0;
+            ItemFinder finder;
+            finder.start(p, pack);
+            auto ask = [&]() {
+                if (lane == 0) {
                     fence_proxy_async_smem();  // the last answer has been read
                     mbar_arrive_expect_tx(block_bar, 16);
                     ask_block(block_answer, block_bar);
                 }
-                if (k >= kItems) ok = __all_sync(0xffffffffu, sleep_wait<200>(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
+            };
+            auto take_answer = [&]() {  // (waited for in every case: it must not arrive after the block's end)
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(block_bar, asked++ & 1u)) && ok;
+                if (ok) index = asked_block(block_answer);
+                __syncwarp();
+            };
+            for (int k = 0; ok; ++k) {
+                Item it;
+                it.last = index < 0 || !finder.find(p, pack, index, it);
+                // The launch has blocks for a tile of every sequence that its rows may not fill; those that turn out to be
+                // no items are taken over, too, rather than left to start one after another.
+                while (it.last && index >= 0 && ok) {
+                    ask();
+                    take_answer();
+                    it.last = index < 0 || !ok || !finder.find(p, pack, index, it);
+                }
+                if (!it.last) ask();
+                if (ok && k >= kItems) ok = __all_sync(0xffffffffu, sleep_wait<200>(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
                 if (ok && lane == 0) {
                     volatile Item &dst = items[k % kItems];
                     dst.start = it.start, dst.end = it.end, dst.tok0 = it.tok0, dst.head0 = it.head0;
@@ -626,14 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (it.last) break;
-                // (waited for in every case: the answer must not arrive after the block's end)
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(block_bar, k & 1))) {
-                    if (lane == 0) record_error(p.err, kErrProducerWait);
-                    *abort_flag = 1;
-                    break;
-                }
-                index = asked_block(block_answer);
-                __syncwarp();
+                take_answer();
             }
             if (!ok) {
                 if (lane == 0) record_error(p.err, kErrProducerWait);

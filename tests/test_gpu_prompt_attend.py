@@ -2,6 +2,8 @@
 f16, exact in the products; the softmax weights are rounded to f16, half an
 ulp, 2^-11 of a weight: attn_ref.bound with 10 bits for it (weights and their
 sum) is the tolerance."""
+import time
+
 import numpy as np
 import pytest
 
@@ -100,6 +102,42 @@ def test_many_short_prompts(d, heads, hk, n_seq, most):
     for _ in range(20):
         assert torch.equal(got, qg.prompt_attend(q, k, v, off))
     check(got, q, k, v, lens, d ** -0.5, heads=[0, heads - 1])
+
+
+@pytest.mark.parametrize("lens", [[1] * 20 + [700, 2, 0, 129, 300] + [0] * 9 + [260] * 3 + [64, 1], [513] + [5] * 40 + [257, 128],
+                                  [0] * 70 + [3] + [0] * 100 + [1000]], ids=["mixed", "long-first", "gaps"])
+def test_more_sequences_than_a_warp(lens):
+    """More than 32 sequences, of one tile and of several, with empty ones among them: the bits of calls that take
+    them one by one."""
+    rng = np.random.default_rng(44)
+    q, k, v = inputs(rng, sum(lens), 8, 2, 64)
+    got, at = qg.prompt_attend(q, k, v, i32(np.cumsum([0] + lens))), 0
+    for n in lens:
+        if n:
+            rows = slice(at, at + n)
+            assert torch.equal(got[rows], qg.prompt_attend(q[rows], k[rows], v[rows], i32([0, n])))
+        at += n
+
+
+def test_very_many_sequences():
+    """300000 sequences of 0 .. 2 rows and a few long ones: the time is that of the work, not of looking through all
+    sequences for each item (which took some 17 s)."""
+    rng = np.random.default_rng(45)
+    lens = rng.integers(0, 3, 300000)
+    lens[[7, 150000, 299990]] = 700, 300, 129
+    ends = np.cumsum(np.concatenate([[0], lens]))
+    q, k, v = inputs(rng, int(ends[-1]), 1, 1, 64)
+    off = i32(ends)
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    got = qg.prompt_attend(q, k, v, off)
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 < 2.0
+    one = torch.from_numpy(ends[:-1][lens == 1]).cuda()
+    assert torch.equal(got[one], v[one])  # (one key: its value)
+    for s in (0, 140000, 149990, 299980):
+        a, b = int(ends[s]), int(ends[s + 20])
+        assert torch.equal(got[a:b], qg.prompt_attend(q[a:b], k[a:b], v[a:b], i32(ends[s:s + 21] - a)))
 
 
 @pytest.mark.parametrize("q_size,v_size,scale", [(1, 1, -0.3), (1, 1, 0.0), (20, 1, 1.0), (1, 5000.0, 0.09),
