@@ -250,27 +250,11 @@ struct Item {
     int last;         // 1: no item, the end
 };
 
-// Sequence s as rows [start, end); empty where its offsets are out of range.
-__device__ __forceinline__ int2 seq_rows(const PromptParams &p, int s) {
-    const int a = __ldg(p.offsets + s), b = __ldg(p.offsets + s + 1);
-    if (a < 0 || b < a || b > p.n_tok) {
-        record_error(p.err, kErrBadIndex);
-        return make_int2(0, 0);
-    }
-    return make_int2(a, b);
-}
-
-// A sequence's rows and its number of items a head pack (0 past the last sequence).
+// A sequence's rows [start, end) and its number of items a head pack (0 where it is left out or past the last).
 struct SeqItems {
     int2 rows;
     int n;
 };
-__device__ __forceinline__ SeqItems seq_items(const PromptParams &p, int toks, int s) {
-    SeqItems q;
-    q.rows = s < p.n_seq ? seq_rows(p, s) : make_int2(0, 0);
-    q.n = (q.rows.y - q.rows.x + toks - 1) / toks;
-    return q;
-}
 
 // Finds items by their index, one warp together. Items come in groups of `packs`
 // (one for each head pack); the groups of a launch of up to 32 sequences are
@@ -289,14 +273,42 @@ __device__ __forceinline__ SeqItems seq_items(const PromptParams &p, int toks, i
 struct ItemFinder {
     SeqItems q;            // of sequence s0 + lane
     int packs, toks, s0;
-    int64_t before, count; // lane c: groups of the classes above c, and of c
+    int reach;             // largest end of the sequences up to these
+    int before, count;     // lane c: groups of the classes above c, and of c
     int cls, base;         // where the last search ended: its class, the class's groups in the sequences before s0
 
     __device__ __forceinline__ int class_of() const { return 31 - __clz(q.n); }  // (-1 without tiles)
-    __device__ __forceinline__ void look(const PromptParams &p, int s) {
-        s0 = s;
-        q = seq_items(p, toks, s + (threadIdx.x & 31));
+
+    // The 32 sequences from s on (0, or 32 after the last ones): their offsets, and what they are as items. Left out is a
+    // sequence whose offsets are out of range or fall, and one that begins before the end of an earlier one that is
+    // not: so no row is in two, and the launch, which has blocks for n_tok rows, has one for every item.
+    __device__ __forceinline__ int2 offsets(const PromptParams &p, int s) const {
+        s += threadIdx.x & 31;
+        return s < p.n_seq ? make_int2(__ldg(p.offsets + s), __ldg(p.offsets + s + 1)) : make_int2(0, 0);
     }
+    __device__ __forceinline__ void settle(const PromptParams &p, int s, int2 rows) {
+        const int lane = threadIdx.x & 31, from = s == 0 ? 0 : reach;
+        const bool there = s + lane < p.n_seq;
+        bool in = there && rows.x >= 0 && rows.y >= rows.x && rows.y <= p.n_tok;
+        for (;;) {  // (once more for each sequence that begins too early)
+            int end = in ? max(rows.y, from) : from;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, end, m);
+                if (lane >= m) end = max(end, o);
+            }
+            reach = __shfl_sync(0xffffffffu, end, 31);
+            const int earlier = __shfl_up_sync(0xffffffffu, end, 1);
+            const uint32_t early = __ballot_sync(0xffffffffu, in && rows.x < (lane == 0 ? from : earlier));
+            if (early == 0) break;
+            if (lane == __ffs(early) - 1) in = false;
+        }
+        if (there && !in) record_error(p.err, kErrBadIndex);
+        s0 = s;
+        q.rows = in ? rows : make_int2(0, 0);
+        q.n = (q.rows.y - q.rows.x + toks - 1) / toks;
+    }
+    __device__ __forceinline__ void look(const PromptParams &p, int s) { settle(p, s, offsets(p, s)); }
 
     __device__ __forceinline__ void start(const PromptParams &p, int pack) {
         packs = p.n_heads / pack, toks = 2 * (kTileRows / pack);
@@ -304,10 +316,11 @@ struct ItemFinder {
         before = count = 0;
         cls = -1, base = 0;
         if (p.n_seq > 32) {
-            SeqItems next = seq_items(p, toks, lane);
+            int2 next = offsets(p, 0);
             for (int s = 0; s < p.n_seq; s += 32) {
-                q = next;
-                if (s + 32 < p.n_seq) next = seq_items(p, toks, s + 32 + lane);
+                const int2 rows = next;
+                next = offsets(p, s + 32);
+                settle(p, s, rows);
                 uint32_t left = __ballot_sync(0xffffffffu, q.n > 0);
                 while (left) {
                     const int c = __shfl_sync(0xffffffffu, class_of(), __ffs(left) - 1);
@@ -317,10 +330,10 @@ struct ItemFinder {
                     left &= ~__ballot_sync(0xffffffffu, in);
                 }
             }
-            int64_t from = count;  // groups of the classes from the lane's on
+            int from = count;  // groups of the classes from the lane's on
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
-                const int64_t o = __shfl_down_sync(0xffffffffu, from, m);
+                const int o = __shfl_down_sync(0xffffffffu, from, m);
                 if (lane + m < 32) from += o;
             }
             before = from - count;
@@ -350,7 +363,7 @@ struct ItemFinder {
         const uint32_t is = __ballot_sync(0xffffffffu, rank >= before && rank < before + count);
         if (is == 0) return false;
         const int c = __ffs(is) - 1;
-        const int r = rank - static_cast<int>(__shfl_sync(0xffffffffu, before, c));
+        const int r = rank - __shfl_sync(0xffffffffu, before, c);
         if (c != cls || r < base) {
             cls = c, base = 0;
             if (s0 != 0) look(p, 0);
@@ -1014,7 +1027,7 @@ template <int D, class TO> cudaError_t launch(const PromptParams &p, int device,
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_acq_rel);
     }
-    // every sequence has at most one tile that its rows do not fill
+    // every sequence has at most one tile that its rows do not fill, and no row is in two
     const int toks = 2 * (kTileRows / pack);
     const int64_t items = (static_cast<int64_t>(p.n_tok) / toks + p.n_seq) * (p.n_heads / pack);
     if (items > INT32_MAX) return cudaErrorInvalidValue;

@@ -244,6 +244,29 @@ def test_offsets_out_of_range():
     check(out[20:], q[20:], k[20:], v[20:], [30], 64 ** -0.5)
 
 
+@pytest.mark.parametrize("offsets,kept", [
+    ([0, 2048, 0, 2048], [(0, 2048)]),  # the third begins again where the first has been
+    ([0, 900, 300, 900, 2048], [(0, 900), (900, 2048)]),
+    ([0, 1100, 4000, 1100, 1100, -1, 1200, 2000, 1999, 2000, 2048], [(0, 1100), (1200, 2000), (2000, 2048)]),
+    ([700, 100, 200, 2048], [(100, 200), (200, 2048)]),  # the falling first one holds no other back
+    ([0, 2048] + [0, 2048] * 40, [(0, 2048)]),  # more than 32 sequences
+    ([0] + [5, 3] * 40 + [2048], [(0, 5)]), ([900, 100] + [100] * 40 + [1800, 1700, 2048], [(100, 1800)])],
+    ids=["again", "inside", "several", "first", "many", "many-short", "many-first"])
+def test_falling_offsets_lose_no_other_rows(offsets, kept):
+    """Sequences of many tiles around offsets that fall: each row of a sequence that is not left out has its result,
+    the others are not written, every time."""
+    rng = np.random.default_rng(38)
+    q, k, v = inputs(rng, 2048, 1, 1, 64)
+    want = torch.full((2048, 1, 64), 9.0, device="cuda", dtype=torch.float16)
+    for a, b in kept:
+        want[a:b] = qg.prompt_attend(q[a:b], k[a:b], v[a:b], i32([0, b - a]))
+    for _ in range(3):
+        out = torch.full((2048, 1, 64), 9.0, device="cuda", dtype=torch.float16)
+        qg.prompt_attend(q, k, v, i32(offsets), out=out)
+        assert qg.device_error() == 4
+        assert torch.equal(out, want)
+
+
 def test_refusals():
     q, k = torch.zeros(5, 4, 128, device="cuda", dtype=torch.float16), torch.zeros(5, 2, 128, device="cuda", dtype=torch.float16)
     off = i32([0, 5])
