@@ -47,6 +47,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 
 #include "kv_cache.cuh"
 #include "tc_common.cuh"
@@ -512,7 +513,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, uint32_
     }
     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
     if (first) {
-        ref = top;
+        ref = fmaxf(top, -FLT_MAX);  // (scores of -inf alone: weights of 0 beside it, where their own difference is NaN)
     } else if (__any_sync(0xffffffffu, top > ref + kGrow)) {
         // S of this tile is complete, so P V of the tiles before is, too
         const float next = fmaxf(ref, top), keep = exp2_approx(ref - next);

@@ -165,6 +165,19 @@ def test_unseen_nan_and_infinity(d, bad):
     assert not torch.isfinite(got[150:300]).all(-1).all() and not torch.isfinite(got[305:340]).all(-1).all()
 
 
+@pytest.mark.parametrize("n_hidden", [1, 127, 128, 129, 256, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_minus_infinity(d, n_hidden):
+    """The first keys hold -inf in a channel where the queries are 1: their scores are -inf and their weights 0, for
+    whole key tiles and parts of one. The rows after them see only the other keys."""
+    rng = np.random.default_rng(39)
+    q, k, v = (t.clone() for t in inputs(rng, 430, 4, 2, d, fused=False))
+    q[..., 0] = 1.0
+    k[:n_hidden, :, 0] = -float("inf")
+    got = qg.prompt_attend(q, k, v, i32([0, 430]))
+    check(got[n_hidden:], q[n_hidden:], k[n_hidden:], v[n_hidden:], [430 - n_hidden], d ** -0.5)
+
+
 def test_infinite_value_that_is_seen():
     """An infinite value with a weight above zero gives that infinity."""
     rng = np.random.default_rng(33)
