@@ -348,9 +348,18 @@ template <int NB> __device__ __forceinline__ __half2 max_scales(const uint32_t (
     if (NB == 4) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2 *>(&w[NB / 2 - 1])));
     return m;
 }
-__device__ __forceinline__ float exponent_field(__half2 m) {
+__device__ __forceinline__ float exponent_field(__half2 m, bool &infinite) {
     const uint32_t f = static_cast<uint32_t>(__half_as_ushort(__hmax(__low2half(m), __high2half(m)))) >> 10;
+    infinite = f > 30u;
     return __uint_as_float(0x4B000000u | min(f, 30u)) - 8388608.0f;
+}
+// Infinite scales as NaN: times a code less 8 they would be an infinity or NaN by the code.
+template <int NB> __device__ __forceinline__ void infinities_to_nan(uint32_t (&w)[NB / 2]) {
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) {
+        if (not_finite(w[i])) w[i] |= 0x0200u;
+        if (not_finite(w[i] >> 16)) w[i] |= 0x02000000u;
+    }
 }
 
 // Eight query elements of a row (elements 0..3 and 16..19 from shared address a on) in f32.
@@ -729,7 +738,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                     __half2 vm[2];
 #pragma unroll
                     for (int gr = 0; gr < 2; ++gr) vm[gr] = __hmax2(max_scales<NB>(dv[gr][0]), max_scales<NB>(dv[gr][1]));
-                    const float ex = exponent_field(__hmax2(vm[0], vm[1]));
+                    bool infinite;
+                    const float ex = exponent_field(__hmax2(vm[0], vm[1]), infinite);
+                    if (TERMS == 1 && infinite)  // (two terms make NaN of it: infinity less infinity)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) infinities_to_nan<NB>(dv[i >> 1][i & 1]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -743,7 +756,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                     for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float ex = exponent_field(max_scales<NB>(dv[gr][h]));
+                            bool infinite;
+                            const float ex = exponent_field(max_scales<NB>(dv[gr][h]), infinite);
+                            if (TERMS == 1 && infinite) infinities_to_nan<NB>(dv[gr][h]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

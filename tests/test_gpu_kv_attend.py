@@ -209,6 +209,33 @@ def test_segments_one_after_another_in_a_thread_block(d, group, per, t):
               [lens[s] - per + m], [m], group, d ** -0.5, t == "f16")
 
 
+@pytest.mark.parametrize("t", ["f32", "f16"])
+@pytest.mark.parametrize("bits", [0x7C00, 0xFC00, 0x7E00], ids=["inf", "-inf", "nan"])
+@pytest.mark.parametrize("tok", [3, 40, 94, 95, 96, 98, 99])
+def test_a_value_scale_that_is_not_finite(t, bits, tok):
+    """All 32 channels of its block are NaN in the rows that see its token, and nothing else is, wherever among the
+    tiles and the rows' limits the token lies."""
+    rng = np.random.default_rng(40)
+    n, d, m = 100, 128, 6
+    for group in (4, 2):
+        cache, table, ks, vs = filled(rng, [n], 1, d, 16)
+        slot = int(table[0, tok // 16]) * 16 + tok % 16
+        at = attn_ref.slot_bytes(16, 1, d, slot, 0)[3][2]
+        cache.data[torch.from_numpy(at).cuda()] = torch.tensor([bits & 255, bits >> 8], dtype=torch.uint8, device="cuda")
+        q = torch.from_numpy(rng.standard_normal((m, group, d)).astype(np.float32)).cuda().to(TYPES[t])
+        got = qg.kv_attend(cache, q, i32(table), i32([n]), q_offsets=i32([0, m]), max_q_len=m)
+        sees = torch.arange(m, device="cuda") + n - m >= tok
+        want = sees.view(-1, 1, 1) & (torch.arange(d, device="cuda") // 32 == 2)
+        assert torch.equal(torch.isnan(got), want.expand_as(got))
+        # the other channels as if the block were of zeros
+        ref = [attn_ref.attend(q[:, h].cpu().numpy().astype(np.float64), ks[0][:, 0], np.where(np.arange(d) // 32 == 2, 0, vs[0][:, 0]),
+                               n - m + 1 + np.arange(m), d ** -0.5) for h in range(group)]
+        for h, (out, pv, mag, big) in enumerate(ref):
+            tol = attn_ref.bound(out, pv, mag, big, d, n, 24 if t == "f16" else 20, 10 if t == "f16" else 20, t == "f16")
+            other = np.arange(d) // 32 != 2
+            assert (np.abs(got[:, h].cpu().numpy().astype(np.float64) - out) <= tol)[:, other].all()
+
+
 @pytest.mark.parametrize("t", [torch.float32, torch.float16], ids=["f32", "f16"])
 @pytest.mark.parametrize("lens", [[5, 40], [777, 3, 40000]], ids=["short", "split"])
 def test_nan_queries_give_nan(t, lens):
