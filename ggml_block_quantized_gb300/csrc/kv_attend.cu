@@ -53,6 +53,7 @@
 // which a tile's work is 1.1: the rest is the place in the list (1.0), the queries
 // (1.3), the join (0.5 and 1.1) and the launches.
 #include <atomic>
+#include <cfloat>
 
 #include "kv_cache.cuh"
 #include "tc_common.cuh"
@@ -562,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
 #pragma unroll
                 for (int m = 1; m < NB * 4; m <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
                 int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;  // exponent of the largest
-                if (e < -116 || e == 128) e = 0;                              // zeros, infinities
-                if (e > 100) e = 100;
+                if (e == 128) e = 0;                                          // infinities
+                if (e < -117) e = -117;                                       // (2^(10 - e) is an f32)
                 const float up = __uint_as_float(static_cast<uint32_t>(10 - e + 127) << 23) * (p.scale < 0.0f ? -1.0f : 1.0f);
                 float sum = 0.0f;
 #pragma unroll
@@ -597,10 +598,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                     ini[0] = ini[2] = sum * -0x1p-17f;  // -8 * 16 * 2^-24, 0 for code - 8
                     if (b == 0) {
                         // 2^(e - 10), for subnormal codes times 2^24 / 16; never 0, which times an unseen
-                        // token's -inf would be NaN
-                        row_factor[r] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * (TERMS == 1 ? 0x1p10f : 0x1p-10f) *
-                                                  __uint_as_float(static_cast<uint32_t>(e + 127) << 23),
-                                              1e-37f);
+                        // token's -inf would be NaN, nor infinite
+                        row_factor[r] = fminf(fmaxf(fabsf(p.scale) * 1.4426950408889634f *
+                                                        __uint_as_float(static_cast<uint32_t>(e + 127) << 23) *
+                                                        (TERMS == 1 ? 0x1p10f : 0x1p-10f),
+                                                    1e-37f),
+                                              FLT_MAX);
                         const int tok = row / p.group;
                         row_limit[r] = live ? before + tok : 0;
                         row_out[r] = live ? (seg.q.q0 + tok) * p.n_heads + seg.head * p.group + row - tok * p.group : -1;

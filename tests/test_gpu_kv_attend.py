@@ -119,6 +119,17 @@ def test_sizes_of_values(t, k_size, v_size, q_size, scale):
     check(got, q, ks, vs, lens, [1, 1], 3, scale, t == "f16")
 
 
+@pytest.mark.parametrize("e", [-125, -118, -100, 90, 110, 120])
+def test_queries_near_the_ends_of_f32(e):
+    """Queries of 2^e with a scale of 2^-e: the scores are ordinary ones."""
+    rng = np.random.default_rng(42)
+    lens = [300, 40]
+    cache, table, ks, vs = filled(rng, lens, 2, 128, 64)
+    q = np.ldexp(rng.standard_normal((2, 6, 128)).astype(np.float32).astype(np.float64), e).astype(np.float32)
+    q, scale = torch.from_numpy(q).cuda(), float(np.ldexp(128 ** -0.5, -e))
+    check(qg.kv_attend(cache, q, i32(table), i32(lens), scale=scale), q, ks, vs, lens, [1, 1], 3, scale, False)
+
+
 def test_values_of_mixed_size():
     """Tokens whose values differ by ten orders of magnitude, large ones late and early."""
     rng = np.random.default_rng(18)
