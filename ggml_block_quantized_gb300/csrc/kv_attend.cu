@@ -33,13 +33,17 @@
 //    2^11 (exact).
 //  * values: B = weight x value scale per token and block (the scale varies
 //    along the summed axis), transposed among lanes with movmatrix. The
-//    softmax's running reference is not the largest score but the largest score
-//    plus the exponent field of its token's largest value scale, less 21, and is
-//    raised only when that sum passes it by 29: every product is then below 2^15
-//    and a row's largest above 2^6, whatever the values' size. Weights, their
-//    sum and the accumulators share that reference, so it cancels. (Raised for
-//    every larger score, with a maximum over the lanes each tile, 131071 tokens
-//    took 50.1 us instead of 48.0.)
+//    softmax's running reference is not the largest score but the largest sum of
+//    a score and the exponent field of its token's largest value scale, less 21,
+//    and is raised only when such a sum passes it by 29: every product is then
+//    below 2^15 and a row's largest above 2^6, whatever the values' size, so that
+//    what f16 loses at its end, 2^-25 of a product, is 2^-31 of the largest.
+//    Weights, their sum and the accumulators share that reference, so it cancels.
+//    (Raised for every larger score, with a maximum over the lanes each tile,
+//    131071 tokens took 50.1 us instead of 48.0. With the largest score and the
+//    largest scale of a lane's four tokens, whichever tokens they are of, 24
+//    sequences took 58.1 us instead of 59.4, but strong scores of small values
+//    beside large ones fell below f16: results off by a third.)
 // So codes enter exactly and only q and the weights are rounded: f16 queries
 // are exact and the weights take one f16 (2^-11 relative); for f32 both are
 // split in two f16 parts and each product is formed twice.
@@ -342,17 +346,18 @@ template <int NB> __device__ __forceinline__ void ld_halves(const uint8_t *p, ui
 }
 __device__ __forceinline__ bool not_finite(uint32_t half_bits) { return (half_bits & 0x7C00u) == 0x7C00u; }
 
-// The largest magnitudes among a row's scales (halves apart; NaN has no say),
-// and the f16 exponent field of the larger one, 0 .. 30, as a float.
-template <int NB> __device__ __forceinline__ __half2 max_scales(const uint32_t (&w)[NB / 2]) {
+// The largest magnitudes among a row's scales (halves apart; NaN has no say).
+template <int NB> __device__ __forceinline__ uint32_t max_scales(const uint32_t (&w)[NB / 2]) {
     __half2 m = __habs2(*reinterpret_cast<const __half2 *>(&w[0]));
     if (NB == 4) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2 *>(&w[NB / 2 - 1])));
-    return m;
+    return *reinterpret_cast<const uint32_t *>(&m);
 }
-__device__ __forceinline__ float exponent_field(__half2 m, bool &infinite) {
-    const uint32_t f = static_cast<uint32_t>(__half_as_ushort(__hmax(__low2half(m), __high2half(m)))) >> 10;
-    infinite = f > 30u;
-    return __uint_as_float(0x4B000000u | min(f, 30u)) - 8388608.0f;
+// The f16 exponent fields of the largest of each of two tokens, from their max_scales: 0 .. 31, the second token's in
+// the high half.
+__device__ __forceinline__ uint32_t exponent_fields(uint32_t a, uint32_t b) {
+    const uint32_t x = __byte_perm(a, b, 0x5410), y = __byte_perm(a, b, 0x7632);
+    const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
+    return (*reinterpret_cast<const uint32_t *>(&m) >> 10) & 0x001F001Fu;
 }
 // Infinite scales as NaN: times a code less 8 they would be an infinity or NaN by the code.
 template <int NB> __device__ __forceinline__ void infinities_to_nan(uint32_t (&w)[NB / 2]) {
@@ -735,38 +740,29 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                         }
                     if (odd) *odd_flag = 1;
                 }
-                // ---- the lane's largest score plus exponent, by column
+                // ---- the lane's largest score plus exponent, by column: of each token by itself, since the largest score
+                // and the largest scale of different tokens could lie far above every product
                 float top[NT][2];
-                if (!masked) {
-                    __half2 vm[2];
+                {
+                    float ex[2][2];
+                    uint32_t infinite = 0;
 #pragma unroll
-                    for (int gr = 0; gr < 2; ++gr) vm[gr] = __hmax2(max_scales<NB>(dv[gr][0]), max_scales<NB>(dv[gr][1]));
-                    bool infinite;
-                    const float ex = exponent_field(__hmax2(vm[0], vm[1]), infinite);
-                    if (TERMS == 1 && infinite)  // (two terms make NaN of it: infinity less infinity)
+                    for (int gr = 0; gr < 2; ++gr) {
+                        const uint32_t f = exponent_fields(max_scales<NB>(dv[gr][0]), max_scales<NB>(dv[gr][1]));
+                        ex[gr][0] = __uint_as_float(__byte_perm(f, 0x4B000000u, 0x7540)) - 8388608.0f;
+                        ex[gr][1] = __uint_as_float(__byte_perm(f, 0x4B000000u, 0x7542)) - 8388608.0f;
+                        infinite |= f + 0x00010001u;
+                    }
+                    if (TERMS == 1 && (infinite & 0x00200020u))  // (two terms make NaN of it: infinity less infinity)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) infinities_to_nan<NB>(dv[i >> 1][i & 1]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            top[nt][c] = fmaf(fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])),
-                                              factor[nt][c], ex);
-                } else {  // token by token: one that a row does not see has no say in its reference
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-#pragma unroll
-                    for (int gr = 0; gr < 2; ++gr)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            bool infinite;
-                            const float ex = exponent_field(max_scales<NB>(dv[gr][h]), infinite);
-                            if (TERMS == 1 && infinite) infinities_to_nan<NB>(dv[gr][h]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int c = 0; c < 2; ++c)
-                                    top[nt][c] = fmaxf(top[nt][c], fmaf(s[gr][nt][2 * h + c], factor[nt][c], ex));
+                        for (int c = 0; c < 2; ++c) {
+                            const float f = factor[nt][c];
+                            top[nt][c] = fmaxf(fmaxf(fmaf(s[0][nt][c], f, ex[0][0]), fmaf(s[0][nt][2 + c], f, ex[0][1])),
+                                               fmaxf(fmaf(s[1][nt][c], f, ex[1][0]), fmaf(s[1][nt][2 + c], f, ex[1][1])));
                         }
                 }
                 // ---- running reference (raised when a product could pass 2^15), weights

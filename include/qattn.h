@@ -119,7 +119,10 @@ size_t qkv_attend_workspace_bytes(int head_dim, int n_kv_heads, int n_heads, int
  *
  * type (QG_F32 or QG_F16) is q's and out's. Codes enter the products exactly;
  * with QG_F16 the softmax weights are rounded to f16 (relative 2^-11), with
- * QG_F32 q and the weights are split in two f16 parts each (about 2^-21).
+ * QG_F32 q and the weights are split in two f16 parts each (about 2^-21). A
+ * weight enters as its product with its token's value scale, whose f16 parts
+ * end at 2^-31 of the row's largest such product: 32 channels whose values
+ * are far smaller than the head's others are only as fine as that.
  * q: [n_tok][n_heads][D], q_stride elements from token to token (a multiple
  * of 16 bytes); out: [n_tok][n_heads][D] contiguous. max_q_len >= every
  * sequence's number of queries; a sequence with more, or with q_offsets

@@ -78,3 +78,16 @@ def bound(out, pv, mag, big, d, n, q_bits, p_bits, out_f16):
     score = (2.0 ** -q_bits + d * 2.0 ** -23) * mag
     e = (2 * score + 2.0 ** -p_bits + 2.0 ** -19 + n * 2.0 ** -23) * pv + n * 2.0 ** -24 * big
     return e + (2.0 ** -11 * np.abs(out) + 2.0 ** -24 if out_f16 else 1e-37)
+
+
+def tight_bound(q, k, v, scale, f16):
+    """attend()'s out for rows q [m, D] that see all of k, and bound() with a smaller allowance for what 16-bit products
+    lose at their last place: the largest product of a weight and a value's scale is 2^6 or more, a product is off by
+    2^-25 at most where f16 ends, the codes are at most 8 and a scale is an eighth of its block's largest value: 2^-31 of
+    the largest product of a weight and a token's largest value, for each token."""
+    out, pv, mag, big = attend(q, k, v, [len(k)] * len(q), scale)
+    s = scale * (q @ k.T)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    most = (p / p.sum(-1, keepdims=True) * np.abs(v).max(-1)).max(-1, keepdims=True)
+    bits = (24, 10) if f16 else (20, 20)
+    return out, bound(out, pv, mag, 0 * big, q.shape[1], len(k), *bits, f16) + len(k) * 2.0 ** -31 * most

@@ -146,6 +146,33 @@ def test_values_of_mixed_size():
             check(qg.kv_attend(cache, q, i32(table), i32([n])), q, [k], [v], [n], [1], 4, d ** -0.5, t == "f16")
 
 
+@pytest.mark.parametrize("t", ["f32", "f16"])
+@pytest.mark.parametrize("by", ["token", "block", "both"])
+@pytest.mark.parametrize("d,n", [(128, 512), (64, 97)])
+def test_strong_scores_beside_large_values(d, n, by, t):
+    """Tokens with nearly all of the weight and values 10^7 times smaller than the others', and blocks of a head 10^4
+    times smaller than its largest: the loss is of the largest weighted value's size, not of the largest value's
+    (attn_ref.tight_bound)."""
+    rng = np.random.default_rng(43)
+    cache, table, _, _ = filled(rng, [n], 1, d, 16)
+    flat = (i32(table[0])[:, None] * 16 + torch.arange(16, device="cuda", dtype=torch.int32)).reshape(-1)[:n].contiguous()
+    q = rng.standard_normal((1, 4, d)).astype(np.float32)
+    k, v = (rng.standard_normal((n, 1, d)).astype(np.float32) for _ in range(2))
+    if by != "block":
+        v *= 1e4
+        for h in range(4):
+            k[n // 5 + n // 7 * h, 0] = q[0, h] * 8
+            v[n // 5 + n // 7 * h, 0] *= 1e-7
+    if by != "token":
+        v *= np.resize(np.repeat(np.float32([1, 1e-2, 1e-4, 1e-1]), 32), d)
+    qg.kv_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), flat)
+    kr, vr = (x.cpu().numpy().astype(np.float64)[:, 0] for x in qg.kv_read(cache, flat))
+    q = torch.from_numpy(q).cuda().to(TYPES[t])
+    got = qg.kv_attend(cache, q, i32(table), i32([n]))[0].cpu().numpy().astype(np.float64)
+    out, tol = attn_ref.tight_bound(q[0].cpu().numpy().astype(np.float64), kr, vr, d ** -0.5, t == "f16")
+    assert (np.abs(got - out) <= tol).all(), float((np.abs(got - out) / tol).max())
+
+
 def test_strided_queries_out_and_stream():
     rng = np.random.default_rng(19)
     lens = [130, 64, 9]
