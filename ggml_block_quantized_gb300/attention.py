@@ -238,6 +238,8 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope=None, rope_pairs
         if len(shape) != 3 or shape[2] != 2 or shape[1] % 4 or not 4 <= shape[1] <= d // 2:
             raise ValueError(f"rope must be [positions, pairs, 2], pairs a multiple of 4 up to {d // 2}")
         n_pos, rot = shape[0], 2 * shape[1]
+        if n > 0 and n_pos == 0:  # (it has no address, and the C call would take it for no rotation)
+            raise ValueError("rope holds no position")
         if positions.shape != (n,):
             raise ValueError(f"positions must be [{n}]")
         pos_ptr = _on(positions, device, "positions", torch.int32)

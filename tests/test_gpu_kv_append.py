@@ -207,6 +207,16 @@ def test_a_cache_past_32_bits():
     assert at[0].min() > 1 << 32
 
 
+def test_an_empty_rope_is_refused():
+    """It is no rotation that any position could have; without tokens there is nothing to rotate."""
+    cache = qg.KVCache(2, 128, 16, torch.full((16 * 2 * 144,), 7, dtype=torch.uint8, device="cuda"))
+    x, s, empty = torch.ones(3, 2, 128, device="cuda"), i32(range(3)), qg.rope_table(0, 128)
+    with pytest.raises(ValueError):
+        qg.kv_append(cache, x, x, s, positions=s, rope=empty)
+    qg.kv_append(cache, x[:0], x[:0], s[:0], positions=s[:0], rope=empty)
+    assert bool((cache.data == 7).all())
+
+
 def test_refusals():
     d = 128
     cache = qg.KVCache.empty(2, 2, d, 16)
