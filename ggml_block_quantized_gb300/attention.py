@@ -141,11 +141,14 @@ def _place(t, name):
 
 
 def _new(shape, dtype, device, stream):
-    """A tensor that work on `stream` may use: torch hands its memory out again
-    only after that work."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """A tensor that work on `stream` may use at once: its memory is that stream's own. (What torch hands out for the
+    current stream may still be in use there by work enqueued before.) The current stream, where the caller goes on,
+    may use it, too: torch hands the memory out again only after that."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 

@@ -67,6 +67,35 @@ def test_layer(heads, kv_heads, head_dim):
         at += n
 
 
+def test_outputs_for_another_stream_are_its_own():
+    """Work on the current stream that still writes to memory it has given back does not reach what a call on another
+    stream allocates for itself (outputs and workspace)."""
+    rng = np.random.default_rng(50)
+    x = torch.from_numpy(rng.standard_normal((40, 12, 128)).astype(np.float32)).cuda()
+    q, k, v = x[:, :8].contiguous(), x[:, 8:10].contiguous(), x[:, 10:].contiguous()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots, table, lengths, ends = i32(list(range(40))), i32([[0, 1, 2]]), i32([40]), i32([0, 40])
+    cache = qg.KVCache(2, 128, 16, torch.zeros(48 * 2 * 144, dtype=torch.uint8, device="cuda"))
+    h = [t.half() for t in (q, k, v)]
+    calls = [lambda s: qg.kv_append(cache, k, v, slots, q=q, stream=s),
+             lambda s: torch.cat(qg.kv_read(cache, slots, stream=s)) if s is None else qg.kv_read(cache, slots, stream=s),
+             lambda s: qg.kv_attend(cache, q, table, lengths, q_offsets=ends, max_q_len=40, stream=s),
+             lambda s: qg.prompt_attend(*h, ends, stream=s)]
+    want = [c(None) for c in calls]
+    sizes = sorted({t.numel() * t.element_size() for t in want} | {x.numel(), qg.kv_attend_workspace_bytes(cache, 8, 40)} |
+                   {k.numel() * 4})
+    side = torch.cuda.Stream()
+    for c, w in zip(calls, want):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)  # some 50 ms, and then writes to blocks that have been given back by then
+        for n in sizes * 3:
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        got = c(side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(torch.cat(got) if isinstance(got, tuple) else got, w)
+
+
 def test_example_command(capsys):
     ex.main()
     text = capsys.readouterr().out
