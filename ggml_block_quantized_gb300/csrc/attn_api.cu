@@ -54,8 +54,8 @@ int qkv_append(const qkv_cache *cache, const qkv_append_args *a, qg_stream_t str
     if (!a) return QG_ERR_NULL;
     if (!float_type(a->in_type) || !float_type(a->out_type)) return QG_ERR_TYPE;
     const int d = cache->head_dim, n_heads = a->q ? a->n_heads : 0;
-    if (a->n_tok < 0 || (a->q && (check_heads(n_heads, cache->n_kv_heads) != QG_OK)) ||
-        a->n_tok * (n_heads + 2 * static_cast<int64_t>(cache->n_kv_heads)) > (1 << 30) || a->n_tok > (1 << 30))
+    if (a->n_tok < 0 || a->n_tok > (1 << 30) || (a->q && (check_heads(n_heads, cache->n_kv_heads) != QG_OK)) ||
+        a->n_tok * (n_heads + 2 * static_cast<int64_t>(cache->n_kv_heads)) > (1 << 30))
         return QG_ERR_SHAPE;
     if (a->rope && (a->rot_dim < 8 || a->rot_dim % 8 != 0 || a->rot_dim > d || a->n_pos < 0)) return QG_ERR_SHAPE;
     if (a->n_tok == 0) return QG_OK;
@@ -126,7 +126,7 @@ int qkv_attend(const qkv_cache *cache, int type, const void *q, int64_t q_stride
     if (!float_type(type)) return QG_ERR_TYPE;
     const int d = cache->head_dim;
     if (check_heads(n_heads, cache->n_kv_heads) != QG_OK || n_seq < 0 || n_tok < 0 || max_q_len < 1 ||
-        n_seq > (1 << 24) || n_tok > (1 << 30) || table_stride < 0 || (!q_offsets && n_tok < n_seq) ||
+        n_seq > (1 << 24) || n_tok > (1 << 30) || table_stride < 0 || table_stride > INT32_MAX || (!q_offsets && n_tok < n_seq) ||
         !(scale == scale) || scale - scale != 0.0f)
         return QG_ERR_SHAPE;
     const size_t need = qkv_attend_workspace_bytes(d, cache->n_kv_heads, n_heads, max_q_len);

@@ -109,7 +109,7 @@ size_t qkv_attend_workspace_bytes(int head_dim, int n_kv_heads, int n_heads, int
 /* Attention of the newest tokens of n_seq sequences over the cache.
  * Sequence s has lengths[s] tokens in the cache, token t in page
  * table[s * table_stride + t / page_size], row t % page_size (entries past
- * the last used page are not read). Its queries are rows q_offsets[s] ..
+ * the last used page are not read; table_stride at most 2^31 - 1). Its queries are rows q_offsets[s] ..
  * q_offsets[s + 1] - 1 of q (q_offsets NULL: row s alone), for its last
  * tokens: query i of m sees cache tokens t < lengths[s] - m + i + 1. With
  * group g = n_heads / n_kv_heads, query head h reads key/value head h / g:

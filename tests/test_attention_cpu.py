@@ -109,6 +109,15 @@ def test_attend_refusals(L, want, kw):
     assert L.qkv_attend(ctypes.byref(cache()), *a.values(), None) == want
 
 
+def test_sizes_whose_products_pass_64_bits(L):
+    """They are refused like other sizes out of range, before any of them is multiplied."""
+    for stride in (1 << 31, 1 << 59, (1 << 63) - 1):
+        assert L.qkv_attend(ctypes.byref(cache()), *{**ATTEND, "table_stride": stride}.values(), None) == ERR_SHAPE
+    for n in ((1 << 62) + 1, (1 << 63) - 1):
+        assert L.qkv_append(ctypes.byref(cache()), ctypes.byref(append_args(n_tok=n)), None) == ERR_SHAPE
+        assert L.qkv_read(ctypes.byref(cache()), A, n, B, C, None) == ERR_SHAPE
+
+
 def test_attend_workspace(L):
     ws = L.qkv_attend_workspace_bytes
     assert ws(128, 8, 32, 1) >= 16 and ws(64, 8, 8, 4) >= 16
