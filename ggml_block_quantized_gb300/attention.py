@@ -162,6 +162,20 @@ def kv_cache_bytes(n_pages: int, n_kv_heads: int, head_dim: int, page_size: int)
     return int(_lib().qkv_cache_bytes(n_pages, n_kv_heads, head_dim, page_size))
 
 
+def _pages(n_bytes, n_kv_heads, head_dim, page_size):
+    """How many pages a cache of n_bytes has."""
+    page = n_kv_heads * (page_size // 16) * 18 * head_dim  # (as kv_cache_bytes has it)
+    n_pages = n_bytes // page if page > 0 else 0
+    if kv_cache_bytes(n_pages, n_kv_heads, head_dim, page_size) == n_bytes:
+        return n_pages
+    if kv_cache_bytes(1, n_kv_heads, head_dim, page_size) < 0:
+        raise ValueError(f"no cache of {n_kv_heads} heads of {head_dim} in pages of {page_size}: heads of 64 or 128, "
+                         "pages of a multiple of 16 tokens")
+    if n_bytes % page:
+        raise ValueError(f"data holds {n_bytes} bytes, not a number of pages of {page}")
+    raise ValueError(f"data holds {n_pages} pages of {page_size} tokens: a cache has at most 2^31 - 1 tokens")
+
+
 class KVCache:
     """A paged cache of keys and values held in 4 bits (the layout of
     qkv_cache in include/qattn.h) over `data`, a uint8 CUDA tensor whose size
@@ -173,14 +187,7 @@ class KVCache:
             raise TypeError("data must be a uint8 CUDA tensor")
         if not data.is_contiguous():
             raise ValueError("data must be contiguous")
-        page = n_kv_heads * (page_size // 16) * 18 * head_dim  # (as kv_cache_bytes has it)
-        n_pages = data.numel() // page if page > 0 else 0
-        total = kv_cache_bytes(n_pages, n_kv_heads, head_dim, page_size)
-        if total < 0 and kv_cache_bytes(1, n_kv_heads, head_dim, page_size) < 0:
-            raise ValueError(f"no cache of {n_kv_heads} heads of {head_dim} in pages of {page_size}: heads of 64 or "
-                             "128, pages of a multiple of 16 tokens")
-        if total != data.numel():
-            raise ValueError(f"data holds {data.numel()} bytes, not a number of pages of {page}")
+        n_pages = _pages(data.numel(), n_kv_heads, head_dim, page_size)
         self.n_kv_heads, self.head_dim, self.page_size, self.n_pages = n_kv_heads, head_dim, page_size, n_pages
         self.data, self.device = data, data.get_device()
         self.c = _Cache(data.data_ptr(), n_pages, n_kv_heads, head_dim, page_size)

@@ -155,6 +155,19 @@ def test_binding_wants_cuda_tensors(L):
             call()
 
 
+def test_pages_of_a_cache(L):
+    """Each reason for a refusal is named."""
+    page = 8 * 16 * 144
+    assert at._pages(0, 8, 128, 16) == 0 and at._pages(5 * page, 8, 128, 16) == 5
+    most = (2 ** 31 - 1) // 16
+    assert at._pages(most * 16 * 72, 1, 64, 16) == most
+    for args, word in (((5 * page, 8, 96, 16), "heads of 64 or 128"), ((5 * page, 8, 128, 24), "multiple of 16"),
+                       ((5 * page + 1, 8, 128, 16), "not a number of pages"),
+                       (((most + 1) * 16 * 72, 1, 64, 16), "a cache has at most")):
+        with pytest.raises(ValueError, match=word):
+            at._pages(*args)
+
+
 def test_rope_table():
     t = qg.rope_table(9, 8, base=100.0, device="cpu")
     assert t.shape == (9, 4, 2) and t.dtype == torch.float32
