@@ -514,13 +514,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
         if (!ok) {
             if (lane == 0) record_error(p.err, kErrProducerWait);
             *abort_flag = 1;
-            // leave no copy in flight into this block's shared memory
-            for (int64_t k = issued > Sh::kSlots ? issued - Sh::kSlots : 0; k < issued; ++k)
-                if (!mbar_wait_bounded(full0 + 8 * static_cast<int>(k % Sh::kSlots),
-                                       static_cast<uint32_t>((k / Sh::kSlots) & 1)))
-                    record_error(p.err, kErrDrainWait);
-            if (seg > 0 && !mbar_wait_bounded(qfull, (seg - 1) & 1)) record_error(p.err, kErrDrainWait);
         }
+        // Leave no copy in flight into this block's shared memory: consumers that gave up waiting for one may be gone
+        // before it lands, even if nothing held the producer up.
+        for (int64_t k = issued > Sh::kSlots ? issued - Sh::kSlots : 0; k < issued; ++k)
+            if (!mbar_wait_bounded(full0 + 8 * static_cast<int>(k % Sh::kSlots),
+                                   static_cast<uint32_t>((k / Sh::kSlots) & 1)))
+                record_error(p.err, kErrDrainWait);
+        if (seg > 0 && !mbar_wait_bounded(qfull, (seg - 1) & 1)) record_error(p.err, kErrDrainWait);
         return;
     }
 
