@@ -679,11 +679,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            if (!ok && lane == 0) {
-                record_error(p.err, kErrProducerWait);
-                *abort_flag = 1;
-                // Leave no copy in flight into this block's shared memory (without an error every copy has been
-                // waited for by those who used it).
+            if (lane == 0) {
+                if (!ok) {
+                    record_error(p.err, kErrProducerWait);
+                    *abort_flag = 1;
+                }
+                // Leave no copy in flight into this block's shared memory: warps that gave up waiting for one may be gone
+                // before it lands, even if nothing held this one up.
                 bool landed = true;
                 for (; n_free < step.n; ++n_free) landed = mbar_wait_bounded(full + 8 * (n_free % kSteps), n_free / kSteps & 1u) && landed;
                 for (int x = 0; x < 2; ++x)
@@ -864,8 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++step.n;
                 }
             }
-            commit(issue, mfinal);  // every mma complete before tensor memory is freed
-            wait(mfinal, 0);
+            commit(issue, mfinal);  // every mma complete before tensor memory is freed, after a wait that gave up, too
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(mfinal, 0)) && issue) record_error(p.err, kErrDrainWait);
             __syncwarp();
         }
     } else if (warp < 12) {
