@@ -482,10 +482,11 @@ __device__ __forceinline__ uint32_t odd_half2(uint32_t w) { return ((w & 0x7C007
 // The softmax of one tile of S, a row a thread: S at s_t becomes P in place,
 // `ref` and `sum` go on, O at o_t is rescaled where a maximum grew too far.
 // Columns past `see` count as -inf; the warp's rows all see those up to
-// see_all.
+// see_all. grow: kGrow, infinite for a row without a query, which would else
+// say with whatever it holds when its warp's rows are rescaled (their roundings).
 template <int D>
 __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, uint32_t bar, float c, bool negate,
-                                             bool first, int see, int see_all, float &ref, float2 &sum) {
+                                             bool first, int see, int see_all, float grow, float &ref, float2 &sum) {
     uint32_t v[4][32];
 #pragma unroll
     for (int i = 0; i < 4; ++i) tm_ld32(s_t + 32 * i, v[i]);
@@ -514,7 +515,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_t, uint32_t o_t, uint32_
     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
     if (first) {
         ref = fmaxf(top, -FLT_MAX);  // (scores of -inf alone: weights of 0 beside it, where their own difference is NaN)
-    } else if (__any_sync(0xffffffffu, top > ref + kGrow)) {
+    } else if (__any_sync(0xffffffffu, top > ref + grow)) {
         // S of this tile is complete, so P V of the tiles before is, too
         const float next = fmaxf(ref, top), keep = exp2_approx(ref - next);
         ref = next;
@@ -890,6 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first_tok = item.tok0 + x * tile_toks, tok = first_tok + row / pack;  // within the sequence
             const int n = x == 0 ? item.tiles[0] : item.tiles[1];
             if (n == 0) continue;
+            const float grow = item.start + tok < item.end && row < pack * tile_toks ? kGrow : INFINITY;
             float ref = -INFINITY;
             float2 sum = make_float2(0.0f, 0.0f);
             for (int j = 0; j < n; ++j, ++n_s) {
@@ -898,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // the last column that the warp's first row sees
                 const int see_all = first_tok + (row & ~31) / pack - j * kTileKeys;
-                softmax_tile<D>(s_t, o_t, p_ready + 8 * x, c, negate, j == 0, tok - j * kTileKeys, see_all, ref, sum);
+                softmax_tile<D>(s_t, o_t, p_ready + 8 * x, c, negate, j == 0, tok - j * kTileKeys, see_all, grow, ref, sum);
             }
             if (!ok) break;
             // the storing warps must have taken the item before (one of a single tile can be through here

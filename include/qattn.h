@@ -151,7 +151,8 @@ int qkv_attend(const qkv_cache *cache, int type, const void *q, int64_t q_stride
  * (relative 2^-11), whatever out_type. Rows that are not seen have no
  * influence, NaN and infinities included. Offsets outside 0 .. n_tok or
  * falling: that sequence is left out (code 4), and so is one that begins
- * before the end of an earlier one that is not. */
+ * before the end of an earlier one that is not. Same inputs, same bits, and a
+ * sequence's result does not depend on what others the call has. */
 int qattn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                  int out_type, void *out, const int32_t *offsets, int64_t n_seq, int64_t n_tok, int n_heads,
                  int n_kv_heads, int head_dim, float scale, qg_stream_t stream);

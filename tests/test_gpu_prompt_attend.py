@@ -178,6 +178,30 @@ def test_scores_of_minus_infinity(d, n_hidden):
     check(got[n_hidden:], q[n_hidden:], k[n_hidden:], v[n_hidden:], [430 - n_hidden], d ** -0.5)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [3, 5, 7, 12, 4])
+def test_same_bits_whatever_ran_before(d, group):
+    """Groups whose tiles have rows without a query: what an earlier launch left there, zeros or large numbers, has no
+    say in the other rows. The same for rows past a sequence's end, which hold the next sequence."""
+    rng = np.random.default_rng(47)
+    n_seq, n = 6, 700
+    q, k, v = inputs(rng, n_seq * n, 2 * group, 2, d, q_size=4.0)
+    off = i32(np.arange(n_seq + 1) * n)
+    x = torch.randn(40 * 256, 12, d, device="cuda").half()
+    ends = i32(np.arange(0, 40 * 256 + 1, 256))
+
+    def after(size):
+        qg.prompt_attend(x[:, :8] * size, x[:, 8:10] * min(size, 1), x[:, 10:], ends)
+        return qg.prompt_attend(q, k, v, off)
+
+    got = after(0.0)
+    for size in (100.0, 0.0, 3000.0):
+        assert torch.equal(after(size), got)
+    qn = q.clone()  # the last sequence alone, with and without queries after it
+    qn[n:2 * n] *= 50
+    assert torch.equal(qg.prompt_attend(qn[:2 * n], k[:2 * n], v[:2 * n], i32([0, n, 2 * n]))[:n], got[:n])
+
+
 def test_infinite_value_that_is_seen():
     """An infinite value with a weight above zero gives that infinity."""
     rng = np.random.default_rng(33)
