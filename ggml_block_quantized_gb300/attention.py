@@ -303,7 +303,9 @@ def kv_attend(cache: KVCache, q, table, lengths, q_offsets=None, max_q_len: int 
     q_offsets[s] .. q_offsets[s + 1] - 1 (int32 [n_seq + 1], at most max_q_len a
     sequence), or row s where q_offsets is None, and belong to its last tokens:
     each sees the tokens up to its own. scale: 1 / sqrt(D) by default. Returns
-    out [n_tok, heads, D] in q's type; zeros for a row that sees nothing."""
+    out [n_tok, heads, D] in q's type; zeros for a row that sees nothing. Rows
+    in no sequence are not written, nor those of a sequence with more queries
+    than max_q_len (device_error() is 4 then)."""
     device = _place(q, "q")
     if cache.device != device:
         raise ValueError(f"the cache is on cuda:{cache.device}, not on cuda:{device}")

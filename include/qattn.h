@@ -17,7 +17,10 @@
  *     that meets a page, slot, position, length or offset outside its range
  *     records code 4 in the device error word, leaves the access out (what
  *     that means is said at each call) and goes on.
- *   - Sums, softmax statistics and accumulators are f32.
+ *   - Sums, softmax statistics and accumulators are f32, scores too: rows
+ *     with one of more than 2^23 in size, whose f32 steps come near 1, may be
+ *     NaN.
+ *   - Outputs overlap no input and no workspace, unless a call says so.
  *   - A kernel may start while the one enqueued before it finishes
  *     (programmatic dependent launch) but touches memory only after it.
  */
@@ -126,7 +129,9 @@ size_t qkv_attend_workspace_bytes(int head_dim, int n_kv_heads, int n_heads, int
  * q: [n_tok][n_heads][D], q_stride elements from token to token (a multiple
  * of 16 bytes); out: [n_tok][n_heads][D] contiguous. max_q_len >= every
  * sequence's number of queries; a sequence with more, or with q_offsets
- * outside 0 .. n_tok or falling, is left out (code 4). A length outside
+ * outside 0 .. n_tok or falling, is left out (code 4). Rows in no sequence,
+ * or in one that is left out, are not written; a row in two (q_offsets that
+ * fall and rise again) is either's. A length outside
  * 0 .. table_stride * page_size is taken as the nearer end, a page outside the
  * cache as tokens that are not seen (both code 4). A value block whose scale
  * is not finite gives NaN in its 32 channels to the rows that see its token.

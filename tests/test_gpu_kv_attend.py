@@ -329,6 +329,36 @@ def test_indexes_out_of_range():
     assert bool((out[1:] == 3).all()) and not bool((out[0] == 3).any())
 
 
+def test_a_length_past_the_table_is_the_tables_end():
+    """And one below zero no tokens, whatever its place among the sequences."""
+    rng = np.random.default_rng(48)
+    lens = [48, 20, 48, 5]
+    cache, table, ks, vs = filled(rng, lens, 2, 128, 16)
+    q = torch.from_numpy(rng.standard_normal((4, 4, 128)).astype(np.float32)).cuda()
+    want = qg.kv_attend(cache, q, i32(table), i32([48, 0, 48, 5]))
+    check(want, q, ks, vs, [48, 0, 48, 5], [1] * 4, 2, 128 ** -0.5, False)
+    assert qg.device_error() == 0
+    for bad in ([49, -1, 2 ** 31 - 1, 5], [1 << 20, -2 ** 31, 48, 5]):
+        assert torch.equal(qg.kv_attend(cache, q, i32(table), i32(bad)), want)
+        assert qg.device_error() == 4
+
+
+@pytest.mark.parametrize("t", ["f32", "f16"])
+def test_very_large_scores(t):
+    """Scores up to 2^23: all of the weight is on the token with the largest one, whose values are the result."""
+    rng = np.random.default_rng(49)
+    n, d = 700, 128
+    cache, table, ks, vs = filled(rng, [n], 1, d, 32)
+    q = torch.from_numpy(rng.standard_normal((1, 4, d)).astype(np.float32)).cuda().to(TYPES[t])
+    s = q[0].cpu().numpy().astype(np.float64) @ ks[0][:, 0].T
+    scale = 0.9 * 2.0 ** 23 / np.abs(s).max()
+    two = np.sort(s * scale, -1)[:, -2:]
+    assert (two[:, 1] - two[:, 0] > 2.0 ** 12).all()  # far above the scores' error, 2^-20 of 2^23 times D terms' size
+    got = qg.kv_attend(cache, q, i32(table), i32([n]), scale=scale)[0].cpu().numpy().astype(np.float64)
+    v = vs[0][s.argmax(-1), 0]
+    assert (np.abs(got - v) <= (2.0 ** -20 + (2.0 ** -10 if t == "f16" else 0)) * np.abs(v)).all()
+
+
 def test_a_long_cache_past_32_bits():
     """A sequence at the far end of a 5 GB cache."""
     hk, d, page, n = 32, 128, 64, 300

@@ -236,6 +236,23 @@ def test_a_query_that_is_not_finite(d, group, bad):
     assert torch.equal(got[rest], clean[rest])
 
 
+def test_very_large_scores():
+    """Scores up to 2^23: a row is the values of the key with its largest one."""
+    rng = np.random.default_rng(49)
+    n, d = 400, 64
+    q, k, v = inputs(rng, n, 2, 1, d)
+    s = np.einsum("mhd,nd->hmn", q.cpu().numpy().astype(np.float64), k[:, 0].cpu().numpy().astype(np.float64))
+    s[:, np.arange(n)[:, None] < np.arange(n)] = -np.inf
+    scale = 0.9 * 2.0 ** 23 / np.abs(s[np.isfinite(s)]).max()
+    two = np.sort(s, -1)[..., -2:] * scale
+    clear = (two[..., 1] - two[..., 0] > 2.0 ** 9).T  # (a score may be off by D 2^-23 of its terms' size)
+    assert clear.mean() > 0.98
+    got = qg.prompt_attend(q, k, v, i32([0, n]), scale=scale).cpu().numpy()
+    want = v[:, 0].cpu().numpy()[s.argmax(-1)].transpose(1, 0, 2)
+    off = np.abs(got.astype(np.float64) - want)  # weight and result rounded to f16 once each
+    assert (off <= 2.0 ** -10 * 1.01 * np.abs(want) + 2.0 ** -24)[clear].all()
+
+
 def test_strides_rows_in_no_sequence_and_stream():
     rng = np.random.default_rng(34)
     q, k, v = inputs(rng, 100, 4, 2, 64)
