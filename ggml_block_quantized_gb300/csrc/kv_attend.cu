@@ -48,14 +48,16 @@
 // are exact and the weights take one f16 (2^-11 relative); for f32 both are
 // split in two f16 parts and each product is formed twice.
 //
-// Bound: the cache's bytes would take 59% (f16 queries) and 44% (f32) of the time;
-// it goes into the consumers' instructions, about 700 and 900 a tile, at 55 and
-// 57% of the issue slots with the 12 warps a multiprocessor that 128 registers
-// allow (14 in two larger blocks were no faster). 24 sequences of 200 .. 4096
-// tokens, 32 heads of 128, f16: 58.7 us, 4.0 TB/s; one of 131071, 64 query and 8
-// key heads, f32: 50.0 us, 3.0 TB/s; 777 tokens, 32 and 8 heads, f32: 7.9 us, of
-// which a tile's work is 1.1: the rest is the place in the list (1.0), the queries
-// (1.3), the join (0.5 and 1.1) and the launches.
+// Bound: the cache's bytes would take 58% (f16 queries) and 43% (f32) of the time.
+// The rest is the consumers' instructions, about 700 and 900 a tile: the issue
+// slots are 56% busy, and a warp that does not issue waits for a result of its
+// own, for the math pipes or for its turn, about alike, with the 12 warps a
+// multiprocessor that 128 registers allow (14 in two larger blocks were no
+// faster). 24 sequences of 200 .. 4096 tokens, 32 heads of 128, f16: 59.3 us, 4.0
+// TB/s; one of 131071, 64 query and 8 key heads, f32: 51.5 us, 2.9 TB/s; 777
+// tokens, 32 and 8 heads, f32: 8.1 us, of which a tile's work is 1.1: the rest is
+// the place in the list (1.0), the queries (1.3), the join (0.5 and 1.1) and the
+// launches.
 #include <atomic>
 #include <cfloat>
 
@@ -139,7 +141,9 @@ __device__ __forceinline__ int row_tiles(const KvAttendParams &p, const Seq &q, 
 // Units of a segment: its tiles, and kStart for its queries and its join. (24
 // sequences of 200 .. 4096 tokens, 32 heads: 70.0 us at 3, 62.9 at 6, 58.4 to 59.1
 // at 8 to 12, 60.9 at 20; 16 of 5 .. 6000, 8 heads, 5 queries: 29.5, 25.0, 22.7 at
-// 8, 20.7 at 9, 19.6 at 11, 20.6 at 20.)
+// 8, 20.7 at 9, 19.6 at 11, 20.6 at 20. One number for every head size, type and
+// row count: only these two were swept, and 131071 tokens in f32 took 49.1 us at 8
+// and 50.4 at 11.)
 __device__ __forceinline__ int tok_tiles(const Seq &q) { return kStart + (q.len + kTile - 1) / kTile; }
 __device__ __forceinline__ int64_t seq_units(const KvAttendParams &p, int s, int rows) {
     const Seq q = load_seq(p, s);

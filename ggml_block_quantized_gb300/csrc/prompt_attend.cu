@@ -19,8 +19,9 @@
 //    into step, softmax with softmax: 524 us at 8192 tokens). A product leaves
 //    the warp only when the one before it is nearly done, so what the warp does
 //    between them is lost to the tensor cores: one wait a step and one a tile.
-//  * warp 2: takes items over, finds their rows and publishes them, up to four
-//    ahead.
+//  * warp 2: takes items over, finds their rows and publishes them, one ahead
+//    (with four, the multiprocessors took up the list before it could balance
+//    them: 374 us at 8192 tokens instead of 359).
 //  * warp 3: looks through the value tiles on the diagonal. The product P V
 //    takes 0 times every value that a row does not see, which is NaN for a
 //    value that is not finite; such values are set to 0 in shared memory
@@ -38,11 +39,12 @@
 // of 16); their P is 0.
 //
 // Bound: the tensor cores for long prompts. 8192 tokens, 32 query and 8 key heads
-// of 128: 360 us, 1526 TFLOP/s, the tensor pipe busy 68% of the time (S takes both
-// operands from shared memory at its full width and waits for every other access
-// there). 16 prompts of 1 .. 700 tokens: 45 us, of which the start and the changes
-// from item to item are most; 61 tokens: 8.2 us, one item's chain of copies,
-// products and softmax.
+// of 128: 361 us, 1522 TFLOP/s (386 us a call once calls have followed one another
+// for a second: the power limit then holds the clock at 1935 of 2070 MHz), the
+// tensor pipe busy 68% of the time (S takes both operands from shared memory at
+// its full width and waits for every other access there). 16 prompts of 1 .. 700
+// tokens: 45 us; 61 tokens: 8.2 us, one item's chain of copies, products and
+// softmax, which short prompts show at every item's start and end.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
