@@ -131,7 +131,7 @@ size_t qkv_attend_workspace_bytes(int head_dim, int n_kv_heads, int n_heads, int
  * sequence's number of queries; a sequence with more, or with q_offsets
  * outside 0 .. n_tok or falling, is left out (code 4). Rows in no sequence,
  * or in one that is left out, are not written; a row in two (q_offsets that
- * fall and rise again) is either's. A length outside
+ * fall and rise again) is undefined. A length outside
  * 0 .. table_stride * page_size is taken as the nearer end, a page outside the
  * cache as tokens that are not seen (both code 4). A value block whose scale
  * is not finite gives NaN in its 32 channels to the rows that see its token.
