@@ -270,9 +270,10 @@ struct SeqItems {
 // the 32 sequences where the last one ended: a block looks at each sequence about
 // once a class, and an item never costs more than one look at all of them. (With
 // the first order's search for each item 33 prompts of 5 .. 60 tokens, 32 and 8
-// heads of 128, took 26.9 us instead of 23.4, 256 151 instead of 74, 4096 27 ms
-// instead of 1.07, and hundreds of thousands seconds, past the waits' limit in the
-// end; 64 of 700, where the order counts for most, 340 instead of 344.)
+// heads of 128, took 26.9 us instead of 24.8, 256 151 instead of 75, 4096 27 ms
+// instead of 1.07, growing with the square of the sequences, so that a search could
+// outlast the waits' limit; 64 of 700, where the order counts for most, 340 instead
+// of 344.)
 struct ItemFinder {
     SeqItems q;            // of sequence s0 + lane
     int packs, toks, s0;

@@ -121,7 +121,7 @@ def test_more_sequences_than_a_warp(lens):
 
 def test_very_many_sequences():
     """300000 sequences of 0 .. 2 rows and a few long ones: the time is that of the work, not of looking through all
-    sequences for each item (which took some 17 s)."""
+    sequences for each item."""
     rng = np.random.default_rng(45)
     lens = rng.integers(0, 3, 300000)
     lens[[7, 150000, 299990]] = 700, 300, 129
