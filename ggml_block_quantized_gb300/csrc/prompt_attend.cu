@@ -720,8 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Item it;
                 it.last = index < 0 || !finder.find(p, pack, index, it);
                 // The launch has blocks for a tile of every sequence that its rows may not fill; those that turn out to be
-                // no items are taken over, too, rather than left to start one after another.
-                while (it.last && index >= 0 && ok) {
+                // no items are taken over, too, rather than left to start one after another, for a quarter of the time that
+                // the others wait for an item at most.
+                const uint64_t t0 = global_timer_ns();
+                while (it.last && index >= 0 && ok && __shfl_sync(0xffffffffu, global_timer_ns() - t0 < kWaitLimitNs / 4, 0)) {
                     ask();
                     take_answer();
                     it.last = index < 0 || !ok || !finder.find(p, pack, index, it);
