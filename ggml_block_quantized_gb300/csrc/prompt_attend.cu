@@ -39,7 +39,7 @@
 // of 16); their P is 0.
 //
 // Bound: the tensor cores for long prompts. 8192 tokens, 32 query and 8 key heads
-// of 128: 361 us, 1522 TFLOP/s (386 us a call once calls have followed one another
+// of 128: 362 us, 1519 TFLOP/s (386 us a call once calls have followed one another
 // for a second: the power limit then holds the clock at 1935 of 2070 MHz), the
 // tensor pipe busy 68% of the time (S takes both operands from shared memory at
 // its full width and waits for every other access there). 16 prompts of 1 .. 700
@@ -718,15 +718,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int k = 0; ok; ++k) {
                 Item it;
-                it.last = index < 0 || !finder.find(p, pack, index, it);
                 // The launch has blocks for a tile of every sequence that its rows may not fill; those that turn out to be
                 // no items are taken over, too, rather than left to start one after another, for a quarter of the time that
                 // the others wait for an item at most.
-                const uint64_t t0 = global_timer_ns();
-                while (it.last && index >= 0 && ok && __shfl_sync(0xffffffffu, global_timer_ns() - t0 < kWaitLimitNs / 4, 0)) {
+                uint64_t t0 = 0;
+                for (;;) {
+                    it.last = index < 0 || !finder.find(p, pack, index, it);
+                    if (!it.last || index < 0 || !ok) break;
+                    const uint64_t now = global_timer_ns();
+                    if (t0 == 0) t0 = now;
+                    if (!__shfl_sync(0xffffffffu, now - t0 < kWaitLimitNs / 4, 0)) break;
                     ask();
                     take_answer();
-                    it.last = index < 0 || !ok || !finder.find(p, pack, index, it);
                 }
                 if (!it.last) ask();
                 if (ok && k >= kItems) ok = __all_sync(0xffffffffu, sleep_wait<200>(item_empty + 8 * (k % kItems), ((k / kItems) - 1) & 1, abort_flag));
