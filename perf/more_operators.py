@@ -24,38 +24,38 @@ own = False
 def listed():
     return [
         # one generated token between two blocks: only latency counts
-        dict(name="norm, 1 token", op="norm", n=1, d=4096, h="f32", y="f32", x="f32", post=False, gate="none",
+        dict(name="norm 1 token", op="norm", n=1, d=4096, h="f32", y="f32", x="f32", post=False, gate="none",
              layer=False),
         # a decode step of 48 requests, a norm on both sides of the block and a gate for each channel
-        dict(name="norm, 48 tokens, both sides", op="norm", n=48, d=5120, h="f32", y="f32", x="f32", post=True,
+        dict(name="norm 48 tokens both sides", op="norm", n=48, d=5120, h="f32", y="f32", x="f32", post=True,
              gate="channel", layer=False),
         # odd rows, layer norms, a gate for each token and channel
-        dict(name="norm, 1037 odd rows", op="norm", n=1037, d=1283, h="f32", y="f32", x="f32", post=True,
+        dict(name="norm 1037 odd rows", op="norm", n=1037, d=1283, h="f32", y="f32", x="f32", post=True,
              gate="token", layer=True),
         # a long prompt, the stream held in f16, the products' f32 results added
-        dict(name="norm, 8191-token prompt", op="norm", n=8191, d=4096, h="f16", y="f32", x="f16", post=False,
+        dict(name="norm 8191-token prompt", op="norm", n=8191, d=4096, h="f16", y="f32", x="f16", post=False,
              gate="none", layer=False),
         # two requests on a short common instruction: latency
-        dict(name="shared, 2 on 300", op="shared", n_seq=2, prefix=300, lo=1, hi=40, lens=1, q_len=1, heads=32,
+        dict(name="shared 2 on 300", op="shared", n_seq=2, prefix=300, lo=1, hi=40, lens=1, q_len=1, heads=32,
              kv_heads=8, head_dim=128, page=16, dtype="f32"),
         # a decode step of a batch on one long instruction
-        dict(name="shared, 32 on 8200", op="shared", n_seq=32, prefix=8200, lo=1, hi=600, lens=2, q_len=1, heads=32,
+        dict(name="shared 32 on 8200", op="shared", n_seq=32, prefix=8200, lo=1, hi=600, lens=2, q_len=1, heads=32,
              kv_heads=8, head_dim=128, page=64, dtype="f32"),
         # three drafted tokens of each request checked at once, small heads
-        dict(name="shared, drafts", op="shared", n_seq=40, prefix=4099, lo=3, hi=300, lens=3, q_len=3, heads=24,
+        dict(name="shared drafts", op="shared", n_seq=40, prefix=4099, lo=3, hi=300, lens=3, q_len=3, heads=24,
              kv_heads=8, head_dim=64, page=32, dtype="f16"),
         # questions on one very long document
-        dict(name="shared, 16 on 65521", op="shared", n_seq=16, prefix=65521, lo=1, hi=2000, lens=4, q_len=1, heads=64,
+        dict(name="shared 16 on 65521", op="shared", n_seq=16, prefix=65521, lo=1, hi=2000, lens=4, q_len=1, heads=64,
              kv_heads=8, head_dim=128, page=128, dtype="f16"),
         # one request's next token, every filter on: latency
-        dict(name="sample, 1 row", op="sample", n=1, vocab=32000, dtype="f32", filters="all", spread=2.5, cut=0.0),
+        dict(name="sample 1 row", op="sample", n=1, vocab=32000, dtype="f32", filters="all", spread=2.5, cut=0.0),
         # a batch of requests with settings of their own, a grammar's mask on some
-        dict(name="sample, 64 rows", op="sample", n=64, vocab=32000, dtype="f32", filters="mixed", spread=2.5, cut=0.3),
+        dict(name="sample 64 rows", op="sample", n=64, vocab=32000, dtype="f32", filters="mixed", spread=2.5, cut=0.3),
         # plain sampling at a temperature from a large vocabulary
-        dict(name="sample, 8 rows, no filter", op="sample", n=8, vocab=130001, dtype="f32", filters="none", spread=3.0,
+        dict(name="sample 8 rows no filter", op="sample", n=8, vocab=130001, dtype="f32", filters="none", spread=3.0,
              cut=0.0),
         # a large batch over a large vocabulary
-        dict(name="sample, 256 rows of 130001", op="sample", n=256, vocab=130001, dtype="f16", filters="mixed",
+        dict(name="sample 256 rows of 130001", op="sample", n=256, vocab=130001, dtype="f16", filters="mixed",
              spread=2.5, cut=0.05),
     ]
 
