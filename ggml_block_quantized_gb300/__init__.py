@@ -1,7 +1,8 @@
 """GB300 block-quantized matrix-vector product: thin Python binding.
 
 The work happens in the CUDA library libqgemv.so (the C ABI of
-include/qgemv.h; attention.py binds include/qattn.h); this module only marshals arguments: it checks dtypes,
+include/qgemv.h; attention.py binds include/qattn.h, step.py
+include/qstep.h); this module only marshals arguments: it checks dtypes,
 devices and sizes of torch tensors, allocates outputs with torch when the
 caller passes none, and calls the C entry points with raw device pointers and
 the current CUDA stream. There is no fallback: if the library is missing,
@@ -24,6 +25,7 @@ __all__ = [
     "gemm_kernel_info",
     "KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes", "prompt_attend",
     "rope_table", "ATTENTION_SYMBOLS",
+    "norm_residual", "sample_tokens", "STEP_SYMBOLS",
 ]
 
 F32, F16, Q4_0, Q4_1, Q5_0, Q8_0, Q8_1 = 0, 1, 2, 3, 6, 8, 9
@@ -399,12 +401,13 @@ def device_error() -> int:
     return v.value
 
 
-# ------------------------------------------------------------ attention
-# The names of attention.py (include/qattn.h) are looked up on first use: they
-# need torch, which the C library's own binding above imports only when a
-# tensor is passed.
+# ------------------------------------------------------------ attention, norms, sampling
+# The names of attention.py (include/qattn.h) and step.py (include/qstep.h) are
+# looked up on first use: they need torch, which the C library's own binding
+# above imports only when a tensor is passed.
 _ATTENTION = frozenset(("KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes",
                         "prompt_attend", "rope_table", "ATTENTION_SYMBOLS"))
+_STEP = frozenset(("norm_residual", "sample_tokens", "STEP_SYMBOLS"))
 
 
 def __getattr__(name):
@@ -412,5 +415,10 @@ def __getattr__(name):
         from . import attention
         for n in _ATTENTION:
             globals()[n] = getattr(attention, n)
+        return globals()[name]
+    if name in _STEP:
+        from . import step
+        for n in _STEP:
+            globals()[n] = getattr(step, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

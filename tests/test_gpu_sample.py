@@ -1,0 +1,200 @@
+"""sample_tokens (include/qstep.h) on the GPU against its definition in 64 bits:
+the tokens are the same, the probabilities off by their rounding to f32 (two
+conversions and a division, each 2^-24) and by their weights' unit (weights are
+whole multiples of 2^-44 of the largest, so off by 2^-45 of it, and the sum is
+no less than the largest)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import ggml_block_quantized_gb300 as qg  # noqa: E402
+import step_ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def cuda(x, dtype):
+    return None if x is None else torch.as_tensor(np.asarray(x), dtype=dtype, device="cuda")
+
+
+def both(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None):
+    """The GPU's tokens and the definition's; asserts that they agree."""
+    f = torch.float32
+    n = logits.shape[0]
+    u = cuda(uniform, f)
+    token, prob = qg.sample_tokens(logits, u, temperature=cuda(temperature, f), top_k=cuda(top_k, torch.int32),
+                                   top_p=cuda(top_p, f), min_p=cuda(min_p, f), prob_out=torch.full((n,), 7.0, device="cuda"))
+    f32 = lambda x: None if x is None else np.asarray(x, np.float32)  # noqa: E731
+    want, want_p = step_ref.sample(logits.float().cpu().numpy(), f32(uniform), f32(temperature), top_k, f32(top_p), f32(min_p))
+    got = token.cpu().numpy()
+    assert token.dtype == torch.int32 and np.array_equal(got, want), (np.nonzero(got != want)[0][:5], got[got != want][:5], want[got != want][:5])
+    assert np.all(np.abs(prob.double().cpu().numpy() - want_p) <= 2.0 ** -22 * want_p + 2.0 ** -45)
+    return want
+
+
+def rows(n, vocab, seed, spread=2.5, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(n, vocab, generator=g, device="cuda") * spread
+    x += (torch.rand(n, vocab, generator=g, device="cuda") < 0.003) * 8 * torch.rand(n, vocab, generator=g, device="cuda")
+    return x.to(dtype), np.random.default_rng(seed)
+
+
+def u01(rng, n):
+    return rng.integers(0, 1 << 24, n) / float(1 << 24)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("n,vocab", [(1, 1), (4, 2), (3, 31), (5, 33), (7, 1000), (2, 1025), (40, 4099), (1, 32000), (6, 32768),
+                                     (3, 50257), (2, 130001), (1, 262144), (2, 524288), (200, 777)])
+def test_sizes_without_filters(n, vocab, dtype):
+    x, rng = rows(n, vocab, n + vocab, dtype=dtype)
+    both(x, u01(rng, n))
+    both(x, u01(rng, n), temperature=rng.uniform(0.3, 3.0, n))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("n,vocab", [(3, 5), (9, 700), (64, 3000), (5, 32000), (2, 130001), (1, 524288)])
+@pytest.mark.parametrize("spread", [0.0, 0.3, 2.5, 12.0])
+def test_filters(n, vocab, spread, dtype):
+    x, rng = rows(n, vocab, n * 3 + vocab, spread, dtype)
+    t = rng.uniform(0.4, 2.0, n)
+    k = np.minimum(rng.choice([0, 1, 2, 5, 40, 129, 1000, 20000, 1 << 20], n), 1 << 20)
+    p = rng.choice([1.0, 0.999, 0.95, 0.7, 0.2, 0.01], n)
+    q = rng.choice([0.0, 0.02, 0.3, 1.0], n)
+    both(x, u01(rng, n), t, k)
+    both(x, u01(rng, n), t, None, p)
+    both(x, u01(rng, n), t, None, None, q)
+    both(x, u01(rng, n), t, k, p, q)
+
+
+@pytest.mark.parametrize("vocab", [100, 5000, 40000])
+def test_equal_logits_go_by_index(vocab):
+    """Ties at the border: the lowest indexes stay."""
+    x = torch.full((8, vocab), 1.5, device="cuda")
+    x[4:, ::3] = 2.0
+    x[6:, 5] = 9.0
+    k = [7, vocab // 2, 0, 0, 7, vocab // 2, 2, 0]
+    p = [1.0, 1.0, 0.5, 0.37, 1.0, 0.9, 1.0, 0.8]
+    for u in (0.0, 0.25, 0.999999):
+        got = both(x, [u] * 8, [1.0] * 8, k, p)
+    assert got[0] == 6 and got[1] == vocab // 2 - 1
+    both(x.half(), [0.5] * 8, [0.7] * 8, k, p)
+
+
+def test_few_values():
+    """Logits of few distinct values, as after a coarse rounding: every border lies among equal ones."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randint(-6, 7, (24, 30011), generator=g, device="cuda").float()
+    rng = np.random.default_rng(1)
+    both(x, u01(rng, 24), rng.uniform(0.5, 2, 24), rng.integers(1, 30000, 24), rng.uniform(0.05, 1, 24), rng.choice([0, 0.1], 24))
+    both(x * 1e-30, u01(rng, 24), rng.uniform(0.5, 2, 24), rng.integers(1, 30000, 24), rng.uniform(0.05, 1, 24))
+
+
+def test_masks_and_odd_values():
+    x, rng = rows(12, 4001, 5)
+    x[0] = -INF
+    x[1] = NAN
+    x[2, :-1] = -INF                      # one token left
+    x[3, 100:] = torch.finfo(torch.float32).min  # masked by the type's lowest value
+    x[4, ::2] = NAN
+    x[5, 7] = INF
+    x[6, [9, 4000]] = INF
+    x[7] = -1e30
+    x[7, 3000] = 1e30
+    x[8] = torch.finfo(torch.float32).min
+    x[9, 50:] = -1e9
+    x[10] = -0.0
+    x[10, 1::2] = 0.0
+    for k, p, q in ((None, None, None), ([40] * 12, [0.9] * 12, [0.01] * 12), (None, [0.9] * 12, None), ([3000] * 12, None, None),
+                    (None, [0.999999] * 12, None)):
+        got = both(x, u01(rng, 12), [1.1] * 12, k, p, q)
+        assert got[0] == got[1] == -1 and got[2] == 4000 and got[5] == 7 and got[6] in (9, 4000) and got[7] == 3000
+
+
+def test_settings_at_their_ends():
+    n = 16
+    x, rng = rows(n, 2500, 8)
+    t = np.array([0.0, -1.0, NAN, 1e-30, 2.0 ** -60, 1e-3, 1e6, INF, 1e-38, 1.0, 1.0, 1.0, 1.0, 1.0, 1.0, 1.0], np.float32)
+    k = [0, 0, 0, 0, 0, 0, 0, 0, 0, -5, 1, 2500, 2501, 1 << 30, 0, 0]
+    p = np.array([1.0] * 9 + [0.0, -1.0, 2.0, NAN, 0.5, 1e-20, 0.99999994], np.float32)
+    q = np.array([0.0] * 12 + [NAN, 2.0, -1.0, 1e-30], np.float32)
+    with np.errstate(invalid="ignore"):
+        both(x, u01(rng, n), t)
+        both(x, u01(rng, n), None, k)
+        both(x, u01(rng, n), None, None, p)
+        both(x, u01(rng, n), None, None, None, q)
+        both(x, u01(rng, n), np.where(t > 0, t, 1), k, p, q)
+        for u in (0.0, 1.0 - 2.0 ** -24, 1.0, 5.0, -1.0, NAN, 2.0 ** -149, INF):
+            both(x, [u] * n, [1.0] * n, k, p)
+
+
+def test_every_token_has_its_share():
+    """The unit interval in 4096 steps: as many of them choose a token as its probability says, in the indexes' order."""
+    x, _ = rows(1, 300, 3, 1.0)
+    n = 4096
+    u = (np.arange(n) + 0.5) / n
+    got = both(x.expand(n, 300), u, np.full(n, 0.8), np.full(n, 50), np.full(n, 0.9))
+    assert np.all(np.diff(got) >= 0) and len(set(got.tolist())) > 20
+
+
+def test_strides_places_and_a_vocabulary_that_is_padded():
+    x, rng = rows(9, 3000, 4)
+    u = u01(rng, 9)
+    want = both(x[:, :2717].contiguous(), u, [0.9] * 9, [50] * 9, [0.8] * 9)
+    assert np.array_equal(both(x[:, :2717], u, [0.9] * 9, [50] * 9, [0.8] * 9), want)  # what lies behind has no say
+    for first in (1, 2, 3, 5):
+        both(x[::2, first:first + 2700], u[:5], [0.9] * 5, [50] * 5, [0.8] * 5)
+        both(x.half()[:, first:2001 + first], u, [0.9] * 9, None, [0.8] * 9)
+    both(x[:1].expand(9, 3000), u)
+
+
+def test_a_row_does_not_depend_on_the_others():
+    """One row alone (many blocks a row) and among many (one block a row), same bits each time."""
+    x, rng = rows(300, 20011, 6)
+    u, t, k, p = u01(rng, 300), rng.uniform(0.5, 1.5, 300), rng.integers(0, 100, 300), rng.uniform(0.5, 1, 300)
+    f, i = torch.float32, torch.int32
+    args = lambda s: dict(temperature=cuda(t[s], f), top_k=cuda(k[s], i), top_p=cuda(p[s], f), prob_out=torch.empty(len(u[s]), device="cuda"))  # noqa: E731
+    a, pa = qg.sample_tokens(x, cuda(u, f), **args(slice(None)))
+    b, pb = qg.sample_tokens(x, cuda(u, f), **args(slice(None)))
+    assert torch.equal(a, b) and torch.equal(pa, pb)
+    for r in (0, 17, 299):
+        s = slice(r, r + 1)
+        c, pc = qg.sample_tokens(x[s], cuda(u[s], f), **args(s))
+        assert torch.equal(c, a[s]) and torch.equal(pc, pa[s])
+
+
+def test_streams_and_graphs():
+    x, rng = rows(5, 32000, 2)
+    u, p = cuda(u01(rng, 5), torch.float32), cuda([0.9] * 5, torch.float32)
+    want, _ = qg.sample_tokens(x, u, top_p=p)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got, _ = qg.sample_tokens(x, u, top_p=p, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qg.sample_tokens(x, u, top_p=p, out=out)
+    for _ in range(3):
+        u.copy_(torch.rand(5, device="cuda"))
+        graph.replay()
+        want, _ = qg.sample_tokens(x, u, top_p=p)
+        assert torch.equal(out, want)
+
+
+def test_no_rows():
+    token, prob = qg.sample_tokens(torch.empty(0, 50, device="cuda"), torch.empty(0, device="cuda"))
+    assert token.shape == (0,) and prob is None
