@@ -23,8 +23,8 @@ __all__ = [
     "qgemv_batched_workspace_bytes", "BatchPlan", "device_error", "kernel_info", "EXPORTED_SYMBOLS",
     "MAX_BATCH", "tune", "qgemm_workspace_bytes", "qgemm", "qgemm_f16", "selftest_bounded_wait",
     "gemm_kernel_info",
-    "KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes", "prompt_attend",
-    "rope_table", "ATTENTION_SYMBOLS",
+    "KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes", "kv_attend_shared",
+    "kv_attend_shared_workspace_bytes", "prompt_attend", "rope_table", "ATTENTION_SYMBOLS",
     "norm_residual", "sample_tokens", "STEP_SYMBOLS",
 ]
 
@@ -406,7 +406,8 @@ def device_error() -> int:
 # looked up on first use: they need torch, which the C library's own binding
 # above imports only when a tensor is passed.
 _ATTENTION = frozenset(("KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes",
-                        "prompt_attend", "rope_table", "ATTENTION_SYMBOLS"))
+                        "kv_attend_shared", "kv_attend_shared_workspace_bytes", "prompt_attend", "rope_table",
+                        "ATTENTION_SYMBOLS"))
 _STEP = frozenset(("norm_residual", "sample_tokens", "STEP_SYMBOLS"))
 
 

@@ -4,7 +4,8 @@ A decoder layer's step in this library:
   q, k, v = the products (qgemv / qgemm)
   kv_append    rotates q and k, writes k and v to a paged cache in 4 bits
   prompt_attend  (a prompt's tokens, on the f16 rows kv_append hands out) or
-  kv_attend    (a few new tokens, over the cache)
+  kv_attend    (a few new tokens, over the cache; kv_attend_shared where the
+               sequences begin with the same tokens)
   the output product.
 
 As in the rest of the package, nothing here computes: tensors are checked,
@@ -14,11 +15,11 @@ called on the current stream (or `stream`).
 import ctypes
 
 __all__ = ["KVCache", "kv_cache_bytes", "kv_append", "kv_read", "kv_attend", "kv_attend_workspace_bytes",
-           "prompt_attend", "rope_table", "ATTENTION_SYMBOLS"]
+           "kv_attend_shared", "kv_attend_shared_workspace_bytes", "prompt_attend", "rope_table", "ATTENTION_SYMBOLS"]
 
 # every function declared in include/qattn.h
 ATTENTION_SYMBOLS = ("qkv_cache_bytes", "qkv_append", "qkv_read", "qkv_attend_workspace_bytes", "qkv_attend",
-                     "qattn_prompt")
+                     "qkv_attend_shared_workspace_bytes", "qkv_attend_shared", "qattn_prompt")
 
 
 class _Cache(ctypes.Structure):
@@ -57,6 +58,11 @@ def _lib():
         L.qkv_attend.argtypes = [cache, i32, vp, i64, vp, vp, i64, vp, vp, i64, i64, i32, i32, f32, vp,
                                  ctypes.c_size_t, vp]
         L.qkv_attend.restype = i32
+        L.qkv_attend_shared_workspace_bytes.argtypes = [i32, i32, i32, i64, i32]
+        L.qkv_attend_shared_workspace_bytes.restype = ctypes.c_size_t
+        L.qkv_attend_shared.argtypes = [cache, i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp, i64, i64, i32, i32, f32,
+                                        vp, ctypes.c_size_t, vp]
+        L.qkv_attend_shared.restype = i32
         L.qattn_prompt.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, vp, i64, i64, i32, i32, i32, f32, vp]
         L.qattn_prompt.restype = i32
         _attn = L
@@ -295,17 +301,8 @@ def kv_attend_workspace_bytes(cache: KVCache, n_heads: int, max_q_len: int = 1) 
     return int(_lib().qkv_attend_workspace_bytes(cache.head_dim, cache.n_kv_heads, n_heads, max_q_len))
 
 
-def kv_attend(cache: KVCache, q, table, lengths, q_offsets=None, max_q_len: int = 1, scale=None, out=None,
-              workspace=None, stream=None):
-    """Attention of new tokens q [n_tok, heads, D] (float32 or float16, rotated)
-    over the cache. Sequence s holds lengths[s] tokens (int32, the new ones
-    included) in the pages table[s] (int32 [n_seq, pages]); its queries are rows
-    q_offsets[s] .. q_offsets[s + 1] - 1 (int32 [n_seq + 1], at most max_q_len a
-    sequence), or row s where q_offsets is None, and belong to its last tokens:
-    each sees the tokens up to its own. scale: 1 / sqrt(D) by default. Returns
-    out [n_tok, heads, D] in q's type; zeros for a row that sees nothing. Rows
-    in no sequence are not written, nor those of a sequence with more queries
-    than max_q_len (device_error() is 4 then)."""
+def _attend_args(cache, q, table, lengths, q_offsets, out, stream):
+    """What kv_attend and kv_attend_shared take alike, checked; `out` allocated where none is given."""
     device = _place(q, "q")
     if cache.device != device:
         raise ValueError(f"the cache is on cuda:{cache.device}, not on cuda:{device}")
@@ -328,16 +325,62 @@ def kv_attend(cache: KVCache, q, table, lengths, q_offsets=None, max_q_len: int 
     if out is None:
         out = _new(q.shape, q.dtype, q.device, stream)
     out_ptr = _out(out, (n_tok, heads, d), (q.dtype,), device, "out")
+    return device, q_ptr, q_stride, n_tok, heads, table_ptr, pages, len_ptr, off_ptr, n_seq, out, out_ptr
+
+
+def kv_attend(cache: KVCache, q, table, lengths, q_offsets=None, max_q_len: int = 1, scale=None, out=None,
+              workspace=None, stream=None):
+    """Attention of new tokens q [n_tok, heads, D] (float32 or float16, rotated)
+    over the cache. Sequence s holds lengths[s] tokens (int32, the new ones
+    included) in the pages table[s] (int32 [n_seq, pages]); its queries are rows
+    q_offsets[s] .. q_offsets[s + 1] - 1 (int32 [n_seq + 1], at most max_q_len a
+    sequence), or row s where q_offsets is None, and belong to its last tokens:
+    each sees the tokens up to its own. scale: 1 / sqrt(D) by default. Returns
+    out [n_tok, heads, D] in q's type; zeros for a row that sees nothing. Rows
+    in no sequence are not written, nor those of a sequence with more queries
+    than max_q_len (device_error() is 4 then)."""
+    device, q_ptr, q_stride, n_tok, heads, table_ptr, pages, len_ptr, off_ptr, n_seq, out, out_ptr = _attend_args(
+        cache, q, table, lengths, q_offsets, out, stream)
     L = _lib()
     if workspace is None:
-        need = L.qkv_attend_workspace_bytes(d, cache.n_kv_heads, heads, max_q_len)
+        need = L.qkv_attend_workspace_bytes(cache.head_dim, cache.n_kv_heads, heads, max_q_len)
         workspace = _new((max(need, 16),), torch.uint8, q.device, stream)
     ws_ptr = _on(workspace, device, "workspace", torch.uint8)
-    st = L.qkv_attend(cache.ref, _TYPE[q.dtype], q_ptr, q_stride, out_ptr, table_ptr, pages, len_ptr, off_ptr,
-                      n_seq, n_tok, heads, max_q_len, d ** -0.5 if scale is None else scale, ws_ptr,
+    st = L.qkv_attend(cache.ref, _TYPE[q.dtype], q_ptr, q_stride, out_ptr, table_ptr, pages, len_ptr, off_ptr, n_seq,
+                      n_tok, heads, max_q_len, cache.head_dim ** -0.5 if scale is None else scale, ws_ptr,
                       workspace.numel(), _stream(stream, device))
     if st:
         _check(st, "kv_attend")
+    return out
+
+
+def kv_attend_shared_workspace_bytes(cache: KVCache, n_heads: int, n_tok: int, max_q_len: int = 1) -> int:
+    return int(_lib().qkv_attend_shared_workspace_bytes(cache.head_dim, cache.n_kv_heads, n_heads, n_tok, max_q_len))
+
+
+def kv_attend_shared(cache: KVCache, q, prefix_table, prefix_len, table, lengths, q_offsets=None, max_q_len: int = 1,
+                     scale=None, out=None, workspace=None, stream=None):
+    """kv_attend for sequences that begin with the same tokens: the prefix_len[0] ones (int32 [1]) in the pages
+    prefix_table (int32 [pages]), which every query sees, and then each sequence's own lengths[s] ones in the pages
+    table[s]. The result is kv_attend's on sequences that hold both; the prefix is read, and its products are formed,
+    once for all of them."""
+    device, q_ptr, q_stride, n_tok, heads, table_ptr, pages, len_ptr, off_ptr, n_seq, out, out_ptr = _attend_args(
+        cache, q, table, lengths, q_offsets, out, stream)
+    prefix_ptr = _on(prefix_table, device, "prefix_table", torch.int32)
+    prefix_len_ptr = _on(prefix_len, device, "prefix_len", torch.int32)
+    if prefix_table.dim() != 1 or prefix_len.numel() != 1:
+        raise ValueError("prefix_table must be [pages] and prefix_len [1]")
+    L = _lib()
+    if workspace is None:
+        need = L.qkv_attend_shared_workspace_bytes(cache.head_dim, cache.n_kv_heads, heads, n_tok, max_q_len)
+        workspace = _new((max(need, 16),), torch.uint8, q.device, stream)
+    ws_ptr = _on(workspace, device, "workspace", torch.uint8)
+    st = L.qkv_attend_shared(cache.ref, _TYPE[q.dtype], q_ptr, q_stride, out_ptr, prefix_ptr, prefix_table.shape[0],
+                             prefix_len_ptr, table_ptr, pages, len_ptr, off_ptr, n_seq, n_tok, heads, max_q_len,
+                             cache.head_dim ** -0.5 if scale is None else scale, ws_ptr, workspace.numel(),
+                             _stream(stream, device))
+    if st:
+        _check(st, "kv_attend_shared")
     return out
 
 

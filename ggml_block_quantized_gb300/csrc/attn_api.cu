@@ -36,6 +36,48 @@ int check_heads(int n_heads, int n_kv_heads) {
     return n_heads >= 1 && n_kv_heads >= 1 && n_heads % n_kv_heads == 0 && n_heads <= 65536 ? QG_OK : QG_ERR_SHAPE;
 }
 
+constexpr int64_t kMaxSharedHeads = int64_t(1) << 26;  // n_tok * n_heads of qkv_attend_shared
+
+// What qkv_attend and qkv_attend_shared check alike, and their kernels' parameters but for the error word.
+int check_attend(const qkv_cache *cache, int type, const void *q, int64_t q_stride, void *out, const int32_t *table,
+                 int64_t table_stride, const int32_t *lengths, const int32_t *q_offsets, int64_t n_seq, int64_t n_tok,
+                 int n_heads, int max_q_len, float scale, void *workspace, size_t workspace_bytes, size_t need,
+                 KvAttendParams *p, bool *nothing) {
+    const int st = check_cache(cache, &p->c);
+    if (st != QG_OK) return st;
+    if (!float_type(type)) return QG_ERR_TYPE;
+    const int d = cache->head_dim;
+    if (check_heads(n_heads, cache->n_kv_heads) != QG_OK || n_seq < 0 || n_tok < 0 || max_q_len < 1 ||
+        n_seq > (1 << 24) || n_tok > (1 << 30) || table_stride < 0 || table_stride > INT32_MAX || (!q_offsets && n_tok < n_seq) ||
+        !(scale == scale) || scale - scale != 0.0f)
+        return QG_ERR_SHAPE;
+    if (need == 0) return QG_ERR_SHAPE;
+    *nothing = n_seq == 0 || n_tok == 0;
+    if (*nothing) return QG_OK;
+    if (!q || !out || !lengths || (!table && table_stride > 0) || (!cache->data && cache->n_pages > 0))
+        return QG_ERR_NULL;
+    if (!aligned16(cache->data) || !aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(table) ||
+        !aligned4(lengths) || !aligned4(q_offsets))
+        return QG_ERR_ALIGN;
+    if (!stride_ok(q_stride, static_cast<int64_t>(n_heads) * d, type)) return QG_ERR_SHAPE;
+    if (!workspace || workspace_bytes < need) return QG_ERR_WORKSPACE;
+    p->q = q;
+    p->out = out;
+    p->table = table;
+    p->lengths = lengths;
+    p->q_offsets = q_offsets;
+    p->q_stride = q_stride;
+    p->table_stride = table_stride;
+    p->partial = static_cast<float *>(workspace);
+    p->scale = scale;
+    p->n_seq = static_cast<int>(n_seq);
+    p->n_tok = static_cast<int>(n_tok);
+    p->n_heads = n_heads;
+    p->group = n_heads / cache->n_kv_heads;
+    p->max_q_len = max_q_len;
+    return QG_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -121,44 +163,49 @@ int qkv_attend(const qkv_cache *cache, int type, const void *q, int64_t q_stride
                int64_t table_stride, const int32_t *lengths, const int32_t *q_offsets, int64_t n_seq, int64_t n_tok,
                int n_heads, int max_q_len, float scale, void *workspace, size_t workspace_bytes, qg_stream_t stream) {
     KvAttendParams p = {};
-    int st = check_cache(cache, &p.c);
-    if (st != QG_OK) return st;
-    if (!float_type(type)) return QG_ERR_TYPE;
-    const int d = cache->head_dim;
-    if (check_heads(n_heads, cache->n_kv_heads) != QG_OK || n_seq < 0 || n_tok < 0 || max_q_len < 1 ||
-        n_seq > (1 << 24) || n_tok > (1 << 30) || table_stride < 0 || table_stride > INT32_MAX || (!q_offsets && n_tok < n_seq) ||
-        !(scale == scale) || scale - scale != 0.0f)
-        return QG_ERR_SHAPE;
-    const size_t need = qkv_attend_workspace_bytes(d, cache->n_kv_heads, n_heads, max_q_len);
-    if (need == 0) return QG_ERR_SHAPE;
-    if (n_seq == 0 || n_tok == 0) return QG_OK;
-    if (!q || !out || !lengths || (!table && table_stride > 0) || (!cache->data && cache->n_pages > 0))
-        return QG_ERR_NULL;
-    if (!aligned16(cache->data) || !aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(table) ||
-        !aligned4(lengths) || !aligned4(q_offsets))
-        return QG_ERR_ALIGN;
-    if (!stride_ok(q_stride, static_cast<int64_t>(n_heads) * d, type)) return QG_ERR_SHAPE;
-    if (!workspace || workspace_bytes < need) return QG_ERR_WORKSPACE;
+    const size_t need = cache ? qkv_attend_workspace_bytes(cache->head_dim, cache->n_kv_heads, n_heads, max_q_len) : 0;
+    bool nothing = false;
+    int st = check_attend(cache, type, q, q_stride, out, table, table_stride, lengths, q_offsets, n_seq, n_tok, n_heads,
+                          max_q_len, scale, workspace, workspace_bytes, need, &p, &nothing);
+    if (st != QG_OK || nothing) return st;
     DeviceInfo dev;
     st = current_device(&dev);
     if (st != QG_OK) return st;
-    p.q = q;
-    p.out = out;
-    p.table = table;
-    p.lengths = lengths;
-    p.q_offsets = q_offsets;
-    p.q_stride = q_stride;
-    p.table_stride = table_stride;
-    p.partial = static_cast<float *>(workspace);
     p.err = dev.err;
-    p.scale = scale;
-    p.n_seq = static_cast<int>(n_seq);
-    p.n_tok = static_cast<int>(n_tok);
-    p.n_heads = n_heads;
-    p.group = n_heads / cache->n_kv_heads;
-    p.max_q_len = max_q_len;
-    const cudaError_t e = launch_kv_attend(p, d, type, dev.sms, dev.device, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e =
+        launch_kv_attend(p, cache->head_dim, type, dev.sms, dev.device, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QG_OK : cuda_fail(e, "kv_attend launch");
+}
+
+size_t qkv_attend_shared_workspace_bytes(int head_dim, int n_kv_heads, int n_heads, int64_t n_tok, int max_q_len) {
+    if (qkv_attend_workspace_bytes(head_dim, n_kv_heads, n_heads, max_q_len) == 0 || n_tok < 0 || n_tok > kMaxSharedHeads / n_heads) return 0;
+    return shared_attend_workspace(head_dim, n_kv_heads, n_heads / n_kv_heads, n_tok, max_q_len);
+}
+
+int qkv_attend_shared(const qkv_cache *cache, int type, const void *q, int64_t q_stride, void *out,
+                      const int32_t *prefix_table, int64_t prefix_pages, const int32_t *prefix_len, const int32_t *table,
+                      int64_t table_stride, const int32_t *lengths, const int32_t *q_offsets, int64_t n_seq,
+                      int64_t n_tok, int n_heads, int max_q_len, float scale, void *workspace, size_t workspace_bytes,
+                      qg_stream_t stream) {
+    SharedParams p = {};
+    const size_t need = cache ? qkv_attend_shared_workspace_bytes(cache->head_dim, cache->n_kv_heads, n_heads, n_tok, max_q_len) : 0;
+    if (prefix_pages < 0 || prefix_pages > INT32_MAX) return QG_ERR_SHAPE;
+    bool nothing = false;
+    int st = check_attend(cache, type, q, q_stride, out, table, table_stride, lengths, q_offsets, n_seq, n_tok, n_heads,
+                          max_q_len, scale, workspace, workspace_bytes, need, &p.own, &nothing);
+    if (st != QG_OK || nothing) return st;
+    if (!prefix_len || (!prefix_table && prefix_pages > 0)) return QG_ERR_NULL;
+    if (!aligned4(prefix_table) || !aligned4(prefix_len)) return QG_ERR_ALIGN;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != QG_OK) return st;
+    p.own.err = dev.err;
+    p.prefix_table = prefix_table;
+    p.prefix_len = prefix_len;
+    p.prefix_pages = prefix_pages;
+    const cudaError_t e =
+        launch_shared_attend(p, cache->head_dim, type, dev.sms, dev.device, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QG_OK : cuda_fail(e, "kv_attend_shared launch");
 }
 
 int qattn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,

@@ -909,6 +909,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 }
                 // a part's result: slot 0 if it enters the segment from outside, slot 1 if the segment starts in it
                 float *part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (from ? 1 : 0)) * part_floats(D, ROWS);
+                float *part_stats = part + ROWS * D + 2 * r;
+                part += r * D;
+                const bool to_out = whole && p.rest == nullptr;
+                if (whole && !to_out) part = p.rest + static_cast<int64_t>(out_row) * D, part_stats = p.rest_stats + 2 * static_cast<int64_t>(out_row);
                 const float inv = !whole ? 1.0f : den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
                 T *out = static_cast<T *>(p.out) + static_cast<int64_t>(out_row) * D;
                 const bool odd = *odd_flag != 0;
@@ -924,14 +928,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                     }
                     if (odd && odd_tokens<D>(p, seg, least, limit, tile0 * kTile, (tile0 + n) * kTile, d >> 5))
                         sum.x = sum.y = sum.z = sum.w = NAN;
-                    if (whole) {
+                    if (!to_out) {
+                        *reinterpret_cast<float4 *>(part + d) = sum;
+                    } else {
                         store2(out + d, sum.x * inv, sum.y * inv);
                         store2(out + d + 2, sum.z * inv, sum.w * inv);
-                    } else {
-                        *reinterpret_cast<float4 *>(part + r * D + d) = sum;
                     }
                 }
-                if (!whole && threadIdx.x % kPer == 0) store2(part + ROWS * D + 2 * r, top, den);
+                if (!to_out && threadIdx.x % kPer == 0) store2(part_stats, top, den);
             }
             if (!whole && from && threadIdx.x == 0) {  // (thread 0 wrote the 0 above)
                 const int row0 = seg.rt * ROWS;
@@ -1028,9 +1032,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvAttend
             }
             const int row = cut.row0 + r, tok = row / p.group;
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-            store2(static_cast<T *>(p.out) +
-                       (static_cast<int64_t>(cut.q0 + tok) * p.n_heads + cut.head * p.group + row - tok * p.group) * D + d,
-                   sum.x * inv, sum.y * inv);
+            const int64_t out_row = static_cast<int64_t>(cut.q0 + tok) * p.n_heads + cut.head * p.group + row - tok * p.group;
+            if (p.rest == nullptr) {
+                store2(static_cast<T *>(p.out) + out_row * D + d, sum.x * inv, sum.y * inv);
+            } else {
+                store2(p.rest + out_row * D + d, sum.x, sum.y);
+                if (d == 0) store2(p.rest_stats + 2 * out_row, top, den);
+            }
         }
         __syncthreads();  // sums and stats are the next row's
     }

@@ -72,10 +72,24 @@ struct KvAttendParams {
     int32_t *err;
     float scale;
     int n_seq, n_tok, n_heads, group, max_q_len;
+    // Not null: instead of out, each row's values before the division, [n_tok][n_heads][D], and its reference (a power
+    // of 2) and sum, for a join with what it sees elsewhere.
+    float *rest, *rest_stats;
 };
 
 size_t kv_attend_workspace(int head_dim, int rows);
 cudaError_t launch_kv_attend(const KvAttendParams &p, int head_dim, int type, int sms, int device, cudaStream_t s);
+
+struct SharedParams {
+    KvAttendParams own;           // of the sequences' own tokens
+    const int32_t *prefix_table, *prefix_len;
+    int64_t prefix_pages;
+    float *stretches;             // (the launch's)
+    int row_tiles;
+};
+
+size_t shared_attend_workspace(int head_dim, int n_kv_heads, int group, int64_t n_tok, int max_q_len);
+cudaError_t launch_shared_attend(SharedParams p, int head_dim, int type, int sms, int device, cudaStream_t s);
 
 struct PromptParams {
     const void *q, *k, *v;

@@ -142,6 +142,37 @@ int qkv_attend(const qkv_cache *cache, int type, const void *q, int64_t q_stride
                int64_t table_stride, const int32_t *lengths, const int32_t *q_offsets, int64_t n_seq, int64_t n_tok,
                int n_heads, int max_q_len, float scale, void *workspace, size_t workspace_bytes, qg_stream_t stream);
 
+/* ---- Attention of a batch that shares a prefix ------------------------------- */
+
+/* Workspace bytes of qkv_attend_shared, for calls of up to n_tok query rows.
+ * 0 on a bad argument. Depends on no length. */
+size_t qkv_attend_shared_workspace_bytes(int head_dim, int n_kv_heads, int n_heads, int64_t n_tok, int max_q_len);
+
+/* Attention of the newest tokens of n_seq sequences that begin with the same
+ * tokens: the prefix's prefix_len[0] ones (device), token t in page
+ * prefix_table[t / page_size] of prefix_pages entries, row t % page_size, and
+ * then each sequence's own, given as qkv_attend's (lengths, table and the rule
+ * of what a query sees count the own tokens alone). Every query sees the whole
+ * prefix:
+ *   s_t = scale q . k_t, out = sum_t exp(s_t - max s) v_t / sum_t exp(s_t - max s)
+ * over the prefix's tokens and the own ones that it sees; the result is that of
+ * qkv_attend on sequences that hold both, but the prefix is read and its products
+ * are formed once for all of them. Where neither holds a token seen, zeros.
+ *
+ * Everything said at qkv_attend holds here, with these differences. Keys and
+ * values of the prefix enter the products as two f16 parts, which hold them
+ * exactly beside the largest ones of their 128 tokens down to 2^-33 of those; a
+ * weight below 2^-31 of its row's largest in the prefix is lost. A prefix length
+ * outside 0 .. prefix_pages * page_size is taken as the nearer end, a page
+ * outside the cache as tokens that are not seen (both code 4). A key block of
+ * the prefix whose scale is not finite makes every row NaN. n_tok * n_heads is
+ * at most 2^26. */
+int qkv_attend_shared(const qkv_cache *cache, int type, const void *q, int64_t q_stride, void *out,
+                      const int32_t *prefix_table, int64_t prefix_pages, const int32_t *prefix_len, const int32_t *table,
+                      int64_t table_stride, const int32_t *lengths, const int32_t *q_offsets, int64_t n_seq,
+                      int64_t n_tok, int n_heads, int max_q_len, float scale, void *workspace, size_t workspace_bytes,
+                      qg_stream_t stream);
+
 /* ---- Attention over whole prompts ------------------------------------------- */
 
 /* Causal attention over n_seq packed sequences: sequence s is rows offsets[s]
