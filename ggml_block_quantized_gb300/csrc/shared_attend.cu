@@ -12,21 +12,40 @@
 #include <atomic>
 #include <cfloat>
 
-#include "kv_cache.cuh"
+#include "tc_attend.cuh"
 
 namespace qg {
 
 namespace {
 
-constexpr int kRows = 128;   // of an item
-constexpr int kTokens = 128; // of a unit
+constexpr int kRows = 128;    // of an item
+constexpr int kTokens = 128;  // of a unit
 constexpr int kMaxParts = 160;
 
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+// Roles by warpgroup; the registers of each (a thread) sum up to no more than the launch's.
+constexpr int kExpanders = 8;  // warps that turn codes into operands
+constexpr int kThreads = (12 + kExpanders) * 32;
+constexpr int kLaunchRegs = 96, kIssueRegs = 40, kSoftmaxRegs = 136, kSumRegs = 168, kExpandRegs = 64;
+static_assert(128 * (kIssueRegs + kSoftmaxRegs + kSumRegs) + 32 * kExpanders * kExpandRegs <= kThreads * kLaunchRegs, "registers");
+
+// Tensor memory: S of even and odd tiles (the weights over its first half), O, the weights' low parts.
+constexpr uint32_t kTmemCols = 512, kTmemO = 256, kTmemLow = 384;
+constexpr float kHigh = 14.0f, kLow = 7.0f;  // log2 of the largest weight, and of the largest when the reference is set
+
+template <int D, int TERMS> struct Shape {
+    using G = KvGroup<D>;
+    static constexpr int kPart = kTokens * D * 2;              // one f16 part of a key, value or query tile
+    static constexpr int kRawCodes = kTokens * D / 2;          // codes of a unit's keys (or values)
+    static constexpr int kRaw = kRawCodes + kTokens * G::kScaleRow;
+    static constexpr int kSlots = TERMS == 2 && D == 128 ? 3 : 6;
+    static constexpr int kOffQ = 0, kOffK = TERMS * kPart, kOffV = kOffK + 2 * kPart;  // parts: high, low
+    static constexpr int kOffRaw = kOffV + 2 * kPart;
+    static constexpr int kOffBars = kOffRaw + kSlots * kRaw;
+    static constexpr int kOffKeep = kOffBars + 512;            // [tile % 4][row]: what the sums before a tile are multiplied by
+    static constexpr int kOffFactor = kOffKeep + 4 * kRows * 4;  // [stretch % 4][row]: a row's scores as powers of 2
+    static constexpr int kSmem = kOffFactor + 4 * kRows * 4 + 1024;  // (alignment)
+    static_assert(kSmem <= kSmemLimit, "shared memory");
+};
 
 // The prefix's length, checked, and the list of units.
 struct Units {
@@ -48,75 +67,505 @@ struct Units {
 // A stretch's place: parts and items both rise along the list, one of them at least from stretch to stretch.
 __host__ __device__ constexpr int64_t stretch_floats(int d) { return static_cast<int64_t>(kRows) * (d + 2); }
 
-// The channel whose value lies at place `at` of a stretch's row.
-template <int D> __device__ __forceinline__ int channel_at(int at) { return at; }
+// A stretch's rows hold the channels in the order in which the value codes lie in the cache: place 8 (8 h + u) + 2 j + b
+// holds channel 64 h + 32 b + 2 u + {0, 1, 16, 17}[j].
 
-// A thread a row.
-template <int D, class T> __global__ void __launch_bounds__(kRows) prefix_kernel(const SharedParams p) {
-    using G = KvGroup<D>;
-    __shared__ float k_row[D], v_row[D];
-    pdl_allow_dependents();
-    pdl_wait_prior_grids();
-    const KvAttendParams &a = p.own;
-    const Units units(p, gridDim.x);
-    int64_t u = blockIdx.x * units.share;
-    const int64_t past = min(u + units.share, units.all);
-    const float c = a.scale * 1.4426950408889634f;
-    while (u < past) {
-        const int64_t item = u / units.tiles;
-        const int tile0 = static_cast<int>(u - item * units.tiles), n = static_cast<int>(min(past - u, static_cast<int64_t>(units.tiles - tile0)));
+// Walks a part's stretches, alike in every role.
+struct Stretch {
+    int64_t u, past;  // the next unit, the part's end
+    int item, tile, n, index = -1;
+    __device__ __forceinline__ bool next(const Units &units) {
+        if (u >= past) return false;
+        item = static_cast<int>(u / units.tiles);
+        tile = static_cast<int>(u - static_cast<int64_t>(item) * units.tiles);
+        n = static_cast<int>(min(past - u, static_cast<int64_t>(units.tiles - tile)));
         u += n;
-        const int head = static_cast<int>(item / p.row_tiles), row = static_cast<int>(item % p.row_tiles) * kRows + threadIdx.x;
-        const int tok = row / a.group;
-        const bool live = tok < a.n_tok;
-        float q[D], o[D];
-        for (int i = 0; i < D; ++i) {
-            q[i] = live ? static_cast<float>(static_cast<const T *>(a.q)[tok * a.q_stride + (static_cast<int64_t>(head) * a.group + row - tok * a.group) * D + i]) : 0.0f;
-            o[i] = 0.0f;
-        }
-        float ref = -INFINITY, sum = 0.0f;
-        for (int t = tile0 * kTokens; t < min((tile0 + n) * kTokens, units.len); ++t) {
-            const int page = __ldg(p.prefix_table + t / a.c.page_size);
-            if (page < 0 || page >= a.c.n_pages) {
-                if (threadIdx.x == 0) record_error(a.err, kErrBadIndex);
-                continue;
-            }
-            const uint8_t *g = a.c.template group<D>(page * a.c.page_size + t % a.c.page_size, head);
-            const int i = t & 15, vr = kv_value_row(i), j = threadIdx.x & 15;
-            __syncthreads();
-            if (threadIdx.x < D / 2) {
-                const int b = threadIdx.x >> 4;
-                const uint8_t kb = g[i * G::kRow + ((j / 4) * G::kNB + b) * 4 + j % 4];
-                const uint8_t vb = g[G::kV + vr * G::kRow + (kv_value_unit(vr, j / 2) * G::kNB + b) * 2 + j % 2];
-                const float ks = f16_bits_to_f32(reinterpret_cast<const unsigned short *>(g + G::kKS + i * G::kScaleRow)[b]);
-                const uint32_t bits = reinterpret_cast<const unsigned short *>(g + G::kVS + i * G::kScaleRow)[b];
-                const float vs = (bits & 0x7C00u) == 0x7C00u ? NAN : f16_bits_to_f32(bits);
-                k_row[32 * b + j] = ((kb & 15) - 8) * ks, k_row[32 * b + 16 + j] = ((kb >> 4) - 8) * ks;
-                v_row[32 * b + j] = ((vb & 15) - 8) * vs, v_row[32 * b + 16 + j] = ((vb >> 4) - 8) * vs;
-            }
-            __syncthreads();
-            float s = 0.0f;
-            for (int d = 0; d < D; ++d) s = fmaf(q[d], k_row[d], s);
-            s *= c;
-            const float next = fmaxf(ref, s), keep = exp2_approx(ref - (next == -INFINITY ? 0.0f : next)), w = exp2_approx(s - (next == -INFINITY ? 0.0f : next));
-            ref = next;
-            sum = fmaf(sum, keep, w);
-            for (int d = 0; d < D; ++d) o[d] = fmaf(o[d], keep, w * v_row[d]);
-        }
-        float *out = p.stretches + (blockIdx.x + item) * stretch_floats(D);
-        for (int d = 0; d < D; ++d) out[threadIdx.x * D + d] = o[d];
-        reinterpret_cast<float2 *>(out + kRows * D)[threadIdx.x] = make_float2(ref, sum);
+        ++index;
+        return true;
+    }
+};
+
+// code - 8 in f16 of the low (high) nibbles of bytes 0 and 2.
+__device__ __forceinline__ __half2 low_codes(uint32_t w) {
+    const uint32_t x = (w & 0x000F000Fu) | 0x64006400u, y = 0x64086408u;  // 1024 + c, 1032
+    return __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
+}
+__device__ __forceinline__ __half2 high_codes(uint32_t w) {
+    const uint32_t x = (w & 0x00F000F0u) | 0x64006400u, y = 0x2C002C00u, z = 0xD480D480u;  // (1024 + 16 c) / 16 - 72
+    return __hfma2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y), *reinterpret_cast<const __half2 *>(&z));
+}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+
+// Two codes' values in two f16 parts, which hold them exactly (four bits times eleven) above f16's end.
+__device__ __forceinline__ void two_parts(__half2 code, __half2 scale, uint32_t &high, uint32_t &low) {
+    const __half2 h = __hmul2(code, scale);
+    high = bits(h);
+    low = bits(__hfma2(code, scale, __hneg2(h)));
+}
+
+// One word of a row: eight values into 16 bytes of each part.
+__device__ __forceinline__ void expand_word(uint32_t w, __half2 scale, uint8_t *high, uint8_t *low) {
+    uint4 h, l;
+    two_parts(low_codes(w), scale, h.x, l.x);
+    two_parts(low_codes(w >> 8), scale, h.y, l.y);
+    two_parts(high_codes(w), scale, h.z, l.z);
+    two_parts(high_codes(w >> 8), scale, h.w, l.w);
+    *reinterpret_cast<uint4 *>(high) = h;
+    *reinterpret_cast<uint4 *>(low) = l;
+}
+
+// The power of two that takes a tile's largest scale to 2^8 .. 2^9 (f16 exponent fields; scales of rows that count,
+// every lane four rows), as its exponent. The tile's values are then below 2^13 and exact down to 2^-33 of that.
+template <int D> __device__ __forceinline__ int tile_exponent(const uint8_t *scales, int rows, uint32_t groups) {
+    const int row = 4 * (threadIdx.x & 31);
+    uint32_t m = 0;
+    if ((groups >> (row >> 4)) & 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row + i < rows)
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w)
+                    m = __vmaxu2(m, reinterpret_cast<const uint32_t *>(scales)[(row + i) * (D / 64) + w] & 0x7FFF7FFFu);
+    const uint32_t most = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) >> 10;
+    return 23 - static_cast<int>(most == 0 ? 1 : most);
+}
+// A row's scales times 2^e, infinities as NaN; 0 for a row that does not count.
+template <int D> __device__ __forceinline__ void row_scales(const uint8_t *scales, int row, bool counts, int e, __half (&d)[D / 32]) {
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {
+        const uint32_t x = counts ? reinterpret_cast<const uint32_t *>(scales)[row * (D / 64) + w] : 0u;
+        float2 f = unpack_half2(x);
+        if ((x & 0x7C00u) == 0x7C00u) f.x = NAN;
+        if ((x & 0x7C000000u) == 0x7C000000u) f.y = NAN;
+        d[2 * w] = __float2half_rn(f.x * up), d[2 * w + 1] = __float2half_rn(f.y * up);
     }
 }
 
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {  // elements 0 .. 3 and 16 .. 19
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p + 16));
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __half *p, float (&x)[8]) {
+    const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p)), b = __ldg(reinterpret_cast<const uint2 *>(p + 16));
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = unpack_half2(w[i]).x, x[2 * i + 1] = unpack_half2(w[i]).y;
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams p) {
+    constexpr int TERMS = sizeof(T) == 4 ? 2 : 1, NB = D / 32;
+    using Sh = Shape<D, TERMS>;
+    using G = KvGroup<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);  // (the swizzle's atoms are 1024 bytes)
+    const uint32_t base = smem_addr(smem), bars = base + Sh::kOffBars;
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * Sh::kSlots, k_ready = raw_empty + 8 * Sh::kSlots, k_done = k_ready + 8;
+    const uint32_t v_ready = k_done + 8, s_full = v_ready + 8, p_ready = s_full + 16, o_full = p_ready + 16, o_free = o_full + 8;
+    const uint32_t mfinal = o_free + 8;  // up to 20 barriers: 160 bytes
+    uint8_t *const words = smem + Sh::kOffBars + 256;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(words);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(words + 4);
+    volatile int *const groups = reinterpret_cast<volatile int *>(words + 16);     // [tile % 16]: its groups that lie in a page
+    volatile int *const k_exp = reinterpret_cast<volatile int *>(words + 80);      // [tile % 4]
+    volatile int *const v_exp = reinterpret_cast<volatile int *>(words + 96);
+    volatile float *const keep = reinterpret_cast<volatile float *>(smem + Sh::kOffKeep);
+    volatile float *const factor = reinterpret_cast<volatile float *>(smem + Sh::kOffFactor);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const KvAttendParams &a = p.own;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, kExpanders);
+        }
+        mbar_init(k_ready, kExpanders);
+        mbar_init(k_done, 1);
+        mbar_init(v_ready, kExpanders);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full + 8 * x, 1);
+            mbar_init(p_ready + 8 * x, 4);
+        }
+        mbar_init(o_full, 1);
+        mbar_init(o_free, 4);
+        mbar_init(mfinal, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        tc_alloc(smem_addr(tmem_slot), kTmemCols);
+        tc_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_prior_grids();
+    pdl_allow_dependents();
+    const Units units(p, gridDim.x);
+    Stretch st;
+    st.u = blockIdx.x * units.share;
+    st.past = min(st.u + units.share, units.all);
+    // A wait of a whole warp that gives up sets the abort flag, with which the others give up soon.
+    auto failed = [&](int32_t code) {
+        if (lane == 0) record_error(a.err, code);
+        *abort_flag = 1;
+        __syncwarp();
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return static_cast<bool>(__all_sync(0xffffffffu, sleep_wait<20>(bar, parity & 1u, abort_flag)));
+    };
+
+    if (warp < 4) {
+        fewer_registers<kIssueRegs>();
+        if (warp == 0) {
+            // ---------------- copies: of each unit the keys' codes and scales, then (a unit behind) the values'
+            int piece = 0, last = 0;  // pieces so far
+            bool ok = true;
+            // this lane's group of a unit, as a byte offset in the cache; -1: none
+            auto source = [&](int item, int tile) -> int64_t {
+                const int t = tile * kTokens + 16 * (lane & 7);
+                if (t >= units.len) return -1;
+                const int page = __ldg(p.prefix_table + t / a.c.page_size);
+                if (page < 0 || page >= a.c.n_pages) {
+                    record_error(a.err, kErrBadIndex);
+                    return -1;
+                }
+                return ((static_cast<int64_t>(page) * a.c.n_heads + item / p.row_tiles) * a.c.page_groups + t % a.c.page_size / 16) * G::kBytes;
+            };
+            auto copy = [&](int64_t src, bool values) {
+                const int slot = piece % Sh::kSlots;
+                if (piece >= Sh::kSlots) ok = wait(raw_empty + 8 * slot, piece / Sh::kSlots - 1);
+                if (!ok) return;
+                const uint32_t valid = __ballot_sync(0xffffffffu, src >= 0) & 255u;
+                const uint32_t dst = base + Sh::kOffRaw + slot * Sh::kRaw, bar = raw_full + 8 * slot;
+                if (lane == 0) {
+                    if (!values) groups[last % 16] = static_cast<int>(valid);
+                    mbar_arrive_expect_tx(bar, __popc(valid) * (18 * D / 2));
+                }
+                __syncwarp();
+                if (src >= 0 && lane < 8)
+                    bulk_copy_g2s_plain(dst + lane * (8 * D), a.c.data + src + (values ? G::kV : 0), 8 * D, bar);
+                else if (src >= 0 && lane < 16)
+                    bulk_copy_g2s_plain(dst + Sh::kRawCodes + (lane & 7) * D, a.c.data + src + (values ? G::kVS : G::kKS), D, bar);
+                ++piece;
+            };
+            int64_t before = -1;  // the unit before's
+            bool any = false;
+            while (ok && st.next(units)) {
+                for (int j = 0; ok && j < st.n; ++j, ++last) {
+                    const int64_t src = source(st.item, st.tile + j);
+                    copy(src, false);
+                    if (ok && any) copy(before, true);
+                    before = src, any = true;
+                }
+            }
+            if (ok && any) copy(before, true);
+            if (!ok) failed(kErrProducerWait);
+            // leave no copy in flight into this block's shared memory
+            bool landed = true;
+            for (int k = piece > Sh::kSlots ? piece - Sh::kSlots : 0; k < piece; ++k)
+                landed = mbar_wait_bounded(raw_full + 8 * (k % Sh::kSlots), (k / Sh::kSlots) & 1) && landed;
+            if (!landed) record_error(a.err, kErrDrainWait);
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------- products (the whole warp, one lane issues)
+            const uint32_t issue = lane == 0;
+            constexpr uint32_t kIdS = tc_idesc_f16(128, kTokens), kIdO = tc_idesc_f16(128, D) | kIdescNMajorB;
+            constexpr uint32_t kPart = Sh::kPart / 16;
+            const uint32_t q = desc_lo(base + Sh::kOffQ, 1), k = desc_lo(base + Sh::kOffK, 1), v = desc_lo(base + Sh::kOffV, 128 * 128 / 16);
+            auto tight = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, tc_wait(bar, parity & 1u, abort_flag))); };
+            bool ok = true;
+            int n = 0;  // units so far
+            auto product_o = [&](int j) {
+                ok = tight(p_ready + 8 * (j & 1), j >> 1) && tight(v_ready, j) && (j == 0 || tight(o_free, j - 1));
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t w = tmem + 128 * (j & 1), w_low = tmem + kTmemLow + 64 * (j & 1);
+                // small terms first: what the tensor cores cut off at each sum is then of the small ones
+                if (TERMS == 2) mma_pv(issue, tmem + kTmemO, w_low, v, kIdO, 0, kDescHi);
+                mma_pv(issue, tmem + kTmemO, w, v + kPart, kIdO, TERMS == 2, kDescHi);
+                mma_pv(issue, tmem + kTmemO, w, v, kIdO, 1, kDescHi);
+                commit(issue, o_full);
+            };
+            while (ok && st.next(units)) {
+                for (int j = 0; ok && j < st.n; ++j, ++n) {
+                    ok = tight(k_ready, n);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t s = tmem + 128 * (n & 1);
+                    if (TERMS == 2) mma_s<D>(issue, s, q + kPart, k, kIdS, kDescHi, 0);
+                    mma_s<D>(issue, s, q, k + kPart, kIdS, kDescHi, TERMS == 2);
+                    mma_s<D>(issue, s, q, k, kIdS, kDescHi, 1);
+                    commit(issue, s_full + 8 * (n & 1));
+                    commit(issue, k_done);
+                    if (n > 0) product_o(n - 1);
+                }
+            }
+            if (ok && n > 0) product_o(n - 1);
+            if (!ok) failed(kErrConsumerWait);
+            commit(issue, mfinal);  // every product complete before tensor memory is freed, after a wait that gave up, too
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(mfinal, 0)) && issue) record_error(a.err, kErrDrainWait);
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ---------------- softmax: thread = row = tensor-memory lane
+        more_registers<kSoftmaxRegs>();
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        bool ok = true;
+        int n = 0;
+        while (ok && st.next(units)) {
+            float ref = -INFINITY;
+            float2 sum = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < st.n; ++j, ++n) {
+                ok = wait(s_full + 8 * (n & 1), n >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t s_t = tmem + lanes + 128 * (n & 1), low_t = tmem + lanes + kTmemLow + 64 * (n & 1);
+                const int rows = min(kTokens, units.len - (st.tile + j) * kTokens);
+                const uint32_t in_page = static_cast<uint32_t>(groups[n % 16]);
+                const bool full = rows == kTokens && in_page == 255u;
+                const float c = fminf(fmaxf(factor[(st.index & 3) * kRows + row] * __uint_as_float(static_cast<uint32_t>(127 - k_exp[n & 3]) << 23), 1e-37f), FLT_MAX);
+                auto load = [&](int i, uint32_t (&v)[32]) {
+                    tm_ld32(s_t + 32 * i, v);
+                    tm_wait_ld(v);
+                    if (!full)
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            if (32 * i + q >= rows || !((in_page >> (2 * i + (q >> 4))) & 1)) v[q] = 0xFF800000u;
+                };
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[32];
+                    load(i, v);
+                    float m[2] = {__uint_as_float(v[0]), __uint_as_float(v[1])};
+#pragma unroll
+                    for (int q = 2; q < 32; q += 2) m[0] = fmaxf(m[0], __uint_as_float(v[q])), m[1] = fmaxf(m[1], __uint_as_float(v[q + 1]));
+                    top = fmaxf(top, fmaxf(m[0], m[1]));
+                }
+                top *= c;
+                float down = 1.0f;
+                if (top - kHigh > ref) {
+                    const float next = fmaxf(top - kLow, -FLT_MAX);
+                    down = exp2_approx(ref - next);
+                    ref = next;
+                    sum.x *= down, sum.y *= down;
+                }
+                keep[(n & 3) * kRows + row] = down;
+                const float r = ref == -INFINITY ? 0.0f : ref;  // (no token seen yet: weights of 0)
+                const float2 c2 = make_float2(c, c), r2 = make_float2(-r, -r);
+                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[32], w[16], w_low[16];
+                    load(i, v);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        float2 e = ffma2(make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), c2, r2);
+                        e.x = exp2_approx(e.x), e.y = exp2_approx(e.y);
+                        part[q & 1] = fadd2(part[q & 1], e);
+                        w[q] = pack_half2(e.x, e.y);
+                        if (TERMS == 2) {
+                            const float2 h = unpack_half2(w[q]);
+                            w_low[q] = pack_half2(e.x - h.x, e.y - h.y);
+                        }
+                    }
+                    tc_st16(s_t + 16 * i, w);
+                    if (TERMS == 2) tc_st16(low_t + 16 * i, w_low);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * (n & 1));
+                sum = fadd2(sum, fadd2(part[0], part[1]));
+            }
+            if (ok)
+                reinterpret_cast<float2 *>(p.stretches + (blockIdx.x + static_cast<int64_t>(st.item)) * stretch_floats(D) + kRows * D)[row] =
+                    make_float2(ref, sum.x + sum.y);
+        }
+        if (!ok) failed(kErrConsumerWait);
+    } else if (warp < 12) {
+        // ---------------- the values' sums: a row a thread, in registers (in tensor memory every addition cuts off)
+        more_registers<kSumRegs>();
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t o_t = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kTmemO;
+        bool ok = true;
+        int n = 0;
+        while (ok && st.next(units)) {
+            float2 o[D / 2];
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) o[i] = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < st.n; ++j, ++n) {
+                ok = wait(o_full, n);
+                if (!ok) break;
+                tc_fence_after();
+                const float f = keep[(n & 3) * kRows + row], u = __uint_as_float(static_cast<uint32_t>(127 - v_exp[n & 3]) << 23);
+                const float2 f2 = make_float2(f, f), u2 = make_float2(u, u);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t v[32];
+                    tm_ld32(o_t + 32 * i, v);
+                    tm_wait_ld(v);
+                    if (i + 1 == D / 32) {  // all of O has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_free);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float2 x = make_float2(o[16 * i + q].x * f2.x, o[16 * i + q].y * f2.y);
+                        o[16 * i + q] = ffma2(make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), u2, x);
+                    }
+                }
+            }
+            if (!ok) break;
+            float *out = p.stretches + (blockIdx.x + static_cast<int64_t>(st.item)) * stretch_floats(D) + row * D;
+#pragma unroll
+            for (int i = 0; i < D / 2; i += 4) {
+                const uint32_t w[8] = {__float_as_uint(o[i].x), __float_as_uint(o[i].y), __float_as_uint(o[i + 1].x), __float_as_uint(o[i + 1].y),
+                                       __float_as_uint(o[i + 2].x), __float_as_uint(o[i + 2].y), __float_as_uint(o[i + 3].x), __float_as_uint(o[i + 3].y)};
+                store32(out + 2 * i, w, true);
+            }
+        }
+        if (!ok) failed(kErrConsumerWait);
+    } else {
+        // ---------------- codes to operands
+        fewer_registers<kExpandRegs>();
+        const int w = warp - 12;
+        bool ok = true;
+        int n = 0, piece = 0;
+        // a piece's operands, once `free` is: 128-byte rows of 64 channels, 16-byte chunks swizzled by the row
+        auto expand = [&](int j, int tile, bool values) {
+            const int slot = piece % Sh::kSlots;
+            ok = wait(raw_full + 8 * slot, piece / Sh::kSlots);
+            if (ok && j > 0) ok = values ? wait(o_full, j - 1) : wait(k_done, j - 1);
+            if (!ok) return;
+            const uint8_t *const raw = smem + Sh::kOffRaw + slot * Sh::kRaw, *const scales = raw + Sh::kRawCodes;
+            uint8_t *const dst = smem + (values ? Sh::kOffV : Sh::kOffK);
+            const int rows = min(kTokens, units.len - tile * kTokens);
+            const uint32_t in_page = static_cast<uint32_t>(groups[j % 16]);
+            const int e = tile_exponent<D>(scales, rows, in_page);
+            if (w == 0 && lane == 0) (values ? v_exp : k_exp)[j & 3] = e;
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+                const int part = lane & 3, x = lane >> 2;
+                // rows of a warp: so that eight lanes that store together have eight different chunk places
+                const int row = 8 * (w + 8 * it) + (values ? x : (x & 1) * 4 + (x >> 1));
+                __half d[NB];
+                row_scales<D>(scales, row, row < rows && ((in_page >> (row >> 4)) & 1), e, d);
+                uint8_t *const to = dst + row * 128;
+                const int turn = row & 7;
+                if (!values) {
+                    uint32_t c[NB];
+                    const uint8_t *src = raw + row * G::kRow + part * (4 * NB);
+                    if (NB == 4) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                        c[0] = v.x, c[1] = v.y, c[NB - 2] = v.z, c[NB - 1] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                        c[0] = v.x, c[1] = v.y;
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        uint8_t *t = to + (b >> 1) * (128 * 128) + ((((b & 1) * 4 + part) ^ turn) << 4);
+                        expand_word(c[b], __half2half2(d[b]), t, t + Sh::kPart);
+                    }
+                } else {
+                    const int vr = kv_value_row(row & 15), at = part ^ (vr & 2);  // (units 2 part and 2 part + 1)
+                    uint32_t c[NB];  // [unit][block pair]
+                    const uint8_t *src = raw + ((row & ~15) + vr) * G::kRow + at * (4 * NB);
+                    if (NB == 4) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                        c[0] = v.x, c[1] = v.y, c[NB - 2] = v.z, c[NB - 1] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                        c[0] = v.x, c[1] = v.y;
+                    }
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const int unit = 2 * part + i / (NB / 2), pair = i % (NB / 2);
+                        uint8_t *t = to + pair * (128 * 128) + ((unit ^ turn) << 4);
+                        expand_word(c[i], __halves2half2(d[2 * pair], d[2 * pair + 1]), t, t + Sh::kPart);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(raw_empty + 8 * slot);
+                mbar_arrive(values ? v_ready : k_ready);
+            }
+            ++piece;
+        };
+        int before = 0;  // the unit before's tile
+        while (ok && st.next(units)) {
+            // ---- the stretch's queries, in the keys' order of channels, once the last one's products are complete
+            if (n > 0) ok = wait(k_done, n - 1);
+            if (!ok) break;
+            const int head = st.item / p.row_tiles, row0 = st.item % p.row_tiles * kRows;
+            constexpr int kLanes = D / 8, kStep = 8 * 32 / kLanes;  // lanes of a row, rows of the eight warps
+            const int chunk = lane % kLanes, b = chunk >> 2, t = chunk & 3;
+#pragma unroll 4
+            for (int r0 = 0; r0 < kRows; r0 += kStep) {
+                const int r = r0 + w * (32 / kLanes) + lane / kLanes, row = row0 + r, tok = row / a.group;
+                float x[8] = {};
+                if (tok < a.n_tok)
+                    load8(static_cast<const T *>(a.q) + tok * a.q_stride + (static_cast<int64_t>(head) * a.group + row - tok * a.group) * D + 32 * b + 4 * t, x);
+                float up = a.scale < 0.0f ? -1.0f : 1.0f, back = fabsf(a.scale) * 1.4426950408889634f;
+                if (TERMS == 2) {  // the largest magnitude to 2^10 .. 2^11
+                    float big = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[i]));
+#pragma unroll
+                    for (int m = 1; m < kLanes; m <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
+                    int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+                    if (e == 128) e = 0;         // infinities
+                    if (e < -117) e = -117;      // (2^(10 - e) is an f32)
+                    up *= __uint_as_float(static_cast<uint32_t>(137 - e) << 23);
+                    back *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * 0x1p-10f;
+                }
+                if (chunk == 0) factor[(st.index & 3) * kRows + r] = fmaxf(back, 1e-37f);  // never 0, which times -inf would be NaN
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // elements 0 2 | 1 3 | 16 18 | 17 19
+                    const int i0 = (i & 2) * 2 + (i & 1);
+                    const float y = x[i0] * up, z = x[i0 + 2] * up;
+                    h[i] = pack_half2(y, z);
+                    const float2 f = unpack_half2(h[i]);
+                    l[i] = pack_half2(y - f.x, z - f.y);
+                }
+                uint8_t *to = smem + Sh::kOffQ + (chunk >> 3) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (TERMS == 2) *reinterpret_cast<uint4 *>(to + Sh::kPart) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+            for (int j = 0; ok && j < st.n; ++j, ++n) {
+                expand(n, st.tile + j, false);
+                if (ok && n > 0) expand(n - 1, before, true);
+                before = st.tile + j;
+            }
+        }
+        if (ok && n > 0) expand(n - 1, before, true);
+        if (!ok) failed(kErrConsumerWait);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tc_dealloc(tmem, kTmemCols);
+}
+
+__device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__half *p, float a, float b) { *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b); }
+
 // Joins each row's results: of its stretches of the prefix, and of its own tokens. Block (s, i): query i of sequence
-// s; a warp a head.
+// s; D / 4 lanes a head, each four places of a stretch's row: two channels and the two 32 after them.
 template <int D, class T> __global__ void __launch_bounds__(256) shared_join_kernel(const SharedParams p, const int parts) {
-    constexpr int kPer = D / 32;
+    constexpr int kLanes = D / 4;
     pdl_allow_dependents();
     pdl_wait_prior_grids();
     const KvAttendParams &a = p.own;
-    const int lane = threadIdx.x & 31;
     int q0 = blockIdx.x, m = 1;
     if (a.q_offsets != nullptr) {
         q0 = __ldg(a.q_offsets + blockIdx.x);
@@ -124,34 +573,36 @@ template <int D, class T> __global__ void __launch_bounds__(256) shared_join_ker
         m = q0 < 0 || q1 < q0 || q1 > a.n_tok || q1 - q0 > a.max_q_len ? 0 : q1 - q0;
     }
     const Units units(p, parts);
+    const int l = threadIdx.x % kLanes, channel = 64 * (l / 16) + 2 * (l / 2 % 8) + 16 * (l & 1);
     for (int i = blockIdx.y; i < m; i += gridDim.y) {
         const int tok = q0 + i;
-        for (int h = threadIdx.x >> 5; h < a.n_heads; h += blockDim.x >> 5) {
+        for (int h = threadIdx.x / kLanes; h < a.n_heads; h += blockDim.x / kLanes) {
             const int kv = h / a.group, row = tok * a.group + h - kv * a.group;
             const int64_t item = static_cast<int64_t>(kv) * p.row_tiles + row / kRows;
             const int64_t rest = static_cast<int64_t>(tok) * a.n_heads + h;
-            float2 ml = reinterpret_cast<const float2 *>(a.rest_stats)[rest];
-            float top = ml.x, den = ml.y, acc[kPer];
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) acc[k] = __ldcg(a.rest + rest * D + channel_at<D>(lane * kPer + k));
+            float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.rest_stats) + rest);
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel));
+            const float2 y = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel + 32));
+            float top = ml.x, den = ml.y;
+            float4 acc = make_float4(x.x, y.x, x.y, y.y);
             if (units.tiles > 0) {
                 const int64_t c0 = item * units.tiles / units.share, c1 = ((item + 1) * units.tiles - 1) / units.share;
                 for (int64_t c = c0; c <= c1; ++c) {
                     const float *part = p.stretches + (c + item) * stretch_floats(D);
                     ml = __ldcg(reinterpret_cast<const float2 *>(part + kRows * D) + row % kRows);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + row % kRows * D) + l);
                     const float next = fmaxf(top, ml.x), ref = next == -INFINITY ? 0.0f : next;
                     const float keep = exp2_approx(top - ref), f = exp2_approx(ml.x - ref);
                     top = next;
-                    den = den * keep + ml.y * f;
-#pragma unroll
-                    for (int k = 0; k < kPer; ++k)
-                        acc[k] = acc[k] * keep + f * __ldcg(part + row % kRows * D + lane * kPer + k);
+                    den = fmaf(den, keep, ml.y * f);
+                    acc.x = fmaf(acc.x, keep, v.x * f), acc.y = fmaf(acc.y, keep, v.y * f);
+                    acc.z = fmaf(acc.z, keep, v.z * f), acc.w = fmaf(acc.w, keep, v.w * f);
                 }
             }
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                static_cast<T *>(a.out)[rest * D + channel_at<D>(lane * kPer + k)] = static_cast<T>(acc[k] * inv);
+            T *out = static_cast<T *>(a.out) + rest * D + channel;
+            store2(out, acc.x * inv, acc.z * inv);
+            store2(out + 32, acc.y * inv, acc.w * inv);
         }
     }
 }
@@ -160,8 +611,22 @@ int64_t row_tiles(int64_t n_tok, int group) { return (n_tok * group + kRows - 1)
 size_t align(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int D, class T> cudaError_t launch(SharedParams &p, int sms, int device, cudaStream_t s) {
+    using Sh = Shape<D, sizeof(T) == 4 ? 2 : 1>;
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (device & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(prefix_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        cudaFuncAttributes attr;
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, prefix_kernel<D, T>);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs != kLaunchRegs) {  // the roles would wait for registers that the block does not have
+            g_launch_step = "prefix_kernel's registers";
+            return cudaErrorInvalidValue;
+        }
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
     const int parts = sms < kMaxParts ? sms : kMaxParts;
-    cudaError_t e = launch_pdl(prefix_kernel<D, T>, parts, kRows, 0, s, p);
+    cudaError_t e = launch_pdl(prefix_kernel<D, T>, parts, kThreads, Sh::kSmem, s, p);
     if (e == cudaSuccess) e = launch_kv_attend(p.own, D, sizeof(T) == 4 ? QG_F32 : QG_F16, sms, device, s);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -173,7 +638,7 @@ template <int D, class T> cudaError_t launch(SharedParams &p, int sms, int devic
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, shared_join_kernel<D, T>, static_cast<const SharedParams>(p), static_cast<const int>(parts));
+    return cudaLaunchKernelEx(&cfg, shared_join_kernel<D, T>, static_cast<SharedParams>(p), parts);
 }
 
 }  // namespace
