@@ -11,6 +11,7 @@
 // joins a row's results in a fixed order.
 #include <atomic>
 #include <cfloat>
+#include <type_traits>
 
 #include "tc_attend.cuh"
 
@@ -28,8 +29,8 @@ constexpr int kThreads = (12 + kExpanders) * 32;
 constexpr int kLaunchRegs = 96, kIssueRegs = 40, kSoftmaxRegs = 136, kSumRegs = 168, kExpandRegs = 64;
 static_assert(128 * (kIssueRegs + kSoftmaxRegs + kSumRegs) + 32 * kExpanders * kExpandRegs <= kThreads * kLaunchRegs, "registers");
 
-// Tensor memory: S of even and odd tiles (the weights over its first half), O, the weights' low parts.
-constexpr uint32_t kTmemCols = 512, kTmemO = 256, kTmemLow = 384;
+// Tensor memory: S of even and odd tiles (the weights over its first half), O, the queries, the weights' low parts.
+constexpr uint32_t kTmemCols = 512, kTmemO = 256, kTmemQ = 384, kTmemLow = 448;
 constexpr float kHigh = 14.0f, kLow = 7.0f;  // log2 of the largest weight, and of the largest when the reference is set
 
 template <int D, int TERMS> struct Shape {
@@ -38,7 +39,8 @@ template <int D, int TERMS> struct Shape {
     static constexpr int kRawCodes = kTokens * D / 2;          // codes of a unit's keys (or values)
     static constexpr int kRaw = kRawCodes + kTokens * G::kScaleRow;
     static constexpr int kSlots = TERMS == 2 && D == 128 ? 3 : 6;
-    static constexpr int kOffQ = 0, kOffK = TERMS * kPart, kOffV = kOffK + 2 * kPart;  // parts: high, low
+    // the queries (high parts on their way to tensor memory), keys, values: parts of 128-byte rows of 64 channels
+    static constexpr int kOffQ = 0, kOffK = TERMS * kPart, kOffV = kOffK + 2 * kPart;
     static constexpr int kOffRaw = kOffV + 2 * kPart;
     static constexpr int kOffBars = kOffRaw + kSlots * kRaw;
     static constexpr int kOffKeep = kOffBars + 512;            // [tile % 4][row]: what the sums before a tile are multiplied by
@@ -96,6 +98,25 @@ __device__ __forceinline__ __half2 high_codes(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 
+template <int NB> __device__ __forceinline__ void ld_words(const uint8_t *p, uint32_t (&w)[NB]) {
+    if (NB == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[NB - 2] = v.z, w[NB - 1] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+// NB f16 as NB/2 words.
+template <int NB> __device__ __forceinline__ void ld_halves(const uint8_t *p, uint32_t (&w)[NB / 2]) {
+    if (NB == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[NB / 2 - 1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
 // Two codes' values in two f16 parts, which hold them exactly (four bits times eleven) above f16's end.
 __device__ __forceinline__ void two_parts(__half2 code, __half2 scale, uint32_t &high, uint32_t &low) {
     const __half2 h = __hmul2(code, scale);
@@ -114,32 +135,43 @@ __device__ __forceinline__ void expand_word(uint32_t w, __half2 scale, uint8_t *
     *reinterpret_cast<uint4 *>(low) = l;
 }
 
-// The power of two that takes a tile's largest scale to 2^8 .. 2^9 (f16 exponent fields; scales of rows that count,
-// every lane four rows), as its exponent. The tile's values are then below 2^13 and exact down to 2^-33 of that.
-template <int D> __device__ __forceinline__ int tile_exponent(const uint8_t *scales, int rows, uint32_t groups) {
-    const int row = 4 * (threadIdx.x & 31);
-    uint32_t m = 0;
-    if ((groups >> (row >> 4)) & 1)
+// Makes a unit's raw scales (keys' or values') ready: 0 for tokens that do not count (rows past `rows`, groups in no
+// page), infinities as NaN, and all times the power of two that takes the largest to 2^8 .. 2^9 (f16 exponent fields),
+// whose exponent is returned. The unit's values are then below 2^13 and exact down to 2^-33 of that. One warp: a lane
+// has two words of four tokens in two places, which its neighbours' follow.
+template <int D> __device__ __forceinline__ int prepare_scales(uint8_t *scales, int rows, uint32_t groups) {
+    constexpr int kChunks = kTokens * (D / 16) / 512, kPer = 256 / D;  // 16-byte chunks of a lane, tokens of one
+    const int lane = threadIdx.x & 31;
+    uint4 *const at = reinterpret_cast<uint4 *>(scales) + lane;
+    uint32_t x[kChunks][4], m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (row + i < rows)
+    for (int i = 0; i < kChunks; ++i) {
+        const uint4 v = at[32 * i];
+        x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
 #pragma unroll
-                for (int w = 0; w < D / 64; ++w)
-                    m = __vmaxu2(m, reinterpret_cast<const uint32_t *>(scales)[(row + i) * (D / 64) + w] & 0x7FFF7FFFu);
-    const uint32_t most = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) >> 10;
-    return 23 - static_cast<int>(most == 0 ? 1 : most);
-}
-// A row's scales times 2^e, infinities as NaN; 0 for a row that does not count.
-template <int D> __device__ __forceinline__ void row_scales(const uint8_t *scales, int row, bool counts, int e, __half (&d)[D / 32]) {
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-    for (int w = 0; w < D / 64; ++w) {
-        const uint32_t x = counts ? reinterpret_cast<const uint32_t *>(scales)[row * (D / 64) + w] : 0u;
-        float2 f = unpack_half2(x);
-        if ((x & 0x7C00u) == 0x7C00u) f.x = NAN;
-        if ((x & 0x7C000000u) == 0x7C000000u) f.y = NAN;
-        d[2 * w] = __float2half_rn(f.x * up), d[2 * w + 1] = __float2half_rn(f.y * up);
+        for (int w = 0; w < 4; ++w) {
+            const int row = (32 * i + lane) * kPer + w * kPer / 4;
+            if (row >= rows || !((groups >> (row >> 4)) & 1)) x[i][w] = 0;
+            m = __vmaxu2(m, x[i][w] & 0x7FFF7FFFu);
+        }
     }
+    const uint32_t most = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) >> 10;
+    const int e = 23 - static_cast<int>(most == 0 ? 1 : most);
+    // 2^e in two factors of f16's range
+    const __half2 up = __float2half2_rn(__uint_as_float(static_cast<uint32_t>(127 + min(e, 15)) << 23));
+    const __half2 more = __float2half2_rn(__uint_as_float(static_cast<uint32_t>(127 + max(e - 15, 0)) << 23));
+    const __half2 zero = __float2half2_rn(0.0f);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        uint32_t y[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const __half2 d = *reinterpret_cast<const __half2 *>(&x[i][w]);
+            y[w] = bits(__hfma2(d, zero, __hmul2(__hmul2(d, up), more)));
+        }
+        at[32 * i] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    return e;
 }
 
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {  // elements 0 .. 3 and 16 .. 19
@@ -163,13 +195,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
     const uint32_t base = smem_addr(smem), bars = base + Sh::kOffBars;
     const uint32_t raw_full = bars, raw_empty = raw_full + 8 * Sh::kSlots, k_ready = raw_empty + 8 * Sh::kSlots, k_done = k_ready + 8;
     const uint32_t v_ready = k_done + 8, s_full = v_ready + 8, p_ready = s_full + 16, o_full = p_ready + 16, o_free = o_full + 8;
-    const uint32_t mfinal = o_free + 8;  // up to 20 barriers: 160 bytes
+    const uint32_t mfinal = o_free + 8, q_staged = mfinal + 8, scaled = q_staged + 8;  // up to 29 barriers: 232 bytes
     uint8_t *const words = smem + Sh::kOffBars + 256;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(words);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(words + 4);
     volatile int *const groups = reinterpret_cast<volatile int *>(words + 16);     // [tile % 16]: its groups that lie in a page
-    volatile int *const k_exp = reinterpret_cast<volatile int *>(words + 80);      // [tile % 4]
-    volatile int *const v_exp = reinterpret_cast<volatile int *>(words + 96);
+    // [tile % 8]: the scales' exponents (the warp that finds them is three tiles ahead of those that expand at most, and
+    // these two ahead of the softmax)
+    volatile int *const k_exp = reinterpret_cast<volatile int *>(words + 80);
+    volatile int *const v_exp = reinterpret_cast<volatile int *>(words + 112);
     volatile float *const keep = reinterpret_cast<volatile float *>(smem + Sh::kOffKeep);
     volatile float *const factor = reinterpret_cast<volatile float *>(smem + Sh::kOffFactor);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -179,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_empty + 8 * i, kExpanders);
+            mbar_init(scaled + 8 * i, 1);
         }
         mbar_init(k_ready, kExpanders);
         mbar_init(k_done, 1);
@@ -190,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
         mbar_init(o_full, 1);
         mbar_init(o_free, 4);
         mbar_init(mfinal, 1);
+        mbar_init(q_staged, kExpanders);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -274,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             const uint32_t issue = lane == 0;
             constexpr uint32_t kIdS = tc_idesc_f16(128, kTokens), kIdO = tc_idesc_f16(128, D) | kIdescNMajorB;
             constexpr uint32_t kPart = Sh::kPart / 16;
-            const uint32_t q = desc_lo(base + Sh::kOffQ, 1), k = desc_lo(base + Sh::kOffK, 1), v = desc_lo(base + Sh::kOffV, 128 * 128 / 16);
+            const uint32_t q_low = desc_lo(base + Sh::kOffQ, 1) + kPart, k = desc_lo(base + Sh::kOffK, 1), v = desc_lo(base + Sh::kOffV, 128 * 128 / 16);
             auto tight = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, tc_wait(bar, parity & 1u, abort_flag))); };
             bool ok = true;
             int n = 0;  // units so far
@@ -282,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 ok = tight(p_ready + 8 * (j & 1), j >> 1) && tight(v_ready, j) && (j == 0 || tight(o_free, j - 1));
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t w = tmem + 128 * (j & 1), w_low = tmem + kTmemLow + 64 * (j & 1);
+                const uint32_t w = tmem + 128 * (j & 1), w_low = tmem + kTmemLow;
                 // small terms first: what the tensor cores cut off at each sum is then of the small ones
                 if (TERMS == 2) mma_pv(issue, tmem + kTmemO, w_low, v, kIdO, 0, kDescHi);
                 mma_pv(issue, tmem + kTmemO, w, v + kPart, kIdO, TERMS == 2, kDescHi);
@@ -295,9 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t s = tmem + 128 * (n & 1);
-                    if (TERMS == 2) mma_s<D>(issue, s, q + kPart, k, kIdS, kDescHi, 0);
-                    mma_s<D>(issue, s, q, k + kPart, kIdS, kDescHi, TERMS == 2);
-                    mma_s<D>(issue, s, q, k, kIdS, kDescHi, 1);
+                    if (TERMS == 2) mma_s<D>(issue, s, q_low, k, kIdS, kDescHi, 0);
+                    mma_s_tm<D>(issue, s, tmem + kTmemQ, k + kPart, kIdS, kDescHi, TERMS == 2);
+                    mma_s_tm<D>(issue, s, tmem + kTmemQ, k, kIdS, kDescHi, 1);
                     commit(issue, s_full + 8 * (n & 1));
                     commit(issue, k_done);
                     if (n > 0) product_o(n - 1);
@@ -308,6 +344,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             commit(issue, mfinal);  // every product complete before tensor memory is freed, after a wait that gave up, too
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(mfinal, 0)) && issue) record_error(a.err, kErrDrainWait);
             __syncwarp();
+        } else if (warp == 2) {
+            // ---------------- scales, in place
+            bool ok = true;
+            int n = 0, piece = 0, before = 0;
+            auto prepare = [&](int j, int tile, bool values) {
+                const int slot = piece % Sh::kSlots;
+                ok = wait(raw_full + 8 * slot, piece / Sh::kSlots);
+                if (!ok) return;
+                const int e = prepare_scales<D>(smem + Sh::kOffRaw + slot * Sh::kRaw + Sh::kRawCodes,
+                                                min(kTokens, units.len - tile * kTokens), static_cast<uint32_t>(groups[j % 16]));
+                fence_proxy_async_smem();  // (the next copy to this place comes after these writes)
+                __syncwarp();
+                if (lane == 0) {
+                    (values ? v_exp : k_exp)[j & 7] = e;
+                    mbar_arrive(scaled + 8 * slot);
+                }
+                ++piece;
+            };
+            while (ok && st.next(units)) {
+                for (int j = 0; ok && j < st.n; ++j, ++n) {
+                    prepare(n, st.tile + j, false);
+                    if (ok && n > 0) prepare(n - 1, before, true);
+                    before = st.tile + j;
+                }
+            }
+            if (ok && n > 0) prepare(n - 1, before, true);
+            if (!ok) failed(kErrConsumerWait);
         }
     } else if (warp < 8) {
         // ---------------- softmax: thread = row = tensor-memory lane
@@ -323,28 +386,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 ok = wait(s_full + 8 * (n & 1), n >> 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t s_t = tmem + lanes + 128 * (n & 1), low_t = tmem + lanes + kTmemLow + 64 * (n & 1);
+                const uint32_t s_t = tmem + lanes + 128 * (n & 1), low_t = tmem + lanes + kTmemLow;
                 const int rows = min(kTokens, units.len - (st.tile + j) * kTokens);
                 const uint32_t in_page = static_cast<uint32_t>(groups[n % 16]);
                 const bool full = rows == kTokens && in_page == 255u;
-                const float c = fminf(fmaxf(factor[(st.index & 3) * kRows + row] * __uint_as_float(static_cast<uint32_t>(127 - k_exp[n & 3]) << 23), 1e-37f), FLT_MAX);
+                const float c = fminf(fmaxf(factor[(st.index & 3) * kRows + row] * __uint_as_float(static_cast<uint32_t>(127 - k_exp[n & 7]) << 23), 1e-37f), FLT_MAX);
                 auto load = [&](int i, uint32_t (&v)[32]) {
                     tm_ld32(s_t + 32 * i, v);
                     tm_wait_ld(v);
-                    if (!full)
+                    if (!full) {
+                        uint32_t seen = (in_page >> (2 * i) & 1u ? 0x0000FFFFu : 0u) | (in_page >> (2 * i) & 2u ? 0xFFFF0000u : 0u);
+                        seen &= rows >= 32 * i + 32 ? 0xFFFFFFFFu : rows <= 32 * i ? 0u : (1u << (rows - 32 * i)) - 1;
 #pragma unroll
                         for (int q = 0; q < 32; ++q)
-                            if (32 * i + q >= rows || !((in_page >> (2 * i + (q >> 4))) & 1)) v[q] = 0xFF800000u;
+                            if (!(seen >> q & 1u)) v[q] = 0xFF800000u;
+                    }
                 };
+                // (rolled loops throughout: the roles of a scheduler run through as many pieces of code, and unrolled ones
+                // came from instruction memory each time)
                 float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     uint32_t v[32];
                     load(i, v);
-                    float m[2] = {__uint_as_float(v[0]), __uint_as_float(v[1])};
+                    float m[2] = {top, __uint_as_float(v[0])};
 #pragma unroll
-                    for (int q = 2; q < 32; q += 2) m[0] = fmaxf(m[0], __uint_as_float(v[q])), m[1] = fmaxf(m[1], __uint_as_float(v[q + 1]));
-                    top = fmaxf(top, fmaxf(m[0], m[1]));
+                    for (int q = 1; q < 31; q += 2) m[q / 2 & 1] = fmaxf(fmaxf(m[q / 2 & 1], __uint_as_float(v[q])), __uint_as_float(v[q + 1]));
+                    top = fmaxf(fmaxf(m[0], m[1]), __uint_as_float(v[31]));
                 }
                 top *= c;
                 float down = 1.0f;
@@ -357,8 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 keep[(n & 3) * kRows + row] = down;
                 const float r = ref == -INFINITY ? 0.0f : ref;  // (no token seen yet: weights of 0)
                 const float2 c2 = make_float2(c, c), r2 = make_float2(-r, -r);
-                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
+                if (TERMS == 2 && n > 0) ok = wait(o_full, n - 1);  // the low parts' place is one
+                if (!ok) break;
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     uint32_t v[32], w[16], w_low[16];
                     load(i, v);
@@ -366,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                     for (int q = 0; q < 16; ++q) {
                         float2 e = ffma2(make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), c2, r2);
                         e.x = exp2_approx(e.x), e.y = exp2_approx(e.y);
-                        part[q & 1] = fadd2(part[q & 1], e);
+                        sum = fadd2(sum, e);
                         w[q] = pack_half2(e.x, e.y);
                         if (TERMS == 2) {
                             const float2 h = unpack_half2(w[q]);
@@ -380,7 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready + 8 * (n & 1));
-                sum = fadd2(sum, fadd2(part[0], part[1]));
             }
             if (ok)
                 reinterpret_cast<float2 *>(p.stretches + (blockIdx.x + static_cast<int64_t>(st.item)) * stretch_floats(D) + kRows * D)[row] =
@@ -402,8 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 ok = wait(o_full, n);
                 if (!ok) break;
                 tc_fence_after();
-                const float f = keep[(n & 3) * kRows + row], u = __uint_as_float(static_cast<uint32_t>(127 - v_exp[n & 3]) << 23);
-                const float2 f2 = make_float2(f, f), u2 = make_float2(u, u);
+                const float f = keep[(n & 3) * kRows + row], u = __uint_as_float(static_cast<uint32_t>(127 - v_exp[n & 7]) << 23);
+                const float2 u2 = make_float2(u, u);
+                if (__any_sync(0xffffffffu, f != 1.0f))
+#pragma unroll
+                    for (int i = 0; i < D / 2; ++i) o[i].x *= f, o[i].y *= f;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t v[32];
@@ -415,10 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                         if (lane == 0) mbar_arrive(o_free);
                     }
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float2 x = make_float2(o[16 * i + q].x * f2.x, o[16 * i + q].y * f2.y);
-                        o[16 * i + q] = ffma2(make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), u2, x);
-                    }
+                    for (int q = 0; q < 16; ++q)
+                        o[16 * i + q] = ffma2(make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), u2, o[16 * i + q]);
                 }
             }
             if (!ok) break;
@@ -438,58 +507,35 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
         bool ok = true;
         int n = 0, piece = 0;
         // a piece's operands, once `free` is: 128-byte rows of 64 channels, 16-byte chunks swizzled by the row
-        auto expand = [&](int j, int tile, bool values) {
+        auto expand = [&](int j, auto of) {
+            constexpr bool values = decltype(of)::value;
             const int slot = piece % Sh::kSlots;
-            ok = wait(raw_full + 8 * slot, piece / Sh::kSlots);
+            ok = wait(scaled + 8 * slot, piece / Sh::kSlots) && wait(raw_full + 8 * slot, piece / Sh::kSlots);
             if (ok && j > 0) ok = values ? wait(o_full, j - 1) : wait(k_done, j - 1);
             if (!ok) return;
-            const uint8_t *const raw = smem + Sh::kOffRaw + slot * Sh::kRaw, *const scales = raw + Sh::kRawCodes;
-            uint8_t *const dst = smem + (values ? Sh::kOffV : Sh::kOffK);
-            const int rows = min(kTokens, units.len - tile * kTokens);
-            const uint32_t in_page = static_cast<uint32_t>(groups[j % 16]);
-            const int e = tile_exponent<D>(scales, rows, in_page);
-            if (w == 0 && lane == 0) (values ? v_exp : k_exp)[j & 3] = e;
-#pragma unroll
+            const uint8_t *const raw = smem + Sh::kOffRaw + slot * Sh::kRaw;
+            // Rows of a warp: so that eight lanes that store together have eight different chunk places, and the same for
+            // both of its turns, 64 rows on (8 groups' rows 4 by 4 KB: one address and constants).
+            const int part = lane & 3, x = lane >> 2, row = 8 * w + (values ? x : (x & 1) * 4 + (x >> 1)), vr = kv_value_row(row & 15);
+            const uint8_t *codes = raw + (values ? ((row & ~15) + vr) * G::kRow + (part ^ (vr & 2)) * (4 * NB) : row * G::kRow + part * (4 * NB));
+            const uint8_t *scales = raw + Sh::kRawCodes + row * G::kScaleRow;
+            uint8_t *const to = smem + (values ? Sh::kOffV : Sh::kOffK) + row * 128;
+            // keys: block b's words go to chunk 4 (b % 2) + part of half b / 2; values: units 2 part and 2 part + 1 of block pair h to half h
+            uint8_t *const first = to + (((values ? 2 * part : part) ^ (row & 7)) << 4);
+            uint8_t *const second = to + (((values ? 2 * part + 1 : part + 4) ^ (row & 7)) << 4);
+#pragma unroll 1
             for (int it = 0; it < 2; ++it) {
-                const int part = lane & 3, x = lane >> 2;
-                // rows of a warp: so that eight lanes that store together have eight different chunk places
-                const int row = 8 * (w + 8 * it) + (values ? x : (x & 1) * 4 + (x >> 1));
-                __half d[NB];
-                row_scales<D>(scales, row, row < rows && ((in_page >> (row >> 4)) & 1), e, d);
-                uint8_t *const to = dst + row * 128;
-                const int turn = row & 7;
-                if (!values) {
-                    uint32_t c[NB];
-                    const uint8_t *src = raw + row * G::kRow + part * (4 * NB);
-                    if (NB == 4) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                        c[0] = v.x, c[1] = v.y, c[NB - 2] = v.z, c[NB - 1] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(src);
-                        c[0] = v.x, c[1] = v.y;
-                    }
+                uint32_t c[NB], d[NB / 2];
+                ld_words<NB>(codes + it * (64 * G::kRow), c);
+                ld_halves<NB>(scales + it * (64 * G::kScaleRow), d);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        uint8_t *t = to + (b >> 1) * (128 * 128) + ((((b & 1) * 4 + part) ^ turn) << 4);
-                        expand_word(c[b], __half2half2(d[b]), t, t + Sh::kPart);
-                    }
-                } else {
-                    const int vr = kv_value_row(row & 15), at = part ^ (vr & 2);  // (units 2 part and 2 part + 1)
-                    uint32_t c[NB];  // [unit][block pair]
-                    const uint8_t *src = raw + ((row & ~15) + vr) * G::kRow + at * (4 * NB);
-                    if (NB == 4) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                        c[0] = v.x, c[1] = v.y, c[NB - 2] = v.z, c[NB - 1] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(src);
-                        c[0] = v.x, c[1] = v.y;
-                    }
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        const int unit = 2 * part + i / (NB / 2), pair = i % (NB / 2);
-                        uint8_t *t = to + pair * (128 * 128) + ((unit ^ turn) << 4);
-                        expand_word(c[i], __halves2half2(d[2 * pair], d[2 * pair + 1]), t, t + Sh::kPart);
-                    }
+                for (int i = 0; i < NB; ++i) {
+                    // word i: keys' block i; values' unit i / (NB / 2), block pair i % (NB / 2)
+                    const bool odd = values ? i / (NB / 2) == 1 : (i & 1) == 1;
+                    const int half = values ? i % (NB / 2) : i >> 1;
+                    const uint32_t s2 = values ? d[half] : __byte_perm(d[i >> 1], 0, i & 1 ? 0x3232 : 0x1010);
+                    uint8_t *t = (odd ? second : first) + half * (128 * 128) + it * (64 * 128);
+                    expand_word(c[i], *reinterpret_cast<const __half2 *>(&s2), t, t + Sh::kPart);
                 }
             }
             fence_proxy_async_smem();
@@ -500,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             }
             ++piece;
         };
-        int before = 0;  // the unit before's tile
         while (ok && st.next(units)) {
             // ---- the stretch's queries, in the keys' order of channels, once the last one's products are complete
             if (n > 0) ok = wait(k_done, n - 1);
@@ -508,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             const int head = st.item / p.row_tiles, row0 = st.item % p.row_tiles * kRows;
             constexpr int kLanes = D / 8, kStep = 8 * 32 / kLanes;  // lanes of a row, rows of the eight warps
             const int chunk = lane % kLanes, b = chunk >> 2, t = chunk & 3;
-#pragma unroll 4
+#pragma unroll 2
             for (int r0 = 0; r0 < kRows; r0 += kStep) {
                 const int r = r0 + w * (32 / kLanes) + lane / kLanes, row = row0 + r, tok = row / a.group;
                 float x[8] = {};
@@ -541,13 +586,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
                 if (TERMS == 2) *reinterpret_cast<uint4 *>(to + Sh::kPart) = make_uint4(l[0], l[1], l[2], l[3]);
             }
+            {  // to tensor memory: a row's 64 channels a thread
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_staged);
+                ok = wait(q_staged, st.index);
+                if (!ok) break;
+                const int r = 32 * (w & 3) + lane, h = w >> 2;
+                if (h < D / 64) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(smem + Sh::kOffQ + h * (128 * 128) + r * 128 + ((i ^ (r & 7)) << 4));
+                        v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                    }
+                    tc_st32(tmem + (static_cast<uint32_t>(32 * (w & 3)) << 16) + kTmemQ + 32 * h, v);
+                    tc_wait_st();
+                    tc_fence_before();
+                }
+            }
             for (int j = 0; ok && j < st.n; ++j, ++n) {
-                expand(n, st.tile + j, false);
-                if (ok && n > 0) expand(n - 1, before, true);
-                before = st.tile + j;
+                expand(n, std::false_type());
+                if (ok && n > 0) expand(n - 1, std::true_type());
             }
         }
-        if (ok && n > 0) expand(n - 1, before, true);
+        if (ok && n > 0) expand(n - 1, std::true_type());
         if (!ok) failed(kErrConsumerWait);
     }
     tc_fence_before();
@@ -559,10 +621,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
 __device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
 __device__ __forceinline__ void store2(__half *p, float a, float b) { *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(a, b); }
 
-// Joins each row's results: of its stretches of the prefix, and of its own tokens. Block (s, i): query i of sequence
-// s; D / 4 lanes a head, each four places of a stretch's row: two channels and the two 32 after them.
-template <int D, class T> __global__ void __launch_bounds__(256) shared_join_kernel(const SharedParams p, const int parts) {
-    constexpr int kLanes = D / 4;
+// Joins each row's results: of its stretches of the prefix, and of its own tokens. Block (s, i, h): query i of sequence
+// s, eight heads (of 64: sixteen); D / 4 lanes a head, each four places of a stretch's row: two channels and the two 32 after them.
+constexpr int kJoinThreads = 256;
+
+template <int D, class T> __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p, const int parts) {
+    constexpr int kLanes = D / 4, kAhead = 4;
     pdl_allow_dependents();
     pdl_wait_prior_grids();
     const KvAttendParams &a = p.own;
@@ -572,38 +636,49 @@ template <int D, class T> __global__ void __launch_bounds__(256) shared_join_ker
         const int q1 = __ldg(a.q_offsets + blockIdx.x + 1);
         m = q0 < 0 || q1 < q0 || q1 > a.n_tok || q1 - q0 > a.max_q_len ? 0 : q1 - q0;
     }
+    const int h = blockIdx.z * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
+    if (h >= a.n_heads) return;
     const Units units(p, parts);
     const int l = threadIdx.x % kLanes, channel = 64 * (l / 16) + 2 * (l / 2 % 8) + 16 * (l & 1);
+    const int kv = h / a.group;
     for (int i = blockIdx.y; i < m; i += gridDim.y) {
-        const int tok = q0 + i;
-        for (int h = threadIdx.x / kLanes; h < a.n_heads; h += blockDim.x / kLanes) {
-            const int kv = h / a.group, row = tok * a.group + h - kv * a.group;
-            const int64_t item = static_cast<int64_t>(kv) * p.row_tiles + row / kRows;
-            const int64_t rest = static_cast<int64_t>(tok) * a.n_heads + h;
-            float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.rest_stats) + rest);
-            const float2 x = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel));
-            const float2 y = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel + 32));
-            float top = ml.x, den = ml.y;
-            float4 acc = make_float4(x.x, y.x, x.y, y.y);
-            if (units.tiles > 0) {
-                const int64_t c0 = item * units.tiles / units.share, c1 = ((item + 1) * units.tiles - 1) / units.share;
-                for (int64_t c = c0; c <= c1; ++c) {
-                    const float *part = p.stretches + (c + item) * stretch_floats(D);
-                    ml = __ldcg(reinterpret_cast<const float2 *>(part + kRows * D) + row % kRows);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + row % kRows * D) + l);
-                    const float next = fmaxf(top, ml.x), ref = next == -INFINITY ? 0.0f : next;
-                    const float keep = exp2_approx(top - ref), f = exp2_approx(ml.x - ref);
+        const int tok = q0 + i, row = tok * a.group + h - kv * a.group;
+        const int64_t rest = static_cast<int64_t>(tok) * a.n_heads + h;
+        float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.rest_stats) + rest);
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel));
+        const float2 y = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel + 32));
+        float top = ml.x, den = ml.y;
+        float4 acc = make_float4(x.x, y.x, x.y, y.y);
+        if (units.tiles > 0) {
+            const int item = kv * p.row_tiles + row / kRows;
+            const int64_t u = static_cast<int64_t>(item) * units.tiles;
+            const int c0 = static_cast<int>(u / units.share), n = static_cast<int>((u + units.tiles - 1) / units.share) - c0 + 1;
+            const float *const first = p.stretches + (c0 + static_cast<int64_t>(item)) * stretch_floats(D);
+            for (int c = 0; c < n; c += kAhead) {
+                float2 s[kAhead];
+                float4 v[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float *part = first + min(c + k, n - 1) * stretch_floats(D);
+                    s[k] = __ldcg(reinterpret_cast<const float2 *>(part + kRows * D) + row % kRows);
+                    v[k] = __ldcg(reinterpret_cast<const float4 *>(part + row % kRows * D) + l);
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (c + k >= n) break;
+                    const float next = fmaxf(top, s[k].x), ref = next == -INFINITY ? 0.0f : next;
+                    const float keep = exp2_approx(top - ref), f = exp2_approx(s[k].x - ref);
                     top = next;
-                    den = fmaf(den, keep, ml.y * f);
-                    acc.x = fmaf(acc.x, keep, v.x * f), acc.y = fmaf(acc.y, keep, v.y * f);
-                    acc.z = fmaf(acc.z, keep, v.z * f), acc.w = fmaf(acc.w, keep, v.w * f);
+                    den = fmaf(den, keep, s[k].y * f);
+                    acc.x = fmaf(acc.x, keep, v[k].x * f), acc.y = fmaf(acc.y, keep, v[k].y * f);
+                    acc.z = fmaf(acc.z, keep, v[k].z * f), acc.w = fmaf(acc.w, keep, v[k].w * f);
                 }
             }
-            const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
-            T *out = static_cast<T *>(a.out) + rest * D + channel;
-            store2(out, acc.x * inv, acc.z * inv);
-            store2(out + 32, acc.y * inv, acc.w * inv);
         }
+        const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no token seen: zeros
+        T *out = static_cast<T *>(a.out) + rest * D + channel;
+        store2(out, acc.x * inv, acc.z * inv);
+        store2(out + 32, acc.y * inv, acc.w * inv);
     }
 }
 
@@ -630,8 +705,10 @@ template <int D, class T> cudaError_t launch(SharedParams &p, int sms, int devic
     if (e == cudaSuccess) e = launch_kv_attend(p.own, D, sizeof(T) == 4 ? QG_F32 : QG_F16, sms, device, s);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.own.n_seq), static_cast<unsigned>(p.own.max_q_len < 64 ? p.own.max_q_len : 64));
-    cfg.blockDim = dim3(256);
+    const int per = kJoinThreads / (D / 4);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.own.n_seq), static_cast<unsigned>(p.own.max_q_len < 64 ? p.own.max_q_len : 64),
+                       static_cast<unsigned>((p.own.n_heads + per - 1) / per));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

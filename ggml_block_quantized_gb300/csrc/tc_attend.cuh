@@ -64,6 +64,28 @@ template <int D> __device__ __forceinline__ void mma_s(uint32_t issue, uint32_t 
             "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(issue), "r"(hi), "r"(acc)
             : "memory");
 }
+// The same with Q in tensor memory, 8 columns a product.
+template <int D> __device__ __forceinline__ void mma_s_tm(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t hi, uint32_t acc) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "setp.ne.u32 p, 1, 0;\n\t"
+            "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 2;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 4;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 6;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "}" ::"r"(d), "r"(a + 32 * h), "r"(b + 1024 * h), "r"(idesc), "r"(h == 0 ? acc : 1u), "r"(issue), "r"(hi)
+            : "memory");
+}
 // O (+)= P V: 16 keys a product, 8 columns of P and 2 KB of V.
 __device__ __forceinline__ void mma_pv(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t hi) {
     asm volatile(
@@ -142,6 +164,14 @@ __device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "r"(taddr)
         : "memory");
 }
+// 32 lanes x 16 columns from this warp's 16 registers each.
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 // Waits for this thread's tensor-memory loads; the registers pass through it,
 // so that nothing reads them earlier.
 __device__ __forceinline__ void tm_wait_ld(uint32_t (&v)[32]) {
@@ -161,15 +191,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// 16 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
 // 32 bytes in one store, or in two where `out` (and with it every row, a multiple
 // of 32 bytes) lies only on the 16-byte boundary that the interface asks for: a
 // 32-byte store there would fault.
@@ -186,6 +207,5 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool wi
 }
 template <int R> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-
 
 }  // namespace qg
