@@ -86,10 +86,10 @@ int qnorm_residual(const qnorm_args *args, qg_stream_t stream);
  * and prob 0. With logits of +inf only they have weight, 1 each. A top_p or
  * min_p that is NaN keeps all, a uniform outside [0, 1) or NaN counts as the
  * nearer end (NaN: 0).
- * Weights are computed to 2^-36 of themselves and held in units of 2^-44 of the
- * largest (a token below 2^-45 of it is not chosen), their sums in 64-bit
+ * Weights are computed to 2^-35 of themselves and held in units of about 2^-44
+ * of the largest (a token below half of that is not chosen), their sums in 64-bit
  * integers: results depend on no order of summing, and agree with 64-bit
- * arithmetic unless a border lies within about 2^-36 of a sum.
+ * arithmetic unless a border lies within about 2^-35 of a sum.
  * temperature, top_k, top_p, min_p and uniform are [n]; all but uniform may be
  * NULL (1, all, all, all). token int32 [n]; prob f32 [n] or NULL. 1 <= vocab <=
  * 524288, 0 <= n <= 2^24. */
