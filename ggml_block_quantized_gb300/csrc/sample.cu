@@ -7,21 +7,20 @@
 //  * the largest logit m;
 //  * with top_k, the threads' own largest logits, a histogram of which gives a cut
 //    that k tokens reach, and few others; with min_p alone its weight is the cut.
-//    The tokens above it are sent to the row's first block, which sorts them (logit
-//    falling, index rising), takes the prefix that the filters keep, sorts that by
-//    index and finds the token there.
+//    The tokens above it are sent to the row's first block, which goes on alone.
 //  * With a large top_k, or top_p alone, a histogram of m - l (with top_p: and of
 //    what the tokens of a bin weigh less than its first would, in 16 bits) gives
 //    the bins in which the border lies, one or two. Their tokens go to the first
-//    block, which sorts them and, with the sum of the weights before them, finds
-//    the last token kept.
+//    block, which finds the last one kept by the sum of the weights before them.
 //  * Then, as without filters, the token at which the sum of the kept weights, in
 //    index order, passes its target: sums per warp, then the block goes through the
 //    one warp's part again.
-// Where those bins hold too many tokens (equal ones, as a rule), or top_p follows a
-// large top_k, bins are divided again, by the bits of the logit, until at most
-// kList tokens are in one, or until all in it are equal and their border is found
-// by counting in index order.
+// The first block compares up to kList tokens with each other, all pairs at once.
+// More of them, and rows whose border's bins hold too many (equal logits, as a
+// rule) or whose top_p follows a large top_k, are searched: for each filter a
+// histogram's bin in which the count or the weights' sum passes its target, that
+// bin divided again by the bits of the logit until kList tokens are left, or until
+// all in it are equal and their border is found by index.
 //
 // Weights are 64-bit integers in units of 2^-44 of the largest. So sums, the
 // histogram's atomic ones among them, depend on no order, every pass agrees with
@@ -47,8 +46,8 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kCap = 1024;       // tokens that one block sorts
-constexpr int kList = 128;       // tokens whose order is counted directly
+constexpr int kCap = 1024;       // tokens that go to one block
+constexpr int kList = 128;       // tokens that are compared with each other
 constexpr int kMaxCluster = 16;
 constexpr int kUnit = 44;        // weights are in units of 2^-44
 constexpr uint64_t kOne = 1ull << kUnit;
@@ -58,20 +57,18 @@ constexpr float kLog2E = 1.44269502162933349609375f, kLog2ERest = 1.925963033500
 
 struct Shared {
     float2 power[64];                 // 2^(i / 64) in two floats
-    union {
-        struct {
-            uint64_t sum[kBins];      // weights of a bin
-            uint32_t count[kBins];
-        };
-        uint64_t weight[kCap];        // of the listed tokens
-    };
-    uint64_t all[kCap];               // (key, ~index) of listed tokens, in the first block
-    uint64_t list[kList];             // of a bin's tokens, this block's
+    uint64_t sum[kBins];              // of a histogram: weights, and tokens
+    uint32_t count[kBins];
+    uint64_t all[kCap];               // tokens sent to the first block: (key, ~index)
+    uint64_t list[kList], near[kList], weight[kList];  // of a bin's tokens: this block's, the cluster's, their weights
+    uint64_t ahead[kList];            // weights before a token, and how many tokens
+    uint32_t rank[kList];
     uint64_t warp_sum[kWarps];
-    uint64_t block_sum[2][kMaxCluster];
+    uint64_t block_sum[2][kMaxCluster][2];
     float2 extremes[kWarps];
     float2 block_extremes[kMaxCluster];
     uint32_t list_count, kept;
+    uint64_t total;
     struct { uint64_t before, value; uint32_t place, count; } found;
 };
 
@@ -197,286 +194,6 @@ __device__ __forceinline__ uint64_t warp_prefix(uint64_t v) {  // inclusive
     return v;
 }
 
-// A row in the cluster's shared memory.
-template <class T> struct Row {
-    Shared *s;
-    const T *data;             // this block's slice
-    int first, count, part;    // its first index and size; a warp's part of it (a multiple of 64)
-    int rank, blocks;
-    int turn = 0;              // which of the two sums' places is next
-
-    __device__ __forceinline__ float logit(int i) const { return static_cast<float>(data[i]); }
-    template <class F> __device__ __forceinline__ void each(F f) const {  // f(logit, index)
-        const int lane = threadIdx.x & 31, from = (threadIdx.x >> 5) * part;
-        const int to = min(from + part, count);
-        for (int i = from + lane; i < to; i += 32) f(logit(i), first + i);
-    }
-    __device__ __forceinline__ void join() const {  // the whole cluster
-        if (blocks == 1) __syncthreads();
-        else cg::this_cluster().sync();
-    }
-    template <class P> __device__ __forceinline__ P *at(P *p, int block) const {
-        return blocks == 1 ? p : cg::this_cluster().map_shared_rank(p, block);
-    }
-    // Sums over the blocks before this one, over this one, and over all.
-    struct Sums { uint64_t before, mine, all; };
-    __device__ __forceinline__ Sums sums(uint64_t v) {
-        v = warp_total(v);
-        if ((threadIdx.x & 31) == 0) s->warp_sum[threadIdx.x >> 5] = v;
-        __syncthreads();
-        uint64_t block = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) block += s->warp_sum[w];
-        uint64_t *const place = s->block_sum[turn];
-        turn ^= 1;
-        if (threadIdx.x < blocks) at(place, threadIdx.x)[rank] = block;
-        join();
-        Sums r{0, block, 0};
-        for (int b = 0; b < blocks; ++b) {
-            if (b < rank) r.before += place[b];
-            r.all += place[b];
-        }
-        return r;
-    }
-    // The token, in index order, at which the sum of value(logit, index) reaches target(sum of all); found.place is its
-    // index, found.value its value. Returns the sum of all.
-    template <class V, class G> __device__ __forceinline__ uint64_t select(V value, G target) {
-        uint64_t mine = 0;
-        each([&](float l, int i) { mine += value(l, i); });
-        const Sums r = sums(mine);
-        const uint64_t t = target(r.all);
-        if (r.before < t && t <= r.before + r.mine) {  // in this block: it goes through the one warp's part again
-            uint64_t before = r.before;
-            int w = 0;
-            while (t > before + s->warp_sum[w]) before += s->warp_sum[w++];
-            __syncthreads();
-            const int from = w * part, to = min(from + part, count), per = (part + kThreads - 1) / kThreads;
-            const int i0 = from + per * threadIdx.x, i1 = min(i0 + per, to);
-            uint64_t sum = 0;
-            for (int i = i0; i < i1; ++i) sum += value(logit(i), first + i);
-            const uint64_t up_to = warp_prefix(sum);
-            if ((threadIdx.x & 31) == 31) s->warp_sum[threadIdx.x >> 5] = up_to;
-            __syncthreads();
-            before += up_to - sum;
-            for (int v = 0; v < (threadIdx.x >> 5); ++v) before += s->warp_sum[v];
-            if (before < t && t <= before + sum)
-                for (int i = i0; i < i1; ++i) {
-                    const uint64_t v = value(logit(i), first + i);
-                    before += v;
-                    if (before >= t) {
-                        for (int b = 0; b < blocks; ++b) {
-                            auto *f = at(&s->found, b);
-                            f->place = first + i, f->value = v;
-                        }
-                        break;
-                    }
-                }
-        }
-        join();
-        return r.all;
-    }
-    // Bins of a histogram, in order of place(bin), each thread two neighbours: where the running sum of v reaches
-    // `target`. found: the bin, the sum before it, and its n. Every thread of every block calls it.
-    __device__ __forceinline__ void find_bin(const uint64_t (&v)[2], const uint32_t (&n)[2], bool rising, uint64_t target) {
-        const uint64_t both = v[0] + v[1], up_to = warp_prefix(both);
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (lane == 31) s->warp_sum[warp] = up_to;
-        __syncthreads();
-        uint64_t before = up_to - both;
-        for (int w = 0; w < warp; ++w) before += s->warp_sum[w];
-        if (rising) {  // counted from the last bin
-            uint64_t whole = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) whole += s->warp_sum[w];
-            before = whole - before - both;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int b = rising ? 1 - i : i;
-            if (before < target && target <= before + v[b]) s->found.place = 2 * threadIdx.x + b, s->found.before = before, s->found.count = n[b];
-            before += v[b];
-        }
-    }
-    __device__ __forceinline__ uint64_t block_total(uint64_t v) {  // over this block's threads
-        v = warp_total(v);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) s->warp_sum[threadIdx.x >> 5] = v;
-        __syncthreads();
-        uint64_t all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) all += s->warp_sum[w];
-        __syncthreads();
-        return all;
-    }
-    __device__ __forceinline__ void clear_bins(bool weights) {
-        for (int b = threadIdx.x; b < kBins; b += kThreads) {
-            s->count[b] = 0;
-            if (weights) s->sum[b] = 0;
-        }
-    }
-    __device__ __forceinline__ void bin_counts(uint32_t (&n)[2]) const {
-        n[0] = n[1] = 0;
-        for (int b = 0; b < blocks; ++b) {
-            const uint2 c = *reinterpret_cast<const uint2 *>(at(s->count, b) + 2 * threadIdx.x);
-            n[0] += c.x, n[1] += c.y;
-        }
-    }
-    // Tokens for which take(logit) holds are sent to the first block, as far as there is room.
-    template <class F> __device__ __forceinline__ void send(F take) {
-        const int lane = threadIdx.x & 31, from = (threadIdx.x >> 5) * part, to = min(from + part, count);
-        uint64_t *const there = at(s->all, 0);
-        uint32_t *const counter = at(&s->list_count, 0);
-        for (int i0 = from; i0 < to; i0 += 32) {
-            const int i = i0 + lane;
-            const float l = i < to ? logit(i) : -INFINITY;
-            const bool in = i < to && take(l);
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
-            if (who == 0) continue;
-            uint32_t place = 0;
-            if (lane == 0) place = atomicAdd(counter, static_cast<uint32_t>(__popc(who)));
-            place = __shfl_sync(0xffffffffu, place, 0) + __popc(who & ((1u << lane) - 1));
-            if (in && place < kCap) there[place] = static_cast<uint64_t>(key_of(l)) << 32 | ~static_cast<uint32_t>(first + i);
-        }
-    }
-    // The border at which the running value (1, or the weight) over the tokens up to `limit`, in falling order,
-    // reaches `target` (at least 1, at most the sum of all): value(l) is a token's.
-    template <bool WEIGHTS, class W>
-    __device__ __forceinline__ Border border(Border limit, uint64_t target, float m, float scale, float reach, W weigh) {
-        uint32_t lo = 0, hi = 0, bin0 = 0;
-        int shift = -1;  // -1: the first histogram, of m - l
-        auto first_bin = [&](float l) { return bin_of(l, m, scale); };
-        auto member = [&](float l, int i, uint32_t &bin) {
-            const uint32_t key = key_of(l);
-            if (key < limit.key || (key == limit.key && static_cast<uint32_t>(i) > limit.index)) return false;
-            bin = first_bin(l);
-            if (shift < 0) return true;
-            if (bin != bin0 || key < lo || key > hi) return false;
-            bin = (key - lo) >> shift;
-            return true;
-        };
-        for (;;) {
-            clear_bins(WEIGHTS);
-            if (threadIdx.x == 0) s->list_count = 0;
-            __syncthreads();
-            each([&](float l, int i) {
-                uint32_t bin;
-                if (WEIGHTS && !(l > reach)) return;
-                if (!member(l, i, bin)) return;
-                atomicAdd(&s->count[bin], 1u);
-                if (WEIGHTS) atomicAdd(reinterpret_cast<unsigned long long *>(&s->sum[bin]), static_cast<unsigned long long>(weigh(l)));
-            });
-            join();
-            uint64_t v[2] = {0, 0};
-            uint32_t n[2];
-            bin_counts(n);
-            for (int b = 0; b < blocks && WEIGHTS; ++b) v[0] += at(s->sum, b)[2 * threadIdx.x], v[1] += at(s->sum, b)[2 * threadIdx.x + 1];
-            if (!WEIGHTS) v[0] = n[0], v[1] = n[1];
-            // bins of the first histogram fall with the logit, those of the others rise
-            find_bin(v, n, shift >= 0, target);
-            join();  // (the histograms have been read, too)
-            const uint32_t bin = s->found.place, in_bin = s->found.count;
-            target -= s->found.before;
-            if (shift < 0) {
-                bin0 = bin;
-                lo = bin == kBins - 1 ? 0u : key_of(m - (bin + 2) / scale);
-                hi = key_of(m - (bin == 0 ? 0.0f : (bin - 1) / scale));
-            } else {
-                lo += bin << shift;
-                const uint32_t top = lo + ((1u << shift) - 1u);
-                hi = top < lo || top > hi ? hi : top;
-            }
-            const uint32_t width = hi - lo;
-            shift = width < kBins ? 0 : 22 - __clz(width);
-            if (in_bin <= kList) break;
-            if (lo == hi) {  // so many equal ones: the border is found by index
-                const float l = logit_of(lo);
-                const uint64_t each_one = WEIGHTS ? weigh(l) : 1;
-                const uint64_t nth = (target + each_one - 1) / each_one;
-                __syncthreads();
-                select([&](float x, int i) -> uint64_t { return key_of(x) == lo && (lo != limit.key || static_cast<uint32_t>(i) <= limit.index); },
-                       [&](uint64_t) { return nth; });
-                return Border{lo, s->found.place};
-            }
-            __syncthreads();
-        }
-        // the few tokens left, compared with each other by every block
-        each([&](float l, int i) {
-            uint32_t bin;
-            if (WEIGHTS && !(l > reach)) return;
-            if (!member(l, i, bin)) return;
-            s->list[atomicAdd(&s->list_count, 1u)] = static_cast<uint64_t>(key_of(l)) << 32 | ~static_cast<uint32_t>(i);
-        });
-        join();
-        int n = 0;
-        for (int b = 0; b < blocks; ++b) {
-            const int m = static_cast<int>(*at(&s->list_count, b));
-            for (int i = threadIdx.x; i < m; i += kThreads) {
-                const uint64_t e = at(s->list, b)[i];
-                s->all[n + i] = e;
-                s->weight[n + i] = WEIGHTS ? weigh(logit_of(static_cast<uint32_t>(e >> 32))) : 1;
-            }
-            n += m;
-        }
-        __syncthreads();
-        if (threadIdx.x < n) {
-            const uint64_t e = s->all[threadIdx.x], v = s->weight[threadIdx.x];
-            uint64_t before = 0;
-            for (int i = 0; i < n; ++i) before += s->all[i] > e ? s->weight[i] : 0;
-            if (before < target && target <= before + v) s->found.value = e;
-        }
-        join();
-        const uint64_t e = s->found.value;
-        __syncthreads();  // (what is found next is written to the same place)
-        return Border{static_cast<uint32_t>(e >> 32), ~static_cast<uint32_t>(e)};
-    }
-};
-
-// A block's 2 kThreads places: thread (w, lane) has 64 w + lane and the one 32 on.
-__device__ __forceinline__ int place_of(int i) { return 64 * (threadIdx.x >> 5) + (threadIdx.x & 31) + 32 * i; }
-
-// Sorts the first n places (a power of two, 64 at least; the others hold 0) so that they fall; `space` holds 2 kThreads.
-// Neighbours up to 32 apart meet by shuffles, the others in memory.
-__device__ __forceinline__ void sort_falling(uint64_t (&v)[2], int n, uint64_t *space) {
-    for (int size = 2; size <= n; size *= 2)
-        for (int stride = size / 2; stride > 0; stride /= 2) {
-            uint64_t o[2] = {v[1], v[0]};
-            if (stride < 64 && 64 * static_cast<int>(threadIdx.x >> 5) >= n) continue;
-            if (stride >= 64) {
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) space[place_of(i)] = v[i];
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) o[i] = space[place_of(i) ^ stride];
-            } else if (stride < 32) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) o[i] = __shfl_xor_sync(0xffffffffu, v[i], stride);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = place_of(i);
-                const bool larger = ((at & stride) == 0) == ((at & size) == 0);
-                if ((o[i] > v[i]) == larger) v[i] = o[i];
-            }
-        }
-}
-// Running sums in the order of the places: what lies before each, and the whole.
-__device__ __forceinline__ uint64_t running(Shared *s, const uint64_t (&w)[2], uint64_t (&before)[2]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t a = warp_prefix(w[0]), b = warp_prefix(w[1]), half = __shfl_sync(0xffffffffu, a, 31);
-    __syncthreads();  // (the places may still be read)
-    if (lane == 31) s->warp_sum[warp] = half + b;
-    __syncthreads();
-    uint64_t base = 0, all = 0;
-#pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
-        if (v < warp) base += s->warp_sum[v];
-        all += s->warp_sum[v];
-    }
-    before[0] = base + a - w[0], before[1] = base + half + b - w[1];
-    return all;
-}
-
 struct Target {  // of a sum's share
     __device__ static __forceinline__ uint64_t share(uint64_t all, float p) {  // the least that is not below it, 1 or more
         bool rest;
@@ -490,56 +207,391 @@ struct Target {  // of a sum's share
     }
 };
 
-__device__ __forceinline__ int places(int n) {  // a power of two
-    int n2 = 64;
-    while (n2 < n) n2 *= 2;
-    return n2;
-}
-
-// The listed tokens of a row (s->all, n of them, sorted here), by one block. The tokens before them weigh `ahead` and
-// stay; of these, the first top_k (0: all); then those before which, `ahead` included, less than `target` has been
-// passed, a share of the sum of the first top_k where target is 0; then those of min_p. Returns how many stay, a prefix.
-__device__ __forceinline__ int keep_listed(Shared *s, int n, int top_k, float top_p, float min_p, uint64_t ahead, uint64_t target,
-                                           const Weigher &weigh, uint64_t (&v)[2], uint64_t (&w)[2]) {
-    if (threadIdx.x == 0) s->kept = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) v[i] = place_of(i) < n ? s->all[place_of(i)] : 0;
-    sort_falling(v, places(n), s->all);
-    if (top_k > 0) n = min(n, top_k);
-    uint64_t before[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = place_of(i) < n ? weigh(logit_of(static_cast<uint32_t>(v[i] >> 32))) : 0;
-    const uint64_t all = running(s, w, before);
-    if (target == 0) target = top_p < 1.0f ? Target::share(all, top_p) : ~0ull;
-    const uint64_t light = min_p > 0.0f ? Target::share(weigh(weigh.m), min_p) : 1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (w[i] >= light && ahead + before[i] < target) atomicMax(&s->kept, static_cast<uint32_t>(place_of(i) + 1));
-    __syncthreads();
-    return static_cast<int>(s->kept);
-}
-
-// The token among the first n places, sorted by their indexes; found.place and found.value. Returns the sum of all.
-__device__ __forceinline__ uint64_t choose_listed(Shared *s, int n, const uint64_t (&v)[2], uint64_t (&w)[2], float u) {
-    uint64_t e[2], before[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        s->weight[place_of(i)] = w[i];
-        e[i] = place_of(i) < n ? v[i] << 32 | static_cast<uint32_t>(place_of(i)) : 0;  // (~index falls)
+// Tokens that are searched: a row in the cluster's shared memory, a contiguous slice a block and part of it a warp ...
+template <class T> struct RowTokens {
+    static constexpr bool kSent = false;
+    Shared *s;
+    const T *data;             // this block's slice
+    int first, count, part;    // its first index and size; a warp's part of it (a multiple of 64)
+    int rank, blocks;
+    __device__ __forceinline__ float logit(int i) const { return static_cast<float>(data[i]); }
+    template <class F> __device__ __forceinline__ void each(F f) const {  // f(logit, index)
+        const int lane = threadIdx.x & 31, from = (threadIdx.x >> 5) * part;
+        const int to = min(from + part, count);
+#pragma unroll 2
+        for (int i = from + lane; i < to; i += 32) f(logit(i), first + i);
     }
-    __syncthreads();
-    sort_falling(e, places(n), s->all);
+};
+// ... or those sent to the first block, n in any order, by that block alone.
+struct SentTokens {
+    static constexpr bool kSent = true;
+    [[maybe_unused]] static constexpr int first = 0, count = 0, part = 0, rank = 0, blocks = 1;
+    Shared *s;
+    int n, index_bits;         // log2 of the indexes that share a bin
+    template <class F> __device__ __forceinline__ void each(F f) const {
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint64_t e = s->all[i];
+            f(logit_of(static_cast<uint32_t>(e >> 32)), static_cast<int>(~static_cast<uint32_t>(e)));
+        }
+    }
+};
+
+template <class Tokens> struct Search : Tokens {
+    using Tokens::s, Tokens::first, Tokens::count, Tokens::part, Tokens::rank, Tokens::blocks, Tokens::each;
+    int turn = 0;              // which of the two sums' places is next
+
+    __device__ __forceinline__ void join() const {  // the whole cluster
+        if (blocks == 1) __syncthreads();
+        else cg::this_cluster().sync();
+    }
+    template <class P> __device__ __forceinline__ P *at(P *p, int block) const {
+        return blocks == 1 ? p : cg::this_cluster().map_shared_rank(p, block);
+    }
+    // Sums over the blocks before this one, over this one, and over all; of a second thing over all (~0: none).
+    struct Sums { uint64_t before, mine, all, all2; };
+    __device__ __forceinline__ Sums sums(uint64_t v, uint64_t v2) {
+        const uint64_t block2 = v2 == ~0ull ? 0 : block_total(v2);
+        uint64_t block = 0;
+        v = warp_total(v);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) s->warp_sum[threadIdx.x >> 5] = v;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = place_of(i) < n ? s->weight[static_cast<uint32_t>(e[i])] : 0;
-    const uint64_t all = running(s, w, before), t = Target::draw(all, u);
+        for (int w = 0; w < kWarps; ++w) block += s->warp_sum[w];
+        uint64_t (*const place)[2] = s->block_sum[turn];
+        turn ^= 1;
+        if (threadIdx.x < blocks) {
+            uint64_t *const there = at(&place[rank][0], threadIdx.x);
+            there[0] = block, there[1] = block2;
+        }
+        join();
+        Sums r{0, block, 0, 0};
+        for (int b = 0; b < blocks; ++b) {
+            if (b < rank) r.before += place[b][0];
+            r.all += place[b][0], r.all2 += place[b][1];
+        }
+        return r;
+    }
+    __device__ __forceinline__ uint64_t block_total(uint64_t v) {  // over this block's threads
+        v = warp_total(v);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) s->warp_sum[threadIdx.x >> 5] = v;
+        __syncthreads();
+        uint64_t all = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (before[i] < t && t <= before[i] + w[i]) s->found.place = ~static_cast<uint32_t>(e[i] >> 32), s->found.value = w[i];
-    __syncthreads();
-    return all;
-}
+        for (int w = 0; w < kWarps; ++w) all += s->warp_sum[w];
+        __syncthreads();
+        return all;
+    }
+    // The token, in index order, at which the sum of value(logit, index) reaches target(sum of all); found.place is its
+    // index, found.value its value. Returns the sum of all.
+    template <class V, class G> __device__ __forceinline__ uint64_t select(V value, G target) {
+        if constexpr (Tokens::kSent) {
+            // by histograms of the indexes' high bits, then of the low ones
+            const int bits = this->index_bits;
+            uint64_t whole = 0, t = 0;
+            uint32_t high = 0;
+            for (int level = 0; level < 2; ++level) {
+                __syncthreads();
+                clear_bins();
+                __syncthreads();
+                each([&](float l, int i) {
+                    const uint64_t v = level == 1 && static_cast<uint32_t>(i) >> bits != high ? 0 : value(l, i);
+                    if (v != 0) atomicAdd(reinterpret_cast<unsigned long long *>(&s->sum[level == 0 ? i >> bits : i & ((1 << bits) - 1)]), static_cast<unsigned long long>(v));
+                });
+                __syncthreads();
+                const uint64_t v[2] = {s->sum[2 * threadIdx.x], s->sum[2 * threadIdx.x + 1]};
+                const uint32_t n[2] = {0, 0};
+                if (level == 0) {
+                    whole = block_total(v[0] + v[1]);
+                    t = target(whole);
+                }
+                find_bin(v, n, false, t);
+                __syncthreads();
+                if (level == 0) high = s->found.place, t -= s->found.before;
+            }
+            __syncthreads();
+            if (threadIdx.x == 0) s->found.value = s->sum[s->found.place], s->found.place += high << bits;
+            __syncthreads();
+            return whole;
+        } else {
+            uint64_t mine = 0;
+            each([&](float l, int i) { mine += value(l, i); });
+            const Sums r = sums(mine, ~0ull);
+            const uint64_t t = target(r.all);
+            if (r.before < t && t <= r.before + r.mine) {  // in this block: it goes through the one warp's part again
+                uint64_t before = r.before;
+                int w = 0;
+                while (t > before + s->warp_sum[w]) before += s->warp_sum[w++];
+                __syncthreads();
+                const int from = w * part, to = min(from + part, count), per = (part + kThreads - 1) / kThreads;
+                const int i0 = from + per * threadIdx.x, i1 = min(i0 + per, to);
+                uint64_t sum = 0;
+                for (int i = i0; i < i1; ++i) sum += value(this->logit(i), first + i);
+                const uint64_t up_to = warp_prefix(sum);
+                if ((threadIdx.x & 31) == 31) s->warp_sum[threadIdx.x >> 5] = up_to;
+                __syncthreads();
+                before += up_to - sum;
+                for (int v = 0; v < (threadIdx.x >> 5); ++v) before += s->warp_sum[v];
+                if (before < t && t <= before + sum)
+                    for (int i = i0; i < i1; ++i) {
+                        const uint64_t v = value(this->logit(i), first + i);
+                        before += v;
+                        if (before >= t) {
+                            for (int b = 0; b < blocks; ++b) {
+                                auto *f = at(&s->found, b);
+                                f->place = first + i, f->value = v;
+                            }
+                            break;
+                        }
+                    }
+            }
+            join();
+            return r.all;
+        }
+    }
+    __device__ __forceinline__ void clear_bins() {
+        for (int b = threadIdx.x; b < kBins; b += kThreads) s->sum[b] = 0, s->count[b] = 0;
+    }
+    // The cluster's counts (sums) of this thread's two bins.
+    __device__ __forceinline__ void bin_counts(uint32_t (&n)[2]) const {
+        n[0] = n[1] = 0;
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) {
+            const uint2 c = *reinterpret_cast<const uint2 *>(at(s->count, b) + 2 * threadIdx.x);
+            n[0] += c.x, n[1] += c.y;
+        }
+    }
+    __device__ __forceinline__ void bin_sums(uint64_t (&v)[2]) const {
+        v[0] = v[1] = 0;
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) {
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(at(s->sum, b) + 2 * threadIdx.x);
+            v[0] += c.x, v[1] += c.y;
+        }
+    }
+    // Bins of a histogram, each thread two neighbours, `rising`: counted from the last one: where the running sum of v
+    // reaches `target`; found: the bin, the sum before it, and its n (left as it was where the sum does not). Every
+    // thread of every block calls it, with a barrier before found is read.
+    __device__ __forceinline__ void find_bin(const uint64_t (&v)[2], const uint32_t (&n)[2], bool rising, uint64_t target) {
+        const uint64_t both = v[0] + v[1], up_to = warp_prefix(both);
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 31) s->warp_sum[warp] = up_to;
+        __syncthreads();
+        uint64_t before = up_to - both, whole = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += s->warp_sum[w];
+            whole += s->warp_sum[w];
+        }
+        if (rising) before = whole - before - both;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int b = rising ? 1 - i : i;
+            if (before < target && target <= before + v[b]) s->found.place = 2 * threadIdx.x + b, s->found.before = before, s->found.count = n[b];
+            before += v[b];
+        }
+    }
+    // Tokens for which take(logit) holds are sent to the first block, as far as there is room.
+    template <class F> __device__ __forceinline__ void send(F take) {
+        const int lane = threadIdx.x & 31, from = (threadIdx.x >> 5) * part, to = min(from + part, count);
+        uint64_t *const there = at(s->all, 0);
+        uint32_t *const counter = at(&s->list_count, 0);
+        for (int i0 = from; i0 < to; i0 += 32) {
+            const int i = i0 + lane;
+            const float l = i < to ? this->logit(i) : -INFINITY;
+            const bool in = i < to && take(l);
+            const uint32_t who = __ballot_sync(0xffffffffu, in);
+            if (who == 0) continue;
+            uint32_t place = 0;
+            if (lane == 0) place = atomicAdd(counter, static_cast<uint32_t>(__popc(who)));
+            place = __shfl_sync(0xffffffffu, place, 0) + __popc(who & ((1u << lane) - 1));
+            if (in && place < kCap) there[place] = static_cast<uint64_t>(key_of(l)) << 32 | ~static_cast<uint32_t>(first + i);
+        }
+    }
+    // The border at which the running value (1, or the weight) over the tokens up to `limit`, in falling order,
+    // reaches `target` (at least 1, at most the sum of all). The first bins are of m - l, `scale` a unit; with weights,
+    // tokens of `reach` and less are known to lie behind it.
+    template <bool WEIGHTS, class W>
+    __device__ __forceinline__ Border border(Border limit, uint64_t target, float m, float scale, float reach, W weigh) {
+        uint32_t lo = 0, hi = 0, bin0 = 0;
+        int shift = -1;  // -1: the first histogram, of m - l
+        auto member = [&](float l, int i, uint32_t &bin) {
+            const uint32_t key = key_of(l);
+            if (key < limit.key || (key == limit.key && static_cast<uint32_t>(i) > limit.index)) return false;
+            bin = bin_of(l, m, scale);
+            if (shift < 0) return true;
+            if (bin != bin0 || key < lo || key > hi) return false;
+            bin = (key - lo) >> shift;
+            return true;
+        };
+        for (;;) {
+            __syncthreads();
+            clear_bins();
+            if (threadIdx.x == 0) s->list_count = 0;
+            __syncthreads();
+            each([&](float l, int i) {
+                uint32_t bin;
+                if (WEIGHTS && !(l > reach)) return;
+                if (!member(l, i, bin)) return;
+                atomicAdd(&s->count[bin], 1u);
+                if (WEIGHTS) atomicAdd(reinterpret_cast<unsigned long long *>(&s->sum[bin]), static_cast<unsigned long long>(weigh(l)));
+            });
+            join();
+            uint64_t v[2];
+            uint32_t n[2];
+            bin_counts(n);
+            if (WEIGHTS) bin_sums(v);
+            else v[0] = n[0], v[1] = n[1];
+            // bins of the first histogram fall with the logit, those of the others rise
+            find_bin(v, n, shift >= 0, target);
+            join();  // (the histograms have been read, too)
+            const uint32_t bin = s->found.place, in_bin = s->found.count;
+            target -= s->found.before;
+            if (shift < 0) {
+                bin0 = bin;
+                lo = bin == kBins - 1 ? 0u : key_of(m - (bin + 2) / scale);
+                hi = key_of(bin == 0 ? INFINITY : m - (bin - 1) / scale);
+            } else {
+                lo += bin << shift;
+                const uint32_t top = lo + ((1u << shift) - 1u);
+                hi = top < lo || top > hi ? hi : top;
+            }
+            const uint32_t width = hi - lo;
+            shift = width < kBins ? 0 : 22 - __clz(width);
+            if (in_bin <= kList) break;
+            if (lo == hi) {  // so many equal ones: the border is found by index
+                const uint64_t each_one = WEIGHTS ? weigh(logit_of(lo)) : 1, nth = (target + each_one - 1) / each_one;
+                __syncthreads();
+                select([&](float x, int i) -> uint64_t { return key_of(x) == lo && (lo != limit.key || static_cast<uint32_t>(i) <= limit.index); },
+                       [&](uint64_t) { return nth; });
+                return Border{lo, s->found.place};
+            }
+        }
+        // the few tokens left, compared with each other by every block
+        each([&](float l, int i) {
+            uint32_t bin;
+            if (WEIGHTS && !(l > reach)) return;
+            if (!member(l, i, bin)) return;
+            s->list[atomicAdd(&s->list_count, 1u)] = static_cast<uint64_t>(key_of(l)) << 32 | ~static_cast<uint32_t>(i);
+        });
+        join();
+        int n = 0;
+        for (int b = 0; b < blocks; ++b) {
+            const int m = static_cast<int>(*at(&s->list_count, b));
+            if (static_cast<int>(threadIdx.x) < m) s->near[n + threadIdx.x] = at(s->list, b)[threadIdx.x];
+            n += m;
+        }
+        compare(s, n, [&](uint64_t e) -> uint64_t { return WEIGHTS ? weigh(logit_of(static_cast<uint32_t>(e >> 32))) : 1; },
+                [](uint64_t a, uint64_t b) { return a > b; });
+        if (threadIdx.x < n && s->ahead[threadIdx.x] < target && target <= s->ahead[threadIdx.x] + s->weight[threadIdx.x])
+            s->found.value = s->near[threadIdx.x];
+        join();
+        const uint64_t e = s->found.value;
+        return Border{static_cast<uint32_t>(e >> 32), ~static_cast<uint32_t>(e)};
+    }
+    // For each of s->near's first n tokens (kList at most), all pairs at once: its weight, how many of the others come
+    // before it, and what those weigh.
+    template <class W, class L> __device__ static __forceinline__ void compare(Shared *s, int n, W weight, L before) {
+        int n2 = 16;
+        while (n2 < n) n2 *= 2;
+        if (threadIdx.x < kList) s->ahead[threadIdx.x] = 0, s->rank[threadIdx.x] = 0;
+        __syncthreads();
+        if (threadIdx.x < n) s->weight[threadIdx.x] = weight(s->near[threadIdx.x]);
+        __syncthreads();
+        const int i = threadIdx.x & (n2 - 1), per = n2 * n2 / kThreads + (n2 * n2 < kThreads), j0 = threadIdx.x / n2 * per;
+        if (i < n) {
+            const uint64_t e = s->near[i];
+            uint64_t sum = 0;
+            uint32_t many = 0;
+            for (int j = j0; j < min(j0 + per, n); ++j)
+                if (before(s->near[j], e)) sum += s->weight[j], ++many;
+            if (many > 0) {
+                atomicAdd(&s->rank[i], many);
+                atomicAdd(reinterpret_cast<unsigned long long *>(&s->ahead[i]), static_cast<unsigned long long>(sum));
+            }
+        }
+        __syncthreads();
+    }
+};
 
 enum Todo { kNothing, kSelect, kTopP, kAll };
+
+// The filters that `todo` leaves open, by a search each, and the token.
+struct Chosen { int32_t token; float prob; };
+template <class Tokens>
+__device__ __forceinline__ Chosen search_all(Search<Tokens> &search, int todo, Border last, int top_k, float top_p, float min_p, float u,
+                                             float t, int vocab, float m, float scale, const Weigher &weigh) {
+    auto kept = [&](float l, int i) {
+        const uint32_t key = key_of(l);
+        return key > last.key || (key == last.key && static_cast<uint32_t>(i) <= last.index);
+    };
+    if (todo == kAll && top_k > 0) last = search.template border<false>(last, top_k, m, scale, 0.0f, weigh);
+    if (todo != kSelect && top_p < 1.0f) {
+        uint64_t mine = 0;
+        search.each([&](float l, int i) {
+            if (kept(l, i)) mine += weigh(l);
+        });
+        const uint64_t all = search.sums(mine, ~0ull).all;
+        // Weights below (1 - top_p) / vocab of the sum are all past the border: their sum is less than what is cut.
+        const float least = (1.0f - top_p) * (static_cast<float>(all) * (1.0f / kOne)) / static_cast<float>(vocab);
+        const float reach = weigh.m == INFINITY ? 0.0f : weigh.m + (log2f(least) - 0.02f) * t * 0.694f - 1e-6f * fabsf(weigh.m);
+        last = search.template border<true>(last, Target::share(all, top_p), m, scale, reach, weigh);
+    }
+    const uint64_t light = min_p > 0.0f ? Target::share(weigh(weigh.m), min_p) : 0;
+    const uint64_t all = search.select(
+        [&](float l, int i) -> uint64_t {
+            if (!kept(l, i)) return 0;
+            const uint64_t w = weigh(l);
+            return w >= light ? w : 0;
+        },
+        [&](uint64_t all) { return Target::draw(all, u); });
+    return Chosen{static_cast<int32_t>(search.s->found.place), static_cast<float>(search.s->found.value) / static_cast<float>(all)};
+}
+
+// The first block's n tokens, all that may be kept, and the filters: the token.
+__device__ __forceinline__ Chosen choose_sent(Shared *s, int n, int index_bits, int top_k, float top_p, float min_p, float u, float t,
+                                              int vocab, float m, float scale, const Weigher &weigh) {
+    using Sent = Search<SentTokens>;
+    if (n > kList) {
+        Sent sent;
+        sent.s = s, sent.n = n, sent.index_bits = index_bits;
+        return search_all(sent, kAll, Border{0u, 0xFFFFFFFFu}, top_k > 0 && top_k < n ? top_k : 0, top_p, min_p, u, t, vocab, m, scale, weigh);
+    }
+    const int i = threadIdx.x;
+    if (i < n) s->near[i] = s->all[i];
+    if (i == 0) s->total = 0;
+    Sent::compare(s, n, [&](uint64_t e) { return weigh(logit_of(static_cast<uint32_t>(e >> 32))); }, [](uint64_t a, uint64_t b) { return a > b; });
+    const bool in = i < n && (top_k == 0 || s->rank[i] < static_cast<uint32_t>(top_k));
+    uint64_t w = in ? s->weight[i] : 0;
+    if (top_p < 1.0f) {
+        const uint64_t sum = warp_total(w);
+        if ((i & 31) == 0 && sum > 0) atomicAdd(reinterpret_cast<unsigned long long *>(&s->total), static_cast<unsigned long long>(sum));
+        __syncthreads();
+        if (i < n && s->ahead[i] >= Target::share(s->total, top_p)) w = 0;
+    }
+    if (min_p > 0.0f && w < Target::share(weigh(weigh.m), min_p)) w = 0;
+    __syncthreads();
+    if (i == 0) s->total = 0;
+    // the kept weights, in the order of the indexes (~index falls)
+    Sent::compare(s, n, [&](uint64_t) { return w; }, [](uint64_t a, uint64_t b) { return static_cast<uint32_t>(a) > static_cast<uint32_t>(b); });
+    const uint64_t sum = warp_total(w);
+    if ((i & 31) == 0 && sum > 0) atomicAdd(reinterpret_cast<unsigned long long *>(&s->total), static_cast<unsigned long long>(sum));
+    __syncthreads();
+    const uint64_t all = s->total, draw = Target::draw(all, u);
+    if (i < n && s->ahead[i] < draw && draw <= s->ahead[i] + w) s->found.place = ~static_cast<uint32_t>(s->near[i]), s->found.value = w;
+    __syncthreads();
+    return Chosen{static_cast<int32_t>(s->found.place), static_cast<float>(s->found.value) / static_cast<float>(all)};
+}
+
+// The first block's n tokens, of the bins in which the border lies: the last one kept, with `target` (a count, or a sum
+// of weights) to be reached among them.
+template <bool WEIGHTS>
+__device__ __forceinline__ Border border_of_sent(Shared *s, int n, int index_bits, uint64_t target, float m, float scale, const Weigher &weigh) {
+    Search<SentTokens> sent;
+    sent.s = s, sent.n = n, sent.index_bits = index_bits;
+    return sent.template border<WEIGHTS>(Border{0u, 0xFFFFFFFFu}, target, m, scale, -INFINITY, weigh);
+}
 
 template <class T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
@@ -548,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     T *const space = reinterpret_cast<T *>(smem + (sizeof(Shared) + 31) / 32 * 32);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r = blockIdx.x / p.blocks;
-    Row<T> row;
+    Search<RowTokens<T>> row;
     row.s = s;
     row.blocks = p.blocks;
     row.rank = static_cast<int>(blockIdx.x % p.blocks);
@@ -557,10 +609,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     row.count = max(0, min(p.vocab - row.first, kWarps * p.part));
     if (threadIdx.x < 64) s->power[threadIdx.x] = p.power[threadIdx.x];
     if (threadIdx.x == 0) s->list_count = 0;
-    row.clear_bins(false);
+    row.clear_bins();
     if (p.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_allow_dependents();
     pdl_wait_prior_grids();
+
+    // ---- the settings
+    const float t = p.temperature ? p.temperature[r] : 1.0f, u = p.uniform[r];
+    float top_p = p.top_p ? p.top_p[r] : 1.0f, min_p = p.min_p ? p.min_p[r] : 0.0f;
+    int top_k = p.top_k ? p.top_k[r] : 0;
+    if (top_k < 0 || top_k >= p.vocab) top_k = 0;
+    if (!(top_p < 1.0f)) top_p = 1.0f;  // (NaN: all)
+    if (!(min_p > 0.0f)) min_p = 0.0f;
 
     // ---- the row, as far from a boundary of eight elements here as there
     const T *const src = static_cast<const T *>(p.logits) + r * p.stride + row.first;
@@ -608,206 +668,158 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     row.join();
     top = -INFINITY, low = INFINITY;
+#pragma unroll 4
     for (int b = 0; b < row.blocks; ++b) top = fmaxf(top, s->block_extremes[b].x), low = fminf(low, s->block_extremes[b].y);
 
-    // ---- the settings
-    const float t = p.temperature ? p.temperature[r] : 1.0f;
-    float top_p = p.top_p ? p.top_p[r] : 1.0f, min_p = p.min_p ? p.min_p[r] : 0.0f;
-    int top_k = p.top_k ? p.top_k[r] : 0;
-    if (top_k < 0 || top_k >= p.vocab) top_k = 0;
-    if (!(top_p < 1.0f)) top_p = 1.0f;  // (NaN: all)
-    if (!(min_p > 0.0f)) min_p = 0.0f;
-    const float u = p.uniform[r];
-    int32_t token = -1;
-    float prob = 0.0f;
-    if (top > -INFINITY) {
-        if (!(t >= kLeastTemperature) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f) {  // the first alone
-            uint32_t first = 0xFFFFFFFFu;
-            if (mine_top == top)
-                for (int i0 = 8 * threadIdx.x - pad; i0 < row.count && first == 0xFFFFFFFFu; i0 += 8 * kThreads)
-                    for (int i = max(i0, 0); i < min(i0 + 8, row.count); ++i)
-                        if (first == 0xFFFFFFFFu && row.logit(i) == top) first = row.first + i;
-            first = __reduce_min_sync(0xffffffffu, first);
-            if (lane == 0 && first != 0xFFFFFFFFu)  // (list_count holds 0 less the least index so far)
-                for (int b = 0; b < row.blocks; ++b) atomicMax(row.at(&s->list_count, b), 0u - 1u - first);
-            row.join();
-            token = static_cast<int32_t>(0u - 1u - s->list_count), prob = 1.0f;
-        } else {
-            Weigher weigh;
-            weigh.set(s->power, top, t);
-            Border last{0u, 0xFFFFFFFFu};
-            int todo = kSelect;  // what is left: the filters (kAll, kTopP), the selection, or nothing
-            // bins per unit of m - l, a power of two, over so much
-            auto bins_over = [&](float most) { return __uint_as_float(__float_as_uint((kBins - 1) / fminf(fmaxf(top - low, 0x1p-100f), most)) & 0x7F800000u); };
-            const bool by_weight = top_k == 0 && top_p < 1.0f;
-            const float scale = bins_over(by_weight ? fminf(32.0f * t, FLT_MAX) : kRange);
-            const float reach = top == INFINITY ? 0.0f : top + (log2f(min_p) - 0.02f) * t * 0.694f - 1e-6f * fabsf(top);  // (of min_p alone)
-            if (top_k > 0 ? top_k <= kThreads * row.blocks : top_p == 1.0f && min_p > 0.0f) {
-                // ---- a cut that as many tokens reach, by the threads' own largest, or that min_p gives
-                uint32_t last_bin = 0;
-                if (top_k > 0) {
-                    if (mine_top > -INFINITY) atomicAdd(&s->count[bin_of(mine_top, top, scale)], 1u);
-                    row.join();
-                    uint32_t n[2];
-                    row.bin_counts(n);
-                    const uint64_t count[2] = {n[0], n[1]};
-                    if (threadIdx.x == 0) s->found.place = kBins - 1;
-                    __syncthreads();
-                    row.find_bin(count, n, false, static_cast<uint64_t>(top_k));
-                    __syncthreads();
-                    last_bin = s->found.place;
-                }
-                row.send([&](float l) { return top_k > 0 ? bin_of(l, top, scale) <= last_bin : l > reach; });
-                row.join();
-                const uint32_t n = *row.at(&s->list_count, 0);
-                if (n <= kCap) {  // the first block goes on alone, in its own memory, and stays until the others have read it
-                    todo = kNothing;
-                    if (p.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-                }
-                if (n > kCap && top_k > 0) todo = kAll;
-                if (todo == kNothing && row.rank == 0) {
-                    uint64_t v[2], w[2];
-                    const int kept = keep_listed(s, n, top_k, top_p, min_p, 0, 0, weigh, v, w);
-                    const uint64_t all = choose_listed(s, kept, v, w, u);
-                    token = static_cast<int32_t>(s->found.place);
-                    prob = static_cast<float>(s->found.value) / static_cast<float>(all);
-                }
-                if (todo == kNothing && p.blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-            } else if (top_k > 0 || by_weight) {
-                todo = kAll;
-            }
-            if (todo == kAll) {
-                // ---- the bins in which the border lies
-                row.join();  // (the memory is used again)
-                row.clear_bins(true);
-                if (threadIdx.x == 0) s->list_count = 0;
-                row.join();
-                uint32_t *const deficit = reinterpret_cast<uint32_t *>(s->sum);  // of a bin's tokens' weights, in 2^-16 of its first possible one
-                const float per_bin = weigh.ch / scale;                         // log2 of the weights' ratio over a bin, 0.1 at most
-                row.each([&](float l, int) {
-                    const uint32_t b = bin_of(l, top, scale);
-                    atomicAdd(&s->count[b], 1u);
-                    if (by_weight && b + 1 < kBins) {
-                        float y;
-                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(((top - l) * scale - b) * -per_bin));
-                        atomicAdd(&deficit[b], static_cast<uint32_t>(__float2int_rn((1.0f - y) * 65536.0f)));
-                    }
-                });
+    Chosen chosen{-1, 0.0f};
+    if (top == -INFINITY) {  // no token
+    } else if (!(t >= kLeastTemperature) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f) {  // the first alone
+        uint32_t first = 0xFFFFFFFFu;
+        if (mine_top == top)
+            for (int i0 = 8 * threadIdx.x - pad; i0 < row.count && first == 0xFFFFFFFFu; i0 += 8 * kThreads)
+                for (int i = max(i0, 0); i < min(i0 + 8, row.count); ++i)
+                    if (first == 0xFFFFFFFFu && row.logit(i) == top) first = row.first + i;
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (lane == 0 && first != 0xFFFFFFFFu)  // (list_count holds 0 less 1 less the least index so far)
+            for (int b = 0; b < row.blocks; ++b) atomicMax(row.at(&s->list_count, b), 0u - 1u - first);
+        row.join();
+        chosen = Chosen{static_cast<int32_t>(0u - 1u - s->list_count), 1.0f};
+    } else {
+        Weigher weigh;
+        weigh.set(s->power, top, t);
+        Border last{0u, 0xFFFFFFFFu};
+        int todo = kSelect;  // what is left: the filters (kAll, kTopP), the selection, or nothing
+        // bins per unit of m - l, a power of two, over so much
+        auto bins_over = [&](float most) { return __uint_as_float(__float_as_uint((kBins - 1) / fminf(fmaxf(top - low, 0x1p-100f), most)) & 0x7F800000u); };
+        const bool by_weight = top_k == 0 && top_p < 1.0f;
+        const float scale = bins_over(by_weight ? fminf(32.0f * t, FLT_MAX) : kRange);
+        const int index_bits = max(0, 22 - __clz(p.vocab - 1));  // of an index, but the highest ten
+        if (top_k > 0 ? top_k <= kThreads * row.blocks : top_p == 1.0f && min_p > 0.0f) {
+            // ---- a cut that as many tokens reach, by the threads' own largest, or that min_p gives
+            uint32_t last_bin = 0;
+            if (top_k > 0) {
+                if (mine_top > -INFINITY) atomicAdd(&s->count[bin_of(mine_top, top, scale)], 1u);
+                if (threadIdx.x == 0) s->found.place = kBins - 1;
                 row.join();
                 uint32_t n[2];
                 row.bin_counts(n);
-                uint32_t bin_lo, bin_hi;
-                if (by_weight) {
-                    // what the bins weigh at most and at least, off by 2^-15 in all: half a unit of 2^-16 for each token and
-                    // the steps to it; of the last bin's tokens only the upper bound is known
-                    uint64_t most[2], least[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int b = 2 * threadIdx.x + i;
-                        uint32_t less = 0;
-                        for (int q = 0; q < row.blocks; ++q) less += row.at(deficit, q)[b];
-                        float y;
-                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-b * per_bin));
-                        y *= static_cast<float>(n[i]) - static_cast<float>(less) * 0x1p-16f;
-                        if (top == INFINITY) y = b == 0 ? static_cast<float>(n[i]) : 0.0f;
-                        most[i] = __float2ull_rn(y * (1.0f + 0x1p-15f) * kOne);
-                        least[i] = b + 1 < kBins || top == INFINITY ? __float2ull_rn(y * (1.0f - 0x1p-15f) * kOne) : 0;
-                    }
-                    const uint64_t all_most = row.block_total(most[0] + most[1]), all_least = row.block_total(least[0] + least[1]);
-                    if (threadIdx.x == 0) s->found.place = kBins - 1;
-                    __syncthreads();
-                    row.find_bin(most, n, false, Target::share(all_least, top_p));
-                    __syncthreads();
-                    bin_lo = s->found.place;
-                    __syncthreads();
-                    if (threadIdx.x == 0) s->found.place = kBins - 1;
-                    __syncthreads();
-                    row.find_bin(least, n, false, Target::share(all_most, top_p));
-                    __syncthreads();
-                    bin_hi = max(bin_lo, s->found.place);
-                } else {
-                    const uint64_t count[2] = {n[0], n[1]};
-                    row.find_bin(count, n, false, static_cast<uint64_t>(top_k));
-                    __syncthreads();
-                    bin_lo = bin_hi = s->found.place;
+                const uint64_t count[2] = {n[0], n[1]};
+                row.find_bin(count, n, false, static_cast<uint64_t>(top_k));
+                __syncthreads();
+                last_bin = s->found.place;
+            }
+            const float reach = top == INFINITY ? 0.0f : top + (log2f(min_p) - 0.02f) * t * 0.694f - 1e-6f * fabsf(top);  // (of min_p alone)
+            row.send([&](float l) { return top_k > 0 ? bin_of(l, top, scale) <= last_bin : l > reach; });
+            row.join();
+            const uint32_t n = *row.at(&s->list_count, 0);
+            if (n <= kCap) {  // the first block goes on alone, in its own memory, and stays until the others have read it
+                todo = kNothing;
+                if (p.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+                if (row.rank == 0) chosen = choose_sent(s, n, index_bits, top_k, top_p, min_p, u, t, p.vocab, top, scale, weigh);
+                if (p.blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            } else if (top_k > 0) {
+                todo = kAll;
+            }
+        } else if (top_k > 0 || by_weight) {
+            todo = kAll;
+        }
+        if (todo == kAll) {
+            // ---- the bins in which the border lies
+            row.join();  // (the memory is used again)
+            row.clear_bins();
+            if (threadIdx.x == 0) s->list_count = 0, s->found.place = kBins - 1;
+            row.join();
+            // s->sum: what a bin's tokens weigh less than its first possible one, in 2^-16 of that
+            const float per_bin = weigh.ch / scale;  // log2 of the weights' ratio over a bin, 0.1 at most
+            row.each([&](float l, int) {
+                const uint32_t b = bin_of(l, top, scale);
+                atomicAdd(&s->count[b], 1u);
+                if (by_weight && b + 1 < kBins) {
+                    float y;
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(((top - l) * scale - b) * -per_bin));
+                    atomicAdd(reinterpret_cast<uint32_t *>(&s->sum[b]), static_cast<uint32_t>(__float2int_rn((1.0f - y) * 65536.0f)));
                 }
-                uint32_t above = 0, in = 0;  // tokens in the bins before these, and in them
+            });
+            row.join();
+            uint32_t n[2];
+            row.bin_counts(n);
+            uint32_t bin_lo, bin_hi;
+            if (by_weight) {
+                // what the bins weigh at most and at least, off by 2^-15 in all: half a unit of 2^-16 for each token and
+                // the steps to it; of the last bin's tokens only the upper bound is known
+                uint64_t less[2], most[2], least[2];
+                row.bin_sums(less);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t b = 2 * threadIdx.x + i;
-                    if (b < bin_lo) above += n[i];
-                    else if (b <= bin_hi) in += n[i];
+                    const int b = 2 * threadIdx.x + i;
+                    float y;
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-b * per_bin));
+                    y *= static_cast<float>(n[i]) - static_cast<float>(less[i]) * 0x1p-16f;
+                    if (top == INFINITY) y = b == 0 ? static_cast<float>(n[i]) : 0.0f;
+                    most[i] = __float2ull_rn(y * (1.0f + 0x1p-15f) * kOne);
+                    least[i] = b + 1 < kBins || top == INFINITY ? __float2ull_rn(y * (1.0f - 0x1p-15f) * kOne) : 0;
                 }
-                const uint64_t both = row.block_total(static_cast<uint64_t>(above) << 32 | in);
-                above = static_cast<uint32_t>(both >> 32), in = static_cast<uint32_t>(both);
-                if (in <= kCap) {
-                    uint64_t before = 0, after = 0;
-                    row.send([&](float l) {
-                        const uint32_t b = bin_of(l, top, scale);
-                        if (by_weight) {
-                            const uint64_t w = weigh(l);
-                            if (b < bin_lo) before += w;
-                            else after += w;
-                        }
-                        return b >= bin_lo && b <= bin_hi;
-                    });
-                    uint64_t ahead = 0, target = ~0ull;
-                    if (by_weight) {
-                        ahead = row.sums(before).all;
-                        target = Target::share(ahead + row.sums(after).all, top_p);
-                    }
-                    if (threadIdx.x == 0) s->found.count = 0;  // (1 once the first block has found the border)
-                    row.join();
-                    if (row.rank == 0) {
-                        uint64_t v[2], w[2];
-                        const int kept = keep_listed(s, in, by_weight ? 0 : top_k - static_cast<int>(above), 1.0f, 0.0f, ahead, target, weigh, v, w);
+                const uint64_t all_most = row.block_total(most[0] + most[1]), all_least = row.block_total(least[0] + least[1]);
+                row.find_bin(most, n, false, Target::share(all_least, top_p));
+                __syncthreads();
+                bin_lo = s->found.place;
+                __syncthreads();
+                if (threadIdx.x == 0) s->found.place = kBins - 1;
+                row.find_bin(least, n, false, Target::share(all_most, top_p));
+                __syncthreads();
+                bin_hi = max(bin_lo, s->found.place);
+            } else {
+                const uint64_t count[2] = {n[0], n[1]};
+                row.find_bin(count, n, false, static_cast<uint64_t>(top_k));
+                __syncthreads();
+                bin_lo = bin_hi = s->found.place;
+            }
+            uint32_t above = 0, in = 0;  // tokens in the bins before these, and in them
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (place_of(i) + 1 == kept)
-                                for (int b = 0; b < row.blocks; ++b) row.at(&s->found, b)->value = v[i], row.at(&s->found, b)->count = 1;
-                    }
-                    row.join();
-                    if (s->found.count != 0) {
-                        last = Border{static_cast<uint32_t>(s->found.value >> 32), ~static_cast<uint32_t>(s->found.value)};
-                        todo = !by_weight && top_p < 1.0f ? kTopP : kSelect;
-                    }
-                }
-                row.join();  // (the memory is used again)
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t b = 2 * threadIdx.x + i;
+                if (b < bin_lo) above += n[i];
+                else if (b <= bin_hi) in += n[i];
             }
-            if (todo != kNothing) {
-                // ---- any number of them
-                auto kept = [&](float l, int i) {
-                    const uint32_t key = key_of(l);
-                    return key > last.key || (key == last.key && static_cast<uint32_t>(i) <= last.index);
-                };
-                if (todo == kAll && top_k > 0) last = row.template border<false>(last, top_k, top, bins_over(kRange), 0.0f, weigh);
-                if (todo != kSelect && top_p < 1.0f) {
-                    uint64_t mine = 0;
-                    row.each([&](float l, int i) {
-                        if (kept(l, i)) mine += weigh(l);
-                    });
-                    const uint64_t all = row.sums(mine).all;
-                    // Weights below (1 - top_p) / vocab of the sum are all past the border: their sum is less than what is cut.
-                    const float least = (1.0f - top_p) * (static_cast<float>(all) * (1.0f / kOne)) / static_cast<float>(p.vocab);
-                    const float reach = top == INFINITY ? 0.0f : top + (log2f(least) - 0.02f) * t * 0.694f - 1e-6f * fabsf(top);
-                    last = row.template border<true>(last, Target::share(all, top_p), top, bins_over(kRange), reach, weigh);
-                }
-                const uint64_t light = min_p > 0.0f ? Target::share(weigh(top), min_p) : 0;
-                const uint64_t all = row.select(
-                    [&](float l, int i) -> uint64_t {
-                        if (!kept(l, i)) return 0;
+            const uint64_t both = row.block_total(static_cast<uint64_t>(above) << 32 | in);
+            above = static_cast<uint32_t>(both >> 32), in = static_cast<uint32_t>(both);
+            if (in <= kCap) {
+                uint64_t before = 0, after = 0;
+                row.send([&](float l) {
+                    const uint32_t b = bin_of(l, top, scale);
+                    if (by_weight) {
                         const uint64_t w = weigh(l);
-                        return w >= light ? w : 0;
-                    },
-                    [&](uint64_t all) { return Target::draw(all, u); });
-                token = static_cast<int32_t>(s->found.place);
-                prob = static_cast<float>(s->found.value) / static_cast<float>(all);
+                        if (b < bin_lo) before += w;
+                        else after += w;
+                    }
+                    return b >= bin_lo && b <= bin_hi;
+                });
+                uint64_t target = top_k - above;
+                if (by_weight) {
+                    const auto sums = row.sums(before, after);
+                    target = Target::share(sums.all + sums.all2, top_p) - sums.all;
+                } else {
+                    row.join();
+                }
+                if (row.rank == 0) {
+                    // finer bins from the first one's edge on (what lies a rounding above it counts as in the first)
+                    const float edge = top == INFINITY ? top : top - bin_lo / scale, finer = scale * __uint_as_float((127u + __clz(bin_hi - bin_lo) - 22u) << 23);
+                    const Border b = by_weight ? border_of_sent<true>(s, in, index_bits, target, edge, finer, weigh)
+                                               : border_of_sent<false>(s, in, index_bits, target, edge, finer, weigh);
+                    __syncthreads();
+                    if (threadIdx.x < row.blocks) row.at(&s->found, threadIdx.x)->value = static_cast<uint64_t>(b.key) << 32 | b.index;
+                }
+                row.join();
+                last = Border{static_cast<uint32_t>(s->found.value >> 32), static_cast<uint32_t>(s->found.value)};
+                todo = !by_weight && top_p < 1.0f ? kTopP : kSelect;
             }
+            row.join();  // (the memory is used again)
         }
+        if (todo != kNothing) chosen = search_all(row, todo, last, top_k, top_p, min_p, u, t, p.vocab, top, bins_over(kRange), weigh);
     }
     if (row.rank == 0 && threadIdx.x == 0) {
-        p.token[r] = token;
-        if (p.prob) p.prob[r] = prob;
+        p.token[r] = chosen.token;
+        if (p.prob) p.prob[r] = chosen.prob;
     }
 }
 
@@ -828,7 +840,7 @@ template <class T> cudaError_t launch(SampleParams p, int n, int sms, int device
     auto part = [&](int blocks) { return (p.vocab + 64 * kWarps * blocks - 1) / (64 * kWarps * blocks) * 64; };
     p.blocks = 1;
     while (p.blocks < kMaxCluster &&
-           (slice_smem<T>(part(p.blocks)) > kSmemLimit / 2 || (static_cast<int64_t>(n) * p.blocks * 2 <= sms && part(p.blocks) >= 256 && p.blocks < 8)))
+           (slice_smem<T>(part(p.blocks)) > kSmemLimit / 2 || (static_cast<int64_t>(n) * p.blocks <= sms && part(p.blocks) >= 256 && p.blocks < 8)))
         p.blocks *= 2;
     p.part = part(p.blocks);
     cudaLaunchConfig_t cfg = {};
