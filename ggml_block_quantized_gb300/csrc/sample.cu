@@ -2,7 +2,7 @@
 //
 // A row is read once into the shared memory of a cluster of thread blocks (one
 // block, or up to 16 for long rows and few of them), each holding a contiguous
-// slice, each warp a contiguous part of it. What follows are passes over that
+// slice, a thread eight logits of each 4096. What follows are passes over that
 // memory:
 //  * the largest logit m;
 //  * with top_k, the threads' own largest logits, a histogram of which gives a cut
@@ -13,8 +13,7 @@
 //    the bins in which the border lies, one or two. Their tokens go to the first
 //    block, which finds the last one kept by the sum of the weights before them.
 //  * Then, as without filters, the token at which the sum of the kept weights, in
-//    index order, passes its target: sums per warp, then the block goes through the
-//    one warp's part again.
+//    index order, passes its target: sums of 256 tokens each, then these one by one.
 // The first block compares up to kList tokens with each other, all pairs at once.
 // More of them, and rows whose border's bins hold too many (equal logits, as a
 // rule) or whose top_p follows a large top_k, are searched: for each filter a
@@ -27,7 +26,9 @@
 // every other, and a border is met as in exact arithmetic: with 32-bit sums a
 // token in some thousands would differ from the one that 64 bits give, since
 // with 10^5 tokens that many borders share the unit interval. 2^x for them takes
-// an argument in two floats, a table of 64 powers and a polynomial of degree 5.
+// an argument in two floats, a table of 64 powers and a polynomial of degree 5, two
+// logits at a time in packed instructions, 27 a logit; the passes are bound by
+// their instructions.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -45,8 +46,10 @@ namespace qg {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kSet = 8;          // neighbouring logits of a thread
+constexpr int kRowSets = kThreads, kSegment = 32 * kSet;  // sets, one a thread, that follow each other; logits of a warp there
 constexpr int kBins = 1024;
-constexpr int kCap = 1024;       // tokens that go to one block
+constexpr int kCap = 2048;       // tokens that go to one block
 constexpr int kList = 128;       // tokens that are compared with each other
 constexpr int kMaxCluster = 16;
 constexpr int kUnit = 44;        // weights are in units of 2^-44
@@ -63,6 +66,7 @@ struct Shared {
     uint64_t list[kList], near[kList], weight[kList];  // of a bin's tokens: this block's, the cluster's, their weights
     uint64_t ahead[kList];            // weights before a token, and how many tokens
     uint32_t rank[kList];
+    uint64_t segment[2 * kThreads];   // kept weights of kSegment logits
     uint64_t warp_sum[kWarps];
     uint64_t block_sum[2][kMaxCluster][2];
     float2 extremes[kWarps];
@@ -85,31 +89,52 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 __device__ __forceinline__ float logit_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
-// Eight logits as they are kept: NaN, which is never chosen, as -inf, and -0 as 0; their extremes go on.
-__device__ __forceinline__ void take8(float4 (&v)[2], float &top, float &low) {
-    float *x = reinterpret_cast<float *>(v);
+// Eight logits as they are kept: NaN, which is never chosen, as -inf, and -0 as 0; their extremes go on (low of what is
+// not -inf: x + (x - x) is NaN there, which a minimum passes over).
+struct Extremes32 {
+    float top = -INFINITY, low = INFINITY;
+    __device__ __forceinline__ void take(float4 (&v)[2]) {
+        float *x = reinterpret_cast<float *>(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = fmaxf(x[i], -INFINITY) + 0.0f;
-        top = fmaxf(top, x[i]);
-        if (x[i] > -INFINITY) low = fminf(low, x[i]);
+        for (int i = 0; i < 8; ++i) {
+            x[i] = fmaxf(x[i], -INFINITY) + 0.0f;
+            top = fmaxf(top, x[i]);
+            low = fminf(low, x[i] + (x[i] - x[i]));
+        }
     }
-}
-__device__ __forceinline__ void take8(uint4 (&v)[1], float &top, float &low) {
-    __half2 *x = reinterpret_cast<__half2 *>(v);
-    const __half2 none = __half2half2(__ushort_as_half(0xFC00u)), zero = __half2half2(__ushort_as_half(0));
+    __device__ __forceinline__ float2 get() const { return make_float2(top, low); }
+};
+struct Extremes16 {
+    __half2 top = __half2half2(__ushort_as_half(0xFC00u)), low = __half2half2(__ushort_as_half(0x7C00u));
+    __device__ __forceinline__ void take(uint4 (&v)[1]) {
+        __half2 *x = reinterpret_cast<__half2 *>(v);
+        const __half2 none = __half2half2(__ushort_as_half(0xFC00u)), zero = __half2half2(__ushort_as_half(0));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[i] = __hadd2(__hmax2(x[i], none), zero);
-        const float2 f = __half22float2(x[i]);
-        top = fmaxf(top, fmaxf(f.x, f.y));
-        if (f.x > -INFINITY) low = fminf(low, f.x);
-        if (f.y > -INFINITY) low = fminf(low, f.y);
+        for (int i = 0; i < 4; ++i) {
+            x[i] = __hadd2(__hmax2(x[i], none), zero);
+            top = __hmax2(top, x[i]);
+            low = __hmin2(low, __hadd2(x[i], __hsub2(x[i], x[i])));
+        }
     }
-}
+    __device__ __forceinline__ float2 get() const {
+        const float2 a = __half22float2(top), b = __half22float2(low);
+        return make_float2(fmaxf(a.x, a.y), fminf(b.x, b.y));
+    }
+};
 template <class T> struct Eight;
-template <> struct Eight<float> { float4 v[2]; };
-template <> struct Eight<__half> { uint4 v[1]; };
+template <> struct Eight<float> {
+    float4 v[2];
+    using Extremes = Extremes32;
+    __device__ __forceinline__ float2 pair(int i) const { return i & 1 ? make_float2(v[i >> 1].z, v[i >> 1].w) : make_float2(v[i >> 1].x, v[i >> 1].y); }
+};
+template <> struct Eight<__half> {
+    uint4 v[1];
+    using Extremes = Extremes16;
+    __device__ __forceinline__ float2 pair(int i) const {
+        const uint32_t w = i == 0 ? v[0].x : i == 1 ? v[0].y : i == 2 ? v[0].z : v[0].w;
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+};
 
 // exp((l - m) / T) but for a factor near 1 that all of a row's share, in units of 2^-44: 2^x for x = l c - M, c =
 // log2(e) / T in two floats and M the multiple of 1/64 next to m c, so that M costs no digits. Where m c is 128 or more,
@@ -131,38 +156,50 @@ struct Weigher {
         least = m == INFINITY ? INFINITY : high - 46.0f;
         all_of_it = m == INFINITY ? INFINITY : NAN;  // logits of infinity: 1 each, and nothing else
     }
-    __device__ __forceinline__ uint64_t operator()(float l) const {
-        const float a = l - base, xh = a * ch;
-        if (l == all_of_it) return kOne;
-        if (!(xh > least)) return 0;  // (-inf among them)
-        const float low = fmaf(a, cl, fmaf(a, ch, -xh));  // 2^-17 at most
+    // The weights of two logits, each high 2^22 + low units; live: whether there is one.
+    struct Pair { uint32_t high[2], low[2]; bool live[2]; };
+    __device__ __forceinline__ Pair pair(float2 l) const {
+        auto both = [](float x) { return make_float2(x, x); };
+        const float2 a = fadd2(l, both(-base)), xh = fmul2(a, both(ch));
+        const float2 low = ffma2(a, both(cl), ffma2(a, both(ch), fmul2(a, both(-ch))));  // 2^-17 at most
         // x = k / 64 + r + low, |r| <= 2^-7: r exact
-        const float km = fmaf(xh, 64.0f, magic);
-        const int k = static_cast<int>(__float_as_uint(km)) - 0x4B400000;
-        const float r = fmaf(km - magic, -0x1p-6f, xh);
+        const float2 km = ffma2(xh, both(64.0f), both(magic));
+        const float2 r = ffma2(fadd2(km, both(-magic)), both(-0x1p-6f), xh);
         // 2^(r + low) - 1 = u + rest, u = r ln 2 rounded (low's square, 2^-36 at most, is left out)
         const float ln2 = 0.693147182464599609375f, ln2_rest = -1.904654323148236e-9f;
-        const float u = r * ln2, low_ln2 = low * ln2;
-        const float p = fmaf(r, fmaf(r, fmaf(r, 1.3333558146e-3f, 9.6181291076e-3f), 5.5504108665e-2f), 2.4022650696e-1f);
-        const float r2 = r * r, rest = fmaf(r2, p, fmaf(low_ln2, fmaf(r2, p, u), fmaf(r, ln2_rest, fmaf(r, ln2, -u)) + low_ln2));
-        const float2 t = power[k & 63];
-        const float v = t.x * u;  // times t.x + t.y, the product by t.x in two parts
-        const float v_low = fmaf(t.x, u, -v) + fmaf(t.x, rest, fmaf(t.y, u, t.y));
-        // to whole units: v + v_low in units of 2^-28, the rest in 2^-44 (conversions by addition: the instruction is four times slower)
-        const float round = 12582912.0f, vi = fmaf(v + v_low, 0x1p28f, round);
-        const float ri = fmaf(fmaf(vi - round, -0x1p-28f, v) + v_low, 0x1p44f, round);
-        const int64_t part = static_cast<int64_t>(static_cast<int>(__float_as_uint(vi)) - 0x4B400000) * (1 << (kUnit - 28)) +
-                             (static_cast<int>(__float_as_uint(ri)) - 0x4B400000);
-        const uint64_t whole = static_cast<uint64_t>((__float_as_uint(t.x) & 0x7FFFFFu) | 0x800000u) * (1u << (kUnit - 23)) + part;
-        const int down = -(k >> 6);
-        return down <= 0 ? whole : (whole + (1ull << (down - 1))) >> down;
+        const float2 u = fmul2(r, both(ln2)), low_ln2 = fmul2(low, both(ln2)), minus_u = fmul2(r, both(-ln2)), r2 = fmul2(r, r);
+        const float2 p = ffma2(r, ffma2(r, ffma2(r, both(1.3333558146e-3f), both(9.6181291076e-3f)), both(5.5504108665e-2f)), both(2.4022650696e-1f));
+        const float2 u_rest = fadd2(ffma2(r, both(ln2_rest), ffma2(r, both(ln2), minus_u)), low_ln2);
+        const float2 rest = ffma2(r2, p, ffma2(low_ln2, ffma2(r2, p, u), u_rest));
+        // times 2^(k / 64) = t + t_low, the product by t in two parts (the exponent: k / 64's whole part, added to 1's)
+        const uint32_t k0 = __float_as_uint(km.x), k1 = __float_as_uint(km.y);
+        const float2 t0 = power[k0 & 63], t1 = power[k1 & 63];
+        const float2 scale = make_float2(__uint_as_float(((k0 & ~63u) << 17) + 0x3F800000u), __uint_as_float(((k1 & ~63u) << 17) + 0x3F800000u));
+        const float2 t = fmul2(make_float2(t0.x, t1.x), scale), t_low = fmul2(make_float2(t0.y, t1.y), scale);
+        const float2 v = fmul2(t, u), v_low = fadd2(ffma2(t, u, fmul2(t, minus_u)), ffma2(t, rest, ffma2(t_low, u, t_low)));
+        // to whole numbers, by additions that leave them in the last bits
+        const float whole = 8388608.0f, half = 12582912.0f;
+        const float2 h = ffma2(fadd2(t, fadd2(v, v_low)), both(0x1p22f), both(whole));
+        const float2 left = fadd2(fadd2(ffma2(fadd2(h, both(-whole)), both(-0x1p-22f), t), v), v_low);
+        const float2 g = ffma2(left, both(0x1p44f), both(half));
+        return Pair{{__float_as_uint(h.x) - 0x4B000000u, __float_as_uint(h.y) - 0x4B000000u},
+                    {__float_as_uint(g.x) - 0x4B400000u, __float_as_uint(g.y) - 0x4B400000u},
+                    {xh.x > least, xh.y > least}};  // (not of -inf)
+    }
+    __device__ __forceinline__ static uint64_t weight(uint32_t high, uint32_t low) {
+        return (static_cast<uint64_t>(high) << 22) + static_cast<int64_t>(static_cast<int32_t>(low));
+    }
+    __device__ __forceinline__ uint64_t operator()(float l) const {
+        if (l == all_of_it) return kOne;
+        const Pair w = pair(make_float2(l, l));
+        return w.live[0] ? weight(w.high[0], w.low[0]) : 0;
     }
 };
 
-// The bin of a histogram of m - l.
-__device__ __forceinline__ uint32_t bin_of(float l, float m, float scale) {
-    return min(static_cast<uint32_t>(max(__float2int_rz((m - l) * scale), 0)), kBins - 1u);
-}
+// The place in a histogram of m - l, and its bin (NaN, of two infinities: 0).
+__device__ __forceinline__ float place_in_bins(float l, float m, float scale) { return fminf(fmaxf((m - l) * scale, 0.0f), kBins - 1.0f); }
+__device__ __forceinline__ uint32_t bin_of_place(float x) { return __float_as_uint(__fadd_rz(x, 8388608.0f)) & (kBins - 1u); }
+__device__ __forceinline__ uint32_t bin_of(float l, float m, float scale) { return bin_of_place(place_in_bins(l, m, scale)); }
 
 // floor(v f) for 0 <= f <= 1, exact, and whether it was cut off.
 __device__ __forceinline__ uint64_t times(uint64_t v, float f, bool &rest) {
@@ -207,25 +244,26 @@ struct Target {  // of a sum's share
     }
 };
 
-// Tokens that are searched: a row in the cluster's shared memory, a contiguous slice a block and part of it a warp ...
+// Tokens that are searched: a row in the cluster's shared memory, a contiguous slice a block ...
 template <class T> struct RowTokens {
     static constexpr bool kSent = false;
     Shared *s;
-    const T *data;             // this block's slice
-    int first, count, part;    // its first index and size; a warp's part of it (a multiple of 64)
+    const T *data;             // this block's slice: sets of kSet, what lies before and behind it in the first and last is -inf
+    int first, sets;           // the index of the first set's first place; sets
     int rank, blocks;
-    __device__ __forceinline__ float logit(int i) const { return static_cast<float>(data[i]); }
+    using Type = T;
+    __device__ __forceinline__ Eight<T> set(int i) const { return *reinterpret_cast<const Eight<T> *>(data + kSet * i); }
     template <class F> __device__ __forceinline__ void each(F f) const {  // f(logit, index)
-        const int lane = threadIdx.x & 31, from = (threadIdx.x >> 5) * part;
-        const int to = min(from + part, count);
+        for (int i = threadIdx.x; i < sets; i += kRowSets) {
 #pragma unroll 2
-        for (int i = from + lane; i < to; i += 32) f(logit(i), first + i);
+            for (int j = kSet * i; j < kSet * i + kSet; ++j) f(static_cast<float>(data[j]), first + j);
+        }
     }
 };
 // ... or those sent to the first block, n in any order, by that block alone.
 struct SentTokens {
     static constexpr bool kSent = true;
-    [[maybe_unused]] static constexpr int first = 0, count = 0, part = 0, rank = 0, blocks = 1;
+    static constexpr int first = 0, rank = 0, blocks = 1;
     Shared *s;
     int n, index_bits;         // log2 of the indexes that share a bin
     template <class F> __device__ __forceinline__ void each(F f) const {
@@ -237,7 +275,7 @@ struct SentTokens {
 };
 
 template <class Tokens> struct Search : Tokens {
-    using Tokens::s, Tokens::first, Tokens::count, Tokens::part, Tokens::rank, Tokens::blocks, Tokens::each;
+    using Tokens::s, Tokens::first, Tokens::rank, Tokens::blocks, Tokens::each;
     int turn = 0;              // which of the two sums' places is next
 
     __device__ __forceinline__ void join() const {  // the whole cluster
@@ -315,61 +353,90 @@ template <class Tokens> struct Search : Tokens {
             __syncthreads();
             return whole;
         } else {
-            uint64_t mine = 0;
-            each([&](float l, int i) { mine += value(l, i); });
-            const Sums r = sums(mine, ~0ull);
-            const uint64_t t = target(r.all);
-            if (r.before < t && t <= r.before + r.mine) {  // in this block: it goes through the one warp's part again
-                uint64_t before = r.before;
-                int w = 0;
-                while (t > before + s->warp_sum[w]) before += s->warp_sum[w++];
-                __syncthreads();
-                const int from = w * part, to = min(from + part, count), per = (part + kThreads - 1) / kThreads;
-                const int i0 = from + per * threadIdx.x, i1 = min(i0 + per, to);
+            for_segments([&](int i) {
                 uint64_t sum = 0;
-                for (int i = i0; i < i1; ++i) sum += value(this->logit(i), first + i);
-                const uint64_t up_to = warp_prefix(sum);
-                if ((threadIdx.x & 31) == 31) s->warp_sum[threadIdx.x >> 5] = up_to;
-                __syncthreads();
-                before += up_to - sum;
-                for (int v = 0; v < (threadIdx.x >> 5); ++v) before += s->warp_sum[v];
-                if (before < t && t <= before + sum)
-                    for (int i = i0; i < i1; ++i) {
-                        const uint64_t v = value(this->logit(i), first + i);
-                        before += v;
-                        if (before >= t) {
-                            for (int b = 0; b < blocks; ++b) {
-                                auto *f = at(&s->found, b);
-                                f->place = first + i, f->value = v;
-                            }
-                            break;
-                        }
-                    }
-            }
-            join();
-            return r.all;
+                const Eight<typename Tokens::Type> e = this->set(i);
+#pragma unroll
+                for (int j = 0; j < kSet; ++j) sum += value(j & 1 ? e.pair(j >> 1).y : e.pair(j >> 1).x, first + kSet * i + j);
+                return sum;
+            });
+            return choose_segment(value, target);
         }
+    }
+    // f(set) of each set of this block, summed up by segments.
+    template <class F> __device__ __forceinline__ void for_segments(F f) {
+        int place = threadIdx.x >> 5;
+        for (int i0 = 0; i0 < this->sets; i0 += kRowSets, place += kWarps) {
+            const int i = i0 + threadIdx.x;
+            const uint64_t sum = warp_total(i < this->sets ? f(i) : 0);
+            if ((threadIdx.x & 31) == 0) s->segment[place] = sum;
+        }
+    }
+    // select, once the segments' sums are there.
+    template <class V, class G> __device__ __forceinline__ uint64_t choose_segment(V value, G target) {
+        __syncthreads();
+        const int segments = (this->sets + kRowSets - 1) / kRowSets * kWarps;
+        uint64_t v[2];
+        const uint32_t n[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = 2 * threadIdx.x + i < segments ? s->segment[2 * threadIdx.x + i] : 0;
+        const Sums r = sums(v[0] + v[1], ~0ull);
+        const uint64_t t = target(r.all);
+        if (r.before < t && t <= r.before + r.mine) {  // in this block
+            find_bin(v, n, false, t - r.before);
+            __syncthreads();
+            const int from = s->found.place * kSegment;
+            const uint64_t before = s->found.before;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = from + 2 * threadIdx.x + i;
+                v[i] = 2 * threadIdx.x + i < kSegment && j < kSet * this->sets ? value(static_cast<float>(this->data[j]), first + j) : 0;
+            }
+            find_bin(v, n, false, t - r.before - before);
+            __syncthreads();
+            const uint32_t place = s->found.place;
+            if (threadIdx.x == place >> 1)
+                for (int b = 0; b < blocks; ++b) {
+                    auto *f = at(&s->found, b);
+                    f->value = v[place & 1], f->place = first + from + place;
+                }
+        }
+        join();
+        return r.all;
     }
     __device__ __forceinline__ void clear_bins() {
         for (int b = threadIdx.x; b < kBins; b += kThreads) s->sum[b] = 0, s->count[b] = 0;
     }
-    // The cluster's counts (sums) of this thread's two bins.
-    __device__ __forceinline__ void bin_counts(uint32_t (&n)[2]) const {
-        n[0] = n[1] = 0;
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-            const uint2 c = *reinterpret_cast<const uint2 *>(at(s->count, b) + 2 * threadIdx.x);
-            n[0] += c.x, n[1] += c.y;
-        }
-    }
-    __device__ __forceinline__ void bin_sums(uint64_t (&v)[2]) const {
+    // The cluster's counts (sums) of this thread's two bins: up to eight blocks' on their way at once.
+    template <class P> __device__ __forceinline__ void gather(uint64_t (&v)[2], const P *p) const {
         v[0] = v[1] = 0;
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(at(s->sum, b) + 2 * threadIdx.x);
-            v[0] += c.x, v[1] += c.y;
+        for (int b0 = 0; b0 < blocks; b0 += 8) {
+            P c[8][2];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                c[q][0] = c[q][1] = 0;
+                if (b0 + q < blocks) {
+                    const P *there = at(p, b0 + q) + 2 * threadIdx.x;
+                    if constexpr (sizeof(P) == 4) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(there);
+                        c[q][0] = x.x, c[q][1] = x.y;
+                    } else {
+                        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(there);
+                        c[q][0] = x.x, c[q][1] = x.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[0] += c[q][0], v[1] += c[q][1];
         }
     }
+    __device__ __forceinline__ void bin_counts(uint32_t (&n)[2]) const {
+        uint64_t v[2];
+        gather(v, s->count);
+        n[0] = static_cast<uint32_t>(v[0]), n[1] = static_cast<uint32_t>(v[1]);
+    }
+    __device__ __forceinline__ void bin_sums(uint64_t (&v)[2]) const { gather(v, s->sum); }
     // Bins of a histogram, each thread two neighbours, `rising`: counted from the last one: where the running sum of v
     // reaches `target`; found: the bin, the sum before it, and its n (left as it was where the sum does not). Every
     // thread of every block calls it, with a barrier before found is read.
@@ -392,21 +459,31 @@ template <class Tokens> struct Search : Tokens {
             before += v[b];
         }
     }
-    // Tokens for which take(logit) holds are sent to the first block, as far as there is room.
-    template <class F> __device__ __forceinline__ void send(F take) {
-        const int lane = threadIdx.x & 31, from = (threadIdx.x >> 5) * part, to = min(from + part, count);
+    // Tokens from logit `least` on (not -inf) for which take(logit) holds are sent to the first block, as far as there is room.
+    template <class F> __device__ __forceinline__ void send(float least, F take) {
         uint64_t *const there = at(s->all, 0);
         uint32_t *const counter = at(&s->list_count, 0);
-        for (int i0 = from; i0 < to; i0 += 32) {
-            const int i = i0 + lane;
-            const float l = i < to ? this->logit(i) : -INFINITY;
-            const bool in = i < to && take(l);
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
+        for (int i = threadIdx.x; i < this->sets; i += kRowSets) {
+            const Eight<typename Tokens::Type> e = this->set(i);
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kSet / 2; ++j) most = fmaxf(fmaxf(most, e.pair(j).x), e.pair(j).y);
+            if (!(most >= least) || most == -INFINITY) continue;
+            uint32_t who = 0;
+#pragma unroll
+            for (int j = 0; j < kSet; ++j) {
+                const float l = j & 1 ? e.pair(j >> 1).y : e.pair(j >> 1).x;
+                if (l >= least && l > -INFINITY && take(l)) who |= 1u << j;
+            }
             if (who == 0) continue;
-            uint32_t place = 0;
-            if (lane == 0) place = atomicAdd(counter, static_cast<uint32_t>(__popc(who)));
-            place = __shfl_sync(0xffffffffu, place, 0) + __popc(who & ((1u << lane) - 1));
-            if (in && place < kCap) there[place] = static_cast<uint64_t>(key_of(l)) << 32 | ~static_cast<uint32_t>(first + i);
+            uint32_t place = atomicAdd(counter, static_cast<uint32_t>(__popc(who)));
+#pragma unroll
+            for (int j = 0; j < kSet; ++j)
+                if (who >> j & 1) {
+                    if (place < kCap)
+                        there[place] = static_cast<uint64_t>(key_of(j & 1 ? e.pair(j >> 1).y : e.pair(j >> 1).x)) << 32 | ~static_cast<uint32_t>(first + kSet * i + j);
+                    ++place;
+                }
         }
     }
     // The border at which the running value (1, or the weight) over the tokens up to `limit`, in falling order,
@@ -515,6 +592,19 @@ template <class Tokens> struct Search : Tokens {
     }
 };
 
+// The weights' sum of a set (no logit of infinity).
+template <class T> __device__ __forceinline__ uint64_t weigh_set(const Eight<T> &e, const Weigher &weigh) {
+    uint32_t high = 0, low = 0;
+#pragma unroll
+    for (int j = 0; j < kSet / 2; ++j) {
+        const Weigher::Pair w = weigh.pair(e.pair(j));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (w.live[i]) high += w.high[i], low += w.low[i];
+    }
+    return Weigher::weight(high, low);
+}
+
 enum Todo { kNothing, kSelect, kTopP, kAll };
 
 // The filters that `todo` leaves open, by a search each, and the token.
@@ -523,6 +613,7 @@ template <class Tokens>
 __device__ __forceinline__ Chosen search_all(Search<Tokens> &search, int todo, Border last, int top_k, float top_p, float min_p, float u,
                                              float t, int vocab, float m, float scale, const Weigher &weigh) {
     auto kept = [&](float l, int i) {
+        if (last.key == 0) return true;
         const uint32_t key = key_of(l);
         return key > last.key || (key == last.key && static_cast<uint32_t>(i) <= last.index);
     };
@@ -539,13 +630,23 @@ __device__ __forceinline__ Chosen search_all(Search<Tokens> &search, int todo, B
         last = search.template border<true>(last, Target::share(all, top_p), m, scale, reach, weigh);
     }
     const uint64_t light = min_p > 0.0f ? Target::share(weigh(weigh.m), min_p) : 0;
-    const uint64_t all = search.select(
-        [&](float l, int i) -> uint64_t {
-            if (!kept(l, i)) return 0;
-            const uint64_t w = weigh(l);
-            return w >= light ? w : 0;
-        },
-        [&](uint64_t all) { return Target::draw(all, u); });
+    auto value = [&](float l, int i) -> uint64_t {
+        if (!kept(l, i)) return 0;
+        const uint64_t w = weigh(l);
+        return w >= light ? w : 0;
+    };
+    auto target = [&](uint64_t all) { return Target::draw(all, u); };
+    uint64_t all;
+    if constexpr (!Tokens::kSent) {
+        if (last.key == 0 && light == 0 && weigh.m < INFINITY) {  // all of them: the weights two by two
+            search.for_segments([&](int i) { return weigh_set(search.set(i), weigh); });
+            all = search.choose_segment(value, target);
+        } else {
+            all = search.select(value, target);
+        }
+    } else {
+        all = search.select(value, target);
+    }
     return Chosen{static_cast<int32_t>(search.s->found.place), static_cast<float>(search.s->found.value) / static_cast<float>(all)};
 }
 
@@ -604,9 +705,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     row.s = s;
     row.blocks = p.blocks;
     row.rank = static_cast<int>(blockIdx.x % p.blocks);
-    row.part = p.part;
-    row.first = row.rank * kWarps * p.part;
-    row.count = max(0, min(p.vocab - row.first, kWarps * p.part));
     if (threadIdx.x < 64) s->power[threadIdx.x] = p.power[threadIdx.x];
     if (threadIdx.x == 0) s->list_count = 0;
     row.clear_bins();
@@ -623,31 +721,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (!(min_p > 0.0f)) min_p = 0.0f;
 
     // ---- the row, as far from a boundary of eight elements here as there
-    const T *const src = static_cast<const T *>(p.logits) + r * p.stride + row.first;
+    const int slice0 = row.rank * p.slice, count = max(0, min(p.vocab - slice0, p.slice));
+    const T *const src = static_cast<const T *>(p.logits) + r * p.stride + slice0;
     const int pad = static_cast<int>(reinterpret_cast<uintptr_t>(src) / sizeof(T) & 7u);
-    row.data = space + pad;
-    float top = -INFINITY, low = INFINITY;
-    constexpr int kAhead = sizeof(T) == 4 ? 4 : 8;  // sets of eight that a thread has under way
-    for (int i0 = 8 * threadIdx.x - pad; i0 < row.count; i0 += 8 * kThreads * kAhead) {
+    row.data = space;
+    row.first = slice0 - pad;
+    row.sets = count > 0 ? (pad + count + kSet - 1) / kSet : 0;
+    typename Eight<T>::Extremes extremes;
+    constexpr int kAhead = sizeof(T) == 4 ? 4 : 8;  // sets that a thread has under way
+    for (int i0 = threadIdx.x; i0 < row.sets; i0 += kRowSets * kAhead) {
         Eight<T> e[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + 8 * kThreads * k;
-            if (i >= 0 && i + 8 <= row.count) {
+            const int i = kSet * (i0 + kRowSets * k) - pad;
+            if (i >= 0 && i + kSet <= count) {
                 e[k] = *reinterpret_cast<const Eight<T> *>(src + i);
             } else {
                 T *x = reinterpret_cast<T *>(&e[k]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = i + j >= 0 && i + j < row.count ? src[i + j] : static_cast<T>(-INFINITY);
+                for (int j = 0; j < kSet; ++j) x[j] = i + j >= 0 && i + j < count ? src[i + j] : static_cast<T>(-INFINITY);
             }
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + 8 * kThreads * k;
-            take8(e[k].v, top, low);
-            if (i < row.count) *reinterpret_cast<Eight<T> *>(space + pad + i) = e[k];
+            extremes.take(e[k].v);
+            if (i0 + kRowSets * k < row.sets) *reinterpret_cast<Eight<T> *>(space + kSet * (i0 + kRowSets * k)) = e[k];
         }
     }
+    float top = extremes.get().x, low = extremes.get().y;
     const float mine_top = top;
 #pragma unroll
     for (int m = 16; m; m >>= 1) {
@@ -676,9 +777,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     } else if (!(t >= kLeastTemperature) || top_k == 1 || top_p <= 0.0f || min_p > 1.0f) {  // the first alone
         uint32_t first = 0xFFFFFFFFu;
         if (mine_top == top)
-            for (int i0 = 8 * threadIdx.x - pad; i0 < row.count && first == 0xFFFFFFFFu; i0 += 8 * kThreads)
-                for (int i = max(i0, 0); i < min(i0 + 8, row.count); ++i)
-                    if (first == 0xFFFFFFFFu && row.logit(i) == top) first = row.first + i;
+            row.each([&](float l, int i) {
+                if (l == top && first == 0xFFFFFFFFu) first = i;
+            });
         first = __reduce_min_sync(0xffffffffu, first);
         if (lane == 0 && first != 0xFFFFFFFFu)  // (list_count holds 0 less 1 less the least index so far)
             for (int b = 0; b < row.blocks; ++b) atomicMax(row.at(&s->list_count, b), 0u - 1u - first);
@@ -692,10 +793,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         // bins per unit of m - l, a power of two, over so much
         auto bins_over = [&](float most) { return __uint_as_float(__float_as_uint((kBins - 1) / fminf(fmaxf(top - low, 0x1p-100f), most)) & 0x7F800000u); };
         const bool by_weight = top_k == 0 && top_p < 1.0f;
-        const float scale = bins_over(by_weight ? fminf(32.0f * t, FLT_MAX) : kRange);
+        const float scale = bins_over(by_weight ? fminf(31.0f * t, FLT_MAX) : kRange);
         const int index_bits = max(0, 22 - __clz(p.vocab - 1));  // of an index, but the highest ten
-        if (top_k > 0 ? top_k <= kThreads * row.blocks : top_p == 1.0f && min_p > 0.0f) {
-            // ---- a cut that as many tokens reach, by the threads' own largest, or that min_p gives
+        if (top_k > 0 ? top_k <= kThreads / 2 * row.blocks : top_p == 1.0f && min_p > 0.0f) {
+            // ---- a cut that as many tokens reach, by the threads' own largest (about half as many again where half of the
+            // threads have one), or that min_p gives
             uint32_t last_bin = 0;
             if (top_k > 0) {
                 if (mine_top > -INFINITY) atomicAdd(&s->count[bin_of(mine_top, top, scale)], 1u);
@@ -709,7 +811,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 last_bin = s->found.place;
             }
             const float reach = top == INFINITY ? 0.0f : top + (log2f(min_p) - 0.02f) * t * 0.694f - 1e-6f * fabsf(top);  // (of min_p alone)
-            row.send([&](float l) { return top_k > 0 ? bin_of(l, top, scale) <= last_bin : l > reach; });
+            // (the bins are half open, and their ends and places rounded: a little more is sent)
+            const float cut = top_k == 0 ? reach : last_bin == kBins - 1 || top == INFINITY ? -INFINITY : top - (last_bin + 1.01f) / scale - 1e-6f * fabsf(top);
+            row.send(cut, [](float) { return true; });
             row.join();
             const uint32_t n = *row.at(&s->list_count, 0);
             if (n <= kCap) {  // the first block goes on alone, in its own memory, and stays until the others have read it
@@ -729,15 +833,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             row.clear_bins();
             if (threadIdx.x == 0) s->list_count = 0, s->found.place = kBins - 1;
             row.join();
-            // s->sum: what a bin's tokens weigh less than its first possible one, in 2^-16 of that
+            // s->sum: what a bin's tokens weigh less than its first possible one, in 2^-16 of that, in 32 bits (atomics of 64
+            // are loops: 292 us instead of 219 with the count in the high bits, 256 rows of 130001, top_p 0.5). Tokens of
+            // -inf are in no bin: with 64 rows, some of them masked, their one bin's atomics took half of the time.
             const float per_bin = weigh.ch / scale;  // log2 of the weights' ratio over a bin, 0.1 at most
             row.each([&](float l, int) {
-                const uint32_t b = bin_of(l, top, scale);
+                const float x = place_in_bins(l, top, scale);
+                const uint32_t b = bin_of_place(x);
+                if (l == -INFINITY) return;
                 atomicAdd(&s->count[b], 1u);
                 if (by_weight && b + 1 < kBins) {
                     float y;
-                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(((top - l) * scale - b) * -per_bin));
-                    atomicAdd(reinterpret_cast<uint32_t *>(&s->sum[b]), static_cast<uint32_t>(__float2int_rn((1.0f - y) * 65536.0f)));
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - (__fadd_rz(x, 8388608.0f) - 8388608.0f)) * -per_bin));
+                    atomicAdd(reinterpret_cast<uint32_t *>(&s->sum[b]), __float_as_uint(fmaf(1.0f - y, 65536.0f, 12582912.0f)) - 0x4B400000u);
                 }
             });
             row.join();
@@ -784,36 +892,74 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const uint64_t both = row.block_total(static_cast<uint64_t>(above) << 32 | in);
             above = static_cast<uint32_t>(both >> 32), in = static_cast<uint32_t>(both);
             if (in <= kCap) {
-                uint64_t before = 0, after = 0;
-                row.send([&](float l) {
+                uint64_t before = 0, all = 0;  // weights of the bins before these, and of all
+                uint64_t target = top_k - above;
+                row.send(-INFINITY, [&](float l) {
                     const uint32_t b = bin_of(l, top, scale);
-                    if (by_weight) {
-                        const uint64_t w = weigh(l);
-                        if (b < bin_lo) before += w;
-                        else after += w;
-                    }
                     return b >= bin_lo && b <= bin_hi;
                 });
-                uint64_t target = top_k - above;
                 if (by_weight) {
-                    const auto sums = row.sums(before, after);
-                    target = Target::share(sums.all + sums.all2, top_p) - sums.all;
+                    row.for_segments([&](int i) {
+                        const Eight<T> e = row.set(i);
+                        uint32_t high[2] = {0, 0}, low[2] = {0, 0};  // of the bins before these, and from them on
+                        uint64_t infinite = 0;
+#pragma unroll
+                        for (int j = 0; j < kSet / 2; ++j) {
+                            const float2 l = e.pair(j);
+                            const Weigher::Pair w = weigh.pair(l);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const bool ahead = bin_of(q ? l.y : l.x, top, scale) < bin_lo;
+                                if (w.live[q] && ahead) high[0] += w.high[q], low[0] += w.low[q];
+                                if (w.live[q] && !ahead) high[1] += w.high[q], low[1] += w.low[q];
+                                if ((q ? l.y : l.x) == weigh.all_of_it) infinite += kOne;
+                            }
+                        }
+                        const uint64_t first = Weigher::weight(high[0], low[0]);
+                        before += first, all += first + Weigher::weight(high[1], low[1]) + infinite;
+                        return first;
+                    });
+                    const auto sums = row.sums(before, all);
+                    target = Target::share(sums.all2, top_p) - sums.all;
                 } else {
                     row.join();
                 }
                 if (row.rank == 0) {
                     // finer bins from the first one's edge on (what lies a rounding above it counts as in the first)
                     const float edge = top == INFINITY ? top : top - bin_lo / scale, finer = scale * __uint_as_float((127u + __clz(bin_hi - bin_lo) - 22u) << 23);
-                    const Border b = by_weight ? border_of_sent<true>(s, in, index_bits, target, edge, finer, weigh)
-                                               : border_of_sent<false>(s, in, index_bits, target, edge, finer, weigh);
+                    const uint32_t n = s->list_count;  // (tokens of -inf are in no list; where the border lies among them, all others stay)
+                    Border b{key_of(-INFINITY), 0xFFFFFFFFu};
+                    if (by_weight) b = border_of_sent<true>(s, n, index_bits, target, edge, finer, weigh);
+                    else if (target <= n) b = border_of_sent<false>(s, n, index_bits, target, edge, finer, weigh);
                     __syncthreads();
                     if (threadIdx.x < row.blocks) row.at(&s->found, threadIdx.x)->value = static_cast<uint64_t>(b.key) << 32 | b.index;
                 }
                 row.join();
                 last = Border{static_cast<uint32_t>(s->found.value >> 32), static_cast<uint32_t>(s->found.value)};
                 todo = !by_weight && top_p < 1.0f ? kTopP : kSelect;
+                if (by_weight && min_p == 0.0f) {
+                    // the segments' sums lack only the bins' tokens that stay
+                    auto kept = [&](float l, int i) {
+                        const uint32_t key = key_of(l);
+                        return key > last.key || (key == last.key && static_cast<uint32_t>(i) <= last.index);
+                    };
+                    for (int i = threadIdx.x; i < row.sets; i += kRowSets) {
+                        const Eight<T> e = row.set(i);
+                        const float lowest = logit_of(last.key);
+#pragma unroll
+                        for (int j = 0; j < kSet; ++j) {
+                            const float l = j & 1 ? e.pair(j >> 1).y : e.pair(j >> 1).x;
+                            if (l >= lowest && bin_of(l, top, scale) >= bin_lo && kept(l, row.first + kSet * i + j))
+                                atomicAdd(reinterpret_cast<unsigned long long *>(&s->segment[i >> 5]), static_cast<unsigned long long>(weigh(l)));
+                        }
+                    }
+                    const uint64_t sum = row.choose_segment([&](float l, int i) -> uint64_t { return kept(l, i) ? weigh(l) : 0; },
+                                                            [&](uint64_t all) { return Target::draw(all, u); });
+                    chosen = Chosen{static_cast<int32_t>(s->found.place), static_cast<float>(s->found.value) / static_cast<float>(sum)};
+                    todo = kNothing;
+                }
             }
-            row.join();  // (the memory is used again)
+            if (todo != kNothing) row.join();  // (the memory is used again)
         }
         if (todo != kNothing) chosen = search_all(row, todo, last, top_k, top_p, min_p, u, t, p.vocab, top, bins_over(kRange), weigh);
     }
@@ -823,8 +969,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
 }
 
-template <class T> int slice_smem(int part) {
-    return (static_cast<int>(sizeof(Shared)) + 31) / 32 * 32 + (kWarps * part + 16) * static_cast<int>(sizeof(T));
+template <class T> int slice_smem(int slice) {
+    return (static_cast<int>(sizeof(Shared)) + 31) / 32 * 32 + (slice + 2 * kSet) * static_cast<int>(sizeof(T));
 }
 
 template <class T> cudaError_t launch(SampleParams p, int n, int sms, int device, cudaStream_t s) {
@@ -837,16 +983,16 @@ template <class T> cudaError_t launch(SampleParams p, int n, int sms, int device
         done.fetch_or(bit, std::memory_order_acq_rel);
     }
     // blocks of a row: as many as its size asks for, and more while there are multiprocessors without a row
-    auto part = [&](int blocks) { return (p.vocab + 64 * kWarps * blocks - 1) / (64 * kWarps * blocks) * 64; };
+    auto slice = [&](int blocks) { return (p.vocab + kSet * blocks - 1) / (kSet * blocks) * kSet; };
     p.blocks = 1;
     while (p.blocks < kMaxCluster &&
-           (slice_smem<T>(part(p.blocks)) > kSmemLimit / 2 || (static_cast<int64_t>(n) * p.blocks <= sms && part(p.blocks) >= 256 && p.blocks < 8)))
+           (slice_smem<T>(slice(p.blocks)) > kSmemLimit / 2 || (static_cast<int64_t>(n) * p.blocks <= sms && slice(p.blocks) > 4096 && p.blocks < 8)))
         p.blocks *= 2;
-    p.part = part(p.blocks);
+    p.slice = slice(p.blocks);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n) * p.blocks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = slice_smem<T>(p.part);
+    cfg.dynamicSmemBytes = slice_smem<T>(p.slice);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -15,7 +15,7 @@ struct SampleParams {
     float *prob;
     int64_t stride;
     int vocab;
-    int blocks, part;  // of a row; logits of a warp (the launch's choice)
+    int blocks, slice;  // of a row; logits of a block (the launch's choice)
     float2 power[64];  // (the launch's)
 };
 
