@@ -432,7 +432,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    pdl_wait_prior_grids();
+    // With p.rest the kernel before does not write what this one reads: it has waited for what came before, and this
+    // one's blocks may run beside it; they wait for its end before their own, so that what comes next finds both done.
+    if (p.rest == nullptr) pdl_wait_prior_grids();
     pdl_allow_dependents();
     __syncthreads();
     const Place place = p.n_seq <= 32 ? locate_few(p, ROWS, blockIdx.x, gridDim.x) : locate<kThreads>(p, ROWS, blockIdx.x, gridDim.x);
@@ -442,7 +444,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
     Cut *const cut = reinterpret_cast<Cut *>(p.partial) + blockIdx.x;
     float *const parts = p.partial + kCutFloats;
     if (threadIdx.x == 0) cut->parts = 0;
-    if (units <= 0) return;
+    if (units <= 0) {
+        if (p.rest != nullptr) pdl_wait_prior_grids();
+        return;
+    }
     Walk walk;
     walk.start(p, place, ROWS, units);
 
@@ -526,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                                    static_cast<uint32_t>((k / Sh::kSlots) & 1)))
                 record_error(p.err, kErrDrainWait);
         if (seg > 0 && !mbar_wait_bounded(qfull, (seg - 1) & 1)) record_error(p.err, kErrDrainWait);
+        if (p.rest != nullptr) pdl_wait_prior_grids();
         return;
     }
 
@@ -937,10 +943,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, (sizeof(T) == 4 ? 2 : 1
                 }
                 if (!to_out && threadIdx.x % kPer == 0) store2(part_stats, top, den);
             }
-            if (!whole && from && threadIdx.x == 0) {  // (thread 0 wrote the 0 above)
-                const int row0 = seg.rt * ROWS;
-                *cut = Cut{1 + static_cast<int>((seg.tiles - units + place.share - 1) / place.share),
-                           min(ROWS, seg.q.m * p.group - row0), row0, seg.q.q0, seg.head, {0, 0, 0}};
+            if (!whole && from) {
+                const int row0 = seg.rt * ROWS, n_parts = 1 + static_cast<int>((seg.tiles - units + place.share - 1) / place.share);
+                if (threadIdx.x == 0)  // (thread 0 wrote the 0 above)
+                    *cut = Cut{n_parts, min(ROWS, seg.q.m * p.group - row0), row0, seg.q.q0, seg.head, {0, 0, 0}};
+                if (p.rest != nullptr && out_row >= 0 && threadIdx.x % kPer == 0)
+                    store2(p.rest_stats + 2 * static_cast<int64_t>(out_row), __int_as_float(static_cast<int>(blockIdx.x)), -static_cast<float>(n_parts));
             }
         }
         // The join's areas are written again after the next segment's first barrier, which comes after these reads; its
@@ -1032,13 +1040,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvAttend
             }
             const int row = cut.row0 + r, tok = row / p.group;
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-            const int64_t out_row = static_cast<int64_t>(cut.q0 + tok) * p.n_heads + cut.head * p.group + row - tok * p.group;
-            if (p.rest == nullptr) {
-                store2(static_cast<T *>(p.out) + out_row * D + d, sum.x * inv, sum.y * inv);
-            } else {
-                store2(p.rest + out_row * D + d, sum.x, sum.y);
-                if (d == 0) store2(p.rest_stats + 2 * out_row, top, den);
-            }
+            store2(static_cast<T *>(p.out) +
+                       (static_cast<int64_t>(cut.q0 + tok) * p.n_heads + cut.head * p.group + row - tok * p.group) * D + d,
+                   sum.x * inv, sum.y * inv);
         }
         __syncthreads();  // sums and stats are the next row's
     }
@@ -1079,7 +1083,7 @@ template <int D, class T, int NT> cudaError_t launch(const KvAttendParams &p, in
     int ctas = sms * Sh::kCtas;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     cudaError_t e = launch_pdl(kv_attend_kernel<D, T, NT>, ctas, kThreads, Sh::kSmem, s, p);
-    if (e != cudaSuccess || ctas == 1) return e;
+    if (e != cudaSuccess || ctas == 1 || p.rest != nullptr) return e;
     const int64_t rows = static_cast<int64_t>(p.max_q_len) * p.group;
     return launch_join(kv_join_kernel<D, T, NT>, dim3(ctas - 1, static_cast<unsigned>(rows < kJoinRows ? rows : kJoinRows)), s, p);
 }
@@ -1092,6 +1096,11 @@ template <int D, class T> cudaError_t launch_rows(const KvAttendParams &p, int s
 }
 
 }  // namespace
+
+KvParts kv_attend_parts(int head_dim, int64_t rows) {
+    const int n = 8 * row_sets(rows);
+    return KvParts{kCutFloats, part_floats(head_dim, n), n};
+}
 
 size_t kv_attend_workspace(int head_dim, int rows) {
     return static_cast<size_t>(kCutFloats + 2 * kMaxCtas * part_floats(head_dim, 8 * row_sets(rows))) * sizeof(float);

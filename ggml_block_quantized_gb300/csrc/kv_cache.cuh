@@ -73,9 +73,19 @@ struct KvAttendParams {
     float scale;
     int n_seq, n_tok, n_heads, group, max_q_len;
     // Not null: instead of out, each row's values before the division, [n_tok][n_heads][D], and its reference (a power
-    // of 2) and sum, for a join with what it sees elsewhere.
+    // of 2) and sum, for a join with what it sees elsewhere; of a segment that thread blocks cut, instead the first
+    // block (as an integer's bits) and less than 0, the number of its parts: they lie as KvParts says. The kernel then
+    // runs beside the one before.
     float *rest, *rest_stats;
 };
+
+// Where the parts of a cut segment lie (floats): part 0 of block c at first + (2 c + 1) pitch, the others at first + 2
+// (c + i) pitch; a part is rows x D values and then the rows' references and sums. Row r of `rows`.
+struct KvParts {
+    int64_t first, pitch;
+    int rows;
+};
+KvParts kv_attend_parts(int head_dim, int64_t rows);
 
 size_t kv_attend_workspace(int head_dim, int rows);
 cudaError_t launch_kv_attend(const KvAttendParams &p, int head_dim, int type, int sms, int device, cudaStream_t s);
@@ -84,8 +94,9 @@ struct SharedParams {
     KvAttendParams own;           // of the sequences' own tokens
     const int32_t *prefix_table, *prefix_len;
     int64_t prefix_pages;
-    float *stretches;             // (the launch's)
+    float *stretches;             // (this and what follows: the launch's)
     int row_tiles;
+    KvParts parts;
 };
 
 size_t shared_attend_workspace(int head_dim, int n_kv_heads, int group, int64_t n_tok, int max_q_len);

@@ -644,11 +644,31 @@ template <int D, class T> __global__ void __launch_bounds__(kJoinThreads) shared
     for (int i = blockIdx.y; i < m; i += gridDim.y) {
         const int tok = q0 + i, row = tok * a.group + h - kv * a.group;
         const int64_t rest = static_cast<int64_t>(tok) * a.n_heads + h;
-        float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.rest_stats) + rest);
-        const float2 x = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel));
-        const float2 y = __ldcg(reinterpret_cast<const float2 *>(a.rest + rest * D + channel + 32));
-        float top = ml.x, den = ml.y;
-        float4 acc = make_float4(x.x, y.x, x.y, y.y);
+        const float2 own = __ldcg(reinterpret_cast<const float2 *>(a.rest_stats) + rest);
+        float top = -INFINITY, den = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        auto add = [&](float2 s, float4 v) {
+            const float next = fmaxf(top, s.x), ref = next == -INFINITY ? 0.0f : next;
+            const float keep = exp2_approx(top - ref), f = exp2_approx(s.x - ref);
+            top = next;
+            den = fmaf(den, keep, s.y * f);
+            acc.x = fmaf(acc.x, keep, v.x * f), acc.y = fmaf(acc.y, keep, v.y * f);
+            acc.z = fmaf(acc.z, keep, v.z * f), acc.w = fmaf(acc.w, keep, v.w * f);
+        };
+        auto of_own = [&](const float *row) {
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(row + channel)), y = __ldcg(reinterpret_cast<const float2 *>(row + channel + 32));
+            return make_float4(x.x, y.x, x.y, y.y);
+        };
+        if (own.y < 0.0f) {  // parts of thread blocks
+            const int c = __float_as_int(own.x), n = static_cast<int>(-own.y), in = (i * a.group + h - kv * a.group) % p.parts.rows;
+            const float *const first = a.partial + p.parts.first + (2 * static_cast<int64_t>(c) + 1) * p.parts.pitch;
+            for (int k = 0; k < n; ++k) {
+                const float *part = first + (k == 0 ? 0 : 2 * k - 1) * p.parts.pitch;
+                add(__ldcg(reinterpret_cast<const float2 *>(part + p.parts.rows * D) + in), of_own(part + in * D));
+            }
+        } else {
+            add(own, of_own(a.rest + rest * D));
+        }
         if (units.tiles > 0) {
             const int item = kv * p.row_tiles + row / kRows;
             const int64_t u = static_cast<int64_t>(item) * units.tiles;
@@ -666,12 +686,7 @@ template <int D, class T> __global__ void __launch_bounds__(kJoinThreads) shared
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
                     if (c + k >= n) break;
-                    const float next = fmaxf(top, s[k].x), ref = next == -INFINITY ? 0.0f : next;
-                    const float keep = exp2_approx(top - ref), f = exp2_approx(s[k].x - ref);
-                    top = next;
-                    den = fmaf(den, keep, s[k].y * f);
-                    acc.x = fmaf(acc.x, keep, v[k].x * f), acc.y = fmaf(acc.y, keep, v[k].y * f);
-                    acc.z = fmaf(acc.z, keep, v[k].z * f), acc.w = fmaf(acc.w, keep, v[k].w * f);
+                    add(s[k], v[k]);
                 }
             }
         }
@@ -738,6 +753,7 @@ cudaError_t launch_shared_attend(SharedParams p, int head_dim, int type, int sms
     at += align(rows * 8);
     p.stretches = reinterpret_cast<float *>(at);
     p.row_tiles = static_cast<int>(row_tiles(a.n_tok, a.group));
+    p.parts = kv_attend_parts(head_dim, static_cast<int64_t>(a.group) * a.max_q_len);
     if (head_dim == 64) return type == QG_F32 ? launch<64, float>(p, sms, device, s) : launch<64, __half>(p, sms, device, s);
     return type == QG_F32 ? launch<128, float>(p, sms, device, s) : launch<128, __half>(p, sms, device, s);
 }
