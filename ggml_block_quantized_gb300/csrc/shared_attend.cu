@@ -38,10 +38,15 @@ template <int D, int TERMS> struct Shape {
     static constexpr int kPart = kTokens * D * 2;              // one f16 part of a key, value or query tile
     static constexpr int kRawCodes = kTokens * D / 2;          // codes of a unit's keys (or values)
     static constexpr int kRaw = kRawCodes + kTokens * G::kScaleRow;
-    static constexpr int kSlots = TERMS == 2 && D == 128 ? 3 : 6;
-    // the queries (high parts on their way to tensor memory), keys, values: parts of 128-byte rows of 64 channels
-    static constexpr int kOffQ = 0, kOffK = TERMS * kPart, kOffV = kOffK + 2 * kPart;
-    static constexpr int kOffRaw = kOffV + 2 * kPart;
+    // Operands, in the order K(0), K(1), V(0), K(2), V(1) ..., each a high and a low part of 128-byte rows of 64
+    // channels: three places let them be made ready a piece ahead of the products (f32 queries leave room for two of
+    // heads of 128). The queries' high parts pass through the last place on their way to tensor memory, f32's low parts
+    // have one of their own.
+    static constexpr bool kTwo = TERMS == 2 && D == 128;
+    static constexpr int kPlaces = kTwo ? 2 : 3, kPlace = 2 * kPart;
+    static constexpr int kOffLow = kPlaces * kPlace;
+    static constexpr int kOffRaw = kOffLow + (TERMS == 2 ? kPart : 0);
+    static constexpr int kSlots = D == 128 && !kTwo ? 3 : 6;   // raw pieces
     static constexpr int kOffBars = kOffRaw + kSlots * kRaw;
     static constexpr int kOffKeep = kOffBars + 512;            // [tile % 4][row]: what the sums before a tile are multiplied by
     static constexpr int kOffFactor = kOffKeep + 4 * kRows * 4;  // [stretch % 4][row]: a row's scores as powers of 2
@@ -85,6 +90,12 @@ struct Stretch {
         ++index;
         return true;
     }
+};
+
+// The pieces of a part, alike in every role: K(0), K(1), V(0), K(2), V(1), ..., V(n - 2), V(n - 1).
+struct Pieces {
+    __device__ static __forceinline__ int of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+    __device__ static __forceinline__ int of_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
 };
 
 // code - 8 in f16 of the low (high) nibbles of bytes 0 and 2.
@@ -193,10 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);  // (the swizzle's atoms are 1024 bytes)
     const uint32_t base = smem_addr(smem), bars = base + Sh::kOffBars;
-    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * Sh::kSlots, k_ready = raw_empty + 8 * Sh::kSlots, k_done = k_ready + 8;
-    const uint32_t v_ready = k_done + 8, s_full = v_ready + 8, p_ready = s_full + 16, o_full = p_ready + 16, o_free = o_full + 8;
-    const uint32_t mfinal = o_free + 8, q_staged = mfinal + 8, scaled = q_staged + 8;  // up to 29 barriers: 232 bytes
-    uint8_t *const words = smem + Sh::kOffBars + 256;
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * Sh::kSlots, k_done = raw_empty + 8 * Sh::kSlots;
+    const uint32_t s_full = k_done + 8, p_ready = s_full + 16, o_full = p_ready + 16, o_free = o_full + 8;
+    const uint32_t mfinal = o_free + 8, q_staged = mfinal + 8, place_ready = q_staged + 8, place_free = place_ready + 24, scaled = place_free + 24;  // up to 33 barriers: 264 bytes
+    uint8_t *const words = smem + Sh::kOffBars + 272;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(words);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(words + 4);
     volatile int *const groups = reinterpret_cast<volatile int *>(words + 16);     // [tile % 16]: its groups that lie in a page
@@ -215,9 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             mbar_init(raw_empty + 8 * i, kExpanders);
             mbar_init(scaled + 8 * i, 1);
         }
-        mbar_init(k_ready, kExpanders);
         mbar_init(k_done, 1);
-        mbar_init(v_ready, kExpanders);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_full + 8 * x, 1);
             mbar_init(p_ready + 8 * x, 4);
@@ -226,6 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
         mbar_init(o_free, 4);
         mbar_init(mfinal, 1);
         mbar_init(q_staged, kExpanders);
+        for (int i = 0; i < Sh::kPlaces; ++i) {
+            mbar_init(place_ready + 8 * i, kExpanders);
+            mbar_init(place_free + 8 * i, 1);
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -310,12 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             const uint32_t issue = lane == 0;
             constexpr uint32_t kIdS = tc_idesc_f16(128, kTokens), kIdO = tc_idesc_f16(128, D) | kIdescNMajorB;
             constexpr uint32_t kPart = Sh::kPart / 16;
-            const uint32_t q_low = desc_lo(base + Sh::kOffQ, 1) + kPart, k = desc_lo(base + Sh::kOffK, 1), v = desc_lo(base + Sh::kOffV, 128 * 128 / 16);
+            const uint32_t q_low = desc_lo(base + Sh::kOffLow, 1);
+            const int units_in_all = static_cast<int>(st.past - st.u);
             auto tight = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, tc_wait(bar, parity & 1u, abort_flag))); };
             bool ok = true;
             int n = 0;  // units so far
             auto product_o = [&](int j) {
-                ok = tight(p_ready + 8 * (j & 1), j >> 1) && tight(v_ready, j) && (j == 0 || tight(o_free, j - 1));
+                const int piece = Pieces::of_v(j, units_in_all), place = piece % Sh::kPlaces;
+                const uint32_t v = desc_lo(base + place * Sh::kPlace, 128 * 128 / 16);
+                ok = tight(p_ready + 8 * (j & 1), j >> 1) && tight(place_ready + 8 * place, piece / Sh::kPlaces) && (j == 0 || tight(o_free, j - 1));
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t w = tmem + 128 * (j & 1), w_low = tmem + kTmemLow;
@@ -323,18 +339,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 if (TERMS == 2) mma_pv(issue, tmem + kTmemO, w_low, v, kIdO, 0, kDescHi);
                 mma_pv(issue, tmem + kTmemO, w, v + kPart, kIdO, TERMS == 2, kDescHi);
                 mma_pv(issue, tmem + kTmemO, w, v, kIdO, 1, kDescHi);
+                commit(issue, place_free + 8 * place);
                 commit(issue, o_full);
             };
             while (ok && st.next(units)) {
                 for (int j = 0; ok && j < st.n; ++j, ++n) {
-                    ok = tight(k_ready, n);
+                    const int piece = Pieces::of_k(n), place = piece % Sh::kPlaces;
+                    ok = tight(place_ready + 8 * place, piece / Sh::kPlaces);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t s = tmem + 128 * (n & 1);
+                    const uint32_t s = tmem + 128 * (n & 1), k = desc_lo(base + place * Sh::kPlace, 1);
                     if (TERMS == 2) mma_s<D>(issue, s, q_low, k, kIdS, kDescHi, 0);
                     mma_s_tm<D>(issue, s, tmem + kTmemQ, k + kPart, kIdS, kDescHi, TERMS == 2);
                     mma_s_tm<D>(issue, s, tmem + kTmemQ, k, kIdS, kDescHi, 1);
                     commit(issue, s_full + 8 * (n & 1));
+                    commit(issue, place_free + 8 * place);
                     commit(issue, k_done);
                     if (n > 0) product_o(n - 1);
                 }
@@ -511,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             constexpr bool values = decltype(of)::value;
             const int slot = piece % Sh::kSlots;
             ok = wait(scaled + 8 * slot, piece / Sh::kSlots) && wait(raw_full + 8 * slot, piece / Sh::kSlots);
-            if (ok && j > 0) ok = values ? wait(o_full, j - 1) : wait(k_done, j - 1);
+            // (a barrier a place: its last piece's products are complete)
+            if (ok && piece >= Sh::kPlaces) ok = wait(place_free + 8 * (piece % Sh::kPlaces), piece / Sh::kPlaces - 1);
             if (!ok) return;
             const uint8_t *const raw = smem + Sh::kOffRaw + slot * Sh::kRaw;
             // Rows of a warp: so that eight lanes that store together have eight different chunk places, and the same for
@@ -519,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             const int part = lane & 3, x = lane >> 2, row = 8 * w + (values ? x : (x & 1) * 4 + (x >> 1)), vr = kv_value_row(row & 15);
             const uint8_t *codes = raw + (values ? ((row & ~15) + vr) * G::kRow + (part ^ (vr & 2)) * (4 * NB) : row * G::kRow + part * (4 * NB));
             const uint8_t *scales = raw + Sh::kRawCodes + row * G::kScaleRow;
-            uint8_t *const to = smem + (values ? Sh::kOffV : Sh::kOffK) + row * 128;
+            uint8_t *const to = smem + piece % Sh::kPlaces * Sh::kPlace + row * 128;
             // keys: block b's words go to chunk 4 (b % 2) + part of half b / 2; values: units 2 part and 2 part + 1 of block pair h to half h
             uint8_t *const first = to + (((values ? 2 * part : part) ^ (row & 7)) << 4);
             uint8_t *const second = to + (((values ? 2 * part + 1 : part + 4) ^ (row & 7)) << 4);
@@ -542,14 +562,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(raw_empty + 8 * slot);
-                mbar_arrive(values ? v_ready : k_ready);
+                mbar_arrive(place_ready + 8 * (piece % Sh::kPlaces));
             }
             ++piece;
         };
         while (ok && st.next(units)) {
             // ---- the stretch's queries, in the keys' order of channels, once the last one's products are complete
-            if (n > 0) ok = wait(k_done, n - 1);
+            // (the low parts' place is read by those products, tensor memory too; the high ones pass through the place of
+            // the piece that comes next, K(n))
+            const int place = piece % Sh::kPlaces;
+            if (n > 0) ok = wait(k_done, n - 1) && (piece < Sh::kPlaces || wait(place_free + 8 * place, piece / Sh::kPlaces - 1));
             if (!ok) break;
+            uint8_t *const staged = smem + place * Sh::kPlace;
             const int head = st.item / p.row_tiles, row0 = st.item % p.row_tiles * kRows;
             constexpr int kLanes = D / 8, kStep = 8 * 32 / kLanes;  // lanes of a row, rows of the eight warps
             const int chunk = lane % kLanes, b = chunk >> 2, t = chunk & 3;
@@ -582,27 +606,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                     const float2 f = unpack_half2(h[i]);
                     l[i] = pack_half2(y - f.x, z - f.y);
                 }
-                uint8_t *to = smem + Sh::kOffQ + (chunk >> 3) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (TERMS == 2) *reinterpret_cast<uint4 *>(to + Sh::kPart) = make_uint4(l[0], l[1], l[2], l[3]);
+                const int to = (chunk >> 3) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4 *>(staged + to) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (TERMS == 2) *reinterpret_cast<uint4 *>(smem + Sh::kOffLow + to) = make_uint4(l[0], l[1], l[2], l[3]);
             }
             {  // to tensor memory: a row's 64 channels a thread
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_staged);
-                ok = wait(q_staged, st.index);
+                ok = wait(q_staged, 0);
                 if (!ok) break;
                 const int r = 32 * (w & 3) + lane, h = w >> 2;
                 if (h < D / 64) {
                     uint32_t v[32];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(smem + Sh::kOffQ + h * (128 * 128) + r * 128 + ((i ^ (r & 7)) << 4));
+                        const uint4 x = *reinterpret_cast<const uint4 *>(staged + h * (128 * 128) + r * 128 + ((i ^ (r & 7)) << 4));
                         v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
                     }
                     tc_st32(tmem + (static_cast<uint32_t>(32 * (w & 3)) << 16) + kTmemQ + 32 * h, v);
                     tc_wait_st();
                     tc_fence_before();
                 }
+                // K(n) takes the place when every warp has read its rows
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_staged);
+                ok = wait(q_staged, 1);
             }
             for (int j = 0; ok && j < st.n; ++j, ++n) {
                 expand(n, std::false_type());
