@@ -11,7 +11,6 @@
 // joins a row's results in a fixed order.
 #include <atomic>
 #include <cfloat>
-#include <type_traits>
 
 #include "tc_attend.cuh"
 
@@ -336,9 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 tc_fence_after();
                 const uint32_t w = tmem + 128 * (j & 1), w_low = tmem + kTmemLow;
                 // small terms first: what the tensor cores cut off at each sum is then of the small ones
-                if (TERMS == 2) mma_pv(issue, tmem + kTmemO, w_low, v, kIdO, 0, kDescHi);
-                mma_pv(issue, tmem + kTmemO, w, v + kPart, kIdO, TERMS == 2, kDescHi);
-                mma_pv(issue, tmem + kTmemO, w, v, kIdO, 1, kDescHi);
+                // (one piece of code for them: what runs once a unit comes from instruction memory each time)
+#pragma unroll 1
+                for (int i = 2 - TERMS; i < 3; ++i)
+                    mma_pv(issue, tmem + kTmemO, i == 0 ? w_low : w, i == 1 ? v + kPart : v, kIdO, i > 2 - TERMS, kDescHi);
                 commit(issue, place_free + 8 * place);
                 commit(issue, o_full);
             };
@@ -350,8 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                     tc_fence_after();
                     const uint32_t s = tmem + 128 * (n & 1), k = desc_lo(base + place * Sh::kPlace, 1);
                     if (TERMS == 2) mma_s<D>(issue, s, q_low, k, kIdS, kDescHi, 0);
-                    mma_s_tm<D>(issue, s, tmem + kTmemQ, k + kPart, kIdS, kDescHi, TERMS == 2);
-                    mma_s_tm<D>(issue, s, tmem + kTmemQ, k, kIdS, kDescHi, 1);
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i)
+                        mma_s_tm<D>(issue, s, tmem + kTmemQ, i == 0 ? k + kPart : k, kIdS, kDescHi, TERMS == 2 || i > 0);
                     commit(issue, s_full + 8 * (n & 1));
                     commit(issue, place_free + 8 * place);
                     commit(issue, k_done);
@@ -526,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
         bool ok = true;
         int n = 0, piece = 0;
         // a piece's operands, once `free` is: 128-byte rows of 64 channels, 16-byte chunks swizzled by the row
-        auto expand = [&](int j, auto of) {
-            constexpr bool values = decltype(of)::value;
+        auto expand = [&](bool values) {
             const int slot = piece % Sh::kSlots;
             ok = wait(scaled + 8 * slot, piece / Sh::kSlots) && wait(raw_full + 8 * slot, piece / Sh::kSlots);
             // (a barrier a place: its last piece's products are complete)
@@ -540,9 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             const uint8_t *codes = raw + (values ? ((row & ~15) + vr) * G::kRow + (part ^ (vr & 2)) * (4 * NB) : row * G::kRow + part * (4 * NB));
             const uint8_t *scales = raw + Sh::kRawCodes + row * G::kScaleRow;
             uint8_t *const to = smem + piece % Sh::kPlaces * Sh::kPlace + row * 128;
-            // keys: block b's words go to chunk 4 (b % 2) + part of half b / 2; values: units 2 part and 2 part + 1 of block pair h to half h
+            // Keys: block b's word goes to chunk 4 (b % 2) + part of half b / 2; values: units 2 part and 2 part + 1 of block
+            // pair h to half h. One piece of code for both, see the softmax's loops.
             uint8_t *const first = to + (((values ? 2 * part : part) ^ (row & 7)) << 4);
             uint8_t *const second = to + (((values ? 2 * part + 1 : part + 4) ^ (row & 7)) << 4);
+            uint8_t *const inner[2] = {values ? first + 128 * 128 : second, values ? second : first + 128 * 128};  // (of four words the second and third)
+            const uint32_t even = values ? 0x3210 : 0x1010, odd = values ? 0x3210 : 0x3232;
 #pragma unroll 1
             for (int it = 0; it < 2; ++it) {
                 uint32_t c[NB], d[NB / 2];
@@ -550,11 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 ld_halves<NB>(scales + it * (64 * G::kScaleRow), d);
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    // word i: keys' block i; values' unit i / (NB / 2), block pair i % (NB / 2)
-                    const bool odd = values ? i / (NB / 2) == 1 : (i & 1) == 1;
-                    const int half = values ? i % (NB / 2) : i >> 1;
-                    const uint32_t s2 = values ? d[half] : __byte_perm(d[i >> 1], 0, i & 1 ? 0x3232 : 0x1010);
-                    uint8_t *t = (odd ? second : first) + half * (128 * 128) + it * (64 * 128);
+                    const uint32_t pair = NB == 2 || i == 0 ? d[0] : i == 3 ? d[NB / 2 - 1] : (values == (i == 1)) ? d[NB / 2 - 1] : d[0];
+                    const uint32_t s2 = __byte_perm(pair, 0, i & 1 ? odd : even);
+                    uint8_t *t = (i == 0 ? first : NB == 2 ? second : i == 3 ? second + 128 * 128 : inner[i - 1]) + it * (64 * 128);
                     expand_word(c[i], *reinterpret_cast<const __half2 *>(&s2), t, t + Sh::kPart);
                 }
             }
@@ -633,11 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 ok = wait(q_staged, 1);
             }
             for (int j = 0; ok && j < st.n; ++j, ++n) {
-                expand(n, std::false_type());
-                if (ok && n > 0) expand(n - 1, std::true_type());
+                for (int values = 0; ok && values < (n > 0 ? 2 : 1); ++values) expand(values != 0);
             }
         }
-        if (ok && n > 0) expand(n - 1, std::true_type());
+        if (ok && n > 0) expand(true);
         if (!ok) failed(kErrConsumerWait);
     }
     tc_fence_before();
