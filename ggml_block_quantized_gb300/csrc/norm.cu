@@ -10,9 +10,10 @@
 //
 // Threads hold eight consecutive elements at a time (rows on 16-byte
 // boundaries: one 32-byte load or two of 16; a block of the activation types is
-// then 4 lanes or one warp, and xq needs no memory), or single elements a row's
-// width apart (any alignment). Up to 8192 elements a thread has one such set,
-// so that a single row is read by as many threads as there can be.
+// then 4 lanes or one warp, and xq needs no memory), or four single ones a row's
+// threads apart (any alignment; eight took 11.7 us for 1037 rows of 1283). Up to
+// 8192 (4096) elements a thread has one such set, so that a single row is read by
+// as many threads as there can be.
 #include "quant_act.cuh"
 #include "step_kernels.cuh"
 
@@ -24,7 +25,7 @@ constexpr int kMaxThreads = 1024;
 
 // Sum over a row's threads; `part` alternates so that one barrier a sum is enough.
 struct RowSum {
-    float *buf;  // [2][warps of the row]
+    float *buf;  // [2][warps of the row, 32 at most]
     int warps, warp, barrier, part = 0;
     __device__ __forceinline__ float operator()(float v) {
 #pragma unroll
@@ -84,9 +85,11 @@ __device__ __forceinline__ void store8(__half *p, const float (&v)[8]) {
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The elements that a thread holds of a row: SETS x 8. WIDE: set k is elements
-// 8 (t + k T) on; else element i of them is t + i T (T threads a row).
+// The elements that a thread holds of a row. WIDE: SETS x 8, set k is elements
+// 8 (t + k T) on; else SETS x 4, element i of them is t + i T (T threads a row).
 template <bool WIDE, int SETS> struct Held {
+    static constexpr int W = WIDE ? 8 : 4;
+    using Values = float[SETS][W];
     int t, threads, d;
     template <class F> __device__ __forceinline__ void each(F f) const {  // f(set, first element) or f(i, element)
         if (WIDE) {
@@ -97,31 +100,31 @@ template <bool WIDE, int SETS> struct Held {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8 * SETS; ++i) {
+            for (int i = 0; i < W * SETS; ++i) {
                 const int e = t + i * threads;
                 if (e < d) f(i, e);
             }
         }
     }
-    template <class T> __device__ __forceinline__ void load(const T *p, float (&v)[SETS][8]) const {
+    template <class T> __device__ __forceinline__ void load(const T *p, Values &v) const {
         each([&](int i, int e) {
             if constexpr (WIDE) load8(p + e, v[i]);
-            else v[i >> 3][i & 7] = static_cast<float>(p[e]);
+            else v[i / W][i % W] = static_cast<float>(p[e]);
         });
     }
-    template <class T> __device__ __forceinline__ void store(T *p, const float (&v)[SETS][8]) const {
+    template <class T> __device__ __forceinline__ void store(T *p, const Values &v) const {
         each([&](int i, int e) {
             if constexpr (WIDE) store8(p + e, v[i]);
-            else p[e] = static_cast<T>(v[i >> 3][i & 7]);
+            else p[e] = static_cast<T>(v[i / W][i % W]);
         });
     }
     // f(value, vector's element) over all held elements; p a [d] vector (nullptr: `none`)
-    template <class T, class F> __device__ __forceinline__ void with(const T *p, float none, float (&v)[SETS][8], F f) const {
+    template <class T, class F> __device__ __forceinline__ void with(const T *p, float none, Values &v, F f) const {
         if (p == nullptr) {
 #pragma unroll
             for (int k = 0; k < SETS; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[k][i] = f(v[k][i], none);
+                for (int i = 0; i < W; ++i) v[k][i] = f(v[k][i], none);
             return;
         }
         each([&](int i, int e) {
@@ -131,34 +134,34 @@ template <bool WIDE, int SETS> struct Held {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = f(v[i][j], w[j]);
             } else {
-                v[i >> 3][i & 7] = f(v[i >> 3][i & 7], static_cast<float>(p[e]));
+                v[i / W][i % W] = f(v[i / W][i % W], static_cast<float>(p[e]));
             }
         });
     }
-    __device__ __forceinline__ float sum(const float (&v)[SETS][8]) const {  // (elements past the row's end are 0)
+    __device__ __forceinline__ float sum(const Values &v) const {  // (elements past the row's end are 0)
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < SETS; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += v[k][i];
+            for (int i = 0; i < W; ++i) s += v[k][i];
         return s;
     }
-    __device__ __forceinline__ float squares(const float (&v)[SETS][8]) const {
+    __device__ __forceinline__ float squares(const Values &v) const {
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < SETS; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(v[k][i], v[k][i], s);
+            for (int i = 0; i < W; ++i) s = fmaf(v[k][i], v[k][i], s);
         return s;
     }
-    __device__ __forceinline__ void clear(float (&v)[SETS][8]) const {
+    __device__ __forceinline__ void clear(Values &v) const {
 #pragma unroll
         for (int k = 0; k < SETS; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
+            for (int i = 0; i < W; ++i) v[k][i] = 0.0f;
     }
     // v becomes N(v; w, b)
-    __device__ __forceinline__ void norm(float (&v)[SETS][8], const float *w, const float *b, bool layer, float eps,
+    __device__ __forceinline__ void norm(Values &v, const float *w, const float *b, bool layer, float eps,
                                          RowSum &row_sum) const {
         const float per = 1.0f / static_cast<float>(d);
         if (layer) {
@@ -168,7 +171,7 @@ template <bool WIDE, int SETS> struct Held {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[i][j] -= mean;
                 } else {
-                    v[i >> 3][i & 7] -= mean;
+                    v[i / W][i % W] -= mean;
                 }
             });
         }
@@ -179,9 +182,12 @@ template <bool WIDE, int SETS> struct Held {
 };
 
 // threads: of a row, a multiple of 32; blockDim.x / threads rows a block.
-template <class TH, class TY, bool WIDE, int SETS>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const qnorm_args a, const int threads) {
-    __shared__ float sums[2 * 32 * 8];
+// MOST: threads of a block at most. With rows on 16-byte boundaries registers are kept few enough for 1280 threads and
+// more a multiprocessor: what is on its way from memory counts (8191 rows of 4096, f16 and f32: 57.4 us with three
+// blocks of 512, 69.5 with two, 57.6 with four).
+template <class TH, class TY, bool WIDE, int SETS, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 1024 || !WIDE ? 1 : MOST == 512 ? 3 : 5) norm_kernel(const qnorm_args a, const int threads) {
+    __shared__ float sums[8 * 64];
     pdl_allow_dependents();
     pdl_wait_prior_grids();
     const int in_block = threadIdx.x / threads, t = threadIdx.x - in_block * threads;
@@ -191,11 +197,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const qnorm_args a, c
     RowSum row_sum{sums + in_block * 64, threads / 32, t / 32, 1 + in_block};
     const bool layer = a.layer != 0;
     const TH *const h = static_cast<const TH *>(a.h) + row * a.h_stride;
-    float v[SETS][8];
+    typename Held<WIDE, SETS>::Values v;
     held.clear(v);
     if (a.y != nullptr) {
         held.load(static_cast<const TY *>(a.y) + row * a.y_stride, v);
-        float early[SETS == 1 ? 1 : SETS][8];  // (of more sets h is read when u is done: both would not fit the registers)
+        typename Held<WIDE, SETS>::Values early;  // (of more sets h is read when u is done: both would not fit the registers)
         if constexpr (SETS == 1) {
             held.clear(early);
             held.load(h, early);
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const qnorm_args a, c
         if (a.gate != nullptr) held.with(a.gate + row * a.gate_stride, 1.0f, v, [](float x, float y) { return x * y; });
         if constexpr (SETS == 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[0][i] = fmaf(a.scale, v[0][i], early[0][i]);
+            for (int i = 0; i < held.W; ++i) v[0][i] = fmaf(a.scale, v[0][i], early[0][i]);
         } else {
             held.with(h, 0.0f, v, [&](float x, float y) { return fmaf(a.scale, x, y); });
         }
@@ -237,14 +243,19 @@ bool wide_rows(const void *p, int64_t stride, int type) {
 }
 
 template <class TH, class TY, bool WIDE> cudaError_t launch(const qnorm_args &a, cudaStream_t s) {
-    const int units = static_cast<int>((a.d + 7) / 8);  // sets of 8 elements
-    const int sets = units <= kMaxThreads ? 1 : 2;
+    constexpr int kWidth = WIDE ? 8 : 4;
+    const int units = static_cast<int>((a.d + kWidth - 1) / kWidth);
+    const int sets = units <= kMaxThreads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
     const int threads = ((units + sets - 1) / sets + 31) / 32 * 32;
     const int rows = threads >= 256 ? 1 : 256 / threads;
     const int64_t grid = (a.n + rows - 1) / rows;
     const int block = threads * rows;
-    if (sets == 1) return launch_pdl(norm_kernel<TH, TY, WIDE, 1>, static_cast<int>(grid), block, 0, s, a, threads);
-    return launch_pdl(norm_kernel<TH, TY, WIDE, 2>, static_cast<int>(grid), block, 0, s, a, threads);
+    if constexpr (!WIDE)
+        if (sets == 4) return launch_pdl(norm_kernel<TH, TY, WIDE, 4, 1024>, static_cast<int>(grid), block, 0, s, a, threads);
+    if (sets == 2) return launch_pdl(norm_kernel<TH, TY, WIDE, 2, 1024>, static_cast<int>(grid), block, 0, s, a, threads);
+    if (block <= 256) return launch_pdl(norm_kernel<TH, TY, WIDE, 1, 256>, static_cast<int>(grid), block, 0, s, a, threads);
+    if (block <= 512) return launch_pdl(norm_kernel<TH, TY, WIDE, 1, 512>, static_cast<int>(grid), block, 0, s, a, threads);
+    return launch_pdl(norm_kernel<TH, TY, WIDE, 1, 1024>, static_cast<int>(grid), block, 0, s, a, threads);
 }
 
 template <class TH, class TY> cudaError_t launch_types(const qnorm_args &a, cudaStream_t s) {
