@@ -11,9 +11,15 @@
 // Threads hold eight consecutive elements at a time (rows on 16-byte
 // boundaries: one 32-byte load or two of 16; a block of the activation types is
 // then 4 lanes or one warp, and xq needs no memory), or four single ones a row's
-// threads apart (any alignment; eight took 11.7 us for 1037 rows of 1283). Up to
-// 8192 (4096) elements a thread has one such set, so that a single row is read by
-// as many threads as there can be.
+// threads apart (any alignment; eight took a fifth longer for 1037 rows of 1283).
+// Up to 8192 (4096) elements a thread has one such set, so that a single row is
+// read by as many threads as there can be.
+//
+// Memory bounds it where there is work for every multiprocessor: 8191 rows of
+// 4096 with both norms, f16 h, f32 y, f16 x take 52.4 us (335 MB at 6.4 TB/s),
+// close to a copy's 49.4; there the instructions of an element count next (38 of
+// them took 57.7 us). 1037 rows of 1283 in f32 take 9.7 us, 48 rows of 4096 4.3,
+// one row 3.1: the chain of launch, load, two sums by shuffles and barrier, store.
 #include "quant_act.cuh"
 #include "step_kernels.cuh"
 
@@ -43,10 +49,8 @@ struct RowSum {
     }
 };
 
-__device__ __forceinline__ bool on32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
-
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    if (on32(p)) {
+__device__ __forceinline__ void load8(const float *p, float (&v)[8], bool wide32) {
+    if (wide32) {
         asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                      : "l"(p)
@@ -56,7 +60,7 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
 }
-__device__ __forceinline__ void load8(const __half *p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const __half *p, float (&v)[8], bool) {
     const uint4 a = *reinterpret_cast<const uint4 *>(p);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -65,8 +69,8 @@ __device__ __forceinline__ void load8(const __half *p, float (&v)[8]) {
         v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    if (on32(p)) {
+__device__ __forceinline__ void store8(float *p, const float (&v)[8], bool wide32) {
+    if (wide32) {
         asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
                      "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                      : "memory");
@@ -75,7 +79,7 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
         reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
 }
-__device__ __forceinline__ void store8(__half *p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__half *p, const float (&v)[8], bool) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -91,6 +95,7 @@ template <bool WIDE, int SETS> struct Held {
     static constexpr int W = WIDE ? 8 : 4;
     using Values = float[SETS][W];
     int t, threads, d;
+    bool wide32;  // rows of f32 lie on 32-byte boundaries
     template <class F> __device__ __forceinline__ void each(F f) const {  // f(set, first element) or f(i, element)
         if (WIDE) {
 #pragma unroll
@@ -108,13 +113,13 @@ template <bool WIDE, int SETS> struct Held {
     }
     template <class T> __device__ __forceinline__ void load(const T *p, Values &v) const {
         each([&](int i, int e) {
-            if constexpr (WIDE) load8(p + e, v[i]);
+            if constexpr (WIDE) load8(p + e, v[i], wide32);
             else v[i / W][i % W] = static_cast<float>(p[e]);
         });
     }
     template <class T> __device__ __forceinline__ void store(T *p, const Values &v) const {
         each([&](int i, int e) {
-            if constexpr (WIDE) store8(p + e, v[i]);
+            if constexpr (WIDE) store8(p + e, v[i], wide32);
             else p[e] = static_cast<T>(v[i / W][i % W]);
         });
     }
@@ -130,7 +135,7 @@ template <bool WIDE, int SETS> struct Held {
         each([&](int i, int e) {
             if constexpr (WIDE) {
                 float w[8];
-                load8(p + e, w);
+                load8(p + e, w, wide32);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = f(v[i][j], w[j]);
             } else {
@@ -161,9 +166,8 @@ template <bool WIDE, int SETS> struct Held {
             for (int i = 0; i < W; ++i) v[k][i] = 0.0f;
     }
     // v becomes N(v; w, b)
-    __device__ __forceinline__ void norm(Values &v, const float *w, const float *b, bool layer, float eps,
+    __device__ __forceinline__ void norm(Values &v, const float *w, const float *b, bool layer, float eps, float per,
                                          RowSum &row_sum) const {
-        const float per = 1.0f / static_cast<float>(d);
         if (layer) {
             const float mean = row_sum(sum(v)) * per;
             each([&](int i, int) {
@@ -175,26 +179,26 @@ template <bool WIDE, int SETS> struct Held {
                 }
             });
         }
-        const float inv = 1.0f / sqrtf(row_sum(squares(v)) * per + eps);
+        const float inv = rsqrtf(row_sum(squares(v)) * per + eps);  // (off by 2^-22 at most)
         with(w, 1.0f, v, [&](float x, float y) { return x * inv * y; });
         if (b != nullptr) with(b, 0.0f, v, [](float x, float y) { return x + y; });
     }
 };
 
-// threads: of a row, a multiple of 32; blockDim.x / threads rows a block.
+// blockDim.x threads a row, a multiple of 32, blockDim.y rows; per: 1 / d.
 // MOST: threads of a block at most. With rows on 16-byte boundaries registers are kept few enough for 1280 threads and
-// more a multiprocessor: what is on its way from memory counts (8191 rows of 4096, f16 and f32: 57.4 us with three
-// blocks of 512, 69.5 with two, 57.6 with four).
+// more a multiprocessor: what is on its way from memory counts (8191 rows of 4096, f16 and f32, before later steps: 57.4 us with
+// three blocks of 512, 69.5 with two, 57.6 with four).
 template <class TH, class TY, bool WIDE, int SETS, int MOST>
-__global__ void __launch_bounds__(MOST, MOST == 1024 || !WIDE ? 1 : MOST == 512 ? 3 : 5) norm_kernel(const qnorm_args a, const int threads) {
+__global__ void __launch_bounds__(MOST, MOST == 1024 || !WIDE ? 1 : MOST == 512 ? 3 : 5) norm_kernel(const qnorm_args a, const float per, const bool wide32) {
     __shared__ float sums[8 * 64];
     pdl_allow_dependents();
     pdl_wait_prior_grids();
-    const int in_block = threadIdx.x / threads, t = threadIdx.x - in_block * threads;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / threads) + in_block;
+    const int t = threadIdx.x, threads = blockDim.x;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= a.n) return;
-    const Held<WIDE, SETS> held{t, threads, static_cast<int>(a.d)};
-    RowSum row_sum{sums + in_block * 64, threads / 32, t / 32, 1 + in_block};
+    const Held<WIDE, SETS> held{t, threads, static_cast<int>(a.d), wide32};
+    RowSum row_sum{sums + threadIdx.y * 64, threads / 32, t / 32, 1 + static_cast<int>(threadIdx.y)};
     const bool layer = a.layer != 0;
     const TH *const h = static_cast<const TH *>(a.h) + row * a.h_stride;
     typename Held<WIDE, SETS>::Values v;
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(MOST, MOST == 1024 || !WIDE ? 1 : MOST == 512 
             held.clear(early);
             held.load(h, early);
         }
-        if (a.post_w != nullptr) held.norm(v, a.post_w, a.post_b, layer, a.eps, row_sum);
+        if (a.post_w != nullptr) held.norm(v, a.post_w, a.post_b, layer, a.eps, per, row_sum);
         if (a.gate != nullptr) held.with(a.gate + row * a.gate_stride, 1.0f, v, [](float x, float y) { return x * y; });
         if constexpr (SETS == 1) {
 #pragma unroll
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(MOST, MOST == 1024 || !WIDE ? 1 : MOST == 512 
     }
     if (a.h_out != nullptr) held.store(static_cast<TH *>(a.h_out) + row * a.h_out_stride, v);
     if (a.x_out == nullptr && a.xq == nullptr) return;
-    held.norm(v, a.w, a.b, layer, a.eps, row_sum);
+    held.norm(v, a.w, a.b, layer, a.eps, per, row_sum);
     if (a.x_out != nullptr) {
         if (a.x_type == QG_F32) held.store(static_cast<float *>(a.x_out) + row * a.d, v);
         else held.store(static_cast<__half *>(a.x_out) + row * a.d, v);
@@ -242,20 +246,32 @@ bool wide_rows(const void *p, int64_t stride, int type) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % (type == QG_F32 ? 4 : 8) == 0;
 }
 
+bool on32(const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && stride % 8 == 0; }
+
 template <class TH, class TY, bool WIDE> cudaError_t launch(const qnorm_args &a, cudaStream_t s) {
     constexpr int kWidth = WIDE ? 8 : 4;
     const int units = static_cast<int>((a.d + kWidth - 1) / kWidth);
     const int sets = units <= kMaxThreads ? 1 : units <= 2 * kMaxThreads ? 2 : 4;
     const int threads = ((units + sets - 1) / sets + 31) / 32 * 32;
     const int rows = threads >= 256 ? 1 : 256 / threads;
-    const int64_t grid = (a.n + rows - 1) / rows;
-    const int block = threads * rows;
+    // (of f16 matrices it says nothing)
+    const bool wide32 = on32(a.h, a.h_stride) && on32(a.y, a.y_stride) && on32(a.gate, a.gate_stride) && on32(a.post_w, 0) && on32(a.post_b, 0) &&
+                        on32(a.w, 0) && on32(a.b, 0) && on32(a.h_out, a.h_out_stride) && on32(a.x_out, a.d);
+    auto kernel = norm_kernel<TH, TY, WIDE, 2, 1024>;
     if constexpr (!WIDE)
-        if (sets == 4) return launch_pdl(norm_kernel<TH, TY, WIDE, 4, 1024>, static_cast<int>(grid), block, 0, s, a, threads);
-    if (sets == 2) return launch_pdl(norm_kernel<TH, TY, WIDE, 2, 1024>, static_cast<int>(grid), block, 0, s, a, threads);
-    if (block <= 256) return launch_pdl(norm_kernel<TH, TY, WIDE, 1, 256>, static_cast<int>(grid), block, 0, s, a, threads);
-    if (block <= 512) return launch_pdl(norm_kernel<TH, TY, WIDE, 1, 512>, static_cast<int>(grid), block, 0, s, a, threads);
-    return launch_pdl(norm_kernel<TH, TY, WIDE, 1, 1024>, static_cast<int>(grid), block, 0, s, a, threads);
+        if (sets == 4) kernel = norm_kernel<TH, TY, WIDE, 4, 1024>;
+    if (sets == 1) kernel = threads * rows <= 256 ? norm_kernel<TH, TY, WIDE, 1, 256> : threads <= 512 ? norm_kernel<TH, TY, WIDE, 1, 512> : norm_kernel<TH, TY, WIDE, 1, 1024>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.n + rows - 1) / rows));
+    cfg.blockDim = dim3(threads, rows);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    g_launch_step = "cudaLaunchKernelEx";
+    return cudaLaunchKernelEx(&cfg, kernel, a, 1.0f / static_cast<float>(a.d), wide32);
 }
 
 template <class TH, class TY> cudaError_t launch_types(const qnorm_args &a, cudaStream_t s) {

@@ -8,10 +8,11 @@ E = 2.0 ** -24  # half a step of f32
 def _norm(v, err, w, b, layer, eps):
     """N(v; w, b) of rows v that are off by at most err, and how far an f32 evaluation may be from it.
 
-    Sums of d terms take at most 8 or 16 additions a thread, ten in the shuffles, and the products: 32 roundings. A
-    mean is off by 32 E of the mean magnitude; what stays of v by that, by its own subtraction and by err; 1 / sqrt(mean
-    square + eps) by half of the sum's 34 roundings, by its own three, and by the elements' errors (their root mean
-    square beside the row's); the two products and the bias one rounding each."""
+    Sums of d terms take at most 16 additions (fused with the products) a thread and ten in the shuffles; 1 / d, the
+    product with it and eps: 29 roundings. A mean is off by less than 34 E of the mean magnitude; what stays of v by
+    that, by its own subtraction and by err; 1 / sqrt(mean square + eps) by half of the sum's 29, by its own 4 E (CUDA's
+    bound of rsqrtf is 2^-22), and by the elements' errors (their root mean square beside the row's); the two products
+    and the bias one rounding each: 14.5 + 4 + 2 < 22."""
     if layer:
         m = v.mean(1, keepdims=True)
         err = err + 34 * E * np.abs(v).mean(1, keepdims=True) + err.mean(1, keepdims=True)
