@@ -4,13 +4,37 @@
 // All query rows of a key/value head see the whole prefix, so it is taken once
 // for all of them: an item is one key/value head and 128 of its rows (token-major
 // over the call's tokens and the head's group), its units tiles of 128 prefix
-// tokens. The items' units form one list that the thread blocks share out in
-// equal contiguous parts; each stretch of an item in a part leaves its rows'
-// values, reference and sum in the workspace. Each sequence's own tokens go
-// through kv_attend's kernels, which leave theirs there, too, and a last kernel
-// joins a row's results in a fixed order.
+// tokens. The thread blocks share out the units; each stretch of an item in a
+// block's part leaves its rows' values, reference and sum in the workspace. Each
+// sequence's own tokens go through kv_attend's kernels, which leave theirs there,
+// too, and a last kernel joins a row's results in a fixed order.
+//
+// S = Q K^T and O = P V are tcgen05 products of f16 with f32 sums. A key or value
+// is a code of four bits times an f16 scale, 15 bits, and so the exact sum of two
+// f16 parts; f32 queries and, for them, the weights are two parts as well. Then S
+// takes two products (f32: three, without low times low) and O two (three), what a
+// plain f32 evaluation loses at that: an f16 part each would cost 2^-12 a factor.
+// The rows' softmax runs over the tiles (references rise by powers of 2 of at least
+// 2^7, so a row's values are rescaled a few times in all), and O of a tile is read
+// back and added up in f32 registers.
+//
+// The warps: one copies the units' groups of the cache, one makes their scales
+// ready, one issues S, one O; four hold a row's softmax a thread, four its values'
+// sums; eight expand codes into operands, four the keys', four the values'. With
+// 128 channels a unit is 32 products of 64 cycles, so 2048 cycles for f16, 3072
+// for f32, and 128 KB of operands written; it takes 2850. What bounds it is the
+// expanders' chain of instructions (3.8 cycles each in turn, 22 a word of eight
+// codes), then the tensor cores. 16 sequences of 64 heads on 65521 tokens, 27 units
+// a block, take 77.8 us. A call with a short prefix is a pipeline's filling, its
+// drain and the join (2 sequences on 300 tokens: 17.8 us), most of them
+// instructions' first fetch. What other arrangements measured on the 65521: one warp for S and O, and eight
+// that expand keys and values in turn, 86.0 us; pieces of a unit's keys and values
+// in three places and three raw pieces ahead 91 (copies were waited for); whole
+// units' keys in one place, values in another 82.3; loops of the expanders
+// unrolled 98 (instructions came from beyond their cache).
 #include <atomic>
 #include <cfloat>
+#include <climits>
 
 #include "tc_attend.cuh"
 
@@ -34,18 +58,16 @@ constexpr float kHigh = 14.0f, kLow = 7.0f;  // log2 of the largest weight, and 
 
 template <int D, int TERMS> struct Shape {
     using G = KvGroup<D>;
-    static constexpr int kPart = kTokens * D * 2;              // one f16 part of a key, value or query tile
-    static constexpr int kRawCodes = kTokens * D / 2;          // codes of a unit's keys (or values)
-    static constexpr int kRaw = kRawCodes + kTokens * G::kScaleRow;
-    // Operands, in the order K(0), K(1), V(0), K(2), V(1) ..., each a high and a low part of 128-byte rows of 64
-    // channels: three places let them be made ready a piece ahead of the products (f32 queries leave room for two of
-    // heads of 128). The queries' high parts pass through the last place on their way to tensor memory, f32's low parts
-    // have one of their own.
-    static constexpr bool kTwo = TERMS == 2 && D == 128;
-    static constexpr int kPlaces = kTwo ? 2 : 3, kPlace = 2 * kPart;
-    static constexpr int kOffLow = kPlaces * kPlace;
-    static constexpr int kOffRaw = kOffLow + (TERMS == 2 ? kPart : 0);
-    static constexpr int kSlots = D == 128 && !kTwo ? 3 : 6;   // raw pieces
+    // Operands in slices, so that the tensor cores read one of a unit while the next is made: of keys 64 channels of all
+    // tokens, of values all channels of 64 tokens (D = 64: all of them), each as a high and a low part of 128-byte rows of
+    // 64 channels. Two places for each kind. Queries pass through the key slices' places on their way to tensor
+    // memory, f32's low parts have a place of their own.
+    static constexpr int kSlices = D / 64, kPart = 128 * 128, kSlice = 2 * kPart;
+    static constexpr int kSliceTokens = kTokens / kSlices;     // of a slice of values
+    static constexpr int kOffV = 2 * kSlice, kOffLow = 4 * kSlice;
+    static constexpr int kRaw = kTokens / 16 * G::kBytes;      // a unit's groups as they lie in the cache
+    static constexpr int kOffRaw = kOffLow + (TERMS == 2 ? kSlices * kPart : 0);
+    static constexpr int kSlots = D == 128 && TERMS == 2 ? 3 : 5;  // units' raw groups
     static constexpr int kOffBars = kOffRaw + kSlots * kRaw;
     static constexpr int kOffKeep = kOffBars + 512;            // [tile % 4][row]: what the sums before a tile are multiplied by
     static constexpr int kOffFactor = kOffKeep + 4 * kRows * 4;  // [stretch % 4][row]: a row's scores as powers of 2
@@ -53,10 +75,13 @@ template <int D, int TERMS> struct Shape {
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
-// The prefix's length, checked, and the list of units.
+// The prefix's length, checked, and how the thread blocks share the units: each item's among as many parts as there are for
+// it, or, where that would leave a part kRestart units more, all items' as one list in equal parts. A part that ends in one
+// item and begins the next drains and fills its pipeline again, and takes other queries: 14000 cycles, as many as 4 units.
+constexpr int kRestart = 3;
 struct Units {
-    int len, tiles;      // tokens, units of an item
-    int64_t all, share;  // of all items, of a part
+    int len, tiles, per_item;  // tokens, units of an item, parts of an item (0: a list)
+    int64_t all, share;        // of all items, of a part
     __device__ __forceinline__ Units(const SharedParams &p, int parts) {
         len = __ldg(p.prefix_len);
         const int64_t room = p.prefix_pages * static_cast<int64_t>(p.own.c.page_size);
@@ -64,13 +89,22 @@ struct Units {
             record_error(p.own.err, kErrBadIndex);
             len = len < 0 ? 0 : static_cast<int>(room);
         }
-        tiles = (len + kTokens - 1) / kTokens;
-        all = static_cast<int64_t>(p.own.c.n_heads) * p.row_tiles * tiles;
-        share = (all + parts - 1) / parts;
+        tiles = static_cast<int>((static_cast<uint32_t>(len) + kTokens - 1) / kTokens);
+        const int64_t items = static_cast<int64_t>(p.own.c.n_heads) * p.row_tiles;
+        all = items * tiles;
+        per_item = 0;
+        if (items <= parts) {  // (below 2^32 units)
+            const uint32_t n = static_cast<uint32_t>(items), m = parts / n;
+            const uint32_t of_one = (tiles + m - 1) / m, of_all = (static_cast<uint32_t>(all) + parts - 1) / parts;
+            per_item = of_one <= of_all + kRestart ? static_cast<int>(m) : 0;
+            share = per_item > 0 ? of_one : of_all;
+        } else {
+            share = (all + parts - 1) / parts;
+        }
         if (share < 1) share = 1;
     }
 };
-// A stretch's place: parts and items both rise along the list, one of them at least from stretch to stretch.
+// A stretch's place is its part's and its item's number: both rise, one of them at least from stretch to stretch.
 __host__ __device__ constexpr int64_t stretch_floats(int d) { return static_cast<int64_t>(kRows) * (d + 2); }
 
 // A stretch's rows hold the channels in the order in which the value codes lie in the cache: place 8 (8 h + u) + 2 j + b
@@ -78,23 +112,32 @@ __host__ __device__ constexpr int64_t stretch_floats(int d) { return static_cast
 
 // Walks a part's stretches, alike in every role.
 struct Stretch {
-    int64_t u, past;  // the next unit, the part's end
-    int item, tile, n, index = -1;
-    __device__ __forceinline__ bool next(const Units &units) {
-        if (u >= past) return false;
-        item = static_cast<int>(u / units.tiles);
-        tile = static_cast<int>(u - static_cast<int64_t>(item) * units.tiles);
-        n = static_cast<int>(min(past - u, static_cast<int64_t>(units.tiles - tile)));
-        u += n;
+    int units;                  // still to come
+    int item, tile, n = 0, index = -1;
+    __device__ __forceinline__ Stretch(const Units &all, int64_t part) {
+        if (all.per_item > 0) {
+            item = static_cast<int>(part) / all.per_item;
+            tile = min((static_cast<int>(part) - item * all.per_item) * static_cast<int>(all.share), all.tiles);
+            units = static_cast<int64_t>(item) * all.tiles < all.all ? min(static_cast<int>(all.share), all.tiles - tile) : 0;
+        } else {
+            const int64_t u = part * all.share;
+            units = static_cast<int>(max(min(all.share, all.all - u), static_cast<int64_t>(0)));
+            item = units <= 0 ? 0 : all.all <= UINT_MAX ? static_cast<int>(static_cast<uint32_t>(u) / all.tiles) : static_cast<int>(u / all.tiles);
+            tile = static_cast<int>(u - static_cast<int64_t>(item) * all.tiles);
+        }
+    }
+    __device__ __forceinline__ bool next(const Units &all) {
+        if (units == 0) return false;
+        if (index >= 0) ++item, tile = 0;
+        n = min(units, all.tiles - tile);
+        units -= n;
         ++index;
         return true;
     }
-};
-
-// The pieces of a part, alike in every role: K(0), K(1), V(0), K(2), V(1), ..., V(n - 2), V(n - 1).
-struct Pieces {
-    __device__ static __forceinline__ int of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
-    __device__ static __forceinline__ int of_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+    // Unit by unit instead.
+    __device__ __forceinline__ void step(const Units &all) {
+        if (++tile == all.tiles) ++item, tile = 0;
+    }
 };
 
 // code - 8 in f16 of the low (high) nibbles of bytes 0 and 2.
@@ -127,22 +170,12 @@ template <int NB> __device__ __forceinline__ void ld_halves(const uint8_t *p, ui
     }
 }
 
-// Two codes' values in two f16 parts, which hold them exactly (four bits times eleven) above f16's end.
-__device__ __forceinline__ void two_parts(__half2 code, __half2 scale, uint32_t &high, uint32_t &low) {
-    const __half2 h = __hmul2(code, scale);
-    high = bits(h);
-    low = bits(__hfma2(code, scale, __hneg2(h)));
-}
-
-// One word of a row: eight values into 16 bytes of each part.
-__device__ __forceinline__ void expand_word(uint32_t w, __half2 scale, uint8_t *high, uint8_t *low) {
-    uint4 h, l;
-    two_parts(low_codes(w), scale, h.x, l.x);
-    two_parts(low_codes(w >> 8), scale, h.y, l.y);
-    two_parts(high_codes(w), scale, h.z, l.z);
-    two_parts(high_codes(w >> 8), scale, h.w, l.w);
-    *reinterpret_cast<uint4 *>(high) = h;
-    *reinterpret_cast<uint4 *>(low) = l;
+// One word of a row: eight values as two f16 parts, 16 bytes of each. The parts are the code times the scale's first six
+// significant bits and times its other five, so that both hold them exactly.
+__device__ __forceinline__ void expand_word(uint32_t w, __half2 scale, __half2 scale_low, uint8_t *high, uint8_t *low) {
+    const __half2 a = low_codes(w), b = low_codes(w >> 8), c = high_codes(w), d = high_codes(w >> 8);
+    *reinterpret_cast<uint4 *>(high) = make_uint4(bits(__hmul2(a, scale)), bits(__hmul2(b, scale)), bits(__hmul2(c, scale)), bits(__hmul2(d, scale)));
+    *reinterpret_cast<uint4 *>(low) = make_uint4(bits(__hmul2(a, scale_low)), bits(__hmul2(b, scale_low)), bits(__hmul2(c, scale_low)), bits(__hmul2(d, scale_low)));
 }
 
 // Makes a unit's raw scales (keys' or values') ready: 0 for tokens that do not count (rows past `rows`, groups in no
@@ -152,11 +185,12 @@ __device__ __forceinline__ void expand_word(uint32_t w, __half2 scale, uint8_t *
 template <int D> __device__ __forceinline__ int prepare_scales(uint8_t *scales, int rows, uint32_t groups) {
     constexpr int kChunks = kTokens * (D / 16) / 512, kPer = 256 / D;  // 16-byte chunks of a lane, tokens of one
     const int lane = threadIdx.x & 31;
-    uint4 *const at = reinterpret_cast<uint4 *>(scales) + lane;
+    uint8_t *const at = scales + lane / (D / 16) * KvGroup<D>::kBytes + lane % (D / 16) * 16;
+    constexpr int kStep = 512 / D * KvGroup<D>::kBytes;
     uint32_t x[kChunks][4], m = 0;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const uint4 v = at[32 * i];
+        const uint4 v = *reinterpret_cast<const uint4 *>(at + i * kStep);
         x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -179,22 +213,38 @@ template <int D> __device__ __forceinline__ int prepare_scales(uint8_t *scales, 
             const __half2 d = *reinterpret_cast<const __half2 *>(&x[i][w]);
             y[w] = bits(__hfma2(d, zero, __hmul2(__hmul2(d, up), more)));
         }
-        at[32 * i] = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4 *>(at + i * kStep) = make_uint4(y[0], y[1], y[2], y[3]);
     }
     return e;
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {  // elements 0 .. 3 and 16 .. 19
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p + 16));
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void load8(const __half *p, float (&x)[8]) {
-    const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p)), b = __ldg(reinterpret_cast<const uint2 *>(p + 16));
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = unpack_half2(w[i]).x, x[2 * i + 1] = unpack_half2(w[i]).y;
+__device__ __forceinline__ void tc_st4(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
+// Bounded wait that gives up once another thread of the block has set the abort flag. Most are short: the clock is read
+// every 64 polls only, and the loop is kept small.
+template <int NS> __device__ __forceinline__ bool poll_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; i < kWaitLimitPolls; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (NS > 0) __nanosleep(NS);
+        if ((i & 63u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (i == 64) t0 = now;
+            if (*abort_flag || now - t0 > kWaitLimitNs) return false;
+        }
+    }
+    return false;
+}
+
+// A wait tells a phase from the next by its parity alone, so no waiter may come to one before its predecessor is complete,
+// nor after its successor is. Each waits for every phase of its barriers in turn (the key warps twice for the last slice's
+// before a stretch), and for the next one of the same barrier something is needed that the waiter does only afterwards.
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams p) {
     constexpr int TERMS = sizeof(T) == 4 ? 2 : 1, NB = D / 32;
@@ -203,15 +253,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);  // (the swizzle's atoms are 1024 bytes)
     const uint32_t base = smem_addr(smem), bars = base + Sh::kOffBars;
-    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * Sh::kSlots, k_done = raw_empty + 8 * Sh::kSlots;
-    const uint32_t s_full = k_done + 8, p_ready = s_full + 16, o_full = p_ready + 16, o_free = o_full + 8;
-    const uint32_t mfinal = o_free + 8, q_staged = mfinal + 8, place_ready = q_staged + 8, place_free = place_ready + 24, scaled = place_free + 24;  // up to 33 barriers: 264 bytes
-    uint8_t *const words = smem + Sh::kOffBars + 272;
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * Sh::kSlots, scaled_k = raw_empty + 8 * Sh::kSlots;
+    const uint32_t scaled_v = scaled_k + 8 * Sh::kSlots, s_full = scaled_v + 8 * Sh::kSlots, p_ready = s_full + 16, o_full = p_ready + 16;
+    const uint32_t o_free = o_full + 16, mfinal = o_free + 8, q_open = mfinal + 16, q_staged = q_open + 8;
+    const uint32_t ready = q_staged + 8, free = ready + 32;  // of the slices' places: two of keys, two of values; up to 39 barriers: 312 bytes
+    uint8_t *const words = smem + Sh::kOffBars + 320;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(words);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(words + 4);
     volatile int *const groups = reinterpret_cast<volatile int *>(words + 16);     // [tile % 16]: its groups that lie in a page
-    // [tile % 8]: the scales' exponents (the warp that finds them is three tiles ahead of those that expand at most, and
-    // these two ahead of the softmax)
+    // [tile % 8]: the scales' exponents (the warp that finds them is five tiles ahead of those that expand values at most,
+    // and these two ahead of the values' sums)
     volatile int *const k_exp = reinterpret_cast<volatile int *>(words + 80);
     volatile int *const v_exp = reinterpret_cast<volatile int *>(words + 112);
     volatile float *const keep = reinterpret_cast<volatile float *>(smem + Sh::kOffKeep);
@@ -223,20 +274,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_empty + 8 * i, kExpanders);
-            mbar_init(scaled + 8 * i, 1);
+            mbar_init(scaled_k + 8 * i, 1);
+            mbar_init(scaled_v + 8 * i, 1);
         }
-        mbar_init(k_done, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_full + 8 * x, 1);
             mbar_init(p_ready + 8 * x, 4);
+            mbar_init(o_full + 8 * x, 1);
+            mbar_init(mfinal + 8 * x, 1);
         }
-        mbar_init(o_full, 1);
         mbar_init(o_free, 4);
-        mbar_init(mfinal, 1);
         mbar_init(q_staged, kExpanders);
-        for (int i = 0; i < Sh::kPlaces; ++i) {
-            mbar_init(place_ready + 8 * i, kExpanders);
-            mbar_init(place_free + 8 * i, 1);
+        mbar_init(q_open, kExpanders / 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(ready + 8 * i, kExpanders / 2);
+            mbar_init(free + 8 * i, 1);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -252,9 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
     pdl_wait_prior_grids();
     pdl_allow_dependents();
     const Units units(p, gridDim.x);
-    Stretch st;
-    st.u = blockIdx.x * units.share;
-    st.past = min(st.u + units.share, units.all);
+    Stretch st(units, blockIdx.x);
+    const int n_units = st.units;
     // A wait of a whole warp that gives up sets the abort flag, with which the others give up soon.
     auto failed = [&](int32_t code) {
         if (lane == 0) record_error(a.err, code);
@@ -262,134 +313,119 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
         __syncwarp();
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return static_cast<bool>(__all_sync(0xffffffffu, sleep_wait<20>(bar, parity & 1u, abort_flag)));
+        return static_cast<bool>(__all_sync(0xffffffffu, poll_wait<20>(bar, parity & 1u, abort_flag)));
     };
 
     if (warp < 4) {
         fewer_registers<kIssueRegs>();
         if (warp == 0) {
-            // ---------------- copies: of each unit the keys' codes and scales, then (a unit behind) the values'
-            int piece = 0, last = 0;  // pieces so far
+            // ---------------- copies: a unit's groups
             bool ok = true;
-            // this lane's group of a unit, as a byte offset in the cache; -1: none
-            auto source = [&](int item, int tile) -> int64_t {
-                const int t = tile * kTokens + 16 * (lane & 7);
-                if (t >= units.len) return -1;
-                const int page = __ldg(p.prefix_table + t / a.c.page_size);
-                if (page < 0 || page >= a.c.n_pages) {
-                    record_error(a.err, kErrBadIndex);
-                    return -1;
+            int n = 0;
+#pragma unroll 1
+            for (; n < n_units; ++n, st.step(units)) {
+                // this lane's group, as a byte offset in the cache; -1: none
+                int64_t src = -1;
+                const int t = st.tile * kTokens + 16 * (lane & 7);
+                if (t < units.len) {
+                    const int page = __ldg(p.prefix_table + t / a.c.page_size);
+                    if (page < 0 || page >= a.c.n_pages) record_error(a.err, kErrBadIndex);
+                    else src = ((static_cast<int64_t>(page) * a.c.n_heads + st.item / p.row_tiles) * a.c.page_groups + t % a.c.page_size / 16) * G::kBytes;
                 }
-                return ((static_cast<int64_t>(page) * a.c.n_heads + item / p.row_tiles) * a.c.page_groups + t % a.c.page_size / 16) * G::kBytes;
-            };
-            auto copy = [&](int64_t src, bool values) {
-                const int slot = piece % Sh::kSlots;
-                if (piece >= Sh::kSlots) ok = wait(raw_empty + 8 * slot, piece / Sh::kSlots - 1);
-                if (!ok) return;
+                const int slot = n % Sh::kSlots;
+                if (n >= Sh::kSlots) ok = wait(raw_empty + 8 * slot, n / Sh::kSlots - 1);
+                if (!ok) break;
                 const uint32_t valid = __ballot_sync(0xffffffffu, src >= 0) & 255u;
                 const uint32_t dst = base + Sh::kOffRaw + slot * Sh::kRaw, bar = raw_full + 8 * slot;
                 if (lane == 0) {
-                    if (!values) groups[last % 16] = static_cast<int>(valid);
-                    mbar_arrive_expect_tx(bar, __popc(valid) * (18 * D / 2));
+                    groups[n % 16] = static_cast<int>(valid);
+                    mbar_arrive_expect_tx(bar, __popc(valid) * G::kBytes);
                 }
                 __syncwarp();
-                if (src >= 0 && lane < 8)
-                    bulk_copy_g2s_plain(dst + lane * (8 * D), a.c.data + src + (values ? G::kV : 0), 8 * D, bar);
-                else if (src >= 0 && lane < 16)
-                    bulk_copy_g2s_plain(dst + Sh::kRawCodes + (lane & 7) * D, a.c.data + src + (values ? G::kVS : G::kKS), D, bar);
-                ++piece;
-            };
-            int64_t before = -1;  // the unit before's
-            bool any = false;
-            while (ok && st.next(units)) {
-                for (int j = 0; ok && j < st.n; ++j, ++last) {
-                    const int64_t src = source(st.item, st.tile + j);
-                    copy(src, false);
-                    if (ok && any) copy(before, true);
-                    before = src, any = true;
-                }
+                if (src >= 0 && lane < 8) bulk_copy_g2s_plain(dst + lane * G::kBytes, a.c.data + src, G::kBytes, bar);
             }
-            if (ok && any) copy(before, true);
             if (!ok) failed(kErrProducerWait);
             // leave no copy in flight into this block's shared memory
             bool landed = true;
-            for (int k = piece > Sh::kSlots ? piece - Sh::kSlots : 0; k < piece; ++k)
+            for (int k = n > Sh::kSlots ? n - Sh::kSlots : 0; k < n; ++k)
                 landed = mbar_wait_bounded(raw_full + 8 * (k % Sh::kSlots), (k / Sh::kSlots) & 1) && landed;
             if (!landed) record_error(a.err, kErrDrainWait);
             __syncwarp();
-        } else if (warp == 1) {
-            // ---------------- products (the whole warp, one lane issues)
+        } else if (warp != 2) {
+            // ---------------- products (the whole warp, one lane issues): S warp 1, O warp 3. A warp that issues stands
+            // still while the tensor cores' short queue is full, so that with one warp for both its waits and commits
+            // between the products would leave them idle.
             const uint32_t issue = lane == 0;
             constexpr uint32_t kIdS = tc_idesc_f16(128, kTokens), kIdO = tc_idesc_f16(128, D) | kIdescNMajorB;
             constexpr uint32_t kPart = Sh::kPart / 16;
-            const uint32_t q_low = desc_lo(base + Sh::kOffLow, 1);
-            const int units_in_all = static_cast<int>(st.past - st.u);
-            auto tight = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, tc_wait(bar, parity & 1u, abort_flag))); };
+            auto tight = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, poll_wait<0>(bar, parity & 1u, abort_flag))); };
             bool ok = true;
-            int n = 0;  // units so far
-            auto product_o = [&](int j) {
-                const int piece = Pieces::of_v(j, units_in_all), place = piece % Sh::kPlaces;
-                const uint32_t v = desc_lo(base + place * Sh::kPlace, 128 * 128 / 16);
-                ok = tight(p_ready + 8 * (j & 1), j >> 1) && tight(place_ready + 8 * place, piece / Sh::kPlaces) && (j == 0 || tight(o_free, j - 1));
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t w = tmem + 128 * (j & 1), w_low = tmem + kTmemLow;
-                // small terms first: what the tensor cores cut off at each sum is then of the small ones
-                // (one piece of code for them: what runs once a unit comes from instruction memory each time)
+            // small terms first: what the tensor cores cut off at each sum is then of the small ones
+            // (one piece of code for them: what runs once a unit comes from instruction memory each time)
+            if (warp == 1) {
+                for (int n = 0, i = 0; n < n_units; ++n) {
+                    const uint32_t s = tmem + 128 * (n & 1);
+                    ok = n < 2 || tight(o_full + 8 * (n & 1), (n - 2) >> 1);
 #pragma unroll 1
-                for (int i = 2 - TERMS; i < 3; ++i)
-                    mma_pv(issue, tmem + kTmemO, i == 0 ? w_low : w, i == 1 ? v + kPart : v, kIdO, i > 2 - TERMS, kDescHi);
-                commit(issue, place_free + 8 * place);
-                commit(issue, o_full);
-            };
-            while (ok && st.next(units)) {
-                for (int j = 0; ok && j < st.n; ++j, ++n) {
-                    const int piece = Pieces::of_k(n), place = piece % Sh::kPlaces;
-                    ok = tight(place_ready + 8 * place, piece / Sh::kPlaces);
+                    for (int h = 0; ok && h < Sh::kSlices; ++h, ++i) {
+                        ok = tight(ready + 8 * (i & 1), i >> 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t k = desc_lo(base + (i & 1) * Sh::kSlice, 1);
+                        if (TERMS == 2) mma_s<64>(issue, s, desc_lo(base + Sh::kOffLow + h * Sh::kPart, 1), k, kIdS, kDescHi, h > 0);
+#pragma unroll 1
+                        for (int t = 0; t < 2; ++t)
+                            mma_s_tm<64>(issue, s, tmem + kTmemQ + 32 * h, t == 0 ? k + kPart : k, kIdS, kDescHi, TERMS == 2 || h > 0 || t > 0);
+                        commit(issue, free + 8 * (i & 1));
+                    }
                     if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t s = tmem + 128 * (n & 1), k = desc_lo(base + place * Sh::kPlace, 1);
-                    if (TERMS == 2) mma_s<D>(issue, s, q_low, k, kIdS, kDescHi, 0);
-#pragma unroll 1
-                    for (int i = 0; i < 2; ++i)
-                        mma_s_tm<D>(issue, s, tmem + kTmemQ, i == 0 ? k + kPart : k, kIdS, kDescHi, TERMS == 2 || i > 0);
                     commit(issue, s_full + 8 * (n & 1));
-                    commit(issue, place_free + 8 * place);
-                    commit(issue, k_done);
-                    if (n > 0) product_o(n - 1);
+                }
+            } else {
+                for (int n = 0, i = 0; n < n_units; ++n) {
+                    ok = tight(p_ready + 8 * (n & 1), n >> 1) && (n == 0 || tight(o_free, n - 1));
+#pragma unroll 1
+                    for (int h = 0; ok && h < Sh::kSlices; ++h, ++i) {
+                        ok = tight(ready + 16 + 8 * (i & 1), i >> 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t v = desc_lo(base + Sh::kOffV + (i & 1) * Sh::kSlice, Sh::kSliceTokens * 128 / 16);
+                        const uint32_t w = tmem + 128 * (n & 1) + 32 * h, w_low = tmem + kTmemLow + 32 * h;
+#pragma unroll 1
+                        for (int t = 2 - TERMS; t < 3; ++t)
+                            mma_pv<Sh::kSliceTokens>(issue, tmem + kTmemO, t == 0 ? w_low : w, t == 1 ? v + kPart : v, kIdO, h > 0 || t > 2 - TERMS, kDescHi);
+                        commit(issue, free + 16 + 8 * (i & 1));
+                    }
+                    if (!ok) break;
+                    commit(issue, o_full + 8 * (n & 1));
                 }
             }
-            if (ok && n > 0) product_o(n - 1);
             if (!ok) failed(kErrConsumerWait);
-            commit(issue, mfinal);  // every product complete before tensor memory is freed, after a wait that gave up, too
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(mfinal, 0)) && issue) record_error(a.err, kErrDrainWait);
+            // every product complete before tensor memory is freed, after a wait that gave up, too
+            const uint32_t end = mfinal + 4 * (warp & 2);
+            commit(issue, end);
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(end, 0)) && issue) record_error(a.err, kErrDrainWait);
             __syncwarp();
-        } else if (warp == 2) {
+        } else {
             // ---------------- scales, in place
             bool ok = true;
-            int n = 0, piece = 0, before = 0;
-            auto prepare = [&](int j, int tile, bool values) {
-                const int slot = piece % Sh::kSlots;
-                ok = wait(raw_full + 8 * slot, piece / Sh::kSlots);
-                if (!ok) return;
-                const int e = prepare_scales<D>(smem + Sh::kOffRaw + slot * Sh::kRaw + Sh::kRawCodes,
-                                                min(kTokens, units.len - tile * kTokens), static_cast<uint32_t>(groups[j % 16]));
-                fence_proxy_async_smem();  // (the next copy to this place comes after these writes)
-                __syncwarp();
-                if (lane == 0) {
-                    (values ? v_exp : k_exp)[j & 7] = e;
-                    mbar_arrive(scaled + 8 * slot);
-                }
-                ++piece;
-            };
-            while (ok && st.next(units)) {
-                for (int j = 0; ok && j < st.n; ++j, ++n) {
-                    prepare(n, st.tile + j, false);
-                    if (ok && n > 0) prepare(n - 1, before, true);
-                    before = st.tile + j;
+#pragma unroll 1
+            for (int n = 0; n < n_units; ++n, st.step(units)) {
+                const int slot = n % Sh::kSlots;
+                ok = wait(raw_full + 8 * slot, n / Sh::kSlots);
+                if (!ok) break;
+#pragma unroll 1
+                for (int values = 0; values < 2; ++values) {
+                    const int e = prepare_scales<D>(smem + Sh::kOffRaw + slot * Sh::kRaw + (values ? G::kVS : G::kKS),
+                                                    min(kTokens, units.len - st.tile * kTokens), static_cast<uint32_t>(groups[n % 16]));
+                    fence_proxy_async_smem();  // (the next copy to this place comes after these writes)
+                    __syncwarp();
+                    if (lane == 0) {
+                        (values ? v_exp : k_exp)[n & 7] = e;
+                        mbar_arrive((values ? scaled_v : scaled_k) + 8 * slot);
+                    }
                 }
             }
-            if (ok && n > 0) prepare(n - 1, before, true);
             if (!ok) failed(kErrConsumerWait);
         }
     } else if (warp < 8) {
@@ -445,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                 keep[(n & 3) * kRows + row] = down;
                 const float r = ref == -INFINITY ? 0.0f : ref;  // (no token seen yet: weights of 0)
                 const float2 c2 = make_float2(c, c), r2 = make_float2(-r, -r);
-                if (TERMS == 2 && n > 0) ok = wait(o_full, n - 1);  // the low parts' place is one
+                if (TERMS == 2 && n > 0) ok = wait(o_full + 8 * ((n - 1) & 1), (n - 1) >> 1);  // the low parts' place is one
                 if (!ok) break;
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
@@ -487,14 +523,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
 #pragma unroll
             for (int i = 0; i < D / 2; ++i) o[i] = make_float2(0.0f, 0.0f);
             for (int j = 0; j < st.n; ++j, ++n) {
-                ok = wait(o_full, n);
+                ok = wait(o_full + 8 * (n & 1), n >> 1);
                 if (!ok) break;
                 tc_fence_after();
                 const float f = keep[(n & 3) * kRows + row], u = __uint_as_float(static_cast<uint32_t>(127 - v_exp[n & 7]) << 23);
                 const float2 u2 = make_float2(u, u);
-                if (__any_sync(0xffffffffu, f != 1.0f))
+                if (__any_sync(0xffffffffu, f != 1.0f)) {
+                    const float2 f2 = make_float2(f, f);
 #pragma unroll
-                    for (int i = 0; i < D / 2; ++i) o[i].x *= f, o[i].y *= f;
+                    for (int i = 0; i < D / 2; ++i) o[i] = fmul2(o[i], f2);
+                }
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t v[32];
@@ -523,121 +561,158 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
     } else {
         // ---------------- codes to operands
         fewer_registers<kExpandRegs>();
+        // four warps the keys', four the values': what one side waits for (operands that are on their way to shared memory,
+        // places) does not keep the other
         const int w = warp - 12;
+        const bool values = w >= kExpanders / 2;
+        constexpr bool kHalves = D == 128;
+        // Rows of a warp, 32 apart: so that eight lanes that store together have eight different chunk places. A lane takes
+        // four words at a time: of keys those of blocks 2 h and 2 h + 1 (h the slice) in two rows, to chunks part and
+        // 4 + part; of values two units of both block pairs in one row, or of D = 64's one in two.
+        const int part = lane & 3, x = lane >> 2, row_x = 8 * (w & 3) + (values ? x : (x & 1) * 4 + (x >> 1)), vr = kv_value_row(row_x & 15);
+        const int group_at = (row_x >> 4) * G::kBytes;
+        const int codes_at = group_at + (values ? G::kV + vr * G::kRow + (part ^ (vr & 2)) * (4 * NB) : (row_x & 15) * G::kRow + part * (4 * NB));
+        const int scales_at = group_at + (values ? G::kVS : G::kKS) + (row_x & 15) * G::kScaleRow;
+        const int first = row_x * 128 + (((values ? 2 * part : part) ^ (row_x & 7)) << 4);
+        const int second = row_x * 128 + (((values ? 2 * part + 1 : part + 4) ^ (row_x & 7)) << 4);
+        const bool pairs = kHalves && values;  // both block pairs, and a row in two turns
+        const uint32_t even = values ? 0x3210 : 0x1010, odd = values ? 0x3210 : 0x3232;
+        const uint32_t my_ready = ready + (values ? 16 : 0), my_free = free + (values ? 16 : 0), my_scaled = values ? scaled_v : scaled_k;
         bool ok = true;
-        int n = 0, piece = 0;
-        // a piece's operands, once `free` is: 128-byte rows of 64 channels, 16-byte chunks swizzled by the row
-        auto expand = [&](bool values) {
-            const int slot = piece % Sh::kSlots;
-            ok = wait(scaled + 8 * slot, piece / Sh::kSlots) && wait(raw_full + 8 * slot, piece / Sh::kSlots);
-            // (a barrier a place: its last piece's products are complete)
-            if (ok && piece >= Sh::kPlaces) ok = wait(place_free + 8 * (piece % Sh::kPlaces), piece / Sh::kPlaces - 1);
+        int n = 0;
+        // slice i, half h of unit n
+        auto expand = [&](int i, int h) {
+            const int slot = n % Sh::kSlots;
+            if (h == 0) ok = wait(my_scaled + 8 * slot, n / Sh::kSlots) && wait(raw_full + 8 * slot, n / Sh::kSlots);
+            if (ok && i >= 2) ok = wait(my_free + 8 * (i & 1), (i - 2) >> 1);
             if (!ok) return;
             const uint8_t *const raw = smem + Sh::kOffRaw + slot * Sh::kRaw;
-            // Rows of a warp: so that eight lanes that store together have eight different chunk places, and the same for
-            // both of its turns, 64 rows on (8 groups' rows 4 by 4 KB: one address and constants).
-            const int part = lane & 3, x = lane >> 2, row = 8 * w + (values ? x : (x & 1) * 4 + (x >> 1)), vr = kv_value_row(row & 15);
-            const uint8_t *codes = raw + (values ? ((row & ~15) + vr) * G::kRow + (part ^ (vr & 2)) * (4 * NB) : row * G::kRow + part * (4 * NB));
-            const uint8_t *scales = raw + Sh::kRawCodes + row * G::kScaleRow;
-            uint8_t *const to = smem + piece % Sh::kPlaces * Sh::kPlace + row * 128;
-            // Keys: block b's word goes to chunk 4 (b % 2) + part of half b / 2; values: units 2 part and 2 part + 1 of block
-            // pair h to half h. One piece of code for both, see the softmax's loops.
-            uint8_t *const first = to + (((values ? 2 * part : part) ^ (row & 7)) << 4);
-            uint8_t *const second = to + (((values ? 2 * part + 1 : part + 4) ^ (row & 7)) << 4);
-            uint8_t *const inner[2] = {values ? first + 128 * 128 : second, values ? second : first + 128 * 128};  // (of four words the second and third)
-            const uint32_t even = values ? 0x3210 : 0x1010, odd = values ? 0x3210 : 0x3232;
+            uint8_t *const to = smem + (values ? Sh::kOffV : 0) + (i & 1) * Sh::kSlice;
+            const uint8_t *codes = raw + codes_at + (pairs ? h * (4 * G::kBytes) : kHalves ? 8 * h : 0);
+            const uint8_t *scales = raw + scales_at + (pairs ? h * (4 * G::kBytes) : kHalves ? 4 * h : 0);
+            uint32_t c[2][2], d[2], c_next[2][2], d_next[2];
+            auto load = [&]() {
+                ld_words<2>(codes, c_next[0]);
+                ld_words<2>(codes + (pairs ? 8 : 2 * G::kBytes), c_next[1]);
+                d_next[0] = *reinterpret_cast<const uint32_t *>(scales);
+                d_next[1] = *reinterpret_cast<const uint32_t *>(scales + (pairs ? 4 : 2 * G::kBytes));
+                codes += pairs ? 2 * G::kBytes : 4 * G::kBytes, scales += pairs ? 2 * G::kBytes : 4 * G::kBytes;
+            };
+            uint8_t *a = to + first, *b = to + (pairs ? first + Sh::kSliceTokens * 128 : second);
+            const int next = pairs ? second - first : 32 * 128;  // (of pairs b - a is the same for both)
+            load();
 #pragma unroll 1
-            for (int it = 0; it < 2; ++it) {
-                uint32_t c[NB], d[NB / 2];
-                ld_words<NB>(codes + it * (64 * G::kRow), c);
-                ld_halves<NB>(scales + it * (64 * G::kScaleRow), d);
+            for (int s = 0; s < 2; ++s) {
+                uint32_t low[2];
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const uint32_t pair = NB == 2 || i == 0 ? d[0] : i == 3 ? d[NB / 2 - 1] : (values == (i == 1)) ? d[NB / 2 - 1] : d[0];
-                    const uint32_t s2 = __byte_perm(pair, 0, i & 1 ? odd : even);
-                    uint8_t *t = (i == 0 ? first : NB == 2 ? second : i == 3 ? second + 128 * 128 : inner[i - 1]) + it * (64 * 128);
-                    expand_word(c[i], *reinterpret_cast<const __half2 *>(&s2), t, t + Sh::kPart);
+                for (int k = 0; k < 2; ++k) {
+                    c[k][0] = c_next[k][0], c[k][1] = c_next[k][1], d[k] = d_next[k];
+                    const __half2 all = *reinterpret_cast<const __half2 *>(&d[k]);
+                    d[k] &= 0xFFE0FFE0u;
+                    low[k] = bits(__hsub2(all, *reinterpret_cast<const __half2 *>(&d[k])));
                 }
+                if (s == 0) load();
+                auto two = [](uint32_t x, uint32_t select) {
+                    x = __byte_perm(x, 0, select);
+                    return *reinterpret_cast<const __half2 *>(&x);
+                };
+                const int x = pairs ? 1 : 0;  // (the scales of the first row's second word and of the second's first)
+                expand_word(c[0][0], two(d[0], even), two(low[0], even), a, a + Sh::kPart);
+                expand_word(c[0][1], two(x ? d[1] : d[0], odd), two(x ? low[1] : low[0], odd), b, b + Sh::kPart);
+                expand_word(c[1][0], two(x ? d[0] : d[1], even), two(x ? low[0] : low[1], even), a + next, a + next + Sh::kPart);
+                expand_word(c[1][1], two(d[1], odd), two(low[1], odd), b + next, b + next + Sh::kPart);
+                a += pairs ? 32 * 128 : 64 * 128, b += pairs ? 32 * 128 : 64 * 128;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(raw_empty + 8 * slot);
-                mbar_arrive(place_ready + 8 * (piece % Sh::kPlaces));
+                if (h == Sh::kSlices - 1) mbar_arrive(raw_empty + 8 * slot);
+                mbar_arrive(my_ready + 8 * (i & 1));
             }
-            ++piece;
         };
         while (ok && st.next(units)) {
-            // ---- the stretch's queries, in the keys' order of channels, once the last one's products are complete
-            // (the low parts' place is read by those products, tensor memory too; the high ones pass through the place of
-            // the piece that comes next, K(n))
-            const int place = piece % Sh::kPlaces;
-            if (n > 0) ok = wait(k_done, n - 1) && (piece < Sh::kPlaces || wait(place_free + 8 * place, piece / Sh::kPlaces - 1));
+            // ---- the stretch's queries, in the keys' order of channels: they come through the key slices' places, once the
+            // last one's products are complete, as the key warps see
+            const int i0 = n * Sh::kSlices;
+            if (!values) {
+                ok = (i0 < 2 || wait(free + 8 * (i0 & 1), (i0 - 2) >> 1)) && (i0 < 1 || wait(free + 8 * ((i0 - 1) & 1), (i0 - 1) >> 1));
+                if (ok && lane == 0) mbar_arrive(q_open);
+            }
+            if (ok) ok = wait(q_open, st.index);
             if (!ok) break;
-            uint8_t *const staged = smem + place * Sh::kPlace;
             const int head = st.item / p.row_tiles, row0 = st.item % p.row_tiles * kRows;
-            constexpr int kLanes = D / 8, kStep = 8 * 32 / kLanes;  // lanes of a row, rows of the eight warps
-            const int chunk = lane % kLanes, b = chunk >> 2, t = chunk & 3;
-#pragma unroll 2
-            for (int r0 = 0; r0 < kRows; r0 += kStep) {
-                const int r = r0 + w * (32 / kLanes) + lane / kLanes, row = row0 + r, tok = row / a.group;
-                float x[8] = {};
-                if (tok < a.n_tok)
-                    load8(static_cast<const T *>(a.q) + tok * a.q_stride + (static_cast<int64_t>(head) * a.group + row - tok * a.group) * D + 32 * b + 4 * t, x);
+            constexpr int kRowBytes = D * static_cast<int>(sizeof(T)), kChunks = kRowBytes / 16, kAtOnce = kExpanders * 32 / kChunks;
+#pragma unroll 1
+            for (int r = w * (32 / kChunks) + lane / kChunks; r < kRows; r += kAtOnce) {
+                const int k = lane % kChunks, row = row0 + r, tok = row / a.group;
+                const bool there = tok < a.n_tok;
+                const T *src = static_cast<const T *>(a.q);
+                if (there) src += tok * a.q_stride + (static_cast<int64_t>(head) * a.group + row - tok * a.group) * D + k * (16 / sizeof(T));
+                copy16_or_zeros(base + r * kRowBytes + ((k ^ (r & 7)) << 4), src, there);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_staged);
+            ok = wait(q_staged, 0);
+            if (!ok) break;
+            if (w < 4 * Sh::kSlices) {  // 64 channels of a row a thread
+                const int r = 32 * (w & 3) + lane, h = w >> 2;
+                const uint8_t *const mine = smem + r * kRowBytes;
+                auto chunk = [&](int k) { return mine + ((k ^ (r & 7)) << 4); };
                 float up = a.scale < 0.0f ? -1.0f : 1.0f, back = fabsf(a.scale) * 1.4426950408889634f;
                 if (TERMS == 2) {  // the largest magnitude to 2^10 .. 2^11
                     float big = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[i]));
-#pragma unroll
-                    for (int m = 1; m < kLanes; m <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
+#pragma unroll 2
+                    for (int k = 0; k < kChunks; ++k) {
+                        const float4 x = *reinterpret_cast<const float4 *>(chunk(k));
+                        big = fmaxf(fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+                    }
                     int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
                     if (e == 128) e = 0;         // infinities
                     if (e < -117) e = -117;      // (2^(10 - e) is an f32)
                     up *= __uint_as_float(static_cast<uint32_t>(137 - e) << 23);
                     back *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * 0x1p-10f;
                 }
-                if (chunk == 0) factor[(st.index & 3) * kRows + r] = fmaxf(back, 1e-37f);  // never 0, which times -inf would be NaN
-                uint32_t h[4], l[4];
+                if (h == 0) factor[(st.index & 3) * kRows + r] = fmaxf(back, 1e-37f);  // never 0, which times -inf would be NaN
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    const int e = 64 * h + 32 * (i >> 2) + 4 * (i & 3);  // the first element
+                    float x[8];
+                    if constexpr (TERMS == 2) {
+                        const float4 y = *reinterpret_cast<const float4 *>(chunk(e / 4)), z = *reinterpret_cast<const float4 *>(chunk(e / 4 + 4));
+                        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w, x[4] = z.x, x[5] = z.y, x[6] = z.z, x[7] = z.w;
+                    } else {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(chunk(e / 8) + 2 * (e & 7)), z = *reinterpret_cast<const uint2 *>(chunk(e / 8 + 2) + 2 * (e & 7));
+                        const uint32_t two[4] = {y.x, y.y, z.x, z.y};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // elements 0 2 | 1 3 | 16 18 | 17 19
-                    const int i0 = (i & 2) * 2 + (i & 1);
-                    const float y = x[i0] * up, z = x[i0 + 2] * up;
-                    h[i] = pack_half2(y, z);
-                    const float2 f = unpack_half2(h[i]);
-                    l[i] = pack_half2(y - f.x, z - f.y);
-                }
-                const int to = (chunk >> 3) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4 *>(staged + to) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (TERMS == 2) *reinterpret_cast<uint4 *>(smem + Sh::kOffLow + to) = make_uint4(l[0], l[1], l[2], l[3]);
-            }
-            {  // to tensor memory: a row's 64 channels a thread
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_staged);
-                ok = wait(q_staged, 0);
-                if (!ok) break;
-                const int r = 32 * (w & 3) + lane, h = w >> 2;
-                if (h < D / 64) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(staged + h * (128 * 128) + r * 128 + ((i ^ (r & 7)) << 4));
-                        v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+                        for (int k = 0; k < 4; ++k) x[2 * k] = unpack_half2(two[k]).x, x[2 * k + 1] = unpack_half2(two[k]).y;
                     }
-                    tc_st32(tmem + (static_cast<uint32_t>(32 * (w & 3)) << 16) + kTmemQ + 32 * h, v);
-                    tc_wait_st();
-                    tc_fence_before();
+                    uint32_t high[4], low[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // elements 0 2 | 1 3 | 16 18 | 17 19
+                        const int k0 = (k & 2) * 2 + (k & 1);
+                        const float y = x[k0] * up, z = x[k0 + 2] * up;
+                        high[k] = pack_half2(y, z);
+                        const float2 f = unpack_half2(high[k]);
+                        low[k] = pack_half2(y - f.x, z - f.y);
+                    }
+                    tc_st4(tmem + (static_cast<uint32_t>(32 * (w & 3)) << 16) + kTmemQ + 32 * h + 4 * i, high);
+                    if (TERMS == 2)
+                        *reinterpret_cast<uint4 *>(smem + Sh::kOffLow + h * Sh::kPart + r * 128 + ((i ^ (r & 7)) << 4)) = make_uint4(low[0], low[1], low[2], low[3]);
                 }
-                // K(n) takes the place when every warp has read its rows
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_staged);
-                ok = wait(q_staged, 1);
+                tc_wait_st();
+                tc_fence_before();
+                if (TERMS == 2) fence_proxy_async_smem();
             }
+            // slices take the places when every warp has read its rows
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_staged);
+            ok = wait(q_staged, 1);
             for (int j = 0; ok && j < st.n; ++j, ++n) {
-                for (int values = 0; ok && values < (n > 0 ? 2 : 1); ++values) expand(values != 0);
+#pragma unroll 1
+                for (int h = 0; ok && h < Sh::kSlices; ++h) expand(n * Sh::kSlices + h, h);
             }
         }
-        if (ok && n > 0) expand(true);
         if (!ok) failed(kErrConsumerWait);
     }
     tc_fence_before();
@@ -700,7 +775,9 @@ template <int D, class T> __global__ void __launch_bounds__(kJoinThreads) shared
         if (units.tiles > 0) {
             const int item = kv * p.row_tiles + row / kRows;
             const int64_t u = static_cast<int64_t>(item) * units.tiles;
-            const int c0 = static_cast<int>(u / units.share), n = static_cast<int>((u + units.tiles - 1) / units.share) - c0 + 1;
+            const int c0 = units.per_item > 0 ? item * units.per_item : static_cast<int>(u / units.share);
+            const int n = units.per_item > 0 ? (units.tiles + static_cast<int>(units.share) - 1) / static_cast<int>(units.share)
+                                             : static_cast<int>((u + units.tiles - 1) / units.share) - c0 + 1;
             const float *const first = p.stretches + (c0 + static_cast<int64_t>(item)) * stretch_floats(D);
             for (int c = 0; c < n; c += kAhead) {
                 float2 s[kAhead];

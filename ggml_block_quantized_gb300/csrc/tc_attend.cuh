@@ -86,37 +86,56 @@ template <int D> __device__ __forceinline__ void mma_s_tm(uint32_t issue, uint32
             "}" ::"r"(d), "r"(a + 32 * h), "r"(b + 1024 * h), "r"(idesc), "r"(h == 0 ? acc : 1u), "r"(issue), "r"(hi)
             : "memory");
 }
-// O (+)= P V: 16 keys a product, 8 columns of P and 2 KB of V.
-__device__ __forceinline__ void mma_pv(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t hi) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "setp.ne.u32 p, 1, 0;\n\t"
-        "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "add.u32 a, %1, 32;\n\tadd.u32 b, %2, 512;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "add.u32 a, %1, 40;\n\tadd.u32 b, %2, 640;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "add.u32 a, %1, 48;\n\tadd.u32 b, %2, 768;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "add.u32 a, %1, 56;\n\tadd.u32 b, %2, 896;\n\t"
-        "mov.b64 db, {b, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
-        "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(issue), "r"(hi)
-        : "memory");
+// O (+)= P V: 16 keys a product, 8 columns of P and 2 KB of V; 128 keys, or 64.
+template <int KEYS = 128> __device__ __forceinline__ void mma_pv(uint32_t issue, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t hi) {
+    if (KEYS == 64)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "setp.ne.u32 p, 1, 0;\n\t"
+            "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(issue), "r"(hi)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "mov.b32 a, %1;\n\tmov.b32 b, %2;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "setp.ne.u32 p, 1, 0;\n\t"
+            "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 32;\n\tadd.u32 b, %2, 512;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 40;\n\tadd.u32 b, %2, 640;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 48;\n\tadd.u32 b, %2, 768;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "add.u32 a, %1, 56;\n\tadd.u32 b, %2, 896;\n\t"
+            "mov.b64 db, {b, %6};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+            "}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(issue), "r"(hi)
+            : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t issue, uint32_t bar) {
     asm volatile(

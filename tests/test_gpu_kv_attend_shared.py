@@ -141,6 +141,31 @@ def test_the_same_as_one_cache():
     assert (a - b).abs().max() < 2e-6 * b.abs().max()
 
 
+@pytest.mark.parametrize("t,d", [("f32", 64), ("f16", 64), ("f32", 128), ("f16", 128)])
+@pytest.mark.parametrize("seqs,group,hk", [(9, 16, 97), (60, 16, 13), (20, 64, 16), (16, 64, 1)])
+@pytest.mark.parametrize("pages", [1, 12, 45])
+def test_parts_of_many_items(t, d, seqs, group, hk, pages):
+    """Thread blocks that go from one head's or rows' tiles to the next ones', and items of one block each: what
+    qkv_attend gives on whole tables, within both calls' bounds (each is held to 64 bits elsewhere; a score's error and
+    a weight's are those of attn_ref.bound, 2^-17 of the largest value here, and two roundings to f16)."""
+    rng = np.random.default_rng(pages * seqs)
+    page = 128
+    table = torch.arange((pages + seqs), dtype=torch.int32, device="cuda")
+    cache = qg.KVCache.empty(pages + seqs, hk, d, page)
+    n = (pages + seqs) * page
+    for s in range(0, n, 2048):
+        m = min(2048, n - s)
+        kv = torch.from_numpy(rng.standard_normal((2, m, hk, d)).astype(np.float32)).cuda()
+        qg.kv_append(cache, kv[0], kv[1], torch.arange(s, s + m, dtype=torch.int32, device="cuda"))
+    lens = i32(rng.integers(1, page, seqs))
+    q = torch.from_numpy(rng.standard_normal((seqs, hk * group, d)).astype(np.float32)).cuda().to(TYPES[t])
+    own = table[pages:, None].contiguous()
+    got = qg.kv_attend_shared(cache, q, table[:pages], i32([pages * page]), own, lens)
+    want = qg.kv_attend(cache, q, torch.cat([table[None, :pages].expand(seqs, -1), own], 1).contiguous(), lens + pages * page)
+    off = (got.double() - want.double()).abs().max()
+    assert off < 4 * 2.0 ** -17 + (2 * 2.0 ** -11 * want.double().abs().max() if t == "f16" else 0), off
+
+
 def test_strided_queries_out_and_stream():
     rng = np.random.default_rng(19)
     lens = [130, 64, 9]
