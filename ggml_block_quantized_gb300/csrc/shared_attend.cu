@@ -170,12 +170,20 @@ template <int NB> __device__ __forceinline__ void ld_halves(const uint8_t *p, ui
     }
 }
 
-// One word of a row: eight values as two f16 parts, 16 bytes of each. The parts are the code times the scale's first six
-// significant bits and times its other five, so that both hold them exactly.
-__device__ __forceinline__ void expand_word(uint32_t w, __half2 scale, __half2 scale_low, uint8_t *high, uint8_t *low) {
-    const __half2 a = low_codes(w), b = low_codes(w >> 8), c = high_codes(w), d = high_codes(w >> 8);
-    *reinterpret_cast<uint4 *>(high) = make_uint4(bits(__hmul2(a, scale)), bits(__hmul2(b, scale)), bits(__hmul2(c, scale)), bits(__hmul2(d, scale)));
-    *reinterpret_cast<uint4 *>(low) = make_uint4(bits(__hmul2(a, scale_low)), bits(__hmul2(b, scale_low)), bits(__hmul2(c, scale_low)), bits(__hmul2(d, scale_low)));
+// One word of a row: eight values as two f16 parts, 16 bytes of each: the value rounded to f16, and what that leaves with
+// its sign turned (minus is the scale's negative), which the products turn back. Above f16's end two parts hold it exactly
+// (four bits times eleven). The low part is at most 2^-11 of the high one: f32 drops low times low.
+__device__ __forceinline__ void expand_word(uint32_t w, __half2 scale, __half2 minus, uint8_t *high, uint8_t *low) {
+    const __half2 c[4] = {low_codes(w), low_codes(w >> 8), high_codes(w), high_codes(w >> 8)};
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 x = __hmul2(c[i], scale);
+        h[i] = bits(x);
+        l[i] = bits(__hfma2(c[i], minus, x));
+    }
+    *reinterpret_cast<uint4 *>(high) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(low) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 // Makes a unit's raw scales (keys' or values') ready: 0 for tokens that do not count (rows past `rows`, groups in no
@@ -360,44 +368,60 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             constexpr uint32_t kPart = Sh::kPart / 16;
             auto tight = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, poll_wait<0>(bar, parity & 1u, abort_flag))); };
             bool ok = true;
-            // small terms first: what the tensor cores cut off at each sum is then of the small ones
-            // (one piece of code for them: what runs once a unit comes from instruction memory each time)
+            // Small terms first: what the tensor cores cut off at each sum is then of the small ones. For f32 that holds
+            // over both slices of a unit (slice by slice its error was up to twice as large), which wait for each other
+            // then; f16 results, rounded to 2^-11, take them as they come.
+            // (loops rolled: what runs once a unit comes from instruction memory each time)
+            auto of_unit = [&](int i, uint32_t bars, auto &&low, auto &&high) {
+                auto come = [&](int h) {
+                    ok = ok && tight(bars + 8 * ((i + h) & 1), (i + h) >> 1);
+                    tc_fence_after();
+                    return ok;
+                };
+                if (TERMS == 2)
+#pragma unroll 1
+                    for (int h = 0; h < Sh::kSlices; ++h) {
+                        if (!come(h)) return;
+                        low(h, (i + h) & 1);
+                    }
+#pragma unroll 1
+                for (int h = 0; h < Sh::kSlices; ++h) {
+                    if (TERMS == 1) {
+                        if (!come(h)) return;
+                        low(h, (i + h) & 1);
+                    }
+                    high(h, (i + h) & 1);
+                    commit(issue, bars + 32 + 8 * ((i + h) & 1));  // (free)
+                }
+            };
             if (warp == 1) {
-                for (int n = 0, i = 0; n < n_units; ++n) {
+                for (int n = 0; ok && n < n_units; ++n) {
                     const uint32_t s = tmem + 128 * (n & 1);
                     ok = n < 2 || tight(o_full + 8 * (n & 1), (n - 2) >> 1);
-#pragma unroll 1
-                    for (int h = 0; ok && h < Sh::kSlices; ++h, ++i) {
-                        ok = tight(ready + 8 * (i & 1), i >> 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t k = desc_lo(base + (i & 1) * Sh::kSlice, 1);
-                        if (TERMS == 2) mma_s<64>(issue, s, desc_lo(base + Sh::kOffLow + h * Sh::kPart, 1), k, kIdS, kDescHi, h > 0);
-#pragma unroll 1
-                        for (int t = 0; t < 2; ++t)
-                            mma_s_tm<64>(issue, s, tmem + kTmemQ + 32 * h, t == 0 ? k + kPart : k, kIdS, kDescHi, TERMS == 2 || h > 0 || t > 0);
-                        commit(issue, free + 8 * (i & 1));
-                    }
-                    if (!ok) break;
-                    commit(issue, s_full + 8 * (n & 1));
+                    of_unit(
+                        n * Sh::kSlices, ready,
+                        [&](int h, int place) {
+                            const uint32_t k = desc_lo(base + place * Sh::kSlice, 1);
+                            if (TERMS == 2) mma_s<64>(issue, s, desc_lo(base + Sh::kOffLow + h * Sh::kPart, 1), k, kIdS, kDescHi, h > 0);
+                            mma_s_tm<64>(issue, s, tmem + kTmemQ + 32 * h, k + kPart, kIdS | kIdescMinusB, kDescHi, TERMS == 2 || h > 0);
+                        },
+                        [&](int h, int place) { mma_s_tm<64>(issue, s, tmem + kTmemQ + 32 * h, desc_lo(base + place * Sh::kSlice, 1), kIdS, kDescHi, 1); });
+                    if (ok) commit(issue, s_full + 8 * (n & 1));
                 }
             } else {
-                for (int n = 0, i = 0; n < n_units; ++n) {
+                for (int n = 0; ok && n < n_units; ++n) {
+                    const uint32_t w = tmem + 128 * (n & 1), w_low = tmem + kTmemLow;
+                    auto desc = [&](int place) { return desc_lo(base + Sh::kOffV + place * Sh::kSlice, Sh::kSliceTokens * 128 / 16); };
                     ok = tight(p_ready + 8 * (n & 1), n >> 1) && (n == 0 || tight(o_free, n - 1));
-#pragma unroll 1
-                    for (int h = 0; ok && h < Sh::kSlices; ++h, ++i) {
-                        ok = tight(ready + 16 + 8 * (i & 1), i >> 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t v = desc_lo(base + Sh::kOffV + (i & 1) * Sh::kSlice, Sh::kSliceTokens * 128 / 16);
-                        const uint32_t w = tmem + 128 * (n & 1) + 32 * h, w_low = tmem + kTmemLow + 32 * h;
-#pragma unroll 1
-                        for (int t = 2 - TERMS; t < 3; ++t)
-                            mma_pv<Sh::kSliceTokens>(issue, tmem + kTmemO, t == 0 ? w_low : w, t == 1 ? v + kPart : v, kIdO, h > 0 || t > 2 - TERMS, kDescHi);
-                        commit(issue, free + 16 + 8 * (i & 1));
-                    }
-                    if (!ok) break;
-                    commit(issue, o_full + 8 * (n & 1));
+                    of_unit(
+                        n * Sh::kSlices, ready + 16,
+                        [&](int h, int place) {
+                            const uint32_t v = desc(place);
+                            if (TERMS == 2) mma_pv<Sh::kSliceTokens>(issue, tmem + kTmemO, w_low + 32 * h, v, kIdO, h > 0, kDescHi);
+                            mma_pv<Sh::kSliceTokens>(issue, tmem + kTmemO, w + 32 * h, v + kPart, kIdO | kIdescMinusB, TERMS == 2 || h > 0, kDescHi);
+                        },
+                        [&](int h, int place) { mma_pv<Sh::kSliceTokens>(issue, tmem + kTmemO, w + 32 * h, desc(place), kIdO, 1, kDescHi); });
+                    if (ok) commit(issue, o_full + 8 * (n & 1));
                 }
             }
             if (!ok) failed(kErrConsumerWait);
@@ -603,13 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
             load();
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
-                uint32_t low[2];
+                uint32_t minus[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     c[k][0] = c_next[k][0], c[k][1] = c_next[k][1], d[k] = d_next[k];
-                    const __half2 all = *reinterpret_cast<const __half2 *>(&d[k]);
-                    d[k] &= 0xFFE0FFE0u;
-                    low[k] = bits(__hsub2(all, *reinterpret_cast<const __half2 *>(&d[k])));
+                    minus[k] = d[k] ^ 0x80008000u;
                 }
                 if (s == 0) load();
                 auto two = [](uint32_t x, uint32_t select) {
@@ -617,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const SharedParams 
                     return *reinterpret_cast<const __half2 *>(&x);
                 };
                 const int x = pairs ? 1 : 0;  // (the scales of the first row's second word and of the second's first)
-                expand_word(c[0][0], two(d[0], even), two(low[0], even), a, a + Sh::kPart);
-                expand_word(c[0][1], two(x ? d[1] : d[0], odd), two(x ? low[1] : low[0], odd), b, b + Sh::kPart);
-                expand_word(c[1][0], two(x ? d[0] : d[1], even), two(x ? low[0] : low[1], even), a + next, a + next + Sh::kPart);
-                expand_word(c[1][1], two(d[1], odd), two(low[1], odd), b + next, b + next + Sh::kPart);
+                expand_word(c[0][0], two(d[0], even), two(minus[0], even), a, a + Sh::kPart);
+                expand_word(c[0][1], two(x ? d[1] : d[0], odd), two(x ? minus[1] : minus[0], odd), b, b + Sh::kPart);
+                expand_word(c[1][0], two(x ? d[0] : d[1], even), two(x ? minus[0] : minus[1], even), a + next, a + next + Sh::kPart);
+                expand_word(c[1][1], two(d[1], odd), two(minus[1], odd), b + next, b + next + Sh::kPart);
                 a += pairs ? 32 * 128 : 64 * 128, b += pairs ? 32 * 128 : 64 * 128;
             }
             fence_proxy_async_smem();

@@ -169,7 +169,7 @@ template <int NS> __device__ __forceinline__ bool sleep_wait(uint32_t bar, uint3
 // a k, and their leading stride is the one between 64-element parts of N.
 constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t start, uint32_t leading) { return ((start >> 4) & 0x3FFFu) | leading << 16; }
-constexpr uint32_t kIdescNMajorB = 1u << 16;
+constexpr uint32_t kIdescNMajorB = 1u << 16, kIdescMinusB = 1u << 14;  // (of the instruction descriptor)
 
 // 32 columns of this warp's 32 lanes, without the wait.
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&v)[32]) {
