@@ -307,6 +307,67 @@ def test_a_prefix_past_32_bits():
     check(got, q, [k[:n], k[320:360]], [v[:n], v[320:360]], n, [40], [1], 1, d ** -0.5, False)
 
 
+def batch(seed, t, d=128, hk=2, group=5, prefix=1500, seqs=7, page=32):
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(1, 90, seqs)]
+    cache, table, ks, vs = filled(rng, [prefix] + lens, hk, d, page)
+    q = torch.from_numpy(rng.standard_normal((seqs, hk * group, d)).astype(np.float32)).cuda().to(TYPES[t])
+    return cache, q, i32(table[0][:-(-prefix // page)]), i32([prefix]), i32(table[1:]), i32(lens)
+
+
+@pytest.mark.parametrize("t", ["f32", "f16"])
+def test_an_empty_prefix_table(t):
+    a = list(batch(7, t))
+    a[2], a[3] = a[2][:0], i32([0])
+    assert torch.equal(qg.kv_attend_shared(*a), qg.kv_attend_shared(*a[:2], i32([0]), *a[3:]))
+    want = qg.kv_attend(a[0], a[1], a[4], a[5])
+    assert (qg.kv_attend_shared(*a).double() - want.double()).abs().max() <= (2.0 ** -17 if t == "f32" else 2.0 ** -9) * want.abs().max()
+
+
+def test_what_lies_in_the_workspace_does_not_matter():
+    """Nor whose it was: two graphs of other shapes and a call on its own share one, each after the other."""
+    a, b = batch(8, "f32"), batch(9, "f16", 64, 3, 4, 700, 11, 16)
+    want = [qg.kv_attend_shared(*x) for x in (a, b)]
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.empty_like(x[1]) for x in (a, b)], []
+    side = torch.cuda.Stream()
+    for x, out in zip((a, b), outs):
+        with torch.cuda.stream(side):
+            qg.kv_attend_shared(*x, out=out, workspace=ws)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qg.kv_attend_shared(*x, out=out, workspace=ws)
+        graphs.append(g)
+    for k in (0, 1, 1, 0, 1, 0):
+        outs[k].fill_(float("nan"))
+        graphs[k].replay()
+        assert torch.equal(outs[k], want[k])
+        assert torch.equal(qg.kv_attend_shared(*(a, b)[1 - k], workspace=ws), want[1 - k])
+
+
+@pytest.mark.parametrize("t,d", [("f32", 64), ("f16", 64), ("f32", 128), ("f16", 128)])
+@pytest.mark.parametrize("hk,prefix,seqs", [(1, 20000, 30), (7, 3000, 60), (40, 1000, 60)])
+def test_the_same_bits_beside_other_work(t, d, hk, prefix, seqs):
+    """Many calls, two at a time on two streams and beside products that keep the multiprocessors busy now and then: the
+    roles of a block then run at other paces towards each other."""
+    a, b = batch(11, t, d, hk, 16, prefix, seqs, 64), batch(12, t, d, 2, 16, 900, 40, 16)
+    want = [qg.kv_attend_shared(*x) for x in (a, b)]
+    m = torch.randn(1024, 1024, device="cuda").half()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(12):
+        got = []
+        for x, s in zip((a, b), streams):
+            got.append([qg.kv_attend_shared(*x, stream=s) for _ in range(3)])
+        with torch.cuda.stream(streams[2]):
+            for _ in range(i % 4):
+                m @ m
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(x, w) for x in g)
+
+
 def test_refusals():
     cache = qg.KVCache.empty(4, 2, 128, 16)
     q, pt, pl, tab, ln = torch.zeros(2, 4, 128, device="cuda"), i32([0]), i32([9]), i32([[1], [2]]), i32([3, 4])

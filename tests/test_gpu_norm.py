@@ -211,3 +211,14 @@ def test_a_chain_into_a_product():
     xq = torch.empty(2 * qg.qtype_nbytes(qg.Q8_0, d), dtype=torch.uint8, device="cuda")
     h, x = run(a, x_out=torch.empty(2, d, device="cuda"), xq=xq, act_type=qg.Q8_0)
     assert torch.equal(qg.qgemv_xq(qg.Q4_0, W, xq, n_out, d, 2), qg.qgemv(qg.Q4_0, W, x, n_out, d, 2))
+
+
+def test_rows_past_32_bits():
+    """Rows of every matrix 2^28 elements apart: the last begins behind 2^31."""
+    apart, n, d = 1 << 28, 9, 96
+    far = lambda x: torch.empty(apart * (n - 1) + d, dtype=x.dtype, device="cuda").as_strided((n, d), (apart, 1)).copy_(x)  # noqa: E731
+    a = make(n, d, h=F16, y=F16, gate=None)
+    want = run(a)
+    b = dict(a, h=far(a["h"]), y=far(a["y"]))
+    got = run(b, h_out=far(torch.zeros_like(a["h"])))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -198,3 +198,14 @@ def test_streams_and_graphs():
 def test_no_rows():
     token, prob = qg.sample_tokens(torch.empty(0, 50, device="cuda"), torch.empty(0, device="cuda"))
     assert token.shape == (0,) and prob is None
+
+
+def test_rows_past_32_bits():
+    """Rows 2^28 elements apart: the last begins behind 2^31."""
+    apart, n, vocab = 1 << 28, 9, 1001
+    logits = torch.empty(apart * (n - 1) + vocab, dtype=torch.float16, device="cuda").as_strided((n, vocab), (apart, 1))
+    x, rng = rows(n, vocab, 77, dtype=torch.float16)
+    logits.copy_(x)
+    u, k = cuda(u01(rng, n), torch.float32), cuda([40] * n, torch.int32)
+    for kw in (dict(), dict(top_k=k), dict(top_p=torch.full((n,), 0.9, device="cuda"))):
+        assert torch.equal(qg.sample_tokens(logits, u, **kw)[0], qg.sample_tokens(x, u, **kw)[0])
