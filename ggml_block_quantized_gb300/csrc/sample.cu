@@ -67,7 +67,8 @@ struct Shared {
     uint64_t ahead[kList];            // weights before a token, and how many tokens
     uint32_t rank[kList];
     uint64_t segment[2 * kThreads];   // kept weights of kSegment logits
-    uint64_t warp_sum[kWarps];
+    uint64_t warp_sum[kWarps], warp_bins[kWarps][3];
+    struct { uint32_t lo, above, hi, up_to; } range;
     uint64_t block_sum[2][kMaxCluster][2];
     float2 extremes[kWarps];
     float2 block_extremes[kMaxCluster];
@@ -126,6 +127,11 @@ template <> struct Eight<float> {
     float4 v[2];
     using Extremes = Extremes32;
     __device__ __forceinline__ float2 pair(int i) const { return i & 1 ? make_float2(v[i >> 1].z, v[i >> 1].w) : make_float2(v[i >> 1].x, v[i >> 1].y); }
+    __device__ __forceinline__ float2 next() {  // the first pair; the others move up
+        const float2 l = make_float2(v[0].x, v[0].y);
+        v[0] = make_float4(v[0].z, v[0].w, v[1].x, v[1].y), v[1].x = v[1].z, v[1].y = v[1].w;
+        return l;
+    }
 };
 template <> struct Eight<__half> {
     uint4 v[1];
@@ -133,6 +139,11 @@ template <> struct Eight<__half> {
     __device__ __forceinline__ float2 pair(int i) const {
         const uint32_t w = i == 0 ? v[0].x : i == 1 ? v[0].y : i == 2 ? v[0].z : v[0].w;
         return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    __device__ __forceinline__ float2 next() {
+        const float2 l = pair(0);
+        v[0].x = v[0].y, v[0].y = v[0].z, v[0].z = v[0].w;
+        return l;
     }
 };
 
@@ -200,6 +211,34 @@ struct Weigher {
 __device__ __forceinline__ float place_in_bins(float l, float m, float scale) { return fminf(fmaxf((m - l) * scale, 0.0f), kBins - 1.0f); }
 __device__ __forceinline__ uint32_t bin_of_place(float x) { return __float_as_uint(__fadd_rz(x, 8388608.0f)) & (kBins - 1u); }
 __device__ __forceinline__ uint32_t bin_of(float l, float m, float scale) { return bin_of_place(place_in_bins(l, m, scale)); }
+
+// The least logits whose bins are a or less, and b or less (NaN where b is -1): bins never fall as logits fall, so each half
+// of a warp searches the keys, 16 at a time.
+__device__ __forceinline__ void least_of_bins(uint32_t a, uint32_t b, float m, float scale, float &of_a, float &of_b) {
+    const uint32_t half = threadIdx.x >> 4 & 1u, k = threadIdx.x & 15u, bin = half ? b + (b == ~0u) : a;
+    // from the edge's place with a bin and two keys to spare on (m's bin is 0)
+    uint32_t lo = key_of(-INFINITY), hi = key_of(m);
+    if (m < INFINITY) {
+        if (bin + 1 < kBins) lo = max(lo, key_of(m - (bin + 2) / scale) - 2u);
+        hi = min(hi, max(lo, key_of(m - bin / scale) + 2u));
+    }
+#pragma unroll 1
+    while (__any_sync(0xffffffffu, lo != hi)) {
+        const uint32_t step = (hi - lo) / 16u + 1u;
+        const uint32_t yes = __ballot_sync(0xffffffffu, bin_of(logit_of(min(lo + k * step, hi)), m, scale) <= bin) >> (16u * half) & 0xFFFFu;
+        const uint32_t first = yes ? __ffs(yes) - 1u : 16u;
+        if (first == 0) hi = lo;
+        else {
+            if (first < 16) hi = min(lo + first * step, hi);
+            lo += (first - 1) * step + 1;
+        }
+    }
+    of_a = logit_of(__shfl_sync(0xffffffffu, lo, 0));
+    of_b = b == ~0u ? NAN : logit_of(__shfl_sync(0xffffffffu, lo, 16));
+}
+__device__ __forceinline__ void add_if(bool yes, uint32_t shared, uint32_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], %2;\n\t}" ::"r"(static_cast<uint32_t>(yes)), "r"(shared), "r"(v) : "memory");
+}
 
 // floor(v f) for 0 <= f <= 1, exact, and whether it was cut off.
 __device__ __forceinline__ uint64_t times(uint64_t v, float f, bool &rest) {
@@ -593,11 +632,11 @@ template <class Tokens> struct Search : Tokens {
 };
 
 // The weights' sum of a set (no logit of infinity).
-template <class T> __device__ __forceinline__ uint64_t weigh_set(const Eight<T> &e, const Weigher &weigh) {
+template <class T> __device__ __forceinline__ uint64_t weigh_set(Eight<T> e, const Weigher &weigh) {
     uint32_t high = 0, low = 0;
-#pragma unroll
+#pragma unroll 2
     for (int j = 0; j < kSet / 2; ++j) {
-        const Weigher::Pair w = weigh.pair(e.pair(j));
+        const Weigher::Pair w = weigh.pair(e.next());
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (w.live[i]) high += w.high[i], low += w.low[i];
@@ -831,27 +870,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             // ---- the bins in which the border lies
             row.join();  // (the memory is used again)
             row.clear_bins();
-            if (threadIdx.x == 0) s->list_count = 0, s->found.place = kBins - 1;
+            if (threadIdx.x == 0) s->list_count = 0, s->found.place = kBins - 1, s->found.count = ~0u;
             row.join();
             // s->sum: what a bin's tokens weigh less than its first possible one, in 2^-16 of that, in 32 bits (atomics of 64
             // are loops: 292 us instead of 219 with the count in the high bits, 256 rows of 130001, top_p 0.5). Tokens of
             // -inf are in no bin: with 64 rows, some of them masked, their one bin's atomics took half of the time.
             const float per_bin = weigh.ch / scale;  // log2 of the weights' ratio over a bin, 0.1 at most
-            row.each([&](float l, int) {
-                const float x = place_in_bins(l, top, scale);
-                const uint32_t b = bin_of_place(x);
-                if (l == -INFINITY) return;
-                atomicAdd(&s->count[b], 1u);
-                if (by_weight && b + 1 < kBins) {
-                    float y;
-                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - (__fadd_rz(x, 8388608.0f) - 8388608.0f)) * -per_bin));
-                    atomicAdd(reinterpret_cast<uint32_t *>(&s->sum[b]), __float_as_uint(fmaf(1.0f - y, 65536.0f, 12582912.0f)) - 0x4B400000u);
+            const uint32_t counts = smem_addr(s->count), less_at = smem_addr(s->sum);
+            for (int i = threadIdx.x; i < row.sets; i += kRowSets) {
+                Eight<T> e = row.set(i);
+#pragma unroll 2
+                for (int j = 0; j < kSet / 2; ++j) {
+                    const float2 l2 = e.next();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float l = q ? l2.y : l2.x, x = place_in_bins(l, top, scale), up = __fadd_rz(x, 8388608.0f);
+                        const uint32_t b = __float_as_uint(up) & (kBins - 1u);
+                        add_if(l > -INFINITY, counts + 4 * b, 1u);
+                        if (by_weight) {
+                            float y;
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - (up - 8388608.0f)) * -per_bin));
+                            add_if(l > -INFINITY && b + 1 < kBins, less_at + 8 * b, __float_as_uint(fmaf(1.0f - y, 65536.0f, 12582912.0f)) - 0x4B400000u);
+                        }
+                    }
                 }
-            });
+            }
             row.join();
             uint32_t n[2];
             row.bin_counts(n);
-            uint32_t bin_lo, bin_hi;
+            uint32_t bin_lo, bin_hi, above, in;  // the bins, and the tokens in those before them, and in them
             if (by_weight) {
                 // what the bins weigh at most and at least, off by 2^-15 in all: half a unit of 2^-16 for each token and
                 // the steps to it; of the last bin's tokens only the upper bound is known
@@ -867,51 +914,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     most[i] = __float2ull_rn(y * (1.0f + 0x1p-15f) * kOne);
                     least[i] = b + 1 < kBins || top == INFINITY ? __float2ull_rn(y * (1.0f - 0x1p-15f) * kOne) : 0;
                 }
-                const uint64_t all_most = row.block_total(most[0] + most[1]), all_least = row.block_total(least[0] + least[1]);
-                row.find_bin(most, n, false, Target::share(all_least, top_p));
+                // where the sums, at most, reach the target at least, and the other way round; the tokens before and up to there
+                const uint64_t m2 = most[0] + most[1], l2 = least[0] + least[1];
+                const uint64_t up_m = warp_prefix(m2), up_l = warp_prefix(l2), up_n = warp_prefix(n[0] + n[1]);
+                if (lane == 31) s->warp_bins[warp][0] = up_m, s->warp_bins[warp][1] = up_l, s->warp_bins[warp][2] = up_n;
+                if (threadIdx.x == 0) s->range = {kBins - 1, 0, kBins - 1, ~0u};
                 __syncthreads();
-                bin_lo = s->found.place;
+                uint64_t before[3] = {up_m - m2, up_l - l2, up_n - (n[0] + n[1])}, whole[3] = {0, 0, 0};
+#pragma unroll 4
+                for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint64_t v = s->warp_bins[w][i];
+                        if (w < warp) before[i] += v;
+                        whole[i] += v;
+                    }
+                const uint64_t target_lo = Target::share(whole[1], top_p), target_hi = Target::share(whole[0], top_p);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (before[0] < target_lo && target_lo <= before[0] + most[i]) s->range.lo = 2 * threadIdx.x + i, s->range.above = static_cast<uint32_t>(before[2]);
+                    if (before[1] < target_hi && target_hi <= before[1] + least[i]) s->range.hi = 2 * threadIdx.x + i, s->range.up_to = static_cast<uint32_t>(before[2]) + n[i];
+                    before[0] += most[i], before[1] += least[i], before[2] += n[i];
+                }
                 __syncthreads();
-                if (threadIdx.x == 0) s->found.place = kBins - 1;
-                row.find_bin(least, n, false, Target::share(all_most, top_p));
-                __syncthreads();
-                bin_hi = max(bin_lo, s->found.place);
+                bin_lo = s->range.lo, bin_hi = s->range.hi, above = s->range.above;
+                in = (s->range.up_to == ~0u ? static_cast<uint32_t>(whole[2]) : s->range.up_to) - above;
             } else {
                 const uint64_t count[2] = {n[0], n[1]};
                 row.find_bin(count, n, false, static_cast<uint64_t>(top_k));
                 __syncthreads();
                 bin_lo = bin_hi = s->found.place;
+                above = static_cast<uint32_t>(s->found.before), in = s->found.count;
+                if (in == ~0u) {  // (fewer tokens than top_k: all but those of -inf)
+                    const bool last = threadIdx.x == kThreads - 1;
+                    const uint64_t both = row.block_total(static_cast<uint64_t>(n[0] + (last ? 0 : n[1])) << 32 | (last ? n[1] : 0));
+                    above = static_cast<uint32_t>(both >> 32), in = static_cast<uint32_t>(both);
+                }
             }
-            uint32_t above = 0, in = 0;  // tokens in the bins before these, and in them
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t b = 2 * threadIdx.x + i;
-                if (b < bin_lo) above += n[i];
-                else if (b <= bin_hi) in += n[i];
-            }
-            const uint64_t both = row.block_total(static_cast<uint64_t>(above) << 32 | in);
-            above = static_cast<uint32_t>(both >> 32), in = static_cast<uint32_t>(both);
             if (in <= kCap) {
                 uint64_t before = 0, all = 0;  // weights of the bins before these, and of all
                 uint64_t target = top_k - above;
-                row.send(-INFINITY, [&](float l) {
-                    const uint32_t b = bin_of(l, top, scale);
-                    return b >= bin_lo && b <= bin_hi;
-                });
+                // the bins' edges as logits: from `from` on up to bin_hi, from `ahead` on before bin_lo (NaN: none)
+                float from, ahead;
+                least_of_bins(bin_hi, bin_lo - 1, top, scale, from, ahead);
+                row.send(from, [&](float l) { return !(l >= ahead); });
                 if (by_weight) {
                     row.for_segments([&](int i) {
-                        const Eight<T> e = row.set(i);
+                        Eight<T> e = row.set(i);
                         uint32_t high[2] = {0, 0}, low[2] = {0, 0};  // of the bins before these, and from them on
                         uint64_t infinite = 0;
-#pragma unroll
+#pragma unroll 2
                         for (int j = 0; j < kSet / 2; ++j) {
-                            const float2 l = e.pair(j);
+                            const float2 l = e.next();
                             const Weigher::Pair w = weigh.pair(l);
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
-                                const bool ahead = bin_of(q ? l.y : l.x, top, scale) < bin_lo;
-                                if (w.live[q] && ahead) high[0] += w.high[q], low[0] += w.low[q];
-                                if (w.live[q] && !ahead) high[1] += w.high[q], low[1] += w.low[q];
+                                const bool first = (q ? l.y : l.x) >= ahead;
+                                if (w.live[q] && first) high[0] += w.high[q], low[0] += w.low[q];
+                                if (w.live[q] && !first) high[1] += w.high[q], low[1] += w.low[q];
                                 if ((q ? l.y : l.x) == weigh.all_of_it) infinite += kOne;
                             }
                         }
@@ -949,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
                         for (int j = 0; j < kSet; ++j) {
                             const float l = j & 1 ? e.pair(j >> 1).y : e.pair(j >> 1).x;
-                            if (l >= lowest && bin_of(l, top, scale) >= bin_lo && kept(l, row.first + kSet * i + j))
+                            if (l >= lowest && !(l >= ahead) && kept(l, row.first + kSet * i + j))
                                 atomicAdd(reinterpret_cast<unsigned long long *>(&s->segment[i >> 5]), static_cast<unsigned long long>(weigh(l)));
                         }
                     }

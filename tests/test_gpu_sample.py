@@ -139,6 +139,20 @@ def test_settings_at_their_ends():
             both(x, [u] * n, [1.0] * n, k, p)
 
 
+@pytest.mark.parametrize("vocab,finite", [(4000, 2500), (9000, 3), (50001, 4100), (50001, 2100), (130001, 0)])
+@pytest.mark.parametrize("k", [2600, 4099, 30000])
+def test_more_asked_for_than_there_are(vocab, finite, k):
+    """top_k beyond the tokens that are not -inf, alone and with the other filters."""
+    x, rng = rows(3, vocab, vocab + finite + k)
+    for r in range(3):
+        x[r, torch.from_numpy(rng.permutation(vocab)[finite:]).cuda()] = -INF
+    x[0, :7] = 0.25
+    u, ks = u01(rng, 3), np.full(3, k)
+    both(x, u, None, ks)
+    both(x, u, np.full(3, 1.3), ks, np.full(3, 0.8))
+    both(x, u, np.full(3, 0.8), ks, np.full(3, 0.95), np.full(3, 0.001))
+
+
 def test_every_token_has_its_share():
     """The unit interval in 4096 steps: as many of them choose a token as its probability says, in the indexes' order."""
     x, _ = rows(1, 300, 3, 1.0)
