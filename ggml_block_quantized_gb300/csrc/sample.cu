@@ -49,7 +49,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kSet = 8;          // neighbouring logits of a thread
 constexpr int kRowSets = kThreads, kSegment = 32 * kSet;  // sets, one a thread, that follow each other; logits of a warp there
 constexpr int kBins = 1024;
-constexpr int kCap = 2048;       // tokens that go to one block
+constexpr int kCap = 2048;       // tokens that go to one block (16 KB of its memory)
 constexpr int kList = 128;       // tokens that are compared with each other
 constexpr int kMaxCluster = 16;
 constexpr int kUnit = 44;        // weights are in units of 2^-44
@@ -57,6 +57,11 @@ constexpr uint64_t kOne = 1ull << kUnit;
 constexpr float kLeastTemperature = 0x1p-60f;
 constexpr float kRange = 64.0f;  // of m - l that the first histogram tells apart
 constexpr float kLog2E = 1.44269502162933349609375f, kLog2ERest = 1.925963033500e-8f;
+
+struct Settings {
+    float t, u, top_p, min_p;
+    int top_k, row;
+};
 
 struct Shared {
     float2 power[64];                 // 2^(i / 64) in two floats
@@ -72,7 +77,9 @@ struct Shared {
     uint64_t block_sum[2][kMaxCluster][2];
     float2 extremes[kWarps];
     float2 block_extremes[kMaxCluster];
-    uint32_t list_count, kept;
+    alignas(16) uint32_t kinds[kWarps];  // of rows: how many a warp has
+    Settings settings;
+    uint32_t list_count;
     uint64_t total;
     struct { uint64_t before, value; uint32_t place, count; } found;
 };
@@ -733,13 +740,57 @@ __device__ __forceinline__ Border border_of_sent(Shared *s, int n, int index_bit
     return sent.template border<WEIGHTS>(Border{0u, 0xFFFFFFFFu}, target, m, scale, -INFINITY, weigh);
 }
 
-template <class T>
+// A row's settings, and what they mean.
+__device__ __forceinline__ Settings settings_of(const SampleParams &p, int64_t r) {
+    return Settings{p.temperature ? p.temperature[r] : 1.0f, p.uniform[r], p.top_p ? p.top_p[r] : 1.0f, p.min_p ? p.min_p[r] : 0.0f,
+                    p.top_k ? p.top_k[r] : 0, static_cast<int>(r)};
+}
+__device__ __forceinline__ void check(Settings &a, int vocab) {
+    if (a.top_k < 0 || a.top_k >= vocab) a.top_k = 0;
+    if (!(a.top_p < 1.0f)) a.top_p = 1.0f;  // (NaN: all)
+    if (!(a.min_p > 0.0f)) a.min_p = 0.0f;
+}
+// Those of the row that is i-th by what they cost: first the rows whose logits are gone through twice (top_p without a small
+// top_k), then those that weigh all of them, then the others. A row a thread.
+__device__ __forceinline__ Settings settings_in_order(const SampleParams &p, Shared *s, int i) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Settings a;
+    int place = -1;  // of the row's kind in the order
+    if (threadIdx.x < p.n) {
+        a = settings_of(p, threadIdx.x);
+        check(a, p.vocab);
+        const bool few = !(a.t >= kLeastTemperature) || (a.top_k > 0 && a.top_k <= kThreads / 2 * p.blocks);
+        place = few ? 2 : a.top_p < 1.0f || a.top_k > 0 ? 0 : a.min_p > 0.0f ? 2 : 1;
+    }
+    uint32_t mine = 0, many = 0;  // ten bits a kind
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+        const uint32_t who = __ballot_sync(0xffffffffu, place == c);
+        if (place == c) mine = __popc(who & ((1u << lane) - 1u));
+        many |= __popc(who) << 10 * c;
+    }
+    if (lane == 0) s->kinds[warp] = many;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const uint32_t n = s->kinds[w];
+        if (w < warp) before += n;
+        all += n;
+    }
+    const uint32_t at = mine + (place > 0 ? all & 1023u : 0u) + (place > 1 ? all >> 10 & 1023u : 0u) + (before >> 10 * max(place, 0) & 1023u);
+    if (place >= 0 && at == static_cast<uint32_t>(i)) s->settings = a;
+    __syncthreads();
+    return s->settings;
+}
+
+// SORTED: the dear rows first.
+template <class T, bool SORTED>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared *const s = reinterpret_cast<Shared *>(smem);
     T *const space = reinterpret_cast<T *>(smem + (sizeof(Shared) + 31) / 32 * 32);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t r = blockIdx.x / p.blocks;
     Search<RowTokens<T>> row;
     row.s = s;
     row.blocks = p.blocks;
@@ -750,14 +801,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (p.blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_allow_dependents();
     pdl_wait_prior_grids();
-
-    // ---- the settings
-    const float t = p.temperature ? p.temperature[r] : 1.0f, u = p.uniform[r];
-    float top_p = p.top_p ? p.top_p[r] : 1.0f, min_p = p.min_p ? p.min_p[r] : 0.0f;
-    int top_k = p.top_k ? p.top_k[r] : 0;
-    if (top_k < 0 || top_k >= p.vocab) top_k = 0;
-    if (!(top_p < 1.0f)) top_p = 1.0f;  // (NaN: all)
-    if (!(min_p > 0.0f)) min_p = 0.0f;
+    const int i_row = static_cast<int>(blockIdx.x / p.blocks);
+    Settings a = SORTED ? settings_in_order(p, s, i_row) : settings_of(p, i_row);
+    const int64_t r = SORTED ? a.row : i_row;
 
     // ---- the row, as far from a boundary of eight elements here as there
     const int slice0 = row.rank * p.slice, count = max(0, min(p.vocab - slice0, p.slice));
@@ -787,6 +833,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             if (i0 + kRowSets * k < row.sets) *reinterpret_cast<Eight<T> *>(space + kSet * (i0 + kRowSets * k)) = e[k];
         }
     }
+    check(a, p.vocab);
+    const float t = a.t, u = a.u, top_p = a.top_p, min_p = a.min_p;
+    const int top_k = a.top_k;
     float top = extremes.get().x, low = extremes.get().y;
     const float mine_top = top;
 #pragma unroll
@@ -1037,18 +1086,26 @@ template <class T> cudaError_t launch(SampleParams p, int n, int sms, int device
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (device & 63);
     if (!(done.load(std::memory_order_acquire) & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
+        for (auto kernel : {sample_kernel<T, false>, sample_kernel<T, true>}) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+        }
         done.fetch_or(bit, std::memory_order_acq_rel);
     }
-    // blocks of a row: as many as its size asks for, and more while there are multiprocessors without a row
+    // blocks of a row: as many as its size asks for (two blocks a multiprocessor), and more while there are
+    // multiprocessors without a row. (64 rows of 32000 with mixed filters: 41.4 us; with twice the blocks 44.9, with
+    // top_p alone 62 instead of 37. One row of 32000 with all filters: 9.6 us by eight blocks, 11.0 by sixteen.)
     auto slice = [&](int blocks) { return (p.vocab + kSet * blocks - 1) / (kSet * blocks) * kSet; };
     p.blocks = 1;
     while (p.blocks < kMaxCluster &&
            (slice_smem<T>(slice(p.blocks)) > kSmemLimit / 2 || (static_cast<int64_t>(n) * p.blocks <= sms && slice(p.blocks) > 4096 && p.blocks < 8)))
         p.blocks *= 2;
     p.slice = slice(p.blocks);
+    // More rows than are at work at once: the dear ones first, so that none of them is left for the end (256 rows of 130001
+    // with mixed filters: 166 us in the rows' order, 143 so; rows that are alike pay 5 us for it, 49 in all with a top_k of 40).
+    p.n = n;
+    const bool sorted = n <= kThreads && static_cast<int64_t>(n) * p.blocks > 2 * sms && (p.top_k || p.top_p || p.min_p || p.temperature);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n) * p.blocks);
     cfg.blockDim = dim3(kThreads);
@@ -1061,7 +1118,7 @@ template <class T> cudaError_t launch(SampleParams p, int n, int sms, int device
     attr[1].val.clusterDim.x = p.blocks, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
+    return cudaLaunchKernelEx(&cfg, sorted ? sample_kernel<T, true> : sample_kernel<T, false>, p);
 }
 
 }  // namespace

@@ -15,8 +15,8 @@ struct SampleParams {
     float *prob;
     int64_t stride;
     int vocab;
-    int blocks, slice;  // of a row; logits of a block (the launch's choice)
-    float2 power[64];  // (the launch's)
+    int n, blocks, slice;  // rows; blocks of a row; logits of a block (these and what follows: the launch's)
+    float2 power[64];
 };
 
 cudaError_t launch_sample(SampleParams p, int type, int n, int sms, int device, cudaStream_t s);

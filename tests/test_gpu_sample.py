@@ -153,6 +153,27 @@ def test_more_asked_for_than_there_are(vocab, finite, k):
     both(x, u, np.full(3, 0.8), ks, np.full(3, 0.95), np.full(3, 0.001))
 
 
+@pytest.mark.parametrize("n", [305, 400, 512, 513, 1100])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_more_rows_than_run_at_once(n, dtype):
+    """Settings of every kind, in any order among the rows."""
+    x, rng = rows(n, 1700, n, dtype=dtype)
+    x[rng.integers(0, n, 9)] = -INF
+    k = rng.choice([0, 0, 1, 3, 40, 700, 1699, 5000, -2], n)
+    p = rng.choice([1.0, 1.0, 0.9, 0.3, 0.0, NAN], n)
+    m = rng.choice([0.0, 0.0, 0.05, 2.0, NAN], n)
+    t = rng.choice([1.0, 0.0, 0.7, 1.9], n)
+    both(x, u01(rng, n), t, np.maximum(k, 0), np.where(np.isnan(p), 1.0, p), np.where(np.isnan(m), 0.0, m))
+    f = lambda a, d=torch.float32: cuda(a, d)  # noqa: E731
+    u = f(u01(rng, n))
+    whole = qg.sample_tokens(x, u, f(t), f(k, torch.int32), f(p), f(m), prob_out=torch.empty(n, device="cuda"))
+    for r0 in range(0, n, 100):
+        part = slice(r0, min(n, r0 + 100))
+        some = qg.sample_tokens(x[part], u[part], f(t[part]), f(k[part], torch.int32), f(p[part]), f(m[part]),
+                                prob_out=torch.empty(part.stop - r0, device="cuda"))
+        assert torch.equal(whole[0][part], some[0]) and torch.equal(whole[1][part], some[1])
+
+
 def test_every_token_has_its_share():
     """The unit interval in 4096 steps: as many of them choose a token as its probability says, in the indexes' order."""
     x, _ = rows(1, 300, 3, 1.0)
