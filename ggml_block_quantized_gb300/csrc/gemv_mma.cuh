@@ -811,6 +811,17 @@ __device__ __forceinline__ uint32_t mma_word(uint32_t base) {
     }
 }
 
+// Packed two-lane f32 product (one instruction for both lanes).
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // The first mma of a block, its accumulator starting from the tail's
 // initial values (rows g, g+8; vectors 2t, 2t+1).
 __device__ __forceinline__ void mma_group_first(float (&C)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,

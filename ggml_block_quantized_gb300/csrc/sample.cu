@@ -37,6 +37,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "packed.cuh"
 #include "step_kernels.cuh"
 
 namespace cg = cooperative_groups;

@@ -36,6 +36,7 @@
 #include <cfloat>
 #include <climits>
 
+#include "packed.cuh"
 #include "tc_attend.cuh"
 
 namespace qg {
