@@ -25,7 +25,7 @@
 // for f32, and 128 KB of operands written; it takes 2850. What bounds it is the
 // expanders' chain of instructions (3.8 cycles each in turn, 22 a word of eight
 // codes), then the tensor cores. 16 sequences of 64 heads on 65521 tokens, 27 units
-// a block, take 77.8 us. A call with a short prefix is a pipeline's filling, its
+// a block, take 76.0 us. A call with a short prefix is a pipeline's filling, its
 // drain and the join (2 sequences on 300 tokens: 17.8 us), most of them
 // instructions' first fetch. What other arrangements measured on the 65521: one warp for S and O, and eight
 // that expand keys and values in turn, 86.0 us; pieces of a unit's keys and values
@@ -752,7 +752,7 @@ __device__ __forceinline__ void store2(__half *p, float a, float b) { *reinterpr
 constexpr int kJoinThreads = 256;
 
 template <int D, class T> __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p, const int parts) {
-    constexpr int kLanes = D / 4, kAhead = 4;
+    constexpr int kLanes = D / 4, kAhead = 10;  // (stretches under way: an item has up to 19; 4 took half a microsecond more)
     pdl_allow_dependents();
     pdl_wait_prior_grids();
     const KvAttendParams &a = p.own;
