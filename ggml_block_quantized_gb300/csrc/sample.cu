@@ -75,6 +75,7 @@ struct Shared {
     uint64_t segment[2 * kThreads];   // kept weights of kSegment logits
     uint64_t warp_sum[kWarps], warp_bins[kWarps][3];
     struct { uint32_t lo, above, hi, up_to; } range;
+    alignas(16) uint4 told;
     uint64_t block_sum[2][kMaxCluster][2];
     float2 extremes[kWarps];
     float2 block_extremes[kMaxCluster];
@@ -446,7 +447,7 @@ template <class Tokens> struct Search : Tokens {
             if (threadIdx.x == place >> 1)
                 for (int b = 0; b < blocks; ++b) {
                     auto *f = at(&s->found, b);
-                    f->value = v[place & 1], f->place = first + from + place;
+                    f->value = place & 1 ? v[1] : v[0], f->place = first + from + place;
                 }
         }
         join();
@@ -500,10 +501,11 @@ template <class Tokens> struct Search : Tokens {
         }
         if (rising) before = whole - before - both;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int b = rising ? 1 - i : i;
-            if (before < target && target <= before + v[b]) s->found.place = 2 * threadIdx.x + b, s->found.before = before, s->found.count = n[b];
-            before += v[b];
+        for (int i = 0; i < 2; ++i) {  // (no array by a variable: with all of shared memory taken, local memory is L2's)
+            const bool b = rising ? i == 0 : i == 1;
+            const uint64_t x = b ? v[1] : v[0];
+            if (before < target && target <= before + x) s->found.place = 2 * threadIdx.x + b, s->found.before = before, s->found.count = b ? n[1] : n[0];
+            before += x;
         }
     }
     // Tokens from logit `least` on (not -inf) for which take(logit) holds are sent to the first block, as far as there is room.
@@ -946,61 +948,68 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 }
             }
             row.join();
-            uint32_t n[2];
-            row.bin_counts(n);
-            uint32_t bin_lo, bin_hi, above, in;  // the bins, and the tokens in those before them, and in them
-            if (by_weight) {
-                // what the bins weigh at most and at least, off by 2^-15 in all: half a unit of 2^-16 for each token and
-                // the steps to it; of the last bin's tokens only the upper bound is known
-                uint64_t less[2], most[2], least[2];
-                row.bin_sums(less);
+            uint32_t bin_lo = 0, bin_hi = 0, above = 0, in = 0;  // the bins, and the tokens in those before them, and in them
+            if (row.rank == 0) {  // (the others reading the histograms, too, took longer than they wait so)
+                uint32_t n[2];
+                row.bin_counts(n);
+                if (by_weight) {
+                    // what the bins weigh at most and at least, off by 2^-15 in all: half a unit of 2^-16 for each token and
+                    // the steps to it; of the last bin's tokens only the upper bound is known
+                    uint64_t less[2], most[2], least[2];
+                    row.bin_sums(less);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int b = 2 * threadIdx.x + i;
-                    float y;
-                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-b * per_bin));
-                    y *= static_cast<float>(n[i]) - static_cast<float>(less[i]) * 0x1p-16f;
-                    if (top == INFINITY) y = b == 0 ? static_cast<float>(n[i]) : 0.0f;
-                    most[i] = __float2ull_rn(y * (1.0f + 0x1p-15f) * kOne);
-                    least[i] = b + 1 < kBins || top == INFINITY ? __float2ull_rn(y * (1.0f - 0x1p-15f) * kOne) : 0;
-                }
-                // where the sums, at most, reach the target at least, and the other way round; the tokens before and up to there
-                const uint64_t m2 = most[0] + most[1], l2 = least[0] + least[1];
-                const uint64_t up_m = warp_prefix(m2), up_l = warp_prefix(l2), up_n = warp_prefix(n[0] + n[1]);
-                if (lane == 31) s->warp_bins[warp][0] = up_m, s->warp_bins[warp][1] = up_l, s->warp_bins[warp][2] = up_n;
-                if (threadIdx.x == 0) s->range = {kBins - 1, 0, kBins - 1, ~0u};
-                __syncthreads();
-                uint64_t before[3] = {up_m - m2, up_l - l2, up_n - (n[0] + n[1])}, whole[3] = {0, 0, 0};
-#pragma unroll 4
-                for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uint64_t v = s->warp_bins[w][i];
-                        if (w < warp) before[i] += v;
-                        whole[i] += v;
+                    for (int i = 0; i < 2; ++i) {
+                        const int b = 2 * threadIdx.x + i;
+                        float y;
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-b * per_bin));
+                        y *= static_cast<float>(n[i]) - static_cast<float>(less[i]) * 0x1p-16f;
+                        if (top == INFINITY) y = b == 0 ? static_cast<float>(n[i]) : 0.0f;
+                        most[i] = __float2ull_rn(y * (1.0f + 0x1p-15f) * kOne);
+                        least[i] = b + 1 < kBins || top == INFINITY ? __float2ull_rn(y * (1.0f - 0x1p-15f) * kOne) : 0;
                     }
-                const uint64_t target_lo = Target::share(whole[1], top_p), target_hi = Target::share(whole[0], top_p);
+                    // where the sums, at most, reach the target at least, and the other way round; the tokens before and up to there
+                    const uint64_t m2 = most[0] + most[1], l2 = least[0] + least[1];
+                    const uint64_t up_m = warp_prefix(m2), up_l = warp_prefix(l2);
+                    const uint32_t up_n = static_cast<uint32_t>(warp_prefix(n[0] + n[1]));
+                    if (lane == 31) s->warp_bins[warp][0] = up_m, s->warp_bins[warp][1] = up_l, s->warp_bins[warp][2] = up_n;
+                    if (threadIdx.x == 0) s->range = {kBins - 1, 0, kBins - 1, ~0u};
+                    __syncthreads();
+                    uint64_t before_m = up_m - m2, before_l = up_l - l2, whole_m = 0, whole_l = 0;
+                    uint32_t before_n = up_n - (n[0] + n[1]), whole_n = 0;
+#pragma unroll 4
+                    for (int w = 0; w < kWarps; ++w) {
+                        const uint64_t m = s->warp_bins[w][0], l = s->warp_bins[w][1];
+                        const uint32_t k = static_cast<uint32_t>(s->warp_bins[w][2]);
+                        if (w < warp) before_m += m, before_l += l, before_n += k;
+                        whole_m += m, whole_l += l, whole_n += k;
+                    }
+                    const uint64_t target_lo = Target::share(whole_l, top_p), target_hi = Target::share(whole_m, top_p);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (before[0] < target_lo && target_lo <= before[0] + most[i]) s->range.lo = 2 * threadIdx.x + i, s->range.above = static_cast<uint32_t>(before[2]);
-                    if (before[1] < target_hi && target_hi <= before[1] + least[i]) s->range.hi = 2 * threadIdx.x + i, s->range.up_to = static_cast<uint32_t>(before[2]) + n[i];
-                    before[0] += most[i], before[1] += least[i], before[2] += n[i];
+                    for (int i = 0; i < 2; ++i) {
+                        if (before_m < target_lo && target_lo <= before_m + most[i]) s->range.lo = 2 * threadIdx.x + i, s->range.above = before_n;
+                        before_m += most[i], before_n += n[i];
+                        if (before_l < target_hi && target_hi <= before_l + least[i]) s->range.hi = 2 * threadIdx.x + i, s->range.up_to = before_n;
+                        before_l += least[i];
+                    }
+                    __syncthreads();
+                    bin_lo = s->range.lo, bin_hi = s->range.hi, above = s->range.above;
+                    in = (s->range.up_to == ~0u ? whole_n : s->range.up_to) - above;
+                } else {
+                    const uint64_t count[2] = {n[0], n[1]};
+                    row.find_bin(count, n, false, static_cast<uint64_t>(top_k));
+                    __syncthreads();
+                    bin_lo = bin_hi = s->found.place;
+                    above = static_cast<uint32_t>(s->found.before), in = s->found.count;
+                    if (in == ~0u) {  // (fewer tokens than top_k: all but those of -inf)
+                        const bool last = threadIdx.x == kThreads - 1;
+                        const uint64_t both = row.block_total(static_cast<uint64_t>(n[0] + (last ? 0 : n[1])) << 32 | (last ? n[1] : 0));
+                        above = static_cast<uint32_t>(both >> 32), in = static_cast<uint32_t>(both);
+                    }
                 }
-                __syncthreads();
-                bin_lo = s->range.lo, bin_hi = s->range.hi, above = s->range.above;
-                in = (s->range.up_to == ~0u ? static_cast<uint32_t>(whole[2]) : s->range.up_to) - above;
-            } else {
-                const uint64_t count[2] = {n[0], n[1]};
-                row.find_bin(count, n, false, static_cast<uint64_t>(top_k));
-                __syncthreads();
-                bin_lo = bin_hi = s->found.place;
-                above = static_cast<uint32_t>(s->found.before), in = s->found.count;
-                if (in == ~0u) {  // (fewer tokens than top_k: all but those of -inf)
-                    const bool last = threadIdx.x == kThreads - 1;
-                    const uint64_t both = row.block_total(static_cast<uint64_t>(n[0] + (last ? 0 : n[1])) << 32 | (last ? n[1] : 0));
-                    above = static_cast<uint32_t>(both >> 32), in = static_cast<uint32_t>(both);
-                }
+                if (threadIdx.x < row.blocks) *row.at(&s->told, threadIdx.x) = make_uint4(bin_lo, bin_hi, above, in);
             }
+            row.join();
+            bin_lo = s->told.x, bin_hi = s->told.y, above = s->told.z, in = s->told.w;
             if (in <= kCap) {
                 uint64_t before = 0, all = 0;  // weights of the bins before these, and of all
                 uint64_t target = top_k - above;
