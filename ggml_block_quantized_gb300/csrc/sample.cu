@@ -73,7 +73,8 @@ struct Shared {
     uint64_t ahead[kList];            // weights before a token, and how many tokens
     uint32_t rank[kList];
     uint64_t segment[2 * kThreads];   // kept weights of kSegment logits
-    uint64_t warp_sum[kWarps], warp_bins[kWarps][3];
+    alignas(16) uint64_t warp_sum[kWarps], warp_most[kWarps], warp_least[kWarps];
+    alignas(16) uint32_t warp_count[kWarps];
     struct { uint32_t lo, above, hi, up_to; } range;
     alignas(16) uint4 told;
     uint64_t block_sum[2][kMaxCluster][2];
@@ -279,6 +280,31 @@ __device__ __forceinline__ uint64_t warp_prefix(uint64_t v) {  // inclusive
     return v;
 }
 
+// Values of the warps: the sum of all, and of those before `warp`, added to `before`. (Every warp reads them: 16 bytes at a
+// time, the fewest instructions.)
+__device__ __forceinline__ void add_up(const uint64_t *of_warps, int warp, uint64_t &before, uint64_t &all) {
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w += 2) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(of_warps + w);
+        if (w < warp) before += v.x;
+        if (w + 1 < warp) before += v.y;
+        all += v.x + v.y;
+    }
+}
+__device__ __forceinline__ void add_up(const uint32_t *of_warps, int warp, uint32_t &before, uint32_t &all) {
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w += 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(of_warps + w);
+        if (w < warp) before += v.x;
+        if (w + 1 < warp) before += v.y;
+        if (w + 2 < warp) before += v.z;
+        if (w + 3 < warp) before += v.w;
+        all += v.x + v.y + v.z + v.w;
+    }
+}
+
 struct Target {  // of a sum's share
     __device__ static __forceinline__ uint64_t share(uint64_t all, float p) {  // the least that is not below it, 1 or more
         bool rest;
@@ -337,13 +363,12 @@ template <class Tokens> struct Search : Tokens {
     struct Sums { uint64_t before, mine, all, all2; };
     __device__ __forceinline__ Sums sums(uint64_t v, uint64_t v2) {
         const uint64_t block2 = v2 == ~0ull ? 0 : block_total(v2);
-        uint64_t block = 0;
+        uint64_t none = 0, block;
         v = warp_total(v);
         __syncthreads();
         if ((threadIdx.x & 31) == 0) s->warp_sum[threadIdx.x >> 5] = v;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) block += s->warp_sum[w];
+        add_up(s->warp_sum, 0, none, block);
         uint64_t (*const place)[2] = s->block_sum[turn];
         turn ^= 1;
         if (threadIdx.x < blocks) {
@@ -363,9 +388,8 @@ template <class Tokens> struct Search : Tokens {
         __syncthreads();
         if ((threadIdx.x & 31) == 0) s->warp_sum[threadIdx.x >> 5] = v;
         __syncthreads();
-        uint64_t all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) all += s->warp_sum[w];
+        uint64_t before = 0, all;
+        add_up(s->warp_sum, 0, before, all);
         __syncthreads();
         return all;
     }
@@ -493,12 +517,8 @@ template <class Tokens> struct Search : Tokens {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         if (lane == 31) s->warp_sum[warp] = up_to;
         __syncthreads();
-        uint64_t before = up_to - both, whole = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s->warp_sum[w];
-            whole += s->warp_sum[w];
-        }
+        uint64_t before = up_to - both, whole;
+        add_up(s->warp_sum, warp, before, whole);
         if (rising) before = whole - before - both;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // (no array by a variable: with all of shared memory taken, local memory is L2's)
@@ -774,13 +794,8 @@ __device__ __forceinline__ Settings settings_in_order(const SampleParams &p, Sha
     }
     if (lane == 0) s->kinds[warp] = many;
     __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const uint32_t n = s->kinds[w];
-        if (w < warp) before += n;
-        all += n;
-    }
+    uint32_t before = 0, all;
+    add_up(s->kinds, warp, before, all);
     const uint32_t at = mine + (place > 0 ? all & 1023u : 0u) + (place > 1 ? all >> 10 & 1023u : 0u) + (before >> 10 * max(place, 0) & 1023u);
     if (place >= 0 && at == static_cast<uint32_t>(i)) s->settings = a;
     __syncthreads();
@@ -971,18 +986,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     const uint64_t m2 = most[0] + most[1], l2 = least[0] + least[1];
                     const uint64_t up_m = warp_prefix(m2), up_l = warp_prefix(l2);
                     const uint32_t up_n = static_cast<uint32_t>(warp_prefix(n[0] + n[1]));
-                    if (lane == 31) s->warp_bins[warp][0] = up_m, s->warp_bins[warp][1] = up_l, s->warp_bins[warp][2] = up_n;
+                    if (lane == 31) s->warp_most[warp] = up_m, s->warp_least[warp] = up_l, s->warp_count[warp] = up_n;
                     if (threadIdx.x == 0) s->range = {kBins - 1, 0, kBins - 1, ~0u};
                     __syncthreads();
-                    uint64_t before_m = up_m - m2, before_l = up_l - l2, whole_m = 0, whole_l = 0;
-                    uint32_t before_n = up_n - (n[0] + n[1]), whole_n = 0;
-#pragma unroll 4
-                    for (int w = 0; w < kWarps; ++w) {
-                        const uint64_t m = s->warp_bins[w][0], l = s->warp_bins[w][1];
-                        const uint32_t k = static_cast<uint32_t>(s->warp_bins[w][2]);
-                        if (w < warp) before_m += m, before_l += l, before_n += k;
-                        whole_m += m, whole_l += l, whole_n += k;
-                    }
+                    uint64_t before_m = up_m - m2, before_l = up_l - l2, whole_m, whole_l;
+                    uint32_t before_n = up_n - (n[0] + n[1]), whole_n;
+                    add_up(s->warp_most, warp, before_m, whole_m);
+                    add_up(s->warp_least, warp, before_l, whole_l);
+                    add_up(s->warp_count, warp, before_n, whole_n);
                     const uint64_t target_lo = Target::share(whole_l, top_p), target_hi = Target::share(whole_m, top_p);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
