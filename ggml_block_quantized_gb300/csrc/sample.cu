@@ -28,7 +28,9 @@
 // with 10^5 tokens that many borders share the unit interval. 2^x for them takes
 // an argument in two floats, a table of 64 powers and a polynomial of degree 5, two
 // logits at a time in packed instructions, 27 a logit; the passes are bound by
-// their instructions.
+// their instructions. 256 rows of 130001 logits in f16 take 93 us without filters,
+// 45 with a top_k of 40, 217 with a top_p of 0.9, one row of 32000 in f32 7.7, 8.5
+// and 19.5: there it is one chain of loads, joins of the cluster and sums.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -1124,7 +1126,8 @@ template <class T> cudaError_t launch(SampleParams p, int n, int sms, int device
         p.blocks *= 2;
     p.slice = slice(p.blocks);
     // More rows than are at work at once: the dear ones first, so that none of them is left for the end (256 rows of 130001
-    // with mixed filters: 166 us in the rows' order, 143 so; rows that are alike pay 5 us for it, 49 in all with a top_k of 40).
+    // with mixed filters: 166 us in the rows' order, 143 so, before later steps; rows that are alike pay 3 us for it, 45 in all
+    // with a top_k of 40).
     p.n = n;
     const bool sorted = n <= kThreads && static_cast<int64_t>(n) * p.blocks > 2 * sms && (p.top_k || p.top_p || p.min_p || p.temperature);
     cudaLaunchConfig_t cfg = {};
