@@ -21,8 +21,8 @@
 // The warps: one copies the units' groups of the cache, one makes their scales
 // ready, one issues S, one O; four hold a row's softmax a thread, four its values'
 // sums; eight expand codes into operands, four the keys', four the values'. With
-// 128 channels a unit is 32 products of 64 cycles, so 2048 cycles for f16, 3072
-// for f32, and 128 KB of operands written; it takes 2850. What bounds it is the
+// 128 channels a unit is 32 products of 64 cycles, so 2048 cycles for f16, half as
+// many again for f32, and 128 KB of operands written; it takes 2850 for f16. What bounds it is the
 // expanders' chain of instructions (3.8 cycles each in turn, 22 a word of eight
 // codes), then the tensor cores. 16 sequences of 64 heads on 65521 tokens, 27 units
 // a block, take 76.0 us. A call with a short prefix is a pipeline's filling, its
