@@ -11,27 +11,27 @@
 //
 // S = Q K^T and O = P V are tcgen05 products of f16 with f32 sums. A key or value
 // is a code of four bits times an f16 scale, 15 bits, and so the exact sum of two
-// f16 parts; f32 queries and, for them, the weights are two parts as well. Then S
-// takes two products (f32: three, without low times low) and O two (three), what a
-// plain f32 evaluation loses at that: an f16 part each would cost 2^-12 a factor.
-// The rows' softmax runs over the tiles (references rise by powers of 2 of at least
-// 2^7, so a row's values are rescaled a few times in all), and O of a tile is read
-// back and added up in f32 registers.
+// f16 parts (one alone would be off by 2^-12); f32 queries and, for them, the
+// weights are two parts as well. So S takes two products (f32: three, without low
+// times low) and O as many. A row's reference, a power of 2 that its weights are
+// taken against, rises in steps of 2^7 at least, so its sums are rescaled a few
+// times in all, and O of a tile is read back and added up in f32 registers.
 //
 // The warps: one copies the units' groups of the cache, one makes their scales
 // ready, one issues S, one O; four hold a row's softmax a thread, four its values'
 // sums; eight expand codes into operands, four the keys', four the values'. With
 // 128 channels a unit is 32 products of 64 cycles, so 2048 cycles for f16, half as
-// many again for f32, and 128 KB of operands written; it takes 2850 for f16. What bounds it is the
-// expanders' chain of instructions (3.8 cycles each in turn, 22 a word of eight
-// codes), then the tensor cores. 16 sequences of 64 heads on 65521 tokens, 27 units
-// a block, take 76.0 us. A call with a short prefix is a pipeline's filling, its
-// drain and the join (2 sequences on 300 tokens: 17.8 us), most of them
-// instructions' first fetch. What other arrangements measured on the 65521: one warp for S and O, and eight
-// that expand keys and values in turn, 86.0 us; pieces of a unit's keys and values
-// in three places and three raw pieces ahead 91 (copies were waited for); whole
-// units' keys in one place, values in another 82.3; loops of the expanders
-// unrolled 98 (instructions came from beyond their cache).
+// many again for f32, and 128 KB of operands written; it takes 2850 for f16. What
+// bounds it is the expanders' chain of instructions (3.8 cycles each in turn, 22 a
+// word of eight codes), then the tensor cores. 16 sequences of 64 heads on 65521
+// tokens, 27 units a block, take 76.0 us. A call with a short prefix is a
+// pipeline's filling, its drain and the join (2 sequences on 300 tokens: 17.8 us),
+// most of them instructions' first fetch. What other arrangements measured on the
+// 65521: one warp for S and O, and eight that expand keys and values in turn, 86.0
+// us; pieces of a unit's keys and values in three places and three raw pieces ahead
+// 91 (copies were waited for); whole units' keys in one place, values in another
+// 82.3; loops of the expanders unrolled 98 (instructions came from beyond their
+// cache).
 #include <atomic>
 #include <cfloat>
 #include <climits>
