@@ -863,11 +863,13 @@ template <int D, class T> cudaError_t launch(SharedParams &p, int sms, int devic
 
 }  // namespace
 
-// The workspace: kv_attend's own, the rows' results of their own tokens, the stretches.
+// The workspace: kv_attend's own, the rows' results of their own tokens, the stretches, which are written 32 bytes at a time
+// and so begin at the next such boundary (the interface asks for 16).
+constexpr size_t kStretchAlign = 32;
 size_t shared_attend_workspace(int head_dim, int n_kv_heads, int group, int64_t n_tok, int max_q_len) {
     const size_t rows = static_cast<size_t>(n_tok) * group * n_kv_heads;
     return align(kv_attend_workspace(head_dim, group * max_q_len)) + align(rows * head_dim * 4) + align(rows * 8) +
-           static_cast<size_t>(kMaxParts + n_kv_heads * row_tiles(n_tok, group)) * stretch_floats(head_dim) * 4;
+           static_cast<size_t>(kMaxParts + n_kv_heads * row_tiles(n_tok, group)) * stretch_floats(head_dim) * 4 + kStretchAlign - 16;
 }
 
 cudaError_t launch_shared_attend(SharedParams p, int head_dim, int type, int sms, int device, cudaStream_t s) {
@@ -879,6 +881,7 @@ cudaError_t launch_shared_attend(SharedParams p, int head_dim, int type, int sms
     at += align(rows * head_dim * 4);
     a.rest_stats = reinterpret_cast<float *>(at);
     at += align(rows * 8);
+    at += (0 - reinterpret_cast<uintptr_t>(at)) % kStretchAlign;
     p.stretches = reinterpret_cast<float *>(at);
     p.row_tiles = static_cast<int>(row_tiles(a.n_tok, a.group));
     p.parts = kv_attend_parts(head_dim, static_cast<int64_t>(a.group) * a.max_q_len);

@@ -347,6 +347,19 @@ def test_what_lies_in_the_workspace_does_not_matter():
 
 
 @pytest.mark.parametrize("t,d", [("f32", 64), ("f16", 64), ("f32", 128), ("f16", 128)])
+@pytest.mark.parametrize("first", [16, 48, 112, 240])
+def test_a_workspace_on_a_16_byte_boundary(t, d, first):
+    """As many bytes as are asked for, 16 into an allocation; what lies before and behind stays."""
+    a = batch(10, t, d, prefix=700)
+    want = qg.kv_attend_shared(*a)
+    need = qg.kv_attend_shared_workspace_bytes(a[0], a[1].shape[1], a[1].shape[0])
+    arena = torch.full((first + need + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    assert arena.data_ptr() % 32 == 0
+    assert torch.equal(qg.kv_attend_shared(*a, workspace=arena[first:first + need]), want)
+    assert (arena[:first] == 0x5A).all() and (arena[first + need:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("t,d", [("f32", 64), ("f16", 64), ("f32", 128), ("f16", 128)])
 @pytest.mark.parametrize("hk,prefix,seqs", [(1, 20000, 30), (7, 3000, 60), (40, 1000, 60)])
 def test_the_same_bits_beside_other_work(t, d, hk, prefix, seqs):
     """Many calls, two at a time on two streams and beside products that keep the multiprocessors busy now and then: the
