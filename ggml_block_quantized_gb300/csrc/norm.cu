@@ -241,12 +241,7 @@ __global__ void __launch_bounds__(MOST, MOST == 1024 || !WIDE ? 1 : MOST == 512 
     }
 }
 
-// Whether a row matrix can be read 8 elements at a time.
-bool wide_rows(const void *p, int64_t stride, int type) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % (type == QG_F32 ? 4 : 8) == 0;
-}
-
-bool on32(const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && stride % 8 == 0; }
+bool on32(const void *p, int64_t stride) { return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 31u) == 0 && stride % 8 == 0); }
 
 template <class TH, class TY, bool WIDE> cudaError_t launch(const qnorm_args &a, cudaStream_t s) {
     constexpr int kWidth = WIDE ? 8 : 4;
@@ -275,11 +270,7 @@ template <class TH, class TY, bool WIDE> cudaError_t launch(const qnorm_args &a,
 }
 
 template <class TH, class TY> cudaError_t launch_types(const qnorm_args &a, cudaStream_t s) {
-    const bool wide = a.d % 8 == 0 && wide_rows(a.h, a.h_stride, a.h_type) && wide_rows(a.y, a.y_stride, a.y_type) &&
-                      wide_rows(a.gate, a.gate_stride, QG_F32) && wide_rows(a.post_w, 0, QG_F32) && wide_rows(a.post_b, 0, QG_F32) &&
-                      wide_rows(a.w, 0, QG_F32) && wide_rows(a.b, 0, QG_F32) && wide_rows(a.h_out, a.h_out_stride, a.h_type) &&
-                      wide_rows(a.x_out, a.d, a.x_type);
-    return wide ? launch<TH, TY, true>(a, s) : launch<TH, TY, false>(a, s);
+    return norm_rows_on_16(a) ? launch<TH, TY, true>(a, s) : launch<TH, TY, false>(a, s);
 }
 
 }  // namespace

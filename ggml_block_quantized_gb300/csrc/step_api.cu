@@ -12,8 +12,6 @@ bool aligned(const void *p, int type) { return (reinterpret_cast<uintptr_t>(p) &
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 bool stride_ok(int64_t stride) { return stride >= 0 && stride <= kMaxStride; }
 bool finite(float x) { return x - x == 0.0f; }
-// Rows that can be read and written 16 bytes at a time.
-bool wide(const void *p, int64_t stride, int type) { return !p || (aligned16(p) && stride % (type == QG_F32 ? 4 : 8) == 0); }
 
 }  // namespace
 
@@ -33,11 +31,7 @@ int qnorm_residual(const qnorm_args *a, qg_stream_t stream) {
         !aligned(a->gate, QG_F32) || !aligned(a->w, QG_F32) || !aligned(a->b, QG_F32) || !aligned(a->h_out, a->h_type) ||
         !aligned(a->x_out, a->x_type))
         return QG_ERR_ALIGN;
-    if (a->xq && (!aligned16(a->xq) || !wide(a->h, a->h_stride, a->h_type) || !wide(a->y, a->y_stride, a->y_type) ||
-                  !wide(a->post_w, 0, QG_F32) || !wide(a->post_b, 0, QG_F32) || !wide(a->gate, a->gate_stride, QG_F32) ||
-                  !wide(a->w, 0, QG_F32) || !wide(a->b, 0, QG_F32) || !wide(a->h_out, a->h_out_stride, a->h_type) ||
-                  !wide(a->x_out, 0, a->x_type)))
-        return QG_ERR_ALIGN;
+    if (a->xq && (!aligned16(a->xq) || !norm_rows_on_16(*a))) return QG_ERR_ALIGN;
     DeviceInfo dev;
     const int st = current_device(&dev);
     if (st != QG_OK) return st;

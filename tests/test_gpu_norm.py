@@ -1,5 +1,7 @@
 """norm_residual (include/qstep.h) on the GPU against its formula in 64 bits;
 the bounds are step_ref's, from the arithmetic."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -7,6 +9,7 @@ torch = pytest.importorskip("torch")
 
 import ggml_block_quantized_gb300 as qg  # noqa: E402
 import step_ref  # noqa: E402
+from ggml_block_quantized_gb300 import step  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 F32, F16 = torch.float32, torch.float16
@@ -128,6 +131,24 @@ def test_blocks_are_quantize_act(act, n, d):
     xq2 = torch.zeros_like(xq)
     h2, none = run(a, xq=xq2, act_type=t)
     assert none is None and torch.equal(xq2, xq) and torch.equal(h, h2)
+
+
+@pytest.mark.parametrize("x_out", [True, False])
+@pytest.mark.parametrize("act", ["Q8_0", "Q8_1", "Q8_K"])
+def test_strides_of_what_is_not_there_do_not_count(act, x_out):
+    """Through the C interface: without y, gate and h_out their strides may be anything."""
+    t, n, d = getattr(qg, act), 3, 512
+    a = make(n, d, seed=7)
+    want = torch.empty(n, d, device="cuda")
+    qg.norm_residual(a["h"], weight=a["weight"], bias=a["bias"], x_out=want)
+    x = torch.empty_like(want)
+    xq = torch.full((n * qg.qtype_nbytes(t, d),), 0x5A, dtype=torch.uint8, device="cuda")
+    args = step._NormArgs(a["h"].data_ptr(), None, d, 1, None, None, None, 3, a["weight"].data_ptr(), a["bias"].data_ptr(), None,
+                          d + 5, x.data_ptr() if x_out else None, xq.data_ptr(), n, d, qg.F32, qg.F16, qg.F32, t, 0, 1.0, 1e-5)
+    assert step._lib().qnorm_residual(ctypes.byref(args), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(xq, qg.quantize_act(t, want, n).flatten())
+    if x_out:
+        assert torch.equal(x, want)
 
 
 def test_blocks_of_zeros_and_odd_values():
