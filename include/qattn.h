@@ -161,8 +161,11 @@ size_t qkv_attend_shared_workspace_bytes(int head_dim, int n_kv_heads, int n_hea
  *
  * Everything said at qkv_attend holds here, with these differences. Keys and
  * values of the prefix enter the products as two f16 parts, which hold them
- * exactly beside the largest ones of their 128 tokens down to 2^-33 of those; a
- * weight below 2^-31 of its row's largest in the prefix is lost. A prefix length
+ * exactly beside the largest ones of their 128 tokens down to 2^-33 of those. Of
+ * the prefix's weights those parts (with QG_F16 the one, whose rounding the sum
+ * below the line does not have) end at 2^-38 of the row's largest: each may be off
+ * by half of that, and what n tokens with weights below it have together, up to
+ * n 2^-39, is missing from the values. A prefix length
  * outside 0 .. prefix_pages * page_size is taken as the nearer end, a page
  * outside the cache as tokens that are not seen (both code 4). A key block of
  * the prefix whose scale is not finite makes every row NaN. n_tok * n_heads is

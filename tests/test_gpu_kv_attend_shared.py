@@ -129,6 +129,36 @@ def test_where_the_weight_lies(t):
     check(call(cache, q, table, [20, 20], n), q, ks, vs, n, [20, 20], [1, 1], 8, d ** -0.5, t == "f16")
 
 
+# Powers of 2 by which the first token outweighs each of the others. Beside a largest weight of 2^14 the weights' f16 parts
+# end at 2^-24: one lies between that and the next step, one below the half of it, others far above.
+@pytest.mark.parametrize("less", [38.415, 39.32, 31.415, 32.32, 20.7])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_small_equal_weights(d, less):
+    """Tokens that are all alike beside one that outweighs them, in parts of the whole prefix: all roundings have one sign.
+    A weight is off by 2^-39 of the largest at most (half a step of 2^-24 beside 2^14) and in two parts by 2^-22 of
+    itself. The sums over the units, n / 128 additions, round by 2^-24 of them each; where all values are 1 by the same
+    above and below the line. A unit's sum is off by 64 additions (2^-24 each) and 32 steps of the products (2^-23)."""
+    n, page, seqs, group = (1 << 18) - 16, 128, 320, 64
+    pages = -(-n // page)
+    cache = qg.KVCache.empty(pages, 1, d, page)
+    k, v = torch.zeros(n, 1, d, device="cuda"), torch.ones(n, 1, d, device="cuda")
+    k[0, 0, 0] = -8.0  # (a block's scale is 1, its first code 0)
+    v[1:, 0, d // 2:] = -3.0
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    qg.kv_append(cache, k, v, slots)
+    kept = qg.kv_read(cache, slots)
+    assert torch.equal(kept[0], k) and torch.equal(kept[1], v)
+    q = torch.zeros(seqs, group, d, device="cuda")
+    q[..., 0] = -less * float(np.log(2.0)) / 8.0
+    got = qg.kv_attend_shared(cache, q, slots[:pages], i32([n]), i32([[0]] * seqs), i32([0] * seqs), scale=1.0).double().cpu().numpy()
+    share = (n - 1) * 2.0 ** (8.0 * float(q[0, 0, 0]) / np.log(2.0))
+    of_weights = (n - 1) * 2.0 ** -39 + 2.0 ** -22 * share
+    of_units = 64 * 2.0 ** -24 + 32 * 2.0 ** -23
+    assert np.abs(got[..., :d // 2] - 1.0).max() <= of_weights + of_units
+    want = (1.0 - 3.0 * share) / (1.0 + share)
+    assert np.abs(got[..., d // 2:] - want).max() <= of_weights * (want + 3.0) + (of_units + n / 128 * 2.0 ** -24) * (1.0 + 3.0 * share + abs(want))
+
+
 def test_the_same_as_one_cache():
     """What qkv_attend gives on sequences whose tables begin with the prefix's pages."""
     rng = np.random.default_rng(5)
