@@ -23,9 +23,10 @@
 //
 // Weights are 64-bit integers in units of 2^-44 of the largest. So sums, the
 // histogram's atomic ones among them, depend on no order, every pass agrees with
-// every other, and a border is met as in exact arithmetic: with 32-bit sums a
-// token in some thousands would differ from the one that 64 bits give, since
-// with 10^5 tokens that many borders share the unit interval. 2^x for them takes
+// every other, and a border is off by the weights' own roundings alone, 2^-35 of a
+// sum and half a unit a token: with 32-bit sums a token in some thousands would
+// differ from the one that 64 bits give, since with 10^5 tokens that many borders
+// share the unit interval. 2^x for them takes
 // an argument in two floats, a table of 64 powers and a polynomial of degree 5, two
 // logits at a time in packed instructions, 27 a logit; the passes are bound by
 // their instructions. 256 rows of 130001 logits in f16 take 93 us without filters,

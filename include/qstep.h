@@ -86,10 +86,12 @@ int qnorm_residual(const qnorm_args *args, qg_stream_t stream);
  * and prob 0. With logits of +inf only they have weight, 1 each. A top_p or
  * min_p that is NaN keeps all, a uniform outside [0, 1) or NaN counts as the
  * nearer end (NaN: 0).
- * Weights are computed to 2^-35 of themselves and held in units of about 2^-44
- * of the largest (a token below half of that is not chosen), their sums in 64-bit
- * integers: results depend on no order of summing, and agree with 64-bit
- * arithmetic unless a border lies within about 2^-35 of a sum.
+ * Weights are computed to 2^-35 of themselves and rounded to whole units of 2^-44
+ * of the largest or a little more (a token below half of that is not chosen),
+ * their sums are 64-bit integers: results depend on no order of summing, and
+ * agree with 64-bit arithmetic unless a border lies within 2^-35 of a sum and
+ * 2^-45 of the largest weight for each token in it: where all tokens are as good
+ * as alike they err alike, 2^19 of them by 2^-26 of the largest.
  * temperature, top_k, top_p, min_p and uniform are [n]; all but uniform may be
  * NULL (1, all, all, all). token int32 [n]; prob f32 [n] or NULL. 1 <= vocab <=
  * 524288, 0 <= n <= 2^24. */

@@ -101,6 +101,35 @@ def test_few_values():
     both(x * 1e-30, u01(rng, 24), rng.uniform(0.5, 2, 24), rng.integers(1, 30000, 24), rng.uniform(0.05, 1, 24))
 
 
+@pytest.mark.parametrize("vocab", [4001, 130001, 524288])
+@pytest.mark.parametrize("tail", [-28.0, -30.8, -31.15, -31.26])  # 6.2, 0.7, 0.52 and 0.47 of a weight's unit
+@pytest.mark.parametrize("at", [0, -1])
+def test_a_flat_tail(tail, vocab, at):
+    """One likely token and very many equally unlikely ones, whose weights' roundings have one sign: a sum is off by 2^-35
+    of itself and by 2^-45 of the largest weight for each token, times 2^(1/128), by which the unit may be larger. The
+    token chosen is one whose borders are no further off than that (top_p's border beside it: as far, and by one token)."""
+    x = torch.full((1, vocab), tail, device="cuda")
+    x[0, at] = 0.0
+    w = np.exp(x[0].double().cpu().numpy())
+    sums = np.cumsum(w)
+    whole = sums[-1]
+    off = 2.0 ** -35 * whole + vocab * 2.0 ** -45 * 2.0 ** (1 / 128)
+    u = np.array([0.0, 2.0 ** -40, 2.0 ** -30, 2.0 ** -28, 2.0 ** -27, 2.0 ** -26, 2.0 ** -25, 0.25, 0.5, 1 - 2.0 ** -10, 1 - 2.0 ** -23, 1 - 2.0 ** -24])
+    for p in (None, 0.99999994):
+        token, prob = qg.sample_tokens(x.expand(len(u), vocab), cuda(u, torch.float32), top_p=None if p is None else torch.full((len(u),), p, device="cuda"),
+                                       prob_out=torch.empty(len(u), device="cuda"))
+        kept = sums
+        if p is not None:
+            order = np.argsort(-w, kind="stable")
+            stay = order[np.concatenate([[0.0], np.cumsum(w[order])[:-1]]) < float(np.float32(p)) * whole]
+            kept = np.cumsum(np.where(np.isin(np.arange(vocab), stay), w, 0.0))
+        slack = (0.0 if p is None else 2 * off + np.exp(tail)) + 2 * off
+        for t, q, v in zip(token.tolist(), prob.tolist(), np.float32(u).astype(np.float64)):
+            before, past = (kept[t - 1] if t > 0 else 0.0), kept[t]
+            assert before - slack <= v * kept[-1] <= past + slack, (t, v)
+            assert abs(q - w[t] / kept[-1]) <= 2.0 ** -22 * w[t] + 2.0 ** -44 + slack * w[t], (t, q)
+
+
 def test_masks_and_odd_values():
     x, rng = rows(12, 4001, 5)
     x[0] = -INF
