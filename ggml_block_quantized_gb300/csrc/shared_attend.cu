@@ -32,6 +32,7 @@
 // 91 (copies were waited for); whole units' keys in one place, values in another
 // 82.3; loops of the expanders unrolled 98 (instructions came from beyond their
 // cache).
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
 #include <climits>
@@ -756,25 +757,20 @@ __device__ __forceinline__ void store2(__half *p, float a, float b) { *reinterpr
 
 // Joins each row's results: of its stretches of the prefix, and of its own tokens. Block (s, i, h): query i of sequence
 // s, eight heads (of 64: sixteen); D / 4 lanes a head, each four places of a stretch's row: two channels and the two 32 after them.
-constexpr int kJoinThreads = 256;
+// Where that would be more than kJoinBlocks blocks (offsets may name 2^24 sequences, most of them without a row) a block takes
+// several queries, and sequences in sets of 32, whose offsets a warp's lanes look at.
+constexpr int kJoinThreads = 256, kJoinBlocks = 1 << 20;
 
 template <int D, class T> __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p, const int parts) {
     constexpr int kLanes = D / 4, kAhead = 10;  // (stretches under way: an item has up to 19; 4 took half a microsecond more)
     pdl_allow_dependents();
     pdl_wait_prior_grids();
     const KvAttendParams &a = p.own;
-    int q0 = blockIdx.x, m = 1;
-    if (a.q_offsets != nullptr) {
-        q0 = __ldg(a.q_offsets + blockIdx.x);
-        const int q1 = __ldg(a.q_offsets + blockIdx.x + 1);
-        m = q0 < 0 || q1 < q0 || q1 > a.n_tok || q1 - q0 > a.max_q_len ? 0 : q1 - q0;
-    }
     const int h = blockIdx.z * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
-    if (h >= a.n_heads) return;
     const Units units(p, parts);
     const int l = threadIdx.x % kLanes, channel = 64 * (l / 16) + 2 * (l / 2 % 8) + 16 * (l & 1);
     const int kv = h / a.group;
-    for (int i = blockIdx.y; i < m; i += gridDim.y) {
+    auto join = [&](int q0, int i) {  // query i of the sequence whose rows begin at q0
         const int tok = q0 + i, row = tok * a.group + h - kv * a.group;
         const int64_t rest = static_cast<int64_t>(tok) * a.n_heads + h;
         const float2 own = __ldcg(reinterpret_cast<const float2 *>(a.rest_stats) + rest);
@@ -829,6 +825,20 @@ template <int D, class T> __global__ void __launch_bounds__(kJoinThreads) shared
         T *out = static_cast<T *>(a.out) + rest * D + channel;
         store2(out, acc.x * inv, acc.z * inv);
         store2(out + 32, acc.y * inv, acc.w * inv);
+    };
+    const int set = a.n_seq > static_cast<int>(gridDim.x) ? 32 : 1;
+    for (int64_t s0 = static_cast<int64_t>(blockIdx.x) * set; s0 < a.n_seq; s0 += static_cast<int64_t>(gridDim.x) * set) {
+        const int s = static_cast<int>(s0) + static_cast<int>(threadIdx.x & (set - 1));
+        int q0 = s, m = s < a.n_seq ? 1 : 0;
+        if (a.q_offsets != nullptr && m > 0) {
+            q0 = __ldg(a.q_offsets + s);
+            const int q1 = __ldg(a.q_offsets + s + 1);
+            m = q0 < 0 || q1 < q0 || q1 > a.n_tok || q1 - q0 > a.max_q_len ? 0 : q1 - q0;
+        }
+        for (uint32_t some = __ballot_sync(0xffffffffu, m > 0) & (set == 1 ? 1u : ~0u); some != 0; some &= some - 1) {
+            const int first = __shfl_sync(0xffffffffu, q0, __ffs(some) - 1), many = __shfl_sync(0xffffffffu, m, __ffs(some) - 1);
+            for (int i = blockIdx.y; i < many && h < a.n_heads; i += gridDim.y) join(first, i);
+        }
     }
 }
 
@@ -855,9 +865,9 @@ template <int D, class T> cudaError_t launch(SharedParams &p, int sms, int devic
     if (e == cudaSuccess) e = launch_kv_attend(p.own, D, sizeof(T) == 4 ? QG_F32 : QG_F16, sms, device, s);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const int per = kJoinThreads / (D / 4);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.own.n_seq), static_cast<unsigned>(p.own.max_q_len < 64 ? p.own.max_q_len : 64),
-                       static_cast<unsigned>((p.own.n_heads + per - 1) / per));
+    const int per = kJoinThreads / (D / 4), of_heads = (p.own.n_heads + per - 1) / per;  // (8192 at most)
+    const int seqs = std::min(p.own.n_seq, kJoinBlocks / of_heads), queries = std::min({p.own.max_q_len, 64, std::max(1, kJoinBlocks / of_heads / seqs)});
+    cfg.gridDim = dim3(static_cast<unsigned>(seqs), static_cast<unsigned>(queries), static_cast<unsigned>(of_heads));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

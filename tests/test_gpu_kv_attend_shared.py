@@ -265,6 +265,30 @@ def test_rows_in_no_sequence_are_left():
     assert (out[2:6] == 3).all() and not (out[:2] == 3).any() and not (out[6:] == 3).any()
 
 
+@pytest.mark.parametrize("d,heads,n_seq,max_q_len", [(64, 8, (1 << 20) + 77, 2), (128, 256, 100003, 64), (64, 8, 5000, 300)])
+def test_many_sequences_most_of_them_empty(d, heads, n_seq, max_q_len):
+    """The bits of a call that names the others alone."""
+    rng = np.random.default_rng(23)
+    held = sorted({0, 5, 31, 32, 33, n_seq - 1, *range(47, n_seq, 50021)})
+    per = rng.integers(1, max_q_len + 1, len(held)) % 7 + 1 if max_q_len > 6 else rng.integers(1, max_q_len + 1, len(held))
+    n = int(per.sum())
+    own = rng.integers(0, 16, len(held))
+    cache = qg.KVCache.empty(20, 1, d, 16)
+    kv = torch.from_numpy(rng.standard_normal((2, 320, 1, d)).astype(np.float32)).cuda()
+    qg.kv_append(cache, kv[0], kv[1], torch.arange(320, dtype=torch.int32, device="cuda"))
+    q = torch.from_numpy(rng.standard_normal((n, heads, d)).astype(np.float32)).cuda()
+    table = torch.from_numpy(rng.integers(0, 20, (len(held), 1)).astype(np.int32)).cuda()
+    offsets = np.concatenate([[0], np.cumsum(per)]).astype(np.int32)
+    args = (cache, q, torch.arange(18, dtype=torch.int32, device="cuda"), i32([283]))
+    want = qg.kv_attend_shared(*args, table, i32(own), q_offsets=i32(offsets), max_q_len=max_q_len)
+    at = torch.tensor(held, device="cuda")
+    all_table, all_own, all_per = torch.zeros(n_seq, 1, dtype=torch.int32, device="cuda"), torch.zeros(n_seq, dtype=torch.int32, device="cuda"), np.zeros(n_seq + 1, np.int64)
+    all_table[at], all_own[at], all_per[np.array(held) + 1] = table, i32(own), per
+    got = qg.kv_attend_shared(*args, all_table, all_own, q_offsets=i32(np.cumsum(all_per)), max_q_len=max_q_len)
+    assert torch.equal(got, want)
+    assert qg.device_error() == 0
+
+
 def test_indexes_out_of_range():
     """A bad page counts as unseen, a length past the table as the table's end."""
     rng = np.random.default_rng(21)
