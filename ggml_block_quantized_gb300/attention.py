@@ -363,7 +363,8 @@ def kv_attend_shared(cache: KVCache, q, prefix_table, prefix_len, table, lengths
     """kv_attend for sequences that begin with the same tokens: the prefix_len[0] ones (int32 [1]) in the pages
     prefix_table (int32 [pages]), which every query sees, and then each sequence's own lengths[s] ones in the pages
     table[s]. The result is kv_attend's on sequences that hold both; the prefix is read, and its products are formed,
-    once for all of them."""
+    once for all of them. Few sequences, or a short prefix, are faster by kv_attend on whole tables (with 8 key/value
+    heads below about 8 sequences or 10^5 sequences times prefix tokens)."""
     device, q_ptr, q_stride, n_tok, heads, table_ptr, pages, len_ptr, off_ptr, n_seq, out, out_ptr = _attend_args(
         cache, q, table, lengths, q_offsets, out, stream)
     prefix_ptr = _on(prefix_table, device, "prefix_table", torch.int32)

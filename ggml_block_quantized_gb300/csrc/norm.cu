@@ -16,10 +16,13 @@
 // read by as many threads as there can be.
 //
 // Memory bounds it where there is work for every multiprocessor: 8191 rows of
-// 4096 with both norms, f16 h, f32 y, f16 x take 52.4 us (335 MB at 6.4 TB/s),
-// close to a copy's 49.4; there the instructions of an element count next (38 of
-// them took 57.7 us). 1037 rows of 1283 in f32 take 9.7 us, 48 rows of 4096 4.3,
-// one row 3.1: the chain of launch, load, two sums by shuffles and barrier, store.
+// 4096, f16 h, f32 y, f16 x take 52.6 us (335 MB at 6.4 TB/s), close to a copy's
+// 49.4; there the instructions of an element count next (38 of them took 57.7 us;
+// a layer norm takes 57.0, activation blocks instead of x 59 to 64). 1037 rows of
+// 1283 in f32 take 9.8 us, 48 rows of 5120 with both norms 4.2, one row of 4096 3.0:
+// the chain of launch, load, two sums by shuffles and barrier, store. Rows off
+// 16-byte boundaries of more than 8192 elements spill 52 to 60 bytes a thread
+// (2048 of 16383 in f32 136 us, of 16384 90).
 #include "quant_act.cuh"
 #include "step_kernels.cuh"
 

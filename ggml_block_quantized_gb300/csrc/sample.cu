@@ -28,10 +28,11 @@
 // differ from the one that 64 bits give, since with 10^5 tokens that many borders
 // share the unit interval. 2^x for them takes
 // an argument in two floats, a table of 64 powers and a polynomial of degree 5, two
-// logits at a time in packed instructions, 27 a logit; the passes are bound by
-// their instructions. 256 rows of 130001 logits in f16 take 93 us without filters,
-// 45 with a top_k of 40, 217 with a top_p of 0.9, one row of 32000 in f32 7.7, 8.5
-// and 19.5: there it is one chain of loads, joins of the cluster and sums.
+// logits at a time in packed instructions, 27 a logit. 256 rows of 130001 logits in
+// f16 take 96 us without filters, 51 with a top_k of 40, 223 with a top_p of 0.9,
+// 133 with settings of their own, where issue slots are 55% used and warps wait for
+// each other at the passes' barriers first. One row of 32000 in f32 takes 7.2, 8.0
+// and 19.1: there it is one chain of loads, joins of the cluster and sums.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -21,17 +21,18 @@
 // ready, one issues S, one O; four hold a row's softmax a thread, four its values'
 // sums; eight expand codes into operands, four the keys', four the values'. With
 // 128 channels a unit is 32 products of 64 cycles, so 2048 cycles for f16, half as
-// many again for f32, and 128 KB of operands written; it takes 2850 for f16. What
-// bounds it is the expanders' chain of instructions (3.8 cycles each in turn, 22 a
-// word of eight codes), then the tensor cores. 16 sequences of 64 heads on 65521
-// tokens, 27 units a block, take 76.0 us. A call with a short prefix is a
-// pipeline's filling, its drain and the join (2 sequences on 300 tokens: 17.8 us),
-// most of them instructions' first fetch. What other arrangements measured on the
-// 65521: one warp for S and O, and eight that expand keys and values in turn, 86.0
-// us; pieces of a unit's keys and values in three places and three raw pieces ahead
-// 91 (copies were waited for); whole units' keys in one place, values in another
-// 82.3; loops of the expanders unrolled 98 (instructions came from beyond their
-// cache).
+// many again for f32, and 128 KB of operands written; it takes 1.73 us for f16,
+// 2.35 for f32. What bounds it is the expanders' chain of instructions (3.8 cycles
+// each in turn, 22 a word of eight codes), then the tensor cores. 16 sequences of
+// 64 heads on 65521 tokens take 75.5 us: 27 units a block 47, three launches and
+// the join 11.5, queries, filling and drain 12, own tokens 6. A call with a short
+// prefix is all but that first part (2 sequences on 300 tokens: 17.5 us, where
+// kv_attend on whole tables takes 8.4; they meet at about 65000 sequences x tokens
+// of 8 key/value heads). What other arrangements measured on the 65521, 76.0 us
+// then: one warp for S and O, and eight that expand keys and values in turn, 86.0;
+// pieces of a unit's keys and values in three places and three raw pieces ahead 91
+// (copies were waited for); whole units' keys in one place, values in another 82.3;
+// loops of the expanders unrolled 98 (instructions came from beyond their cache).
 #include <algorithm>
 #include <atomic>
 #include <cfloat>

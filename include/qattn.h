@@ -157,7 +157,9 @@ size_t qkv_attend_shared_workspace_bytes(int head_dim, int n_kv_heads, int n_hea
  *   s_t = scale q . k_t, out = sum_t exp(s_t - max s) v_t / sum_t exp(s_t - max s)
  * over the prefix's tokens and the own ones that it sees; the result is that of
  * qkv_attend on sequences that hold both, but the prefix is read and its products
- * are formed once for all of them. Where neither holds a token seen, zeros.
+ * are formed once for all of them. Where neither holds a token seen, zeros. A call
+ * has one prefix. With 8 key/value heads it is faster than qkv_attend on whole tables
+ * from about 8 sequences and 10^5 sequences times prefix tokens on.
  *
  * Everything said at qkv_attend holds here, with these differences. Keys and
  * values of the prefix enter the products as two f16 parts, which hold them

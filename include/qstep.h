@@ -59,8 +59,8 @@ typedef struct {
  *                (v - m) / sqrt(mean((v - m)^2) + eps) * w + b, m = mean(v)
  * computed in f32, each output rounded once: x follows from h' before its
  * rounding to h_type. xq holds what quantize_act(act_type) makes of x in f32,
- * byte for byte, for qgemv_xq: d is a multiple of its block then, h, y, gate,
- * post_w, post_b, w, b and xq lie on 16-byte boundaries and the strides are multiples of
+ * byte for byte, for qgemv_xq: d is a multiple of its block then, every array that
+ * is given lies on a 16-byte boundary, and its stride is a multiple of
  * 16 bytes. At least one of h_out, x_out and xq is given. h_out may be h
  * (same stride); x_out may be h or y where type and stride are the same and
  * h_out is not that one too. Infinities and NaN in a row stay in that row.
